@@ -16,7 +16,8 @@
  * Conventions for every call:
  *   - Pointers marked "device" are CUDA device pointers owned by the caller; the library
  *     never frees them.  Pointers marked "host" are read during the call only.
- *   - fp16 means IEEE binary16 stored as 2-byte values.
+ *   - fp16 means IEEE binary16 stored as 2-byte values.  Where a call below takes or gives fp16, a
+ *     context of io_type RQ_BF16 takes and gives bf16.
  *   - `stream` is a cudaStream_t (NULL = legacy default stream).  Calls enqueue work and
  *     return without synchronising; the caller keeps inputs alive until the stream passes.
  *   - A context holds one split-K workspace: calls on the same context must not overlap on
@@ -48,6 +49,16 @@
  *                 boundaries are midpoints of consecutive centroids; a vector of norm 0
  *                 codes every coordinate as 2^(bits-1) - 1.
  *   norm        : ||x|| rounded to fp16 (nearest even).
+ *   RQ_FP8      : the chunk of (page, kv head) is instead P / 16 blocks of 4112 bytes, one per 16
+ *                 tokens: 2048 key codes, 2048 value codes (e4m3, byte-for-byte the format's), then
+ *                 the two scales' exponent bytes EK and EV and 14 unused bytes; a key is code *
+ *                 2^(EK - 127), a value code * 2^(EV - 127).  The key code of the block's token r,
+ *                 dim d is byte ((r/8 * 2 + d/64) * 32 + r%8 * 4 + d%64/16) * 16 + d%16, its value
+ *                 code byte 2048 + (d/32 * 32 + d/4%8 * 4 + r%8/2) * 16 + d%4 * 4 + r/8 * 2 + r%2.
+ *                 A scale is 2^E with the smallest E in [-60, 60] for which the largest magnitude
+ *                 is at most 448 * 2^E.  Appending a block's first token (offset a multiple of 16)
+ *                 starts its scales anew from the tokens of that call; a later token raises a scale
+ *                 if it must, and the codes already there are rounded to the new scale.
  *   slot        : page * P + offset in page; block_table[b][i] is the page holding tokens
  *                 i*P .. i*P+P-1 of sequence b.
  */
@@ -73,6 +84,7 @@ extern "C" {
 #define RQ_STATUS_BAD_SLOT 2   /* slot_mapping entry >= num_pages * page_size */
 #define RQ_STATUS_BAD_LEN 4    /* seq_len < 0 or above max_pages * page_size, or below T */
 #define RQ_STATUS_NORM_OVERFLOW 8 /* a vector norm above the fp16 range (stored as inf) */
+#define RQ_STATUS_NOT_FINITE 32 /* an infinity or NaN among the values an RQ_FP8 append coded */
 #define RQ_STATUS_TIMEOUT 16   /* an attention kernel's staged page copy did not complete within
                                   its bounded wait (outputs of that call are unspecified) */
 
@@ -82,6 +94,14 @@ extern "C" {
 #define RQ_PLANAR 0            /* PlanarQuant: 2D Givens rotation per dimension pair */
 #define RQ_ISO 1               /* IsoQuant: unit quaternion per 4-dimension block */
 #define RQ_DENSE 2             /* TurboQuant: one dense orthogonal head_dim x head_dim matrix */
+/* Source: this library.  No rotation: the cache holds e4m3 codes with a power-of-two scale for each
+   block of 16 tokens of a kv head, separately for K and V (bits must be 8).  Twice the bytes of
+   RQ_PLANAR / RQ_ISO at 4 bits, for the models and layers whose outlier channels those lose. */
+#define RQ_FP8 8
+
+/* Element types of q, k, v and out.  RQ_BF16 needs an RQ_FP8 context. */
+#define RQ_F16 0
+#define RQ_BF16 1
 
 typedef struct rq_ctx rq_ctx;  /* opaque, owned by the library */
 
@@ -89,8 +109,8 @@ typedef struct {
   int head_dim;              /* must be 128 */
   int num_q_heads;           /* Hq, a multiple of num_kv_heads */
   int num_kv_heads;          /* Hkv >= 1 */
-  int bits;                  /* 2, 3 or 4 */
-  int mode;                  /* RQ_PLANAR, RQ_ISO or RQ_DENSE */
+  int bits;                  /* 2, 3 or 4; 8 for RQ_FP8 */
+  int mode;                  /* RQ_PLANAR, RQ_ISO, RQ_DENSE or RQ_FP8 */
   int page_size;             /* P: a multiple of 16, at most 256 */
   int num_pages;             /* pages in the caller's pool */
   int max_batch;             /* largest B of an attention call */
@@ -102,14 +122,15 @@ typedef struct {
      (Hamilton product, q on the left);
      dense -> [Hkv][d][d] = row-major R, y_i = sum_j R[i][j] x_j.  R must be orthogonal (the
      library does not check; decoding multiplies by R^T).
-     rot_k turns keys and queries, rot_v values. */
+     rot_k turns keys and queries, rot_v values.  RQ_FP8 reads neither. */
   const float *rot_k;
   const float *rot_v;
   /* host float32 [2^bits] ascending centroids, or NULL for the Lloyd-Max quantizer of
-     N(0, 1/head_dim) (the levels of N(0,1) divided by sqrt(head_dim)). */
+     N(0, 1/head_dim) (the levels of N(0,1) divided by sqrt(head_dim)).  RQ_FP8: must be NULL. */
   const float *codebook;
   float sm_scale;            /* softmax scale; 0 selects 1/sqrt(head_dim) */
   int device;                /* CUDA device ordinal the context lives on; -1 = current */
+  int io_type;               /* RQ_F16, or RQ_BF16 (RQ_FP8 only): every q, k, v and out of the context */
 } rq_config;
 
 /* Source: this library (the constructor of the context that rq_free releases); the tables it holds
@@ -125,7 +146,7 @@ int rq_create(rq_ctx **out, const rq_config *cfg);
 void rq_free(rq_ctx *ctx);
 
 /* Source: this library's storage contract (above).  Bytes of one (page, kv head) chunk: page_size *
-   (2 * head_dim * bits / 8 + 4).  0 for NULL. */
+   (2 * head_dim * bits / 8 + 4), RQ_FP8 page_size / 16 * 4112.  0 for NULL. */
 size_t rq_page_bytes(const rq_ctx *ctx);
 
 /* Source: README, Acknowledgments (TurboQuant entry: "Lloyd-Max scalar quantization"), read as the
@@ -137,7 +158,7 @@ int rq_lloyd_max_codebook(int bits, int head_dim, float *centroids);
 
 /* Source: this library.  Host copies of the context's centroids [2^bits] and bin boundaries
    [2^bits - 1] (float32; boundary j = float((centroid_j + centroid_{j+1}) / 2) computed in
-   double).  Either may be NULL. */
+   double).  Either may be NULL.  RQ_ERR_UNSUPPORTED for RQ_FP8 (no codebook). */
 int rq_get_codebook(const rq_ctx *ctx, float *centroids, float *boundaries);
 
 /*
@@ -151,6 +172,10 @@ int rq_get_codebook(const rq_ctx *ctx, float *centroids, float *boundaries);
  * < 0 is skipped (padding); a slot >= num_pages * page_size sets RQ_STATUS_BAD_SLOT and is
  * skipped.  Slots within one call must be distinct.  n = 0 is a no-op.  k, v and kv_pages must be
  * 16-byte aligned (RQ_ERR_INVALID otherwise).
+ * RQ_FP8: k and v have the context's io_type, no rotation; tokens of one block of 16 must stand
+ * next to one another in the call, in ascending slots, as a sequence's tokens do (otherwise that
+ * block's contents are unspecified).  Infinities are stored as the block's largest value, NaN as
+ * NaN; either sets RQ_STATUS_NOT_FINITE and neither counts for the scale.
  */
 int rq_quantize_append(rq_ctx *ctx, const void *k, const void *v, const int32_t *slot_mapping,
                        int n, void *kv_pages, int32_t *d_status, void *stream);
@@ -209,7 +234,7 @@ int rq_extend_attention(rq_ctx *ctx, const void *q, int T, const void *kv_pages,
  * The result equals rq_quantize_append of the tokens followed by rq_decode_attention (the same
  * bytes written, the same output).  A dense rotation (RQ_DENSE) codes the new tokens in the
  * launch that rotates the queries, before the split-K kernel (which applies the output
- * rotation itself): two launches instead of four.  A page id out of range for the new token sets RQ_STATUS_BAD_PAGE
+ * rotation itself): two launches instead of four.  RQ_FP8 appends in a launch of its own.  A page id out of range for the new token sets RQ_STATUS_BAD_PAGE
  * and skips its write.  Errors as rq_decode_attention, plus RQ_ERR_INVALID for a NULL or
  * non-16-byte-aligned k_new / v_new.
  */
@@ -258,8 +283,8 @@ int rq_tree_verify_attention(rq_ctx *ctx, const void *q, int T, const uint64_t *
  * everything comes in as arguments:
  *   cfg         host; only head_dim, num_q_heads, num_kv_heads, bits, mode, page_size, num_pages
  *               and sm_scale are read (the max_* limits, host tables, codebook and device are
- *               ignored).  mode RQ_DENSE returns RQ_ERR_UNSUPPORTED (its query rotation needs
- *               a workspace).
+ *               ignored).  modes RQ_DENSE (its query rotation needs a workspace) and RQ_FP8
+ *               return RQ_ERR_UNSUPPORTED.
  *   d_rot_k, d_rot_v   device float32 [Hkv][head_dim], laid out as rq_config.rot_k / rot_v
  *   d_centroids        device float32 [2^bits], ascending (e.g. from rq_lloyd_max_codebook)
  *   other arguments    as rq_decode_attention, on the CURRENT device
@@ -280,6 +305,78 @@ int rq_decode_attention_noalloc(const rq_config *cfg, const float *d_rot_k, cons
                                 const float *d_centroids, const void *q, const void *kv_pages,
                                 const int32_t *block_table, int max_pages, const int32_t *seq_lens,
                                 int B, void *out, int32_t *d_status, void *stream);
+
+/*
+ * Source: this library.  What stands between a model's projections and the cache: the norm of each
+ * query and key head and the position rotation.  rq_quantize_append takes keys that have been
+ * through it.
+ *   norm      y = x / sqrt(mean over the head's 128 dims of x^2 + eps) * weight
+ *   rotation  pair i of the first rotary_dim dims turns by the angle t = position * inv_freq[i]:
+ *             (a, b) -> scale * (a cos t - b sin t, a sin t + b cos t).  The angle is exact to
+ *             2^-33 turns at every int32 position.  Dims past rotary_dim pass through unscaled.
+ * Both are computed in float32 and rounded once.
+ */
+typedef struct rq_rope rq_rope;  /* opaque, owned by the library: the frequencies on one device */
+
+typedef struct {
+  int rotary_dim;            /* a multiple of 8, 0 (no rotation) to 128 */
+  int interleaved;           /* 0: pair i = dims (i, i + rotary_dim / 2); 1: dims (2i, 2i + 1) */
+  int num_axes;              /* position axes, 1 to 8: text 1; images and video 3 (time, height, width) */
+  const double *inv_freq;    /* host [rotary_dim / 2]: radians per position, 0 <= f <= 65536 */
+  const int *axis;           /* host [rotary_dim / 2]: the axis whose position turns the pair; NULL: axis 0 */
+  float scale;               /* multiplies cos and sin (length extrapolation); 0 selects 1 */
+  int device;                /* CUDA device ordinal; -1 = current */
+} rq_rope_config;
+
+/* Source: this library.  Validates cfg and copies the frequencies to the device.  On success *out is
+   new, else NULL with nothing allocated.  Errors: RQ_ERR_INVALID, RQ_ERR_CUDA. */
+int rq_rope_create(rq_rope **out, const rq_rope_config *cfg);
+
+/* Source: this library.  Releases what rq_rope_create allocated.  NULL-safe; no call that uses it may
+   still be running. */
+void rq_rope_free(rq_rope *rope);
+
+/* The rows of one tensor: token t, head h stands at x + t * stride + h * 128 elements, so a slice of
+   a fused projection's output is taken as it is. */
+typedef struct {
+  const void *x;             /* device, 16-byte aligned */
+  long long stride;          /* elements from token to token: a multiple of 8, >= heads * 128 */
+  int heads;
+  const float *weight;       /* device float32 [128], 16-byte aligned: the norm's; NULL: no norm */
+  void *out;                 /* device, 16-byte aligned; x itself (with x's stride): in place */
+  long long out_stride;
+} rq_rows;
+
+/*
+ * Source: this library.  The norm and rotation of n tokens' query and key rows in one launch.
+ *   rope       NULL: norms only.  It must live on the current device (as must every pointer).
+ *   q, k       either may be NULL, not both
+ *   io_type    RQ_F16 or RQ_BF16: element type of x and out
+ *   positions  device int32 [num_axes][n]; negative positions turn the other way; unused (may be
+ *              NULL) without a rotation
+ * n = 0 is a no-op.  An out that overlaps any of the call's rows except its own x in place is
+ * refused.  Errors: RQ_ERR_INVALID, RQ_ERR_CUDA.
+ */
+int rq_norm_rope(const rq_rope *rope, const rq_rows *q, const rq_rows *k, int io_type, float eps,
+                 const int32_t *positions, int n, void *stream);
+
+/*
+ * Source: this library.  Append to an RQ_FP8 context's cache with the norm and rotation of keys on
+ * the way, and the same tokens' queries turned by the same launch: everything between the
+ * projections and attention.  Equals rq_norm_rope of q and k followed by rq_quantize_append, except
+ * that the keys are coded from float32 and not rounded to io_type in between.
+ *   rope       NULL: no rotation; it must live on the context's device
+ *   q          NULL, or rows whose out receives the turned queries
+ *   k          heads must be the context's num_kv_heads; k->out must be NULL
+ *   v          device, 16-byte aligned; token t, head h at v + t * v_stride + h * 128, a multiple of 8
+ *              and >= num_kv_heads * 128
+ *   the rest   as rq_norm_rope and rq_quantize_append; a padding token's query is turned all the same
+ * Errors: RQ_ERR_INVALID, RQ_ERR_CUDA, and RQ_ERR_UNSUPPORTED for a context of another mode (turn
+ * the keys with rq_norm_rope and append those).
+ */
+int rq_rope_append(rq_ctx *ctx, const rq_rope *rope, const rq_rows *q, const rq_rows *k, const void *v,
+                   long long v_stride, float eps, const int32_t *positions, const int32_t *slot_mapping, int n,
+                   void *kv_pages, int32_t *d_status, void *stream);
 
 /* Source: this library.  Diagnostics.  While set, every attention call records ev_start on its
    stream just before its split-K kernel and ev_end just after it (both cudaEvent_t created by the

@@ -110,28 +110,128 @@ double centroid_scale(const float* c, int L) {
   return best_s;
 }
 
-int check_geometry(const rq_config* c) {
-  if (c->head_dim <= 0 || c->num_q_heads <= 0 || c->num_kv_heads <= 0 || c->page_size <= 0 || c->num_pages <= 0 ||
-      c->max_batch <= 0 || c->max_query_tokens <= 0 || c->max_pages_per_seq <= 0)
-    return RQ_ERR_INVALID;
-  if (c->num_q_heads % c->num_kv_heads != 0) return RQ_ERR_INVALID;
-  if (c->mode != RQ_PLANAR && c->mode != RQ_ISO && c->mode != RQ_DENSE) return RQ_ERR_INVALID;
-  if (!c->rot_k || !c->rot_v) return RQ_ERR_INVALID;
-  if (c->head_dim != rq::kHeadDim) return RQ_ERR_UNSUPPORTED;
-  if (c->bits < 2 || c->bits > 4) return RQ_ERR_UNSUPPORTED;
+// Limits that every mode shares; chunk_bytes: bytes of one (page, kv head) chunk.
+int check_sizes(const rq_config* c, long long chunk_bytes) {
   if (c->page_size % 16 != 0 || c->page_size > 256) return RQ_ERR_UNSUPPORTED;
   if ((long long)c->num_pages * c->page_size > INT32_MAX) return RQ_ERR_UNSUPPORTED;
   if ((long long)c->max_pages_per_seq * c->page_size > INT32_MAX) return RQ_ERR_UNSUPPORTED;  // positions are int
   // one page's chunks of all kv heads stay below 2^31 bytes (32-bit page strides in the kernels)
-  if ((long long)c->num_kv_heads * c->page_size * (2 * 16 * c->bits + 4) > INT32_MAX) return RQ_ERR_UNSUPPORTED;
+  if (c->num_kv_heads * chunk_bytes > INT32_MAX) return RQ_ERR_UNSUPPORTED;
   if (c->max_batch > rq::kMaxBatch) return RQ_ERR_UNSUPPORTED;
   if (!(c->sm_scale >= 0.0f) || std::isinf(c->sm_scale)) return RQ_ERR_INVALID;
   return RQ_OK;
 }
 
+int check_geometry(const rq_config* c) {
+  if (c->head_dim <= 0 || c->num_q_heads <= 0 || c->num_kv_heads <= 0 || c->page_size <= 0 || c->num_pages <= 0 ||
+      c->max_batch <= 0 || c->max_query_tokens <= 0 || c->max_pages_per_seq <= 0)
+    return RQ_ERR_INVALID;
+  if (c->num_q_heads % c->num_kv_heads != 0) return RQ_ERR_INVALID;
+  if (c->mode != RQ_PLANAR && c->mode != RQ_ISO && c->mode != RQ_DENSE && c->mode != RQ_FP8) return RQ_ERR_INVALID;
+  if (c->io_type != RQ_F16 && c->io_type != RQ_BF16) return RQ_ERR_INVALID;
+  if (c->mode == RQ_FP8) {
+    if (c->codebook) return RQ_ERR_INVALID;
+    if (c->head_dim != rq::kHeadDim || c->bits != 8) return RQ_ERR_UNSUPPORTED;
+    return check_sizes(c, (long long)c->page_size / 16 * rq::kBlockBytes);
+  }
+  if (c->io_type != RQ_F16) return RQ_ERR_UNSUPPORTED;
+  if (!c->rot_k || !c->rot_v) return RQ_ERR_INVALID;
+  if (c->head_dim != rq::kHeadDim) return RQ_ERR_UNSUPPORTED;
+  if (c->bits < 2 || c->bits > 4) return RQ_ERR_UNSUPPORTED;
+  return check_sizes(c, (long long)c->page_size * (2 * 16 * c->bits + 4));
+}
+
+// Creation of an RQ_FP8 context, on the current device: no tables.
+int create_block(rq_ctx* ctx, const rq_config* cfg) {
+  rq::Geometry& g = ctx->g;
+  g.num_q_heads = cfg->num_q_heads;
+  g.num_kv_heads = cfg->num_kv_heads;
+  g.group = cfg->num_q_heads / cfg->num_kv_heads;
+  g.bits = 8;
+  g.mode = RQ_FP8;
+  g.bf16 = cfg->io_type == RQ_BF16;
+  g.page_size = cfg->page_size;
+  g.num_pages = cfg->num_pages;
+  g.vec_bytes = cfg->head_dim;
+  g.page_bytes = cfg->page_size / 16 * rq::kBlockBytes;
+  g.sm_scale = cfg->sm_scale > 0.f ? cfg->sm_scale : (float)(1.0 / std::sqrt((double)cfg->head_dim));
+  return RQ_OK;
+}
+
+bool misaligned16(const void* p) { return (uintptr_t)p % 16 != 0; }
+
+// 1 / (2 pi) as a 128-bit binary fraction, high and low words.
+constexpr uint64_t kTurnHi = 0x28BE60DB9391054Aull, kTurnLo = 0x7F09D5F47D4D3770ull;
+
+// f / (2 pi) * 2^64 modulo 2^64, rounded, for 0 <= f <= 2^16: f = m * 2^e exactly, and m times the
+// fraction above is an integer of three 64-bit words to be shifted by 64 - e bits.
+uint64_t turns_per_position(double f) {
+  if (!(f > 0.0)) return 0;
+  int e;
+  const uint64_t m = (uint64_t)std::ldexp(std::frexp(f, &e), 53);  // 53 bits
+  e -= 53;                                                       // f = m * 2^e
+  typedef unsigned __int128 u128;
+  const u128 lo = (u128)m * kTurnLo, hi = (u128)m * kTurnHi + (uint64_t)(lo >> 64);
+  uint64_t w[4] = {(uint64_t)lo, (uint64_t)hi, (uint64_t)(hi >> 64), 0};  // m / (2 pi) * 2^128
+  const int shift = 64 - e;  // result = w * 2^-shift, rounded; e <= 16 - 52, so shift >= 100
+  if (shift > 191) return 0;
+  const int word = (shift - 1) / 64, bit = (shift - 1) % 64;
+  uint64_t x = w[word] >> bit, y = word + 1 < 4 ? w[word + 1] : 0, z = word + 2 < 4 ? w[word + 2] : 0;
+  // x | y | z from bit `bit` of word `word` on: 65 bits, the lowest of them the rounding bit
+  if (bit) {
+    x |= y << (64 - bit);
+    y = y >> bit | z << (64 - bit);
+  }
+  return (x >> 1 | y << 63) + (x & 1);
+}
+
+// Whether the rows of two tensors share memory.
+struct Span {
+  uintptr_t at;
+  uintptr_t stride, row, end;  // bytes
+};
+Span span(const void* p, long long stride, int heads, int n) {
+  Span s;
+  s.at = (uintptr_t)p;
+  s.stride = (uintptr_t)stride * 2;
+  s.row = (uintptr_t)heads * rq::kHeadDim * 2;
+  s.end = s.at + (uintptr_t)(n - 1) * s.stride + s.row;
+  return s;
+}
+bool overlap(const Span& a, const Span& b) {
+  if (a.end <= b.at || b.end <= a.at) return false;
+  if (a.stride != b.stride) return true;  // interleaved rows of one buffer have one stride
+  const uintptr_t d = a.at <= b.at ? (b.at - a.at) % b.stride : (a.stride - (a.at - b.at) % a.stride) % a.stride;
+  return d < a.row || d + b.row > a.stride;
+}
+
+// Rows of a call: absent (null) or checked; `with_out` rows have an output.
+int check_rows(const rq_rows* r, bool with_out) {
+  if (!r) return RQ_OK;
+  if (!r->x || r->heads <= 0 || r->heads > 65535 || misaligned16(r->x) || misaligned16(r->weight)) return RQ_ERR_INVALID;
+  const long long row = (long long)r->heads * rq::kHeadDim;
+  if (r->stride < row || r->stride % 8 != 0 || r->stride > INT32_MAX) return RQ_ERR_INVALID;
+  if (!with_out) return r->out ? RQ_ERR_INVALID : RQ_OK;
+  if (!r->out || misaligned16(r->out) || r->out_stride < row || r->out_stride % 8 != 0 || r->out_stride > INT32_MAX)
+    return RQ_ERR_INVALID;
+  return RQ_OK;
+}
+
+rq::RowsDev rows_dev(const rq_rows* r) {
+  rq::RowsDev d{};
+  if (r) d = rq::RowsDev{r->x, r->stride, r->weight, r->out, r->out_stride, r->heads};
+  return d;
+}
+
 int to_status(cudaError_t e) { return e == cudaSuccess ? RQ_OK : RQ_ERR_CUDA; }
 
 }  // namespace
+
+struct rq_rope {
+  rq::RopeTable table;
+  uint64_t* d_pairs;
+  int device;
+};
 
 extern "C" {
 
@@ -195,6 +295,25 @@ int rq_create(rq_ctx** out, const rq_config* cfg) {
   rq_ctx* ctx = new (std::nothrow) rq_ctx();
   if (!ctx) return RQ_ERR_CUDA;
   ctx->cfg = *cfg;
+  if (cfg->mode == RQ_FP8) {
+    ctx->cfg.rot_k = ctx->cfg.rot_v = nullptr;
+    int dev = cfg->device;
+    if (dev < 0 && cudaGetDevice(&dev) != cudaSuccess) {
+      delete ctx;
+      return RQ_ERR_CUDA;
+    }
+    ctx->device = dev;
+    DeviceScope scope(dev);
+    st = scope.ok() && cudaDeviceGetAttribute(&ctx->num_sms, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess
+             ? create_block(ctx, cfg)
+             : RQ_ERR_CUDA;
+    if (st != RQ_OK) {
+      delete ctx;
+      return st;
+    }
+    *out = ctx;
+    return RQ_OK;
+  }
   const int L = 1 << cfg->bits;
   if (cfg->codebook) {
     for (int j = 0; j < L; ++j) {
@@ -401,6 +520,7 @@ size_t rq_page_bytes(const rq_ctx* ctx) { return ctx ? (size_t)ctx->g.page_bytes
 
 int rq_get_codebook(const rq_ctx* ctx, float* centroids, float* boundaries) {
   if (!ctx) return RQ_ERR_INVALID;
+  if (ctx->g.mode == RQ_FP8) return RQ_ERR_UNSUPPORTED;
   const int L = 1 << ctx->g.bits;
   if (centroids) std::memcpy(centroids, ctx->centroids, L * sizeof(float));
   if (boundaries) std::memcpy(boundaries, ctx->boundaries, (L - 1) * sizeof(float));
@@ -416,11 +536,55 @@ int rq_quantize_append(rq_ctx* ctx, const void* k, const void* v, const int32_t*
     return RQ_ERR_INVALID;  // 16-byte vector loads and stores
   DeviceScope scope(ctx->device);
   if (!scope.ok()) return RQ_ERR_CUDA;
+  if (ctx->g.mode == RQ_FP8) {
+    rq::BlockAppendArgs a{};
+    a.in.k.x = k;
+    a.in.k.stride = a.v_stride = (long long)ctx->g.num_kv_heads * rq::kHeadDim;
+    a.in.k.heads = ctx->g.num_kv_heads;
+    a.in.n = n;
+    a.v = v;
+    a.slots = slot_mapping;
+    a.pages = (uint8_t*)kv_pages;
+    a.status = d_status;
+    return to_status(rq::launch_block_append(ctx->g, a, ctx->num_sms, (cudaStream_t)stream));
+  }
   return to_status(rq::launch_append(ctx->g, k, v, slot_mapping, n, (uint8_t*)kv_pages, d_status,
                                      (cudaStream_t)stream));
 }
 
-static bool misaligned16(const void* p) { return (uintptr_t)p % 16 != 0; }
+// An attention call of an RQ_FP8 context, its arguments checked and its device current.
+static int block_attention(rq_ctx* ctx, const void* q, int T, const uint64_t* tree_mask, const void* kv_pages,
+                           const int32_t* block_table, int max_pages, const int32_t* seq_lens, int B, void* out,
+                           int32_t* d_status, cudaStream_t stream, const void* k_new, const void* v_new) {
+  if (k_new) {
+    rq::BlockAppendArgs n{};
+    n.in.k.x = k_new;
+    n.in.k.stride = n.v_stride = (long long)ctx->g.num_kv_heads * rq::kHeadDim;
+    n.in.k.heads = ctx->g.num_kv_heads;
+    n.in.n = B;
+    n.v = v_new;
+    n.block_table = block_table;
+    n.max_pages = max_pages;
+    n.seq_lens = seq_lens;
+    n.pages = (uint8_t*)const_cast<void*>(kv_pages);
+    n.status = d_status;
+    const cudaError_t e = rq::launch_block_append(ctx->g, n, ctx->num_sms, stream);
+    if (e != cudaSuccess) return RQ_ERR_CUDA;
+  }
+  rq::AttnArgs a{};
+  a.q = q;
+  a.pages = (const uint8_t*)kv_pages;
+  a.block_table = block_table;
+  a.max_pages = max_pages;
+  a.seq_lens = seq_lens;
+  a.B = B;
+  a.T = T;
+  a.out = out;
+  a.status = d_status;
+  a.tree_mask = tree_mask;
+  a.rows = T * ctx->g.group;
+  return to_status(rq::launch_block_attention(ctx->g, a, stream, ctx->prof_start, ctx->prof_end));
+}
 
 static int attention_call(rq_ctx* ctx, const void* q, int T, const uint64_t* tree_mask, const void* kv_pages,
                           const int32_t* block_table, int max_pages, const int32_t* seq_lens, int B, void* out,
@@ -433,6 +597,9 @@ static int attention_call(rq_ctx* ctx, const void* q, int T, const uint64_t* tre
     return RQ_ERR_CAPACITY;
   DeviceScope scope(ctx->device);
   if (!scope.ok()) return RQ_ERR_CUDA;
+  if (ctx->g.mode == RQ_FP8)
+    return block_attention(ctx, q, T, tree_mask, kv_pages, block_table, max_pages, seq_lens, B, out, d_status,
+                           (cudaStream_t)stream, k_new, v_new);
 
   rq::AttnArgs a;
   a.q = q;
@@ -482,6 +649,9 @@ int rq_extend_attention(rq_ctx* ctx, const void* q, int T, const void* kv_pages,
   if ((long long)T * ctx->g.group > INT32_MAX / 2) return RQ_ERR_CAPACITY;
   DeviceScope scope(ctx->device);
   if (!scope.ok()) return RQ_ERR_CUDA;
+  if (ctx->g.mode == RQ_FP8)
+    return block_attention(ctx, q, T, nullptr, kv_pages, block_table, max_pages, seq_lens, B, out, d_status,
+                           (cudaStream_t)stream, nullptr, nullptr);
   rq::AttnArgs a{};
   a.q = q;
   a.pages = (const uint8_t*)kv_pages;
@@ -509,6 +679,122 @@ int rq_decode_step(rq_ctx* ctx, const void* q, const void* k_new, const void* v_
 int rq_decode_attention(rq_ctx* ctx, const void* q, const void* kv_pages, const int32_t* block_table, int max_pages,
                         const int32_t* seq_lens, int B, void* out, int32_t* d_status, void* stream) {
   return attention_call(ctx, q, 1, nullptr, kv_pages, block_table, max_pages, seq_lens, B, out, d_status, stream);
+}
+
+int rq_rope_create(rq_rope** out, const rq_rope_config* cfg) {
+  if (!out) return RQ_ERR_INVALID;
+  *out = nullptr;
+  if (!cfg || cfg->rotary_dim < 0 || cfg->rotary_dim > rq::kHeadDim || cfg->rotary_dim % 8 != 0 ||
+      cfg->num_axes < 1 || cfg->num_axes > 8 || (cfg->rotary_dim > 0 && !cfg->inv_freq) || !std::isfinite(cfg->scale))
+    return RQ_ERR_INVALID;
+  const int pairs = cfg->rotary_dim / 2;
+  uint64_t host[rq::kHeadDim] = {};
+  for (int i = 0; i < pairs; ++i) {
+    const int axis = cfg->axis ? cfg->axis[i] : 0;
+    if (!(cfg->inv_freq[i] >= 0.0 && cfg->inv_freq[i] <= 65536.0) || axis < 0 || axis >= cfg->num_axes)
+      return RQ_ERR_INVALID;
+    host[2 * i] = turns_per_position(cfg->inv_freq[i]);
+    host[2 * i + 1] = (uint64_t)axis;
+  }
+  int dev = cfg->device;
+  if (dev < 0 && cudaGetDevice(&dev) != cudaSuccess) return RQ_ERR_CUDA;
+  DeviceScope scope(dev);
+  if (!scope.ok()) return RQ_ERR_CUDA;
+  rq_rope* r = new (std::nothrow) rq_rope();
+  if (!r) return RQ_ERR_CUDA;
+  cudaError_t e = cudaMalloc(&r->d_pairs, sizeof(host));
+  if (e == cudaSuccess) e = cudaMemcpy(r->d_pairs, host, sizeof(host), cudaMemcpyHostToDevice);
+  if (e != cudaSuccess) {
+    cudaFree(r->d_pairs);
+    delete r;
+    return RQ_ERR_CUDA;
+  }
+  r->device = dev;
+  r->table = rq::RopeTable{r->d_pairs, cfg->scale == 0.f ? 1.f : cfg->scale, cfg->rotary_dim, cfg->interleaved != 0};
+  *out = r;
+  return RQ_OK;
+}
+
+void rq_rope_free(rq_rope* rope) {
+  if (!rope) return;
+  {
+    DeviceScope scope(rope->device);
+    cudaFree(rope->d_pairs);
+  }
+  delete rope;
+}
+
+int rq_norm_rope(const rq_rope* rope, const rq_rows* q, const rq_rows* k, int io_type, float eps,
+                 const int32_t* positions, int n, void* stream) {
+  if (n < 0 || (!q && !k) || (io_type != RQ_F16 && io_type != RQ_BF16) || !(eps >= 0.f) || std::isinf(eps))
+    return RQ_ERR_INVALID;
+  if (n == 0) return RQ_OK;
+  if (check_rows(q, true) != RQ_OK || check_rows(k, true) != RQ_OK) return RQ_ERR_INVALID;
+  if (rope && rope->table.rotary_dim > 0 && !positions) return RQ_ERR_INVALID;
+  const rq_rows* rows[2] = {q, k};
+  for (int i = 0; i < 2; ++i) {
+    if (!rows[i]) continue;
+    const Span o = span(rows[i]->out, rows[i]->out_stride, rows[i]->heads, n);
+    if (overlap(o, span(rows[i]->x, rows[i]->stride, rows[i]->heads, n)) &&
+        !(rows[i]->out == rows[i]->x && (n == 1 || rows[i]->out_stride == rows[i]->stride)))
+      return RQ_ERR_INVALID;
+    const rq_rows* other = rows[1 - i];
+    if (other && (overlap(o, span(other->x, other->stride, other->heads, n)) ||
+                  overlap(o, span(other->out, other->out_stride, other->heads, n))))
+      return RQ_ERR_INVALID;
+  }
+  int dev = 0, sms = 0;
+  if (rope)
+    dev = rope->device;
+  else if (cudaGetDevice(&dev) != cudaSuccess)
+    return RQ_ERR_CUDA;
+  DeviceScope scope(dev);
+  if (!scope.ok() || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return RQ_ERR_CUDA;
+  rq::NormRopeArgs a{};
+  a.q = rows_dev(q);
+  a.k = rows_dev(k);
+  if (rope) a.rope = rope->table;
+  a.positions = positions;
+  a.n = n;
+  a.eps = eps;
+  a.bf16 = io_type == RQ_BF16;
+  return to_status(rq::launch_norm_rope(a, sms, (cudaStream_t)stream));
+}
+
+int rq_rope_append(rq_ctx* ctx, const rq_rope* rope, const rq_rows* q, const rq_rows* k, const void* v,
+                   long long v_stride, float eps, const int32_t* positions, const int32_t* slot_mapping, int n,
+                   void* kv_pages, int32_t* d_status, void* stream) {
+  if (!ctx || n < 0 || !(eps >= 0.f) || std::isinf(eps)) return RQ_ERR_INVALID;
+  if (ctx->g.mode != RQ_FP8) return RQ_ERR_UNSUPPORTED;
+  if (n == 0) return RQ_OK;
+  if (!k || !v || !slot_mapping || !kv_pages || misaligned16(v) || misaligned16(kv_pages)) return RQ_ERR_INVALID;
+  if (check_rows(q, true) != RQ_OK || check_rows(k, false) != RQ_OK) return RQ_ERR_INVALID;
+  const int hkv = ctx->g.num_kv_heads;
+  if (k->heads != hkv || v_stride < (long long)hkv * rq::kHeadDim || v_stride % 8 != 0 || v_stride > INT32_MAX)
+    return RQ_ERR_INVALID;
+  if (rope && ((rope->table.rotary_dim > 0 && !positions) || rope->device != ctx->device)) return RQ_ERR_INVALID;
+  if (q) {
+    const Span o = span(q->out, q->out_stride, q->heads, n);
+    if (overlap(o, span(q->x, q->stride, q->heads, n)) &&
+        !(q->out == q->x && (n == 1 || q->out_stride == q->stride)))
+      return RQ_ERR_INVALID;
+    if (overlap(o, span(k->x, k->stride, hkv, n)) || overlap(o, span(v, v_stride, hkv, n))) return RQ_ERR_INVALID;
+  }
+  DeviceScope scope(ctx->device);
+  if (!scope.ok()) return RQ_ERR_CUDA;
+  rq::BlockAppendArgs a{};
+  a.in.q = rows_dev(q);
+  a.in.k = rows_dev(k);
+  if (rope) a.in.rope = rope->table;
+  a.in.positions = positions;
+  a.in.n = n;
+  a.in.eps = eps;
+  a.v = v;
+  a.v_stride = v_stride;
+  a.slots = slot_mapping;
+  a.pages = (uint8_t*)kv_pages;
+  a.status = d_status;
+  return to_status(rq::launch_block_append(ctx->g, a, ctx->num_sms, (cudaStream_t)stream));
 }
 
 }  // extern "C"

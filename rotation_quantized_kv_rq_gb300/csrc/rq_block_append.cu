@@ -1,0 +1,304 @@
+// Append to the 8-bit block-scaled cache, with the key's norm and position rotation on the way and
+// the queries of the same tokens turned in the same launch.
+//
+// A block's key scale (and value scale) is 2^E with the smallest E that holds the largest magnitude
+// of its tokens.  Tokens arrive a few at a time, so E can only be known so far: the first token of
+// a block starts it anew, a later one raises it if it must, and the codes already there are then
+// divided by the power of two in place.  Codes are floating point, so that division is exact but
+// for codes it makes subnormal (below 2^-14 of the scale's largest value).
+//
+// Work is split by runs: consecutive tokens of the call in consecutive slots of one block.  One warp
+// codes a run's keys and values of one head, so that a block's scale is one reduction in one warp
+// and no atomics order anything; the run's tokens all belong to one block by construction, and two
+// runs of one call never share a block (include/rq.h asks for that).
+#include "../../include/rq.h"
+#include "rq_block.cuh"
+#include "rq_rope.cuh"
+
+namespace rq {
+namespace {
+
+using namespace rope;
+using namespace block;
+
+constexpr int kMaxWarps = 8;
+
+__device__ __forceinline__ bool finite(float x) { return (__float_as_uint(x) & 0x7F800000u) != 0x7F800000u; }
+
+__device__ __forceinline__ float warp_max(float x) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+  return x;
+}
+
+// Token t's slot, or -1: padding, past the call's end, or a fault (reported once, by `report`).
+__device__ __forceinline__ int slot_of(const Geometry& g, const BlockAppendArgs& a, long long t, bool report) {
+  if (t < 0 || t >= a.in.n) return -1;
+  int fault = 0, s;
+  if (a.slots != nullptr) {
+    s = __ldg(a.slots + t);
+    if (s >= g.num_pages * g.page_size) fault = RQ_STATUS_BAD_SLOT;
+  } else {
+    const int len = __ldg(a.seq_lens + t), cap = a.max_pages * g.page_size;
+    s = -1;
+    if (len < 0 || len > cap) {
+      fault = RQ_STATUS_BAD_LEN;
+    } else if (len > 0) {
+      const int page = __ldg(a.block_table + t * a.max_pages + (len - 1) / g.page_size);
+      if (page < 0 || page >= g.num_pages)
+        fault = RQ_STATUS_BAD_PAGE;
+      else
+        s = page * g.page_size + (len - 1) % g.page_size;
+    }
+  }
+  if (fault) {
+    if (report && a.status) atomicOr(a.status, fault);
+    return -1;
+  }
+  return s;
+}
+
+// Rows `off` .. off + cnt - 1 of a block's keys from tokens t0 .. (head h).  cs: cosines and sines
+// of token t0 + i at cs[i].  Returns the exponent; sets bad on a value that is not finite.
+template <typename T, bool INTERLEAVED>
+__device__ __forceinline__ int append_keys(const BlockAppendArgs& a, uint8_t* blk, int h, long long t0, int off,
+                                           int cnt, int e_old, const float4 (*cs)[2][16], int lane, bool& bad) {
+  const int j = lane & 15, half = lane >> 4;
+  const Lane l = lane_of<INTERLEAVED>(j, a.in.rope.rotary_dim);
+  const T* src = reinterpret_cast<const T*>(a.in.k.x) + (long long)h * kHeadDim;
+  uint2 raw[8][2];
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (2 * i + half < cnt) load8(raw[i], src + (t0 + 2 * i + half) * a.in.k.stride, l);
+  float x[8][8], top = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    if (2 * i + half < cnt) {
+      widen8<T>(x[i], raw[i]);
+      norm8(x[i], a.in.k.weight, a.in.eps, l);
+      if (l.pair >= 0) {
+        const float4 c0 = cs[2 * i + half][0][j], c1 = cs[2 * i + half][1][j];
+        const float2 p[4] = {make_float2(c0.x, c0.y), make_float2(c0.z, c0.w), make_float2(c1.x, c1.y),
+                             make_float2(c1.z, c1.w)};
+        turn8<INTERLEAVED>(x[i], p, l);
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        if (finite(x[i][k]))
+          top = fmaxf(top, fabsf(x[i][k]));
+        else
+          bad = true;
+      }
+    }
+  }
+  const int e_new = exp_of(warp_max(top)), e = off == 0 ? e_new : max(e_old, e_new);
+  if (off > 0 && e > e_old) {
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      uint4* p = reinterpret_cast<uint4*>(blk) + 32 * u + lane;
+      uint4 c = *p;
+      c.x = shrink4(c.x, e - e_old), c.y = shrink4(c.y, e - e_old);
+      c.z = shrink4(c.z, e - e_old), c.w = shrink4(c.w, e - e_old);
+      *p = c;
+    }
+    __syncwarp();  // the rows below overwrite some of these bytes
+  }
+  const float s = pow2(-e);
+  auto place = [&](int r, int d) { return ((2 * (r >> 3) + (d >> 6)) * 32 + (r & 7) * 4 + ((d & 63) >> 4)) * 16 + (d & 15); };
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    if (2 * i + half < cnt) {
+      const int r = off + 2 * i + half;
+      *reinterpret_cast<uint32_t*>(blk + place(r, l.o0)) = code4(x[i][0] * s, x[i][1] * s, x[i][2] * s, x[i][3] * s);
+      *reinterpret_cast<uint32_t*>(blk + place(r, l.o1)) = code4(x[i][4] * s, x[i][5] * s, x[i][6] * s, x[i][7] * s);
+    }
+  }
+  return e;
+}
+
+// The same of values: lane takes dims 4 lane .. 4 lane + 3 of every row, whose 64 bytes of a block
+// are its own; bytes of rows outside the run stay as they are.
+template <typename T>
+__device__ __forceinline__ int append_values(const BlockAppendArgs& a, uint8_t* blk, int h, long long t0, int off,
+                                             int cnt, int e_old, int lane, bool& bad) {
+  const T* src = reinterpret_cast<const T*>(a.v) + (long long)h * kHeadDim + 4 * lane;
+  uint2 raw[16];
+#pragma unroll
+  for (int r = 0; r < 16; ++r) {
+    raw[r] = make_uint2(0u, 0u);
+    if (r >= off && r < off + cnt) raw[r] = __ldg(reinterpret_cast<const uint2*>(src + (t0 + r - off) * a.v_stride));
+  }
+  float top = 0.f;
+#pragma unroll
+  for (int r = 0; r < 16; ++r) {
+    const float2 p = unpack2<T>(raw[r].x), q = unpack2<T>(raw[r].y);
+    const float x[4] = {p.x, p.y, q.x, q.y};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (finite(x[k]))
+        top = fmaxf(top, fabsf(x[k]));
+      else
+        bad = true;
+    }
+  }
+  const int e_new = exp_of(warp_max(top)), e = off == 0 ? e_new : max(e_old, e_new);
+  const bool grow = off > 0 && e > e_old;
+  const float s = pow2(-e);
+  uint4* const dst = reinterpret_cast<uint4*>(blk + kValues + 512 * (lane >> 3) + 64 * (lane & 7));
+#pragma unroll
+  for (int t = 0; t < 4; ++t) {
+    const int rows[4] = {2 * t, 2 * t + 1, 2 * t + 8, 2 * t + 9};
+    uint32_t w[4], mask = 0u;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float2 p = unpack2<T>(raw[rows[k]].x), q = unpack2<T>(raw[rows[k]].y);
+      w[k] = code4(p.x * s, p.y * s, q.x * s, q.y * s);  // one token, four dims
+      if (rows[k] >= off && rows[k] < off + cnt) mask |= 0xFFu << (8 * k);
+    }
+    if (mask == 0u && !grow) continue;
+    // to one dim, four tokens: a 4 x 4 transpose of bytes
+    const uint32_t a0 = __byte_perm(w[0], w[1], 0x5140), a1 = __byte_perm(w[2], w[3], 0x5140);
+    const uint32_t b0 = __byte_perm(w[0], w[1], 0x7362), b1 = __byte_perm(w[2], w[3], 0x7362);
+    uint4 c = make_uint4(__byte_perm(a0, a1, 0x5410), __byte_perm(a0, a1, 0x7632), __byte_perm(b0, b1, 0x5410),
+                         __byte_perm(b0, b1, 0x7632));
+    if (mask != 0xFFFFFFFFu) {
+      uint4 o = dst[t];
+      if (grow) {
+        o.x = shrink4(o.x, e - e_old), o.y = shrink4(o.y, e - e_old);
+        o.z = shrink4(o.z, e - e_old), o.w = shrink4(o.w, e - e_old);
+      }
+      c.x = (c.x & mask) | (o.x & ~mask), c.y = (c.y & mask) | (o.y & ~mask);
+      c.z = (c.z & mask) | (o.z & ~mask), c.w = (c.w & mask) | (o.w & ~mask);
+    }
+    dst[t] = c;
+  }
+  return e;
+}
+
+// A CTA takes the runs that start among its W tokens, and those W tokens' queries.  W = 1 spreads a
+// decode step's single tokens over the SMs; W = 16 (long appends) makes one block of a run a
+// CTA's work.  blockIdx.y splits the heads.
+template <typename T, bool INTERLEAVED, int W>
+__global__ void __launch_bounds__(32 * kMaxWarps) block_append_kernel(const Geometry g, const BlockAppendArgs a) {
+  constexpr int kTokens = W == 1 ? 16 : 32;  // a run reaches at most 15 tokens past its first
+  __shared__ float4 cs[kTokens][2][16];  // [token][c][j]: pairs 4j + 2c and 4j + 2c + 1
+  __shared__ int run_at[W], run_cnt[W], run_slot[W], num_runs, reach;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
+  const long long base = (long long)blockIdx.x * W;
+  if (warp == 0) {
+    const int s = lane < kTokens ? slot_of(g, a, base + lane, lane < W && blockIdx.y == 0) : -1;
+    int prev = __shfl_up_sync(0xffffffffu, s, 1);
+    if (lane == 0) prev = slot_of(g, a, base - 1, false);
+    const bool cont = s >= 0 && s % kBlockTokens != 0 && prev == s - 1;
+    const uint32_t conts = __ballot_sync(0xffffffffu, cont);
+    const uint32_t leads = __ballot_sync(0xffffffffu, lane < W && s >= 0 && !cont);
+    int cnt = 0;
+    if (leads >> lane & 1) {
+      const uint32_t after = lane < 31 ? conts >> (lane + 1) : 0u;
+      cnt = __ffs(~after);  // 1 + the tokens that continue it
+      const int i = __popc(leads & ((1u << lane) - 1u));
+      run_at[i] = lane, run_cnt[i] = cnt, run_slot[i] = s;
+    }
+    const int ends = __reduce_max_sync(0xffffffffu, cnt > 0 ? lane + cnt : 0);
+    if (lane == 0) {
+      num_runs = __popc(leads);
+      reach = max(ends, a.in.q.heads > 0 ? (int)min((long long)W, a.in.n - base) : 0);
+    }
+  }
+  __syncthreads();
+  const int hw = tid >> 4, hws = blockDim.x >> 4, j = tid & 15;
+  if (a.in.rope.rotary_dim > 0) {
+    if (4 * j < a.in.rope.rotary_dim >> 1) {
+      for (int i = hw; i < reach; i += hws) {
+        float2 p[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) p[k] = cos_sin(a.in.rope, 4 * j + k, a.in.positions, a.in.n, base + i);
+        cs[i][0][j] = make_float4(p[0].x, p[0].y, p[1].x, p[1].y);
+        cs[i][1][j] = make_float4(p[2].x, p[2].y, p[3].x, p[3].y);
+      }
+    }
+    __syncthreads();
+  }
+
+  bool bad = false;
+  const int items = num_runs * g.num_kv_heads;
+  for (int it = blockIdx.y * warps + warp; it < items; it += gridDim.y * warps) {
+    const int run = it / g.num_kv_heads, h = it % g.num_kv_heads;
+    const int at = run_at[run], cnt = run_cnt[run], slot = run_slot[run], off = slot % kBlockTokens;
+    uint8_t* blk = a.pages + ((size_t)(slot / g.page_size) * g.num_kv_heads + h) * g.page_bytes +
+                   (size_t)(slot % g.page_size / kBlockTokens) * kBlockBytes;
+    const uint32_t old = off > 0 ? *reinterpret_cast<const uint16_t*>(blk + kExps) : 0u;
+    const int ek_old = exp_of_byte(old & 0xFF), ev_old = exp_of_byte(old >> 8);
+    const int ek = append_keys<T, INTERLEAVED>(a, blk, h, base + at, off, cnt, ek_old, cs + at, lane, bad);
+    const int ev = append_values<T>(a, blk, h, base + at, off, cnt, ev_old, lane, bad);
+    if (lane == 0) *reinterpret_cast<uint16_t*>(blk + kExps) = (uint16_t)((ek + 127) | (ev + 127) << 8);
+  }
+  if (bad && a.status) atomicOr(a.status, RQ_STATUS_NOT_FINITE);
+
+  if (a.in.q.heads > 0) {
+    const Lane l = lane_of<INTERLEAVED>(j, a.in.rope.rotary_dim);
+    // W = 16: a half-warp takes a token's heads; W = 1: the half-warps share the token's heads
+    const int i0 = W == 1 ? 0 : hw, h0 = W == 1 ? blockIdx.y * hws + hw : blockIdx.y;
+    const int hstep = W == 1 ? gridDim.y * hws : gridDim.y;
+    for (int i = i0; i < W && base + i < a.in.n; i += hws) {
+      float2 p[4];
+      if (l.pair >= 0) {
+        const float4 c0 = cs[i][0][j], c1 = cs[i][1][j];
+        p[0] = make_float2(c0.x, c0.y), p[1] = make_float2(c0.z, c0.w);
+        p[2] = make_float2(c1.x, c1.y), p[3] = make_float2(c1.z, c1.w);
+      }
+      const T* src = reinterpret_cast<const T*>(a.in.q.x) + (base + i) * a.in.q.stride;
+      T* dst = reinterpret_cast<T*>(a.in.q.out) + (base + i) * a.in.q.out_stride;
+      for (int h = h0; h < a.in.q.heads; h += 4 * hstep) {
+        uint2 raw[4][2];
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          if (h + u * hstep < a.in.q.heads) load8(raw[u], src + (long long)(h + u * hstep) * kHeadDim, l);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          if (h + u * hstep >= a.in.q.heads) break;
+          float x[8];
+          widen8<T>(x, raw[u]);
+          norm8(x, a.in.q.weight, a.in.eps, l);
+          turn8<INTERLEAVED>(x, p, l);
+          store8(dst + (long long)(h + u * hstep) * kHeadDim, x, l);
+        }
+      }
+    }
+  }
+}
+
+template <typename T, bool INTERLEAVED>
+void launch(const Geometry& g, const BlockAppendArgs& a, int num_sms, cudaStream_t stream) {
+  const int hkv = g.num_kv_heads, hq = a.in.q.heads;
+  int warps = hkv < 2 ? 2 : (hkv > kMaxWarps ? kMaxWarps : hkv);
+  if (a.in.n < 16LL * num_sms * 2) {  // too few tokens for every SM to have two CTAs of 16
+    if (hq > 0) warps = kMaxWarps;
+    const int most = max((hkv + warps - 1) / warps, (hq + 2 * warps - 1) / (2 * warps));
+    long long split = (2LL * num_sms + a.in.n - 1) / a.in.n;
+    split = split > most ? most : split;
+    block_append_kernel<T, INTERLEAVED, 1><<<dim3((unsigned)a.in.n, (unsigned)split), 32 * warps, 0, stream>>>(g, a);
+  } else {
+    block_append_kernel<T, INTERLEAVED, 16><<<dim3((unsigned)((a.in.n + 15) / 16), 1), 32 * warps, 0, stream>>>(g, a);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_block_append(const Geometry& g, const BlockAppendArgs& a, int num_sms, cudaStream_t stream) {
+  if (a.in.n <= 0) return cudaSuccess;
+  if (g.bf16) {
+    if (a.in.rope.interleaved)
+      launch<__nv_bfloat16, true>(g, a, num_sms, stream);
+    else
+      launch<__nv_bfloat16, false>(g, a, num_sms, stream);
+  } else {
+    if (a.in.rope.interleaved)
+      launch<__half, true>(g, a, num_sms, stream);
+    else
+      launch<__half, false>(g, a, num_sms, stream);
+  }
+  return cudaGetLastError();
+}
+
+}  // namespace rq

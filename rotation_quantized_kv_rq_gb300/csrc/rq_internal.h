@@ -26,8 +26,9 @@ struct Geometry {
   int num_q_heads;
   int num_kv_heads;
   int group;           // Hq / Hkv
-  int bits;            // 2, 3 or 4
-  int mode;            // 0 planar, 1 iso, 2 dense
+  int bits;            // 2, 3 or 4; 8 for the 8-bit cache
+  int mode;            // 0 planar, 1 iso, 2 dense, 8 the 8-bit block-scaled cache
+  int bf16;            // 8-bit cache: q, k, v and out are bf16 (else fp16)
   int page_size;
   int num_pages;
   int vec_bytes;       // head_dim * bits / 8
@@ -37,6 +38,7 @@ struct Geometry {
   // the final normalisation carry it back, so the results are those of c.
   float q_scale;       // sm_scale * log2(e) * out_scale: scores are kept in base 2
   float out_scale;     // multiplies every attention output row (with its 1 / sum of p)
+  float sm_scale;      // 8-bit cache: the softmax scale
   // planar / iso: device [Hkv][128] rotation parameters.
   // dense: rot_k = device [Hkv][128][128] R_k TRANSPOSED (query rotation reads it column-wise),
   //        rot_v = device [Hkv][128][128] R_v (output rotation R_v^T o reads it row-wise).
@@ -124,6 +126,59 @@ inline void attention_workspace(long long B, int hkv, int n_tiles, bool step, in
   *units = B * hkv * ((n_tiles + nt - 1) / nt);
   *partial_floats = (*units + grid) * 8LL * nt * kPartialStride;
 }
+
+// ---- the 8-bit block-scaled cache (RQ_FP8) and the position rotation ----
+
+constexpr int kBlockTokens = 16;    // tokens that share a key scale and a value scale
+constexpr int kBlockBytes = 4112;   // 2048 key codes, 2048 value codes, 2 exponent bytes, 14 unused
+constexpr int kMinExp = -60, kMaxExp = 60;  // scales are 2^kMinExp .. 2^kMaxExp
+
+// Device view of an rq_rope.
+struct RopeTable {
+  const uint64_t* pairs;  // device [rotary_dim / 2][2]: turns per position * 2^64, the pair's axis
+  float scale;            // multiplies cos and sin
+  int rotary_dim;         // 0: no rotation
+  int interleaved;
+};
+
+// Rows of one of the q / k tensors: token t, head h at x + t * stride + h * 128 (elements).
+struct RowsDev {
+  const void* x;
+  long long stride;
+  const float* weight;  // f32 [128], or null: no norm
+  void* out;
+  long long out_stride;
+  int heads;
+};
+
+struct NormRopeArgs {
+  RowsDev q, k;  // heads 0: absent
+  RopeTable rope;
+  const int32_t* positions;  // [axes][n]
+  long long n;
+  float eps;
+  int bf16;
+};
+cudaError_t launch_norm_rope(const NormRopeArgs& a, int num_sms, cudaStream_t stream);
+
+// Append to the 8-bit cache.  Token t goes to slots[t], or, when slots is null, to position
+// seq_lens[t] - 1 of sequence t of the block table (a decode step).
+struct BlockAppendArgs {
+  NormRopeArgs in;  // q is turned into q.out (heads 0: none); k is coded
+  const void* v;
+  long long v_stride;
+  const int32_t* slots;
+  const int32_t* block_table;
+  int max_pages;
+  const int32_t* seq_lens;
+  uint8_t* pages;
+  int32_t* status;
+};
+cudaError_t launch_block_append(const Geometry& g, const BlockAppendArgs& a, int num_sms, cudaStream_t stream);
+
+// Attention over the 8-bit cache; the AttnArgs fields of the split-K kernel's planning are unused.
+cudaError_t launch_block_attention(const Geometry& g, const AttnArgs& a, cudaStream_t stream, cudaEvent_t ev_start,
+                                   cudaEvent_t ev_end);
 
 // Dynamic shared memory the attention kernel needs (set as the kernel's maximum once).
 size_t attention_smem_bytes();

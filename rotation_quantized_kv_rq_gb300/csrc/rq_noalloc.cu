@@ -65,10 +65,10 @@ extern "C" int rq_decode_attention_noalloc(const rq_config* cfg, const float* d_
   if (!cfg || B < 0 || max_pages < 1) return RQ_ERR_INVALID;
   if (cfg->num_q_heads <= 0 || cfg->num_kv_heads <= 0 || cfg->page_size <= 0 || cfg->num_pages <= 0 ||
       cfg->num_q_heads % cfg->num_kv_heads != 0 ||
-      (cfg->mode != RQ_PLANAR && cfg->mode != RQ_ISO && cfg->mode != RQ_DENSE) ||
+      (cfg->mode != RQ_PLANAR && cfg->mode != RQ_ISO && cfg->mode != RQ_DENSE && cfg->mode != RQ_FP8) ||
       !(cfg->sm_scale >= 0.0f) || std::isinf(cfg->sm_scale))
     return RQ_ERR_INVALID;
-  if (cfg->mode == RQ_DENSE) return RQ_ERR_UNSUPPORTED;  // its query rotation needs a workspace
+  if (cfg->mode == RQ_DENSE || cfg->mode == RQ_FP8) return RQ_ERR_UNSUPPORTED;  // RQ_DENSE's query rotation needs a workspace
   if (cfg->head_dim != rq::kHeadDim || cfg->bits < 2 || cfg->bits > 4 || cfg->page_size % 16 != 0 ||
       cfg->page_size > 256 || (long long)cfg->num_kv_heads * cfg->page_size * (2 * 16 * cfg->bits + 4) > INT32_MAX)
     return RQ_ERR_UNSUPPORTED;

@@ -1,0 +1,80 @@
+// Norms of queries and keys per head with the position rotation, in one pass over the rows.
+#include "rq_rope.cuh"
+
+namespace rq {
+namespace {
+
+using namespace rope;
+
+constexpr int kThreads = 256;
+constexpr int kBatch = 4;  // rows a half-warp has in flight
+
+// A half-warp takes `per` rows of one token (rows part, part + parts, ...: neighbouring half-warps
+// read neighbouring rows), so that the token's cosines and sines, in registers, serve all of them.
+// Loads of kBatch rows are in flight together.  In place is safe: a row is read by the half-warp
+// that writes it, before it writes.
+template <typename T, bool INTERLEAVED>
+__global__ void __launch_bounds__(kThreads) norm_rope_kernel(const NormRopeArgs a, int parts) {
+  const int j = threadIdx.x & 15;
+  const long long hw = ((long long)blockIdx.x * kThreads + threadIdx.x) >> 4;
+  const long long t = hw / parts;
+  if (t >= a.n) return;  // whole half-warps; the shuffles pair lanes of one half-warp
+  const int part = (int)(hw % parts), rows = a.q.heads + a.k.heads;
+  const Lane l = lane_of<INTERLEAVED>(j, a.rope.rotary_dim);
+  float2 cs[4];
+  if (l.pair >= 0) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) cs[i] = cos_sin(a.rope, l.pair + i, a.positions, a.n, t);
+  }
+  for (int r0 = part; r0 < rows; r0 += kBatch * parts) {
+    uint2 raw[kBatch][2];
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int r = r0 + u * parts;
+      if (r >= rows) break;
+      const RowsDev& s = r < a.q.heads ? a.q : a.k;
+      const int h = r < a.q.heads ? r : r - a.q.heads;
+      load8(raw[u], reinterpret_cast<const T*>(s.x) + t * s.stride + (long long)h * kHeadDim, l);
+    }
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int r = r0 + u * parts;
+      if (r >= rows) break;
+      const RowsDev& s = r < a.q.heads ? a.q : a.k;
+      const int h = r < a.q.heads ? r : r - a.q.heads;
+      float x[8];
+      widen8<T>(x, raw[u]);
+      norm8(x, s.weight, a.eps, l);
+      turn8<INTERLEAVED>(x, cs, l);
+      store8(reinterpret_cast<T*>(s.out) + t * s.out_stride + (long long)h * kHeadDim, x, l);
+    }
+  }
+}
+
+template <typename T>
+cudaError_t launch(const NormRopeArgs& a, int parts, unsigned ctas, cudaStream_t stream) {
+  if (a.rope.interleaved)
+    norm_rope_kernel<T, true><<<ctas, kThreads, 0, stream>>>(a, parts);
+  else
+    norm_rope_kernel<T, false><<<ctas, kThreads, 0, stream>>>(a, parts);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_norm_rope(const NormRopeArgs& a, int num_sms, cudaStream_t stream) {
+  const int rows = a.q.heads + a.k.heads;
+  // the fewest parts per token (the most rows behind one set of cosines) that still give every SM
+  // eight CTAs' half-warps
+  const long long want = (long long)num_sms * 8 * (kThreads / 16);
+  int parts = (int)((want + a.n - 1) / a.n);
+  const int most = (rows + kBatch - 1) / kBatch;
+  parts = parts > rows ? rows : (parts < 1 ? 1 : parts);
+  if (parts > most && a.n * (long long)most >= num_sms * 16) parts = most;
+  const long long ctas = (a.n * (long long)parts * 16 + kThreads - 1) / kThreads;
+  if (ctas > 0x7fffffffLL) return cudaErrorInvalidValue;
+  return a.bf16 ? launch<__nv_bfloat16>(a, parts, (unsigned)ctas, stream)
+                : launch<__half>(a, parts, (unsigned)ctas, stream);
+}
+
+}  // namespace rq
