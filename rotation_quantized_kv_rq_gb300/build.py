@@ -15,7 +15,7 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "librq.so")
 SOURCES = ["rq_api.cpp", "rq_append.cu", "rq_attention.cu", "rq_extend.cu", "rq_noalloc.cu", "rq_rope.cu",
-           "rq_block_append.cu", "rq_block_attention.cu"]
+           "rq_block_append.cu", "rq_block_attention.cu", "rq_block_extend.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall"]
 

@@ -141,7 +141,7 @@ int check_geometry(const rq_config* c) {
   return check_sizes(c, (long long)c->page_size * (2 * 16 * c->bits + 4));
 }
 
-// Creation of an RQ_FP8 context, on the current device: no tables.
+// Creation of an RQ_FP8 context, on the current device: no tables, the attention workspace alone.
 int create_block(rq_ctx* ctx, const rq_config* cfg) {
   rq::Geometry& g = ctx->g;
   g.num_q_heads = cfg->num_q_heads;
@@ -155,6 +155,17 @@ int create_block(rq_ctx* ctx, const rq_config* cfg) {
   g.vec_bytes = cfg->head_dim;
   g.page_bytes = cfg->page_size / 16 * rq::kBlockBytes;
   g.sm_scale = cfg->sm_scale > 0.f ? cfg->sm_scale : (float)(1.0 / std::sqrt((double)cfg->head_dim));
+  size_t counters = 0;
+  ctx->ws_floats = rq::block_attention_workspace(ctx->num_sms, &counters);
+  cudaError_t e = cudaMalloc(&ctx->d_ws, ctx->ws_floats * sizeof(float));
+  if (e == cudaSuccess) e = cudaMalloc(&ctx->d_frag, counters * sizeof(int));
+  if (e == cudaSuccess) e = cudaMemset(ctx->d_frag, 0, counters * sizeof(int));  // as every launch leaves them
+  if (e == cudaSuccess) e = rq::block_attention_prepare();
+  if (e != cudaSuccess) {
+    cudaFree(ctx->d_ws);
+    cudaFree(ctx->d_frag);
+    return RQ_ERR_CUDA;
+  }
   return RQ_OK;
 }
 
@@ -555,7 +566,8 @@ int rq_quantize_append(rq_ctx* ctx, const void* k, const void* v, const int32_t*
 // An attention call of an RQ_FP8 context, its arguments checked and its device current.
 static int block_attention(rq_ctx* ctx, const void* q, int T, const uint64_t* tree_mask, const void* kv_pages,
                            const int32_t* block_table, int max_pages, const int32_t* seq_lens, int B, void* out,
-                           int32_t* d_status, cudaStream_t stream, const void* k_new, const void* v_new) {
+                           int32_t* d_status, cudaStream_t stream, const void* k_new, const void* v_new,
+                           bool extend) {
   if (k_new) {
     rq::BlockAppendArgs n{};
     n.in.k.x = k_new;
@@ -583,7 +595,10 @@ static int block_attention(rq_ctx* ctx, const void* q, int T, const uint64_t* tr
   a.status = d_status;
   a.tree_mask = tree_mask;
   a.rows = T * ctx->g.group;
-  return to_status(rq::launch_block_attention(ctx->g, a, stream, ctx->prof_start, ctx->prof_end));
+  if (extend) return to_status(rq::launch_block_extend(ctx->g, a, stream, ctx->prof_start, ctx->prof_end));
+  a.ws = ctx->d_ws;
+  a.cnt = ctx->d_frag;
+  return to_status(rq::launch_block_attention(ctx->g, a, ctx->num_sms, stream, ctx->prof_start, ctx->prof_end));
 }
 
 static int attention_call(rq_ctx* ctx, const void* q, int T, const uint64_t* tree_mask, const void* kv_pages,
@@ -599,7 +614,7 @@ static int attention_call(rq_ctx* ctx, const void* q, int T, const uint64_t* tre
   if (!scope.ok()) return RQ_ERR_CUDA;
   if (ctx->g.mode == RQ_FP8)
     return block_attention(ctx, q, T, tree_mask, kv_pages, block_table, max_pages, seq_lens, B, out, d_status,
-                           (cudaStream_t)stream, k_new, v_new);
+                           (cudaStream_t)stream, k_new, v_new, false);
 
   rq::AttnArgs a;
   a.q = q;
@@ -651,7 +666,7 @@ int rq_extend_attention(rq_ctx* ctx, const void* q, int T, const void* kv_pages,
   if (!scope.ok()) return RQ_ERR_CUDA;
   if (ctx->g.mode == RQ_FP8)
     return block_attention(ctx, q, T, nullptr, kv_pages, block_table, max_pages, seq_lens, B, out, d_status,
-                           (cudaStream_t)stream, nullptr, nullptr);
+                           (cudaStream_t)stream, nullptr, nullptr, true);
   rq::AttnArgs a{};
   a.q = q;
   a.pages = (const uint8_t*)kv_pages;

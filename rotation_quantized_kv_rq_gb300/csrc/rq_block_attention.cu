@@ -1,110 +1,573 @@
-// Attention over the 8-bit block-scaled cache.
+// Attention over the 8-bit block-scaled cache: decode, chain verify and tree verify.
+//
+//   out = softmax(sm_scale q K^T) V,  K = code * 2^EK, V = code * 2^EV (a block's exponents)
+//
+// For a tile of 16 tokens (one block) and 8 query rows of a kv head, with e4m3 codes widened to
+// fp16 (exact) as the A operands of m16n8k16 MMAs and f32 accumulators:
+//   S^T = code_K q^T;   t = S 2^EK sm_scale log2(e) + EV - m;   w = 2^t
+//   O^T += code_V^T w;   l += w 2^-EV;   out = O / l
+// The value scale is part of the weight's exponent, so codes are never multiplied by it, and m is
+// the running maximum of score + EV: w, rounded to fp16 for the MMA (2^-11 of it), is then largest
+// where a token weighs most in the output, whatever the scales.  m moves only past a margin of
+// 2^8.  Queries are fp16 as they are; a bf16 row is brought into fp16's range by a power of two.
+//
+// What bounds it: the cache is read once, 257 bytes a (token, kv head), against 4 MMAs' worth of
+// work; so the design keeps copies in flight.  A block is one 4112-byte bulk copy into a ring of
+// the warp's own, no thread of the CTA waits for another inside a fragment, and four CTAs of four
+// warps share an SM (48 tiles in flight), so that one's opening and joining hide behind the
+// others' copies.  Rows of a kv head beyond 8 (group > 8, verify) share the widened tile: up to
+// three n-tiles of 8 rows a warp (one CTA less per SM for each).
+//
+// Work is cut evenly: a unit is (sequence, kv head, group of n-tiles) and costs one round per four
+// tiles; the rounds of all units in order are cut into one range per CTA, on the device from
+// seq_lens.  A unit that spans ranges is joined by the last of its CTAs to finish, in the order of
+// the ranges (the result does not depend on which came last).  A CTA has at most two such
+// fragments, its first and its last, so the workspace is two slots and one counter a CTA.
 #include <math_constants.h>
+
+#include <type_traits>
 
 #include "../../include/rq.h"
 #include "rq_block.cuh"
 #include "rq_rope.cuh"
+#include "rq_tc.cuh"
 
 namespace rq {
 namespace {
 
 using namespace block;
 
-constexpr int kWarps = 4;
+constexpr int kWarps = 4, kThreads = 32 * kWarps;
+constexpr float kMargin = 8.f;      // log2 slack of the running maximum
+constexpr float kNone = -1e30f;     // running maximum before any visible token
+constexpr int kRowStride = 132;     // floats per joined row (128 and padding)
 
-// One CTA per (sequence, query row): its warps take every fourth block of 16 tokens, each with a
-// running maximum and sum, and are joined at the end.  Scores: lane (half, token) sums 64 dims.
-template <typename T>
-__global__ void __launch_bounds__(32 * kWarps) rows_kernel(const Geometry g, const AttnArgs a) {
-  __shared__ float q[kHeadDim], part[kWarps][kHeadDim], ms[kWarps], ls[kWarps];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const long long row = blockIdx.x;  // (b, j, head)
-  const int head = (int)(row % g.num_q_heads), b = (int)(row / g.num_q_heads / a.T);
-  const int j = (int)(row / g.num_q_heads % a.T), h = head / g.group;
-  const int cap = a.max_pages * g.page_size;
-  int len = a.seq_lens[b];
-  if (len < 0 || len > cap || (len > 0 && len < a.T)) {
-    if (tid == 0 && a.status) atomicOr(a.status, RQ_STATUS_BAD_LEN);
-    len = len < 0 ? 0 : min(len, cap);
-  }
-  const T* src = reinterpret_cast<const T*>(a.q) + row * kHeadDim;
-  q[tid] = (float)src[tid] * (g.sm_scale * 1.44269504088896340736f);
-  __syncthreads();
-  const int prefix = len - a.T;  // position of draft 0
-  const uint64_t mask = a.tree_mask ? a.tree_mask[(size_t)b * a.T + j] : 0;
-  const int end = a.tree_mask ? len : min(len, prefix + j + 1);
-  const int r = lane & 15, half = lane >> 4;
-  float m = -CUDART_INF_F, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-  for (int t0 = kBlockTokens * warp; t0 < end; t0 += kBlockTokens * kWarps) {
-    int page = a.block_table[(size_t)b * a.max_pages + t0 / g.page_size];
-    if (page < 0 || page >= g.num_pages) {
-      if (lane == 0 && a.status) atomicOr(a.status, RQ_STATUS_BAD_PAGE);
-      page = 0;
+__host__ __device__ constexpr int ctas_per_sm(int nt) { return nt == 1 ? 4 : nt == 2 ? 3 : 2; }
+__host__ __device__ constexpr int stages(int nt) { return nt == 1 ? 3 : nt == 2 ? 4 : 6; }  // tiles of a warp's ring
+constexpr int ring_bytes(int nt) { return kWarps * stages(nt) * kBlockBytes; }
+constexpr int smem_bytes(int nt) { return ring_bytes(nt) + kWarps * stages(nt) * 8; }
+
+__device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                    uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_t bar) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(kBlockBytes) : "memory");
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(kBlockBytes), "r"(bar)
+               : "memory");
+}
+__device__ __forceinline__ bool bounded_wait(uint32_t bar, uint32_t parity) {
+  for (int i = 0; i < tc::kWaitLimit; ++i)
+    if (tc::mbar_test(bar, parity)) return true;
+  return false;
+}
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ uint32_t word(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
+// 1.0 in fp16 for each of the two codes that is NaN, else 0
+__device__ __forceinline__ uint32_t nan2(uint32_t codes) {
+  return ((codes & 0x7Fu) == 0x7Fu ? 0x3C00u : 0u) | ((codes & 0x7F00u) == 0x7F00u ? 0x3C000000u : 0u);
+}
+// the codes with NaNs replaced by 0
+__device__ __forceinline__ uint32_t without_nan4(uint32_t codes) {
+  const uint32_t is = __vcmpeq4(codes & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+  return codes & ~is;
+}
+
+// The partition: rounds of sequence b's units, and the sums over sequences.
+struct Plan {
+  int tiles, rounds;
+};
+__device__ __forceinline__ Plan plan_of(int len) {
+  Plan p;
+  p.tiles = (len + kBlockTokens - 1) / kBlockTokens;
+  p.rounds = max(1, (p.tiles + kWarps - 1) / kWarps);  // an empty sequence's rows are written too
+  return p;
+}
+
+template <int NT, typename T>
+__global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) splitk_kernel(const Geometry g, const AttnArgs a) {
+  constexpr int S = stages(NT), kRows = 8 * NT;
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ long long s_scan[kThreads];
+  __shared__ long long s_begin;  // first sequence's rounds before it (all units), and its index
+  __shared__ int s_seq, s_last;
+  __shared__ float s_m[kWarps][kRows], s_l[kWarps][kRows];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, gq = lane >> 2, tq = lane & 3;
+  const int cap = a.max_pages * g.page_size, groups = (a.n_tiles_n + NT - 1) / NT;
+  const int per_seq = g.num_kv_heads * groups;  // units of a sequence
+
+  auto length = [&](int b, bool report) {
+    int len = __ldg(a.seq_lens + b);
+    if (len < 0 || len > cap || (len > 0 && len < a.T)) {
+      if (report && a.status) atomicOr(a.status, RQ_STATUS_BAD_LEN);
+      len = len < 0 ? 0 : min(len, cap);
     }
-    const uint8_t* blk = a.pages + ((size_t)page * g.num_kv_heads + h) * g.page_bytes +
-                         (size_t)(t0 % g.page_size / kBlockTokens) * kBlockBytes;
-    const float ek = pow2(exp_of_byte(blk[kExps])), ev = pow2(exp_of_byte(blk[kExps + 1]));
-    float s = 0.f;
-    for (int u = 0; u < 4; ++u) {
-      const uint4 c = reinterpret_cast<const uint4*>(blk)[(2 * (r >> 3) + half) * 32 + (r & 7) * 4 + u];
-      const uint32_t w[4] = {c.x, c.y, c.z, c.w};
-      for (int k = 0; k < 4; ++k) {
-        const float2 x = rope::unpack2<__half>(widen2(w[k])), y = rope::unpack2<__half>(widen2_hi(w[k]));
-        const float* qq = q + 64 * half + 16 * u + 4 * k;
-        s += x.x * qq[0] + x.y * qq[1] + y.x * qq[2] + y.y * qq[3];
+    return len;
+  };
+
+  // ---- the CTA's range of rounds ----
+  const int chunk = (a.B + kThreads - 1) / kThreads;
+  long long mine = 0;
+  for (int b = tid * chunk; b < min(a.B, (tid + 1) * chunk); ++b) mine += plan_of(length(b, blockIdx.x == 0)).rounds;
+  s_scan[tid] = mine;
+  const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem) + warp * S * kBlockBytes;
+  const uint32_t bars = (uint32_t)__cvta_generic_to_shared(smem) + kWarps * S * kBlockBytes + warp * S * 8;
+  if (lane == 0) {
+    for (int i = 0; i < S; ++i) tc::mbar_init(bars + 8 * i, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  __syncthreads();
+  for (int o = 1; o < kThreads; o <<= 1) {  // inclusive scan
+    const long long v = tid >= o ? s_scan[tid - o] : 0;
+    __syncthreads();
+    s_scan[tid] += v;
+    __syncthreads();
+  }
+  const long long total = s_scan[kThreads - 1] * per_seq;
+  const long long parts = min((long long)gridDim.x, total);
+  if ((long long)blockIdx.x >= parts) return;
+  auto part_begin = [&](long long c) { return c * total / parts; };
+  auto part_of = [&](long long x) { return ((x + 1) * parts - 1) / total; };  // the range that holds round x
+  long long x = part_begin(blockIdx.x);
+  const long long end = part_begin(blockIdx.x + 1ll);
+  {
+    const long long before = (s_scan[tid] - mine) * per_seq;
+    if (x >= before && x < s_scan[tid] * per_seq) {
+      long long at = before;
+      int b = tid * chunk;
+      for (;; ++b) {
+        const long long r = (long long)plan_of(length(b, false)).rounds * per_seq;
+        if (x < at + r) break;
+        at += r;
+      }
+      s_begin = at;
+      s_seq = b;
+    }
+  }
+  __syncthreads();
+  long long at = s_begin;
+  int b = s_seq;
+
+  uint32_t issued = 0, done = 0;  // tiles of this warp so far: ring positions and parities
+  bool failed = false;
+  while (x < end) {
+    // ---- the fragment: rounds r0 .. r1 - 1 of unit u of sequence b ----
+    const int len = length(b, false);
+    const Plan pl = plan_of(len);
+    const int u = (int)((x - at) / pl.rounds), r0 = (int)((x - at) % pl.rounds);
+    const int r1 = (int)min((long long)pl.rounds, r0 + (end - x));
+    const int h = u / groups, row0 = (u % groups) * kRows;
+    const int first = r0 * kWarps + warp;  // the warp's tiles: first, first + kWarps, ...
+    const int last = min(pl.tiles, r1 * kWarps);
+    const int count = first < last ? (last - first + kWarps - 1) / kWarps : 0;
+    const int32_t* table = a.block_table + (size_t)b * a.max_pages;
+
+    // page of tile first + kWarps * i, for i in the lane's place of the current and next 32
+    auto page_at = [&](int i) {
+      if (i >= count) return 0;
+      int page = __ldg(table + (first + kWarps * i) * kBlockTokens / g.page_size);
+      if (page < 0 || page >= g.num_pages) {
+        if (a.status) atomicOr(a.status, RQ_STATUS_BAD_PAGE);
+        page = 0;
+      }
+      return page;
+    };
+    int pages_now = page_at(lane), pages_next = page_at(32 + lane);
+    int batch = 0;
+    auto issue = [&](int i) {  // tile i of the warp, by the whole warp
+      if ((i >> 5) != batch) {
+        batch = i >> 5;
+        pages_now = pages_next;
+        pages_next = page_at(32 * (batch + 1) + lane);
+      }
+      const int page = __shfl_sync(0xffffffffu, pages_now, i & 31);
+      if (lane == 0) {
+        const int in_page = (first + kWarps * i) * kBlockTokens % g.page_size / kBlockTokens;
+        const uint32_t s = issued % S;
+        bulk_copy(ring + s * kBlockBytes,
+                  a.pages + ((size_t)page * g.num_kv_heads + h) * g.page_bytes + (size_t)in_page * kBlockBytes, bars + 8 * s);
+      }
+      ++issued;
+    };
+    if (!failed)
+      for (int i = 0; i < min(S, count); ++i) issue(i);
+
+    // ---- queries: B fragments, lane (row gq, dims 64 (ks / 4) + 16 tq + 4 (ks % 4) ..) ----
+    uint32_t qf[NT][8][2];
+    float qs[NT][2];  // factor of the scores of columns 2 tq, 2 tq + 1
+    int lim[NT][2];   // last visible position of those columns' rows
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const int row = row0 + 8 * n + gq;
+      uint4 raw[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) raw[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (row < a.rows) {
+        const int j = row / g.group, head = h * g.group + row % g.group;
+        const uint4* src = reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(a.q) +
+                                                          (((size_t)b * a.T + j) * g.num_q_heads + head) * kHeadDim);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) raw[i] = __ldg(src + 8 * (i >> 1) + 2 * tq + (i & 1));
+      }
+      float f = g.sm_scale * 1.44269504088896340736f;
+      if constexpr (sizeof(T) == 2 && !std::is_same<T, __half>::value) {
+        float top = 0.f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const float2 v = rope::unpack2<T>(word(raw[i >> 2], i & 3));
+          top = fmaxf(top, fmaxf(fabsf(v.x), fabsf(v.y)));
+        }
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        const int e = min(max((int)(__float_as_uint(top) >> 23) - 127, -100), 127);
+        const float down = pow2(14 - e);  // the row's largest magnitude to 2^14 .. 2^15
+        f *= pow2(e - 14);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const float2 v = rope::unpack2<T>(word(raw[i >> 2], i & 3));
+          qf[n][i >> 1][i & 1] = rope::pack2<__half>(v.x * down, v.y * down);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) qf[n][i >> 1][i & 1] = word(raw[i >> 2], i & 3);
+      }
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        qs[n][c] = __shfl_sync(0xffffffffu, f, 4 * (2 * tq + c));
+        lim[n][c] = len - a.T + (row0 + 8 * n + 2 * tq + c) / g.group;
       }
     }
-    s += __shfl_xor_sync(0xffffffffu, s, 16);
-    const int p = t0 + r;
-    bool seen = p < end;
-    if (a.tree_mask && p >= prefix) seen = seen && (mask >> (p - prefix) & 1);
-    s = seen ? s * ek : -CUDART_INF_F;
-    float top = s;
-    for (int x = 8; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-    const float m_new = fmaxf(m, top), base = m_new == -CUDART_INF_F ? 0.f : m_new;
-    const float alpha = exp2f(m - base), w = exp2f(s - base);
-    m = m_new;
-    float sum = w;
-    for (int x = 8; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
-    l = l * alpha + sum;
-    for (int d = 0; d < 4; ++d) o[d] *= alpha;
-    for (int t = 0; t < 4; ++t) {
-      const uint4 c = reinterpret_cast<const uint4*>(blk + kValues)[4 * lane + t];
-      const uint32_t cw[4] = {c.x, c.y, c.z, c.w};
-      const int rows[4] = {2 * t, 2 * t + 1, 2 * t + 8, 2 * t + 9};
-      for (int k = 0; k < 4; ++k) {
-        const float wr = __shfl_sync(0xffffffffu, w, rows[k]) * ev;
-        if (wr == 0.f) continue;  // a masked token's bytes may be anything
-        for (int d = 0; d < 4; ++d) o[d] += wr * rope::unpack2<__half>(widen2(cw[d] >> (8 * k) & 0xFF)).x;
+
+    float o[NT][8][4], m[NT][2], l[NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      m[n][0] = m[n][1] = kNone;
+      l[n][0] = l[n][1] = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) o[n][i][0] = o[n][i][1] = o[n][i][2] = o[n][i][3] = 0.f;
+    }
+
+    for (int i = 0; i < count; ++i) {
+      const uint32_t st = done % S, tile = ring + st * kBlockBytes;
+      if (failed || !__all_sync(0xffffffffu, bounded_wait(bars + 8 * st, (done / S) & 1))) {
+        if (!failed && lane == 0 && a.status) atomicOr(a.status, RQ_STATUS_TIMEOUT);
+        for (; done != issued; ++done) bounded_wait(bars + 8 * (done % S), (done / S) & 1);  // its own copies
+        failed = true;
+        break;
+      }
+      ++done;
+      const int t0 = (first + kWarps * i) * kBlockTokens;
+      const bool tail = t0 + kBlockTokens - 1 > len - a.T;  // rows see different parts of the tile
+      uint32_t exps;
+      asm volatile("ld.shared.u16 %0, [%1];" : "=r"(exps) : "r"(tile + kExps));
+      const float ks = pow2(exp_of_byte(exps & 0xFF));
+      const int ev = exp_of_byte(exps >> 8);
+
+      float s[NT][4];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const uint4 lo = lds128(tile + 16 * (32 * half + lane)), hi = lds128(tile + 16 * (32 * (2 + half) + lane));
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint32_t w0 = word(lo, k), w1 = word(hi, k);
+          const uint32_t a0 = widen2(w0), a1 = widen2(w1), a2 = widen2_hi(w0), a3 = widen2_hi(w1);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) mma(s[n], a0, a1, a2, a3, qf[n][4 * half + k][0], qf[n][4 * half + k][1]);
+        }
+      }
+      if (tail) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const int p = t0 + gq + 8 * (c >> 1), row = row0 + 8 * n + 2 * tq + (c & 1);
+            bool seen = p <= lim[n][c & 1];
+            if (a.tree_mask) {
+              const int d = p - (len - a.T);
+              seen = p < len && (d < 0 || (row < a.rows &&
+                                           (__ldg(a.tree_mask + (size_t)b * a.T + row / g.group) >> d & 1)));
+            }
+            if (!seen) s[n][c] = -CUDART_INF_F;
+          }
+        }
+      }
+      const float fev = (float)ev, down = pow2(-ev);
+      float t[NT][4];
+      bool past = false;
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          t[n][c] = fmaf(s[n][c], qs[n][c & 1] * ks, fev);  // rounded once: t - m <= 0 for the m it gives, at any size
+          past = past || t[n][c] - m[n][c & 1] > kMargin;
+        }
+      }
+      if (__any_sync(0xffffffffu, past)) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            float top = fmaxf(t[n][c], t[n][c + 2]);
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+            const float m_new = fmaxf(m[n][c], top), alpha = ex2(m[n][c] - m_new);
+            m[n][c] = m_new;
+            l[n][c] *= alpha;
+#pragma unroll
+            for (int d = 0; d < 8; ++d) o[n][d][c] *= alpha, o[n][d][c + 2] *= alpha;
+          }
+        }
+      }
+      uint32_t p[NT][2];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const float w0 = ex2(t[n][0] - m[n][0]), w1 = ex2(t[n][1] - m[n][1]);
+        const float w2 = ex2(t[n][2] - m[n][0]), w3 = ex2(t[n][3] - m[n][1]);
+        l[n][0] = fmaf(w0 + w2, down, l[n][0]);
+        l[n][1] = fmaf(w1 + w3, down, l[n][1]);
+        p[n][0] = transpose8x8(rope::pack2<__half>(w0, w1));
+        p[n][1] = transpose8x8(rope::pack2<__half>(w2, w3));
+      }
+      uint4 v[4];
+#pragma unroll
+      for (int q4 = 0; q4 < 4; ++q4) v[q4] = lds128(tile + kValues + 16 * (32 * q4 + lane));
+      if (tail) {
+        // bytes past the sequence may be anything; a NaN value of a token that some rows see and
+        // others do not reaches those that see it only
+        uint32_t keep = 0u;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (t0 + 2 * tq + (k & 1) + 8 * (k >> 1) < len) keep |= 0xFFu << (8 * k);
+        bool any_nan = false;
+#pragma unroll
+        for (int q4 = 0; q4 < 4; ++q4) {
+          v[q4].x &= keep, v[q4].y &= keep, v[q4].z &= keep, v[q4].w &= keep;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) any_nan = any_nan || without_nan4(word(v[q4], k)) != word(v[q4], k);
+        }
+        if (__any_sync(0xffffffffu, any_nan)) {
+#pragma unroll
+          for (int q4 = 0; q4 < 4; ++q4) {
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const uint32_t w0 = word(v[q4], 2 * k), w1 = word(v[q4], 2 * k + 1);
+#pragma unroll
+              for (int n = 0; n < NT; ++n) {
+                float hit[4] = {0.f, 0.f, 0.f, 0.f};
+                mma(hit, nan2(w0), nan2(w1), nan2(w0 >> 16), nan2(w1 >> 16), p[n][0], p[n][1]);
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                  if (hit[c] > 0.f) o[n][2 * q4 + k][c] = CUDART_NAN_F;
+              }
+            }
+            v[q4].x = without_nan4(v[q4].x), v[q4].y = without_nan4(v[q4].y);
+            v[q4].z = without_nan4(v[q4].z), v[q4].w = without_nan4(v[q4].w);
+          }
+        }
+      }
+#pragma unroll
+      for (int q4 = 0; q4 < 4; ++q4) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const uint32_t w0 = word(v[q4], 2 * k), w1 = word(v[q4], 2 * k + 1);
+          const uint32_t a0 = widen2(w0), a1 = widen2(w1), a2 = widen2_hi(w0), a3 = widen2_hi(w1);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) mma(o[n][2 * q4 + k], a0, a1, a2, a3, p[n][0], p[n][1]);
+        }
+      }
+      __syncwarp();  // every lane has read the stage
+      if (i + S < count) issue(i + S);
+    }
+
+    // ---- join the warps ----
+    const int rows = min(kRows, a.rows - row0);
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) l[n][c] += __shfl_xor_sync(0xffffffffu, l[n][c], d);
+        if (gq == 0) {
+          s_m[warp][8 * n + 2 * tq + c] = m[n][c];
+          s_l[warp][8 * n + 2 * tq + c] = l[n][c];
+        }
       }
     }
+    __syncthreads();  // also: every warp is done with its ring
+    float* const join = reinterpret_cast<float*>(smem);  // [warp][row][kRowStride]
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int r = 8 * n + 2 * tq + c;
+        float top = s_m[0][r];
+#pragma unroll
+        for (int w = 1; w < kWarps; ++w) top = fmaxf(top, s_m[w][r]);
+        const float f = ex2(m[n][c] - top);
+#pragma unroll
+        for (int d = 0; d < 8; ++d)  // dims 32 (d / 2) + 4 gq + 2 (d % 2), and the next
+          *reinterpret_cast<float2*>(join + (warp * kRows + r) * kRowStride + 32 * (d >> 1) + 4 * gq + 2 * (d & 1)) =
+              make_float2(o[n][d][c] * f, o[n][d][c + 2] * f);
+      }
+    }
+    __syncthreads();
+    const long long u0 = at + (long long)u * pl.rounds;
+    const bool whole = r0 == 0 && r1 == pl.rounds;
+    const long long cf = part_of(u0), cl = part_of(u0 + pl.rounds - 1);
+    float* const ws = a.ws;
+    auto slot_of = [&](long long c) {  // a unit's fragment in range c is c's first, or the last of the first range
+      return ws + (2 * c + (c == cf && part_begin(c) != u0 ? 1 : 0)) * (kRows * kRowStride);
+    };
+    auto out_row = [&](int r) {
+      const int row = row0 + r, j = row / g.group, head = h * g.group + row % g.group;
+      return reinterpret_cast<T*>(a.out) + (((size_t)b * a.T + j) * g.num_q_heads + head) * kHeadDim;
+    };
+    for (int r = 0; r < rows; ++r) {
+      float top = s_m[0][r], sum = 0.f, acc = 0.f;
+#pragma unroll
+      for (int w = 1; w < kWarps; ++w) top = fmaxf(top, s_m[w][r]);
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        sum += s_l[w][r] * ex2(s_m[w][r] - top);
+        acc += join[(w * kRows + r) * kRowStride + tid];
+      }
+      if (whole) {
+        out_row(r)[tid] = (T)(sum == 0.f ? 0.f : acc / sum);
+      } else {
+        float* const dst = slot_of(blockIdx.x) + r * kRowStride;
+        dst[tid] = acc;
+        if (tid == 0) dst[kHeadDim] = top, dst[kHeadDim + 1] = sum;
+      }
+    }
+    if (!whole) {
+      const int frags = (int)(cl - cf + 1);
+      __threadfence();
+      __syncthreads();
+      if (tid == 0) s_last = atomicAdd(a.cnt + cf, 1) == frags - 1;
+      __syncthreads();
+      if (s_last) {
+        __threadfence();
+        if (tid == 0) a.cnt[cf] = 0;  // as every launch finds it
+        float* const wt = reinterpret_cast<float*>(smem);  // weights [frag][kRows]
+        for (int i = tid; i < frags * rows; i += kThreads) {
+          const int f = i / rows, r = i % rows;
+          wt[f * kRows + r] = __ldcg(slot_of(cf + f) + r * kRowStride + kHeadDim);
+        }
+        __syncthreads();
+        for (int r = warp; r < rows; r += kWarps) {
+          float top = kNone, sum = 0.f;
+          for (int f = lane; f < frags; f += 32) top = fmaxf(top, wt[f * kRows + r]);
+#pragma unroll
+          for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+          for (int f = lane; f < frags; f += 32) {
+            const float w = ex2(wt[f * kRows + r] - top);
+            wt[f * kRows + r] = w;
+            sum = fmaf(__ldcg(slot_of(cf + f) + r * kRowStride + kHeadDim + 1), w, sum);
+          }
+#pragma unroll
+          for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+          if (lane == 0) s_l[0][r] = sum;
+        }
+        __syncthreads();
+        for (int rb = 0; rb < rows; rb += 8) {
+          float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+          const int nr = min(8, rows - rb);
+#pragma unroll 2
+          for (int f = 0; f < frags; ++f) {
+            const float* src = slot_of(cf + f) + rb * kRowStride + tid;
+#pragma unroll
+            for (int r = 0; r < 8; ++r)
+              if (r < nr) acc[r] = fmaf(__ldcg(src + r * kRowStride), wt[f * kRows + rb + r], acc[r]);
+          }
+          for (int r = 0; r < nr; ++r) {
+            const float sum = s_l[0][rb + r];
+            float y = acc[0];
+#pragma unroll
+            for (int k = 1; k < 8; ++k) y = r == k ? acc[k] : y;
+            out_row(rb + r)[tid] = (T)(sum == 0.f ? 0.f : y / sum);
+          }
+        }
+      }
+    }
+    tc::fence_async_smem();  // the join's accesses to the ring, before the next fragment's copies
+    __syncthreads();
+    x += r1 - r0;
+    if (x - at == (long long)pl.rounds * per_seq) {
+      at = x;
+      ++b;
+    }
   }
-  if (lane == 0) ms[warp] = m, ls[warp] = l;
-  for (int d = 0; d < 4; ++d) part[warp][4 * lane + d] = o[d];
-  __syncthreads();
-  float top = -CUDART_INF_F, sum = 0.f, out = 0.f;
-  for (int w = 0; w < kWarps; ++w) top = fmaxf(top, ms[w]);
-  for (int w = 0; w < kWarps; ++w) {
-    const float f = ms[w] == -CUDART_INF_F ? 0.f : exp2f(ms[w] - top);
-    sum += ls[w] * f;
-    out += part[w][tid] * f;
-  }
-  out = sum > 0.f || sum != sum ? out / sum : 0.f;  // a row that sees nothing gives zeros
-  reinterpret_cast<T*>(a.out)[row * kHeadDim + tid] = (T)out;
+}
+
+template <int NT>
+cudaError_t launch(const Geometry& g, const AttnArgs& a, cudaStream_t stream) {
+  if (g.bf16)
+    splitk_kernel<NT, __nv_bfloat16><<<a.grid, kThreads, smem_bytes(NT), stream>>>(g, a);
+  else
+    splitk_kernel<NT, __half><<<a.grid, kThreads, smem_bytes(NT), stream>>>(g, a);
+  return cudaGetLastError();
+}
+
+template <int NT>
+cudaError_t prepare() {
+  cudaError_t e = cudaFuncSetAttribute(splitk_kernel<NT, __half>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes(NT));
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(splitk_kernel<NT, __nv_bfloat16>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes(NT));
+  return e;
+}
+
+// n-tiles a unit carries: as few units as three n-tiles each allow, evenly filled
+int unit_tiles(int n_tiles) {
+  const int units = (n_tiles + 2) / 3;
+  return (n_tiles + units - 1) / units;
 }
 
 }  // namespace
 
-cudaError_t launch_block_attention(const Geometry& g, const AttnArgs& a, cudaStream_t stream, cudaEvent_t ev_start,
+size_t block_attention_workspace(int num_sms, size_t* counters) {
+  size_t most = 0;
+  for (int nt = 1; nt <= 3; ++nt) {
+    const size_t f = (size_t)2 * num_sms * ctas_per_sm(nt) * 8 * nt * kRowStride;
+    most = f > most ? f : most;
+  }
+  *counters = (size_t)num_sms * ctas_per_sm(1);
+  return most;
+}
+
+cudaError_t block_attention_prepare() {
+  cudaError_t e = prepare<1>();
+  if (e == cudaSuccess) e = prepare<2>();
+  if (e == cudaSuccess) e = prepare<3>();
+  return e;
+}
+
+cudaError_t launch_block_attention(const Geometry& g, AttnArgs a, int num_sms, cudaStream_t stream, cudaEvent_t ev_start,
                                    cudaEvent_t ev_end) {
-  const long long rows = (long long)a.B * a.T * g.num_q_heads;
-  if (rows > 0x7fffffffLL) return cudaErrorInvalidValue;
+  a.n_tiles_n = (a.rows + 7) / 8;
+  a.nt = unit_tiles(a.n_tiles_n);
+  a.grid = num_sms * ctas_per_sm(a.nt);
   if (ev_start) cudaEventRecord(ev_start, stream);
-  if (g.bf16)
-    rows_kernel<__nv_bfloat16><<<(unsigned)rows, 32 * kWarps, 0, stream>>>(g, a);
-  else
-    rows_kernel<__half><<<(unsigned)rows, 32 * kWarps, 0, stream>>>(g, a);
-  const cudaError_t e = cudaGetLastError();
+  const cudaError_t e = a.nt == 1 ? launch<1>(g, a, stream) : a.nt == 2 ? launch<2>(g, a, stream) : launch<3>(g, a, stream);
   if (e == cudaSuccess && ev_end) cudaEventRecord(ev_end, stream);
   return e;
 }

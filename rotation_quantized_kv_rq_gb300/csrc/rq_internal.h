@@ -176,9 +176,16 @@ struct BlockAppendArgs {
 };
 cudaError_t launch_block_append(const Geometry& g, const BlockAppendArgs& a, int num_sms, cudaStream_t stream);
 
-// Attention over the 8-bit cache; the AttnArgs fields of the split-K kernel's planning are unused.
-cudaError_t launch_block_attention(const Geometry& g, const AttnArgs& a, cudaStream_t stream, cudaEvent_t ev_start,
-                                   cudaEvent_t ev_end);
+// Attention over the 8-bit cache (decode, chain and tree verify): a.ws and a.cnt hold
+// block_attention_workspace floats and counters (the counters zero between launches); n_tiles_n,
+// nt and grid are chosen by the launch.
+size_t block_attention_workspace(int num_sms, size_t* counters);
+cudaError_t block_attention_prepare();
+cudaError_t launch_block_attention(const Geometry& g, AttnArgs a, int num_sms, cudaStream_t stream,
+                                   cudaEvent_t ev_start, cudaEvent_t ev_end);
+// Extend attention over the 8-bit cache: no workspace.
+cudaError_t launch_block_extend(const Geometry& g, const AttnArgs& a, cudaStream_t stream, cudaEvent_t ev_start,
+                                cudaEvent_t ev_end);
 
 // Dynamic shared memory the attention kernel needs (set as the kernel's maximum once).
 size_t attention_smem_bytes();
