@@ -157,10 +157,13 @@ int create_block(rq_ctx* ctx, const rq_config* cfg) {
   g.sm_scale = cfg->sm_scale > 0.f ? cfg->sm_scale : (float)(1.0 / std::sqrt((double)cfg->head_dim));
   size_t counters = 0;
   ctx->ws_floats = rq::block_attention_workspace(ctx->num_sms, &counters);
+  const size_t extend_floats = rq::block_extend_workspace(ctx->num_sms);
+  if (extend_floats > ctx->ws_floats) ctx->ws_floats = extend_floats;
   cudaError_t e = cudaMalloc(&ctx->d_ws, ctx->ws_floats * sizeof(float));
   if (e == cudaSuccess) e = cudaMalloc(&ctx->d_frag, counters * sizeof(int));
   if (e == cudaSuccess) e = cudaMemset(ctx->d_frag, 0, counters * sizeof(int));  // as every launch leaves them
   if (e == cudaSuccess) e = rq::block_attention_prepare();
+  if (e == cudaSuccess) e = rq::block_extend_prepare();
   if (e != cudaSuccess) {
     cudaFree(ctx->d_ws);
     cudaFree(ctx->d_frag);
@@ -595,9 +598,9 @@ static int block_attention(rq_ctx* ctx, const void* q, int T, const uint64_t* tr
   a.status = d_status;
   a.tree_mask = tree_mask;
   a.rows = T * ctx->g.group;
-  if (extend) return to_status(rq::launch_block_extend(ctx->g, a, stream, ctx->prof_start, ctx->prof_end));
   a.ws = ctx->d_ws;
   a.cnt = ctx->d_frag;
+  if (extend) return to_status(rq::launch_block_extend(ctx->g, a, ctx->num_sms, stream, ctx->prof_start, ctx->prof_end));
   return to_status(rq::launch_block_attention(ctx->g, a, ctx->num_sms, stream, ctx->prof_start, ctx->prof_end));
 }
 

@@ -183,8 +183,11 @@ size_t block_attention_workspace(int num_sms, size_t* counters);
 cudaError_t block_attention_prepare();
 cudaError_t launch_block_attention(const Geometry& g, AttnArgs a, int num_sms, cudaStream_t stream,
                                    cudaEvent_t ev_start, cudaEvent_t ev_end);
-// Extend attention over the 8-bit cache: no workspace.
-cudaError_t launch_block_extend(const Geometry& g, const AttnArgs& a, cudaStream_t stream, cudaEvent_t ev_start,
+// Extend attention over the 8-bit cache: a.ws holds block_extend_workspace floats, a.cnt num_sms
+// counters (zero between launches).
+size_t block_extend_workspace(int num_sms);
+cudaError_t block_extend_prepare();
+cudaError_t launch_block_extend(const Geometry& g, AttnArgs a, int num_sms, cudaStream_t stream, cudaEvent_t ev_start,
                                 cudaEvent_t ev_end);
 
 // Dynamic shared memory the attention kernel needs (set as the kernel's maximum once).
