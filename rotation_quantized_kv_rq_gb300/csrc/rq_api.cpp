@@ -245,6 +245,7 @@ struct rq_rope {
   rq::RopeTable table;
   uint64_t* d_pairs;
   int device;
+  int num_sms;
 };
 
 extern "C" {
@@ -722,6 +723,7 @@ int rq_rope_create(rq_rope** out, const rq_rope_config* cfg) {
   if (!r) return RQ_ERR_CUDA;
   cudaError_t e = cudaMalloc(&r->d_pairs, sizeof(host));
   if (e == cudaSuccess) e = cudaMemcpy(r->d_pairs, host, sizeof(host), cudaMemcpyHostToDevice);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&r->num_sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) {
     cudaFree(r->d_pairs);
     delete r;
@@ -767,7 +769,11 @@ int rq_norm_rope(const rq_rope* rope, const rq_rows* q, const rq_rows* k, int io
   else if (cudaGetDevice(&dev) != cudaSuccess)
     return RQ_ERR_CUDA;
   DeviceScope scope(dev);
-  if (!scope.ok() || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return RQ_ERR_CUDA;
+  if (!scope.ok()) return RQ_ERR_CUDA;
+  if (rope)
+    sms = rope->num_sms;
+  else if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return RQ_ERR_CUDA;
   rq::NormRopeArgs a{};
   a.q = rows_dev(q);
   a.k = rows_dev(k);

@@ -152,8 +152,10 @@ def _dtype(ctx):
 
 
 def _stream(stream, device) -> int:
-    s = stream if stream is not None else torch.cuda.current_stream(device)
-    return s.cuda_stream if hasattr(s, "cuda_stream") else int(s)
+    if stream is None:  # the handle alone: a Stream object costs 2 us a call
+        index = device.index
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if index is None else index)
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def rq_lloyd_max_codebook(bits: int, head_dim: int = HEAD_DIM) -> np.ndarray:
@@ -316,18 +318,25 @@ def rq_decode_attention_noalloc(mode: int, bits: int, num_q_heads: int, num_kv_h
 
 def _rows(t, name: str, weight=None, out=None) -> rq_rows:
     """rq_rows of t [n][heads][128] (heads and dims contiguous, any stride from token to token)."""
-    for x in (t,) if out is None else (t, out):
-        if x.dim() != 3 or x.shape[2] != HEAD_DIM or x.stride(2) != 1 or (x.shape[1] > 1 and x.stride(1) != HEAD_DIM):
-            raise RQError(name, RQ_ERR_INVALID)
-    if out is not None and (out.shape != t.shape or out.dtype != t.dtype or out.device != t.device):
+    shape, stride = t.shape, t.stride()
+    heads = shape[1] if len(shape) == 3 else 0
+    least = heads * HEAD_DIM
+    # the stride of a single token says nothing
+    st, out_st, out_ptr = stride[0] if shape[0] > 1 else least, 0, None
+    ok = heads > 0 and shape[2] == HEAD_DIM and stride[2] == 1 and (stride[1] == HEAD_DIM or heads == 1)
+    if out is not None:
+        o = out.stride()
+        ok = ok and out.shape == shape and out.dtype == t.dtype and out.device == t.device
+        ok = ok and o[2] == 1 and (o[1] == HEAD_DIM or heads == 1)
+        out_st, out_ptr = o[0] if shape[0] > 1 else least, out.data_ptr()
+    wptr = None
+    if weight is not None:
+        ok = (ok and weight.dtype == torch.float32 and weight.shape == (HEAD_DIM,) and weight.is_contiguous() and
+              weight.device == t.device)
+        wptr = weight.data_ptr()
+    if not ok:
         raise RQError(name, RQ_ERR_INVALID)
-    if weight is not None and (weight.dtype != torch.float32 or tuple(weight.shape) != (HEAD_DIM,) or
-                               not weight.is_contiguous() or weight.device != t.device):
-        raise RQError(name, RQ_ERR_INVALID)
-    least = t.shape[1] * HEAD_DIM  # a single token's stride says nothing
-    stride = t.stride(0) if t.shape[0] > 1 else least
-    out_stride = 0 if out is None else (out.stride(0) if out.shape[0] > 1 else least)
-    return rq_rows(t.data_ptr(), stride, t.shape[1], _ptr(weight), _ptr(out), out_stride)
+    return rq_rows(t.data_ptr(), st, heads, wptr, out_ptr, out_st)
 
 
 def _positions(positions, n: int, axes: int, device, name: str):
@@ -335,7 +344,8 @@ def _positions(positions, n: int, axes: int, device, name: str):
     if axes == 0:
         return None
     if (positions is None or positions.dtype != torch.int32 or positions.device != device or
-            not positions.is_contiguous() or tuple(positions.shape) not in (((n,), (1, n)) if axes == 1 else ((axes, n),))):
+            not positions.is_contiguous() or
+            (positions.shape != (axes, n) and (axes > 1 or positions.shape != (n,)))):
         raise RQError(name, RQ_ERR_INVALID)
     return positions
 
@@ -426,14 +436,16 @@ class Rope:
         [n][heads][128], either None; slices of a fused projection's output are taken as they are.
         q_out, k_out: where to write (q, k themselves: in place); new tensors by default."""
         given = [t for t in (q, k) if t is not None]
-        if (not given or given[0].dtype not in _IO_TYPES or any(t.dim() != 3 for t in given) or
-                any(t.device != self.device or t.dtype != given[0].dtype or t.shape[0] != given[0].shape[0] for t in given)):
+        first = given[0] if given else None
+        if first is None or first.dtype not in _IO_TYPES or first.dim() != 3 or first.device != self.device:
             raise RQError("rq_norm_rope", RQ_ERR_INVALID)
-        n = given[0].shape[0]
+        n = first.shape[0]
+        if len(given) == 2 and (k.dtype != first.dtype or k.dim() != 3 or k.shape[0] != n or k.device != self.device):
+            raise RQError("rq_norm_rope", RQ_ERR_INVALID)
         if q is not None and q_out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
         if k is not None and k_out is None:
-            k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+            k_out = torch.empty_like(k, memory_format=torch.contiguous_format)
         rq_norm_rope(self.rope, q, k, self.positions(positions, n, "rq_norm_rope"), q_weight, k_weight, eps, q_out,
                      k_out, stream)
         return q_out, k_out
@@ -480,6 +492,7 @@ class KVCache:
               not pages.is_contiguous()):
             raise RQError("rq_create", RQ_ERR_INVALID)
         self.pages = pages
+        self._views = None
         self.status = torch.zeros(1, dtype=torch.int32, device=self.device)
 
     def codebook(self):
@@ -494,15 +507,16 @@ class KVCache:
         a weight is given) and rotation (rope: a Rope, or None) of k on its way into the cache, v
         beside it, and of q, whose result is returned (None without q).  q, k, v: [n][heads][128],
         slices of a fused projection's output are taken as they are; slot_mapping int32 [n]."""
-        name, n = "rq_rope_append", slot_mapping.numel()
-        given = [t for t in (q, k, v) if t is not None]
+        name, n, device, dtype = "rq_rope_append", slot_mapping.numel(), self.device, _dtype(self.ctx)
+        shape = (n, self.num_kv_heads, HEAD_DIM)
         if (k is None or v is None or slot_mapping.dtype != torch.int32 or not slot_mapping.is_contiguous() or
-                slot_mapping.device != self.device or (rope is not None and rope.device != self.device) or
-                any(t.dim() != 3 or t.dtype != _dtype(self.ctx) or t.device != self.device or t.shape[0] != n
-                    for t in given) or k.shape[1] != self.num_kv_heads or v.shape != k.shape):
+                slot_mapping.device != device or (rope is not None and rope.device != device) or
+                k.shape != shape or k.dtype != dtype or k.device != device or
+                v.shape != shape or v.dtype != dtype or v.device != device or
+                (q is not None and (q.dim() != 3 or q.shape[0] != n or q.dtype != dtype or q.device != device))):
             raise RQError(name, RQ_ERR_INVALID)
         if q is not None and q_out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
         positions = rope.positions(positions, n, name) if rope is not None else None
         rq_rope_append(self.ctx, rope.rope if rope is not None else None, q, k, v, positions, slot_mapping, self.pages,
                        q_weight, k_weight, eps, q_out, self.status, stream)
@@ -511,17 +525,21 @@ class KVCache:
     def codes(self):
         """RQ_FP8: the pool's codes as float8_e4m3fn [num_pages][Hkv][page_size / 16][4096] (a view), each
         block's 2048 key codes, then its value codes, in the byte order of include/rq.h."""
-        return self._blocks()[..., :2 * BLOCK_TOKENS * HEAD_DIM].view(torch.float8_e4m3fn)
+        return self._block_views()[0]
 
     def scales(self):
         """RQ_FP8: the key and value scale of each block, float8_e8m0fnu [num_pages][Hkv][page_size / 16][2] (a view)."""
-        at = 2 * BLOCK_TOKENS * HEAD_DIM
-        return self._blocks()[..., at:at + 2].view(torch.float8_e8m0fnu)
+        return self._block_views()[1]
 
-    def _blocks(self):
+    def _block_views(self):
         if self.mode != RQ_FP8:
             raise RQError("codes", RQ_ERR_UNSUPPORTED)
-        return self.pages.view(self.num_pages, self.num_kv_heads, self.page_size // BLOCK_TOKENS, BLOCK_BYTES)
+        if self._views is None or self._views[2] is not self.pages:
+            blocks = self.pages.view(self.num_pages, self.num_kv_heads, self.page_size // BLOCK_TOKENS, BLOCK_BYTES)
+            at = 2 * BLOCK_TOKENS * HEAD_DIM
+            self._views = (blocks[..., :at].view(torch.float8_e4m3fn),
+                           blocks[..., at:at + 2].view(torch.float8_e8m0fnu), self.pages)
+        return self._views[:2]
 
     def decode(self, q, block_table, seq_lens, out=None, stream=None):
         if out is None:
