@@ -6,26 +6,32 @@
 // 4 * 128 flops a (query row, token) against 257 cache bytes a token that 256 rows share.
 //
 // A CTA (one per SM) takes 256 query rows of one (sequence, kv head), two blocks of 128, and walks
-// the cache in tiles of 64 tokens, its warps specialised and coupled through mbarriers:
-//   softmax (warps 0-7, a thread per row): reads its row of S from tensor memory, applies scales and
-//     mask, writes fp16 weights over S;
-//   codes (warps 8-11): widen a tile's key and value codes (exact) into fp16 shared-memory operands,
-//     loading the next tile's codes meanwhile;
-//   MMA (one thread of warp 12; warps 13-15 only fill the warpgroup, 16 warps have 128 registers
-//     a thread where 17 would have 96): O_b += W_b V(t) and behind it S_b(t + 1) = Q_b K(t + 1)^T, one block
-//     on the tensor cores while the other is in its softmax.  Q and W come from tensor memory (O 2 x
-//     128 columns, Q 2 x 64, S 2 x 64 with W over it: all 512), so that shared memory has only K and
-//     V to feed: 64 of its 128 bytes a cycle.
-// The order of tokens inside a tile is free as long as S's columns and V's rows agree.  It is the one
-// in which the cache holds values: column 32 p + 8 t + 4 b + i is token {2t, 2t + 1, 2t + 8, 2t + 9}[i]
-// of block 2 p + b, so that a thread's 16 bytes of two blocks' value codes become four whole 16-byte
-// chunks of V^T, stored without bank conflicts, and no byte is ever shuffled.
+// the cache in tiles of 128 tokens, its warps specialised and coupled through mbarriers:
+//   softmax (warps 0-7, a thread per row): reads its row of S from tensor memory 64 columns at a
+//     time, applies scales and mask, writes fp16 weights over S;
+//   codes (warps 8-11): widen a tile's key and value codes (exact) into fp16 operands;
+//   MMA (one thread of warp 12): per block, O_b += W_b V(t) as each half of the weights is there,
+//     and behind it S_b(t + 1) = Q_b K(t + 1)^T: one block on the tensor cores while the other is in
+//     its softmax;
+//   copies (warp 13): a block is one 4112-byte bulk copy into a ring, page ids looked up 8 half
+//     tiles ahead.
+// (Warps 14 and 15 only fill the warpgroup: 16 warps have 128 registers a thread, 17 would have 96.)
+// Why these shapes: an MMA with N = 64 takes as long as one with N = 128 (64.5 and 65.5 cycles for M =
+// 128, K = 16, A in tensor memory; 78.7 for both with A in shared memory), so S is 128 columns wide.
+// That fills tensor memory (O 2 x 128 columns, S 2 x 128 with W over it) and puts Q into shared memory.
+// Shared memory then moves 322 KB a tile (Q and K into the MMAs twice, V twice, codes in and out,
+// operands in), 2516 cycles at 128 bytes, against 2308 of MMAs.
+// The order of tokens inside a half tile of 64 is free as long as S's columns and V's rows agree.  It
+// is the one in which the cache holds values: column 32 p + 8 t + 4 b + i is token {2t, 2t + 1, 2t + 8,
+// 2t + 9}[i] of block 2 p + b, so that a thread's 16 bytes of two blocks' value codes become four
+// whole 16-byte chunks of V^T, stored without bank conflicts, and no byte is ever shuffled.
 //
 // Work is cut evenly: tiles of all units (sequence, 256 rows, kv head) in order, one range per CTA.
 // A unit that spans ranges is joined by the last of its CTAs to finish, in the ranges' order.
 // Every wait is bounded: one that runs out sets RQ_STATUS_TIMEOUT and an abort flag every role polls.
 #include <math_constants.h>
 
+#include <cstddef>
 #include <type_traits>
 
 #include "../../include/rq.h"
@@ -40,29 +46,44 @@ using namespace block;
 using namespace tc;
 
 constexpr int kSoftWarps = 8, kCodeWarps = 4, kThreads = 512;
+constexpr int kMmaThread = 32 * (kSoftWarps + kCodeWarps), kCopyWarp = kSoftWarps + kCodeWarps + 1;
 constexpr int kHalf = 128, kRows = 2 * kHalf;  // rows of a block (M of the MMAs), of a CTA
-constexpr int kTok = 64;                       // tokens of a tile
-constexpr int kStages = 4;                     // K and V operand rings
-constexpr int kScaleSlots = 8;                 // tiles whose scales are kept
-constexpr uint32_t kOperand = 16384;           // bytes of a K or V stage
-constexpr int kSmem = 2 * kStages * (int)kOperand + 1024 + 1024;  // + alignment, + the part below
-constexpr int kScanThreads = 512;
+constexpr int kTok = 128, kPart = 64;          // tokens of a tile, of the half that softmax and V take at a time
+constexpr int kKeyStages = 2, kValueStages = 3, kRawStages = 3;  // tiles, halves, halves
+constexpr uint32_t kKeyBytes = 32768, kValueBytes = 16384, kRawBytes = 4 * kBlockBytes;
+constexpr uint32_t kQBytes = 2 * 32768;
+constexpr int kScaleSlots = 4;      // tiles whose scales are kept
 constexpr float kMargin = 8.f;      // log2 slack of the running maximum
 constexpr float kNone = -1e30f;     // running maximum before any visible token
 constexpr float kLarge = 1048576.f; // |maximum| from which weights are formed in two roundings
-constexpr int kMinTiles = 8;        // a CTA's least work, while there is enough
-// tensor-memory columns
-constexpr uint32_t kColQ = 256, kColS = 384;
+constexpr int kMinTiles = 4;        // a CTA's least work, while there is enough
+constexpr uint32_t kColS = 256;     // tensor memory: O_b at 128 b, S_b at 256 + 128 b
 // floats of a fragment's slot: 256 rows x 128 (as [dim / 4][row][4]), then the rows' m and l
 constexpr size_t kSlotFloats = (size_t)kRows * kHeadDim + 2 * kRows;
 
-struct Misc {  // shared, after the operands
-  uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
-  uint64_t s_full[2], p_full[2], o_done[2], drain;
-  uint32_t tmem;
-  int abort;
-  float scales[kScaleSlots][3][4];  // per block of a tile: 2^EK, EV, 2^-EV
+struct Frag {           // tiles r0 .. r0 + n - 1 of one unit
+  int b, rb, h, r0, n, len;
+  int whole, frags;     // the unit is all here; else its number of fragments
+  long long range;      // its first range, and whether the fragment there is that range's last
+  int range_last;
+  int done;             // no more fragments
 };
+struct Misc {
+  uint64_t raw_full[kRawStages], raw_empty[kRawStages], k_full[kKeyStages], k_empty[kKeyStages];
+  uint64_t v_full[kValueStages], v_empty[kValueStages], s_full[2];
+  uint64_t p_full[2][2], o_done[2][2], drain;  // [block][half]: one phase a tile each, a tile may be a whole half ahead
+  Frag f;
+  uint32_t tmem;
+  int abort, last;
+  alignas(16) float scales[kScaleSlots][2][3][4];  // [half][2^EK, EV, 2^-EV][block], read as float4
+  int nan_from[kHeadDim];              // first position with a NaN value in a dim
+};
+// from a 1024-byte boundary on: Q, keys, values, raw codes, Misc
+constexpr uint32_t kOffK = kQBytes, kOffV = kOffK + kKeyStages * kKeyBytes, kOffRaw = kOffV + kValueStages * kValueBytes;
+constexpr uint32_t kOffMisc = kOffRaw + kRawStages * kRawBytes;
+constexpr int kSmem = (int)(kOffMisc + sizeof(Misc)) + 1024;
+static_assert(kOffMisc % 16 == 0 && offsetof(Misc, scales) % 16 == 0, "float4 reads");
+static_assert(kSmem + 64 <= 232448, "one CTA's shared memory");
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -93,10 +114,18 @@ __device__ __forceinline__ void add2(uint64_t& a, float x, float y) {
 }
 __device__ __forceinline__ uint32_t word(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
 __device__ __forceinline__ uint32_t smem_addr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
-// Place of column c inside its tile: the token's offset.
+// Place of column c of a half tile: the token's offset.
 __host__ __device__ constexpr int token_of(int c) {
   const int i = c & 3, t = c >> 3 & 3;
   return 32 * (c >> 5) + 16 * (c >> 2 & 1) + 2 * t + (i & 1) + 8 * (i >> 1);
+}
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ void sts128(uint32_t addr, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
 }
 
 // One unit's geometry: 256 rows rb of sequence b.
@@ -119,139 +148,125 @@ __device__ __forceinline__ Unit unit_of(const AttnArgs& a, int group, int cap, i
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const Geometry g, const AttnArgs a) {
   extern __shared__ uint8_t smem_raw[];
-  __shared__ Misc ms;
-  __shared__ long long s_scan[kScanThreads], s_begin;
-  __shared__ int s_item, s_last;
-  __shared__ int nan_from[kHeadDim];  // first position with a NaN value in a dim
-  uint8_t* const ops = smem_raw + (1024 - (smem_addr(smem_raw) & 1023) & 1023);
-  const uint32_t k_ring = smem_addr(ops), v_ring = k_ring + kStages * kOperand;
+  const uint32_t base = smem_addr(smem_raw) + (1024 - (smem_addr(smem_raw) & 1023) & 1023);
+  Misc& ms = *reinterpret_cast<Misc*>(smem_raw + (base - smem_addr(smem_raw)) + kOffMisc);
+  const uint32_t q_ops = base, k_ring = base + kOffK, v_ring = base + kOffV, raw_ring = base + kOffRaw;
   volatile int* const abort_flag = &ms.abort;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int cap = a.max_pages * g.page_size, n_rb = (a.rows + kRows - 1) / kRows;
-  const long long n_items = (long long)a.B * n_rb;  // (sequence, rows): num_kv_heads units each
 
-  // ---- the CTA's range of tiles ----
-  long long mine = 0, chunk = (n_items + kScanThreads - 1) / kScanThreads;
-  if (tid < kScanThreads) {
+  // ---- the CTA's range of tiles: x .. end - 1 of `total`, kept by thread 0 ----
+  long long total, parts, x = 0, end = 0, at = 0;
+  long long item = 0;  // (sequence, rows): num_kv_heads units each, the first at tile `at`
+  {
+    long long* const scan = reinterpret_cast<long long*>(smem_raw + (base - smem_addr(smem_raw)));  // over Q
+    __shared__ long long s_found[2];
+    const long long n_items = (long long)a.B * n_rb, chunk = (n_items + kThreads - 1) / kThreads;
+    long long mine = 0;
     for (long long i = tid * chunk; i < min(n_items, (tid + 1) * chunk); ++i)
       mine += unit_of(a, g.group, cap, (int)(i / n_rb), (int)(i % n_rb), blockIdx.x == 0).tiles;
-    s_scan[tid] = mine;
+    scan[tid] = mine;
+    __syncthreads();
+    for (int o = 1; o < kThreads; o <<= 1) {
+      const long long v = tid >= o ? scan[tid - o] : 0;
+      __syncthreads();
+      scan[tid] += v;
+      __syncthreads();
+    }
+    total = scan[kThreads - 1] * g.num_kv_heads;
+    parts = min((long long)gridDim.x, max(1ll, total / kMinTiles));
+    if ((long long)blockIdx.x >= parts) return;
+    x = blockIdx.x * total / parts;
+    end = (blockIdx.x + 1ll) * total / parts;
+    const long long before = (scan[tid] - mine) * g.num_kv_heads;
+    if (x >= before && x < scan[tid] * g.num_kv_heads) {
+      long long p = before, i = tid * chunk;
+      for (;; ++i) {
+        const long long n =
+            (long long)unit_of(a, g.group, cap, (int)(i / n_rb), (int)(i % n_rb), false).tiles * g.num_kv_heads;
+        if (x < p + n) break;
+        p += n;
+      }
+      s_found[0] = p;
+      s_found[1] = i;
+    }
+    __syncthreads();
+    at = s_found[0];
+    item = s_found[1];
   }
   if (tid == 0) {
-    for (int i = 0; i < kStages; ++i) {
+    for (int i = 0; i < kRawStages; ++i) {
+      mbar_init(smem_addr(&ms.raw_full[i]), 1);
+      mbar_init(smem_addr(&ms.raw_empty[i]), kCodeWarps);
+    }
+    for (int i = 0; i < kKeyStages; ++i) {
       mbar_init(smem_addr(&ms.k_full[i]), 32 * kCodeWarps);
-      mbar_init(smem_addr(&ms.v_full[i]), 32 * kCodeWarps);
       mbar_init(smem_addr(&ms.k_empty[i]), 1);
+    }
+    for (int i = 0; i < kValueStages; ++i) {
+      mbar_init(smem_addr(&ms.v_full[i]), 32 * kCodeWarps);
       mbar_init(smem_addr(&ms.v_empty[i]), 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_addr(&ms.s_full[i]), 1);
-      mbar_init(smem_addr(&ms.p_full[i]), kHalf);
-      mbar_init(smem_addr(&ms.o_done[i]), 1);
+      for (int part = 0; part < 2; ++part) {
+        mbar_init(smem_addr(&ms.p_full[i][part]), kHalf);
+        mbar_init(smem_addr(&ms.o_done[i][part]), 1);
+      }
     }
     mbar_init(smem_addr(&ms.drain), 1);
     ms.abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (tid < kHeadDim) nan_from[tid] = INT32_MAX;
-  __syncthreads();
-  for (int o = 1; o < kScanThreads; o <<= 1) {
-    const long long v = tid >= o && tid < kScanThreads ? s_scan[tid - o] : 0;
-    __syncthreads();
-    if (tid < kScanThreads) s_scan[tid] += v;
-    __syncthreads();
-  }
-  const long long total = s_scan[kScanThreads - 1] * g.num_kv_heads;
-  const long long parts = min((long long)gridDim.x, max(1ll, total / kMinTiles));
-  if ((long long)blockIdx.x >= parts) return;
-  auto part_begin = [&](long long c) { return c * total / parts; };
-  auto part_of = [&](long long x) { return ((x + 1) * parts - 1) / total; };
-  long long x = part_begin(blockIdx.x);
-  const long long end = part_begin(blockIdx.x + 1ll);
-  if (tid < kScanThreads) {
-    const long long before = (s_scan[tid] - mine) * g.num_kv_heads;
-    if (x >= before && x < s_scan[tid] * g.num_kv_heads) {
-      long long at = before, i = tid * chunk;
-      for (;; ++i) {
-        const long long n =
-            (long long)unit_of(a, g.group, cap, (int)(i / n_rb), (int)(i % n_rb), false).tiles * g.num_kv_heads;
-        if (x < at + n) break;
-        at += n;
-      }
-      s_begin = at;
-      s_item = (int)i;
-    }
-  }
   __syncwarp();
   if (warp == 0) tmem_alloc(smem_addr(&ms.tmem), 512);
-  fence_before_sync();
-  __syncthreads();
-  fence_after_sync();
-  const uint32_t tmem = *(volatile uint32_t*)&ms.tmem;
-  long long at = s_begin;
-  int item = s_item;
 
   uint32_t done_tiles = 0;  // tiles of the fragments before: ring positions and parities
-  bool ok = true;           // this role has not given up
-  while (x < end) {
-    // ---- the fragment: tiles r0 .. r1 - 1 of kv head h, rows rb of sequence b ----
-    const int b = item / n_rb, rb = item % n_rb;
-    const Unit un = unit_of(a, g.group, cap, b, rb, false);
-    const int len = un.len, tiles = un.tiles;
-    const int h = (int)((x - at) / tiles), r0 = (int)((x - at) % tiles);
-    const int r1 = (int)min((long long)tiles, r0 + (end - x)), n = r1 - r0;
-    const int32_t* table = a.block_table + (size_t)b * a.max_pages;
-    const int blk = warp >> 2 & 1, brow = 32 * (warp & 3) + lane;  // softmax: row block, row in it (= lane of tensor memory)
-    const int row = rb * kRows + kHalf * blk + brow;
-    const bool valid = row < a.rows;
-    const uint32_t lane_off = (uint32_t)(32 * (warp & 3)) << 16;
-    const int qj = valid ? row / g.group : 0, head = h * g.group + (valid ? row % g.group : 0);
-    const size_t row_at = (((size_t)b * a.T + qj) * g.num_q_heads + head) * kHeadDim;
-    float q_scale = g.sm_scale * 1.44269504088896340736f, m_run = kNone, l_run = 0.f;
-
-    // the code loads of a tile, units of 16 bytes (rq_block.cuh): code warp dw takes the keys of block dw
-    // and half of the dims of the values of blocks p16 and p16 + 1
-    const int dw = warp & 3, p16 = dw & 2;
-    auto block_at = [&](int t, int blk16) -> const uint8_t* {  // block blk16 of tile t, or null past the sequence
-      const int p = t * kTok + 16 * blk16;
-      if (p >= len) return nullptr;
-      int page = __ldg(table + p / g.page_size);
-      if (page < 0 || page >= g.num_pages) {
-        if (a.status) atomicOr(a.status, RQ_STATUS_BAD_PAGE);
-        page = 0;
+  uint32_t fills = 0;       // copy warp: half tiles asked for
+  for (;;) {
+    if (tid == 0) {  // the next fragment
+      Frag& f = ms.f;
+      f.done = x >= end;
+      if (!f.done) {
+        f.b = (int)(item / n_rb);
+        f.rb = (int)(item % n_rb);
+        const Unit un = unit_of(a, g.group, cap, f.b, f.rb, false);
+        f.len = un.len;
+        f.h = (int)((x - at) / un.tiles);
+        f.r0 = (int)((x - at) % un.tiles);
+        f.n = (int)min((long long)un.tiles - f.r0, end - x);
+        f.whole = f.n == un.tiles;
+        const long long u0 = x - f.r0, u1 = u0 + un.tiles - 1;
+        f.range = ((u0 + 1) * parts - 1) / total;  // the range that holds tile u0
+        f.range_last = f.range * total / parts != u0;
+        f.frags = (int)(((u1 + 1) * parts - 1) / total - f.range) + 1;
+        x += f.n;
+        if (x - at == (long long)un.tiles * g.num_kv_heads) {
+          at = x;
+          ++item;
+        }
       }
-      return a.pages + ((size_t)page * g.num_kv_heads + h) * g.page_bytes + (size_t)(p % g.page_size / 16) * kBlockBytes;
-    };
-    const uint8_t *src_a = nullptr, *src_b = nullptr;  // blocks p16 and p16 + 1 of the tile
-    auto look_up = [&](int t) {
-      if (t >= r1) return;
-      src_a = block_at(t, p16);
-      src_b = block_at(t, p16 + 1);
-    };
-    uint4 kraw[4], vraw[4];
-    uint32_t raw_exps = 0;
-    auto load = [&]() {  // from the blocks looked up
-      const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-      const uint8_t* own = dw & 1 ? src_b : src_a;
-#pragma unroll
-      for (int u = 0; u < 4; ++u) kraw[u] = own ? __ldg(reinterpret_cast<const uint4*>(own) + 32 * u + lane) : zero;
-      raw_exps = own ? __ldg(reinterpret_cast<const uint16_t*>(own + kExps)) : 0x7F7Fu;
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int at16 = kValues / 16 + 32 * (2 * (dw & 1) + i) + lane;
-        vraw[2 * i] = src_a ? __ldg(reinterpret_cast<const uint4*>(src_a) + at16) : zero;
-        vraw[2 * i + 1] = src_b ? __ldg(reinterpret_cast<const uint4*>(src_b) + at16) : zero;
-      }
-    };
-    if (warp >= kSoftWarps && warp < kSoftWarps + kCodeWarps) {
-      look_up(r0);
-      load();
-      look_up(r0 + 1);
     }
+    if (tid < kHeadDim) ms.nan_from[tid] = INT32_MAX;
+    fence_before_sync();
+    __syncthreads();
+    fence_after_sync();
+    if (ms.f.done) break;
+    const uint32_t tmem = *(volatile uint32_t*)&ms.tmem;
+    const int b = ms.f.b, h = ms.f.h, r0 = ms.f.r0, n = ms.f.n, len = ms.f.len;
+    const uint32_t lane_off = (uint32_t)(32 * (warp & 3)) << 16;
+    // softmax: row block, row in it (= lane of tensor memory), query row
+    const int blk = warp >> 2 & 1, brow = 32 * (warp & 3) + lane, row = ms.f.rb * kRows + kHalf * blk + brow;
+    const bool valid = row < a.rows;
+    float q_scale = g.sm_scale * 1.44269504088896340736f, m_run = kNone, l_run = 0.f;
+    auto row_offset = [&]() {
+      const int j = valid ? row / g.group : 0, head = h * g.group + (valid ? row % g.group : 0);
+      return (((size_t)b * a.T + j) * g.num_q_heads + head) * kHeadDim;
+    };
 
-    // ---- Q of the row into tensor memory: fp16 as it is; a bf16 row by a power of two ----
+    // ---- Q of the row as an operand: fp16 as it is; a bf16 row by a power of two ----
     if (warp < kSoftWarps) {
-      const uint4* src = reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(a.q) + row_at);
+      const uint4* src = reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(a.q) + row_offset());
       float down = 1.f;
       if constexpr (!std::is_same<T, __half>::value) {
         float top = 0.f;
@@ -269,246 +284,270 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const Geometry g, c
         down = pow2(14 - e);
         q_scale *= pow2(e - 14);
       }
-#pragma unroll 1
-      for (int cc = 0; cc < 4; ++cc) {
-        uint32_t qw[16];
+#pragma unroll 4
+      for (int c = 0; c < 16; ++c) {
+        const uint4 v = valid ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
+        uint32_t w[4];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const uint4 v = valid ? __ldg(src + 4 * cc + c) : make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            uint32_t w = word(v, k);
-            if constexpr (!std::is_same<T, __half>::value) {
-              const float2 f = rope::unpack2<T>(w);
-              w = rope::pack2<__half>(f.x * down, f.y * down);
-            }
-            qw[4 * c + k] = w;
+        for (int k = 0; k < 4; ++k) {
+          w[k] = word(v, k);
+          if constexpr (!std::is_same<T, __half>::value) {
+            const float2 f = rope::unpack2<T>(w[k]);
+            w[k] = rope::pack2<__half>(f.x * down, f.y * down);
           }
         }
-        tmem_st16u(tmem + lane_off + kColQ + 64 * blk + 16 * cc, qw);
+        sts128(q_ops + 32768 * blk + 16384 * (c >> 3) + sw128(brow, c & 7), w[0], w[1], w[2], w[3]);
       }
-      tmem_wait_st();
+      fence_async_smem();
     }
-    fence_before_sync();
     __syncthreads();
-    fence_after_sync();
 
+    bool ok = true;
     const uint32_t t_base = done_tiles;
     if (warp < kSoftWarps) {
       // ================= softmax: one thread per row =================
-      const int qpos = valid ? len - a.T + qj : -1;
-      const uint32_t s_cols = tmem + lane_off + kColS + 64 * blk, o_cols = tmem + lane_off + 128 * blk;
+      const int qpos = valid ? len - a.T + row / g.group : -1;
+      const uint32_t s_tile = tmem + lane_off + kColS + 128 * blk, o_cols = tmem + lane_off + 128 * blk;
       for (int t = 0; t < n && ok; ++t) {
         const uint32_t k = t_base + t;
-        const int t0 = (r0 + t) * kTok;
         // S_b(t) complete: so is every MMA issued before it, W_b(t - 1) V included
         ok = __all_sync(0xffffffffu, role_wait(smem_addr(&ms.s_full[blk]), k & 1, abort_flag));
         if (!ok) break;
         fence_after_sync();
-        float s[kTok];
-#pragma unroll
-        for (int c = 0; c < kTok / 16; ++c) {
-          float v[16];
-          tmem_ld16(s_cols + 16 * c, v);
-#pragma unroll
-          for (int i = 0; i < 16; ++i) s[16 * c + i] = v[i];
-        }
-        const float4* sc = reinterpret_cast<const float4*>(ms.scales[k % kScaleSlots]);
-        const float4 ks4 = sc[0], ev4 = sc[1], dn4 = sc[2];
-        const float ks[4] = {ks4.x, ks4.y, ks4.z, ks4.w}, ev[4] = {ev4.x, ev4.y, ev4.z, ev4.w};
-        const float dn[4] = {dn4.x, dn4.y, dn4.z, dn4.w};
-        tmem_wait_ld();
-        const bool large = __any_sync(0xffffffffu, fabsf(m_run) > kLarge && m_run != kNone);
-        const float base = m_run == kNone || large ? 0.f : m_run;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {  // block q of the tile: columns 32 (q / 2) + 4 (q % 2) + 8 t + i
-          const uint64_t f = pair(q_scale * ks[q], q_scale * ks[q]), d = pair(ev[q] - base, ev[q] - base);
-#pragma unroll
-          for (int t4 = 0; t4 < 4; ++t4) {
-            const int c = 32 * (q >> 1) + 4 * (q & 1) + 8 * t4;
-            fma2(s[c], s[c + 1], f, d);
-            fma2(s[c + 2], s[c + 3], f, d);
-          }
-        }
-        if (t0 + kTok - 1 > qpos) {  // mask what the row may not see
-#pragma unroll
-          for (int c = 0; c < kTok; ++c)
-            if (t0 + token_of(c) > qpos) s[c] = -CUDART_INF_F;
-        }
-        float tm[4] = {s[0], s[1], s[2], s[3]};
-#pragma unroll
-        for (int c = 4; c < kTok - 4; c += 8)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) tm[i] = max3(tm[i], s[c + i], s[c + 4 + i]);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) tm[i] = fmaxf(tm[i], s[kTok - 4 + i]);
-        // relative to `base`: the running maximum, or 0 (none yet, or the large case)
-        const float top = fmaxf(max3(tm[0], tm[1], tm[2]), tm[3]);
-        float alpha = 1.f, shift = large ? -m_run : 0.f;
-        if (top > (m_run == kNone ? -CUDART_INF_F : m_run - base + kMargin)) {
-          const float m_new = top + base;
-          alpha = ex2(m_run - m_new);
-          shift = base - m_new;
-          m_run = m_new;
-        }
-        if (__any_sync(0xffffffffu, shift != 0.f)) {
-          const uint64_t one = pair(1.f, 1.f), d = pair(shift, shift);
-#pragma unroll
-          for (int c = 0; c < kTok; c += 2) fma2(s[c], s[c + 1], one, d);
-        }
-        l_run *= alpha;
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          uint32_t pw[16];
-          uint64_t sum[2] = {0ull, 0ull};
-#pragma unroll
-          for (int c = 0; c < 32; c += 2) {
-            const float w0 = ex2(s[32 * half + c]), w1 = ex2(s[32 * half + c + 1]);
-            add2(sum[c >> 2 & 1], w0, w1);
-            pw[c >> 1] = rope::pack2<__half>(w0, w1);
-          }
-          tmem_st16u(s_cols + 16 * half, pw);
-#pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            float lo, hi;
-            unpair(sum[q], lo, hi);
-            l_run = fmaf(lo + hi, dn[2 * half + q], l_run);
-          }
-        }
-        if (t > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {  // O *= alpha (the warp's rows)
 #pragma unroll 1
-          for (int c = 0; c < kHeadDim / 16; ++c) {
-            float v[16];
-            tmem_ld16(o_cols + 16 * c, v);
-            tmem_wait_ld();
+        for (int part = 0; part < 2; ++part) {
+          const int t0 = (r0 + t) * kTok + kPart * part;
+          const uint32_t s_cols = s_tile + kPart * part;
+          float s[kPart];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) v[i] *= alpha;
-            tmem_st16(o_cols + 16 * c, v);
+          for (int c = 0; c < kPart / 16; ++c) {
+            float v[16];
+            tmem_ld16(s_cols + 16 * c, v);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) s[16 * c + i] = v[i];
           }
+          const float4* sc = reinterpret_cast<const float4*>(ms.scales[k % kScaleSlots][part]);
+          const float4 ks4 = sc[0], ev4 = sc[1];
+          const float ks[4] = {ks4.x, ks4.y, ks4.z, ks4.w}, ev[4] = {ev4.x, ev4.y, ev4.z, ev4.w};
+          tmem_wait_ld();
+          const bool large = __any_sync(0xffffffffu, fabsf(m_run) > kLarge && m_run != kNone);
+          const float from = m_run == kNone || large ? 0.f : m_run;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {  // block q of the half: columns 32 (q / 2) + 4 (q % 2) + 8 t + i
+            const uint64_t f = pair(q_scale * ks[q], q_scale * ks[q]), d = pair(ev[q] - from, ev[q] - from);
+#pragma unroll
+            for (int t4 = 0; t4 < 4; ++t4) {
+              const int c = 32 * (q >> 1) + 4 * (q & 1) + 8 * t4;
+              fma2(s[c], s[c + 1], f, d);
+              fma2(s[c + 2], s[c + 3], f, d);
+            }
+          }
+          if (t0 + kPart - 1 > qpos) {  // mask what the row may not see
+#pragma unroll
+            for (int c = 0; c < kPart; ++c)
+              if (t0 + token_of(c) > qpos) s[c] = -CUDART_INF_F;
+          }
+          float tm[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+          for (int c = 4; c < kPart - 4; c += 8)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) tm[i] = max3(tm[i], s[c + i], s[c + 4 + i]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) tm[i] = fmaxf(tm[i], s[kPart - 4 + i]);
+          // relative to `from`: the running maximum, or 0 (none yet, or the large case)
+          const float top = fmaxf(max3(tm[0], tm[1], tm[2]), tm[3]);
+          float alpha = 1.f, shift = large ? -m_run : 0.f;
+          if (top > (m_run == kNone ? -CUDART_INF_F : m_run - from + kMargin)) {
+            const float m_new = top + from;
+            alpha = ex2(m_run - m_new);
+            shift = from - m_new;
+            m_run = m_new;
+          }
+          if (__any_sync(0xffffffffu, shift != 0.f)) {
+            const uint64_t one = pair(1.f, 1.f), d = pair(shift, shift);
+#pragma unroll
+            for (int c = 0; c < kPart; c += 2) fma2(s[c], s[c + 1], one, d);
+            if (__any_sync(0xffffffffu, alpha != 1.f) && (t > 0 || part > 0)) {  // O *= alpha (the warp's rows)
+              l_run *= alpha;
+              if (part == 1) {  // W_b(t) V of the first half still adds to O
+                ok = __all_sync(0xffffffffu, role_wait(smem_addr(&ms.o_done[blk][0]), k & 1, abort_flag));
+                if (!ok) break;
+                fence_after_sync();
+              }
+#pragma unroll 1
+              for (int c = 0; c < kHeadDim / 16; ++c) {
+                float v[16];
+                tmem_ld16(o_cols + 16 * c, v);
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 16; ++i) v[i] *= alpha;
+                tmem_st16(o_cols + 16 * c, v);
+              }
+            }
+          }
+          const float4 dn4 = sc[2];
+          const float dn[4] = {dn4.x, dn4.y, dn4.z, dn4.w};
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            uint32_t pw[16];
+            uint64_t sum[2] = {0ull, 0ull};
+#pragma unroll
+            for (int c = 0; c < 32; c += 2) {
+              const float w0 = ex2(s[32 * half + c]), w1 = ex2(s[32 * half + c + 1]);
+              add2(sum[c >> 2 & 1], w0, w1);
+              pw[c >> 1] = rope::pack2<__half>(w0, w1);
+            }
+            tmem_st16u(s_cols + 16 * half, pw);
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+              float lo, hi;
+              unpair(sum[q], lo, hi);
+              l_run = fmaf(lo + hi, dn[2 * half + q], l_run);
+            }
+          }
+          tmem_wait_st();
+          fence_before_sync();
+          mbar_arrive(smem_addr(&ms.p_full[blk][part]));
         }
-        tmem_wait_st();
-        fence_before_sync();
-        mbar_arrive(smem_addr(&ms.p_full[blk]));
       }
-      if (ok)
-        ok = __all_sync(0xffffffffu, role_wait(smem_addr(&ms.o_done[blk]), (t_base + n - 1) & 1, abort_flag));
+      if (ok) ok = __all_sync(0xffffffffu, role_wait(smem_addr(&ms.o_done[blk][1]), (t_base + n - 1) & 1, abort_flag));
       fence_after_sync();
       if (!ok && lane == 0 && a.status) atomicOr(a.status, RQ_STATUS_TIMEOUT);
     } else if (warp < kSoftWarps + kCodeWarps) {
       // ================= codes =================
-      const int g8 = lane >> 2, t4 = lane & 3;
-      for (int t = 0; t < n && ok; ++t) {
-        const uint32_t k = t_base + t, st = k % kStages;
-        const int t0 = (r0 + t) * kTok;
-        if (k >= kStages &&
-            !(ok = __all_sync(0xffffffffu, role_wait(smem_addr(&ms.k_empty[st]), (k / kStages - 1) & 1, abort_flag))))
-          break;
+      // warp dw takes the keys of block dw of a half tile, and half of the dims of the values of blocks
+      // p16 and p16 + 1
+      const int dw = warp & 3, p16 = dw & 2, g8 = lane >> 2, t4 = lane & 3;
+      for (int t2 = 0; t2 < 2 * n && ok; ++t2) {
+        const uint32_t k2 = 2 * t_base + t2, k = k2 >> 1, part = t2 & 1, rs = k2 % kRawStages, vs = k2 % kValueStages;
+        const int t0 = r0 * kTok + kPart * t2;
+        const uint32_t raw = raw_ring + rs * kRawBytes;
+        ok = role_wait(smem_addr(&ms.raw_full[rs]), (k2 / kRawStages) & 1, abort_flag);
+        if (part == 0 && k >= kKeyStages)
+          ok = ok && role_wait(smem_addr(&ms.k_empty[k % kKeyStages]), (k / kKeyStages - 1) & 1, abort_flag);
+        if (!(ok = __all_sync(0xffffffffu, ok))) break;
         {  // unit u: token 8 (u / 2) + g8, dims 64 (u % 2) + 16 t4 ..; the token's row is its column of S
-          uint8_t* const dst = ops + st * kOperand;
+          const uint32_t dst = k_ring + k % kKeyStages * kKeyBytes;
+          const bool there = t0 + 16 * dw < len;  // else nothing was copied
 #pragma unroll
           for (int u = 0; u < 4; ++u) {
-            const int r = 32 * (dw >> 1) + 8 * (g8 >> 1) + 4 * (dw & 1) + (g8 & 1) + 2 * (u >> 1);
-            uint8_t* const atom = dst + (u & 1) * 8192;
-            *reinterpret_cast<uint4*>(atom + sw128(r, 2 * t4)) =
-                make_uint4(widen2(kraw[u].x), widen2_hi(kraw[u].x), widen2(kraw[u].y), widen2_hi(kraw[u].y));
-            *reinterpret_cast<uint4*>(atom + sw128(r, 2 * t4 + 1)) =
-                make_uint4(widen2(kraw[u].z), widen2_hi(kraw[u].z), widen2(kraw[u].w), widen2_hi(kraw[u].w));
+            uint4 c = make_uint4(0u, 0u, 0u, 0u);
+            if (there) c = lds128(raw + dw * kBlockBytes + 16 * (32 * u + lane));
+            const int r = kPart * part + 32 * (dw >> 1) + 8 * (g8 >> 1) + 4 * (dw & 1) + (g8 & 1) + 2 * (u >> 1);
+            const uint32_t atom = dst + (u & 1) * 16384;
+            sts128(atom + sw128(r, 2 * t4), widen2(c.x), widen2_hi(c.x), widen2(c.y), widen2_hi(c.y));
+            sts128(atom + sw128(r, 2 * t4 + 1), widen2(c.z), widen2_hi(c.z), widen2(c.w), widen2_hi(c.w));
           }
-          // k_empty: S(t - 4) of both blocks is done, which was issued behind W(t - 5) V: both softmaxes
-          // are past the scales of tile t - 5, and so of t - 8, whose slot this is
+          // k_empty: S(t - 2) of both blocks is done, which was issued behind W(t - 3) V: both softmaxes
+          // are past the scales of tile t - 3, and so of t - 4, whose slot this is
           if (lane == 0) {
-            const int ev = exp_of_byte(raw_exps >> 8);
-            ms.scales[k % kScaleSlots][0][dw] = pow2(exp_of_byte(raw_exps & 0xFF));
-            ms.scales[k % kScaleSlots][1][dw] = (float)ev;
-            ms.scales[k % kScaleSlots][2][dw] = pow2(-ev);
+            uint32_t exps = 0x7F7Fu;
+            if (there) asm volatile("ld.shared.u16 %0, [%1];" : "=r"(exps) : "r"(raw + dw * kBlockBytes + kExps));
+            const int ev = exp_of_byte(exps >> 8);
+            float(*sc)[4] = ms.scales[k % kScaleSlots][part];
+            sc[0][dw] = pow2(exp_of_byte(exps & 0xFF));
+            sc[1][dw] = (float)ev;
+            sc[2][dw] = pow2(-ev);
           }
-          fence_async_smem();
-          mbar_arrive(smem_addr(&ms.k_full[st]));
+          if (part == 1) {
+            fence_async_smem();
+            mbar_arrive(smem_addr(&ms.k_full[k % kKeyStages]));
+          }
         }
-        if (k >= kStages &&
-            !(ok = __all_sync(0xffffffffu, role_wait(smem_addr(&ms.v_empty[st]), (k / kStages - 1) & 1, abort_flag))))
-          break;
+        uint4 vc[4];  // vc[2 i + b]: block p16 + b, dims 32 (2 (dw % 2) + i) + 4 g8 ..
         uint32_t bad = 0u;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < 4; ++i) {
+          vc[i] = make_uint4(0u, 0u, 0u, 0u);
+          if (t0 + 16 * (p16 + (i & 1)) < len)
+            vc[i] = lds128(raw + (p16 + (i & 1)) * kBlockBytes + kValues + 16 * (32 * (2 * (dw & 1) + (i >> 1)) + lane));
 #pragma unroll
-          for (int k4 = 0; k4 < 4; ++k4) bad |= __vcmpeq4(word(vraw[i], k4) & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
-        if (__any_sync(0xffffffffu, bad != 0u || t0 + kTok > len)) {
+          for (int k4 = 0; k4 < 4; ++k4) bad |= __vcmpeq4(word(vc[i], k4) & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(&ms.raw_empty[rs]));  // the warp has read its codes
+        if (__any_sync(0xffffffffu, bad != 0u) || t0 + kPart > len) {
           // bytes past the sequence may be anything; a NaN value goes to the rows that see it at the end
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {  // vraw[2 i + b]: block p16 + b, dims 32 (2 (dw % 2) + i) + 4 g8 ..
+          for (int i = 0; i < 4; ++i) {
             uint32_t w[4];
 #pragma unroll
             for (int k4 = 0; k4 < 4; ++k4) {
-              w[k4] = word(vraw[i], k4);
+              w[k4] = word(vc[i], k4);
 #pragma unroll
               for (int c = 0; c < 4; ++c) {
                 const int p = t0 + 16 * (p16 + (i & 1)) + 2 * t4 + (c & 1) + 8 * (c >> 1);
                 const bool isnan = (w[k4] >> (8 * c) & 0x7Fu) == 0x7Fu;
-                if (isnan && p < len) atomicMin(&nan_from[32 * (2 * (dw & 1) + (i >> 1)) + 4 * g8 + k4], p);
+                if (isnan && p < len) atomicMin(&ms.nan_from[32 * (2 * (dw & 1) + (i >> 1)) + 4 * g8 + k4], p);
                 if (isnan || p >= len) w[k4] &= ~(0xFFu << (8 * c));
               }
             }
-            vraw[i] = make_uint4(w[0], w[1], w[2], w[3]);
+            vc[i] = make_uint4(w[0], w[1], w[2], w[3]);
           }
         }
-        uint8_t* const dst = ops + (kStages + st) * kOperand;
+        if (k2 >= kValueStages &&
+            !(ok = __all_sync(0xffffffffu, role_wait(smem_addr(&ms.v_empty[vs]), (k2 / kValueStages - 1) & 1, abort_flag))))
+          break;
+        const uint32_t dst = v_ring + vs * kValueBytes;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
 #pragma unroll
           for (int k4 = 0; k4 < 4; ++k4) {
             const int d = 32 * (2 * (dw & 1) + i) + 4 * g8 + k4;
-            const uint32_t wa = word(vraw[2 * i], k4), wb = word(vraw[2 * i + 1], k4);
-            *reinterpret_cast<uint4*>(dst + sw128(d, t4 + 4 * (dw >> 1))) =
-                make_uint4(widen2(wa), widen2_hi(wa), widen2(wb), widen2_hi(wb));
+            const uint32_t wa = word(vc[2 * i], k4), wb = word(vc[2 * i + 1], k4);
+            sts128(dst + sw128(d, t4 + 4 * (dw >> 1)), widen2(wa), widen2_hi(wa), widen2(wb), widen2_hi(wb));
           }
         }
         fence_async_smem();
-        mbar_arrive(smem_addr(&ms.v_full[st]));
-        if (t + 1 < n) {
-          load();
-          look_up(r0 + t + 2);
-        }
+        mbar_arrive(smem_addr(&ms.v_full[vs]));
       }
       if (!ok && lane == 0 && a.status) atomicOr(a.status, RQ_STATUS_TIMEOUT);
-    } else if (tid == 32 * (kSoftWarps + kCodeWarps)) {
+    } else if (tid == kMmaThread) {
       // ================= MMA issue (one thread) =================
-      const uint32_t id_s = idesc_f16(kHalf, kTok), id_o = idesc_f16(kHalf, kHeadDim);
+      const uint32_t id = idesc_f16(kHalf, 128);  // S: N = 128 tokens; O: N = 128 dims
       bool issued = false;
-      auto s_mmas = [&](int bb, uint32_t kb) {
+      auto s_mmas = [&](int bb, uint32_t k) {
+        const uint32_t kb = k_ring + k % kKeyStages * kKeyBytes, qb = q_ops + 32768 * bb;
 #pragma unroll
         for (int ks = 0; ks < 8; ++ks)
-          umma_f16_ts(tmem + kColS + 64 * bb, tmem + kColQ + 64 * bb + 8 * ks, sdesc(kb + (ks >> 2) * 8192 + (ks & 3) * 32),
-                      id_s, ks > 0);
+          umma_f16_ss(tmem + kColS + 128 * bb, sdesc(qb + (ks >> 2) * 16384 + (ks & 3) * 32),
+                      sdesc(kb + (ks >> 2) * 16384 + (ks & 3) * 32), id, ks > 0);
         umma_commit(smem_addr(&ms.s_full[bb]));
         issued = true;
       };
-      auto wait_k = [&](uint32_t k) { return role_wait(smem_addr(&ms.k_full[k % kStages]), (k / kStages) & 1, abort_flag); };
-      if (ok && (ok = wait_k(t_base))) {
+      auto wait_k = [&](uint32_t k) {
+        return role_wait(smem_addr(&ms.k_full[k % kKeyStages]), (k / kKeyStages) & 1, abort_flag);
+      };
+      if ((ok = wait_k(t_base))) {
         fence_after_sync();
-        s_mmas(0, k_ring + t_base % kStages * kOperand);
-        s_mmas(1, k_ring + t_base % kStages * kOperand);
-        umma_commit(smem_addr(&ms.k_empty[t_base % kStages]));
+        s_mmas(0, t_base);
+        s_mmas(1, t_base);
+        umma_commit(smem_addr(&ms.k_empty[t_base % kKeyStages]));
       }
       for (int t = 0; t < n && ok; ++t) {
-        const uint32_t k = t_base + t, vs = k % kStages, ks1 = (k + 1) % kStages;
+        const uint32_t k = t_base + t;
         const bool next = t + 1 < n;
-        if (!(ok = role_wait(smem_addr(&ms.v_full[vs]), (k / kStages) & 1, abort_flag))) break;
-        if (next && !(ok = wait_k(k + 1))) break;
 #pragma unroll 1
-        for (int bb = 0; bb < 2; ++bb) {
-          if (!(ok = role_wait(smem_addr(&ms.p_full[bb]), k & 1, abort_flag))) break;
-          fence_after_sync();
+        for (int bb = 0; bb < 2 && ok; ++bb) {
+#pragma unroll 1
+          for (int part = 0; part < 2; ++part) {
+            const uint32_t k2 = 2 * k + part, vs = k2 % kValueStages;
+            if (bb == 0 && !(ok = role_wait(smem_addr(&ms.v_full[vs]), (k2 / kValueStages) & 1, abort_flag))) break;
+            if (!(ok = role_wait(smem_addr(&ms.p_full[bb][part]), k & 1, abort_flag))) break;
+            fence_after_sync();
 #pragma unroll
-          for (int ks = 0; ks < 4; ++ks)
-            umma_f16_ts(tmem + 128 * bb, tmem + kColS + 64 * bb + 8 * ks, sdesc(v_ring + vs * kOperand + ks * 32), id_o,
-                        t > 0 || ks > 0);
-          umma_commit(smem_addr(&ms.o_done[bb]));
-          if (next) s_mmas(bb, k_ring + ks1 * kOperand);  // over the same columns, behind the MMAs that read them
+            for (int ks = 0; ks < 4; ++ks)
+              umma_f16_ts(tmem + 128 * bb, tmem + kColS + 128 * bb + 64 * part + 8 * ks,
+                          sdesc(v_ring + vs * kValueBytes + ks * 32), id, t > 0 || part > 0 || ks > 0);
+            umma_commit(smem_addr(&ms.o_done[bb][part]));
+            if (bb == 1) umma_commit(smem_addr(&ms.v_empty[vs]));
+          }
+          if (!ok || !next) continue;
+          if (bb == 0 && !(ok = wait_k(k + 1))) break;
+          fence_after_sync();
+          s_mmas(bb, k + 1);  // over the same columns, behind the MMAs that read them
+          if (bb == 1) umma_commit(smem_addr(&ms.k_empty[(k + 1) % kKeyStages]));
         }
-        if (!ok) break;
-        umma_commit(smem_addr(&ms.v_empty[vs]));
-        if (next) umma_commit(smem_addr(&ms.k_empty[ks1]));
       }
       if (!ok) {
         if (issued) {  // nothing may be running when the tensor memory is freed
@@ -518,28 +557,72 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const Geometry g, c
         }
         if (a.status) atomicOr(a.status, RQ_STATUS_TIMEOUT);
       }
+    } else if (warp == kCopyWarp) {
+      // ================= copies of the cache's blocks =================
+      const int32_t* table = a.block_table + (size_t)b * a.max_pages;
+      const int last = min(len, (r0 + n) * kTok);  // the fragment's tokens end here
+      auto pages_of = [&](int batch) {  // pages of 32 blocks, a lane each
+        const int p = r0 * kTok + 16 * (32 * batch + lane);
+        if (p >= last) return 0;
+        int page = __ldg(table + p / g.page_size);
+        if (page < 0 || page >= g.num_pages) {
+          if (a.status) atomicOr(a.status, RQ_STATUS_BAD_PAGE);
+          page = 0;
+        }
+        return page;
+      };
+      int now = pages_of(0), later = pages_of(1);
+      for (int t2 = 0; t2 < 2 * n && ok; ++t2) {
+        const uint32_t k2 = 2 * t_base + t2, rs = k2 % kRawStages;
+        if (t2 > 0 && (t2 & 7) == 0) {
+          now = later;
+          later = pages_of((t2 >> 3) + 1);
+        }
+        if (k2 >= kRawStages &&
+            !(ok = __all_sync(0xffffffffu, role_wait(smem_addr(&ms.raw_empty[rs]), (k2 / kRawStages - 1) & 1, abort_flag))))
+          break;
+        fills = k2 + 1;
+        const uint32_t bar = smem_addr(&ms.raw_full[rs]);
+        const int p = r0 * kTok + kPart * t2, count = min(4, max(0, (last - p + 15) / 16));
+        const int page = __shfl_sync(0xffffffffu, now, 4 * (t2 & 7) + (lane & 3));
+        if (lane == 0)
+          asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(count * kBlockBytes) : "memory");
+        __syncwarp();
+        if (lane < count) {
+          const int in_page = (p + 16 * lane) % g.page_size / 16;
+          const uint8_t* src = a.pages + ((size_t)page * g.num_kv_heads + h) * g.page_bytes + (size_t)in_page * kBlockBytes;
+          asm volatile(
+              "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                  raw_ring + rs * kRawBytes + lane * kBlockBytes),
+              "l"(src), "r"(kBlockBytes), "r"(bar)
+              : "memory");
+        }
+      }
+      if (!ok) {
+        if (lane == 0 && a.status) atomicOr(a.status, RQ_STATUS_TIMEOUT);
+      }
     }
     done_tiles += n;
     fence_before_sync();
     __syncthreads();
     fence_after_sync();
-    if (ms.abort) break;  // uniform: read after the barrier, and no role raises it between here and there
+    if (ms.abort) break;  // uniform: no role raises it between the barrier and here
 
     // ---- write the rows, or the fragment's part of them ----
-    const bool whole = r0 == 0 && r1 == tiles;
-    const long long u0 = at + (long long)h * tiles, cf = part_of(u0), cl = part_of(u0 + tiles - 1);
+    const bool whole = ms.f.whole;
     auto slot_of = [&](long long c) {  // range c's first fragment, or the last of the unit's first range
-      return a.ws + (2 * c + (c == cf && part_begin(c) != u0 ? 1 : 0)) * kSlotFloats;
+      return a.ws + (2 * c + (c == ms.f.range ? ms.f.range_last : 0)) * kSlotFloats;
     };
     auto store16 = [&](int c, const float (&y)[16]) {  // dims 16 c .. of the thread's row
-      uint4* const dst = reinterpret_cast<uint4*>(reinterpret_cast<T*>(a.out) + row_at) + 2 * c;
+      uint4* const dst = reinterpret_cast<uint4*>(reinterpret_cast<T*>(a.out) + row_offset()) + 2 * c;
 #pragma unroll
       for (int i = 0; i < 2; ++i)
         dst[i] = make_uint4(rope::pack2<T>(y[8 * i], y[8 * i + 1]), rope::pack2<T>(y[8 * i + 2], y[8 * i + 3]),
                             rope::pack2<T>(y[8 * i + 4], y[8 * i + 5]), rope::pack2<T>(y[8 * i + 6], y[8 * i + 7]));
     };
-    const int qpos = valid ? len - a.T + qj : -1, srow = kHalf * blk + brow;
+    const int srow = kHalf * blk + brow;
     if (warp < kSoftWarps) {
+      const int qpos = valid ? len - a.T + row / g.group : -1;
       const float inv = whole ? (l_run == 0.f ? 0.f : 1.f / l_run) : 1.f;
       float* const slot = slot_of(blockIdx.x);
 #pragma unroll 1
@@ -551,7 +634,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const Geometry g, c
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           y[i] = l_run == 0.f ? 0.f : y[i] * inv;
-          if (nan_from[16 * c + i] <= qpos) y[i] = CUDART_NAN_F;
+          if (ms.nan_from[16 * c + i] <= qpos) y[i] = CUDART_NAN_F;
         }
         if (whole) {
           if (valid) store16(c, y);
@@ -566,15 +649,15 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const Geometry g, c
         slot[kRows * kHeadDim + srow] = m_run;
         slot[kRows * kHeadDim + kRows + srow] = l_run;
       }
-      fence_before_sync();
     }
     if (!whole) {
-      const int frags = (int)(cl - cf + 1);
+      const int frags = ms.f.frags;
+      const long long cf = ms.f.range;
       __threadfence();
       __syncthreads();
-      if (tid == 0) s_last = atomicAdd(a.cnt + cf, 1) == frags - 1;
+      if (tid == 0) ms.last = atomicAdd(a.cnt + cf, 1) == frags - 1;
       __syncthreads();
-      if (s_last) {
+      if (ms.last) {
         __threadfence();
         if (tid == 0) a.cnt[cf] = 0;  // as every launch finds it
         if (warp < kSoftWarps) {
@@ -605,16 +688,15 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const Geometry g, c
         }
       }
     }
-    __syncthreads();
-    if (tid < kHeadDim) nan_from[tid] = INT32_MAX;  // the next fragment's roles start behind a barrier
-    x += n;
-    if (x - at == (long long)tiles * g.num_kv_heads) {
-      at = x;
-      ++item;
-    }
+    __syncthreads();  // ms.f and nan_from are written again
+  }
+  if (ms.abort && warp == kCopyWarp) {  // copies in flight land before the block ends
+    for (uint32_t i = fills > kRawStages ? fills - kRawStages : 0; i < fills; ++i)
+      for (int w = 0; w < kWaitLimit; ++w)
+        if (mbar_test(smem_addr(&ms.raw_full[i % kRawStages]), (i / kRawStages) & 1)) break;
   }
   __syncthreads();
-  if (warp == 0) tmem_dealloc(tmem, 512);
+  if (warp == 0) tmem_dealloc(*(volatile uint32_t*)&ms.tmem, 512);
 }
 
 }  // namespace
