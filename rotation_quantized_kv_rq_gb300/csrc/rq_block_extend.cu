@@ -10,12 +10,13 @@
 //   softmax (warps 0-7, a thread per row): reads its row of S from tensor memory 64 columns at a
 //     time, applies scales and mask, writes fp16 weights over S;
 //   codes (warps 8-11): widen a tile's key and value codes (exact) into fp16 operands;
-//   MMA (one thread of warp 12): per block, O_b += W_b V(t) as each half of the weights is there,
+//   MMA (one thread of warp 12 + b for block b): O_b += W_b V(t) as each half of the weights is there,
 //     and behind it S_b(t + 1) = Q_b K(t + 1)^T: one block on the tensor cores while the other is in
-//     its softmax;
-//   copies (warp 13): a block is one 4112-byte bulk copy into a ring, page ids looked up 8 half
+//     its softmax.  A thread each, because issuing costs about 50 cycles an MMA, 70 a commit and 170 a
+//     wait for a barrier that is ready: 4000 a tile in one thread, against 2300 of MMAs;
+//   copies (warp 14): a block is one 4112-byte bulk copy into a ring, page ids looked up 8 half
 //     tiles ahead.
-// (Warps 14 and 15 only fill the warpgroup: 16 warps have 128 registers a thread, 17 would have 96.)
+// (Warp 15 only fills the warpgroup: 16 warps have 128 registers a thread, 17 would have 96.)
 // Why these shapes: an MMA with N = 64 takes as long as one with N = 128 (64.5 and 65.5 cycles for M =
 // 128, K = 16, A in tensor memory; 78.7 for both with A in shared memory), so S is 128 columns wide.
 // That fills tensor memory (O 2 x 128 columns, S 2 x 128 with W over it) and puts Q into shared memory.
@@ -46,7 +47,7 @@ using namespace block;
 using namespace tc;
 
 constexpr int kSoftWarps = 8, kCodeWarps = 4, kThreads = 512;
-constexpr int kMmaThread = 32 * (kSoftWarps + kCodeWarps), kCopyWarp = kSoftWarps + kCodeWarps + 1;
+constexpr int kMmaWarp = kSoftWarps + kCodeWarps, kCopyWarp = kMmaWarp + 2;  // MMA: block b by warp kMmaWarp + b
 constexpr int kHalf = 128, kRows = 2 * kHalf;  // rows of a block (M of the MMAs), of a CTA
 constexpr int kTok = 128, kPart = 64;          // tokens of a tile, of the half that softmax and V take at a time
 constexpr int kKeyStages = 2, kValueStages = 3, kRawStages = 3;  // tiles, halves, halves
@@ -71,7 +72,7 @@ struct Frag {           // tiles r0 .. r0 + n - 1 of one unit
 struct Misc {
   uint64_t raw_full[kRawStages], raw_empty[kRawStages], k_full[kKeyStages], k_empty[kKeyStages];
   uint64_t v_full[kValueStages], v_empty[kValueStages], s_full[2];
-  uint64_t p_full[2][2], o_done[2][2], drain;  // [block][half]: one phase a tile each, a tile may be a whole half ahead
+  uint64_t p_full[2][2], o_done[2][2], drain[2];  // [block][half]: one phase a tile each, a tile may be a whole half ahead
   Frag f;
   uint32_t tmem;
   int abort, last;
@@ -201,20 +202,20 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const Geometry g, c
     }
     for (int i = 0; i < kKeyStages; ++i) {
       mbar_init(smem_addr(&ms.k_full[i]), 32 * kCodeWarps);
-      mbar_init(smem_addr(&ms.k_empty[i]), 1);
+      mbar_init(smem_addr(&ms.k_empty[i]), 2);
     }
     for (int i = 0; i < kValueStages; ++i) {
       mbar_init(smem_addr(&ms.v_full[i]), 32 * kCodeWarps);
-      mbar_init(smem_addr(&ms.v_empty[i]), 1);
+      mbar_init(smem_addr(&ms.v_empty[i]), 2);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_addr(&ms.s_full[i]), 1);
+      mbar_init(smem_addr(&ms.drain[i]), 1);
       for (int part = 0; part < 2; ++part) {
         mbar_init(smem_addr(&ms.p_full[i][part]), kHalf);
         mbar_init(smem_addr(&ms.o_done[i][part]), 1);
       }
     }
-    mbar_init(smem_addr(&ms.drain), 1);
     ms.abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -502,60 +503,51 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const Geometry g, c
         mbar_arrive(smem_addr(&ms.v_full[vs]));
       }
       if (!ok && lane == 0 && a.status) atomicOr(a.status, RQ_STATUS_TIMEOUT);
-    } else if (tid == kMmaThread) {
-      // ================= MMA issue (one thread) =================
-      const uint32_t id = idesc_f16(kHalf, 128);  // S: N = 128 tokens; O: N = 128 dims
-      bool issued = false;
-      auto s_mmas = [&](int bb, uint32_t k) {
-        const uint32_t kb = k_ring + k % kKeyStages * kKeyBytes, qb = q_ops + 32768 * bb;
+    } else if (warp < kMmaWarp + 2) {
+      // ================= MMA issue (one thread per block) =================
+      if (lane == 0) {
+        const int bb = warp - kMmaWarp;
+        const uint32_t id = idesc_f16(kHalf, 128);  // S: N = 128 tokens; O: N = 128 dims
+        const uint32_t s_cols = tmem + kColS + 128 * bb, q_at = q_ops + 32768 * bb;
+        bool issued = false;
+        auto s_mmas = [&](uint32_t k) {  // S_b of tile k
+          const uint32_t k_at = k_ring + k % kKeyStages * kKeyBytes;
+          if (!(ok = role_wait(smem_addr(&ms.k_full[k % kKeyStages]), (k / kKeyStages) & 1, abort_flag))) return;
+          fence_after_sync();
 #pragma unroll
-        for (int ks = 0; ks < 8; ++ks)
-          umma_f16_ss(tmem + kColS + 128 * bb, sdesc(qb + (ks >> 2) * 16384 + (ks & 3) * 32),
-                      sdesc(kb + (ks >> 2) * 16384 + (ks & 3) * 32), id, ks > 0);
-        umma_commit(smem_addr(&ms.s_full[bb]));
-        issued = true;
-      };
-      auto wait_k = [&](uint32_t k) {
-        return role_wait(smem_addr(&ms.k_full[k % kKeyStages]), (k / kKeyStages) & 1, abort_flag);
-      };
-      if ((ok = wait_k(t_base))) {
-        fence_after_sync();
-        s_mmas(0, t_base);
-        s_mmas(1, t_base);
-        umma_commit(smem_addr(&ms.k_empty[t_base % kKeyStages]));
-      }
-      for (int t = 0; t < n && ok; ++t) {
-        const uint32_t k = t_base + t;
-        const bool next = t + 1 < n;
-#pragma unroll 1
-        for (int bb = 0; bb < 2 && ok; ++bb) {
+          for (int ks = 0; ks < 8; ++ks)
+            umma_f16_ss(s_cols, sdesc(q_at + (ks >> 2) * 16384 + (ks & 3) * 32), sdesc(k_at + (ks >> 2) * 16384 + (ks & 3) * 32),
+                        id, ks > 0);
+          umma_commit(smem_addr(&ms.s_full[bb]));
+          umma_commit(smem_addr(&ms.k_empty[k % kKeyStages]));
+          issued = true;
+        };
+        s_mmas(t_base);
+        for (int t = 0; t < n && ok; ++t) {
+          const uint32_t k = t_base + t;
 #pragma unroll 1
           for (int part = 0; part < 2; ++part) {
             const uint32_t k2 = 2 * k + part, vs = k2 % kValueStages;
-            if (bb == 0 && !(ok = role_wait(smem_addr(&ms.v_full[vs]), (k2 / kValueStages) & 1, abort_flag))) break;
+            if (!(ok = role_wait(smem_addr(&ms.v_full[vs]), (k2 / kValueStages) & 1, abort_flag))) break;
             if (!(ok = role_wait(smem_addr(&ms.p_full[bb][part]), k & 1, abort_flag))) break;
             fence_after_sync();
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks)
-              umma_f16_ts(tmem + 128 * bb, tmem + kColS + 128 * bb + 64 * part + 8 * ks,
-                          sdesc(v_ring + vs * kValueBytes + ks * 32), id, t > 0 || part > 0 || ks > 0);
+              umma_f16_ts(tmem + 128 * bb, s_cols + 64 * part + 8 * ks, sdesc(v_ring + vs * kValueBytes + ks * 32), id,
+                          t > 0 || part > 0 || ks > 0);
             umma_commit(smem_addr(&ms.o_done[bb][part]));
-            if (bb == 1) umma_commit(smem_addr(&ms.v_empty[vs]));
+            umma_commit(smem_addr(&ms.v_empty[vs]));
           }
-          if (!ok || !next) continue;
-          if (bb == 0 && !(ok = wait_k(k + 1))) break;
-          fence_after_sync();
-          s_mmas(bb, k + 1);  // over the same columns, behind the MMAs that read them
-          if (bb == 1) umma_commit(smem_addr(&ms.k_empty[(k + 1) % kKeyStages]));
+          if (ok && t + 1 < n) s_mmas(k + 1);  // over the same columns, behind the MMAs that read them
         }
-      }
-      if (!ok) {
-        if (issued) {  // nothing may be running when the tensor memory is freed
-          umma_commit(smem_addr(&ms.drain));
-          for (int i = 0; i < kWaitLimit; ++i)
-            if (mbar_test(smem_addr(&ms.drain), 0u)) break;
+        if (!ok) {
+          if (issued) {  // nothing may be running when the tensor memory is freed
+            umma_commit(smem_addr(&ms.drain[bb]));
+            for (int i = 0; i < kWaitLimit; ++i)
+              if (mbar_test(smem_addr(&ms.drain[bb]), 0u)) break;
+          }
+          if (a.status) atomicOr(a.status, RQ_STATUS_TIMEOUT);
         }
-        if (a.status) atomicOr(a.status, RQ_STATUS_TIMEOUT);
       }
     } else if (warp == kCopyWarp) {
       // ================= copies of the cache's blocks =================
