@@ -8,7 +8,7 @@
 // for codes it makes subnormal (below 2^-14 of the scale's largest value).
 //
 // Work is split by runs: consecutive tokens of the call in consecutive slots of one block.  One warp
-// codes a run's keys and values of one head, so that a block's scale is one reduction in one warp
+// codes a run's keys or its values of one head, so that a block's scale is one reduction in one warp
 // and no atomics order anything; the run's tokens all belong to one block by construction, and two
 // runs of one call never share a block (include/rq.h asks for that).
 #include "../../include/rq.h"
@@ -23,12 +23,18 @@ using namespace block;
 
 constexpr int kMaxWarps = 8;
 
-__device__ __forceinline__ bool finite(float x) { return (__float_as_uint(x) & 0x7F800000u) != 0x7F800000u; }
+constexpr uint32_t kInf = 0x7F800000u;
 
-__device__ __forceinline__ float warp_max(float x) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
-  return x;
+// The scale's exponent for values whose largest magnitude over the warp has the bits `top`, or, if
+// that is not finite, for the finite ones among them (a second look, given by `finite_top`).
+template <typename F>
+__device__ __forceinline__ int warp_exp(uint32_t top, bool& bad, F finite_top) {
+  top = __reduce_max_sync(0xffffffffu, top);
+  if (top >= kInf) {
+    bad = true;
+    top = __reduce_max_sync(0xffffffffu, finite_top());
+  }
+  return exp_of(__uint_as_float(top));
 }
 
 // Token t's slot, or -1: padding, past the call's end, or a fault (reported once, by `report`).
@@ -59,39 +65,62 @@ __device__ __forceinline__ int slot_of(const Geometry& g, const BlockAppendArgs&
 }
 
 // Rows `off` .. off + cnt - 1 of a block's keys from tokens t0 .. (head h).  cs: cosines and sines
-// of token t0 + i at cs[i].  Returns the exponent; sets bad on a value that is not finite.
+// of token t0 + i at cs[i].  Returns the exponent; sets bad on a value that is not finite.  The rows
+// stay in registers as they came (32, where the turned f32 values would take 64 and leave an SM one
+// CTA): they are turned once for the largest magnitude and again for the codes.
 template <typename T, bool INTERLEAVED>
 __device__ __forceinline__ int append_keys(const BlockAppendArgs& a, uint8_t* blk, int h, long long t0, int off,
                                            int cnt, int e_old, const float4 (*cs)[2][16], int lane, bool& bad) {
   const int j = lane & 15, half = lane >> 4;
   const Lane l = lane_of<INTERLEAVED>(j, a.in.rope.rotary_dim);
   const T* src = reinterpret_cast<const T*>(a.in.k.x) + (long long)h * kHeadDim;
+  const bool norm = a.in.k.weight != nullptr;
   uint2 raw[8][2];
 #pragma unroll
   for (int i = 0; i < 8; ++i)
     if (2 * i + half < cnt) load8(raw[i], src + (t0 + 2 * i + half) * a.in.k.stride, l);
-  float x[8][8], top = 0.f;
+  float w[8], inv[8];
+  if (norm) load_weights(w, a.in.k.weight, l);
+  auto turned = [&](float (&x)[8], int i, bool first) {
+    widen8<T>(x, raw[i]);
+    if (norm) {
+      if (first) inv[i] = inv_rms(x, a.in.eps);
+      scale8(x, inv[i], w);
+    }
+    if (l.pair >= 0) {
+      const float4 c0 = cs[2 * i + half][0][j], c1 = cs[2 * i + half][1][j];
+      const float2 p[4] = {make_float2(c0.x, c0.y), make_float2(c0.z, c0.w), make_float2(c1.x, c1.y),
+                           make_float2(c1.z, c1.w)};
+      turn8<INTERLEAVED>(x, p, l);
+    }
+  };
+  uint32_t top = 0;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     if (2 * i + half < cnt) {
-      widen8<T>(x[i], raw[i]);
-      norm8(x[i], a.in.k.weight, a.in.eps, l);
-      if (l.pair >= 0) {
-        const float4 c0 = cs[2 * i + half][0][j], c1 = cs[2 * i + half][1][j];
-        const float2 p[4] = {make_float2(c0.x, c0.y), make_float2(c0.z, c0.w), make_float2(c1.x, c1.y),
-                             make_float2(c1.z, c1.w)};
-        turn8<INTERLEAVED>(x[i], p, l);
-      }
+      float x[8];
+      turned(x, i, true);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        if (finite(x[i][k]))
-          top = fmaxf(top, fabsf(x[i][k]));
-        else
-          bad = true;
-      }
+      for (int k = 0; k < 8; ++k) top = max(top, __float_as_uint(x[k]) & 0x7FFFFFFFu);
     }
   }
-  const int e_new = exp_of(warp_max(top)), e = off == 0 ? e_new : max(e_old, e_new);
+  const int e_new = warp_exp(top, bad, [&]() {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (2 * i + half < cnt) {
+        float x[8];
+        turned(x, i, false);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const uint32_t u = __float_as_uint(x[k]) & 0x7FFFFFFFu;
+          m = max(m, u < kInf ? u : 0u);
+        }
+      }
+    }
+    return m;
+  });
+  const int e = off == 0 ? e_new : max(e_old, e_new);
   if (off > 0 && e > e_old) {
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
@@ -109,11 +138,23 @@ __device__ __forceinline__ int append_keys(const BlockAppendArgs& a, uint8_t* bl
   for (int i = 0; i < 8; ++i) {
     if (2 * i + half < cnt) {
       const int r = off + 2 * i + half;
-      *reinterpret_cast<uint32_t*>(blk + place(r, l.o0)) = code4(x[i][0] * s, x[i][1] * s, x[i][2] * s, x[i][3] * s);
-      *reinterpret_cast<uint32_t*>(blk + place(r, l.o1)) = code4(x[i][4] * s, x[i][5] * s, x[i][6] * s, x[i][7] * s);
+      float x[8];
+      turned(x, i, false);
+      *reinterpret_cast<uint32_t*>(blk + place(r, l.o0)) = code4(x[0] * s, x[1] * s, x[2] * s, x[3] * s);
+      *reinterpret_cast<uint32_t*>(blk + place(r, l.o1)) = code4(x[4] * s, x[5] * s, x[6] * s, x[7] * s);
     }
   }
   return e;
+}
+
+__device__ __forceinline__ uint32_t abs_max2(uint32_t a, uint32_t b, __half) {  // per half: max(a, |b|), NaN if any is
+  const __half2 m = __hmax2_nan(*reinterpret_cast<const __half2*>(&a), __habs2(*reinterpret_cast<const __half2*>(&b)));
+  return *reinterpret_cast<const uint32_t*>(&m);
+}
+__device__ __forceinline__ uint32_t abs_max2(uint32_t a, uint32_t b, __nv_bfloat16) {
+  const __nv_bfloat162 m =
+      __hmax2_nan(*reinterpret_cast<const __nv_bfloat162*>(&a), __habs2(*reinterpret_cast<const __nv_bfloat162*>(&b)));
+  return *reinterpret_cast<const uint32_t*>(&m);
 }
 
 // The same of values: lane takes dims 4 lane .. 4 lane + 3 of every row, whose 64 bytes of a block
@@ -128,20 +169,26 @@ __device__ __forceinline__ int append_values(const BlockAppendArgs& a, uint8_t* 
     raw[r] = make_uint2(0u, 0u);
     if (r >= off && r < off + cnt) raw[r] = __ldg(reinterpret_cast<const uint2*>(src + (t0 + r - off) * a.v_stride));
   }
-  float top = 0.f;
+  uint32_t m2 = 0u;
 #pragma unroll
-  for (int r = 0; r < 16; ++r) {
-    const float2 p = unpack2<T>(raw[r].x), q = unpack2<T>(raw[r].y);
-    const float x[4] = {p.x, p.y, q.x, q.y};
+  for (int r = 0; r < 16; ++r) m2 = abs_max2(abs_max2(m2, raw[r].x, T()), raw[r].y, T());
+  const float2 m = unpack2<T>(m2);
+  const uint32_t top = max(__float_as_uint(m.x) & 0x7FFFFFFFu, __float_as_uint(m.y) & 0x7FFFFFFFu);
+  const int e_new = warp_exp(top, bad, [&]() {
+    uint32_t f = 0;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      if (finite(x[k]))
-        top = fmaxf(top, fabsf(x[k]));
-      else
-        bad = true;
+    for (int r = 0; r < 16; ++r) {
+      const float2 p = unpack2<T>(raw[r].x), q = unpack2<T>(raw[r].y);
+      const float x[4] = {p.x, p.y, q.x, q.y};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t u = __float_as_uint(x[k]) & 0x7FFFFFFFu;
+        f = max(f, u < kInf ? u : 0u);
+      }
     }
-  }
-  const int e_new = exp_of(warp_max(top)), e = off == 0 ? e_new : max(e_old, e_new);
+    return f;
+  });
+  const int e = off == 0 ? e_new : max(e_old, e_new);
   const bool grow = off > 0 && e > e_old;
   const float s = pow2(-e);
   uint4* const dst = reinterpret_cast<uint4*>(blk + kValues + 512 * (lane >> 3) + 64 * (lane & 7));
@@ -179,12 +226,22 @@ __device__ __forceinline__ int append_values(const BlockAppendArgs& a, uint8_t* 
 // decode step's single tokens over the SMs; W = 16 (long appends) makes one block of a run a
 // CTA's work.  blockIdx.y splits the heads.
 template <typename T, bool INTERLEAVED, int W>
-__global__ void __launch_bounds__(32 * kMaxWarps) block_append_kernel(const Geometry g, const BlockAppendArgs a) {
+__global__ void __launch_bounds__(32 * kMaxWarps, 3) block_append_kernel(const Geometry g, const BlockAppendArgs a) {
   constexpr int kTokens = W == 1 ? 16 : 32;  // a run reaches at most 15 tokens past its first
   __shared__ float4 cs[kTokens][2][16];  // [token][c][j]: pairs 4j + 2c and 4j + 2c + 1
   __shared__ int run_at[W], run_cnt[W], run_slot[W], num_runs, reach;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
   const long long base = (long long)blockIdx.x * W;
+  const int hw = tid >> 4, hws = blockDim.x >> 4, j = tid & 15;
+  auto angles = [&](int i) {  // cosines and sines of token base + i, by a half-warp
+    if (4 * j < a.in.rope.rotary_dim >> 1 && base + i < a.in.n) {
+      float2 p[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) p[k] = cos_sin(a.in.rope, 4 * j + k, a.in.positions, a.in.n, base + i);
+      cs[i][0][j] = make_float4(p[0].x, p[0].y, p[1].x, p[1].y);
+      cs[i][1][j] = make_float4(p[2].x, p[2].y, p[3].x, p[3].y);
+    }
+  };
   if (warp == 0) {
     const int s = lane < kTokens ? slot_of(g, a, base + lane, lane < W && blockIdx.y == 0) : -1;
     int prev = __shfl_up_sync(0xffffffffu, s, 1);
@@ -200,43 +257,37 @@ __global__ void __launch_bounds__(32 * kMaxWarps) block_append_kernel(const Geom
       run_at[i] = lane, run_cnt[i] = cnt, run_slot[i] = s;
     }
     const int ends = __reduce_max_sync(0xffffffffu, cnt > 0 ? lane + cnt : 0);
-    if (lane == 0) {
-      num_runs = __popc(leads);
-      reach = max(ends, a.in.q.heads > 0 ? (int)min((long long)W, a.in.n - base) : 0);
-    }
+    if (lane == 0) num_runs = __popc(leads), reach = ends;
+  } else {  // meanwhile the angles of the W tokens
+    for (int i = hw - 2; i < W; i += hws - 2) angles(i);
   }
   __syncthreads();
-  const int hw = tid >> 4, hws = blockDim.x >> 4, j = tid & 15;
-  if (a.in.rope.rotary_dim > 0) {
-    if (4 * j < a.in.rope.rotary_dim >> 1) {
-      for (int i = hw; i < reach; i += hws) {
-        float2 p[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) p[k] = cos_sin(a.in.rope, 4 * j + k, a.in.positions, a.in.n, base + i);
-        cs[i][0][j] = make_float4(p[0].x, p[0].y, p[1].x, p[1].y);
-        cs[i][1][j] = make_float4(p[2].x, p[2].y, p[3].x, p[3].y);
-      }
-    }
+  if (reach > W) {  // a run goes on past them
+    for (int i = W + hw; i < reach; i += hws) angles(i);
     __syncthreads();
   }
 
   bool bad = false;
-  const int items = num_runs * g.num_kv_heads;
+  const int items = 2 * num_runs * g.num_kv_heads;  // (run, keys or values, head)
   for (int it = blockIdx.y * warps + warp; it < items; it += gridDim.y * warps) {
-    const int run = it / g.num_kv_heads, h = it % g.num_kv_heads;
+    const int run = it / (2 * g.num_kv_heads), of = it % (2 * g.num_kv_heads), h = of % g.num_kv_heads;
+    const bool keys = of < g.num_kv_heads;
     const int at = run_at[run], cnt = run_cnt[run], slot = run_slot[run], off = slot % kBlockTokens;
     uint8_t* blk = a.pages + ((size_t)(slot / g.page_size) * g.num_kv_heads + h) * g.page_bytes +
                    (size_t)(slot % g.page_size / kBlockTokens) * kBlockBytes;
-    const uint32_t old = off > 0 ? *reinterpret_cast<const uint16_t*>(blk + kExps) : 0u;
-    const int ek_old = exp_of_byte(old & 0xFF), ev_old = exp_of_byte(old >> 8);
-    const int ek = append_keys<T, INTERLEAVED>(a, blk, h, base + at, off, cnt, ek_old, cs + at, lane, bad);
-    const int ev = append_values<T>(a, blk, h, base + at, off, cnt, ev_old, lane, bad);
-    if (lane == 0) *reinterpret_cast<uint16_t*>(blk + kExps) = (uint16_t)((ek + 127) | (ev + 127) << 8);
+    uint8_t* const exp_at = blk + kExps + (keys ? 0 : 1);
+    const int e_old = off > 0 ? exp_of_byte(*exp_at) : kMinExp;
+    const int e = keys ? append_keys<T, INTERLEAVED>(a, blk, h, base + at, off, cnt, e_old, cs + at, lane, bad)
+                       : append_values<T>(a, blk, h, base + at, off, cnt, e_old, lane, bad);
+    if (lane == 0) *exp_at = (uint8_t)(e + 127);
   }
   if (bad && a.status) atomicOr(a.status, RQ_STATUS_NOT_FINITE);
 
   if (a.in.q.heads > 0) {
     const Lane l = lane_of<INTERLEAVED>(j, a.in.rope.rotary_dim);
+    const bool norm = a.in.q.weight != nullptr;
+    float w[8];
+    if (norm) load_weights(w, a.in.q.weight, l);
     // W = 16: a half-warp takes a token's heads; W = 1: the half-warps share the token's heads
     const int i0 = W == 1 ? 0 : hw, h0 = W == 1 ? blockIdx.y * hws + hw : blockIdx.y;
     const int hstep = W == 1 ? gridDim.y * hws : gridDim.y;
@@ -259,7 +310,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps) block_append_kernel(const Geom
           if (h + u * hstep >= a.in.q.heads) break;
           float x[8];
           widen8<T>(x, raw[u]);
-          norm8(x, a.in.q.weight, a.in.eps, l);
+          if (norm) scale8(x, inv_rms(x, a.in.eps), w);
           turn8<INTERLEAVED>(x, p, l);
           store8(dst + (long long)(h + u * hstep) * kHeadDim, x, l);
         }
@@ -271,10 +322,10 @@ __global__ void __launch_bounds__(32 * kMaxWarps) block_append_kernel(const Geom
 template <typename T, bool INTERLEAVED>
 void launch(const Geometry& g, const BlockAppendArgs& a, int num_sms, cudaStream_t stream) {
   const int hkv = g.num_kv_heads, hq = a.in.q.heads;
-  int warps = hkv < 2 ? 2 : (hkv > kMaxWarps ? kMaxWarps : hkv);
+  int warps = hkv < 2 ? 2 : (2 * hkv > kMaxWarps ? kMaxWarps : 2 * hkv);
   if (a.in.n < 16LL * num_sms * 2) {  // too few tokens for every SM to have two CTAs of 16
     if (hq > 0) warps = kMaxWarps;
-    const int most = max((hkv + warps - 1) / warps, (hq + 2 * warps - 1) / (2 * warps));
+    const int most = max((2 * hkv + warps - 1) / warps, (hq + 2 * warps - 1) / (2 * warps));
     long long split = (2LL * num_sms + a.in.n - 1) / a.in.n;
     split = split > most ? most : split;
     block_append_kernel<T, INTERLEAVED, 1><<<dim3((unsigned)a.in.n, (unsigned)split), 32 * warps, 0, stream>>>(g, a);

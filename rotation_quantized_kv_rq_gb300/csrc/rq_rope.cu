@@ -44,7 +44,11 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const NormRopeArgs 
       const int h = r < a.q.heads ? r : r - a.q.heads;
       float x[8];
       widen8<T>(x, raw[u]);
-      norm8(x, s.weight, a.eps, l);
+      if (s.weight != nullptr) {
+        float w[8];
+        load_weights(w, s.weight, l);
+        scale8(x, inv_rms(x, a.eps), w);
+      }
       turn8<INTERLEAVED>(x, cs, l);
       store8(reinterpret_cast<T*>(s.out) + t * s.out_stride + (long long)h * kHeadDim, x, l);
     }

@@ -95,20 +95,25 @@ __device__ __forceinline__ void widen8(float (&x)[8], const uint2 (&raw)[2]) {
   }
 }
 
-// The row's norm (weight w, null for none).  Every lane of the warp must call it.
-__device__ __forceinline__ void norm8(float (&x)[8], const float* w, float eps, const Lane& l) {
-  if (w == nullptr) return;  // uniform over the half-warp: the shuffles below pair its lanes only
+// 1 / sqrt(mean(x^2) + eps) of the row.  All lanes of the half-warp call it.
+__device__ __forceinline__ float inv_rms(const float (&x)[8], float eps) {
   float ss = 0.f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
   const uint32_t mask = 0xFFFFu << (threadIdx.x & 16);
 #pragma unroll
   for (int o = 8; o > 0; o >>= 1) ss += __shfl_xor_sync(mask, ss, o);
-  const float r = __frsqrt_rn(fmaf(ss, 1.f / kHeadDim, eps));
-  const float4 w0 = __ldg(reinterpret_cast<const float4*>(w + l.o0));
-  const float4 w1 = __ldg(reinterpret_cast<const float4*>(w + l.o1));
-  x[0] *= r * w0.x, x[1] *= r * w0.y, x[2] *= r * w0.z, x[3] *= r * w0.w;
-  x[4] *= r * w1.x, x[5] *= r * w1.y, x[6] *= r * w1.z, x[7] *= r * w1.w;
+  return __frsqrt_rn(fmaf(ss, 1.f / kHeadDim, eps));
+}
+// The lane's eight weights.
+__device__ __forceinline__ void load_weights(float (&w)[8], const float* weight, const Lane& l) {
+  const float4 w0 = __ldg(reinterpret_cast<const float4*>(weight + l.o0));
+  const float4 w1 = __ldg(reinterpret_cast<const float4*>(weight + l.o1));
+  w[0] = w0.x, w[1] = w0.y, w[2] = w0.z, w[3] = w0.w, w[4] = w1.x, w[5] = w1.y, w[6] = w1.z, w[7] = w1.w;
+}
+__device__ __forceinline__ void scale8(float (&x)[8], float r, const float (&w)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] *= r * w[i];
 }
 
 // Turns the lane's four pairs; cs[i] = (cos, sin) of pair l.pair + i.
