@@ -226,7 +226,7 @@ __device__ __forceinline__ int append_values(const BlockAppendArgs& a, uint8_t* 
 // decode step's single tokens over the SMs; W = 16 (long appends) makes one block of a run a
 // CTA's work.  blockIdx.y splits the heads.
 template <typename T, bool INTERLEAVED, int W>
-__global__ void __launch_bounds__(32 * kMaxWarps, 3) block_append_kernel(const Geometry g, const BlockAppendArgs a) {
+__global__ void __launch_bounds__(32 * kMaxWarps, 2) block_append_kernel(const Geometry g, const BlockAppendArgs a) {
   constexpr int kTokens = W == 1 ? 16 : 32;  // a run reaches at most 15 tokens past its first
   __shared__ float4 cs[kTokens][2][16];  // [token][c][j]: pairs 4j + 2c and 4j + 2c + 1
   __shared__ int run_at[W], run_cnt[W], run_slot[W], num_runs, reach;
@@ -285,12 +285,8 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 3) block_append_kernel(const G
 
   if (a.in.q.heads > 0) {
     const Lane l = lane_of<INTERLEAVED>(j, a.in.rope.rotary_dim);
-    const bool norm = a.in.q.weight != nullptr;
-    float w[8];
-    if (norm) load_weights(w, a.in.q.weight, l);
     // W = 16: a half-warp takes a token's heads; W = 1: the half-warps share the token's heads
     const int i0 = W == 1 ? 0 : hw, h0 = W == 1 ? blockIdx.y * hws + hw : blockIdx.y;
-    const int hstep = W == 1 ? gridDim.y * hws : gridDim.y;
     for (int i = i0; i < W && base + i < a.in.n; i += hws) {
       float2 p[4];
       if (l.pair >= 0) {
@@ -298,23 +294,9 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 3) block_append_kernel(const G
         p[0] = make_float2(c0.x, c0.y), p[1] = make_float2(c0.z, c0.w);
         p[2] = make_float2(c1.x, c1.y), p[3] = make_float2(c1.z, c1.w);
       }
-      const T* src = reinterpret_cast<const T*>(a.in.q.x) + (base + i) * a.in.q.stride;
-      T* dst = reinterpret_cast<T*>(a.in.q.out) + (base + i) * a.in.q.out_stride;
-      for (int h = h0; h < a.in.q.heads; h += 4 * hstep) {
-        uint2 raw[4][2];
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-          if (h + u * hstep < a.in.q.heads) load8(raw[u], src + (long long)(h + u * hstep) * kHeadDim, l);
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          if (h + u * hstep >= a.in.q.heads) break;
-          float x[8];
-          widen8<T>(x, raw[u]);
-          if (norm) scale8(x, inv_rms(x, a.in.eps), w);
-          turn8<INTERLEAVED>(x, p, l);
-          store8(dst + (long long)(h + u * hstep) * kHeadDim, x, l);
-        }
-      }
+      turn_rows<T, INTERLEAVED>(reinterpret_cast<const T*>(a.in.q.x) + (base + i) * a.in.q.stride,
+                                reinterpret_cast<T*>(a.in.q.out) + (base + i) * a.in.q.out_stride, h0,
+                                W == 1 ? gridDim.y * hws : gridDim.y, a.in.q.heads, a.in.q.weight, a.in.eps, p, l);
     }
   }
 }
@@ -323,7 +305,7 @@ template <typename T, bool INTERLEAVED>
 void launch(const Geometry& g, const BlockAppendArgs& a, int num_sms, cudaStream_t stream) {
   const int hkv = g.num_kv_heads, hq = a.in.q.heads;
   int warps = hkv < 2 ? 2 : (2 * hkv > kMaxWarps ? kMaxWarps : 2 * hkv);
-  if (a.in.n < 16LL * num_sms * 2) {  // too few tokens for every SM to have two CTAs of 16
+  if (a.in.n < 1024) {
     if (hq > 0) warps = kMaxWarps;
     const int most = max((2 * hkv + warps - 1) / warps, (hq + 2 * warps - 1) / (2 * warps));
     long long split = (2LL * num_sms + a.in.n - 1) / a.in.n;

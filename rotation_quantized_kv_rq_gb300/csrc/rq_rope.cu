@@ -7,52 +7,29 @@ namespace {
 using namespace rope;
 
 constexpr int kThreads = 256;
-constexpr int kBatch = 4;  // rows a half-warp has in flight
+constexpr int kBatch = 4;  // rows that a half-warp has in flight
 
 // A half-warp takes `per` rows of one token (rows part, part + parts, ...: neighbouring half-warps
 // read neighbouring rows), so that the token's cosines and sines, in registers, serve all of them.
-// Loads of kBatch rows are in flight together.  In place is safe: a row is read by the half-warp
-// that writes it, before it writes.
 template <typename T, bool INTERLEAVED>
 __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const NormRopeArgs a, int parts) {
   const int j = threadIdx.x & 15;
   const long long hw = ((long long)blockIdx.x * kThreads + threadIdx.x) >> 4;
   const long long t = hw / parts;
   if (t >= a.n) return;  // whole half-warps; the shuffles pair lanes of one half-warp
-  const int part = (int)(hw % parts), rows = a.q.heads + a.k.heads;
+  const int part = (int)(hw % parts);
   const Lane l = lane_of<INTERLEAVED>(j, a.rope.rotary_dim);
   float2 cs[4];
   if (l.pair >= 0) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) cs[i] = cos_sin(a.rope, l.pair + i, a.positions, a.n, t);
   }
-  for (int r0 = part; r0 < rows; r0 += kBatch * parts) {
-    uint2 raw[kBatch][2];
-#pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-      const int r = r0 + u * parts;
-      if (r >= rows) break;
-      const RowsDev& s = r < a.q.heads ? a.q : a.k;
-      const int h = r < a.q.heads ? r : r - a.q.heads;
-      load8(raw[u], reinterpret_cast<const T*>(s.x) + t * s.stride + (long long)h * kHeadDim, l);
-    }
-#pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-      const int r = r0 + u * parts;
-      if (r >= rows) break;
-      const RowsDev& s = r < a.q.heads ? a.q : a.k;
-      const int h = r < a.q.heads ? r : r - a.q.heads;
-      float x[8];
-      widen8<T>(x, raw[u]);
-      if (s.weight != nullptr) {
-        float w[8];
-        load_weights(w, s.weight, l);
-        scale8(x, inv_rms(x, a.eps), w);
-      }
-      turn8<INTERLEAVED>(x, cs, l);
-      store8(reinterpret_cast<T*>(s.out) + t * s.out_stride + (long long)h * kHeadDim, x, l);
-    }
-  }
+  turn_rows<T, INTERLEAVED>(reinterpret_cast<const T*>(a.q.x) + t * a.q.stride, reinterpret_cast<T*>(a.q.out) + t * a.q.out_stride,
+                            part, parts, a.q.heads, a.q.weight, a.eps, cs, l);
+  // the keys go on where the queries end: row heads + h of the token
+  const int k0 = part >= a.q.heads ? part - a.q.heads : (parts - (a.q.heads - part) % parts) % parts;
+  turn_rows<T, INTERLEAVED>(reinterpret_cast<const T*>(a.k.x) + t * a.k.stride, reinterpret_cast<T*>(a.k.out) + t * a.k.out_stride,
+                            k0, parts, a.k.heads, a.k.weight, a.eps, cs, l);
 }
 
 template <typename T>

@@ -46,6 +46,26 @@ __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// Two f32 operations in one instruction (half the issue slots; the rate is the same).
+__device__ __forceinline__ uint64_t f2(float lo, float hi) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+  return d;
+}
+__device__ __forceinline__ void split2(uint64_t d, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(d));
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+
 // Where lane j of a half-warp stands in a row.
 struct Lane {
   int o0, o1;  // its two runs of four dims
@@ -97,9 +117,12 @@ __device__ __forceinline__ void widen8(float (&x)[8], const uint2 (&raw)[2]) {
 
 // 1 / sqrt(mean(x^2) + eps) of the row.  All lanes of the half-warp call it.
 __device__ __forceinline__ float inv_rms(const float (&x)[8], float eps) {
-  float ss = 0.f;
+  uint64_t s2 = 0ull;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
+  for (int i = 0; i < 8; i += 2) s2 = fma2(f2(x[i], x[i + 1]), f2(x[i], x[i + 1]), s2);
+  float ss, hi;
+  split2(s2, ss, hi);
+  ss += hi;
   const uint32_t mask = 0xFFFFu << (threadIdx.x & 16);
 #pragma unroll
   for (int o = 8; o > 0; o >>= 1) ss += __shfl_xor_sync(mask, ss, o);
@@ -112,20 +135,30 @@ __device__ __forceinline__ void load_weights(float (&w)[8], const float* weight,
   w[0] = w0.x, w[1] = w0.y, w[2] = w0.z, w[3] = w0.w, w[4] = w1.x, w[5] = w1.y, w[6] = w1.z, w[7] = w1.w;
 }
 __device__ __forceinline__ void scale8(float (&x)[8], float r, const float (&w)[8]) {
+  const uint64_t r2 = f2(r, r);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) x[i] *= r * w[i];
+  for (int i = 0; i < 8; i += 2) split2(mul2(f2(x[i], x[i + 1]), mul2(r2, f2(w[i], w[i + 1]))), x[i], x[i + 1]);
 }
 
 // Turns the lane's four pairs; cs[i] = (cos, sin) of pair l.pair + i.
 template <bool INTERLEAVED>
 __device__ __forceinline__ void turn8(float (&x)[8], const float2 (&cs)[4], const Lane& l) {
   if (l.pair < 0) return;
+  if (INTERLEAVED) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int a = INTERLEAVED ? 2 * i : i, b = INTERLEAVED ? 2 * i + 1 : 4 + i;
-    const float u = x[a], v = x[b];
-    x[a] = u * cs[i].x - v * cs[i].y;
-    x[b] = u * cs[i].y + v * cs[i].x;
+    for (int i = 0; i < 4; ++i) {
+      const float u = x[2 * i], v = x[2 * i + 1];
+      x[2 * i] = u * cs[i].x - v * cs[i].y;
+      x[2 * i + 1] = u * cs[i].y + v * cs[i].x;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; i += 2) {
+      const uint64_t c = f2(cs[i].x, cs[i + 1].x), s = f2(cs[i].y, cs[i + 1].y), ns = f2(-cs[i].y, -cs[i + 1].y);
+      const uint64_t u = f2(x[i], x[i + 1]), v = f2(x[4 + i], x[5 + i]);
+      split2(fma2(u, c, mul2(v, ns)), x[i], x[i + 1]);
+      split2(fma2(u, s, mul2(v, c)), x[4 + i], x[5 + i]);
+    }
   }
 }
 
@@ -133,6 +166,38 @@ template <typename T>
 __device__ __forceinline__ void store8(T* row, const float (&x)[8], const Lane& l) {
   *reinterpret_cast<uint2*>(row + l.o0) = make_uint2(pack2<T>(x[0], x[1]), pack2<T>(x[2], x[3]));
   *reinterpret_cast<uint2*>(row + l.o1) = make_uint2(pack2<T>(x[4], x[5]), pack2<T>(x[6], x[7]));
+}
+
+// Heads first, first + step, ... of one token's rows at src to dst: norm (weight: the norm's, null for
+// none) and rotation.  Loads of four rows are in flight together.  In place is safe: a row is read by
+// the half-warp that writes it, before it writes.
+template <typename T, bool INTERLEAVED>
+__device__ __forceinline__ void turn_rows(const T* src, T* dst, int first, int step, int heads, const float* weight,
+                                          float eps, const float2 (&cs)[4], const Lane& l) {
+  constexpr int kBatch = 4;
+  if (first >= heads) return;
+  float w[8];
+  if (weight) load_weights(w, weight, l);
+  src += first * kHeadDim;
+  dst += first * kHeadDim;
+  const int stride = step * kHeadDim;
+  for (int left = (heads - first + step - 1) / step; left > 0; left -= kBatch) {
+    uint2 raw[kBatch][2];
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u)
+      if (u < left) load8(raw[u], src + u * stride, l);
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      if (u >= left) break;
+      float x[8];
+      widen8<T>(x, raw[u]);
+      if (weight) scale8(x, inv_rms(x, eps), w);
+      turn8<INTERLEAVED>(x, cs, l);
+      store8(dst + u * stride, x, l);
+    }
+    src += kBatch * stride;
+    dst += kBatch * stride;
+  }
 }
 
 }  // namespace rope
