@@ -22,8 +22,17 @@ using namespace rope;
 using namespace block;
 
 constexpr int kMaxWarps = 8;
+constexpr int kLongAppend = 1024;  // tokens from which a CTA takes 16 of them
+constexpr int kSplitAppend = 8192; // tokens from which the queries have a launch of their own
 
 constexpr uint32_t kInf = 0x7F800000u;
+
+__device__ __forceinline__ uint32_t code4(uint64_t a, uint64_t b) {
+  float x0, x1, x2, x3;
+  split2(a, x0, x1);
+  split2(b, x2, x3);
+  return block::code4(x0, x1, x2, x3);
+}
 
 // The scale's exponent for values whose largest magnitude over the warp has the bits `top`, or, if
 // that is not finite, for the finite ones among them (a second look, given by `finite_top`).
@@ -79,29 +88,28 @@ __device__ __forceinline__ int append_keys(const BlockAppendArgs& a, uint8_t* bl
 #pragma unroll
   for (int i = 0; i < 8; ++i)
     if (2 * i + half < cnt) load8(raw[i], src + (t0 + 2 * i + half) * a.in.k.stride, l);
-  float w[8], inv[8];
+  uint64_t w[4];
+  float inv[8];
   if (norm) load_weights(w, a.in.k.weight, l);
-  auto turned = [&](float (&x)[8], int i, bool first) {
+  auto turned = [&](uint64_t (&x)[4], int i, bool first) {
     widen8<T>(x, raw[i]);
     if (norm) {
       if (first) inv[i] = inv_rms(x, a.in.eps);
       scale8(x, inv[i], w);
     }
-    if (l.pair >= 0) {
-      const float4 c0 = cs[2 * i + half][0][j], c1 = cs[2 * i + half][1][j];
-      const float2 p[4] = {make_float2(c0.x, c0.y), make_float2(c0.z, c0.w), make_float2(c1.x, c1.y),
-                           make_float2(c1.z, c1.w)};
-      turn8<INTERLEAVED>(x, p, l);
-    }
+    if (l.pair >= 0) turn8<INTERLEAVED>(x, angles_of(cs[2 * i + half][0][j], cs[2 * i + half][1][j]), l);
+  };
+  auto largest = [](uint32_t m, uint64_t x) {  // of the magnitudes' bits
+    return max(max(m, (uint32_t)x & 0x7FFFFFFFu), (uint32_t)(x >> 32) & 0x7FFFFFFFu);
   };
   uint32_t top = 0;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     if (2 * i + half < cnt) {
-      float x[8];
+      uint64_t x[4];
       turned(x, i, true);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) top = max(top, __float_as_uint(x[k]) & 0x7FFFFFFFu);
+      for (int k = 0; k < 4; ++k) top = largest(top, x[k]);
     }
   }
   const int e_new = warp_exp(top, bad, [&]() {
@@ -109,11 +117,11 @@ __device__ __forceinline__ int append_keys(const BlockAppendArgs& a, uint8_t* bl
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       if (2 * i + half < cnt) {
-        float x[8];
+        uint64_t x[4];
         turned(x, i, false);
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-          const uint32_t u = __float_as_uint(x[k]) & 0x7FFFFFFFu;
+          const uint32_t u = (uint32_t)(x[k >> 1] >> (32 * (k & 1))) & 0x7FFFFFFFu;
           m = max(m, u < kInf ? u : 0u);
         }
       }
@@ -132,16 +140,18 @@ __device__ __forceinline__ int append_keys(const BlockAppendArgs& a, uint8_t* bl
     }
     __syncwarp();  // the rows below overwrite some of these bytes
   }
-  const float s = pow2(-e);
-  auto place = [&](int r, int d) { return ((2 * (r >> 3) + (d >> 6)) * 32 + (r & 7) * 4 + ((d & 63) >> 4)) * 16 + (d & 15); };
+  const uint64_t s2 = f2(pow2(-e), pow2(-e));
+  auto place = [&](int d) { return ((d >> 6) * 32 + ((d & 63) >> 4)) * 16 + (d & 15); };  // of token 0
+  uint8_t* const d0 = blk + place(l.o0);
+  uint8_t* const d1 = blk + place(l.o1);
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     if (2 * i + half < cnt) {
-      const int r = off + 2 * i + half;
-      float x[8];
+      const int r = off + 2 * i + half, at = (r >> 3) * 1024 + (r & 7) * 64;
+      uint64_t x[4];
       turned(x, i, false);
-      *reinterpret_cast<uint32_t*>(blk + place(r, l.o0)) = code4(x[0] * s, x[1] * s, x[2] * s, x[3] * s);
-      *reinterpret_cast<uint32_t*>(blk + place(r, l.o1)) = code4(x[4] * s, x[5] * s, x[6] * s, x[7] * s);
+      *reinterpret_cast<uint32_t*>(d0 + at) = code4(mul2(x[0], s2), mul2(x[1], s2));
+      *reinterpret_cast<uint32_t*>(d1 + at) = code4(mul2(x[2], s2), mul2(x[3], s2));
     }
   }
   return e;
@@ -190,7 +200,7 @@ __device__ __forceinline__ int append_values(const BlockAppendArgs& a, uint8_t* 
   });
   const int e = off == 0 ? e_new : max(e_old, e_new);
   const bool grow = off > 0 && e > e_old;
-  const float s = pow2(-e);
+  const uint64_t s2 = f2(pow2(-e), pow2(-e));
   uint4* const dst = reinterpret_cast<uint4*>(blk + kValues + 512 * (lane >> 3) + 64 * (lane & 7));
 #pragma unroll
   for (int t = 0; t < 4; ++t) {
@@ -199,7 +209,7 @@ __device__ __forceinline__ int append_values(const BlockAppendArgs& a, uint8_t* 
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const float2 p = unpack2<T>(raw[rows[k]].x), q = unpack2<T>(raw[rows[k]].y);
-      w[k] = code4(p.x * s, p.y * s, q.x * s, q.y * s);  // one token, four dims
+      w[k] = code4(mul2(f2(p.x, p.y), s2), mul2(f2(q.x, q.y), s2));  // one token, four dims
       if (rows[k] >= off && rows[k] < off + cnt) mask |= 0xFFu << (8 * k);
     }
     if (mask == 0u && !grow) continue;
@@ -228,18 +238,17 @@ __device__ __forceinline__ int append_values(const BlockAppendArgs& a, uint8_t* 
 template <typename T, bool INTERLEAVED, int W>
 __global__ void __launch_bounds__(32 * kMaxWarps, 2) block_append_kernel(const Geometry g, const BlockAppendArgs a) {
   constexpr int kTokens = W == 1 ? 16 : 32;  // a run reaches at most 15 tokens past its first
-  __shared__ float4 cs[kTokens][2][16];  // [token][c][j]: pairs 4j + 2c and 4j + 2c + 1
+  __shared__ float4 cs[kTokens][2][16];  // [token][cosines, sines][j]: pairs 4j .. 4j + 3
   __shared__ int run_at[W], run_cnt[W], run_slot[W], num_runs, reach;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
   const long long base = (long long)blockIdx.x * W;
   const int hw = tid >> 4, hws = blockDim.x >> 4, j = tid & 15;
   auto angles = [&](int i) {  // cosines and sines of token base + i, by a half-warp
     if (4 * j < a.in.rope.rotary_dim >> 1 && base + i < a.in.n) {
-      float2 p[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) p[k] = cos_sin(a.in.rope, 4 * j + k, a.in.positions, a.in.n, base + i);
-      cs[i][0][j] = make_float4(p[0].x, p[0].y, p[1].x, p[1].y);
-      cs[i][1][j] = make_float4(p[2].x, p[2].y, p[3].x, p[3].y);
+      float4 c, s;
+      cos_sin4(c, s, a.in.rope, 4 * j, a.in.positions, a.in.n, base + i);
+      cs[i][0][j] = c;
+      cs[i][1][j] = s;
     }
   };
   if (warp == 0) {
@@ -288,12 +297,8 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 2) block_append_kernel(const G
     // W = 16: a half-warp takes a token's heads; W = 1: the half-warps share the token's heads
     const int i0 = W == 1 ? 0 : hw, h0 = W == 1 ? blockIdx.y * hws + hw : blockIdx.y;
     for (int i = i0; i < W && base + i < a.in.n; i += hws) {
-      float2 p[4];
-      if (l.pair >= 0) {
-        const float4 c0 = cs[i][0][j], c1 = cs[i][1][j];
-        p[0] = make_float2(c0.x, c0.y), p[1] = make_float2(c0.z, c0.w);
-        p[2] = make_float2(c1.x, c1.y), p[3] = make_float2(c1.z, c1.w);
-      }
+      Angles p;
+      if (l.pair >= 0) p = angles_of(cs[i][0][j], cs[i][1][j]);
       turn_rows<T, INTERLEAVED>(reinterpret_cast<const T*>(a.in.q.x) + (base + i) * a.in.q.stride,
                                 reinterpret_cast<T*>(a.in.q.out) + (base + i) * a.in.q.out_stride, h0,
                                 W == 1 ? gridDim.y * hws : gridDim.y, a.in.q.heads, a.in.q.weight, a.in.eps, p, l);
@@ -305,7 +310,7 @@ template <typename T, bool INTERLEAVED>
 void launch(const Geometry& g, const BlockAppendArgs& a, int num_sms, cudaStream_t stream) {
   const int hkv = g.num_kv_heads, hq = a.in.q.heads;
   int warps = hkv < 2 ? 2 : (2 * hkv > kMaxWarps ? kMaxWarps : 2 * hkv);
-  if (a.in.n < 1024) {
+  if (a.in.n < kLongAppend) {
     if (hq > 0) warps = kMaxWarps;
     const int most = max((2 * hkv + warps - 1) / warps, (hq + 2 * warps - 1) / (2 * warps));
     long long split = (2LL * num_sms + a.in.n - 1) / a.in.n;
@@ -318,8 +323,17 @@ void launch(const Geometry& g, const BlockAppendArgs& a, int num_sms, cudaStream
 
 }  // namespace
 
-cudaError_t launch_block_append(const Geometry& g, const BlockAppendArgs& a, int num_sms, cudaStream_t stream) {
+cudaError_t launch_block_append(const Geometry& g, BlockAppendArgs a, int num_sms, cudaStream_t stream) {
   if (a.in.n <= 0) return cudaSuccess;
+  if (a.in.n >= kSplitAppend && a.in.q.heads > 0) {
+    // long calls turn the queries in a launch of their own, with twice this kernel's warps on an SM
+    NormRopeArgs q = a.in;
+    q.k = RowsDev{};
+    q.bf16 = g.bf16;
+    const cudaError_t e = launch_norm_rope(q, num_sms, stream);
+    if (e != cudaSuccess) return e;
+    a.in.q = RowsDev{};
+  }
   if (g.bf16) {
     if (a.in.rope.interleaved)
       launch<__nv_bfloat16, true>(g, a, num_sms, stream);

@@ -174,7 +174,7 @@ struct BlockAppendArgs {
   uint8_t* pages;
   int32_t* status;
 };
-cudaError_t launch_block_append(const Geometry& g, const BlockAppendArgs& a, int num_sms, cudaStream_t stream);
+cudaError_t launch_block_append(const Geometry& g, BlockAppendArgs a, int num_sms, cudaStream_t stream);
 
 // Attention over the 8-bit cache (decode, chain and tree verify): a.ws and a.cnt hold
 // block_attention_workspace floats and counters (the counters zero between launches); n_tiles_n,

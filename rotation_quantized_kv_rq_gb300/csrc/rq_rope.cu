@@ -19,10 +19,11 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const NormRopeArgs 
   if (t >= a.n) return;  // whole half-warps; the shuffles pair lanes of one half-warp
   const int part = (int)(hw % parts);
   const Lane l = lane_of<INTERLEAVED>(j, a.rope.rotary_dim);
-  float2 cs[4];
+  Angles cs;
   if (l.pair >= 0) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) cs[i] = cos_sin(a.rope, l.pair + i, a.positions, a.n, t);
+    float4 c, si;
+    cos_sin4(c, si, a.rope, l.pair, a.positions, a.n, t);
+    cs = angles_of(c, si);
   }
   turn_rows<T, INTERLEAVED>(reinterpret_cast<const T*>(a.q.x) + t * a.q.stride, reinterpret_cast<T*>(a.q.out) + t * a.q.out_stride,
                             part, parts, a.q.heads, a.q.weight, a.eps, cs, l);

@@ -46,7 +46,9 @@ __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// Two f32 operations in one instruction (half the issue slots; the rate is the same).
+// Two f32 values in one 64-bit register pair and two operations in one instruction (half the issue
+// slots at the same rate).  A lane's eight values stay in four such pairs throughout: packing and
+// unpacking around single operations would cost more moves than it saves.
 __device__ __forceinline__ uint64_t f2(float lo, float hi) {
   uint64_t d;
   asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
@@ -100,26 +102,46 @@ __device__ __forceinline__ float2 cos_sin(const RopeTable& r, int p, const int32
   sincospif((float)frac * 4.656612873077393e-10f, &s, &c);  // 2^-31: half turns
   return make_float2(c * r.scale, s * r.scale);
 }
+// Cosines, sines and negated sines of the lane's pairs, two to a word.
+struct Angles {
+  uint64_t c[2], s[2], n[2];
+};
+__device__ __forceinline__ Angles angles_of(const float4& c, const float4& s) {
+  Angles a;
+  a.c[0] = f2(c.x, c.y), a.c[1] = f2(c.z, c.w);
+  a.s[0] = f2(s.x, s.y), a.s[1] = f2(s.z, s.w);
+  a.n[0] = f2(-s.x, -s.y), a.n[1] = f2(-s.z, -s.w);
+  return a;
+}
+__device__ __forceinline__ void cos_sin4(float4& c, float4& s, const RopeTable& r, int p, const int32_t* positions,
+                                         long long n, long long t) {
+  const float2 a0 = cos_sin(r, p, positions, n, t), a1 = cos_sin(r, p + 1, positions, n, t);
+  const float2 a2 = cos_sin(r, p + 2, positions, n, t), a3 = cos_sin(r, p + 3, positions, n, t);
+  c = make_float4(a0.x, a1.x, a2.x, a3.x);
+  s = make_float4(a0.y, a1.y, a2.y, a3.y);
+}
 
 template <typename T>
 __device__ __forceinline__ void load8(uint2 (&raw)[2], const T* row, const Lane& l) {
   raw[0] = *reinterpret_cast<const uint2*>(row + l.o0);  // plain loads: the row may be written in place
   raw[1] = *reinterpret_cast<const uint2*>(row + l.o1);
 }
+// The lane's eight values: dims (o0, o0 + 1), (o0 + 2, o0 + 3), (o1, o1 + 1), (o1 + 2, o1 + 3).
 template <typename T>
-__device__ __forceinline__ void widen8(float (&x)[8], const uint2 (&raw)[2]) {
+__device__ __forceinline__ void widen8(uint64_t (&x)[4], const uint2 (&raw)[2]) {
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const float2 a = unpack2<T>(raw[i].x), b = unpack2<T>(raw[i].y);
-    x[4 * i] = a.x, x[4 * i + 1] = a.y, x[4 * i + 2] = b.x, x[4 * i + 3] = b.y;
+    x[2 * i] = f2(a.x, a.y);
+    x[2 * i + 1] = f2(b.x, b.y);
   }
 }
 
 // 1 / sqrt(mean(x^2) + eps) of the row.  All lanes of the half-warp call it.
-__device__ __forceinline__ float inv_rms(const float (&x)[8], float eps) {
-  uint64_t s2 = 0ull;
+__device__ __forceinline__ float inv_rms(const uint64_t (&x)[4], float eps) {
+  uint64_t s2 = mul2(x[0], x[0]);
 #pragma unroll
-  for (int i = 0; i < 8; i += 2) s2 = fma2(f2(x[i], x[i + 1]), f2(x[i], x[i + 1]), s2);
+  for (int i = 1; i < 4; ++i) s2 = fma2(x[i], x[i], s2);
   float ss, hi;
   split2(s2, ss, hi);
   ss += hi;
@@ -129,43 +151,51 @@ __device__ __forceinline__ float inv_rms(const float (&x)[8], float eps) {
   return __frsqrt_rn(fmaf(ss, 1.f / kHeadDim, eps));
 }
 // The lane's eight weights.
-__device__ __forceinline__ void load_weights(float (&w)[8], const float* weight, const Lane& l) {
+__device__ __forceinline__ void load_weights(uint64_t (&w)[4], const float* weight, const Lane& l) {
   const float4 w0 = __ldg(reinterpret_cast<const float4*>(weight + l.o0));
   const float4 w1 = __ldg(reinterpret_cast<const float4*>(weight + l.o1));
-  w[0] = w0.x, w[1] = w0.y, w[2] = w0.z, w[3] = w0.w, w[4] = w1.x, w[5] = w1.y, w[6] = w1.z, w[7] = w1.w;
+  w[0] = f2(w0.x, w0.y), w[1] = f2(w0.z, w0.w), w[2] = f2(w1.x, w1.y), w[3] = f2(w1.z, w1.w);
 }
-__device__ __forceinline__ void scale8(float (&x)[8], float r, const float (&w)[8]) {
+__device__ __forceinline__ void scale8(uint64_t (&x)[4], float r, const uint64_t (&w)[4]) {
   const uint64_t r2 = f2(r, r);
 #pragma unroll
-  for (int i = 0; i < 8; i += 2) split2(mul2(f2(x[i], x[i + 1]), mul2(r2, f2(w[i], w[i + 1]))), x[i], x[i + 1]);
+  for (int i = 0; i < 4; ++i) x[i] = mul2(x[i], mul2(r2, w[i]));
 }
 
-// Turns the lane's four pairs; cs[i] = (cos, sin) of pair l.pair + i.
+// Turns the lane's four pairs.
 template <bool INTERLEAVED>
-__device__ __forceinline__ void turn8(float (&x)[8], const float2 (&cs)[4], const Lane& l) {
+__device__ __forceinline__ void turn8(uint64_t (&x)[4], const Angles& a, const Lane& l) {
   if (l.pair < 0) return;
-  if (INTERLEAVED) {
+  if (INTERLEAVED) {  // pair i = x[i]
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float u = x[2 * i], v = x[2 * i + 1];
-      x[2 * i] = u * cs[i].x - v * cs[i].y;
-      x[2 * i + 1] = u * cs[i].y + v * cs[i].x;
+      float u, v, c0, c1, s0, s1;
+      split2(x[i], u, v);
+      split2(a.c[i >> 1], c0, c1);
+      split2(a.s[i >> 1], s0, s1);
+      const float c = i & 1 ? c1 : c0, s = i & 1 ? s1 : s0;
+      x[i] = f2(u * c - v * s, u * s + v * c);
     }
-  } else {
+  } else {  // pair 2 i + k = (half k of x[i], half k of x[i + 2])
 #pragma unroll
-    for (int i = 0; i < 4; i += 2) {
-      const uint64_t c = f2(cs[i].x, cs[i + 1].x), s = f2(cs[i].y, cs[i + 1].y), ns = f2(-cs[i].y, -cs[i + 1].y);
-      const uint64_t u = f2(x[i], x[i + 1]), v = f2(x[4 + i], x[5 + i]);
-      split2(fma2(u, c, mul2(v, ns)), x[i], x[i + 1]);
-      split2(fma2(u, s, mul2(v, c)), x[4 + i], x[5 + i]);
+    for (int i = 0; i < 2; ++i) {
+      const uint64_t u = x[i], v = x[i + 2];
+      x[i] = fma2(u, a.c[i], mul2(v, a.n[i]));
+      x[i + 2] = fma2(u, a.s[i], mul2(v, a.c[i]));
     }
   }
 }
 
 template <typename T>
-__device__ __forceinline__ void store8(T* row, const float (&x)[8], const Lane& l) {
-  *reinterpret_cast<uint2*>(row + l.o0) = make_uint2(pack2<T>(x[0], x[1]), pack2<T>(x[2], x[3]));
-  *reinterpret_cast<uint2*>(row + l.o1) = make_uint2(pack2<T>(x[4], x[5]), pack2<T>(x[6], x[7]));
+__device__ __forceinline__ uint32_t narrow2(uint64_t x) {
+  float lo, hi;
+  split2(x, lo, hi);
+  return pack2<T>(lo, hi);
+}
+template <typename T>
+__device__ __forceinline__ void store8(T* row, const uint64_t (&x)[4], const Lane& l) {
+  *reinterpret_cast<uint2*>(row + l.o0) = make_uint2(narrow2<T>(x[0]), narrow2<T>(x[1]));
+  *reinterpret_cast<uint2*>(row + l.o1) = make_uint2(narrow2<T>(x[2]), narrow2<T>(x[3]));
 }
 
 // Heads first, first + step, ... of one token's rows at src to dst: norm (weight: the norm's, null for
@@ -173,10 +203,10 @@ __device__ __forceinline__ void store8(T* row, const float (&x)[8], const Lane& 
 // the half-warp that writes it, before it writes.
 template <typename T, bool INTERLEAVED>
 __device__ __forceinline__ void turn_rows(const T* src, T* dst, int first, int step, int heads, const float* weight,
-                                          float eps, const float2 (&cs)[4], const Lane& l) {
+                                          float eps, const Angles& cs, const Lane& l) {
   constexpr int kBatch = 4;
   if (first >= heads) return;
-  float w[8];
+  uint64_t w[4];
   if (weight) load_weights(w, weight, l);
   src += first * kHeadDim;
   dst += first * kHeadDim;
@@ -189,7 +219,7 @@ __device__ __forceinline__ void turn_rows(const T* src, T* dst, int first, int s
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
       if (u >= left) break;
-      float x[8];
+      uint64_t x[4];
       widen8<T>(x, raw[u]);
       if (weight) scale8(x, inv_rms(x, eps), w);
       turn8<INTERLEAVED>(x, cs, l);
