@@ -167,28 +167,37 @@ __device__ __forceinline__ uint32_t abs_max2(uint32_t a, uint32_t b, __nv_bfloat
   return *reinterpret_cast<const uint32_t*>(&m);
 }
 
-// The same of values: lane takes dims 4 lane .. 4 lane + 3 of every row, whose 64 bytes of a block
-// are its own; bytes of rows outside the run stay as they are.
+// The same of values.  Lane 4 g + t takes tokens 2t, 2t + 1, 2t + 8, 2t + 9 and of each the dims 32 u + 4 g
+// .. + 3, which are unit u of its 16 bytes in the block: a store of the warp is 512 bytes in a row, a
+// load 64 of four rows.  Bytes of rows outside the run stay as they are.
 template <typename T>
 __device__ __forceinline__ int append_values(const BlockAppendArgs& a, uint8_t* blk, int h, long long t0, int off,
                                              int cnt, int e_old, int lane, bool& bad) {
-  const T* src = reinterpret_cast<const T*>(a.v) + (long long)h * kHeadDim + 4 * lane;
-  uint2 raw[16];
+  const int g4 = 4 * (lane >> 2), t2 = 2 * (lane & 3);
+  uint2 raw[4][4];  // [token][unit]
+  uint32_t mask = 0u;
 #pragma unroll
-  for (int r = 0; r < 16; ++r) {
-    raw[r] = make_uint2(0u, 0u);
-    if (r >= off && r < off + cnt) raw[r] = __ldg(reinterpret_cast<const uint2*>(src + (t0 + r - off) * a.v_stride));
+  for (int i = 0; i < 4; ++i) {
+    const int r = t2 + (i & 1) + 8 * (i >> 1);
+    const bool here = r >= off && r < off + cnt;
+    const T* src = reinterpret_cast<const T*>(a.v) + (t0 + r - off) * a.v_stride + (long long)h * kHeadDim + g4;
+    if (here) mask |= 0xFFu << (8 * i);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      raw[i][u] = make_uint2(0u, 0u);
+      if (here) raw[i][u] = __ldg(reinterpret_cast<const uint2*>(src + 32 * u));
+    }
   }
   uint32_t m2 = 0u;
 #pragma unroll
-  for (int r = 0; r < 16; ++r) m2 = abs_max2(abs_max2(m2, raw[r].x, T()), raw[r].y, T());
+  for (int i = 0; i < 16; ++i) m2 = abs_max2(abs_max2(m2, raw[i >> 2][i & 3].x, T()), raw[i >> 2][i & 3].y, T());
   const float2 m = unpack2<T>(m2);
   const uint32_t top = max(__float_as_uint(m.x) & 0x7FFFFFFFu, __float_as_uint(m.y) & 0x7FFFFFFFu);
   const int e_new = warp_exp(top, bad, [&]() {
     uint32_t f = 0;
 #pragma unroll
-    for (int r = 0; r < 16; ++r) {
-      const float2 p = unpack2<T>(raw[r].x), q = unpack2<T>(raw[r].y);
+    for (int i = 0; i < 16; ++i) {
+      const float2 p = unpack2<T>(raw[i >> 2][i & 3].x), q = unpack2<T>(raw[i >> 2][i & 3].y);
       const float x[4] = {p.x, p.y, q.x, q.y};
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
@@ -200,26 +209,24 @@ __device__ __forceinline__ int append_values(const BlockAppendArgs& a, uint8_t* 
   });
   const int e = off == 0 ? e_new : max(e_old, e_new);
   const bool grow = off > 0 && e > e_old;
+  if (mask == 0u && !grow) return e;
   const uint64_t s2 = f2(pow2(-e), pow2(-e));
-  uint4* const dst = reinterpret_cast<uint4*>(blk + kValues + 512 * (lane >> 3) + 64 * (lane & 7));
+  uint4* const dst = reinterpret_cast<uint4*>(blk + kValues) + lane;
 #pragma unroll
-  for (int t = 0; t < 4; ++t) {
-    const int rows[4] = {2 * t, 2 * t + 1, 2 * t + 8, 2 * t + 9};
-    uint32_t w[4], mask = 0u;
+  for (int u = 0; u < 4; ++u) {
+    uint32_t w[4];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const float2 p = unpack2<T>(raw[rows[k]].x), q = unpack2<T>(raw[rows[k]].y);
-      w[k] = code4(mul2(f2(p.x, p.y), s2), mul2(f2(q.x, q.y), s2));  // one token, four dims
-      if (rows[k] >= off && rows[k] < off + cnt) mask |= 0xFFu << (8 * k);
+    for (int i = 0; i < 4; ++i) {
+      const float2 p = unpack2<T>(raw[i][u].x), q = unpack2<T>(raw[i][u].y);
+      w[i] = code4(mul2(f2(p.x, p.y), s2), mul2(f2(q.x, q.y), s2));  // one token, four dims
     }
-    if (mask == 0u && !grow) continue;
     // to one dim, four tokens: a 4 x 4 transpose of bytes
     const uint32_t a0 = __byte_perm(w[0], w[1], 0x5140), a1 = __byte_perm(w[2], w[3], 0x5140);
     const uint32_t b0 = __byte_perm(w[0], w[1], 0x7362), b1 = __byte_perm(w[2], w[3], 0x7362);
     uint4 c = make_uint4(__byte_perm(a0, a1, 0x5410), __byte_perm(a0, a1, 0x7632), __byte_perm(b0, b1, 0x5410),
                          __byte_perm(b0, b1, 0x7632));
     if (mask != 0xFFFFFFFFu) {
-      uint4 o = dst[t];
+      uint4 o = dst[32 * u];
       if (grow) {
         o.x = shrink4(o.x, e - e_old), o.y = shrink4(o.y, e - e_old);
         o.z = shrink4(o.z, e - e_old), o.w = shrink4(o.w, e - e_old);
@@ -227,7 +234,7 @@ __device__ __forceinline__ int append_values(const BlockAppendArgs& a, uint8_t* 
       c.x = (c.x & mask) | (o.x & ~mask), c.y = (c.y & mask) | (o.y & ~mask);
       c.z = (c.z & mask) | (o.z & ~mask), c.w = (c.w & mask) | (o.w & ~mask);
     }
-    dst[t] = c;
+    dst[32 * u] = c;
   }
   return e;
 }
