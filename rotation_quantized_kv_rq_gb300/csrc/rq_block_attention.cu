@@ -468,44 +468,47 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) splitk_kernel(const
       if (s_last) {
         __threadfence();
         if (tid == 0) a.cnt[cf] = 0;  // as every launch finds it
-        float* const wt = reinterpret_cast<float*>(smem);  // weights [frag][kRows]
-        for (int i = tid; i < frags * rows; i += kThreads) {
-          const int f = i / rows, r = i % rows;
-          wt[f * kRows + r] = __ldcg(slot_of(cf + f) + r * kRowStride + kHeadDim);
-        }
+        // all (m, l) at once, then a warp per row with eight fragments' loads in flight: the join is as
+        // long as its chain of memory latencies (one thread per dim and two fragments at a time took
+        // 16 us for 76 fragments)
+        float2* const ml = reinterpret_cast<float2*>(smem);  // [row][frag]
+        for (int i = tid; i < frags * rows; i += kThreads)
+          ml[i] = __ldcg(reinterpret_cast<const float2*>(slot_of(cf + i % frags) + i / frags * kRowStride + kHeadDim));
         __syncthreads();
         for (int r = warp; r < rows; r += kWarps) {
           float top = kNone, sum = 0.f;
-          for (int f = lane; f < frags; f += 32) top = fmaxf(top, wt[f * kRows + r]);
+          for (int f = lane; f < frags; f += 32) top = fmaxf(top, ml[r * frags + f].x);
 #pragma unroll
           for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
           for (int f = lane; f < frags; f += 32) {
-            const float w = ex2(wt[f * kRows + r] - top);
-            wt[f * kRows + r] = w;
-            sum = fmaf(__ldcg(slot_of(cf + f) + r * kRowStride + kHeadDim + 1), w, sum);
+            const float w = ex2(ml[r * frags + f].x - top);
+            sum = fmaf(ml[r * frags + f].y, w, sum);
+            ml[r * frags + f].x = w;
           }
 #pragma unroll
           for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-          if (lane == 0) s_l[0][r] = sum;
-        }
-        __syncthreads();
-        for (int rb = 0; rb < rows; rb += 8) {
-          float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-          const int nr = min(8, rows - rb);
-#pragma unroll 2
-          for (int f = 0; f < frags; ++f) {
-            const float* src = slot_of(cf + f) + rb * kRowStride + tid;
+          __syncwarp();
+          float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+          const float4* src = reinterpret_cast<const float4*>(slot_of(cf) + r * kRowStride) + lane;
+          const float4* next = reinterpret_cast<const float4*>(slot_of(cf + 1) + r * kRowStride) + lane;  // and evenly on
+          auto add = [&](const float4& v, float w) {
+            acc.x = fmaf(v.x, w, acc.x), acc.y = fmaf(v.y, w, acc.y), acc.z = fmaf(v.z, w, acc.z), acc.w = fmaf(v.w, w, acc.w);
+          };
+          add(__ldcg(src), ml[r * frags].x);
+          int f = 1;
+          for (; f + 8 <= frags; f += 8) {
+            float4 v[8];
 #pragma unroll
-            for (int r = 0; r < 8; ++r)
-              if (r < nr) acc[r] = fmaf(__ldcg(src + r * kRowStride), wt[f * kRows + rb + r], acc[r]);
-          }
-          for (int r = 0; r < nr; ++r) {
-            const float sum = s_l[0][rb + r];
-            float y = acc[0];
+            for (int i = 0; i < 8; ++i) v[i] = __ldcg(next + (size_t)i * (2 * kRows * kRowStride / 4));
 #pragma unroll
-            for (int k = 1; k < 8; ++k) y = r == k ? acc[k] : y;
-            out_row(rb + r)[tid] = (T)(sum == 0.f ? 0.f : y / sum);
+            for (int i = 0; i < 8; ++i) add(v[i], ml[r * frags + f + i].x);
+            next += (size_t)8 * (2 * kRows * kRowStride / 4);
           }
+          for (; f < frags; ++f, next += 2 * kRows * kRowStride / 4) add(__ldcg(next), ml[r * frags + f].x);
+          const float inv = sum == 0.f ? 0.f : 1.f / sum;
+          if (sum == 0.f) acc = make_float4(0.f, 0.f, 0.f, 0.f);
+          *(reinterpret_cast<uint2*>(out_row(r)) + lane) =
+              make_uint2(rope::pack2<T>(acc.x * inv, acc.y * inv), rope::pack2<T>(acc.z * inv, acc.w * inv));
         }
       }
     }
