@@ -13,16 +13,20 @@
 //
 // What bounds it: the cache is read once, 257 bytes a (token, kv head), against 4 MMAs' worth of
 // work; so the design keeps copies in flight.  A block is one 4112-byte bulk copy into a ring of
-// the warp's own, no thread of the CTA waits for another inside a fragment, and four CTAs of four
-// warps share an SM (48 tiles in flight), so that one's opening and joining hide behind the
-// others' copies.  Rows of a kv head beyond 8 (group > 8, verify) share the widened tile: up to
-// three n-tiles of 8 rows a warp (one CTA less per SM for each).
+// the warp's own, and no thread of the CTA waits for another inside a fragment; an SM has 48 tiles
+// in flight.  With many units, four CTAs of four warps share an SM, so that one's opening and
+// joining hide behind the others' copies; with fewer units than SMs one CTA of 16 warps does, which
+// cuts a unit into a quarter of the parts to join (1 x 32K: 19 instead of 76).  Rows of a kv head beyond
+// 8 (group > 8, verify) share the widened tile: up to three n-tiles of 8 rows a warp, with the
+// registers for 12 and 8 warps an SM.
 //
-// Work is cut evenly: a unit is (sequence, kv head, group of n-tiles) and costs one round per four
-// tiles; the rounds of all units in order are cut into one range per CTA, on the device from
+// Work is cut evenly: a unit is (sequence, kv head, group of n-tiles) and costs one round per tile of
+// each warp; the rounds of all units in order are cut into one range per CTA, on the device from
 // seq_lens.  A unit that spans ranges is joined by the last of its CTAs to finish, in the order of
 // the ranges (the result does not depend on which came last).  A CTA has at most two such
-// fragments, its first and its last, so the workspace is two slots and one counter a CTA.
+// fragments, its first and its last, so the workspace is two slots and one counter a CTA.  Short
+// calls are chains of memory latencies (0.6 us each), so what can load together does: a fragment's
+// page ids with its queries, the parts to join by bulk copies of a chunk at once.
 #include <math_constants.h>
 
 #include <type_traits>
@@ -37,15 +41,17 @@ namespace {
 
 using namespace block;
 
-constexpr int kWarps = 4, kThreads = 32 * kWarps;
 constexpr float kMargin = 8.f;      // log2 slack of the running maximum
 constexpr float kNone = -1e30f;     // running maximum before any visible token
 constexpr int kRowStride = 132;     // floats per joined row (128 and padding)
 
-__host__ __device__ constexpr int ctas_per_sm(int nt) { return nt == 1 ? 4 : nt == 2 ? 3 : 2; }
-__host__ __device__ constexpr int stages(int nt) { return nt == 1 ? 3 : nt == 2 ? 4 : 6; }  // tiles of a warp's ring
-constexpr int ring_bytes(int nt) { return kWarps * stages(nt) * kBlockBytes; }
-constexpr int smem_bytes(int nt) { return ring_bytes(nt) + kWarps * stages(nt) * 8; }
+constexpr int kRowBytes = kRowStride * 4;  // a joined row: 128 sums, the maximum, the weights' sum
+
+// W warps a CTA; 16, 12 or 8 warps an SM for 1, 2 or 3 n-tiles
+__host__ __device__ constexpr int warps_per_sm(int nt) { return nt == 1 ? 16 : nt == 2 ? 12 : 8; }
+__host__ __device__ constexpr int stages(int nt) { return 48 / warps_per_sm(nt); }  // tiles of a warp's ring
+constexpr int ring_bytes(int nt, int w) { return w * stages(nt) * kBlockBytes; }
+constexpr int smem_bytes(int nt, int w) { return ring_bytes(nt, w) + (w * stages(nt) + 1) * 8; }
 
 __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                     uint32_t b1) {
@@ -64,10 +70,12 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-__device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_t bar) {
-  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(kBlockBytes) : "memory");
+__device__ __forceinline__ void expect_bytes(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-               "l"(src), "r"(kBlockBytes), "r"(bar)
+               "l"(src), "r"(bytes), "r"(bar)
                : "memory");
 }
 __device__ __forceinline__ bool bounded_wait(uint32_t bar, uint32_t parity) {
@@ -95,26 +103,27 @@ __device__ __forceinline__ uint32_t without_nan4(uint32_t codes) {
 struct Plan {
   int tiles, rounds;
 };
+template <int W>
 __device__ __forceinline__ Plan plan_of(int len) {
   Plan p;
   p.tiles = (len + kBlockTokens - 1) / kBlockTokens;
-  p.rounds = max(1, (p.tiles + kWarps - 1) / kWarps);  // an empty sequence's rows are written too
+  p.rounds = max(1, (p.tiles + W - 1) / W);  // an empty sequence's rows are written too
   return p;
 }
 
-template <int NT, typename T>
-__global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) splitk_kernel(const Geometry g, const AttnArgs a) {
-  constexpr int S = stages(NT), kRows = 8 * NT;
+template <int NT, int W, typename T>
+__global__ void __launch_bounds__(32 * W, warps_per_sm(NT) / W) splitk_kernel(const Geometry g, const AttnArgs a) {
+  constexpr int S = stages(NT), kRows = 8 * NT, kThreads = 32 * W;
+  constexpr int kLens = 32 * W;  // sequences whose lengths are kept
   extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ long long s_scan[kThreads];
-  __shared__ long long s_begin;  // first sequence's rounds before it (all units), and its index
-  __shared__ int s_seq, s_last;
-  __shared__ float s_m[kWarps][kRows], s_l[kWarps][kRows];
+  __shared__ long long s_sum[W], s_begin;  // rounds per warp's sequences; first sequence's rounds before it
+  __shared__ int s_seq, s_last, s_len[kLens];
+  __shared__ float s_m[W][kRows], s_l[W][kRows];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, gq = lane >> 2, tq = lane & 3;
   const int cap = a.max_pages * g.page_size, groups = (a.n_tiles_n + NT - 1) / NT;
   const int per_seq = g.num_kv_heads * groups;  // units of a sequence
 
-  auto length = [&](int b, bool report) {
+  auto load_length = [&](int b, bool report) {
     int len = __ldg(a.seq_lens + b);
     if (len < 0 || len > cap || (len > 0 && len < a.T)) {
       if (report && a.status) atomicOr(a.status, RQ_STATUS_BAD_LEN);
@@ -122,74 +131,88 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) splitk_kernel(const
     }
     return len;
   };
+  auto length = [&](int b) { return a.B <= kLens ? s_len[b] : load_length(b, false); };
 
   // ---- the CTA's range of rounds ----
   const int chunk = (a.B + kThreads - 1) / kThreads;
   long long mine = 0;
-  for (int b = tid * chunk; b < min(a.B, (tid + 1) * chunk); ++b) mine += plan_of(length(b, blockIdx.x == 0)).rounds;
-  s_scan[tid] = mine;
+  for (int b = tid * chunk; b < min(a.B, (tid + 1) * chunk); ++b) {
+    const int len = load_length(b, blockIdx.x == 0);
+    if (b < kLens) s_len[b] = len;
+    mine += plan_of<W>(len).rounds;
+  }
   const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem) + warp * S * kBlockBytes;
-  const uint32_t bars = (uint32_t)__cvta_generic_to_shared(smem) + kWarps * S * kBlockBytes + warp * S * 8;
+  const uint32_t bars = (uint32_t)__cvta_generic_to_shared(smem) + W * S * kBlockBytes + warp * S * 8;
+  const uint32_t join_bar = (uint32_t)__cvta_generic_to_shared(smem) + W * S * (kBlockBytes + 8);
   if (lane == 0) {
     for (int i = 0; i < S; ++i) tc::mbar_init(bars + 8 * i, 1);
+    if (warp == 0) tc::mbar_init(join_bar, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  __syncthreads();
-  for (int o = 1; o < kThreads; o <<= 1) {  // inclusive scan
-    const long long v = tid >= o ? s_scan[tid - o] : 0;
-    __syncthreads();
-    s_scan[tid] += v;
-    __syncthreads();
+  long long upto = mine;  // inclusive scan over the threads
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long v = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += v;
   }
-  const long long total = s_scan[kThreads - 1] * per_seq;
+  if (lane == 31) s_sum[warp] = upto;
+  __syncthreads();
+  long long total = 0;
+#pragma unroll
+  for (int w = 0; w < W; ++w) {
+    if (w == warp) upto += total;
+    total += s_sum[w];
+  }
+  total *= per_seq;
   const long long parts = min((long long)gridDim.x, total);
   if ((long long)blockIdx.x >= parts) return;
   auto part_begin = [&](long long c) { return c * total / parts; };
   auto part_of = [&](long long x) { return ((x + 1) * parts - 1) / total; };  // the range that holds round x
   long long x = part_begin(blockIdx.x);
   const long long end = part_begin(blockIdx.x + 1ll);
-  {
-    const long long before = (s_scan[tid] - mine) * per_seq;
-    if (x >= before && x < s_scan[tid] * per_seq) {
-      long long at = before;
-      int b = tid * chunk;
-      for (;; ++b) {
-        const long long r = (long long)plan_of(length(b, false)).rounds * per_seq;
-        if (x < at + r) break;
-        at += r;
-      }
-      s_begin = at;
-      s_seq = b;
+  if (x >= (upto - mine) * per_seq && x < upto * per_seq) {
+    long long at = (upto - mine) * per_seq;
+    int b = tid * chunk;
+    for (; chunk > 1; ++b) {
+      const long long r = (long long)plan_of<W>(length(b)).rounds * per_seq;
+      if (x < at + r) break;
+      at += r;
     }
+    s_begin = at;
+    s_seq = b;
   }
   __syncthreads();
   long long at = s_begin;
   int b = s_seq;
 
   uint32_t issued = 0, done = 0;  // tiles of this warp so far: ring positions and parities
+  uint32_t joins = 0;
   bool failed = false;
   while (x < end) {
     // ---- the fragment: rounds r0 .. r1 - 1 of unit u of sequence b ----
-    const int len = length(b, false);
-    const Plan pl = plan_of(len);
+    const int len = length(b);
+    const Plan pl = plan_of<W>(len);
     const int u = (int)((x - at) / pl.rounds), r0 = (int)((x - at) % pl.rounds);
     const int r1 = (int)min((long long)pl.rounds, r0 + (end - x));
     const int h = u / groups, row0 = (u % groups) * kRows;
-    const int first = r0 * kWarps + warp;  // the warp's tiles: first, first + kWarps, ...
-    const int last = min(pl.tiles, r1 * kWarps);
-    const int count = first < last ? (last - first + kWarps - 1) / kWarps : 0;
+    const int first = r0 * W + warp;  // the warp's tiles: first, first + W, ...
+    const int last = min(pl.tiles, r1 * W);
+    const int count = first < last ? (last - first + W - 1) / W : 0;
     const int32_t* table = a.block_table + (size_t)b * a.max_pages;
 
-    // page of tile first + kWarps * i, for i in the lane's place of the current and next 32
-    auto page_at = [&](int i) {
-      if (i >= count) return 0;
-      int page = __ldg(table + (first + kWarps * i) * kBlockTokens / g.page_size);
-      if (page < 0 || page >= g.num_pages) {
-        if (a.status) atomicOr(a.status, RQ_STATUS_BAD_PAGE);
-        page = 0;
-      }
-      return page;
-    };
+    // the warp's queries, rows past the last one as that one (they are not written), and the pages of
+    // its first 64 tiles: all loads in flight together
+    uint4 raw[NT][4];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const int row = min(row0 + 8 * n + gq, a.rows - 1), j = row / g.group, head = h * g.group + row % g.group;
+      const uint4* src = reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(a.q) +
+                                                        (((size_t)b * a.T + j) * g.num_q_heads + head) * kHeadDim);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) raw[n][i] = __ldg(src + 8 * (i >> 1) + 2 * tq + (i & 1));
+    }
+    // page of tile first + W * i, for i in the lane's place of the current and next 32
+    auto page_at = [&](int i) { return i < count ? __ldg(table + (first + W * i) * kBlockTokens / g.page_size) : 0; };
     int pages_now = page_at(lane), pages_next = page_at(32 + lane);
     int batch = 0;
     auto issue = [&](int i) {  // tile i of the warp, by the whole warp
@@ -198,12 +221,18 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) splitk_kernel(const
         pages_now = pages_next;
         pages_next = page_at(32 * (batch + 1) + lane);
       }
-      const int page = __shfl_sync(0xffffffffu, pages_now, i & 31);
+      int page = __shfl_sync(0xffffffffu, pages_now, i & 31);
       if (lane == 0) {
-        const int in_page = (first + kWarps * i) * kBlockTokens % g.page_size / kBlockTokens;
+        if (page < 0 || page >= g.num_pages) {
+          if (a.status) atomicOr(a.status, RQ_STATUS_BAD_PAGE);
+          page = 0;
+        }
+        const int in_page = (first + W * i) * kBlockTokens % g.page_size / kBlockTokens;
         const uint32_t s = issued % S;
+        expect_bytes(bars + 8 * s, kBlockBytes);
         bulk_copy(ring + s * kBlockBytes,
-                  a.pages + ((size_t)page * g.num_kv_heads + h) * g.page_bytes + (size_t)in_page * kBlockBytes, bars + 8 * s);
+                  a.pages + ((size_t)page * g.num_kv_heads + h) * g.page_bytes + (size_t)in_page * kBlockBytes, kBlockBytes,
+                  bars + 8 * s);
       }
       ++issued;
     };
@@ -216,23 +245,12 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) splitk_kernel(const
     int lim[NT][2];   // last visible position of those columns' rows
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      const int row = row0 + 8 * n + gq;
-      uint4 raw[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) raw[i] = make_uint4(0u, 0u, 0u, 0u);
-      if (row < a.rows) {
-        const int j = row / g.group, head = h * g.group + row % g.group;
-        const uint4* src = reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(a.q) +
-                                                          (((size_t)b * a.T + j) * g.num_q_heads + head) * kHeadDim);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) raw[i] = __ldg(src + 8 * (i >> 1) + 2 * tq + (i & 1));
-      }
       float f = g.sm_scale * 1.44269504088896340736f;
-      if constexpr (sizeof(T) == 2 && !std::is_same<T, __half>::value) {
+      if constexpr (!std::is_same<T, __half>::value) {
         float top = 0.f;
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-          const float2 v = rope::unpack2<T>(word(raw[i >> 2], i & 3));
+          const float2 v = rope::unpack2<T>(word(raw[n][i >> 2], i & 3));
           top = fmaxf(top, fmaxf(fabsf(v.x), fabsf(v.y)));
         }
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
@@ -242,12 +260,12 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) splitk_kernel(const
         f *= pow2(e - 14);
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-          const float2 v = rope::unpack2<T>(word(raw[i >> 2], i & 3));
+          const float2 v = rope::unpack2<T>(word(raw[n][i >> 2], i & 3));
           qf[n][i >> 1][i & 1] = rope::pack2<__half>(v.x * down, v.y * down);
         }
       } else {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) qf[n][i >> 1][i & 1] = word(raw[i >> 2], i & 3);
+        for (int i = 0; i < 16; ++i) qf[n][i >> 1][i & 1] = word(raw[n][i >> 2], i & 3);
       }
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
@@ -274,7 +292,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) splitk_kernel(const
         break;
       }
       ++done;
-      const int t0 = (first + kWarps * i) * kBlockTokens;
+      const int t0 = (first + W * i) * kBlockTokens;
       const bool tail = t0 + kBlockTokens - 1 > len - a.T;  // rows see different parts of the tile
       uint32_t exps;
       asm volatile("ld.shared.u16 %0, [%1];" : "=r"(exps) : "r"(tile + kExps));
@@ -422,7 +440,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) splitk_kernel(const
         const int r = 8 * n + 2 * tq + c;
         float top = s_m[0][r];
 #pragma unroll
-        for (int w = 1; w < kWarps; ++w) top = fmaxf(top, s_m[w][r]);
+        for (int w = 1; w < W; ++w) top = fmaxf(top, s_m[w][r]);
         const float f = ex2(m[n][c] - top);
 #pragma unroll
         for (int d = 0; d < 8; ++d)  // dims 32 (d / 2) + 4 gq + 2 (d % 2), and the next
@@ -434,29 +452,35 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) splitk_kernel(const
     const long long u0 = at + (long long)u * pl.rounds;
     const bool whole = r0 == 0 && r1 == pl.rounds;
     const long long cf = part_of(u0), cl = part_of(u0 + pl.rounds - 1);
-    float* const ws = a.ws;
     auto slot_of = [&](long long c) {  // a unit's fragment in range c is c's first, or the last of the first range
-      return ws + (2 * c + (c == cf && part_begin(c) != u0 ? 1 : 0)) * (kRows * kRowStride);
+      return a.ws + (2 * c + (c == cf && part_begin(c) != u0 ? 1 : 0)) * (kRows * kRowStride);
     };
-    auto out_row = [&](int r) {
+    auto write_row = [&](int r, float4 v, float sum) {  // a lane's four dims of a row of the output
       const int row = row0 + r, j = row / g.group, head = h * g.group + row % g.group;
-      return reinterpret_cast<T*>(a.out) + (((size_t)b * a.T + j) * g.num_q_heads + head) * kHeadDim;
+      T* dst = reinterpret_cast<T*>(a.out) + (((size_t)b * a.T + j) * g.num_q_heads + head) * kHeadDim;
+      const float inv = 1.f / sum;
+      if (sum == 0.f) v = make_float4(0.f, 0.f, 0.f, 0.f);  // the row sees nothing
+      *(reinterpret_cast<uint2*>(dst) + lane) =
+          sum == 0.f ? make_uint2(0u, 0u)
+                     : make_uint2(rope::pack2<T>(v.x * inv, v.y * inv), rope::pack2<T>(v.z * inv, v.w * inv));
     };
-    for (int r = 0; r < rows; ++r) {
-      float top = s_m[0][r], sum = 0.f, acc = 0.f;
+    for (int r = warp; r < rows; r += W) {
+      float top = s_m[0][r], sum = 0.f;
 #pragma unroll
-      for (int w = 1; w < kWarps; ++w) top = fmaxf(top, s_m[w][r]);
+      for (int w = 1; w < W; ++w) top = fmaxf(top, s_m[w][r]);
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
+      for (int w = 0; w < W; ++w) {
         sum += s_l[w][r] * ex2(s_m[w][r] - top);
-        acc += join[(w * kRows + r) * kRowStride + tid];
+        const float4 v = *(reinterpret_cast<const float4*>(join + (w * kRows + r) * kRowStride) + lane);
+        acc.x += v.x, acc.y += v.y, acc.z += v.z, acc.w += v.w;
       }
       if (whole) {
-        out_row(r)[tid] = (T)(sum == 0.f ? 0.f : acc / sum);
+        write_row(r, acc, sum);
       } else {
         float* const dst = slot_of(blockIdx.x) + r * kRowStride;
-        dst[tid] = acc;
-        if (tid == 0) dst[kHeadDim] = top, dst[kHeadDim + 1] = sum;
+        *(reinterpret_cast<float4*>(dst) + lane) = acc;
+        if (lane == 0) *reinterpret_cast<float2*>(dst + kHeadDim) = make_float2(top, sum);
       }
     }
     if (!whole) {
@@ -467,49 +491,45 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) splitk_kernel(const
       __syncthreads();
       if (s_last) {
         __threadfence();
+        asm volatile("fence.proxy.async;" ::: "memory");  // the other CTAs' stores, before copies of them
         if (tid == 0) a.cnt[cf] = 0;  // as every launch finds it
-        // all (m, l) at once, then a warp per row with eight fragments' loads in flight: the join is as
-        // long as its chain of memory latencies (one thread per dim and two fragments at a time took
-        // 16 us for 76 fragments)
-        float2* const ml = reinterpret_cast<float2*>(smem);  // [row][frag]
-        for (int i = tid; i < frags * rows; i += kThreads)
-          ml[i] = __ldcg(reinterpret_cast<const float2*>(slot_of(cf + i % frags) + i / frags * kRowStride + kHeadDim));
-        __syncthreads();
-        for (int r = warp; r < rows; r += kWarps) {
-          float top = kNone, sum = 0.f;
-          for (int f = lane; f < frags; f += 32) top = fmaxf(top, ml[r * frags + f].x);
+        constexpr int kMine = (kRows + W - 1) / W;  // rows of a warp
+        float4 acc[kMine];
+        float top[kMine], sum[kMine];
 #pragma unroll
-          for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-          for (int f = lane; f < frags; f += 32) {
-            const float w = ex2(ml[r * frags + f].x - top);
-            sum = fmaf(ml[r * frags + f].y, w, sum);
-            ml[r * frags + f].x = w;
+        for (int i = 0; i < kMine; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f), top[i] = kNone, sum[i] = 0.f;
+        const int bytes = rows * kRowBytes, at_once = min(32, W * S * kBlockBytes / bytes);
+        for (int f0 = 0; f0 < frags; f0 += at_once) {
+          const int nf = min(at_once, frags - f0);
+          if (warp == 0) {
+            if (lane == 0) expect_bytes(join_bar, nf * bytes);
+            __syncwarp();
+            if (lane < nf)
+              bulk_copy((uint32_t)__cvta_generic_to_shared(smem) + lane * bytes, slot_of(cf + f0 + lane), bytes, join_bar);
           }
+          if (!bounded_wait(join_bar, joins & 1) && lane == 0 && a.status) atomicOr(a.status, RQ_STATUS_TIMEOUT);
+          ++joins;
 #pragma unroll
-          for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-          __syncwarp();
-          float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-          const float4* src = reinterpret_cast<const float4*>(slot_of(cf) + r * kRowStride) + lane;
-          const float4* next = reinterpret_cast<const float4*>(slot_of(cf + 1) + r * kRowStride) + lane;  // and evenly on
-          auto add = [&](const float4& v, float w) {
-            acc.x = fmaf(v.x, w, acc.x), acc.y = fmaf(v.y, w, acc.y), acc.z = fmaf(v.z, w, acc.z), acc.w = fmaf(v.w, w, acc.w);
-          };
-          add(__ldcg(src), ml[r * frags].x);
-          int f = 1;
-          for (; f + 8 <= frags; f += 8) {
-            float4 v[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = __ldcg(next + (size_t)i * (2 * kRows * kRowStride / 4));
-#pragma unroll
-            for (int i = 0; i < 8; ++i) add(v[i], ml[r * frags + f + i].x);
-            next += (size_t)8 * (2 * kRows * kRowStride / 4);
+          for (int i = 0; i < kMine; ++i) {
+            const int r = warp + W * i;
+            if (r >= rows) break;
+            const float* src = join + r * kRowStride;
+            for (int f = 0; f < nf; ++f, src += rows * kRowStride) {  // in the order of the ranges
+              const float2 ml = *reinterpret_cast<const float2*>(src + kHeadDim);
+              const float4 v = *(reinterpret_cast<const float4*>(src) + lane);
+              const float t = fmaxf(top[i], ml.x), wa = ex2(top[i] - t), wv = ex2(ml.x - t);
+              top[i] = t;
+              sum[i] = sum[i] * wa + ml.y * wv;
+              acc[i].x = acc[i].x * wa + v.x * wv, acc[i].y = acc[i].y * wa + v.y * wv;
+              acc[i].z = acc[i].z * wa + v.z * wv, acc[i].w = acc[i].w * wa + v.w * wv;
+            }
           }
-          for (; f < frags; ++f, next += 2 * kRows * kRowStride / 4) add(__ldcg(next), ml[r * frags + f].x);
-          const float inv = sum == 0.f ? 0.f : 1.f / sum;
-          if (sum == 0.f) acc = make_float4(0.f, 0.f, 0.f, 0.f);
-          *(reinterpret_cast<uint2*>(out_row(r)) + lane) =
-              make_uint2(rope::pack2<T>(acc.x * inv, acc.y * inv), rope::pack2<T>(acc.z * inv, acc.w * inv));
+          tc::fence_async_smem();
+          __syncthreads();  // read, before the next chunk's copies
         }
+#pragma unroll
+        for (int i = 0; i < kMine; ++i)
+          if (warp + W * i < rows) write_row(warp + W * i, acc[i], sum[i]);
       }
     }
     tc::fence_async_smem();  // the join's accesses to the ring, before the next fragment's copies
@@ -522,20 +542,22 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) splitk_kernel(const
   }
 }
 
-template <int NT>
-cudaError_t launch(const Geometry& g, const AttnArgs& a, cudaStream_t stream) {
+template <int NT, int W>
+cudaError_t launch(const Geometry& g, const AttnArgs& a, int num_sms, cudaStream_t stream) {
+  const int grid = num_sms * (warps_per_sm(NT) / W);
   if (g.bf16)
-    splitk_kernel<NT, __nv_bfloat16><<<a.grid, kThreads, smem_bytes(NT), stream>>>(g, a);
+    splitk_kernel<NT, W, __nv_bfloat16><<<grid, 32 * W, smem_bytes(NT, W), stream>>>(g, a);
   else
-    splitk_kernel<NT, __half><<<a.grid, kThreads, smem_bytes(NT), stream>>>(g, a);
+    splitk_kernel<NT, W, __half><<<grid, 32 * W, smem_bytes(NT, W), stream>>>(g, a);
   return cudaGetLastError();
 }
 
-template <int NT>
+template <int NT, int W>
 cudaError_t prepare() {
-  cudaError_t e = cudaFuncSetAttribute(splitk_kernel<NT, __half>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes(NT));
+  constexpr int bytes = smem_bytes(NT, W);
+  cudaError_t e = cudaFuncSetAttribute(splitk_kernel<NT, W, __half>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(splitk_kernel<NT, __nv_bfloat16>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes(NT));
+    e = cudaFuncSetAttribute(splitk_kernel<NT, W, __nv_bfloat16>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   return e;
 }
 
@@ -548,19 +570,17 @@ int unit_tiles(int n_tiles) {
 }  // namespace
 
 size_t block_attention_workspace(int num_sms, size_t* counters) {
-  size_t most = 0;
-  for (int nt = 1; nt <= 3; ++nt) {
-    const size_t f = (size_t)2 * num_sms * ctas_per_sm(nt) * 8 * nt * kRowStride;
-    most = f > most ? f : most;
-  }
-  *counters = (size_t)num_sms * ctas_per_sm(1);
+  const size_t row = 8 * kRowStride;
+  size_t most = 2 * (size_t)num_sms * 4 * row;  // two slots a CTA: four of 8 rows an SM, or one of 16 or 24
+  *counters = (size_t)num_sms * 4;
   return most;
 }
 
 cudaError_t block_attention_prepare() {
-  cudaError_t e = prepare<1>();
-  if (e == cudaSuccess) e = prepare<2>();
-  if (e == cudaSuccess) e = prepare<3>();
+  cudaError_t e = prepare<1, 4>();
+  if (e == cudaSuccess) e = prepare<1, 16>();
+  if (e == cudaSuccess) e = prepare<2, 12>();
+  if (e == cudaSuccess) e = prepare<3, 8>();
   return e;
 }
 
@@ -568,9 +588,13 @@ cudaError_t launch_block_attention(const Geometry& g, AttnArgs a, int num_sms, c
                                    cudaEvent_t ev_end) {
   a.n_tiles_n = (a.rows + 7) / 8;
   a.nt = unit_tiles(a.n_tiles_n);
-  a.grid = num_sms * ctas_per_sm(a.nt);
+  const long long units = (long long)a.B * g.num_kv_heads * ((a.n_tiles_n + a.nt - 1) / a.nt);
   if (ev_start) cudaEventRecord(ev_start, stream);
-  const cudaError_t e = a.nt == 1 ? launch<1>(g, a, stream) : a.nt == 2 ? launch<2>(g, a, stream) : launch<3>(g, a, stream);
+  cudaError_t e;
+  if (a.nt == 1)
+    e = units < num_sms ? launch<1, 16>(g, a, num_sms, stream) : launch<1, 4>(g, a, num_sms, stream);
+  else
+    e = a.nt == 2 ? launch<2, 12>(g, a, num_sms, stream) : launch<3, 8>(g, a, num_sms, stream);
   if (e == cudaSuccess && ev_end) cudaEventRecord(ev_end, stream);
   return e;
 }
