@@ -10,10 +10,9 @@
 //   softmax (warps 0-7, a thread per row): reads its row of S from tensor memory 64 columns at a
 //     time, applies scales and mask, writes fp16 weights over S;
 //   codes (warps 8-11): widen a tile's key and value codes (exact) into fp16 operands;
-//   MMA (one thread of warp 12 + b for block b): O_b += W_b V(t) as each half of the weights is there,
-//     and behind it S_b(t + 1) = Q_b K(t + 1)^T: one block on the tensor cores while the other is in
-//     its softmax.  A thread each, because issuing costs about 50 cycles an MMA, 70 a commit and 170 a
-//     wait for a barrier that is ready: 4000 a tile in one thread, against 2300 of MMAs;
+//   MMA (warp 12 + b for block b): O_b += W_b V(t) and behind it S_b(t + 1) = Q_b K(t + 1)^T, one
+//     block on the tensor cores while the other is in its softmax.  A warp each, and few barriers: a
+//     commit costs about 50 cycles and a wait for a barrier that is ready 120;
 //   copies (warp 14): a block is one 4112-byte bulk copy into a ring, page ids looked up 8 half
 //     tiles ahead.
 // (Warp 15 only fills the warpgroup: 16 warps have 128 registers a thread, 17 would have 96.)
@@ -47,11 +46,11 @@ using namespace block;
 using namespace tc;
 
 constexpr int kSoftWarps = 8, kCodeWarps = 4, kThreads = 512;
-constexpr int kMmaWarp = kSoftWarps + kCodeWarps, kCopyWarp = kMmaWarp + 2;  // MMA: block b by warp kMmaWarp + b
+constexpr int kMmaWarp = kSoftWarps + kCodeWarps, kCopyWarp = kMmaWarp + 1;
 constexpr int kHalf = 128, kRows = 2 * kHalf;  // rows of a block (M of the MMAs), of a CTA
 constexpr int kTok = 128, kPart = 64;          // tokens of a tile, of the half that softmax and V take at a time
-constexpr int kKeyStages = 2, kValueStages = 3, kRawStages = 3;  // tiles, halves, halves
-constexpr uint32_t kKeyBytes = 32768, kValueBytes = 16384, kRawBytes = 4 * kBlockBytes;
+constexpr int kKeyStages = 2, kRawStages = 4;  // K operands (tiles; V has one), raw codes (half tiles)
+constexpr uint32_t kOperand = 32768, kRawBytes = 4 * kBlockBytes;
 constexpr uint32_t kQBytes = 2 * 32768;
 constexpr int kScaleSlots = 4;      // tiles whose scales are kept
 constexpr float kMargin = 8.f;      // log2 slack of the running maximum
@@ -70,9 +69,10 @@ struct Frag {           // tiles r0 .. r0 + n - 1 of one unit
   int done;             // no more fragments
 };
 struct Misc {
-  uint64_t raw_full[kRawStages], raw_empty[kRawStages], k_full[kKeyStages], k_empty[kKeyStages];
-  uint64_t v_full[kValueStages], v_empty[kValueStages], s_full[2];
-  uint64_t p_full[2][2], o_done[2][2], drain[2];  // [block][half]: one phase a tile each, a tile may be a whole half ahead
+  uint64_t raw_full[kRawStages], raw_empty[kRawStages];
+  // K(t), V(t) are there; W V(t) and S(t + 1) of both blocks done; [block] S(t); [block] W(t); [block] the
+  // fragment's last W V; drained
+  uint64_t k_full[kKeyStages], v_full, read, s_full[2], p_full[2], o_done[2], drain;
   Frag f;
   uint32_t tmem;
   int abort, last;
@@ -80,9 +80,10 @@ struct Misc {
   int nan_from[kHeadDim];              // first position with a NaN value in a dim
 };
 // from a 1024-byte boundary on: Q, keys, values, raw codes, Misc
-constexpr uint32_t kOffK = kQBytes, kOffV = kOffK + kKeyStages * kKeyBytes, kOffRaw = kOffV + kValueStages * kValueBytes;
+constexpr uint32_t kOffK = kQBytes, kOffV = kOffK + kKeyStages * kOperand, kOffRaw = kOffV + kOperand;
 constexpr uint32_t kOffMisc = kOffRaw + kRawStages * kRawBytes;
 constexpr int kSmem = (int)(kOffMisc + sizeof(Misc)) + 1024;
+static_assert(kRawStages == 4, "two tiles' halves");
 static_assert(kOffMisc % 16 == 0 && offsetof(Misc, scales) % 16 == 0, "float4 reads");
 static_assert(kSmem + 64 <= 232448, "one CTA's shared memory");
 
@@ -115,6 +116,49 @@ __device__ __forceinline__ void add2(uint64_t& a, float x, float y) {
 }
 __device__ __forceinline__ uint32_t word(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
 __device__ __forceinline__ uint32_t smem_addr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+// A warp's wait, bounded (about a second) like tc::role_wait, but asleep between its looks at the
+// barrier.  All lanes look: one lane's loop beside 31 waiting ones took about 1000 cycles longer.
+__device__ __forceinline__ bool warp_wait(const uint64_t& bar, uint32_t parity, volatile int* abort_flag) {
+  bool ok = false;
+  for (int i = 0; i < (1 << 16); ++i) {
+    uint32_t done;
+    asm volatile("{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}"
+                 : "=r"(done)
+                 : "r"(smem_addr(&bar)), "r"(parity & 1), "r"(20000u)  // ns
+                 : "memory");
+    ok = done;
+    if (done || *abort_flag) break;
+  }
+  if (!ok) *abort_flag = 1;
+  return __all_sync(0xffffffffu, ok);
+}
+// A warp's arrival, by one lane (a predicate, no branch) behind all lanes' accesses.
+__device__ __forceinline__ void warp_arrive(uint64_t& bar) {
+  __syncwarp();
+  asm volatile("{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n @e mbarrier.arrive.shared::cta.b64 _, [%0];\n}" ::"r"(
+                   smem_addr(&bar))
+               : "memory");
+}
+// The MMAs and commit of tc::, by one elected lane of a whole warp: with the operands uniform over the
+// warp an MMA is issued in 16 to 22 cycles, against 50 in a branch that one lane takes.
+__device__ __forceinline__ void elect_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p, e;\n elect.sync _|e, 0xffffffff;\n setp.ne.b32 p, %4, 0;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+      "l"(a), "l"(b), "r"(id), "r"(accumulate));
+}
+__device__ __forceinline__ void elect_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p, e;\n elect.sync _|e, 0xffffffff;\n setp.ne.b32 p, %4, 0;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
+      "r"(a), "l"(b), "r"(id), "r"(accumulate));
+}
+__device__ __forceinline__ void elect_commit(uint32_t mbar) {
+  asm volatile(
+      "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
+      " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}" ::"r"(mbar)
+      : "memory");
+}
 // Place of column c of a half tile: the token's offset.
 __host__ __device__ constexpr int token_of(int c) {
   const int i = c & 3, t = c >> 3 & 3;
@@ -200,21 +244,14 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const Geometry g, c
       mbar_init(smem_addr(&ms.raw_full[i]), 1);
       mbar_init(smem_addr(&ms.raw_empty[i]), kCodeWarps);
     }
-    for (int i = 0; i < kKeyStages; ++i) {
-      mbar_init(smem_addr(&ms.k_full[i]), 32 * kCodeWarps);
-      mbar_init(smem_addr(&ms.k_empty[i]), 2);
-    }
-    for (int i = 0; i < kValueStages; ++i) {
-      mbar_init(smem_addr(&ms.v_full[i]), 32 * kCodeWarps);
-      mbar_init(smem_addr(&ms.v_empty[i]), 2);
-    }
+    for (int i = 0; i < kKeyStages; ++i) mbar_init(smem_addr(&ms.k_full[i]), kCodeWarps);
+    mbar_init(smem_addr(&ms.v_full), kCodeWarps);
+    mbar_init(smem_addr(&ms.read), 1);
+    mbar_init(smem_addr(&ms.drain), 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_addr(&ms.s_full[i]), 1);
-      mbar_init(smem_addr(&ms.drain[i]), 1);
-      for (int part = 0; part < 2; ++part) {
-        mbar_init(smem_addr(&ms.p_full[i][part]), kHalf);
-        mbar_init(smem_addr(&ms.o_done[i][part]), 1);
-      }
+      mbar_init(smem_addr(&ms.p_full[i]), kSoftWarps / 2);
+      mbar_init(smem_addr(&ms.o_done[i]), 1);
     }
     ms.abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -222,7 +259,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const Geometry g, c
   __syncwarp();
   if (warp == 0) tmem_alloc(smem_addr(&ms.tmem), 512);
 
-  uint32_t done_tiles = 0;  // tiles of the fragments before: ring positions and parities
+  uint32_t done_tiles = 0, done_frags = 0;  // tiles and fragments before: ring positions and parities
   uint32_t fills = 0;       // copy warp: half tiles asked for
   for (;;) {
     if (tid == 0) {  // the next fragment
@@ -309,85 +346,95 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const Geometry g, c
       // ================= softmax: one thread per row =================
       const int qpos = valid ? len - a.T + row / g.group : -1;
       const uint32_t s_tile = tmem + lane_off + kColS + 128 * blk, o_cols = tmem + lane_off + 128 * blk;
+      // weights are 2^(score + EV - from): `from` is the running maximum, or 0 (none yet)
+      float from = 0.f;
       for (int t = 0; t < n && ok; ++t) {
         const uint32_t k = t_base + t;
+        const int t0 = (r0 + t) * kTok;
         // S_b(t) complete: so is every MMA issued before it, W_b(t - 1) V included
-        ok = __all_sync(0xffffffffu, role_wait(smem_addr(&ms.s_full[blk]), k & 1, abort_flag));
+        ok = warp_wait(ms.s_full[blk], k, abort_flag);
         if (!ok) break;
         fence_after_sync();
-#pragma unroll 1
-        for (int part = 0; part < 2; ++part) {
-          const int t0 = (r0 + t) * kTok + kPart * part;
-          const uint32_t s_cols = s_tile + kPart * part;
-          float s[kPart];
+        const float4* sc = reinterpret_cast<const float4*>(ms.scales[k % kScaleSlots]);  // [half][2^EK, EV, 2^-EV]
+        auto load = [&](float (&s)[kPart], int part) {
 #pragma unroll
           for (int c = 0; c < kPart / 16; ++c) {
             float v[16];
-            tmem_ld16(s_cols + 16 * c, v);
+            tmem_ld16(s_tile + kPart * part + 16 * c, v);
 #pragma unroll
             for (int i = 0; i < 16; ++i) s[16 * c + i] = v[i];
           }
-          const float4* sc = reinterpret_cast<const float4*>(ms.scales[k % kScaleSlots][part]);
-          const float4 ks4 = sc[0], ev4 = sc[1];
-          const float ks[4] = {ks4.x, ks4.y, ks4.z, ks4.w}, ev[4] = {ev4.x, ev4.y, ev4.z, ev4.w};
           tmem_wait_ld();
-          const bool large = __any_sync(0xffffffffu, fabsf(m_run) > kLarge && m_run != kNone);
-          const float from = m_run == kNone || large ? 0.f : m_run;
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {  // block q of the half: columns 32 (q / 2) + 4 (q % 2) + 8 t + i
-            const uint64_t f = pair(q_scale * ks[q], q_scale * ks[q]), d = pair(ev[q] - from, ev[q] - from);
-#pragma unroll
-            for (int t4 = 0; t4 < 4; ++t4) {
-              const int c = 32 * (q >> 1) + 4 * (q & 1) + 8 * t4;
-              fma2(s[c], s[c + 1], f, d);
-              fma2(s[c + 2], s[c + 3], f, d);
-            }
-          }
-          if (t0 + kPart - 1 > qpos) {  // mask what the row may not see
+          if (t0 + kPart * part + kPart - 1 > qpos) {  // mask what the row may not see
 #pragma unroll
             for (int c = 0; c < kPart; ++c)
-              if (t0 + token_of(c) > qpos) s[c] = -CUDART_INF_F;
+              if (t0 + kPart * part + token_of(c) > qpos) s[c] = -CUDART_INF_F;
           }
-          float tm[4] = {s[0], s[1], s[2], s[3]};
+        };
+        // the largest score + EV: the largest product of each block, then its scales
+        float top = -CUDART_INF_F;
+        auto highest = [&](const float (&s)[kPart], int part) {
+          const float4 ks4 = sc[3 * part], ev4 = sc[3 * part + 1];
+          const float ks[4] = {ks4.x, ks4.y, ks4.z, ks4.w}, ev[4] = {ev4.x, ev4.y, ev4.z, ev4.w};
 #pragma unroll
-          for (int c = 4; c < kPart - 4; c += 8)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) tm[i] = max3(tm[i], s[c + i], s[c + 4 + i]);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) tm[i] = fmaxf(tm[i], s[kPart - 4 + i]);
-          // relative to `from`: the running maximum, or 0 (none yet, or the large case)
-          const float top = fmaxf(max3(tm[0], tm[1], tm[2]), tm[3]);
-          float alpha = 1.f, shift = large ? -m_run : 0.f;
-          if (top > (m_run == kNone ? -CUDART_INF_F : m_run - from + kMargin)) {
-            const float m_new = top + from;
-            alpha = ex2(m_run - m_new);
-            shift = from - m_new;
-            m_run = m_new;
+          for (int q = 0; q < 4; ++q) {  // block q of the half: columns 32 (q / 2) + 4 (q % 2) + 8 t + i
+            const int c = 32 * (q >> 1) + 4 * (q & 1);
+            float m0 = max3(s[c], s[c + 1], s[c + 2]), m1 = max3(s[c + 3], s[c + 8], s[c + 9]);
+            m0 = max3(m0, s[c + 10], s[c + 11]), m1 = max3(m1, s[c + 16], s[c + 17]);
+            m0 = max3(m0, s[c + 18], s[c + 19]), m1 = max3(m1, s[c + 24], s[c + 25]);
+            m0 = max3(m0, s[c + 26], s[c + 27]);
+            top = fmaxf(top, fmaf(fmaxf(m0, m1), q_scale * ks[q], ev[q]));
           }
-          if (__any_sync(0xffffffffu, shift != 0.f)) {
-            const uint64_t one = pair(1.f, 1.f), d = pair(shift, shift);
-#pragma unroll
-            for (int c = 0; c < kPart; c += 2) fma2(s[c], s[c + 1], one, d);
-            if (__any_sync(0xffffffffu, alpha != 1.f) && (t > 0 || part > 0)) {  // O *= alpha (the warp's rows)
-              l_run *= alpha;
-              if (part == 1) {  // W_b(t) V of the first half still adds to O
-                ok = __all_sync(0xffffffffu, role_wait(smem_addr(&ms.o_done[blk][0]), k & 1, abort_flag));
-                if (!ok) break;
-                fence_after_sync();
-              }
+        };
+        float s[kPart];
+        load(s, 1);
+        highest(s, 1);
+        load(s, 0);
+        highest(s, 0);
+        if (__any_sync(0xffffffffu, top > (m_run == kNone ? -CUDART_INF_F : m_run + kMargin))) {
+          float alpha = 1.f;
+          if (top > (m_run == kNone ? -CUDART_INF_F : m_run + kMargin)) {
+            alpha = ex2(m_run - top);
+            from = m_run = top;
+            l_run *= alpha;
+          }
+          if (t > 0) {  // O *= alpha (the warp's rows)
 #pragma unroll 1
-              for (int c = 0; c < kHeadDim / 16; ++c) {
-                float v[16];
-                tmem_ld16(o_cols + 16 * c, v);
-                tmem_wait_ld();
+            for (int c = 0; c < kHeadDim / 16; ++c) {
+              float v[16];
+              tmem_ld16(o_cols + 16 * c, v);
+              tmem_wait_ld();
 #pragma unroll
-                for (int i = 0; i < 16; ++i) v[i] *= alpha;
-                tmem_st16(o_cols + 16 * c, v);
+              for (int i = 0; i < 16; ++i) v[i] *= alpha;
+              tmem_st16(o_cols + 16 * c, v);
+            }
+          }
+        }
+        const bool large = __any_sync(0xffffffffu, fabsf(from) > kLarge);  // the difference needs the rounded product
+#pragma unroll
+        for (int part = 0; part < 2; ++part) {
+          if (part == 1) load(s, 1);
+          const float4 ks4 = sc[3 * part], ev4 = sc[3 * part + 1], dn4 = sc[3 * part + 2];
+          const float ks[4] = {ks4.x, ks4.y, ks4.z, ks4.w}, ev[4] = {ev4.x, ev4.y, ev4.z, ev4.w};
+          const float dn[4] = {dn4.x, dn4.y, dn4.z, dn4.w};
+          if (large) {
+#pragma unroll
+            for (int c = 0; c < kPart; ++c) {
+              const int q = 2 * (c >> 5) + (c >> 2 & 1);
+              s[c] = fmaf(s[c], q_scale * ks[q], ev[q]) - from;
+            }
+          } else {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const uint64_t f = pair(q_scale * ks[q], q_scale * ks[q]), d = pair(ev[q] - from, ev[q] - from);
+#pragma unroll
+              for (int t4 = 0; t4 < 4; ++t4) {
+                const int c = 32 * (q >> 1) + 4 * (q & 1) + 8 * t4;
+                fma2(s[c], s[c + 1], f, d);
+                fma2(s[c + 2], s[c + 3], f, d);
               }
             }
           }
-          const float4 dn4 = sc[2];
-          const float dn[4] = {dn4.x, dn4.y, dn4.z, dn4.w};
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
             uint32_t pw[16];
@@ -398,7 +445,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const Geometry g, c
               add2(sum[c >> 2 & 1], w0, w1);
               pw[c >> 1] = rope::pack2<__half>(w0, w1);
             }
-            tmem_st16u(s_cols + 16 * half, pw);
+            tmem_st16u(s_tile + kPart * part + 16 * half, pw);
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
               float lo, hi;
@@ -406,12 +453,12 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const Geometry g, c
               l_run = fmaf(lo + hi, dn[2 * half + q], l_run);
             }
           }
-          tmem_wait_st();
-          fence_before_sync();
-          mbar_arrive(smem_addr(&ms.p_full[blk][part]));
         }
+        tmem_wait_st();
+        fence_before_sync();
+        warp_arrive(ms.p_full[blk]);
       }
-      if (ok) ok = __all_sync(0xffffffffu, role_wait(smem_addr(&ms.o_done[blk][1]), (t_base + n - 1) & 1, abort_flag));
+      if (ok) ok = warp_wait(ms.o_done[blk], done_frags, abort_flag);
       fence_after_sync();
       if (!ok && lane == 0 && a.status) atomicOr(a.status, RQ_STATUS_TIMEOUT);
     } else if (warp < kSoftWarps + kCodeWarps) {
@@ -419,135 +466,144 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const Geometry g, c
       // warp dw takes the keys of block dw of a half tile, and half of the dims of the values of blocks
       // p16 and p16 + 1
       const int dw = warp & 3, p16 = dw & 2, g8 = lane >> 2, t4 = lane & 3;
-      for (int t2 = 0; t2 < 2 * n && ok; ++t2) {
-        const uint32_t k2 = 2 * t_base + t2, k = k2 >> 1, part = t2 & 1, rs = k2 % kRawStages, vs = k2 % kValueStages;
-        const int t0 = r0 * kTok + kPart * t2;
-        const uint32_t raw = raw_ring + rs * kRawBytes;
-        ok = role_wait(smem_addr(&ms.raw_full[rs]), (k2 / kRawStages) & 1, abort_flag);
-        if (part == 0 && k >= kKeyStages)
-          ok = ok && role_wait(smem_addr(&ms.k_empty[k % kKeyStages]), (k / kKeyStages - 1) & 1, abort_flag);
-        if (!(ok = __all_sync(0xffffffffu, ok))) break;
-        {  // unit u: token 8 (u / 2) + g8, dims 64 (u % 2) + 16 t4 ..; the token's row is its column of S
-          const uint32_t dst = k_ring + k % kKeyStages * kKeyBytes;
-          const bool there = t0 + 16 * dw < len;  // else nothing was copied
+      const int kr = 32 * (dw >> 1) + 8 * (g8 >> 1) + 4 * (dw & 1) + (g8 & 1), vd = 64 * (dw & 1) + 4 * g8;
+      const uint32_t k_off[2] = {sw128(kr, 2 * t4), sw128(kr + 2, 2 * t4)};  // + 16384 (u % 2); the next chunk: ^ 16
+      uint32_t v_off[4];
+#pragma unroll
+      for (int k4 = 0; k4 < 4; ++k4) v_off[k4] = sw128(vd + k4, t4 + 4 * (dw >> 1));  // + 4096 i
+      for (int t = 0; t < n && ok; ++t) {
+        const uint32_t k = t_base + t;
+        const int t0 = (r0 + t) * kTok;
+        // K(t - 2) is read: S(t - 1) was waited for before the last tile's values
+#pragma unroll
+        for (int part = 0; part < 2; ++part) {
+          const uint32_t rs = (2 * k + part) % kRawStages, raw = raw_ring + rs * kRawBytes + dw * kBlockBytes;
+          if (!(ok = warp_wait(ms.raw_full[rs], (2 * k + part) / kRawStages, abort_flag))) break;
+          // unit u: token 8 (u / 2) + g8, dims 64 (u % 2) + 16 t4 ..; the token's row is its column of S
+          const uint32_t dst = k_ring + k % kKeyStages * kOperand + part * (kPart * 128);
+          const bool there = t0 + kPart * part + 16 * dw < len;  // else nothing was copied
 #pragma unroll
           for (int u = 0; u < 4; ++u) {
             uint4 c = make_uint4(0u, 0u, 0u, 0u);
-            if (there) c = lds128(raw + dw * kBlockBytes + 16 * (32 * u + lane));
-            const int r = kPart * part + 32 * (dw >> 1) + 8 * (g8 >> 1) + 4 * (dw & 1) + (g8 & 1) + 2 * (u >> 1);
-            const uint32_t atom = dst + (u & 1) * 16384;
-            sts128(atom + sw128(r, 2 * t4), widen2(c.x), widen2_hi(c.x), widen2(c.y), widen2_hi(c.y));
-            sts128(atom + sw128(r, 2 * t4 + 1), widen2(c.z), widen2_hi(c.z), widen2(c.w), widen2_hi(c.w));
+            if (there) c = lds128(raw + 16 * (32 * u + lane));
+            sts128(dst + k_off[u >> 1] + (u & 1) * 16384, widen2(c.x), widen2_hi(c.x), widen2(c.y), widen2_hi(c.y));
+            sts128(dst + (k_off[u >> 1] ^ 16) + (u & 1) * 16384, widen2(c.z), widen2_hi(c.z), widen2(c.w), widen2_hi(c.w));
           }
-          // k_empty: S(t - 2) of both blocks is done, which was issued behind W(t - 3) V: both softmaxes
-          // are past the scales of tile t - 3, and so of t - 4, whose slot this is
+          // (S(t - 1) came behind W V(t - 2): both softmaxes are past tile t - 2, t - 4's slot is free)
           if (lane == 0) {
             uint32_t exps = 0x7F7Fu;
-            if (there) asm volatile("ld.shared.u16 %0, [%1];" : "=r"(exps) : "r"(raw + dw * kBlockBytes + kExps));
+            if (there) asm volatile("ld.shared.u16 %0, [%1];" : "=r"(exps) : "r"(raw + kExps));
             const int ev = exp_of_byte(exps >> 8);
             float(*sc)[4] = ms.scales[k % kScaleSlots][part];
             sc[0][dw] = pow2(exp_of_byte(exps & 0xFF));
             sc[1][dw] = (float)ev;
             sc[2][dw] = pow2(-ev);
           }
-          if (part == 1) {
-            fence_async_smem();
-            mbar_arrive(smem_addr(&ms.k_full[k % kKeyStages]));
-          }
         }
-        uint4 vc[4];  // vc[2 i + b]: block p16 + b, dims 32 (2 (dw % 2) + i) + 4 g8 ..
+        if (!ok) break;
+        fence_async_smem();
+        warp_arrive(ms.k_full[k % kKeyStages]);
+        uint4 vc[2][4];  // [part][2 i + b]: block p16 + b, dims 32 (2 (dw % 2) + i) + 4 g8 ..
         uint32_t bad = 0u;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          vc[i] = make_uint4(0u, 0u, 0u, 0u);
-          if (t0 + 16 * (p16 + (i & 1)) < len)
-            vc[i] = lds128(raw + (p16 + (i & 1)) * kBlockBytes + kValues + 16 * (32 * (2 * (dw & 1) + (i >> 1)) + lane));
-#pragma unroll
-          for (int k4 = 0; k4 < 4; ++k4) bad |= __vcmpeq4(word(vc[i], k4) & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_addr(&ms.raw_empty[rs]));  // the warp has read its codes
-        if (__any_sync(0xffffffffu, bad != 0u) || t0 + kPart > len) {
-          // bytes past the sequence may be anything; a NaN value goes to the rows that see it at the end
+        for (int part = 0; part < 2; ++part) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
+            uint4& c = vc[part][i];
+            c = make_uint4(0u, 0u, 0u, 0u);
+            if (t0 + kPart * part + 16 * (p16 + (i & 1)) < len)
+              c = lds128(raw_ring + (2 * k + part) % kRawStages * kRawBytes + (p16 + (i & 1)) * kBlockBytes + kValues +
+                         16 * (32 * (2 * (dw & 1) + (i >> 1)) + lane));
+#pragma unroll
+            for (int k4 = 0; k4 < 4; ++k4) bad |= (word(c, k4) & 0x7F7F7F7Fu) + 0x01010101u;  // bit 7 of a byte: NaN
+          }
+        }
+        __syncwarp();
+        if (lane < 2) mbar_arrive(smem_addr(&ms.raw_empty[(2 * k + lane) % kRawStages]));  // the warp has read its codes
+        if (__any_sync(0xffffffffu, (bad & 0x80808080u) != 0u) || t0 + kTok > len) {
+          // bytes past the sequence may be anything; a NaN value goes to the rows that see it at the end
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const int part = j >> 2, i = j & 3;
             uint32_t w[4];
 #pragma unroll
             for (int k4 = 0; k4 < 4; ++k4) {
-              w[k4] = word(vc[i], k4);
+              w[k4] = word(vc[part][i], k4);
 #pragma unroll
               for (int c = 0; c < 4; ++c) {
-                const int p = t0 + 16 * (p16 + (i & 1)) + 2 * t4 + (c & 1) + 8 * (c >> 1);
+                const int p = t0 + kPart * part + 16 * (p16 + (i & 1)) + 2 * t4 + (c & 1) + 8 * (c >> 1);
                 const bool isnan = (w[k4] >> (8 * c) & 0x7Fu) == 0x7Fu;
                 if (isnan && p < len) atomicMin(&ms.nan_from[32 * (2 * (dw & 1) + (i >> 1)) + 4 * g8 + k4], p);
                 if (isnan || p >= len) w[k4] &= ~(0xFFu << (8 * c));
               }
             }
-            vc[i] = make_uint4(w[0], w[1], w[2], w[3]);
+            vc[part][i] = make_uint4(w[0], w[1], w[2], w[3]);
           }
         }
-        if (k2 >= kValueStages &&
-            !(ok = __all_sync(0xffffffffu, role_wait(smem_addr(&ms.v_empty[vs]), (k2 / kValueStages - 1) & 1, abort_flag))))
-          break;
-        const uint32_t dst = v_ring + vs * kValueBytes;
+        // W V(t - 1) of both blocks is done, whose values stand here, and S(t)
+        if (k > 0 && !(ok = warp_wait(ms.read, k - 1, abort_flag))) break;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+        for (int part = 0; part < 2; ++part) {
+          const uint32_t dst = v_ring + part * (kOperand / 2);
 #pragma unroll
-          for (int k4 = 0; k4 < 4; ++k4) {
-            const int d = 32 * (2 * (dw & 1) + i) + 4 * g8 + k4;
-            const uint32_t wa = word(vc[2 * i], k4), wb = word(vc[2 * i + 1], k4);
-            sts128(dst + sw128(d, t4 + 4 * (dw >> 1)), widen2(wa), widen2_hi(wa), widen2(wb), widen2_hi(wb));
+          for (int i = 0; i < 2; ++i) {
+#pragma unroll
+            for (int k4 = 0; k4 < 4; ++k4) {
+              const uint32_t wa = word(vc[part][2 * i], k4), wb = word(vc[part][2 * i + 1], k4);
+              sts128(dst + v_off[k4] + 4096 * i, widen2(wa), widen2_hi(wa), widen2(wb), widen2_hi(wb));
+            }
           }
         }
         fence_async_smem();
-        mbar_arrive(smem_addr(&ms.v_full[vs]));
+        warp_arrive(ms.v_full);
       }
       if (!ok && lane == 0 && a.status) atomicOr(a.status, RQ_STATUS_TIMEOUT);
-    } else if (warp < kMmaWarp + 2) {
-      // ================= MMA issue (one thread per block) =================
-      if (lane == 0) {
-        const int bb = warp - kMmaWarp;
-        const uint32_t id = idesc_f16(kHalf, 128);  // S: N = 128 tokens; O: N = 128 dims
-        const uint32_t s_cols = tmem + kColS + 128 * bb, q_at = q_ops + 32768 * bb;
-        bool issued = false;
-        auto s_mmas = [&](uint32_t k) {  // S_b of tile k
-          const uint32_t k_at = k_ring + k % kKeyStages * kKeyBytes;
-          if (!(ok = role_wait(smem_addr(&ms.k_full[k % kKeyStages]), (k / kKeyStages) & 1, abort_flag))) return;
+    } else if (warp == kMmaWarp) {
+      // ================= MMA issue =================
+      const uint32_t id = idesc_f16(kHalf, 128);  // S: N = 128 tokens; O: N = 128 dims
+      bool issued = false;
+      auto wait = [&](uint64_t& bar, uint32_t parity) { return ok = warp_wait(bar, parity, abort_flag); };
+      auto s_mmas = [&](int bb, uint32_t k) {  // S_b of tile k
+        const uint32_t q_at = q_ops + 32768 * bb, k_at = k_ring + k % kKeyStages * kOperand;
+#pragma unroll
+        for (int ks = 0; ks < 8; ++ks)
+          elect_mma_ss(tmem + kColS + 128 * bb, sdesc(q_at + (ks >> 2) * 16384 + (ks & 3) * 32),
+                       sdesc(k_at + (ks >> 2) * 16384 + (ks & 3) * 32), id, ks > 0);
+        elect_commit(smem_addr(&ms.s_full[bb]));
+        issued = true;
+      };
+      if (wait(ms.k_full[t_base % kKeyStages], t_base / kKeyStages)) {
+        fence_after_sync();
+        s_mmas(0, t_base);
+        s_mmas(1, t_base);
+      }
+      for (int t = 0; t < n && ok; ++t) {
+        const uint32_t k = t_base + t;
+        const bool next = t + 1 < n;
+        if (!wait(ms.v_full, k)) break;
+        if (next && !wait(ms.k_full[(k + 1) % kKeyStages], (k + 1) / kKeyStages)) break;
+#pragma unroll
+        for (int bb = 0; bb < 2; ++bb) {
+          if (!wait(ms.p_full[bb], k)) break;
           fence_after_sync();
 #pragma unroll
-          for (int ks = 0; ks < 8; ++ks)
-            umma_f16_ss(s_cols, sdesc(q_at + (ks >> 2) * 16384 + (ks & 3) * 32), sdesc(k_at + (ks >> 2) * 16384 + (ks & 3) * 32),
-                        id, ks > 0);
-          umma_commit(smem_addr(&ms.s_full[bb]));
-          umma_commit(smem_addr(&ms.k_empty[k % kKeyStages]));
-          issued = true;
-        };
-        s_mmas(t_base);
-        for (int t = 0; t < n && ok; ++t) {
-          const uint32_t k = t_base + t;
-#pragma unroll 1
-          for (int part = 0; part < 2; ++part) {
-            const uint32_t k2 = 2 * k + part, vs = k2 % kValueStages;
-            if (!(ok = role_wait(smem_addr(&ms.v_full[vs]), (k2 / kValueStages) & 1, abort_flag))) break;
-            if (!(ok = role_wait(smem_addr(&ms.p_full[bb][part]), k & 1, abort_flag))) break;
-            fence_after_sync();
-#pragma unroll
-            for (int ks = 0; ks < 4; ++ks)
-              umma_f16_ts(tmem + 128 * bb, s_cols + 64 * part + 8 * ks, sdesc(v_ring + vs * kValueBytes + ks * 32), id,
-                          t > 0 || part > 0 || ks > 0);
-            umma_commit(smem_addr(&ms.o_done[bb][part]));
-            umma_commit(smem_addr(&ms.v_empty[vs]));
-          }
-          if (ok && t + 1 < n) s_mmas(k + 1);  // over the same columns, behind the MMAs that read them
+          for (int ks = 0; ks < 8; ++ks)  // tokens 16 ks ..: W 64 columns past S's for the second half
+            elect_mma_ts(tmem + 128 * bb, tmem + kColS + 128 * bb + 64 * (ks >> 2) + 8 * (ks & 3),
+                         sdesc(v_ring + (ks >> 2) * (kOperand / 2) + (ks & 3) * 32), id, t > 0 || ks > 0);
+          if (next)
+            s_mmas(bb, k + 1);  // over the same columns, behind the MMAs that read them
+          else
+            elect_commit(smem_addr(&ms.o_done[bb]));
         }
-        if (!ok) {
-          if (issued) {  // nothing may be running when the tensor memory is freed
-            umma_commit(smem_addr(&ms.drain[bb]));
-            for (int i = 0; i < kWaitLimit; ++i)
-              if (mbar_test(smem_addr(&ms.drain[bb]), 0u)) break;
-          }
-          if (a.status) atomicOr(a.status, RQ_STATUS_TIMEOUT);
+        if (ok) elect_commit(smem_addr(&ms.read));
+      }
+      if (!ok) {
+        if (issued) {  // nothing may be running when the tensor memory is freed
+          elect_commit(smem_addr(&ms.drain));
+          for (int i = 0; i < kWaitLimit; ++i)
+            if (mbar_test(smem_addr(&ms.drain), 0u)) break;
         }
+        if (lane == 0 && a.status) atomicOr(a.status, RQ_STATUS_TIMEOUT);
       }
     } else if (warp == kCopyWarp) {
       // ================= copies of the cache's blocks =================
@@ -570,9 +626,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const Geometry g, c
           now = later;
           later = pages_of((t2 >> 3) + 1);
         }
-        if (k2 >= kRawStages &&
-            !(ok = __all_sync(0xffffffffu, role_wait(smem_addr(&ms.raw_empty[rs]), (k2 / kRawStages - 1) & 1, abort_flag))))
-          break;
+        if (k2 >= kRawStages && !(ok = warp_wait(ms.raw_empty[rs], k2 / kRawStages - 1, abort_flag))) break;
         fills = k2 + 1;
         const uint32_t bar = smem_addr(&ms.raw_full[rs]);
         const int p = r0 * kTok + kPart * t2, count = min(4, max(0, (last - p + 15) / 16));
@@ -595,6 +649,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const Geometry g, c
       }
     }
     done_tiles += n;
+    ++done_frags;
     fence_before_sync();
     __syncthreads();
     fence_after_sync();
@@ -693,7 +748,10 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const Geometry g, c
 
 }  // namespace
 
-size_t block_extend_workspace(int num_sms) { return 2 * (size_t)num_sms * kSlotFloats; }
+size_t block_extend_workspace(int num_sms, size_t* n) {
+  *n = 2 * (size_t)num_sms * kSlotFloats * 4;
+  return 2 * (size_t)num_sms * kSlotFloats + num_sms * 128;
+}
 
 cudaError_t block_extend_prepare() {
   cudaError_t e = cudaFuncSetAttribute(extend_kernel<__half>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);

@@ -184,8 +184,8 @@ cudaError_t block_attention_prepare();
 cudaError_t launch_block_attention(const Geometry& g, AttnArgs a, int num_sms, cudaStream_t stream,
                                    cudaEvent_t ev_start, cudaEvent_t ev_end);
 // Extend attention over the 8-bit cache: a.ws holds block_extend_workspace floats, a.cnt num_sms
-// counters (zero between launches).
-size_t block_extend_workspace(int num_sms);
+// counters (zero between launches); its bytes from nan_bytes_at on are 0x7F between launches.
+size_t block_extend_workspace(int num_sms, size_t* nan_bytes_at);
 cudaError_t block_extend_prepare();
 cudaError_t launch_block_extend(const Geometry& g, AttnArgs a, int num_sms, cudaStream_t stream, cudaEvent_t ev_start,
                                 cudaEvent_t ev_end);
