@@ -471,14 +471,13 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const Geometry g, c
       uint32_t v_off[4];
 #pragma unroll
       for (int k4 = 0; k4 < 4; ++k4) v_off[k4] = sw128(vd + k4, t4 + 4 * (dw >> 1));  // + 4096 i
-      for (int t = 0; t < n && ok; ++t) {
+      auto widen_keys = [&](int t) {  // K(t), once S(t - 2) is done
         const uint32_t k = t_base + t;
         const int t0 = (r0 + t) * kTok;
-        // K(t - 2) is read: S(t - 1) was waited for before the last tile's values
 #pragma unroll
         for (int part = 0; part < 2; ++part) {
           const uint32_t rs = (2 * k + part) % kRawStages, raw = raw_ring + rs * kRawBytes + dw * kBlockBytes;
-          if (!(ok = warp_wait(ms.raw_full[rs], (2 * k + part) / kRawStages, abort_flag))) break;
+          if (!(ok = warp_wait(ms.raw_full[rs], (2 * k + part) / kRawStages, abort_flag))) return;
           // unit u: token 8 (u / 2) + g8, dims 64 (u % 2) + 16 t4 ..; the token's row is its column of S
           const uint32_t dst = k_ring + k % kKeyStages * kOperand + part * (kPart * 128);
           const bool there = t0 + kPart * part + 16 * dw < len;  // else nothing was copied
@@ -489,7 +488,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const Geometry g, c
             sts128(dst + k_off[u >> 1] + (u & 1) * 16384, widen2(c.x), widen2_hi(c.x), widen2(c.y), widen2_hi(c.y));
             sts128(dst + (k_off[u >> 1] ^ 16) + (u & 1) * 16384, widen2(c.z), widen2_hi(c.z), widen2(c.w), widen2_hi(c.w));
           }
-          // (S(t - 1) came behind W V(t - 2): both softmaxes are past tile t - 2, t - 4's slot is free)
+          // (W V(t - 3) is done, both softmaxes are past tile t - 3: t - 4's slot is free)
           if (lane == 0) {
             uint32_t exps = 0x7F7Fu;
             if (there) asm volatile("ld.shared.u16 %0, [%1];" : "=r"(exps) : "r"(raw + kExps));
@@ -500,9 +499,13 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const Geometry g, c
             sc[2][dw] = pow2(-ev);
           }
         }
-        if (!ok) break;
         fence_async_smem();
         warp_arrive(ms.k_full[k % kKeyStages]);
+      };
+      widen_keys(0);
+      for (int t = 0; t < n && ok; ++t) {
+        const uint32_t k = t_base + t;
+        const int t0 = (r0 + t) * kTok;
         uint4 vc[2][4];  // [part][2 i + b]: block p16 + b, dims 32 (2 (dw % 2) + i) + 4 g8 ..
         uint32_t bad = 0u;
 #pragma unroll
@@ -540,8 +543,10 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const Geometry g, c
             vc[part][i] = make_uint4(w[0], w[1], w[2], w[3]);
           }
         }
+        // the next keys while the values' stage is still read
+        if (t + 1 < n) widen_keys(t + 1);
         // W V(t - 1) of both blocks is done, whose values stand here, and S(t)
-        if (k > 0 && !(ok = warp_wait(ms.read, k - 1, abort_flag))) break;
+        if (!ok || (k > 0 && !(ok = warp_wait(ms.read, k - 1, abort_flag)))) break;
 #pragma unroll
         for (int part = 0; part < 2; ++part) {
           const uint32_t dst = v_ring + part * (kOperand / 2);
