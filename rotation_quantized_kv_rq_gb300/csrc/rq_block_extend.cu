@@ -70,9 +70,9 @@ struct Frag {           // tiles r0 .. r0 + n - 1 of one unit
 };
 struct Misc {
   uint64_t raw_full[kRawStages], raw_empty[kRawStages];
-  // K(t), V(t) are there; W V(t) and S(t + 1) of both blocks done; [block] S(t); [block] W(t); [block] the
+  // K(t), V(t) are there; S(t), W V(t) of both blocks done: K(t), V(t) are read; [block] S(t); [block] W(t); [block] the
   // fragment's last W V; drained
-  uint64_t k_full[kKeyStages], v_full, read, s_full[2], p_full[2], o_done[2], drain;
+  uint64_t k_full[kKeyStages], v_full, k_read[kKeyStages], v_read, s_full[2], p_full[2], o_done[2], drain;
   Frag f;
   uint32_t tmem;
   int abort, last;
@@ -244,9 +244,12 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const Geometry g, c
       mbar_init(smem_addr(&ms.raw_full[i]), 1);
       mbar_init(smem_addr(&ms.raw_empty[i]), kCodeWarps);
     }
-    for (int i = 0; i < kKeyStages; ++i) mbar_init(smem_addr(&ms.k_full[i]), kCodeWarps);
+    for (int i = 0; i < kKeyStages; ++i) {
+      mbar_init(smem_addr(&ms.k_full[i]), kCodeWarps);
+      mbar_init(smem_addr(&ms.k_read[i]), 1);
+    }
     mbar_init(smem_addr(&ms.v_full), kCodeWarps);
-    mbar_init(smem_addr(&ms.read), 1);
+    mbar_init(smem_addr(&ms.v_read), 1);
     mbar_init(smem_addr(&ms.drain), 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_addr(&ms.s_full[i]), 1);
@@ -411,7 +414,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const Geometry g, c
           }
         }
         const bool large = __any_sync(0xffffffffu, fabsf(from) > kLarge);  // the difference needs the rounded product
-#pragma unroll
+#pragma unroll 1  // (unrolled, the second half's registers spill: 1.84 -> 2.03 ms at 8 x 1,024 over 15K)
         for (int part = 0; part < 2; ++part) {
           if (part == 1) load(s, 1);
           const float4 ks4 = sc[3 * part], ev4 = sc[3 * part + 1], dn4 = sc[3 * part + 2];
@@ -474,6 +477,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const Geometry g, c
       auto widen_keys = [&](int t) {  // K(t), once S(t - 2) is done
         const uint32_t k = t_base + t;
         const int t0 = (r0 + t) * kTok;
+        if (k >= kKeyStages && !(ok = warp_wait(ms.k_read[k % kKeyStages], k / kKeyStages - 1, abort_flag))) return;
 #pragma unroll
         for (int part = 0; part < 2; ++part) {
           const uint32_t rs = (2 * k + part) % kRawStages, raw = raw_ring + rs * kRawBytes + dw * kBlockBytes;
@@ -488,7 +492,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const Geometry g, c
             sts128(dst + k_off[u >> 1] + (u & 1) * 16384, widen2(c.x), widen2_hi(c.x), widen2(c.y), widen2_hi(c.y));
             sts128(dst + (k_off[u >> 1] ^ 16) + (u & 1) * 16384, widen2(c.z), widen2_hi(c.z), widen2(c.w), widen2_hi(c.w));
           }
-          // (W V(t - 3) is done, both softmaxes are past tile t - 3: t - 4's slot is free)
+          // (S(t - 2) came behind W V(t - 3): both softmaxes are past tile t - 3, t - 4's slot is free)
           if (lane == 0) {
             uint32_t exps = 0x7F7Fu;
             if (there) asm volatile("ld.shared.u16 %0, [%1];" : "=r"(exps) : "r"(raw + kExps));
@@ -545,8 +549,8 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const Geometry g, c
         }
         // the next keys while the values' stage is still read
         if (t + 1 < n) widen_keys(t + 1);
-        // W V(t - 1) of both blocks is done, whose values stand here, and S(t)
-        if (!ok || (k > 0 && !(ok = warp_wait(ms.read, k - 1, abort_flag)))) break;
+        // W V(t - 1) of both blocks is done, whose values stand here
+        if (!ok || (k > 0 && !(ok = warp_wait(ms.v_read, k - 1, abort_flag)))) break;
 #pragma unroll
         for (int part = 0; part < 2; ++part) {
           const uint32_t dst = v_ring + part * (kOperand / 2);
@@ -581,6 +585,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const Geometry g, c
         fence_after_sync();
         s_mmas(0, t_base);
         s_mmas(1, t_base);
+        elect_commit(smem_addr(&ms.k_read[t_base % kKeyStages]));
       }
       for (int t = 0; t < n && ok; ++t) {
         const uint32_t k = t_base + t;
@@ -595,12 +600,13 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const Geometry g, c
           for (int ks = 0; ks < 8; ++ks)  // tokens 16 ks ..: W 64 columns past S's for the second half
             elect_mma_ts(tmem + 128 * bb, tmem + kColS + 128 * bb + 64 * (ks >> 2) + 8 * (ks & 3),
                          sdesc(v_ring + (ks >> 2) * (kOperand / 2) + (ks & 3) * 32), id, t > 0 || ks > 0);
+          if (bb == 1) elect_commit(smem_addr(&ms.v_read));
           if (next)
             s_mmas(bb, k + 1);  // over the same columns, behind the MMAs that read them
           else
             elect_commit(smem_addr(&ms.o_done[bb]));
         }
-        if (ok) elect_commit(smem_addr(&ms.read));
+        if (ok && next) elect_commit(smem_addr(&ms.k_read[(k + 1) % kKeyStages]));
       }
       if (!ok) {
         if (issued) {  // nothing may be running when the tensor memory is freed
