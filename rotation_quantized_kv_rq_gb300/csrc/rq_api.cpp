@@ -157,12 +157,9 @@ int create_block(rq_ctx* ctx, const rq_config* cfg) {
   g.sm_scale = cfg->sm_scale > 0.f ? cfg->sm_scale : (float)(1.0 / std::sqrt((double)cfg->head_dim));
   size_t counters = 0;
   ctx->ws_floats = rq::block_attention_workspace(ctx->num_sms, &counters);
-  size_t nan_at = 0;  // past what the split-K kernel uses
-  const size_t extend_floats = rq::block_extend_workspace(ctx->num_sms, &nan_at);
-  if (nan_at < ctx->ws_floats * sizeof(float)) return RQ_ERR_CUDA;
-  ctx->ws_floats = extend_floats;
+  const size_t extend_floats = rq::block_extend_workspace(ctx->num_sms);
+  if (extend_floats > ctx->ws_floats) ctx->ws_floats = extend_floats;
   cudaError_t e = cudaMalloc(&ctx->d_ws, ctx->ws_floats * sizeof(float));
-  if (e == cudaSuccess) e = cudaMemset((char*)ctx->d_ws + nan_at, 0x7F, ctx->ws_floats * sizeof(float) - nan_at);
   if (e == cudaSuccess) e = cudaMalloc(&ctx->d_frag, counters * sizeof(int));
   if (e == cudaSuccess) e = cudaMemset(ctx->d_frag, 0, counters * sizeof(int));  // as every launch leaves them
   if (e == cudaSuccess) e = rq::block_attention_prepare();
@@ -604,7 +601,9 @@ static int block_attention(rq_ctx* ctx, const void* q, int T, const uint64_t* tr
   a.rows = T * ctx->g.group;
   a.ws = ctx->d_ws;
   a.cnt = ctx->d_frag;
-  if (extend) return to_status(rq::launch_block_extend(ctx->g, a, ctx->num_sms, stream, ctx->prof_start, ctx->prof_end));
+  const double work = (double)B * T * ctx->g.num_q_heads * max_pages * ctx->g.page_size;
+  if (extend && work > rq::kSmallExtend)
+    return to_status(rq::launch_block_extend(ctx->g, a, ctx->num_sms, stream, ctx->prof_start, ctx->prof_end));
   return to_status(rq::launch_block_attention(ctx->g, a, ctx->num_sms, stream, ctx->prof_start, ctx->prof_end));
 }
 

@@ -28,6 +28,9 @@
 //
 // Work is cut evenly: tiles of all units (sequence, 256 rows, kv head) in order, one range per CTA.
 // A unit that spans ranges is joined by the last of its CTAs to finish, in the ranges' order.
+// Calls with little work (at most 2^23 rows x tokens of the block tables) go to the split-K kernel: a fragment
+// opens and closes in some 10 us here.  Measured, split-K and this kernel: 3 x 77 rows of up to 2K (5.7 M)
+// 28 and 46 us, 2 x 128 of 4K (8.4 M) 36 and 42, 4 x 128 of 2K (34 M) 110 and 58.
 // Every wait is bounded: one that runs out sets RQ_STATUS_TIMEOUT and an abort flag every role polls.
 #include <math_constants.h>
 
@@ -71,11 +74,11 @@ struct Frag {           // tiles r0 .. r0 + n - 1 of one unit
 struct Misc {
   uint64_t raw_full[kRawStages], raw_empty[kRawStages];
   // K(t), V(t) are there; S(t), W V(t) of both blocks done: K(t), V(t) are read; [block] S(t); [block] W(t); [block] the
-  // fragment's last W V; drained
-  uint64_t k_full[kKeyStages], v_full, k_read[kKeyStages], v_read, s_full[2], p_full[2], o_done[2], drain;
+  // fragment's last W V; the fragment's queries; drained
+  uint64_t k_full[kKeyStages], v_full, k_read[kKeyStages], v_read, s_full[2], p_full[2], o_done[2], q_full, drain;
   Frag f;
   uint32_t tmem;
-  int abort, last;
+  int abort, last, any_nan;
   alignas(16) float scales[kScaleSlots][2][3][4];  // [half][2^EK, EV, 2^-EV][block], read as float4
   int nan_from[kHeadDim];              // first position with a NaN value in a dim
 };
@@ -251,6 +254,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const Geometry g, c
     mbar_init(smem_addr(&ms.v_full), kCodeWarps);
     mbar_init(smem_addr(&ms.v_read), 1);
     mbar_init(smem_addr(&ms.drain), 1);
+    mbar_init(smem_addr(&ms.q_full), kSoftWarps);
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_addr(&ms.s_full[i]), 1);
       mbar_init(smem_addr(&ms.p_full[i]), kSoftWarps / 2);
@@ -289,6 +293,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const Geometry g, c
       }
     }
     if (tid < kHeadDim) ms.nan_from[tid] = INT32_MAX;
+    if (tid == 0) ms.any_nan = 0;
     fence_before_sync();
     __syncthreads();
     fence_after_sync();
@@ -306,26 +311,26 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const Geometry g, c
     };
 
     // ---- Q of the row as an operand: fp16 as it is; a bf16 row by a power of two ----
+    // (the keys' and values' roles start meanwhile; the MMAs wait for q_full)
     if (warp < kSoftWarps) {
       const uint4* src = reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(a.q) + row_offset());
       float down = 1.f;
       if constexpr (!std::is_same<T, __half>::value) {
         float top = 0.f;
-        if (valid)
-#pragma unroll 4
-          for (int c = 0; c < 16; ++c) {
-            const uint4 v = __ldg(src + c);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const float2 f = rope::unpack2<T>(word(v, k));
-              top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
-            }
+        for (int c = 0; c < 16; ++c) {
+          const uint4 v = valid ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float2 f = rope::unpack2<T>(word(v, k));
+            top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
           }
+        }
         const int e = min(max((int)(__float_as_uint(top) >> 23) - 127, -100), 127);
         down = pow2(14 - e);
         q_scale *= pow2(e - 14);
       }
-#pragma unroll 4
+#pragma unroll 8
       for (int c = 0; c < 16; ++c) {
         const uint4 v = valid ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
         uint32_t w[4];
@@ -340,8 +345,8 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const Geometry g, c
         sts128(q_ops + 32768 * blk + 16384 * (c >> 3) + sw128(brow, c & 7), w[0], w[1], w[2], w[3]);
       }
       fence_async_smem();
+      warp_arrive(ms.q_full);
     }
-    __syncthreads();
 
     bool ok = true;
     const uint32_t t_base = done_tiles;
@@ -540,7 +545,10 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const Geometry g, c
               for (int c = 0; c < 4; ++c) {
                 const int p = t0 + kPart * part + 16 * (p16 + (i & 1)) + 2 * t4 + (c & 1) + 8 * (c >> 1);
                 const bool isnan = (w[k4] >> (8 * c) & 0x7Fu) == 0x7Fu;
-                if (isnan && p < len) atomicMin(&ms.nan_from[32 * (2 * (dw & 1) + (i >> 1)) + 4 * g8 + k4], p);
+                if (isnan && p < len) {
+                  atomicMin(&ms.nan_from[32 * (2 * (dw & 1) + (i >> 1)) + 4 * g8 + k4], p);
+                  ms.any_nan = 1;
+                }
                 if (isnan || p >= len) w[k4] &= ~(0xFFu << (8 * c));
               }
             }
@@ -581,7 +589,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const Geometry g, c
         elect_commit(smem_addr(&ms.s_full[bb]));
         issued = true;
       };
-      if (wait(ms.k_full[t_base % kKeyStages], t_base / kKeyStages)) {
+      if (wait(ms.q_full, done_frags) && wait(ms.k_full[t_base % kKeyStages], t_base / kKeyStages)) {
         fence_after_sync();
         s_mmas(0, t_base);
         s_mmas(1, t_base);
@@ -683,16 +691,18 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const Geometry g, c
       const int qpos = valid ? len - a.T + row / g.group : -1;
       const float inv = whole ? (l_run == 0.f ? 0.f : 1.f / l_run) : 1.f;
       float* const slot = slot_of(blockIdx.x);
-#pragma unroll 1
+#pragma unroll 2
       for (int c = 0; c < kHeadDim / 16; ++c) {
         float y[16];
         __syncwarp();
         tmem_ld16(tmem + lane_off + 128 * blk + 16 * c, y);
         tmem_wait_ld();
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          y[i] = l_run == 0.f ? 0.f : y[i] * inv;
-          if (ms.nan_from[16 * c + i] <= qpos) y[i] = CUDART_NAN_F;
+        for (int i = 0; i < 16; ++i) y[i] = l_run == 0.f ? 0.f : y[i] * inv;
+        if (ms.any_nan) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            if (ms.nan_from[16 * c + i] <= qpos) y[i] = CUDART_NAN_F;
         }
         if (whole) {
           if (valid) store16(c, y);
@@ -719,29 +729,36 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const Geometry g, c
         __threadfence();
         if (tid == 0) a.cnt[cf] = 0;  // as every launch finds it
         if (warp < kSoftWarps) {
-          float top = kNone, sum = 0.f;
-          for (int f = 0; f < frags; ++f) top = fmaxf(top, __ldcg(slot_of(cf + f) + kRows * kHeadDim + srow));
-          for (int f = 0; f < frags; ++f) {
-            const float* s = slot_of(cf + f) + kRows * kHeadDim + srow;
-            sum = fmaf(__ldcg(s + kRows), ex2(__ldcg(s) - top), sum);
-          }
-          const float inv = sum == 0.f ? 0.f : 1.f / sum;
+          // a fragment's 64 dims and its m and l load together, the sums grow with the maximum
 #pragma unroll 1
-          for (int c = 0; c < kHeadDim / 16; ++c) {
-            float y[16];
+          for (int d = 0; d < 2; ++d) {
+            float y[64], top = kNone, sum = 0.f;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) y[i] = 0.f;
+            for (int i = 0; i < 64; ++i) y[i] = 0.f;
+#pragma unroll 1
             for (int f = 0; f < frags; ++f) {
               const float* s = slot_of(cf + f);
-              const float w = ex2(__ldcg(s + kRows * kHeadDim + srow) - top) * inv;
+              const float mf = __ldcg(s + kRows * kHeadDim + srow), lf = __ldcg(s + kRows * kHeadDim + kRows + srow);
+              const float t = fmaxf(top, mf), wa = ex2(top - t), w = ex2(mf - t);
+              top = t;
+              sum = fmaf(sum, wa, lf * w);
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const float4 v = __ldcg(reinterpret_cast<const float4*>(s) + (4 * c + i) * kRows + srow);
-                y[4 * i] = fmaf(v.x, w, y[4 * i]), y[4 * i + 1] = fmaf(v.y, w, y[4 * i + 1]);
-                y[4 * i + 2] = fmaf(v.z, w, y[4 * i + 2]), y[4 * i + 3] = fmaf(v.w, w, y[4 * i + 3]);
+              for (int i = 0; i < 16; ++i) {
+                const float4 v = __ldcg(reinterpret_cast<const float4*>(s) + (16 * d + i) * kRows + srow);
+                y[4 * i] = fmaf(y[4 * i], wa, v.x * w), y[4 * i + 1] = fmaf(y[4 * i + 1], wa, v.y * w);
+                y[4 * i + 2] = fmaf(y[4 * i + 2], wa, v.z * w), y[4 * i + 3] = fmaf(y[4 * i + 3], wa, v.w * w);
               }
             }
-            if (valid) store16(c, y);
+            const float inv = sum == 0.f ? 0.f : 1.f / sum;
+            if (valid) {
+#pragma unroll
+              for (int c = 0; c < 4; ++c) {
+                float z[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) z[i] = y[16 * c + i] * inv;
+                store16(4 * d + c, z);
+              }
+            }
           }
         }
       }
@@ -759,10 +776,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const Geometry g, c
 
 }  // namespace
 
-size_t block_extend_workspace(int num_sms, size_t* n) {
-  *n = 2 * (size_t)num_sms * kSlotFloats * 4;
-  return 2 * (size_t)num_sms * kSlotFloats + num_sms * 128;
-}
+size_t block_extend_workspace(int num_sms) { return 2 * (size_t)num_sms * kSlotFloats; }  // two slots a CTA
 
 cudaError_t block_extend_prepare() {
   cudaError_t e = cudaFuncSetAttribute(extend_kernel<__half>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);

@@ -183,9 +183,10 @@ size_t block_attention_workspace(int num_sms, size_t* counters);
 cudaError_t block_attention_prepare();
 cudaError_t launch_block_attention(const Geometry& g, AttnArgs a, int num_sms, cudaStream_t stream,
                                    cudaEvent_t ev_start, cudaEvent_t ev_end);
+constexpr double kSmallExtend = 8388608.0;  // rows x tokens up to which an extend call takes the split-K kernel (rq_block_extend.cu)
 // Extend attention over the 8-bit cache: a.ws holds block_extend_workspace floats, a.cnt num_sms
-// counters (zero between launches); its bytes from nan_bytes_at on are 0x7F between launches.
-size_t block_extend_workspace(int num_sms, size_t* nan_bytes_at);
+// counters (zero between launches).
+size_t block_extend_workspace(int num_sms);
 cudaError_t block_extend_prepare();
 cudaError_t launch_block_extend(const Geometry& g, AttnArgs a, int num_sms, cudaStream_t stream, cudaEvent_t ev_start,
                                 cudaEvent_t ev_end);
