@@ -244,11 +244,16 @@ def test_append_refusals():
 
 # --------------------------------------------------------------------------------- attention
 
-def filled(rng, hq, hkv, P, lens, dtype, t=1, spread=0):
+def wide(B, T, hq, P):
+    """Block-table width from which an extend call has its own kernel (narrower, smaller calls share the split-K one)."""
+    return 2 ** 23 // (B * T * hq * P) + 1
+
+
+def filled(rng, hq, hkv, P, lens, dtype, t=1, spread=0, width=0):
     """A cache of sequences of `lens` tokens on random pages; what no token was written to holds NaN
     codes and the largest exponents.  spread: keys and values of blocks differ by up to 2^spread."""
     need = [(int(x) + P - 1) // P for x in lens]
-    width = max(max(need), 1) + 1
+    width = max(max(need) + 1, 2, width)
     pages = sum(need) + 2
     table = np.zeros((len(lens), width), np.int32)
     order = rng.permutation(pages)
@@ -308,31 +313,65 @@ def test_decode(dtype, hq, hkv, P, lens, spread):
     assert torch.equal(out, again)
 
 
-@pytest.mark.parametrize("dtype", ["f16", "bf16"])
-@pytest.mark.parametrize("T,hq,hkv,P,lens,spread", [
+VERIFY = [
     (6, 32, 8, 16, [70, 100, 6, 7, 0], 0), (2, 5, 5, 32, [2, 33], 2), (5, 24, 2, 16, [90, 1033], 0),
     (3, 64, 1, 64, [1500, 3, 64], 3), (64, 4, 4, 16, [64, 200], 0), (17, 1, 1, 16, [17, 300], 0),
-])
-def test_verify_and_extend(dtype, T, hq, hkv, P, lens, spread):
+]
+EXTEND = VERIFY + [
+    (300, 32, 8, 16, [300, 555, 1024], 0), (129, 12, 4, 48, [129, 0, 700], 3), (513, 3, 1, 64, [2000], 0),
+    (100, 40, 2, 16, [101, 115, 117], 5), (1, 4, 4, 16, [1, 128, 129, 4000], 2), (257, 1, 1, 256, [257, 300, 9000], 0),
+]
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("T,hq,hkv,P,lens,spread", VERIFY)
+def test_verify(dtype, T, hq, hkv, P, lens, spread):
     rng, dtype = gen(T * hq), DT[dtype]
     cache, table, lens = filled(rng, hq, hkv, P, lens, dtype, t=T, spread=spread)
     q = dev(rng.standard_normal((len(lens), T, hq, 128)), dtype)
-    see = lambda b, j, p: p <= lens[b] - T + j  # noqa: E731
-    check(cache, table, lens, q, cache.verify(q, dev(table), dev(lens)), see, "verify")
-    check(cache, table, lens, q, cache.extend(q, dev(table), dev(lens)), see, "extend")
+    out = cache.verify(q, dev(table), dev(lens))
+    check(cache, table, lens, q, out, lambda b, j, p: p <= lens[b] - T + j, "verify")
+    assert torch.equal(out, cache.verify(q, dev(table), dev(lens)))
 
 
 @pytest.mark.parametrize("dtype", ["f16", "bf16"])
-@pytest.mark.parametrize("T,hq,hkv,P,lens,spread", [
-    (300, 32, 8, 16, [300, 555, 1024], 0), (129, 12, 4, 48, [129, 0, 700], 3), (513, 3, 1, 64, [2000], 0),
-    (100, 40, 2, 16, [101, 115, 117], 5),
-])
-def test_extend(dtype, T, hq, hkv, P, lens, spread):
+@pytest.mark.parametrize("own_kernel", [False, True])
+@pytest.mark.parametrize("T,hq,hkv,P,lens,spread", EXTEND)
+def test_extend(dtype, own_kernel, T, hq, hkv, P, lens, spread):
     rng, dtype = gen(T * hq), DT[dtype]
-    cache, table, lens = filled(rng, hq, hkv, P, lens, dtype, spread=spread)  # max_query_tokens 1: no limit here
+    width = wide(len(lens), T, hq, P) if own_kernel else 0
+    # max_query_tokens is 1: no limit here
+    cache, table, lens = filled(rng, hq, hkv, P, lens, dtype, spread=spread, width=width)
     q = dev(rng.standard_normal((len(lens), T, hq, 128)), dtype)
     out = cache.extend(q, dev(table), dev(lens))
     check(cache, table, lens, q, out, lambda b, j, p: p <= lens[b] - T + j, "extend")
+    assert torch.equal(out, cache.extend(q, dev(table), dev(lens)))
+
+
+@pytest.mark.parametrize("call", ["verify", "extend", "extend, own kernel"])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_what_is_not_finite_reaches_the_rows_that_see_it(call, value):
+    """Key and value of new token 3 not finite: rows 0-2 do not see it.  A NaN value shows in its dim
+    only, a NaN key in all; infinities are stored as the largest value."""
+    T, L, hq = 6, 40, 4
+    cache, table, lens = filled(gen(12), hq, 2, 16, [L, 300], torch.float16, t=T,
+                                width=wide(2, T, hq, 16) if "own" in call else 0)
+    kv = torch.ones((2, 1, 2, 128), dtype=torch.float16, device="cuda")
+    kv[1, 0, 0, 37] = value  # value of kv head 0
+    kv[0, 0, 1, 5] = value   # key of kv head 1
+    at = L - T + 3
+    cache.append(kv[0], kv[1], torch.tensor([table[0, at // 16] * 16 + at % 16], dtype=torch.int32, device="cuda"))
+    assert int(cache.status.item()) == rq.RQ_STATUS_NOT_FINITE
+    q = dev(gen(13).standard_normal((2, T, hq, 128)), torch.float16)
+    out = (cache.verify if call == "verify" else cache.extend)(q, dev(table), dev(lens))
+    fin = torch.isfinite(out)
+    assert fin[1].all() and fin[0, :3].all()
+    if value != value:
+        want = torch.ones((3, hq, 128), dtype=torch.bool, device="cuda")
+        want[:, :2, 37], want[:, 2:] = False, False
+        assert torch.equal(fin[0, 3:], want)
+    else:
+        assert fin.all()
 
 
 @pytest.mark.parametrize("T,hq,hkv,P,lens", [(7, 32, 8, 16, [7, 40, 300]), (64, 4, 2, 32, [64, 90]), (1, 3, 3, 16, [1, 50])])
@@ -398,11 +437,12 @@ def test_decode_step_equals_append_and_decode():
 
 
 @pytest.mark.parametrize("fault", ["page", "negative page", "length", "negative length", "short"])
-@pytest.mark.parametrize("call", ["decode", "verify", "extend", "step"])
+@pytest.mark.parametrize("call", ["decode", "verify", "extend", "extend, own kernel", "step"])
 def test_faults_are_reported_and_clamped(fault, call):
     if fault == "short" and call in ("decode", "step"):
         return
-    cache, table, lens = filled(gen(6), 4, 2, 16, [50, 40], torch.float16, t=3)
+    cache, table, lens = filled(gen(6), 4, 2, 16, [50, 40], torch.float16, t=3,
+                                width=wide(2, 3, 4, 16) if "own" in call else 0)
     want = rq.RQ_STATUS_BAD_PAGE if "page" in fault else rq.RQ_STATUS_BAD_LEN
     if "page" in fault:
         table[0, 3] = 2 ** 31 - 1 if fault == "page" else -7  # the newest token's
@@ -414,7 +454,7 @@ def test_faults_are_reported_and_clamped(fault, call):
     fn = dict(decode=lambda: cache.decode(q[:, 0].contiguous(), dev(table), dev(lens))[:, None],
               step=lambda: cache.decode_step(q[:, 0].contiguous(), k, k, dev(table), dev(lens))[:, None],
               verify=lambda: cache.verify(q, dev(table), dev(lens)),
-              extend=lambda: cache.extend(q, dev(table), dev(lens)))[call]
+              extend=lambda: cache.extend(q, dev(table), dev(lens)))[call.split(",")[0]]
     out = fn()
     torch.cuda.synchronize()
     assert int(cache.status.item()) == want
@@ -522,7 +562,11 @@ def test_offsets_past_32_bits():
     small = make(hkv, hkv, P, 2, torch.float16, batch=1, max_pages=2)
     small.append(k, v, dev(pos.astype(np.int32)))
     assert torch.equal(cache.pages[pages - 1], small.pages[0]) and torch.equal(cache.pages[pages - 2], small.pages[1])
-    q = dev(rng.standard_normal((1, 20, hkv, 128)), torch.float16)
+    q = dev(rng.standard_normal((1, 290, hkv, 128)), torch.float16)
     ln, near = dev(np.array([L], np.int32)), dev(np.array([[0, 1]], np.int32))
-    assert torch.equal(cache.extend(q, dev(table), ln), small.extend(q, near, ln))
+    assert torch.equal(cache.extend(q[:, :20].contiguous(), dev(table), ln), small.extend(q[:, :20].contiguous(), near, ln))
+    far = cache, np.pad(table, ((0, 0), (0, 20))), small, np.pad(near.cpu().numpy(), ((0, 0), (0, 20)))
+    for c in (cache, small):  # contexts of wide tables over the same pools: the extend kernel of its own
+        c.wide = rq.KVCache(rq.RQ_FP8, 8, hkv, hkv, P, c.num_pages, None, None, max_batch=1, max_pages_per_seq=22, pages=c.pages)
+    assert torch.equal(far[0].wide.extend(q, dev(far[1]), ln), far[2].wide.extend(q, dev(far[3]), ln))
     assert torch.equal(cache.decode(q[:, 0].contiguous(), dev(table), ln), small.decode(q[:, 0].contiguous(), near, ln))
