@@ -97,9 +97,19 @@ __device__ __forceinline__ float2 cos_sin(const RopeTable& r, int p, const int32
   const ulonglong2 e = __ldg(reinterpret_cast<const ulonglong2*>(r.pairs) + p);  // (turns per position, axis)
   const int32_t pos = __ldg(positions + (long long)e.y * n + t);
   const uint64_t turns = (uint64_t)(int64_t)pos * e.x;
+  // quarter turns, and what is left of one (|left| <= 1/8 turn) before the rounding to 24 bits: an
+  // angle of half a turn rounded as it is would be off by 9e-8 rad, a third of all the f32 error here
   const int32_t frac = (int32_t)((turns + 0x80000000ull) >> 32);  // signed fraction of a turn, * 2^32
+  const uint32_t quarter = ((uint32_t)frac + 0x20000000u) >> 30;
+  const int32_t left = (int32_t)((uint32_t)frac - (quarter << 30));
   float s, c;
-  sincospif((float)frac * 4.656612873077393e-10f, &s, &c);  // 2^-31: half turns
+  sincospif((float)left * 4.656612873077393e-10f, &s, &c);  // 2^-31: half turns
+  if (quarter & 1) {  // (c, s) turned by a quarter: (-s, c)
+    const float t = c;
+    c = -s;
+    s = t;
+  }
+  if (quarter & 2) c = -c, s = -s;
   return make_float2(c * r.scale, s * r.scale);
 }
 // Cosines, sines and negated sines of the lane's pairs, two to a word.

@@ -11,9 +11,9 @@ pytestmark = pytest.mark.gpu
 
 DT = {"f16": torch.float16, "bf16": torch.bfloat16}
 # f32 arithmetic of the norm and the rotation, relative to |a| + |b| of a pair: the mean of 128
-# squares (12 roundings, halved by the root), the root, two products: 9 * 2^-24; the angle rounded
-# to 24 bits of half a turn (pi * 2^-25), sincospif (2^-23), the rotation's three roundings
-TURN_ERR = 9 * 2.0 ** -24 + np.pi * 2.0 ** -25 + 2.0 ** -23 + 3 * 2.0 ** -24
+# squares (12 roundings, halved by the root), the root, two products: 9 * 2^-24; the angle rounded to
+# 24 bits within an eighth of a turn (pi / 4 * 2^-24), sincospif (2^-23), the rotation's three roundings
+TURN_ERR = 9 * 2.0 ** -24 + np.pi / 4 * 2.0 ** -24 + 2.0 ** -23 + 3 * 2.0 ** -24
 
 
 def gen(seed):
