@@ -22,8 +22,12 @@ using namespace rope;
 using namespace block;
 
 constexpr int kMaxWarps = 8;
-constexpr int kLongAppend = 1024;  // tokens from which a CTA takes 16 of them
-constexpr int kSplitAppend = 8192; // tokens from which the queries have a launch of their own
+// Tokens from which a CTA takes 16 of them.  Device time, us, one token of a sequence or 16 to a CTA:
+// 1,024 x 1 token 27 | 70; 128 x 8 17.5 | 28; 256 x 8 27.3 | 28.5; 1 x 1,500 20 | 22; 1 x 2,048 29 | 30;
+// 1 x 8,000 (one head) 53 | 21; 1 x 16,000 130 | 79.  The slots say how long the runs are, and they
+// are on the device: a call with as many tokens is taken for a prompt's, unless each is a sequence's.
+constexpr int kLongAppend = 2048;
+constexpr int kSplitAppend = 8192;  // tokens from which the queries have a launch of their own
 
 constexpr uint32_t kInf = 0x7F800000u;
 
@@ -317,7 +321,7 @@ template <typename T, bool INTERLEAVED>
 void launch(const Geometry& g, const BlockAppendArgs& a, int num_sms, cudaStream_t stream) {
   const int hkv = g.num_kv_heads, hq = a.in.q.heads;
   int warps = hkv < 2 ? 2 : (2 * hkv > kMaxWarps ? kMaxWarps : 2 * hkv);
-  if (a.in.n < kLongAppend) {
+  if (a.in.n < kLongAppend || a.slots == nullptr) {
     if (hq > 0) warps = kMaxWarps;
     const int most = max((2 * hkv + warps - 1) / warps, (hq + 2 * warps - 1) / (2 * warps));
     long long split = (2LL * num_sms + a.in.n - 1) / a.in.n;
