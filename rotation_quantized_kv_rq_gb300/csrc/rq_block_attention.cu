@@ -42,7 +42,7 @@ namespace {
 using namespace block;
 
 constexpr float kMargin = 8.f;      // log2 slack of the running maximum
-constexpr float kNone = -1e30f;     // running maximum before any visible token
+constexpr float kNone = -3.402823466e38f;  // running maximum before any visible token: no finite score is below
 constexpr int kRowStride = 132;     // floats per joined row (128 and padding)
 
 constexpr int kRowBytes = kRowStride * 4;  // a joined row: 128 sums, the maximum, the weights' sum
@@ -458,11 +458,17 @@ __global__ void __launch_bounds__(32 * W, warps_per_sm(NT) / W) splitk_kernel(co
     auto write_row = [&](int r, float4 v, float sum) {  // a lane's four dims of a row of the output
       const int row = row0 + r, j = row / g.group, head = h * g.group + row % g.group;
       T* dst = reinterpret_cast<T*>(a.out) + (((size_t)b * a.T + j) * g.num_q_heads + head) * kHeadDim;
+      if (sum == 0.f) {  // the row sees nothing, or only scores of minus infinity: their softmax is 0 / 0
+        const int lo = max(0, a.T - len);  // first of the T query tokens that the sequence holds
+        const bool sees = a.tree_mask ? len > a.T || (lo < a.T && __ldg(a.tree_mask + (size_t)b * a.T + j) << (64 - a.T) >> (64 - a.T + lo))
+                                      : len - a.T + j >= 0;
+        const float x = sees ? CUDART_NAN_F : 0.f;
+        v = make_float4(x, x, x, x);
+        sum = 1.f;
+      }
       const float inv = 1.f / sum;
-      if (sum == 0.f) v = make_float4(0.f, 0.f, 0.f, 0.f);  // the row sees nothing
       *(reinterpret_cast<uint2*>(dst) + lane) =
-          sum == 0.f ? make_uint2(0u, 0u)
-                     : make_uint2(rope::pack2<T>(v.x * inv, v.y * inv), rope::pack2<T>(v.z * inv, v.w * inv));
+          make_uint2(rope::pack2<T>(v.x * inv, v.y * inv), rope::pack2<T>(v.z * inv, v.w * inv));
     };
     for (int r = warp; r < rows; r += W) {
       float top = s_m[0][r], sum = 0.f;

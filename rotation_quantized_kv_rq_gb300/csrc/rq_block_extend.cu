@@ -57,7 +57,7 @@ constexpr uint32_t kOperand = 32768, kRawBytes = 4 * kBlockBytes;
 constexpr uint32_t kQBytes = 2 * 32768;
 constexpr int kScaleSlots = 4;      // tiles whose scales are kept
 constexpr float kMargin = 8.f;      // log2 slack of the running maximum
-constexpr float kNone = -1e30f;     // running maximum before any visible token
+constexpr float kNone = -3.402823466e38f;  // running maximum before any visible token: no finite score is below
 constexpr float kLarge = 1048576.f; // |maximum| from which weights are formed in two roundings
 constexpr int kMinTiles = 4;        // a CTA's least work, while there is enough
 constexpr uint32_t kColS = 256;     // tensor memory: O_b at 128 b, S_b at 256 + 128 b
@@ -689,7 +689,9 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const Geometry g, c
     const int srow = kHalf * blk + brow;
     if (warp < kSoftWarps) {
       const int qpos = valid ? len - a.T + row / g.group : -1;
-      const float inv = whole ? (l_run == 0.f ? 0.f : 1.f / l_run) : 1.f;
+      const float inv = whole ? 1.f / l_run : 1.f;
+      // a row that sees nothing, or only scores of minus infinity (their softmax is 0 / 0)
+      const float empty = whole && qpos >= 0 ? CUDART_NAN_F : 0.f;
       float* const slot = slot_of(blockIdx.x);
 #pragma unroll 2
       for (int c = 0; c < kHeadDim / 16; ++c) {
@@ -698,7 +700,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const Geometry g, c
         tmem_ld16(tmem + lane_off + 128 * blk + 16 * c, y);
         tmem_wait_ld();
 #pragma unroll
-        for (int i = 0; i < 16; ++i) y[i] = l_run == 0.f ? 0.f : y[i] * inv;
+        for (int i = 0; i < 16; ++i) y[i] = l_run == 0.f ? empty : y[i] * inv;
         if (ms.any_nan) {
 #pragma unroll
           for (int i = 0; i < 16; ++i)
@@ -749,7 +751,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const Geometry g, c
                 y[4 * i + 2] = fmaf(y[4 * i + 2], wa, v.z * w), y[4 * i + 3] = fmaf(y[4 * i + 3], wa, v.w * w);
               }
             }
-            const float inv = sum == 0.f ? 0.f : 1.f / sum;
+            const float inv = sum == 0.f ? (len - a.T + row / g.group >= 0 ? CUDART_NAN_F : 0.f) : 1.f / sum;
             if (valid) {
 #pragma unroll
               for (int c = 0; c < 4; ++c) {

@@ -405,6 +405,44 @@ def test_large_scores_and_equal_scores():
     check(cache, table, lens, q, out[:, None], lambda b, j, p: p <= lens[b] - 1, "decode")
 
 
+@pytest.mark.parametrize("call", ["verify", "tree", "extend", "extend, own kernel"])
+def test_scores_near_the_ends_of_the_range(call):
+    """Scores of about -1e32: the one key of half the size takes all the weight.  Scores of minus
+    infinity only: a softmax of 0 / 0, where a row that sees nothing is 0."""
+    T, lens = 6, [40, 300, 6, 4]
+    width = wide(4, T, 4, 16) if "own" in call else 0
+    cache, table, lens = filled(gen(20), 4, 2, 16, lens, torch.bfloat16, t=T, width=width)
+    want = torch.empty((4, 2, 128), dtype=torch.bfloat16, device="cuda")
+    for b, L in enumerate(lens):
+        pos = np.arange(L)
+        k = torch.ones((L, 2, 128), dtype=torch.bfloat16, device="cuda")
+        k[2] = 0.5
+        v = dev(gen(21 + b).integers(-8, 9, (L, 2, 128)), torch.bfloat16)
+        cache.append(k, v, dev((table[b, pos // 16] * 16 + pos % 16).astype(np.int32)))
+        want[b] = v[2]
+    q = torch.full((4, T, 4, 128), -1e31, dtype=torch.bfloat16, device="cuda")
+    q[:, :, 1] = 0
+    q[:, :, 1, 0] = -float("inf")
+    if call == "tree":
+        mask = torch.full((4, T), 0x3F, dtype=torch.int64, device="cuda")
+        mask[2, 0], mask[3, 5], mask[3, 4] = 0, 3, ~63  # bits of drafts that the sequence does not hold
+        out = cache.tree_verify(q, mask, dev(table), dev(lens))
+        rows = {0: range(6), 1: range(6), 2: range(1, 6), 3: range(4)}
+        blind = [(2, 0), (3, 4), (3, 5)]
+    else:
+        out = (cache.verify if call == "verify" else cache.extend)(q, dev(table), dev(lens))
+        rows = {0: range(6), 1: range(6), 2: range(2, 6), 3: range(4, 6)}
+        blind = [(3, 0), (3, 1)]
+        assert torch.isnan(out[2, :, 1]).all() and torch.isnan(out[3, 2:, 1]).all()
+    for b in rows:
+        for j in rows[b]:
+            for head in (0, 2, 3):
+                assert torch.equal(out[b, j, head], want[b, head // 2]), (b, j, head)
+            assert torch.isnan(out[b, j, 1]).all()
+    for b, j in blind:
+        assert (out[b, j] == 0).all(), (b, j)
+
+
 def test_nan_key_reaches_its_readers_only():
     cache, table, lens = filled(gen(4), 2, 2, 16, [40, 40], torch.float16)
     k = torch.ones((1, 2, 128), dtype=torch.float16, device="cuda")
