@@ -18,7 +18,10 @@
 // joining hide behind the others' copies; with fewer units than SMs one CTA of 16 warps does, which
 // cuts a unit into a quarter of the parts to join (1 x 32K: 19 instead of 76).  Rows of a kv head beyond
 // 8 (group > 8, verify) share the widened tile: up to three n-tiles of 8 rows a warp, with the
-// registers for 12 and 8 warps an SM.
+// registers for 12 and 8 warps an SM and the queries in shared memory.  Three n-tiles are bound by the
+// chain wait - widen - MMA - softmax - MMA of two warps a quarter SM (0.36 instructions a cycle, the MMAs
+// busy 31%).  8 x 16K, 6 rows x 4 heads, us: 69 so, 72 with 12 warps (spills), 74 with the next tile's
+// products before this one's softmax, 74 with the values loaded a quarter at a time.
 //
 // Work is cut evenly: a unit is (sequence, kv head, group of n-tiles) and costs one round per tile of
 // each warp; the rounds of all units in order are cut into one range per CTA, on the device from
@@ -55,14 +58,14 @@ constexpr int smem_bytes(int nt, int w) { return ring_bytes(nt, w) + (w * stages
 
 __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                     uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   uint32_t y;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
 __device__ __forceinline__ float ex2(float x) {
@@ -119,6 +122,7 @@ __global__ void __launch_bounds__(32 * W, warps_per_sm(NT) / W) splitk_kernel(co
   __shared__ long long s_sum[W], s_begin;  // rounds per warp's sequences; first sequence's rounds before it
   __shared__ int s_seq, s_last, s_len[kLens];
   __shared__ float s_m[W][kRows], s_l[W][kRows];
+  __shared__ uint4 s_q[NT > 1 ? NT * 4 * 32 : 1];  // query fragments [n][ks / 2][lane], the same in every warp
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, gq = lane >> 2, tq = lane & 3;
   const int cap = a.max_pages * g.page_size, groups = (a.n_tiles_n + NT - 1) / NT;
   const int per_seq = g.num_kv_heads * groups;  // units of a sequence
@@ -185,6 +189,7 @@ __global__ void __launch_bounds__(32 * W, warps_per_sm(NT) / W) splitk_kernel(co
   long long at = s_begin;
   int b = s_seq;
 
+  const uint32_t s_q_addr = (uint32_t)__cvta_generic_to_shared(s_q) + 16 * lane;
   uint32_t issued = 0, done = 0;  // tiles of this warp so far: ring positions and parities
   uint32_t joins = 0;
   bool failed = false;
@@ -274,6 +279,17 @@ __global__ void __launch_bounds__(32 * W, warps_per_sm(NT) / W) splitk_kernel(co
       }
     }
 
+    if constexpr (NT > 1) {  // the fragment's queries are the same in every warp: kept once
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if ((4 * n + k) % W == warp)
+            s_q[(4 * n + k) * 32 + lane] = make_uint4(qf[n][2 * k][0], qf[n][2 * k][1], qf[n][2 * k + 1][0], qf[n][2 * k + 1][1]);
+      }
+      __syncthreads();
+    }
+
     float o[NT][8][4], m[NT][2], l[NT][2];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
@@ -305,12 +321,24 @@ __global__ void __launch_bounds__(32 * W, warps_per_sm(NT) / W) splitk_kernel(co
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
         const uint4 lo = lds128(tile + 16 * (32 * half + lane)), hi = lds128(tile + 16 * (32 * (2 + half) + lane));
+        uint4 qw[NT];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
+          if constexpr (NT > 1) {
+            if ((k & 1) == 0) {
+#pragma unroll
+              for (int n = 0; n < NT; ++n) qw[n] = lds128(s_q_addr + 512 * (4 * n + 2 * half + (k >> 1)));
+            }
+          }
           const uint32_t w0 = word(lo, k), w1 = word(hi, k);
           const uint32_t a0 = widen2(w0), a1 = widen2(w1), a2 = widen2_hi(w0), a3 = widen2_hi(w1);
 #pragma unroll
-          for (int n = 0; n < NT; ++n) mma(s[n], a0, a1, a2, a3, qf[n][4 * half + k][0], qf[n][4 * half + k][1]);
+          for (int n = 0; n < NT; ++n) {
+            if constexpr (NT > 1)
+              mma(s[n], a0, a1, a2, a3, word(qw[n], 2 * (k & 1)), word(qw[n], 2 * (k & 1) + 1));
+            else
+              mma(s[n], a0, a1, a2, a3, qf[n][4 * half + k][0], qf[n][4 * half + k][1]);
+          }
         }
       }
       if (tail) {
