@@ -1229,7 +1229,6 @@ attn_splitk_kernel(const Geometry g, const AttnArgs a, int smem_bytes) {
       for (int i = 0; i < NT; ++i) vis_min = min(vis_min, min(last_pos[i][0], last_pos[i][1]));
       const bool interior = __all_sync(0xffffffffu, pos0 + 31 <= vis_min);
       if (!interior) {
-        if (pos0 + 16 > pos_lim) nv_bits[1] = 0u;  // no second tile: the stage holds an older one's norms there
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
           const int draft0 = last_pos[i][0] + 1;  // tree: the first draft follows the prefix
@@ -1255,6 +1254,7 @@ attn_splitk_kernel(const Geometry g, const AttnArgs a, int smem_bytes) {
           }
         }
       }
+      if (!interior && pos0 + 16 > pos_lim) nv_bits[1] = 0u;  // no second tile: the stage holds an older one's norms there
       float cmax[NT][2];
       bool grow = false;
 #pragma unroll
