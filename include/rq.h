@@ -86,7 +86,8 @@ extern "C" {
 #define RQ_STATUS_NORM_OVERFLOW 8 /* a vector norm above the fp16 range (stored as inf) */
 #define RQ_STATUS_NOT_FINITE 32 /* an infinity or NaN among the values an RQ_FP8 append coded */
 #define RQ_STATUS_TIMEOUT 16   /* an attention kernel's staged page copy did not complete within
-                                  its bounded wait (outputs of that call are unspecified) */
+                                  its bounded wait (outputs of that call are unspecified; free an
+                                  RQ_FP8 context, whose workspace the call may not have put back) */
 
 /* Rotation families.  Source: README, CLI Reference > KV Cache Compression Flags (--kv-cache-dtype
    rq{3,4}_{planar,iso}, tq{2,3,4}) and the two mode tables under Core Features (RotorQuant: 2D
@@ -130,13 +131,14 @@ typedef struct {
   const float *codebook;
   float sm_scale;            /* softmax scale; 0 selects 1/sqrt(head_dim) */
   int device;                /* CUDA device ordinal the context lives on; -1 = current */
-  int io_type;               /* RQ_F16, or RQ_BF16 (RQ_FP8 only): every q, k, v and out of the context */
+  int io_type;               /* RQ_F16 (0), or RQ_BF16 (RQ_FP8 only): every q, k, v and out of the context */
 } rq_config;
 
 /* Source: this library (the constructor of the context that rq_free releases); the tables it holds
    are the rotations of README > Core Features > RotorQuant / TurboQuant KV Cache Compression and
    the Lloyd-Max codebook named in its Acknowledgments (TurboQuant entry). Validates cfg, copies the
-   rotation tables and codebook to the device and allocates the split-K workspace on cfg->device.
+   rotation tables and codebook to the device and allocates the split-K workspace on cfg->device
+   (RQ_FP8: 266 KB an SM, 40 MB).
    On success *out is a new context; on failure *out is NULL and nothing stays allocated.  Errors:
    RQ_ERR_INVALID, RQ_ERR_UNSUPPORTED, RQ_ERR_CUDA. */
 int rq_create(rq_ctx **out, const rq_config *cfg);
@@ -191,7 +193,8 @@ int rq_quantize_append(rq_ctx *ctx, const void *k, const void *v, const int32_t 
  *   block_table device int32 [B][max_pages]
  *   seq_lens    device int32 [B]: tokens of sequence b, all attended (0 gives zeros)
  *   out         device fp16 [B][Hq][head_dim]; head hq reads kv head hq / (Hq / Hkv)
- * out = softmax(sm_scale * q K^T) V over the dequantised cache.  B may be 0.  q, kv_pages and
+ * out = softmax(sm_scale * q K^T) V over the dequantised cache (RQ_FP8: a row whose scores are all
+ * minus infinity is NaN; one that sees no token is 0).  B may be 0.  q, kv_pages and
  * out must be 16-byte aligned (this and every attention entry point below).
  * Errors: RQ_ERR_INVALID (also a misaligned q, kv_pages or out), RQ_ERR_CAPACITY (B > max_batch, max_pages > max_pages_per_seq),
  * RQ_ERR_CUDA.
@@ -210,10 +213,12 @@ int rq_decode_attention(rq_ctx *ctx, const void *q, const void *kv_pages, const 
  * dequantized tile of the cache; tensor-core QK^T and PV).  Planar and iso rotations use no
  * workspace: T is limited only by the q / out buffers, not by max_query_tokens.  A dense rotation
  * (RQ_DENSE) rotates the queries into the context's workspace first, so there T must not exceed
- * max_query_tokens (RQ_ERR_CAPACITY otherwise).
+ * max_query_tokens (RQ_ERR_CAPACITY otherwise).  RQ_FP8 joins a row block's parts in the context's
+ * workspace, whatever T is; calls with B * T * Hq * max_pages * P up to 2^23 share the kernel of
+ * rq_verify_attention.
  *   q   device fp16 [B][T][Hq][head_dim],   out device fp16 [B][T][Hq][head_dim]
  * Other arguments as rq_verify_attention.  Errors as rq_verify_attention (except that T above
- * max_query_tokens is allowed for planar and iso rotations).
+ * max_query_tokens is allowed for planar and iso rotations and RQ_FP8).
  */
 int rq_extend_attention(rq_ctx *ctx, const void *q, int T, const void *kv_pages, const int32_t *block_table,
                         int max_pages, const int32_t *seq_lens, int B, void *out, int32_t *d_status,
@@ -234,8 +239,8 @@ int rq_extend_attention(rq_ctx *ctx, const void *q, int T, const void *kv_pages,
  * The result equals rq_quantize_append of the tokens followed by rq_decode_attention (the same
  * bytes written, the same output).  A dense rotation (RQ_DENSE) codes the new tokens in the
  * launch that rotates the queries, before the split-K kernel (which applies the output
- * rotation itself): two launches instead of four.  RQ_FP8 appends in a launch of its own.  A page id out of range for the new token sets RQ_STATUS_BAD_PAGE
- * and skips its write.  Errors as rq_decode_attention, plus RQ_ERR_INVALID for a NULL or
+ * rotation itself): two launches instead of four.  RQ_FP8 appends in a launch of its own.  A page
+ * id out of range for the new token sets RQ_STATUS_BAD_PAGE and skips its write.  Errors as rq_decode_attention, plus RQ_ERR_INVALID for a NULL or
  * non-16-byte-aligned k_new / v_new.
  */
 int rq_decode_step(rq_ctx *ctx, const void *q, const void *k_new, const void *v_new, void *kv_pages,
@@ -349,7 +354,8 @@ typedef struct {
 
 /*
  * Source: this library.  The norm and rotation of n tokens' query and key rows in one launch.
- *   rope       NULL: norms only.  It must live on the current device (as must every pointer).
+ *   rope       NULL: norms only, on the current device; else the call runs on the rope's device.
+ *              Every pointer must be of that device
  *   q, k       either may be NULL, not both
  *   io_type    RQ_F16 or RQ_BF16: element type of x and out
  *   positions  device int32 [num_axes][n]; negative positions turn the other way; unused (may be

@@ -162,6 +162,7 @@ int create_block(rq_ctx* ctx, const rq_config* cfg) {
   cudaError_t e = cudaMalloc(&ctx->d_ws, ctx->ws_floats * sizeof(float));
   if (e == cudaSuccess) e = cudaMalloc(&ctx->d_frag, counters * sizeof(int));
   if (e == cudaSuccess) e = cudaMemset(ctx->d_frag, 0, counters * sizeof(int));  // as every launch leaves them
+  if (e == cudaSuccess) e = cudaStreamSynchronize(nullptr);  // a non-blocking stream's first call would not wait for it
   if (e == cudaSuccess) e = rq::block_attention_prepare();
   if (e == cudaSuccess) e = rq::block_extend_prepare();
   if (e != cudaSuccess) {
@@ -725,6 +726,7 @@ int rq_rope_create(rq_rope** out, const rq_rope_config* cfg) {
   if (!r) return RQ_ERR_CUDA;
   cudaError_t e = cudaMalloc(&r->d_pairs, sizeof(host));
   if (e == cudaSuccess) e = cudaMemcpy(r->d_pairs, host, sizeof(host), cudaMemcpyHostToDevice);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(nullptr);  // the copy may still be on its way
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&r->num_sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) {
     cudaFree(r->d_pairs);

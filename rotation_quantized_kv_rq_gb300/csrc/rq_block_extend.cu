@@ -9,18 +9,23 @@
 // the cache in tiles of 128 tokens, its warps specialised and coupled through mbarriers:
 //   softmax (warps 0-7, a thread per row): reads its row of S from tensor memory 64 columns at a
 //     time, applies scales and mask, writes fp16 weights over S;
-//   codes (warps 8-11): widen a tile's key and value codes (exact) into fp16 operands;
-//   MMA (warp 12 + b for block b): O_b += W_b V(t) and behind it S_b(t + 1) = Q_b K(t + 1)^T, one
-//     block on the tensor cores while the other is in its softmax.  A warp each, and few barriers: a
-//     commit costs about 50 cycles and a wait for a barrier that is ready 120;
-//   copies (warp 14): a block is one 4112-byte bulk copy into a ring, page ids looked up 8 half
-//     tiles ahead.
-// (Warp 15 only fills the warpgroup: 16 warps have 128 registers a thread, 17 would have 96.)
+//   codes (warps 8-11): widen a tile's key and value codes (exact) into fp16 operands, keys in two
+//     stages, values in one;
+//   MMA (warp 12): for each block in turn O_b += W_b V(t) and behind it S_b(t + 1) = Q_b K(t + 1)^T, so
+//     that one block is on the tensor cores while the other is in its softmax.  All of it in one warp
+//     with uniform operands and an elected lane: an MMA takes 16 to 22 cycles to issue so, 50 in a
+//     branch of one lane;
+//   copies (warp 13): a block is one 4112-byte bulk copy into a ring of two tiles, page ids looked up
+//     8 half tiles ahead.
+// (Warps 14 and 15 only fill the warpgroup: 16 warps have 128 registers a thread.)
 // Why these shapes: an MMA with N = 64 takes as long as one with N = 128 (64.5 and 65.5 cycles for M =
-// 128, K = 16, A in tensor memory; 78.7 for both with A in shared memory), so S is 128 columns wide.
-// That fills tensor memory (O 2 x 128 columns, S 2 x 128 with W over it) and puts Q into shared memory.
-// Shared memory then moves 322 KB a tile (Q and K into the MMAs twice, V twice, codes in and out,
-// operands in), 2516 cycles at 128 bytes, against 2308 of MMAs.
+// 128, K = 16, A in tensor memory), so S is 128 columns wide.  That fills tensor memory (O 2 x 128
+// columns, S 2 x 128 with W over it) and puts Q into shared memory.  A tile is 32 MMAs, 2064 cycles
+// measured alone; 8 x 1,024 rows over 15K take 1.81 ms, 1,180 TFLOP/s, 62% of the burst rate of a
+// large matrix product and 69% of its sustained rate.  What is left is the softmax between a block's S
+// and its W: two passes over 128 scores a thread, beside which the tensor cores have one other block.
+// Measured and slower: the two blocks' softmaxes kept in turns 3.0 ms (2.1 with turns of half a
+// tile), 16 softmax warps of 80 registers 2.9, an MMA warp for each block 2.5, 32 columns at a time.
 // The order of tokens inside a half tile of 64 is free as long as S's columns and V's rows agree.  It
 // is the one in which the cache holds values: column 32 p + 8 t + 4 b + i is token {2t, 2t + 1, 2t + 8,
 // 2t + 9}[i] of block 2 p + b, so that a thread's 16 bytes of two blocks' value codes become four

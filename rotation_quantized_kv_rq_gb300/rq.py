@@ -418,7 +418,7 @@ class Rope:
         if inv_freq is None:
             inv_freq = base ** (-2.0 * np.arange(pairs, dtype=np.float64) / max(rotary_dim, 1))
         if sections is not None:
-            if axis is not None or sum(sections) != pairs or min(sections) < 0:
+            if axis is not None or sum(sections) != pairs or min(sections, default=-1) < 0:
                 raise RQError("rq_rope_create", RQ_ERR_INVALID)
             axis = np.repeat(np.arange(len(sections)), sections)
         self.num_axes = len(sections) if sections is not None else 1 if axis is None else int(np.max(axis, initial=0)) + 1
