@@ -587,6 +587,108 @@ def test_a_model_s_steps_together():
         check(cache2, table, ln, qs[:, None].clone(), outs[:, None], lambda b, j, p: p <= ln[b] - 1, f"step {i}")
 
 
+def test_long_appends_equal_short_ones():
+    """Three sequences of 8,229 tokens in one call, their starts inside blocks, against calls that end at
+    block ends: the same bytes, and the queries as Rope.apply turns them."""
+    rng, hq, hkv, P = gen(31), 5, 2, 32
+    n, starts = [5003, 9, 3217], [7, 0, 21]
+    per = 5024 // P + 1
+    a, b = (make(hkv, hkv, P, 3 * per, torch.bfloat16) for _ in range(2))
+    table = rng.permutation(3 * per).reshape(3, per)
+    pos = np.concatenate([np.arange(s, s + m) for s, m in zip(starts, n)])
+    seq = np.repeat(np.arange(3), n)
+    slots = (table[seq, pos // P] * P + pos % P).astype(np.int32)
+    q, k, v = fused(rng, sum(n), hq, hkv, torch.bfloat16)
+    rope, w = rq.Rope(128), dev((1 + 0.2 * rng.standard_normal(128)).astype(np.float32))
+    d_pos, d_slots = dev(pos.astype(np.int32)), dev(slots)
+    out = a.append_rope(k, v, d_slots, rope, d_pos, q=q, q_weight=w, k_weight=w)
+    assert torch.equal(out, rope.apply(q, None, d_pos, q_weight=w)[0])
+    at = 0
+    while at < len(pos):
+        to = min(at + 1000, len(pos))
+        while to < len(pos) and pos[to] % 16 and seq[to] == seq[to - 1]:
+            to -= 1
+        part = b.append_rope(k[at:to], v[at:to], d_slots[at:to], rope, d_pos[at:to], q=q[at:to], q_weight=w, k_weight=w)
+        assert torch.equal(part, out[at:to])
+        at = to
+    assert torch.equal(a.pages, b.pages) and int(a.status.item()) == 0
+
+
+def test_tokens_of_many_sequences():
+    """One token each of 2,500 sequences, in one call of either kind and in calls of 100."""
+    rng, B = gen(32), 2500
+    caches = [make(1, 1, 16, B, torch.float16, batch=B) for _ in range(3)]
+    off = rng.integers(0, 16, B)
+    slots = (rng.permutation(B) * 16 + off).astype(np.int32)
+    lens = np.where(np.arange(B) % 7 == 3, 0, off + 1).astype(np.int32)
+    first = [dev(rng.standard_normal((16 * B, 1, 128)), torch.float16) for _ in range(2)]
+    k, v = (dev(rng.standard_normal((B, 1, 128)) * 2.0 ** rng.integers(-4, 5, (B, 1, 1)), torch.float16) for _ in range(2))
+    q = dev(rng.standard_normal((B, 1, 128)), torch.float16)
+    table = dev((slots // 16)[:, None].astype(np.int32))
+    given = dev(np.where(lens > 0, slots, -1).astype(np.int32))
+    for c in caches:
+        c.append(*first, torch.arange(16 * B, dtype=torch.int32, device="cuda"))
+    caches[0].append(k, v, given)
+    out = caches[1].decode_step(q, k, v, table, dev(lens))
+    for i in range(0, B, 100):
+        caches[2].append(k[i:i + 100].contiguous(), v[i:i + 100].contiguous(), given[i:i + 100].contiguous())
+    assert torch.equal(caches[0].pages, caches[2].pages) and torch.equal(caches[1].pages, caches[2].pages)
+    assert torch.equal(out, caches[0].decode(q, table, dev(lens)))
+    check(caches[0], table.cpu().numpy(), lens, q[:, None], out[:, None], lambda b, j, p: p <= lens[b] - 1, "decode")
+
+
+@pytest.mark.parametrize("B,T,hq", [(700, 1, 8), (300, 2, 8)])
+def test_many_sequences(B, T, hq):
+    rng = gen(B)
+    lens = np.where(rng.random(B) < 0.1, 0, rng.integers(T, 300, B))
+    cache, table, lens = filled(rng, hq, 1, 32, lens, torch.bfloat16, t=T)
+    q = dev(rng.standard_normal((B, T, hq, 128)), torch.bfloat16)
+    check(cache, table, lens, q, cache.verify(q, dev(table), dev(lens)), lambda b, j, p: p <= lens[b] - T + j, "verify")
+
+
+def test_many_rows_of_a_kv_head():
+    rng = gen(33)  # 64 drafts x 64 heads of one kv head: 512 groups of 8 rows
+    cache, table, lens = filled(rng, 64, 1, 16, [64, 333], torch.float16, t=64)
+    q = dev(rng.standard_normal((2, 64, 64, 128)), torch.float16)
+    check(cache, table, lens, q, cache.verify(q, dev(table), dev(lens)), lambda b, j, p: p <= lens[b] - 64 + j, "verify")
+
+
+def test_two_contexts_at_once():
+    """Calls of two contexts on two streams, eagerly and replayed from two graphs."""
+    sets = []
+    for i in range(2):
+        cache, table, lens = filled(gen(40 + i), 16, 4, 16, [3000, 70 + i, 1200], torch.bfloat16, t=9, width=300)
+        q = dev(gen(42 + i).standard_normal((3, 9, 16, 128)), torch.bfloat16)
+        calls = [lambda o, c=cache, a=(q, dev(table), dev(lens)): c.verify(*a, out=o),
+                 lambda o, c=cache, a=(q.repeat(1, 60, 1, 1)[:, :70].contiguous(), dev(table), dev(lens)): c.extend(*a, out=o)]
+        outs = [torch.empty((3, t, 16, 128), dtype=torch.bfloat16, device="cuda") for t in (9, 70)]
+        for call, o in zip(calls, outs):
+            call(o)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        again = [torch.empty_like(o) for o in outs]
+        with torch.cuda.graph(graph):
+            for call, o in zip(calls, again):
+                call(o)
+        sets.append((calls, outs, again, graph, torch.cuda.Stream()))
+    for replay in (False, True):
+        for calls, outs, again, graph, stream in sets:
+            for o in again:
+                o.zero_()
+            stream.wait_stream(torch.cuda.current_stream())
+        for _ in range(10):
+            for calls, outs, again, graph, stream in sets:
+                with torch.cuda.stream(stream):
+                    if replay:
+                        graph.replay()
+                    else:
+                        for call, o in zip(calls, again):
+                            call(o)
+        torch.cuda.synchronize()
+        for calls, outs, again, graph, stream in sets:
+            assert all(torch.equal(a, o) for a, o in zip(again, outs))
+
+
 def test_offsets_past_32_bits():
     """Pages past 4 GiB of the pool: append, then decode and extend over them."""
     hkv, P, pages = 8, 256, 8300  # 526 KB a page of all heads
