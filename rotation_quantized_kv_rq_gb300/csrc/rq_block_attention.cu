@@ -27,7 +27,10 @@
 // each warp; the rounds of all units in order are cut into one range per CTA, on the device from
 // seq_lens.  A unit that spans ranges is joined by the last of its CTAs to finish, in the order of
 // the ranges (the result does not depend on which came last).  A CTA has at most two such
-// fragments, its first and its last, so the workspace is two slots and one counter a CTA.  Short
+// fragments, its first and its last, so the workspace is two slots and one counter a CTA.  Where up to
+// 32 sequences have no more units than CTAs, ranges that lie in one unit each are taken instead, if they
+// are at most 6 rounds longer (us: 4 x 4K + 6 rows x 4 heads 23.9 -> 19.7, 1 x 16K + 8 x 8 28.4 -> 23.0,
+// 8 x 4K decode 19.4 -> 16.5; 8 x 16K + 6, where they are 10 longer, 69 -> 70 for the search).  Short
 // calls are chains of memory latencies (0.6 us each), so what can load together does: a fragment's
 // page ids with its queries, the parts to join by bulk copies of a chunk at once.
 #include <math_constants.h>
@@ -46,6 +49,7 @@ using namespace block;
 
 constexpr float kMargin = 8.f;      // log2 slack of the running maximum
 constexpr float kNone = -3.402823466e38f;  // running maximum before any visible token: no finite score is below
+constexpr int kOpening = 6;         // rounds that a CTA's second fragment costs (opening, joining), about
 constexpr int kRowStride = 132;     // floats per joined row (128 and padding)
 
 constexpr int kRowBytes = kRowStride * 4;  // a joined row: 128 sums, the maximum, the weights' sum
@@ -107,10 +111,11 @@ struct Plan {
   int tiles, rounds;
 };
 template <int W>
-__device__ __forceinline__ Plan plan_of(int len) {
+__device__ __forceinline__ Plan plan_of(int len, int step = 1) {
   Plan p;
   p.tiles = (len + kBlockTokens - 1) / kBlockTokens;
   p.rounds = max(1, (p.tiles + W - 1) / W);  // an empty sequence's rows are written too
+  if (step > 1) p.rounds = (p.rounds + step - 1) / step * step;
   return p;
 }
 
@@ -120,7 +125,7 @@ __global__ void __launch_bounds__(32 * W, warps_per_sm(NT) / W) splitk_kernel(co
   constexpr int kLens = 32 * W;  // sequences whose lengths are kept
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ long long s_sum[W], s_begin;  // rounds per warp's sequences; first sequence's rounds before it
-  __shared__ int s_seq, s_last, s_len[kLens];
+  __shared__ int s_seq, s_last, s_len[kLens], s_parts;  // s_parts: ranges of the launch
   __shared__ float s_m[W][kRows], s_l[W][kRows];
   __shared__ uint4 s_q[NT > 1 ? NT * 4 * 32 : 1];  // query fragments [n][ks / 2][lane], the same in every warp
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, gq = lane >> 2, tq = lane & 3;
@@ -137,14 +142,6 @@ __global__ void __launch_bounds__(32 * W, warps_per_sm(NT) / W) splitk_kernel(co
   };
   auto length = [&](int b) { return a.B <= kLens ? s_len[b] : load_length(b, false); };
 
-  // ---- the CTA's range of rounds ----
-  const int chunk = (a.B + kThreads - 1) / kThreads;
-  long long mine = 0;
-  for (int b = tid * chunk; b < min(a.B, (tid + 1) * chunk); ++b) {
-    const int len = load_length(b, blockIdx.x == 0);
-    if (b < kLens) s_len[b] = len;
-    mine += plan_of<W>(len).rounds;
-  }
   const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem) + warp * S * kBlockBytes;
   const uint32_t bars = (uint32_t)__cvta_generic_to_shared(smem) + W * S * kBlockBytes + warp * S * 8;
   const uint32_t join_bar = (uint32_t)__cvta_generic_to_shared(smem) + W * S * (kBlockBytes + 8);
@@ -153,41 +150,95 @@ __global__ void __launch_bounds__(32 * W, warps_per_sm(NT) / W) splitk_kernel(co
     if (warp == 0) tc::mbar_init(join_bar, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  long long upto = mine;  // inclusive scan over the threads
+
+  // ---- the CTA's range of rounds ----
+  long long total, at;
+  int b, step = 1;
+  auto part_begin = [&](long long c) { return c * total / s_parts; };
+  auto part_of = [&](long long x) { return ((x + 1) * s_parts - 1) / total; };  // the range that holds round x
+  long long x;
+  if (a.B <= 32) {  // a lane has a sequence, in every warp alike: no barrier before the first copies
+    const int len = lane < a.B ? load_length(lane, blockIdx.x == 0 && warp == 0) : 0;
+    s_len[lane] = len;  // (all warps write the same)
+    int r = lane < a.B ? plan_of<W>(len).rounds : 0;
+    total = (long long)__reduce_add_sync(0xffffffffu, r) * per_seq;
+    // A range that crosses into a second unit opens and joins twice.  Ranges of `step` rounds, each in
+    // one unit, if they are not longer by more than that costs (and there is not work for long).
+    int parts = 0;
+    if (a.B * per_seq <= (int)gridDim.x && total > gridDim.x && total < 1 << 18) {
+      const uint32_t even = ((uint32_t)total + gridDim.x - 1) / gridDim.x;
+      const uint32_t recip = 0xFFFFFFFFu / (even + (lane & 7)) + 1;  // n / d is exact so for n d < 2^32
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long v = __shfl_up_sync(0xffffffffu, upto, o);
-    if (lane >= o) upto += v;
-  }
-  if (lane == 31) s_sum[warp] = upto;
-  __syncthreads();
-  long long total = 0;
-#pragma unroll
-  for (int w = 0; w < W; ++w) {
-    if (w == warp) upto += total;
-    total += s_sum[w];
-  }
-  total *= per_seq;
-  const long long parts = min((long long)gridDim.x, total);
-  if ((long long)blockIdx.x >= parts) return;
-  auto part_begin = [&](long long c) { return c * total / parts; };
-  auto part_of = [&](long long x) { return ((x + 1) * parts - 1) / total; };  // the range that holds round x
-  long long x = part_begin(blockIdx.x);
-  const long long end = part_begin(blockIdx.x + 1ll);
-  if (x >= (upto - mine) * per_seq && x < upto * per_seq) {
-    long long at = (upto - mine) * per_seq;
-    int b = tid * chunk;
-    for (; chunk > 1; ++b) {
-      const long long r = (long long)plan_of<W>(length(b)).rounds * per_seq;
-      if (x < at + r) break;
-      at += r;
+      for (int k = kOpening; k >= 0; --k) {
+        const uint32_t rec = __shfl_sync(0xffffffffu, recip, k), up = r + even + k - 1;
+        const int pieces = __reduce_add_sync(0xffffffffu, even + k == 1 ? up : __umulhi(up, rec)) * per_seq;
+        if (pieces <= (int)gridDim.x) step = even + k, parts = pieces;
+      }
     }
-    s_begin = at;
-    s_seq = b;
+    if (step > 1) {
+      r = (r + step - 1) / step * step;
+      total = (long long)parts * step;
+      if ((int)blockIdx.x >= parts) return;
+      x = (long long)blockIdx.x * step;
+    } else {
+      parts = (int)min((long long)gridDim.x, total);
+      if ((int)blockIdx.x >= parts) return;
+      x = blockIdx.x * total / parts;
+    }
+    s_parts = parts;
+    __syncwarp();
+    int upto = r;  // inclusive scan
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += v;
+    }
+    b = __ffs(__ballot_sync(0xffffffffu, x < (long long)upto * per_seq)) - 1;
+    at = (long long)__shfl_sync(0xffffffffu, upto - r, b) * per_seq;
+  } else {
+    const int chunk = (a.B + kThreads - 1) / kThreads;
+    long long mine = 0;
+    for (int i = tid * chunk; i < min(a.B, (tid + 1) * chunk); ++i) {
+      const int len = load_length(i, blockIdx.x == 0);
+      if (i < kLens) s_len[i] = len;
+      mine += plan_of<W>(len).rounds;
+    }
+    long long upto = mine;  // inclusive scan over the threads
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long v = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += v;
+    }
+    if (lane == 31) s_sum[warp] = upto;
+    __syncthreads();
+    total = 0;
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      if (w == warp) upto += total;
+      total += s_sum[w];
+    }
+    total *= per_seq;
+    const int parts = (int)min((long long)gridDim.x, total);
+    if ((int)blockIdx.x >= parts) return;
+    s_parts = parts;
+    __syncwarp();
+    x = part_begin(blockIdx.x);
+    if (x >= (upto - mine) * per_seq && x < upto * per_seq) {
+      long long begin = (upto - mine) * per_seq;
+      int i = tid * chunk;
+      for (; chunk > 1; ++i) {
+        const long long r = (long long)plan_of<W>(length(i)).rounds * per_seq;
+        if (x < begin + r) break;
+        begin += r;
+      }
+      s_begin = begin;
+      s_seq = i;
+    }
+    __syncthreads();
+    at = s_begin;
+    b = s_seq;
   }
-  __syncthreads();
-  long long at = s_begin;
-  int b = s_seq;
+  const long long end = step > 1 ? x + step : part_begin(blockIdx.x + 1ll);
 
   const uint32_t s_q_addr = (uint32_t)__cvta_generic_to_shared(s_q) + 16 * lane;
   uint32_t issued = 0, done = 0;  // tiles of this warp so far: ring positions and parities
@@ -196,7 +247,7 @@ __global__ void __launch_bounds__(32 * W, warps_per_sm(NT) / W) splitk_kernel(co
   while (x < end) {
     // ---- the fragment: rounds r0 .. r1 - 1 of unit u of sequence b ----
     const int len = length(b);
-    const Plan pl = plan_of<W>(len);
+    const Plan pl = plan_of<W>(len, step);
     const int u = (int)((x - at) / pl.rounds), r0 = (int)((x - at) % pl.rounds);
     const int r1 = (int)min((long long)pl.rounds, r0 + (end - x));
     const int h = u / groups, row0 = (u % groups) * kRows;
