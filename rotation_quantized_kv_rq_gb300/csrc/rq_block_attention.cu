@@ -360,7 +360,8 @@ __global__ void __launch_bounds__(32 * W, warps_per_sm(NT) / W) splitk_kernel(co
       }
       ++done;
       const int t0 = (first + W * i) * kBlockTokens;
-      const bool tail = t0 + kBlockTokens - 1 > len - a.T;  // rows see different parts of the tile
+      // rows see different parts of the tile: draft 0 is every chain row's, but a tree row's only by its bit
+      const bool tail = t0 + kBlockTokens - 1 > len - a.T - (a.tree_mask ? 1 : 0);
       uint32_t exps;
       asm volatile("ld.shared.u16 %0, [%1];" : "=r"(exps) : "r"(tile + kExps));
       const float ks = pow2(exp_of_byte(exps & 0xFF));
