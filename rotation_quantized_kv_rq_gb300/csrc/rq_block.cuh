@@ -66,5 +66,30 @@ __device__ __forceinline__ int exp_of(float amax) {
 __device__ __forceinline__ int exp_of_byte(uint32_t byte) { return min(max((int)byte - 127, kMinExp), kMaxExp); }
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }  // |e| <= 126
 
+// A query row as an fp16 operand is the row times `down`; its scores are the products times `factor` times a
+// block's key scale.  A bf16 row is brought by a power of two to a largest magnitude `top` of 2^14 .. 2^15, an
+// fp16 row (BF16 false) is taken as it is; sm: the softmax scale times log2(e).
+// factor is at least 2^-66, so that with a key scale (2^-60 at least) it stays above 0 in f32: a score that the
+// mask made minus infinity has to stay that, and a row of zeros over keys of zeros would come to -inf * 0.
+// For smaller rows the operand is smaller instead.  It is then off by 2^-25 at most, which moves a score by
+// 2^-25 * 448 * 128 * 2^-65 * 2^60 < 2^-14 at the largest key scale there is (2^60), 2^-66 at 2^8.
+// (An fp16 row meets the bound only below sm = 2^-66, where its scores come to 2^-26 at most either way.)
+struct RowScale {
+  float down, factor;
+};
+template <bool BF16>
+__device__ __forceinline__ RowScale row_scale(float top, float sm) {
+  constexpr int kLeast = -66;
+  RowScale r{1.f, sm};
+  if (BF16) {
+    const int least = kLeast + 14 + 127 - (int)(__float_as_uint(sm) >> 23);
+    const int e = min(max((int)(__float_as_uint(top) >> 23) - 127, max(least, -100)), 127);
+    r.down = pow2(14 - e);
+    r.factor *= pow2(e - 14);
+  }
+  r.factor = fmaxf(r.factor, pow2(kLeast));
+  return r;
+}
+
 }  // namespace block
 }  // namespace rq

@@ -301,9 +301,9 @@ __global__ void __launch_bounds__(32 * W, warps_per_sm(NT) / W) splitk_kernel(co
     int lim[NT][2];   // last visible position of those columns' rows
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      float f = g.sm_scale * 1.44269504088896340736f;
-      if constexpr (!std::is_same<T, __half>::value) {
-        float top = 0.f;
+      constexpr bool kBf16 = !std::is_same<T, __half>::value;
+      float top = 0.f;
+      if constexpr (kBf16) {
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           const float2 v = rope::unpack2<T>(word(raw[n][i >> 2], i & 3));
@@ -311,13 +311,13 @@ __global__ void __launch_bounds__(32 * W, warps_per_sm(NT) / W) splitk_kernel(co
         }
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        const int e = min(max((int)(__float_as_uint(top) >> 23) - 127, -100), 127);
-        const float down = pow2(14 - e);  // the row's largest magnitude to 2^14 .. 2^15
-        f *= pow2(e - 14);
+      }
+      const RowScale scale = row_scale<kBf16>(top, g.sm_scale * 1.44269504088896340736f);
+      if constexpr (kBf16) {
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           const float2 v = rope::unpack2<T>(word(raw[n][i >> 2], i & 3));
-          qf[n][i >> 1][i & 1] = rope::pack2<__half>(v.x * down, v.y * down);
+          qf[n][i >> 1][i & 1] = rope::pack2<__half>(v.x * scale.down, v.y * scale.down);
         }
       } else {
 #pragma unroll
@@ -325,7 +325,7 @@ __global__ void __launch_bounds__(32 * W, warps_per_sm(NT) / W) splitk_kernel(co
       }
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        qs[n][c] = __shfl_sync(0xffffffffu, f, 4 * (2 * tq + c));
+        qs[n][c] = __shfl_sync(0xffffffffu, scale.factor, 4 * (2 * tq + c));
         lim[n][c] = len - a.T + (row0 + 8 * n + 2 * tq + c) / g.group;
       }
     }

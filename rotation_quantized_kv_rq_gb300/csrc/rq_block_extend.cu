@@ -309,7 +309,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const Geometry g, c
     // softmax: row block, row in it (= lane of tensor memory), query row
     const int blk = warp >> 2 & 1, brow = 32 * (warp & 3) + lane, row = ms.f.rb * kRows + kHalf * blk + brow;
     const bool valid = row < a.rows;
-    float q_scale = g.sm_scale * 1.44269504088896340736f, m_run = kNone, l_run = 0.f;
+    float q_scale = 0.f, m_run = kNone, l_run = 0.f;
     auto row_offset = [&]() {
       const int j = valid ? row / g.group : 0, head = h * g.group + (valid ? row % g.group : 0);
       return (((size_t)b * a.T + j) * g.num_q_heads + head) * kHeadDim;
@@ -319,9 +319,9 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const Geometry g, c
     // (the keys' and values' roles start meanwhile; the MMAs wait for q_full)
     if (warp < kSoftWarps) {
       const uint4* src = reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(a.q) + row_offset());
-      float down = 1.f;
-      if constexpr (!std::is_same<T, __half>::value) {
-        float top = 0.f;
+      constexpr bool kBf16 = !std::is_same<T, __half>::value;
+      float top = 0.f;
+      if constexpr (kBf16) {
 #pragma unroll
         for (int c = 0; c < 16; ++c) {
           const uint4 v = valid ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
@@ -331,10 +331,9 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const Geometry g, c
             top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
           }
         }
-        const int e = min(max((int)(__float_as_uint(top) >> 23) - 127, -100), 127);
-        down = pow2(14 - e);
-        q_scale *= pow2(e - 14);
       }
+      const RowScale scale = row_scale<kBf16>(top, g.sm_scale * 1.44269504088896340736f);
+      q_scale = scale.factor;
 #pragma unroll 8
       for (int c = 0; c < 16; ++c) {
         const uint4 v = valid ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
@@ -342,9 +341,9 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const Geometry g, c
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           w[k] = word(v, k);
-          if constexpr (!std::is_same<T, __half>::value) {
+          if constexpr (kBf16) {
             const float2 f = rope::unpack2<T>(w[k]);
-            w[k] = rope::pack2<__half>(f.x * down, f.y * down);
+            w[k] = rope::pack2<__half>(f.x * scale.down, f.y * scale.down);
           }
         }
         sts128(q_ops + 32768 * blk + 16384 * (c >> 3) + sw128(brow, c & 7), w[0], w[1], w[2], w[3]);

@@ -4,8 +4,9 @@ import numpy as np
 import pytest
 import torch
 
+from rotation_quantized_kv_rq_gb300 import rq
 from tests import block_ref as R
-from tests.test_block_gpu import DT, check, dev, filled, gen
+from tests.test_block_gpu import DT, check, dev, filled, gen, wide
 
 pytestmark = pytest.mark.gpu
 
@@ -43,3 +44,47 @@ def test_tree_mask_of_the_first_draft(dtype, T, hq, hkv):
     blind = torch.from_numpy(without).cuda()
     assert torch.equal(again[blind], out[blind])
     assert torch.isnan(again[~blind]).all()
+
+
+CALLS = ["decode", "verify", "tree", "extend", "extend, own kernel"]
+
+
+@pytest.mark.parametrize("dtype,sm_scale", [("bf16", 0.0), ("f16", 0.0), ("f16", 1e-30), ("bf16", 1e-30)])
+@pytest.mark.parametrize("values", [False, True])
+@pytest.mark.parametrize("call", CALLS)
+def test_zero_queries_over_zero_keys(call, values, dtype, sm_scale):
+    """The product of the factors of a score (of the query row, of the softmax, of the keys' block) can be
+    below f32's range: what a row may not see keeps no weight all the same, and what it sees has equal
+    weights.  values: keys of zeros were appended with values; else a pool of zeros as it is made."""
+    dtype, rng, P, hq, hkv = DT[dtype], gen(50), 16, 4, 2
+    T = 1 if call == "decode" else 3
+    lens = np.array([1, 15, 17, 0, 40, 300], np.int32)
+    need = (lens + P - 1) // P
+    width = max(int(need.max()), wide(len(lens), T, hq, P) if "own" in call else 0)
+    table = np.zeros((len(lens), width), np.int32)
+    for b, at in enumerate(np.cumsum(need) - need):
+        table[b, :need[b]] = np.arange(at, at + need[b])
+    cache = rq.KVCache(rq.RQ_FP8, 8, hq, hkv, P, int(need.sum()), None, None, max_batch=len(lens), max_query_tokens=T,
+                       max_pages_per_seq=width, sm_scale=sm_scale, dtype=dtype)
+    lens = np.where((lens > 0) & (lens < T), T, lens).astype(np.int32)  # (a sequence holds its query tokens)
+    if values:
+        for b, L in enumerate(lens):
+            if L:
+                pos = np.arange(L)
+                v = dev(rng.standard_normal((L, hkv, 128)), dtype)
+                cache.append(torch.zeros_like(v), v, dev((table[b, pos // P] * P + pos % P).astype(np.int32)))
+    q = torch.zeros((len(lens), T, hq, 128), dtype=dtype, device="cuda")
+    args = dev(table), dev(lens)
+    if call == "decode":
+        out = cache.decode(q[:, 0].contiguous(), *args)[:, None]
+    elif call == "tree":
+        out = cache.tree_verify(q, torch.tensor([[1, 3, 5]] * len(lens), device="cuda"), *args)
+    else:
+        out = (cache.verify if call == "verify" else cache.extend)(q, *args)
+
+    def see(b, j, p):
+        i = p - (lens[b] - T)
+        return i <= (0, 1, 2)[j] if call != "tree" else (i < 0) | ((1, 3, 5)[j] >> np.maximum(i, 0) & 1).astype(bool)
+    check(cache, table, lens, q, out, see, call)
+    if not values:
+        assert (out == 0).all()
