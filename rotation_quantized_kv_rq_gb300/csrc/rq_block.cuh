@@ -66,6 +66,14 @@ __device__ __forceinline__ int exp_of(float amax) {
 __device__ __forceinline__ int exp_of_byte(uint32_t byte) { return min(max((int)byte - 127, kMinExp), kMaxExp); }
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }  // |e| <= 126
 
+// The softmax weights, rounded to fp16 for their product with the values: 2^(score + EV - m), where m is a
+// running maximum of score + EV less kLift, moved where a score is past it by more than kReach.  So the largest
+// weight of a row stands between 2^kLift and 2^kReach, near the top of fp16's range, and its smallest steps,
+// 2^-24, are 2^-31 of it or less: a token below half of that is lost from the product (not from the
+// weights' sum), at most 2^-32 of the largest, 2^-12 for 2^20 such tokens, which is the rounding of the largest itself.
+constexpr float kLift = 7.f, kReach = 15.f;  // (a maximum of 2^26 and more, 8 apart, gives a lift of 8 or 0)
+constexpr float kNone = -3.402823466e38f;    // m before any visible token: no finite score is below
+
 // A query row as an fp16 operand is the row times `down`; its scores are the products times `factor` times a
 // block's key scale.  A bf16 row is brought by a power of two to a largest magnitude `top` of 2^14 .. 2^15, an
 // fp16 row (BF16 false) is taken as it is; sm: the softmax scale times log2(e).

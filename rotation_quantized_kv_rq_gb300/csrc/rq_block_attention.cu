@@ -6,10 +6,9 @@
 // fp16 (exact) as the A operands of m16n8k16 MMAs and f32 accumulators:
 //   S^T = code_K q^T;   t = S 2^EK sm_scale log2(e) + EV - m;   w = 2^t
 //   O^T += code_V^T w;   l += w 2^-EV;   out = O / l
-// The value scale is part of the weight's exponent, so codes are never multiplied by it, and m is
+// The value scale is part of the weight's exponent, so codes are never multiplied by it, and m follows
 // the running maximum of score + EV: w, rounded to fp16 for the MMA (2^-11 of it), is then largest
-// where a token weighs most in the output, whatever the scales.  m moves only past a margin of
-// 2^8.  Queries are fp16 as they are; a bf16 row is brought into fp16's range by a power of two.
+// where a token weighs most in the output, whatever the scales (its range: rq_block.cuh).  Queries are fp16 as they are; a bf16 row is brought into fp16's range by a power of two.
 //
 // What bounds it: the cache is read once, 257 bytes a (token, kv head), against 4 MMAs' worth of
 // work; so the design keeps copies in flight.  A block is one 4112-byte bulk copy into a ring of
@@ -47,8 +46,6 @@ namespace {
 
 using namespace block;
 
-constexpr float kMargin = 8.f;      // log2 slack of the running maximum
-constexpr float kNone = -3.402823466e38f;  // running maximum before any visible token: no finite score is below
 constexpr int kOpening = 6;         // rounds that a CTA's second fragment costs (opening, joining), about
 constexpr int kRowStride = 132;     // floats per joined row (128 and padding)
 
@@ -417,7 +414,7 @@ __global__ void __launch_bounds__(32 * W, warps_per_sm(NT) / W) splitk_kernel(co
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           t[n][c] = fmaf(s[n][c], qs[n][c & 1] * ks, fev);  // rounded once: t - m <= 0 for the m it gives, at any size
-          past = past || t[n][c] - m[n][c & 1] > kMargin;
+          past = past || t[n][c] - m[n][c & 1] > kReach;
         }
       }
       if (__any_sync(0xffffffffu, past)) {
@@ -428,7 +425,7 @@ __global__ void __launch_bounds__(32 * W, warps_per_sm(NT) / W) splitk_kernel(co
             float top = fmaxf(t[n][c], t[n][c + 2]);
 #pragma unroll
             for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-            const float m_new = fmaxf(m[n][c], top), alpha = ex2(m[n][c] - m_new);
+            const float m_new = fmaxf(m[n][c], top - kLift), alpha = ex2(m[n][c] - m_new);
             m[n][c] = m_new;
             l[n][c] *= alpha;
 #pragma unroll

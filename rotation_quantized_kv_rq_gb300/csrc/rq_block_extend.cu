@@ -61,8 +61,6 @@ constexpr int kKeyStages = 2, kRawStages = 4;  // K operands (tiles; V has one),
 constexpr uint32_t kOperand = 32768, kRawBytes = 4 * kBlockBytes;
 constexpr uint32_t kQBytes = 2 * 32768;
 constexpr int kScaleSlots = 4;      // tiles whose scales are kept
-constexpr float kMargin = 8.f;      // log2 slack of the running maximum
-constexpr float kNone = -3.402823466e38f;  // running maximum before any visible token: no finite score is below
 constexpr float kLarge = 1048576.f; // |maximum| from which weights are formed in two roundings
 constexpr int kMinTiles = 4;        // a CTA's least work, while there is enough
 constexpr uint32_t kColS = 256;     // tensor memory: O_b at 128 b, S_b at 256 + 128 b
@@ -403,11 +401,13 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const Geometry g, c
         highest(s, 1);
         load(s, 0);
         highest(s, 0);
-        if (__any_sync(0xffffffffu, top > (m_run == kNone ? -CUDART_INF_F : m_run + kMargin))) {
+        const float above = top - (m_run == kNone ? -CUDART_INF_F : m_run);  // (NaN where nothing is seen: no move)
+        if (__any_sync(0xffffffffu, above > kReach)) {
           float alpha = 1.f;
-          if (top > (m_run == kNone ? -CUDART_INF_F : m_run + kMargin)) {
-            alpha = ex2(m_run - top);
-            from = m_run = top;
+          if (above > kReach) {
+            from = top - kLift;
+            alpha = ex2(m_run - from);
+            m_run = from;
             l_run *= alpha;
           }
           if (t > 0) {  // O *= alpha (the warp's rows)

@@ -1,12 +1,14 @@
 """The 8-bit block-scaled cache where its calls can go wrong, on the GPU against the float64
 definitions of block_ref."""
+import math
+
 import numpy as np
 import pytest
 import torch
 
 from rotation_quantized_kv_rq_gb300 import rq
 from tests import block_ref as R
-from tests.test_block_gpu import DT, check, dev, filled, gen, wide
+from tests.test_block_gpu import DT, check, dev, filled, gen, host, wide, within
 
 pytestmark = pytest.mark.gpu
 
@@ -88,3 +90,25 @@ def test_zero_queries_over_zero_keys(call, values, dtype, sm_scale):
     check(cache, table, lens, q, out, see, call)
     if not values:
         assert (out == 0).all()
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("call", ["decode", "extend"])
+def test_a_long_flat_tail_beside_a_heavy_token(call, dtype):
+    """One token with a value of 0, and 2^17 with values of 1 whose weights are 2^-26 of its own: the result
+    is 2^-9.  Many sequences on the same pages, so that all of one is summed in few places.  A weight's
+    step is at most 2^-31 of the row's largest weight, half of which a token may lose."""
+    dtype, N, P = DT[dtype], 1 << 17, 256
+    B, hq, T = (640, 1, 1) if call == "decode" else (160, 64, 1)
+    cache = rq.KVCache(rq.RQ_FP8, 8, hq, 1, P, N // P + 1, None, None, max_batch=B, dtype=dtype)
+    k, v = torch.zeros((N + 1, 1, 128), dtype=dtype, device="cuda"), torch.ones((N + 1, 1, 128), dtype=dtype, device="cuda")
+    k[0, 0, 0], v[0] = 1, 0
+    cache.append(k, v, torch.arange(N + 1, dtype=torch.int32, device="cuda"))
+    q = torch.zeros((B, T, hq, 128), dtype=dtype, device="cuda")
+    q[..., 0] = 26 * math.log(2) * math.sqrt(128)
+    table = torch.arange(N // P + 1, dtype=torch.int32, device="cuda").repeat(B, 1)
+    lens = torch.full((B,), N + 1, dtype=torch.int32, device="cuda")
+    out = cache.decode(q[:, 0], table, lens)[:, None] if call == "decode" else cache.extend(q, table, lens)
+    tail = N * math.exp(-float(q[0, 0, 0, 0]) / math.sqrt(128))
+    ref = np.full(tuple(out.shape), tail / (1 + tail))
+    within(host(out), ref, N * 2.0 ** -32 + (2.0 ** -11 + 2.0 ** -20) * ref + R.half_step(dtype, ref) * (1 + 2.0 ** -8))
