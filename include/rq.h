@@ -56,7 +56,8 @@
  *                 dim d is byte ((r/8 * 2 + d/64) * 32 + r%8 * 4 + d%64/16) * 16 + d%16, its value
  *                 code byte 2048 + (d/32 * 32 + d/4%8 * 4 + r%8/2) * 16 + d%4 * 4 + r/8 * 2 + r%2.
  *                 A scale is 2^E with the smallest E in [-60, 60] for which the largest magnitude
- *                 is at most 448 * 2^E.  Appending a block's first token (offset a multiple of 16)
+ *                 is at most 448 * 2^E (60 if none is: larger ones are clipped and
+ *                 RQ_STATUS_NORM_OVERFLOW is set).  Appending a block's first token (offset a multiple of 16)
  *                 starts its scales anew from the tokens of that call; a later token raises a scale
  *                 if it must, and the codes already there are rounded to the new scale.
  *   slot        : page * P + offset in page; block_table[b][i] is the page holding tokens
@@ -83,7 +84,8 @@ extern "C" {
 #define RQ_STATUS_BAD_PAGE 1   /* block-table entry outside [0, num_pages) */
 #define RQ_STATUS_BAD_SLOT 2   /* slot_mapping entry >= num_pages * page_size */
 #define RQ_STATUS_BAD_LEN 4    /* seq_len < 0 or above max_pages * page_size, or below T */
-#define RQ_STATUS_NORM_OVERFLOW 8 /* a vector norm above the fp16 range (stored as inf) */
+#define RQ_STATUS_NORM_OVERFLOW 8 /* a vector norm above the fp16 range (stored as inf); RQ_FP8: a finite
+                                     magnitude above 448 * 2^60 (stored as that) */
 #define RQ_STATUS_NOT_FINITE 32 /* an infinity or NaN among the values an RQ_FP8 append coded */
 #define RQ_STATUS_TIMEOUT 16   /* an attention kernel's staged page copy did not complete within
                                   its bounded wait (outputs of that call are unspecified; free an

@@ -37,6 +37,7 @@ constexpr int kLongAppend = 2048;
 constexpr int kSplitAppend = 8192;  // tokens from which the queries have a launch of their own
 
 constexpr uint32_t kInf = 0x7F800000u;
+constexpr uint32_t kMost = (kMaxExp + 8 + 127) << 23 | 0x600000u;  // 448 * 2^kMaxExp: larger values are stored as that
 
 __device__ __forceinline__ uint32_t code4(uint64_t a, uint64_t b) {
   float x0, x1, x2, x3;
@@ -46,13 +47,17 @@ __device__ __forceinline__ uint32_t code4(uint64_t a, uint64_t b) {
 }
 
 // The scale's exponent for values whose largest magnitude over the warp has the bits `top`, or, if
-// that is not finite, for the finite ones among them (a second look, given by `finite_top`).
+// that is not finite, for the finite ones among them (a second look, given by `finite_top`).  What the
+// values have that d_status reports is added to `faults`.
 template <typename F>
-__device__ __forceinline__ int warp_exp(uint32_t top, bool& bad, F finite_top) {
+__device__ __forceinline__ int warp_exp(uint32_t top, int& faults, F finite_top) {
   top = __reduce_max_sync(0xffffffffu, top);
-  if (top >= kInf) {
-    bad = true;
-    top = __reduce_max_sync(0xffffffffu, finite_top());
+  if (top > kMost) {
+    if (top >= kInf) {
+      faults |= RQ_STATUS_NOT_FINITE;
+      top = __reduce_max_sync(0xffffffffu, finite_top());
+    }
+    if (top > kMost) faults |= RQ_STATUS_NORM_OVERFLOW;
   }
   return exp_of(__uint_as_float(top));
 }
@@ -85,12 +90,12 @@ __device__ __forceinline__ int slot_of(const Geometry& g, const BlockAppendArgs&
 }
 
 // Rows `off` .. off + cnt - 1 of a block's keys from tokens t0 .. (head h).  cs: cosines and sines
-// of token t0 + i at cs[i].  Returns the exponent; sets bad on a value that is not finite.  The rows
+// of token t0 + i at cs[i].  Returns the exponent.  The rows
 // stay in registers as they came (32, where the turned f32 values would take 64 and leave an SM one
 // CTA): they are turned once for the largest magnitude and again for the codes.
 template <typename T, bool INTERLEAVED>
 __device__ __forceinline__ int append_keys(const BlockAppendArgs& a, uint8_t* blk, int h, long long t0, int off,
-                                           int cnt, int e_old, const float4 (*cs)[2][16], int lane, bool& bad) {
+                                           int cnt, int e_old, const float4 (*cs)[2][16], int lane, int& faults) {
   const int j = lane & 15, half = lane >> 4;
   const Lane l = lane_of<INTERLEAVED>(j, a.in.rope.rotary_dim);
   const T* src = reinterpret_cast<const T*>(a.in.k.x) + (long long)h * kHeadDim;
@@ -123,7 +128,7 @@ __device__ __forceinline__ int append_keys(const BlockAppendArgs& a, uint8_t* bl
       for (int k = 0; k < 4; ++k) top = largest(top, x[k]);
     }
   }
-  const int e_new = warp_exp(top, bad, [&]() {
+  const int e_new = warp_exp(top, faults, [&]() {
     uint32_t m = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -183,7 +188,7 @@ __device__ __forceinline__ uint32_t abs_max2(uint32_t a, uint32_t b, __nv_bfloat
 // load 64 of four rows.  Bytes of rows outside the run stay as they are.
 template <typename T>
 __device__ __forceinline__ int append_values(const BlockAppendArgs& a, uint8_t* blk, int h, long long t0, int off,
-                                             int cnt, int e_old, int lane, bool& bad) {
+                                             int cnt, int e_old, int lane, int& faults) {
   const int g4 = 4 * (lane >> 2), t2 = 2 * (lane & 3);
   uint2 raw[4][4];  // [token][unit]
   uint32_t mask = 0u;
@@ -204,7 +209,7 @@ __device__ __forceinline__ int append_values(const BlockAppendArgs& a, uint8_t* 
   for (int i = 0; i < 16; ++i) m2 = abs_max2(abs_max2(m2, raw[i >> 2][i & 3].x, T()), raw[i >> 2][i & 3].y, T());
   const float2 m = unpack2<T>(m2);
   const uint32_t top = max(__float_as_uint(m.x) & 0x7FFFFFFFu, __float_as_uint(m.y) & 0x7FFFFFFFu);
-  const int e_new = warp_exp(top, bad, [&]() {
+  const int e_new = warp_exp(top, faults, [&]() {
     uint32_t f = 0;
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
@@ -294,7 +299,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 2) block_append_kernel(const G
     __syncthreads();
   }
 
-  bool bad = false;
+  int faults = 0;
   const int items = 2 * num_runs * g.num_kv_heads;  // (run, keys or values, head)
   for (int it = blockIdx.y * warps + warp; it < items; it += gridDim.y * warps) {
     const int run = it / (2 * g.num_kv_heads), of = it % (2 * g.num_kv_heads), h = of % g.num_kv_heads;
@@ -304,11 +309,11 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 2) block_append_kernel(const G
                    (size_t)(slot % g.page_size / kBlockTokens) * kBlockBytes;
     uint8_t* const exp_at = blk + kExps + (keys ? 0 : 1);
     const int e_old = off > 0 ? exp_of_byte(*exp_at) : kMinExp;
-    const int e = keys ? append_keys<T, INTERLEAVED>(a, blk, h, base + at, off, cnt, e_old, cs + at, lane, bad)
-                       : append_values<T>(a, blk, h, base + at, off, cnt, e_old, lane, bad);
+    const int e = keys ? append_keys<T, INTERLEAVED>(a, blk, h, base + at, off, cnt, e_old, cs + at, lane, faults)
+                       : append_values<T>(a, blk, h, base + at, off, cnt, e_old, lane, faults);
     if (lane == 0) *exp_at = (uint8_t)(e + 127);
   }
-  if (bad && a.status) atomicOr(a.status, RQ_STATUS_NOT_FINITE);
+  if (faults && a.status) atomicOr(a.status, faults);
 
   if (a.in.q.heads > 0) {
     const Lane l = lane_of<INTERLEAVED>(j, a.in.rope.rotary_dim);

@@ -112,3 +112,21 @@ def test_a_long_flat_tail_beside_a_heavy_token(call, dtype):
     tail = N * math.exp(-float(q[0, 0, 0, 0]) / math.sqrt(128))
     ref = np.full(tuple(out.shape), tail / (1 + tail))
     within(host(out), ref, N * 2.0 ** -32 + (2.0 ** -11 + 2.0 ** -20) * ref + R.half_step(dtype, ref) * (1 + 2.0 ** -8))
+
+
+@pytest.mark.parametrize("which", ["k", "v"])
+def test_append_reports_clipped_values(which):
+    """A finite magnitude above 448 * 2^60 is stored as that, and reported; one of just that is not."""
+    cache = rq.KVCache(rq.RQ_FP8, 8, 2, 2, 16, 2, None, None, max_batch=1, dtype=torch.bfloat16)
+    x = dict(k=torch.ones((2, 2, 128), dtype=torch.bfloat16, device="cuda"), v=torch.ones((2, 2, 128), dtype=torch.bfloat16, device="cuda"))
+    x[which][0, 0, 5] = -448 * 2.0 ** 60
+    slots = torch.tensor([0, 16], dtype=torch.int32, device="cuda")
+    cache.append(x["k"], x["v"], slots)
+    assert int(cache.status.item()) == 0
+    x[which][1, 1, 7] = 450 * 2.0 ** 60
+    cache.append(x["k"], x["v"], slots)
+    assert int(cache.status.item()) == rq.RQ_STATUS_NORM_OVERFLOW
+    codes, exps = R.unpack(cache.pages.cpu().numpy(), 16)
+    kind = "kv".index(which)
+    assert exps[kind][0, 0, 0] == exps[kind][1, 1, 0] == 60
+    assert codes[kind][0, 0, 0, 5] == -448 and codes[kind][1, 1, 0, 7] == 448
