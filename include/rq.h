@@ -87,6 +87,7 @@ extern "C" {
 #define RQ_STATUS_NORM_OVERFLOW 8 /* a vector norm above the fp16 range (stored as inf); RQ_FP8: a finite
                                      magnitude above 448 * 2^60 (stored as that) */
 #define RQ_STATUS_NOT_FINITE 32 /* an infinity or NaN among the values an RQ_FP8 append coded */
+#define RQ_STATUS_BAD_ORDER 64  /* an RQ_FP8 append with tokens of one block apart from one another */
 #define RQ_STATUS_TIMEOUT 16   /* an attention kernel's staged page copy did not complete within
                                   its bounded wait (outputs of that call are unspecified; free an
                                   RQ_FP8 context, whose workspace the call may not have put back) */
@@ -177,8 +178,9 @@ int rq_get_codebook(const rq_ctx *ctx, float *centroids, float *boundaries);
  * skipped.  Slots within one call must be distinct.  n = 0 is a no-op.  k, v and kv_pages must be
  * 16-byte aligned (RQ_ERR_INVALID otherwise).
  * RQ_FP8: k and v have the context's io_type, no rotation; tokens of one block of 16 must stand
- * next to one another in the call, in ascending slots, as a sequence's tokens do (otherwise that
- * block's contents are unspecified).  Infinities are stored as the block's largest value, NaN as
+ * next to one another in the call, in consecutive slots, as a sequence's tokens do: [sequence][token] and
+ * not [token][sequence], padding before or behind them.  Of a block's tokens that stand apart at most one run
+ * is written (the one that starts the block, if the call has it), and RQ_STATUS_BAD_ORDER is set.  Infinities are stored as the block's largest value, NaN as
  * NaN; either sets RQ_STATUS_NOT_FINITE and neither counts for the scale.
  */
 int rq_quantize_append(rq_ctx *ctx, const void *k, const void *v, const int32_t *slot_mapping,

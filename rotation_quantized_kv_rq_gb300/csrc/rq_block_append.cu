@@ -9,8 +9,10 @@
 //
 // Work is split by runs: consecutive tokens of the call in consecutive slots of one block.  One warp
 // codes a run's keys or its values of one head, so that a block's scale is one reduction in one warp
-// and no atomics order anything; the run's tokens all belong to one block by construction, and two
-// runs of one call never share a block (include/rq.h asks for that).
+// and no atomics order anything; the run's tokens all belong to one block by construction.  No two runs
+// that are written share a block: a run that starts inside a block is dropped, and reported, where the
+// call has tokens of that block elsewhere (of two runs at most one starts it).  To know that, such a run's CTA
+// looks through all the call's slots; prompts have one such run a sequence.
 //
 // What bounds it: 512 bytes in and 257 out a (token, kv head), and the queries' rows in and out.  32,768
 // tokens x (32 + 8) heads, 739 MB: 164 us (4.5 TB/s, 67% of the copy rate).  The queries, in a launch of
@@ -87,6 +89,47 @@ __device__ __forceinline__ int slot_of(const Geometry& g, const BlockAppendArgs&
     return -1;
   }
   return s;
+}
+
+// The slots of a call in groups of four (16-byte loads between ends of up to three): groups i, i + threads, ...,
+// N of them, in flight together, and the ends with group threadIdx.x.
+template <int N>
+struct SlotQuads {
+  int4 v[N];
+  int ends[2];
+  long long count;  // groups of the call
+  __device__ __forceinline__ static int head(const int32_t* slots, long long n) {
+    return (int)min(n, (long long)((4 - ((uintptr_t)slots >> 2 & 3)) & 3));
+  }
+  __device__ __forceinline__ void load(const int32_t* slots, long long n, long long i) {
+    const int h = head(slots, n);
+    count = (n - h) / 4;
+    const int4* p = reinterpret_cast<const int4*>(slots + h);
+#pragma unroll
+    for (int u = 0; u < N; ++u) {
+      const long long at = i + u * (int)blockDim.x;
+      v[u] = at < count ? __ldg(p + at) : make_int4(-1, -1, -1, -1);
+    }
+    const long long tail = h + 4 * count + i;
+    ends[0] = i < h ? __ldg(slots + i) : -1;
+    ends[1] = tail < n ? __ldg(slots + tail) : -1;
+  }
+  template <typename F>
+  __device__ __forceinline__ void each(const int32_t* slots, long long n, long long i, F f) const {  // f(token, slot)
+    const int h = head(slots, n);
+#pragma unroll
+    for (int u = 0; u < N; ++u) {
+      const long long t = h + 4 * (i + u * (int)blockDim.x);
+      f(t, v[u].x), f(t + 1, v[u].y), f(t + 2, v[u].z), f(t + 3, v[u].w);
+    }
+    f(i, ends[0]), f(h + 4 * count + i, ends[1]);
+  }
+};
+// Whether the token at distance d from a run's first, in slot s0, has its slot s in the run's block, but not the slot
+// of a token that continues the run.  (Behind a gap there may be one that would continue it: it starts a run
+// of its own, and this one is elsewhere to that.)  So of two runs of a block that both start inside it the later is dropped.
+__device__ __forceinline__ bool elsewhere(long long d, int s, int s0) {
+  return s >= 0 && s / kBlockTokens == s0 / kBlockTokens && (d < 0 || s != s0 + d);
 }
 
 // Rows `off` .. off + cnt - 1 of a block's keys from tokens t0 .. (head h).  cs: cosines and sines
@@ -255,6 +298,58 @@ __device__ __forceinline__ int append_values(const BlockAppendArgs& a, uint8_t* 
   return e;
 }
 
+// The runs that start among a CTA's W = 16 tokens.
+constexpr int kFilterWords = 512;
+struct Runs {
+  int at[16], cnt[16], slot[16], num;  // first token (of the CTA's), tokens, first slot; runs
+  uint32_t inside, apart;  // first tokens of runs that start inside a block; of them those whose block has tokens elsewhere
+  uint32_t filter[kFilterWords];  // bits of those blocks' numbers modulo 16,384
+  __device__ __forceinline__ uint32_t maybe(int s) const {  // (padding: past all blocks)
+    const uint32_t blk = (uint32_t)s / kBlockTokens;
+    return filter[(blk >> 5) % kFilterWords] >> (blk & 31) & 1;
+  }
+};
+// Drops, and reports, the runs that start inside a block that has tokens elsewhere in the call; `apart` already
+// holds those with tokens among the kSeen of the CTA's first.  By the whole CTA.  (Not inlined: that cost the
+// kernel's loop 4 to 28%, in calls without such runs too.)
+template <int kSeen>
+__device__ __noinline__ void drop_apart(Runs& runs, const int32_t* slots, long long n, long long base, int32_t* status) {
+  const int tid = threadIdx.x;
+  uint32_t mine = 0u;
+  constexpr int N = 4;
+  SlotQuads<N> quads;
+  for (long long i = tid;; i += N * blockDim.x) {
+    quads.load(slots, n, i);
+    uint32_t hits = 0u;  // all looks at the filter together, no branch between
+    int at = 0;
+    quads.each(slots, n, i, [&](long long t, int s) { hits |= (t < base || t >= base + kSeen ? runs.maybe(s) : 0u) << at++; });
+    if (hits != 0u) {
+      at = 0;
+      quads.each(slots, n, i, [&](long long t, int s) {
+        if (!(hits >> at++ & 1)) return;
+        for (int r = 0; r < runs.num; ++r)
+          if ((runs.inside >> runs.at[r] & 1) && elsewhere(t - base - runs.at[r], s, runs.slot[r])) mine |= 1u << runs.at[r];
+      });
+    }
+    if (i - tid + N * blockDim.x >= quads.count) break;
+  }
+  mine = __reduce_or_sync(0xffffffffu, mine);
+  if ((tid & 31) == 0 && mine != 0u) atomicOr(&runs.apart, mine);
+  __syncthreads();
+  if (runs.apart == 0u) return;
+  if (tid == 0) {  // what is left of the runs
+    int kept = 0;
+    for (int i = 0; i < runs.num; ++i) {
+      if (runs.apart >> runs.at[i] & 1) continue;
+      runs.at[kept] = runs.at[i], runs.cnt[kept] = runs.cnt[i], runs.slot[kept] = runs.slot[i];
+      ++kept;
+    }
+    runs.num = kept;
+    if (status) atomicOr(status, RQ_STATUS_BAD_ORDER);
+  }
+  __syncthreads();
+}
+
 // A CTA takes the runs that start among its W tokens, and those W tokens' queries.  W = 1 spreads a
 // decode step's single tokens over the SMs; W = 16 (long appends) makes one block of a run a
 // CTA's work.  blockIdx.y splits the heads.
@@ -262,7 +357,8 @@ template <typename T, bool INTERLEAVED, int W>
 __global__ void __launch_bounds__(32 * kMaxWarps, 2) block_append_kernel(const Geometry g, const BlockAppendArgs a) {
   constexpr int kTokens = W == 1 ? 16 : 32;  // a run reaches at most 15 tokens past its first
   __shared__ float4 cs[kTokens][2][16];  // [token][cosines, sines][j]: pairs 4j .. 4j + 3
-  __shared__ int run_at[W], run_cnt[W], run_slot[W], num_runs, reach;
+  __shared__ Runs runs;  // (W = 1: one run, nothing of its filter)
+  __shared__ int reach;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
   const long long base = (long long)blockIdx.x * W;
   const int hw = tid >> 4, hws = blockDim.x >> 4, j = tid & 15;
@@ -274,6 +370,14 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 2) block_append_kernel(const G
       cs[i][1][j] = s;
     }
   };
+  // W = 1: the first of the call's slots, loaded beside the rest of the opening
+  int slot0 = -1, before = -1;
+  SlotQuads<1> quads;
+  if (W == 1 && a.slots != nullptr) {
+    slot0 = __ldg(a.slots + base);
+    if (base > 0) before = __ldg(a.slots + base - 1);
+    quads.load(a.slots, a.in.n, tid);
+  }
   if (warp == 0) {
     const int s = lane < kTokens ? slot_of(g, a, base + lane, lane < W && blockIdx.y == 0) : -1;
     int prev = __shfl_up_sync(0xffffffffu, s, 1);
@@ -286,25 +390,57 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 2) block_append_kernel(const G
       const uint32_t after = lane < 31 ? conts >> (lane + 1) : 0u;
       cnt = __ffs(~after);  // 1 + the tokens that continue it
       const int i = __popc(leads & ((1u << lane) - 1u));
-      run_at[i] = lane, run_cnt[i] = cnt, run_slot[i] = s;
+      runs.at[i] = lane, runs.cnt[i] = cnt, runs.slot[i] = s;
     }
     const int ends = __reduce_max_sync(0xffffffffu, cnt > 0 ? lane + cnt : 0);
-    if (lane == 0) num_runs = __popc(leads), reach = ends;
+    if (W > 1) {
+      const bool in = (leads >> lane & 1) && s % kBlockTokens != 0 && a.slots != nullptr;
+      const uint32_t ins = __ballot_sync(0xffffffffu, in);
+      uint32_t apart = 0u;
+      if (ins != 0u) {
+        for (int i = lane; i < kFilterWords; i += 32) runs.filter[i] = 0u;
+        __syncwarp();
+        if (in) atomicOr(&runs.filter[(s / kBlockTokens >> 5) % kFilterWords], 1u << (s / kBlockTokens & 31));
+        // among these tokens: those of the block, but for later ones in the slots of tokens that continue the run
+        const uint32_t same = __match_any_sync(0xffffffffu, s >= 0 ? s / kBlockTokens : -1 - lane);
+        const uint32_t line = __match_any_sync(0xffffffffu, s >= 0 ? s - lane : INT32_MIN + lane);
+        apart = __ballot_sync(0xffffffffu, in && (same & ~(line & 0xffffffffu << lane)) != 0u);
+      }
+      if (lane == 0) runs.inside = ins, runs.apart = apart;
+    }
+    if (lane == 0) runs.num = __popc(leads), reach = ends;
   } else {  // meanwhile the angles of the W tokens
     for (int i = hw - 2; i < W; i += hws - 2) angles(i);
   }
-  __syncthreads();
+  bool dropped = false;  // W = 1: the run (a decode step's tokens are each a sequence's: no look)
+  if (W == 1) {
+    bool other = false;
+    if (slot0 > 0 && slot0 % kBlockTokens != 0 && before != slot0 - 1) {
+      auto look = [&](long long t, int s) { other = other || elsewhere(t - base, s, slot0); };
+      quads.each(a.slots, a.in.n, tid, look);
+      SlotQuads<1> more;
+      for (long long i = tid + blockDim.x; i < quads.count; i += blockDim.x) {
+        more.load(a.slots, a.in.n, i);
+        more.each(a.slots, a.in.n, i, look);
+      }
+    }
+    dropped = __syncthreads_or(other);
+    if (dropped && tid == 0 && blockIdx.y == 0 && runs.num > 0 && a.status) atomicOr(a.status, RQ_STATUS_BAD_ORDER);
+  } else {
+    __syncthreads();
+  }
   if (reach > W) {  // a run goes on past them
     for (int i = W + hw; i < reach; i += hws) angles(i);
     __syncthreads();
   }
+  if (W > 1 && runs.inside != 0u) drop_apart<kTokens>(runs, a.slots, a.in.n, base, a.status);
 
   int faults = 0;
-  const int items = 2 * num_runs * g.num_kv_heads;  // (run, keys or values, head)
+  const int items = dropped ? 0 : 2 * runs.num * g.num_kv_heads;  // (run, keys or values, head)
   for (int it = blockIdx.y * warps + warp; it < items; it += gridDim.y * warps) {
     const int run = it / (2 * g.num_kv_heads), of = it % (2 * g.num_kv_heads), h = of % g.num_kv_heads;
     const bool keys = of < g.num_kv_heads;
-    const int at = run_at[run], cnt = run_cnt[run], slot = run_slot[run], off = slot % kBlockTokens;
+    const int at = runs.at[run], cnt = runs.cnt[run], slot = runs.slot[run], off = slot % kBlockTokens;
     uint8_t* blk = a.pages + ((size_t)(slot / g.page_size) * g.num_kv_heads + h) * g.page_bytes +
                    (size_t)(slot % g.page_size / kBlockTokens) * kBlockBytes;
     uint8_t* const exp_at = blk + kExps + (keys ? 0 : 1);

@@ -19,7 +19,7 @@ from . import build as _build
 
 RQ_OK, RQ_ERR_INVALID, RQ_ERR_UNSUPPORTED, RQ_ERR_CUDA, RQ_ERR_CAPACITY = 0, 1, 2, 3, 4
 RQ_STATUS_BAD_PAGE, RQ_STATUS_BAD_SLOT, RQ_STATUS_BAD_LEN, RQ_STATUS_NORM_OVERFLOW, RQ_STATUS_TIMEOUT = 1, 2, 4, 8, 16
-RQ_STATUS_NOT_FINITE = 32
+RQ_STATUS_NOT_FINITE, RQ_STATUS_BAD_ORDER = 32, 64
 RQ_PLANAR, RQ_ISO, RQ_DENSE = 0, 1, 2
 RQ_FP8 = 8
 RQ_F16, RQ_BF16 = 0, 1

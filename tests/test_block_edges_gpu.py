@@ -130,3 +130,55 @@ def test_append_reports_clipped_values(which):
     kind = "kv".index(which)
     assert exps[kind][0, 0, 0] == exps[kind][1, 1, 0] == 60
     assert codes[kind][0, 0, 0, 5] == -448 and codes[kind][1, 1, 0, 7] == 448
+
+
+@pytest.mark.parametrize("slots,written", [
+    ([3, -1, 4], []), ([3, -1, 5], [3]), ([0, 1, -1, 2], [0, 1]), ([3, 5], []), ([6, 5], []), ([16, 18, 17], [16]), ([5, 5], []),
+    ([9, 40, 10, 41, 20], [20]),                                      # [token][sequence]
+    ([0, 16, 32, 1, 17, 33], [0, 16, 32]),
+    ([-1, 9, 10, -1, 40, 41, -1, -1], [9, 10, 40, 41]),               # in order, padded
+    (list(range(7, 39)) + [6], list(range(16, 39))),                  # a stray token of the first run's block
+], ids=str)
+@pytest.mark.parametrize("more", [0, 300, 2200])
+def test_append_reports_tokens_apart(slots, written, more):
+    """Tokens of one block that do not stand together: at most one run of them is written, the one that
+    starts the block if the call has it, and that is reported.  more: tokens of a further sequence behind them, which are all written."""
+    rng, hkv, hq, P = gen(len(slots) + more), 2, 3, 16
+    caches = [rq.KVCache(rq.RQ_FP8, 8, hkv, hkv, P, 160, None, None, max_batch=1) for _ in range(2)]
+    fill = dev(rng.standard_normal((48, hkv, 128)), torch.float16)
+    for c in caches:
+        c.append(fill, fill, torch.arange(48, dtype=torch.int32, device="cuda"))
+    extra = list(range(53, 53 + more))
+    all_slots = np.array(slots + extra, np.int32)
+    n = len(all_slots)
+    q, k, v = (dev(rng.standard_normal((n, h, 128)) * 4, torch.float16) for h in (hq, hkv, hkv))
+    rope, pos = rq.Rope(128), torch.arange(n, dtype=torch.int32, device="cuda")
+    out = caches[0].append_rope(k, v, dev(all_slots), rope, pos, q=q)
+    keep = np.array([i for i, s in enumerate(all_slots) if s in written or s in extra], np.int64)
+    if keep.size:
+        at = torch.from_numpy(keep).cuda()
+        caches[1].append_rope(k[at], v[at], dev(all_slots[keep]), rope, pos[at])
+    assert torch.equal(caches[0].pages, caches[1].pages)
+    assert torch.equal(out, rope.apply(q, None, pos)[0])
+    assert int(caches[1].status.item()) == 0
+    apart = sum(s >= 0 for s in slots) > len(written)
+    assert int(caches[0].status.item()) == (rq.RQ_STATUS_BAD_ORDER if apart else 0)
+
+
+@pytest.mark.parametrize("slots,dropped", [
+    (list(range(5, 2605)) + [3], list(range(5, 16)) + [3]),
+    (list(range(5, 805)) + list(range(806, 2606)) + [805], list(range(806, 816)) + [805]),
+    ([2605] + list(range(5, 2605)), [2605]),                    # its block's start comes last
+])
+@pytest.mark.parametrize("skip", [0, 1, 3])
+def test_append_reports_a_stray_token_of_a_long_call(slots, dropped, skip):
+    """The same far apart in a call of many tokens, slots at every alignment."""
+    rng, n = gen(skip), len(slots)
+    caches = [rq.KVCache(rq.RQ_FP8, 8, 1, 1, 32, 82, None, None, max_batch=1, dtype=torch.bfloat16) for _ in range(2)]
+    k, v = (dev(rng.standard_normal((n, 1, 128)), torch.bfloat16) for _ in range(2))
+    s = torch.tensor([0] * skip + slots, dtype=torch.int32, device="cuda")[skip:]
+    caches[0].append(k, v, s)
+    at = torch.tensor([i for i in range(n) if slots[i] not in dropped], device="cuda")
+    caches[1].append(k[at], v[at], s[at])
+    assert torch.equal(caches[0].pages, caches[1].pages)
+    assert [int(c.status.item()) for c in caches] == [rq.RQ_STATUS_BAD_ORDER, 0]
