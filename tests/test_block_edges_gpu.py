@@ -182,3 +182,39 @@ def test_append_reports_a_stray_token_of_a_long_call(slots, dropped, skip):
     caches[1].append(k[at], v[at], s[at])
     assert torch.equal(caches[0].pages, caches[1].pages)
     assert [int(c.status.item()) for c in caches] == [rq.RQ_STATUS_BAD_ORDER, 0]
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("P,hkv,B", [(16, 1, 1), (32, 3, 40), (256, 8, 9)])
+def test_decode_step_over_a_cache_in_use(dtype, P, hkv, B):
+    """Steps one after the other against append and decode of the same tokens: the same pages and results."""
+    dtype, rng, hq = DT[dtype], gen(60 + B), 2 * hkv
+    start = rng.integers(0, 3 * P, B)
+    a, table, lens = filled(rng, hq, hkv, P, start, dtype)
+    extra = make_wider(a, table, start, 20)
+    pages = extra.max() + 1
+    caches = [rq.KVCache(rq.RQ_FP8, 8, hq, hkv, P, int(pages), None, None, max_batch=B, dtype=dtype) for _ in range(2)]
+    for c in caches:
+        c.pages[:a.num_pages] = a.pages
+    for i in range(18):
+        lens = (start + i + 1).astype(np.int32)
+        q, k, v = (dev(rng.standard_normal((B, h, 128)) * 2.0 ** rng.integers(-2, 3), dtype) for h in (hq, hkv, hkv))
+        got = caches[0].decode_step(q, k, v, dev(extra), dev(lens))
+        slots = extra[np.arange(B), (lens - 1) // P] * P + (lens - 1) % P
+        caches[1].append(k, v, dev(slots.astype(np.int32)))
+        assert torch.equal(got, caches[1].decode(q, dev(extra), dev(lens))), i
+    assert torch.equal(caches[0].pages, caches[1].pages)
+    check(caches[0], extra, lens, q[:, None], got[:, None], lambda b, j, p: p <= lens[b] - 1, "step")
+
+
+def make_wider(cache, table, start, more):
+    """The block table with pages of their own for `more` further tokens of every sequence."""
+    P = cache.page_size
+    need = (start + more + P - 1) // P
+    out, at = np.zeros((len(start), need.max()), np.int32), cache.num_pages
+    for b, s in enumerate(start):
+        have = (s + P - 1) // P
+        out[b, :have] = table[b, :have]
+        out[b, have:need[b]] = np.arange(at, at + need[b] - have)
+        at += need[b] - have
+    return out
