@@ -119,7 +119,8 @@ typedef struct {
   int num_pages;             /* pages in the caller's pool */
   int max_batch;             /* largest B of an attention call */
   int max_query_tokens;      /* largest T of a verify call (>= 1) */
-  int max_pages_per_seq;     /* largest block-table width (max_pages) of an attention call */
+  int max_pages_per_seq;     /* largest block-table width (max_pages) of an attention call; times P below 2^31
+                                (RQ_FP8: 2^31 - 4096) */
   /* host float32.  planar -> [Hkv][d/2][2] = (cos t, sin t) of the pair (2i, 2i+1),
      y_2i = c x_2i - s x_2i+1, y_2i+1 = s x_2i + c x_2i+1;
      iso -> [Hkv][d/4][4] = unit quaternion (a, b, c, d) of block 4i..4i+3, y = q (x) x

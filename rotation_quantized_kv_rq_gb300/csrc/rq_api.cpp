@@ -132,6 +132,8 @@ int check_geometry(const rq_config* c) {
   if (c->mode == RQ_FP8) {
     if (c->codebook) return RQ_ERR_INVALID;
     if (c->head_dim != rq::kHeadDim || c->bits != 8) return RQ_ERR_UNSUPPORTED;
+    // the extend kernel looks up pages for positions up to a tile and 1,024 tokens past a sequence's end
+    if ((long long)c->max_pages_per_seq * c->page_size > INT32_MAX - 4096) return RQ_ERR_UNSUPPORTED;
     return check_sizes(c, (long long)c->page_size / 16 * rq::kBlockBytes);
   }
   if (c->io_type != RQ_F16) return RQ_ERR_UNSUPPORTED;
