@@ -59,7 +59,9 @@
  *                 is at most 448 * 2^E (60 if none is: larger ones are clipped and
  *                 RQ_STATUS_NORM_OVERFLOW is set).  Appending a block's first token (offset a multiple of 16)
  *                 starts its scales anew from the tokens of that call; a later token raises a scale
- *                 if it must, and the codes already there are rounded to the new scale.
+ *                 if it must, and the codes already there are rounded to the new scale.  A scale does
+ *                 not come down again inside a block: a draft that is rejected and written over leaves
+ *                 the block as coarse as it made it, until the block's first token is appended again.
  *   slot        : page * P + offset in page; block_table[b][i] is the page holding tokens
  *                 i*P .. i*P+P-1 of sequence b.
  */
@@ -109,6 +111,8 @@ extern "C" {
 
 typedef struct rq_ctx rq_ctx;  /* opaque, owned by the library */
 
+/* The structs of this header carry no size: a program is compiled with the header of the library that it
+   loads.  Zero a struct before setting its fields, so that those it does not know keep their defaults. */
 typedef struct {
   int head_dim;              /* must be 128 */
   int num_q_heads;           /* Hq, a multiple of num_kv_heads */
@@ -181,8 +185,9 @@ int rq_get_codebook(const rq_ctx *ctx, float *centroids, float *boundaries);
  * RQ_FP8: k and v have the context's io_type, no rotation; tokens of one block of 16 must stand
  * next to one another in the call, in consecutive slots, as a sequence's tokens do: [sequence][token] and
  * not [token][sequence], padding before or behind them.  Of a block's tokens that stand apart at most one run
- * is written (the one that starts the block, if the call has it), and RQ_STATUS_BAD_ORDER is set.  Infinities are stored as the block's largest value, NaN as
- * NaN; either sets RQ_STATUS_NOT_FINITE and neither counts for the scale.
+ * is written (the one that starts the block, if the call has it), and RQ_STATUS_BAD_ORDER is set.
+ * Infinities are stored as the block's largest value, NaN as NaN; either sets RQ_STATUS_NOT_FINITE and
+ * neither counts for the scale.
  */
 int rq_quantize_append(rq_ctx *ctx, const void *k, const void *v, const int32_t *slot_mapping,
                        int n, void *kv_pages, int32_t *d_status, void *stream);
@@ -220,7 +225,8 @@ int rq_decode_attention(rq_ctx *ctx, const void *q, const void *kv_pages, const 
  * (RQ_DENSE) rotates the queries into the context's workspace first, so there T must not exceed
  * max_query_tokens (RQ_ERR_CAPACITY otherwise).  RQ_FP8 joins a row block's parts in the context's
  * workspace, whatever T is; calls with B * T * Hq * max_pages * P up to 2^23 share the kernel of
- * rq_verify_attention.
+ * rq_verify_attention, which is the faster one for little work: a table no wider than the longest
+ * sequence needs lets short chunks over short sequences have it.
  *   q   device fp16 [B][T][Hq][head_dim],   out device fp16 [B][T][Hq][head_dim]
  * Other arguments as rq_verify_attention.  Errors as rq_verify_attention (except that T above
  * max_query_tokens is allowed for planar and iso rotations and RQ_FP8).
@@ -244,7 +250,8 @@ int rq_extend_attention(rq_ctx *ctx, const void *q, int T, const void *kv_pages,
  * The result equals rq_quantize_append of the tokens followed by rq_decode_attention (the same
  * bytes written, the same output).  A dense rotation (RQ_DENSE) codes the new tokens in the
  * launch that rotates the queries, before the split-K kernel (which applies the output
- * rotation itself): two launches instead of four.  RQ_FP8 appends in a launch of its own.  A page
+ * rotation itself): two launches instead of four.  RQ_FP8 appends in a launch of its own: a token that
+ * raises a scale rewrites its block, which the attention kernel would have in flight.  A page
  * id out of range for the new token sets RQ_STATUS_BAD_PAGE and skips its write.  Errors as rq_decode_attention, plus RQ_ERR_INVALID for a NULL or
  * non-16-byte-aligned k_new / v_new.
  */
@@ -258,7 +265,8 @@ int rq_decode_step(rq_ctx *ctx, const void *q, const void *k_new, const void *v_
  * drafts); a chain is a top-1 draft.
  * Speculative chain-verify attention: T query tokens per sequence, the last T cached tokens
  * being the drafts themselves (append them first).  Query row j (0 <= j < T) attends to
- * positions 0 .. seq_lens[b] - T + j (causal over the draft tail).
+ * positions 0 .. seq_lens[b] - T + j (causal over the draft tail).  (RQ_FP8: rejected drafts can leave
+ * their block's scales raised; see the storage contract.)
  *   q   device fp16 [B][T][Hq][head_dim],   out device fp16 [B][T][Hq][head_dim]
  * Other arguments as rq_decode_attention; T = 1 is decode.  0 < seq_lens[b] < T sets
  * RQ_STATUS_BAD_LEN.  Errors as rq_decode_attention, plus RQ_ERR_CAPACITY for

@@ -70,7 +70,8 @@ __device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)
 // running maximum of score + EV less kLift, moved where a score is past it by more than kReach.  So the largest
 // weight of a row stands between 2^kLift and 2^kReach, near the top of fp16's range, and its smallest steps,
 // 2^-24, are 2^-31 of it or less: a token below half of that is lost from the product (not from the
-// weights' sum), at most 2^-32 of the largest, 2^-12 for 2^20 such tokens, which is the rounding of the largest itself.
+// weights' sum), at most 2^-32 of the largest, 2^-12 for 2^20 such tokens, where the largest itself is rounded
+// by up to 2^-11.
 constexpr float kLift = 7.f, kReach = 15.f;  // (a maximum of 2^26 and more, 8 apart, gives a lift of 8 or 0)
 constexpr float kNone = -3.402823466e38f;    // m before any visible token: no finite score is below
 

@@ -19,7 +19,9 @@
 // their own, run at rq_rope.cu's rate; the coding of keys and values is bound by its latencies at 16 warps
 // an SM (128 registers hold a warp's 16 rows; issue in 47% of the cycles).  Neither 20% fewer instructions
 // (whole blocks apart from parts of one), nor more CTAs an SM with the rows read again, was faster.  64
-// single tokens x 72 heads: 5.8 us, the chain slot - row - norm - largest value - old scale - codes.
+// single tokens x 72 heads: 6.2 us, the chain slot - row - norm - largest value - old scale - codes.  The look
+// for tokens elsewhere is beside that chain in short calls (0.1 to 0.4 us) and ahead of one CTA's work a sequence in
+// prompts (32,768 tokens from inside a block 162.8 -> 163.1 us; 8,000 of one head, 64 threads, 20 -> 25).
 #include "../../include/rq.h"
 #include "rq_block.cuh"
 #include "rq_rope.cuh"
@@ -31,10 +33,12 @@ using namespace rope;
 using namespace block;
 
 constexpr int kMaxWarps = 8;
-// Tokens from which a CTA takes 16 of them.  Device time, us, one token of a sequence or 16 to a CTA:
-// 1,024 x 1 token 27 | 70; 128 x 8 17.5 | 28; 256 x 8 27.3 | 28.5; 1 x 1,500 20 | 22; 1 x 2,048 29 | 30;
-// 1 x 8,000 (one head) 53 | 21; 1 x 16,000 130 | 79.  The slots say how long the runs are, and they
-// are on the device: a call with as many tokens is taken for a prompt's, unless each is a sequence's.
+// Tokens from which a CTA takes 16 of them.  Device time, us, 32 and 8 heads, one token or 16 to a CTA:
+// 1,024 x 1 token 28 | 72; 128 x 8 17.6 | 29.5; 256 x 8 28.3 | 29.6; 1 x 1,500 20.4 | 23.4; 1 x 2,048 25 | 23.6;
+// 1 x 8,000 (one head) 55 | 27; 1 x 16,000 143 | 90.  The slots say how long the runs are, and they
+// are on the device: a call with as many tokens is taken for a prompt's, unless each is a sequence's by the
+// call's form (a decode step).  Single tokens given by slots pay for it up to some 3,500 of them: 2,048 x 1 52 | 77,
+// 3,000 x 1 92 | 106, 4,096 x 1 133 | 115.
 constexpr int kLongAppend = 2048;
 constexpr int kSplitAppend = 8192;  // tokens from which the queries have a launch of their own
 
@@ -322,7 +326,9 @@ __device__ __noinline__ void drop_apart(Runs& runs, const int32_t* slots, long l
     quads.load(slots, n, i);
     uint32_t hits = 0u;  // all looks at the filter together, no branch between
     int at = 0;
-    quads.each(slots, n, i, [&](long long t, int s) { hits |= (t < base || t >= base + kSeen ? runs.maybe(s) : 0u) << at++; });
+    quads.each(slots, n, i, [&](long long t, int s) {
+      hits |= (t < base || t >= base + kSeen ? runs.maybe(s) : 0u) << at++;
+    });
     if (hits != 0u) {
       at = 0;
       quads.each(slots, n, i, [&](long long t, int s) {

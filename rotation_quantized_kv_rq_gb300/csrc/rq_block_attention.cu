@@ -8,7 +8,8 @@
 //   O^T += code_V^T w;   l += w 2^-EV;   out = O / l
 // The value scale is part of the weight's exponent, so codes are never multiplied by it, and m follows
 // the running maximum of score + EV: w, rounded to fp16 for the MMA (2^-11 of it), is then largest
-// where a token weighs most in the output, whatever the scales (its range: rq_block.cuh).  Queries are fp16 as they are; a bf16 row is brought into fp16's range by a power of two.
+// where a token weighs most in the output, whatever the scales (its range: rq_block.cuh).  Queries are
+// fp16 as they are; a bf16 row is brought into fp16's range by a power of two.
 //
 // What bounds it: the cache is read once, 257 bytes a (token, kv head), against 4 MMAs' worth of
 // work; so the design keeps copies in flight.  A block is one 4112-byte bulk copy into a ring of
@@ -19,8 +20,10 @@
 // 8 (group > 8, verify) share the widened tile: up to three n-tiles of 8 rows a warp, with the
 // registers for 12 and 8 warps an SM and the queries in shared memory.  Three n-tiles are bound by the
 // chain wait - widen - MMA - softmax - MMA of two warps a quarter SM (0.36 instructions a cycle, the MMAs
-// busy 31%).  8 x 16K, 6 rows x 4 heads, us: 69 so, 72 with 12 warps (spills), 74 with the next tile's
-// products before this one's softmax, 74 with the values loaded a quarter at a time.
+// busy 31%).  8 x 16K, 6 rows x 4 heads: 71 us (3.8 TB/s).  Beside 69 us of the same kernel with an older
+// partition: 72 with 12 warps (spills), 74 with the next tile's products before this one's softmax, 74 with the
+// values loaded a quarter at a time.  Two n-tiles with 12 warps spill 26 to 32 bytes; 8 x 16K, 4 rows x 4
+// heads: 55 us (4.9 TB/s).
 //
 // Work is cut evenly: a unit is (sequence, kv head, group of n-tiles) and costs one round per tile of
 // each warp; the rounds of all units in order are cut into one range per CTA, on the device from
@@ -28,8 +31,8 @@
 // the ranges (the result does not depend on which came last).  A CTA has at most two such
 // fragments, its first and its last, so the workspace is two slots and one counter a CTA.  Where up to
 // 32 sequences have no more units than CTAs, ranges that lie in one unit each are taken instead, if they
-// are at most 6 rounds longer (us: 4 x 4K + 6 rows x 4 heads 23.9 -> 19.7, 1 x 16K + 8 x 8 28.4 -> 23.0,
-// 8 x 4K decode 19.4 -> 16.5; 8 x 16K + 6, where they are 10 longer, 69 -> 70 for the search).  Short
+// are at most 6 rounds longer (us: 4 x 4K + 6 rows x 4 heads 23.9 -> 19.4, 1 x 16K + 8 x 8 28.4 -> 23.1,
+// 8 x 4K decode 19.4 -> 16.8; 8 x 16K + 6, where they are 10 longer, 1 more for the search).  Short
 // calls are chains of memory latencies (0.6 us each), so what can load together does: a fragment's
 // page ids with its queries, the parts to join by bulk copies of a chunk at once.
 #include <math_constants.h>

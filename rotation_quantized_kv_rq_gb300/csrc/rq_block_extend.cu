@@ -21,7 +21,7 @@
 // Why these shapes: an MMA with N = 64 takes as long as one with N = 128 (64.5 and 65.5 cycles for M =
 // 128, K = 16, A in tensor memory), so S is 128 columns wide.  That fills tensor memory (O 2 x 128
 // columns, S 2 x 128 with W over it) and puts Q into shared memory.  A tile is 32 MMAs, 2064 cycles
-// measured alone; 8 x 1,024 rows over 15K take 1.81 ms, 1,180 TFLOP/s, 62% of the burst rate of a
+// measured alone; 8 x 1,024 rows over 15K take 1.80 ms, 1,185 TFLOP/s, 63% of the burst rate of a
 // large matrix product and 69% of its sustained rate.  What is left is the softmax between a block's S
 // and its W: two passes over 128 scores a thread, beside which the tensor cores have one other block.
 // Measured and slower: the two blocks' softmaxes kept in turns 3.0 ms (2.1 with turns of half a
