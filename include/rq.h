@@ -397,6 +397,129 @@ int rq_rope_append(rq_ctx *ctx, const rq_rope *rope, const rq_rows *q, const rq_
                    long long v_stride, float eps, const int32_t *positions, const int32_t *slot_mapping, int n,
                    void *kv_pages, int32_t *d_status, void *stream);
 
+/*
+ * Latent attention: models whose cache is one latent vector (512) a token, which all heads share, and one position
+ * part (64), the rotated part of every head's key.  Source: this library.
+ *   absorbed form   a head's key and value projections are taken into its query and its output, so that attention runs
+ *                   in the latents' space: score = sm_scale (q_c . c + q_pe . p), out = sum softmax(score) c
+ *   expanded form   latents are read back and projected to keys and values for each head (rq_latent_read, a matrix
+ *                   product of the caller's, rq_prompt_attention): less work where many new tokens stand over a prefix
+ *
+ * Storage: device bytes [num_pages][page_bytes], page_bytes = 641 P; offset r of a page holds
+ *   512 e4m3 codes    dim d at byte d/128 * 128 P + 128 r + ((d%128/16) ^ (r%8)) * 16 + d%16
+ *   64 16-bit values  (the context's io_type) dim i of the position part at byte 512 P + 128 r + ((i/8) ^ (r%8)) * 16 + 2 (i%8)
+ *   an exponent byte  at 640 P + r: codes and position part are times 2^(byte - 127)
+ * The exponent is the smallest E in [-60, 60] with which no code is past 448 and no value of the position part past 2^15
+ * (60 if none is: larger ones are stored as those, RQ_STATUS_NORM_OVERFLOW).  A token with an infinity or NaN is stored as
+ * byte 255 over zeros and reads as NaN (RQ_STATUS_NOT_FINITE): rows that see it are NaN, rows that do not are not
+ * touched by it.  Pages may hold anything where no token was appended.
+ */
+typedef struct rq_latent rq_latent;  /* opaque, owned by the library */
+
+typedef struct {
+  int num_heads;             /* query heads, 1 to 1024 */
+  int latent_dim;            /* must be 512 */
+  int position_dim;          /* must be 64 */
+  int page_size;             /* P: a multiple of 16, at most 256 */
+  int num_pages;             /* pages in the caller's pool; times P below 2^31 */
+  int max_batch;             /* largest B of an attention call, at most 8000 */
+  int max_query_tokens;      /* largest T of an attention call */
+  int max_pages_per_seq;     /* largest block-table width; times P below 2^31 - 4096 */
+  float sm_scale;            /* softmax scale, the expanded heads' own; 0 selects 1/sqrt(192) */
+  int device;                /* CUDA device ordinal the context lives on; -1 = current */
+  int io_type;               /* RQ_F16 or RQ_BF16: latents, position parts, queries and outputs */
+} rq_latent_config;
+
+/* Source: this library.  Validates cfg and allocates the attention workspace (40 MB).  On success *out is a new context,
+   else NULL with nothing allocated.  Errors: RQ_ERR_INVALID, RQ_ERR_UNSUPPORTED, RQ_ERR_CUDA. */
+int rq_latent_create(rq_latent **out, const rq_latent_config *cfg);
+
+/* Source: this library.  Releases what rq_latent_create allocated.  NULL-safe; no call that uses it may still be running. */
+void rq_latent_free(rq_latent *ctx);
+
+/* Source: this library.  Bytes of a page, 641 P.  0 for NULL. */
+size_t rq_latent_page_bytes(const rq_latent *ctx);
+
+/* Rows of heads: token t, head h stands at x + t * stride + h * head_stride elements, so slices of a projection's output
+   and products that are laid out head after head are taken as they are. */
+typedef struct {
+  const void *x;             /* device, 16-byte aligned */
+  long long stride;          /* elements from token to token, a multiple of 8 */
+  long long head_stride;     /* elements from head to head, a multiple of 8, at least a head's dims */
+  int heads;
+} rq_heads;
+
+/*
+ * Source: this library.  Everything between the projections and the cache, in one launch: for token t < n the norm of
+ * its latent over 512 dims (weight: device float32 [512], 16-byte aligned; NULL: none), the rotation of its position part
+ * and of its queries' position parts, and the coding into slot slot_mapping[t] (page * P + offset).  A slot < 0 is
+ * skipped, one past the pool sets RQ_STATUS_BAD_SLOT and is skipped (its queries are turned all the same).  Slots of a call
+ * must be distinct.  The norm and the rotation are computed in float32 and coded from there.
+ *   rope        of rotary_dim at most 64; NULL: no rotation.  It must live on the context's device
+ *   c, k_pe     device, 16-byte aligned: token t at c + t * c_stride (512 elements) and k_pe + t * k_pe_stride (64);
+ *               strides are multiples of 8
+ *   q_pe        NULL, or the queries' position parts (64 elements a head, any number of heads)
+ *   q_pe_out    with q_pe: where they go, itself for in place; other overlaps with the call's inputs are refused, and so is
+ *               an output between the heads of q_pe
+ *   positions   device int32 [num_axes][n]; may be NULL without a rotation
+ * n = 0 is a no-op.  Errors: RQ_ERR_INVALID, RQ_ERR_CUDA.
+ */
+int rq_latent_append(rq_latent *ctx, const rq_rope *rope, const void *c, long long c_stride, const float *weight, float eps,
+                     const void *k_pe, long long k_pe_stride, const rq_heads *q_pe, const rq_heads *q_pe_out,
+                     const int32_t *positions, const int32_t *slot_mapping, int n, void *pages, int32_t *d_status, void *stream);
+
+/*
+ * Source: this library.  Attention in the absorbed form over the cache, of T query tokens per sequence, the last T
+ * cached tokens (append them first): a decode step (T = 1), a chain of drafts (tree_mask NULL: row j sees positions
+ * 0 .. seq_lens[b] - T + j) or a tree of them (device uint64 [B][T], T <= 64: row j sees the prefix and draft i exactly when bit
+ * i of tree_mask[b][j] is set).  A row that sees no token gives zeros.
+ *   q_c, q_pe   rows of num_heads heads, 512 and 64 elements, of B * T tokens
+ *   pages, block_table, max_pages, seq_lens   as rq_decode_attention
+ *   out         device [B][T][num_heads][512], 16-byte aligned
+ * 0 < seq_lens[b] < T sets RQ_STATUS_BAD_LEN.  Calls on one context must not overlap on the GPU.
+ * Errors: RQ_ERR_INVALID, RQ_ERR_CAPACITY (B, T or max_pages above the context's), RQ_ERR_CUDA.
+ */
+int rq_latent_attention(rq_latent *ctx, const rq_heads *q_c, const rq_heads *q_pe, int T, const uint64_t *tree_mask,
+                        const void *pages, const int32_t *block_table, int max_pages, const int32_t *seq_lens, int B, void *out,
+                        int32_t *d_status, void *stream);
+
+/*
+ * Source: this library.  Reads tokens back: positions starts[b] .. starts[b] + offsets[b + 1] - offsets[b] - 1 of sequence
+ * b into rows offsets[b] .. offsets[b + 1] - 1 of c [n][512] and k_pe [n][64] (device, 16-byte aligned, the context's io_type).
+ *   starts      device int32 [B], or NULL: from position 0
+ *   offsets     device int32 [B + 1], not falling
+ * Rows of no sequence are left as they are.  Positions outside the block table set RQ_STATUS_BAD_LEN, page ids outside the
+ * pool RQ_STATUS_BAD_PAGE; their rows are left as they are.  Errors: RQ_ERR_INVALID, RQ_ERR_CUDA.
+ */
+int rq_latent_read(rq_latent *ctx, const void *pages, const int32_t *block_table, int max_pages, const int32_t *starts,
+                   const int32_t *offsets, int B, int n, void *c, void *k_pe, int32_t *d_status, void *stream);
+
+/*
+ * Source: this library.  Causal attention of new tokens in the expanded form, for a batch of sequences packed one
+ * after the other: sequence b has queries q_offsets[b] .. q_offsets[b + 1] - 1 and keys k_offsets[b] .. k_offsets[b + 1] - 1, the
+ * queries being its last tokens: its query j sees its keys 0 .. nk_b - nq_b + j.  A head's key is its own 128 dims and the 64 that
+ * all heads share.  out = softmax(sm_scale (q[:128] . k + q[128:] . k_pe)) v; a row that sees no key gives zeros.
+ * Sequences whose offsets fall, pass nq or nk, or have more than max_new queries set RQ_STATUS_BAD_LEN and are skipped;
+ * rows of no sequence are left as they are.
+ */
+typedef struct {
+  rq_heads q;                /* [nq] rows of num_heads heads of 192 */
+  rq_heads k, v;             /* [nk] rows of num_heads heads of 128 */
+  const void *k_pe;          /* device [nk] rows of 64, 16-byte aligned */
+  long long k_pe_stride;     /* elements from row to row, a multiple of 8 */
+  void *out;                 /* device [nq][num_heads][128], 16-byte aligned */
+  const int32_t *q_offsets;  /* device int32 [B + 1] */
+  const int32_t *k_offsets;  /* device int32 [B + 1] */
+  int B;                     /* sequences, at most 65535 */
+  int nq, nk;                /* rows of q and out, rows of k, k_pe and v */
+  int max_new;               /* the most queries of a sequence */
+  float sm_scale;            /* 0 selects 1/sqrt(192) */
+  int io_type;               /* RQ_F16 or RQ_BF16 */
+} rq_prompt;
+
+/* On the current device, which every pointer must be of.  B or nq = 0 is a no-op.  Errors: RQ_ERR_INVALID, RQ_ERR_CUDA. */
+int rq_prompt_attention(const rq_prompt *args, int32_t *d_status, void *stream);
+
 /* Source: this library.  Diagnostics.  While set, every attention call records ev_start on its
    stream just before its split-K kernel and ev_end just after it (both cudaEvent_t created by the
    caller, who reads the elapsed time); NULL, NULL stops recording.  Costs nothing when unset. */

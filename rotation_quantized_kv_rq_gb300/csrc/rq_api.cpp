@@ -11,7 +11,12 @@
 #include <vector>
 
 #include "../../include/rq.h"
+#include "rq_host.h"
 #include "rq_internal.h"
+
+using rq::DeviceScope;
+using rq::misaligned16;
+using rq::to_status;
 
 struct rq_ctx {
   rq_config cfg;          // host pointers cleared after creation
@@ -37,26 +42,6 @@ struct rq_ctx {
 };
 
 namespace {
-
-// Makes `dev` current for the scope and restores the previous device afterwards.
-class DeviceScope {
- public:
-  explicit DeviceScope(int dev) {
-    ok_ = cudaGetDevice(&prev_) == cudaSuccess;
-    if (ok_ && dev >= 0 && dev != prev_) {
-      ok_ = cudaSetDevice(dev) == cudaSuccess;
-      switched_ = ok_;
-    }
-  }
-  ~DeviceScope() {
-    if (switched_) cudaSetDevice(prev_);
-  }
-  bool ok() const { return ok_; }
-
- private:
-  int prev_ = 0;
-  bool ok_ = false, switched_ = false;
-};
 
 // Lloyd-Max levels of the standard normal with 2^bits levels.  The quantizer is symmetric,
 // so only the positive half is iterated: cells [x_{k-1}, x_k) with x_0 = 0 and x_K = inf,
@@ -175,8 +160,6 @@ int create_block(rq_ctx* ctx, const rq_config* cfg) {
   return RQ_OK;
 }
 
-bool misaligned16(const void* p) { return (uintptr_t)p % 16 != 0; }
-
 // 1 / (2 pi) as a 128-bit binary fraction, high and low words.
 constexpr uint64_t kTurnHi = 0x28BE60DB9391054Aull, kTurnLo = 0x7F09D5F47D4D3770ull;
 
@@ -240,16 +223,7 @@ rq::RowsDev rows_dev(const rq_rows* r) {
   return d;
 }
 
-int to_status(cudaError_t e) { return e == cudaSuccess ? RQ_OK : RQ_ERR_CUDA; }
-
 }  // namespace
-
-struct rq_rope {
-  rq::RopeTable table;
-  uint64_t* d_pairs;
-  int device;
-  int num_sms;
-};
 
 extern "C" {
 

@@ -191,6 +191,79 @@ cudaError_t block_extend_prepare();
 cudaError_t launch_block_extend(const Geometry& g, AttnArgs a, int num_sms, cudaStream_t stream, cudaEvent_t ev_start,
                                 cudaEvent_t ev_end);
 
+// ---- latent attention ----
+
+constexpr int kLatentDim = 512, kPositionDim = 64, kPromptDim = 192;  // a latent, a position part, an expanded query or key
+constexpr int kLatentTokenBytes = 641;  // 512 codes, 64 16-bit values, an exponent byte
+
+// Rows of heads (rq_heads).
+struct HeadsDev {
+  const void* x;
+  long long stride, head_stride;
+  int heads;
+};
+
+struct LatentPool {
+  const uint8_t* pages;
+  int page_size, num_pages;
+  int bf16;
+};
+
+struct LatentAppendArgs {
+  const void *c, *k_pe;
+  long long c_stride, k_pe_stride;
+  const float* weight;
+  float eps;
+  HeadsDev q, q_out;  // heads 0: absent
+  RopeTable rope;
+  const int32_t* positions;
+  const int32_t* slots;
+  long long n;
+  int32_t* status;
+};
+cudaError_t launch_latent_append(const LatentPool& pool, const LatentAppendArgs& a, int num_sms, cudaStream_t stream);
+
+struct LatentReadArgs {
+  const int32_t* block_table;
+  int max_pages;
+  const int32_t* starts;
+  const int32_t* offsets;
+  int B, n;
+  void *c, *k_pe;
+  int32_t* status;
+};
+cudaError_t launch_latent_read(const LatentPool& pool, const LatentReadArgs& a, cudaStream_t stream);
+
+struct LatentAttnArgs {
+  HeadsDev q_c, q_pe;
+  int T;
+  const uint64_t* tree_mask;  // [B][T], or null
+  const int32_t* block_table;
+  int max_pages;
+  const int32_t* seq_lens;
+  int B, heads;
+  void* out;
+  float sm_scale;
+  int32_t* status;
+  float* ws;  // latent_attention_workspace floats
+};
+size_t latent_attention_workspace(int num_sms);
+cudaError_t latent_attention_prepare();
+cudaError_t launch_latent_attention(const LatentPool& pool, const LatentAttnArgs& a, int num_sms, cudaStream_t stream);
+
+struct PromptArgs {
+  HeadsDev q, k, v;
+  const void* k_pe;
+  long long k_pe_stride;
+  void* out;
+  const int32_t *q_offsets, *k_offsets;
+  int B, nq, nk, max_new;
+  float sm_scale;
+  int bf16;
+  int32_t* status;
+};
+cudaError_t launch_prompt_attention(const PromptArgs& a, cudaStream_t stream);
+
 // Dynamic shared memory the attention kernel needs (set as the kernel's maximum once).
 size_t attention_smem_bytes();
 cudaError_t attention_prepare();

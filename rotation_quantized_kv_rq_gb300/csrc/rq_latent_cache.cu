@@ -1,0 +1,297 @@
+// Append to the cache of latents, with the latent's norm and the position rotation on the way and the same tokens'
+// queries turned in the same launch, and reading the cache back.
+#include "../../include/rq.h"
+#include "rq_block.cuh"
+#include "rq_latent.cuh"
+#include "rq_rope.cuh"
+
+namespace rq {
+namespace {
+
+using namespace rope;
+using namespace latent;
+
+constexpr int kThreads = 256;
+constexpr uint32_t kInf = 0x7F800000u;
+constexpr uint32_t kMostCode = (kMaxExp + 8 + 127) << 23 | 0x600000u;  // 448 * 2^kMaxExp
+constexpr uint32_t kMostPart = (uint32_t)(kMaxExp + 15 + 127) << 23;   // 2^15 * 2^kMaxExp
+
+// The smallest E with top <= 2^(15 + E), within the range of scales.
+__device__ __forceinline__ int exp_of_part(float top) {
+  const uint32_t b = __float_as_uint(top);
+  return min(max((int)(b >> 23) - 127 - 15 + ((b & 0x7FFFFFu) != 0u ? 1 : 0), kMinExp), kMaxExp);
+}
+
+// A position part, 64 dims, is held by a half-warp, lane j dims 4j .. 4j + 3.  Pairs (2i, 2i + 1) are a lane's own; of
+// pairs (i, i + rotary_dim / 2) the other half is rotary_dim / 8 lanes away.
+struct Turn {
+  float c[4], s[4];  // of the pair of each of the four dims; s negated where the dim is a pair's first
+  int other;         // lane of the half-warp that holds the other halves; -1: past rotary_dim
+};
+template <bool INTERLEAVED>
+__device__ __forceinline__ Turn turn_of(const RopeTable& r, int j, const int32_t* positions, long long n, long long t) {
+  Turn u;
+  u.other = -1;
+  if (4 * j >= r.rotary_dim) return u;
+  if (INTERLEAVED) {
+    u.other = j;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float2 cs = cos_sin(r, 2 * j + i, positions, n, t);
+      u.c[2 * i] = u.c[2 * i + 1] = cs.x;
+      u.s[2 * i] = -cs.y, u.s[2 * i + 1] = cs.y;
+    }
+  } else {
+    const int away = r.rotary_dim >> 3;
+    const bool first = j < away;
+    u.other = first ? j + away : j - away;
+    const int pair = first ? 4 * j : 4 * (j - away);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 cs = cos_sin(r, pair + i, positions, n, t);
+      u.c[i] = cs.x;
+      u.s[i] = first ? -cs.y : cs.y;
+    }
+  }
+  return u;
+}
+// All lanes of the warp call it.
+template <bool INTERLEAVED>
+__device__ __forceinline__ void turn4(float (&x)[4], const Turn& u) {
+  float y[4];
+  if (INTERLEAVED) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) y[i] = x[i ^ 1];
+  } else {
+    const int from = (threadIdx.x & 16) | (u.other < 0 ? (threadIdx.x & 15) : u.other);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) y[i] = __shfl_sync(0xffffffffu, x[i], from);
+  }
+  if (u.other < 0) return;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) x[i] = fmaf(y[i], u.s[i], x[i] * u.c[i]);
+}
+
+template <typename T>
+__device__ __forceinline__ void widen4(float (&x)[4], const uint2& w) {
+  const float2 a = unpack2<T>(w.x), b = unpack2<T>(w.y);
+  x[0] = a.x, x[1] = a.y, x[2] = b.x, x[3] = b.y;
+}
+
+// Warp (token, part): part 0 codes the token's latent and position part, part 1 + i turns queries of heads
+// i * per .. .
+template <typename T, bool INTERLEAVED>
+__global__ void __launch_bounds__(kThreads) latent_append_kernel(const LatentPool pool, const LatentAppendArgs a, int parts, int per) {
+  const int lane = threadIdx.x & 31, j = lane & 15, half = lane >> 4;
+  const long long w = ((long long)blockIdx.x * kThreads + threadIdx.x) >> 5;
+  const long long t = w / parts;
+  if (t >= a.n) return;
+  const int part = (int)(w % parts);
+  Turn u;
+  u.other = -1;
+  if (a.rope.rotary_dim > 0) u = turn_of<INTERLEAVED>(a.rope, j, a.positions, a.n, t);
+  if (part > 0) {
+    const int first = (part - 1) * per, last = min(a.q.heads, first + per);
+    const T* src = reinterpret_cast<const T*>(a.q.x) + t * a.q.stride + 4 * j;
+    T* dst = reinterpret_cast<T*>(const_cast<void*>(a.q_out.x)) + t * a.q_out.stride + 4 * j;
+    constexpr int kBatch = 4;
+    for (int h0 = first; h0 < last; h0 += 2 * kBatch) {
+      uint2 raw[kBatch];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int h = h0 + 2 * i + half;
+        raw[i] = h < last ? *reinterpret_cast<const uint2*>(src + h * a.q.head_stride) : make_uint2(0u, 0u);  // (may be in place)
+      }
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int h = h0 + 2 * i + half;
+        float x[4];
+        widen4<T>(x, raw[i]);
+        turn4<INTERLEAVED>(x, u);
+        if (h < last)
+          *reinterpret_cast<uint2*>(dst + h * a.q_out.head_stride) = make_uint2(pack2<T>(x[0], x[1]), pack2<T>(x[2], x[3]));
+      }
+    }
+    return;
+  }
+  const int slot = __ldg(a.slots + t);
+  if (slot < 0) return;
+  if (slot >= pool.num_pages * pool.page_size) {
+    if (lane == 0 && a.status) atomicOr(a.status, RQ_STATUS_BAD_SLOT);
+    return;
+  }
+  // the latent: 16 dims to a lane, one chunk of codes
+  const uint4* row = reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(a.c) + t * a.c_stride) + 2 * lane;
+  const uint4 r0 = __ldg(row), r1 = __ldg(row + 1);
+  const uint2 rp = __ldg(reinterpret_cast<const uint2*>(reinterpret_cast<const T*>(a.k_pe) + t * a.k_pe_stride) + j);
+  float x[16];
+  {
+    const uint32_t w8[8] = {r0.x, r0.y, r0.z, r0.w, r1.x, r1.y, r1.z, r1.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float2 f = unpack2<T>(w8[i]);
+      x[2 * i] = f.x, x[2 * i + 1] = f.y;
+    }
+  }
+  if (a.weight) {
+    float ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) ss = fmaf(x[i], x[i], ss);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    const float r = __frsqrt_rn(fmaf(ss, 1.f / kLatentDim, a.eps));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float4 wt = __ldg(reinterpret_cast<const float4*>(a.weight) + 4 * lane + i);
+      x[4 * i] *= r * wt.x, x[4 * i + 1] *= r * wt.y, x[4 * i + 2] *= r * wt.z, x[4 * i + 3] *= r * wt.w;
+    }
+  }
+  float p[4];
+  widen4<T>(p, rp);
+  turn4<INTERLEAVED>(p, u);
+  uint32_t top_c = 0u, top_p = 0u;  // magnitudes order as their bits do, NaN above infinity above the rest
+#pragma unroll
+  for (int i = 0; i < 16; ++i) top_c = max(top_c, __float_as_uint(x[i]) & 0x7FFFFFFFu);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) top_p = max(top_p, __float_as_uint(p[i]) & 0x7FFFFFFFu);
+  top_c = __reduce_max_sync(0xffffffffu, top_c);
+  top_p = __reduce_max_sync(0xffffffffu, top_p);
+  const bool bad = max(top_c, top_p) >= kInf;
+  if (lane == 0 && a.status) {
+    const int fault = bad ? RQ_STATUS_NOT_FINITE : top_c > kMostCode || top_p > kMostPart ? RQ_STATUS_NORM_OVERFLOW : 0;
+    if (fault) atomicOr(a.status, fault);
+  }
+  const int e = max(block::exp_of(__uint_as_float(top_c)), exp_of_part(__uint_as_float(top_p)));
+  const float down = block::pow2(-e);
+  uint4 codes = make_uint4(0u, 0u, 0u, 0u);
+  uint2 pe = make_uint2(0u, 0u);
+  if (!bad) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) x[i] *= down;
+    codes = make_uint4(block::code4(x[0], x[1], x[2], x[3]), block::code4(x[4], x[5], x[6], x[7]),
+                       block::code4(x[8], x[9], x[10], x[11]), block::code4(x[12], x[13], x[14], x[15]));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) p[i] = fminf(fmaxf(p[i] * down, -32768.f), 32768.f);
+    pe = make_uint2(pack2<T>(p[0], p[1]), pack2<T>(p[2], p[3]));
+  }
+  const int P = pool.page_size, r = slot % P;
+  uint8_t* const page = const_cast<uint8_t*>(pool.pages) + page_at(slot / P, P);
+  *reinterpret_cast<uint4*>(page + (lane >> 3) * 128 * P + chunk_at(r, lane & 7)) = codes;
+  if (half == 0) *reinterpret_cast<uint2*>(page + 512 * P + chunk_at(r, j >> 1) + 8 * (j & 1)) = pe;
+  if (lane == 0) page[640 * P + r] = (uint8_t)(bad ? kNanExp : e + 127);
+}
+
+// A warp reads eight rows: their sequences and pages are looked up by a lane each, then their bytes are in flight together.
+constexpr int kRows = 8;
+template <typename T>
+__global__ void __launch_bounds__(kThreads) latent_read_kernel(const LatentPool pool, const LatentReadArgs a) {
+  const int lane = threadIdx.x & 31, P = pool.page_size;
+  const long long row0 = (((long long)blockIdx.x * kThreads + threadIdx.x) >> 5) * kRows;
+  if (row0 >= a.n) return;
+  const uint8_t* at = nullptr;  // page of the lane's row, and the row's offset in it
+  int r = 0;
+  {
+    const long long row = row0 + (lane & (kRows - 1));
+    int lo = 0, hi = a.B - 1;  // the last sequence that starts at or before the row
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (__ldg(a.offsets + mid) <= row) lo = mid; else hi = mid - 1;
+    }
+    const long long first = __ldg(a.offsets + lo), end = __ldg(a.offsets + lo + 1);
+    if (row < a.n && row >= first && row < end) {
+      const long long pos = (a.starts ? (long long)__ldg(a.starts + lo) : 0) + (row - first);
+      int fault = 0;
+      if (pos < 0 || pos >= (long long)a.max_pages * P || first < 0) {
+        fault = RQ_STATUS_BAD_LEN;
+      } else {
+        const int page = __ldg(a.block_table + (size_t)lo * a.max_pages + pos / P);
+        r = (int)(pos % P);
+        if (page < 0 || page >= pool.num_pages)
+          fault = RQ_STATUS_BAD_PAGE;
+        else
+          at = pool.pages + page_at(page, P);
+      }
+      if (fault && a.status) atomicOr(a.status, fault);
+    }
+  }
+  uint4 code[kRows];
+  float scale[kRows];
+  uint32_t there = __ballot_sync(0xffffffffu, at != nullptr);
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) {
+    const uint8_t* page = reinterpret_cast<const uint8_t*>(__shfl_sync(0xffffffffu, (unsigned long long)at, i));
+    const int ri = __shfl_sync(0xffffffffu, r, i);
+    if (there >> i & 1) {
+      code[i] = __ldg(reinterpret_cast<const uint4*>(page + (lane >> 3) * 128 * P + chunk_at(ri, lane & 7)));
+      scale[i] = scale_of_byte(__ldg(page + 640 * P + ri));
+    }
+  }
+  T* const c = reinterpret_cast<T*>(a.c);
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) {
+    if (!(there >> i & 1)) continue;
+    const uint32_t w[4] = {code[i].x, code[i].y, code[i].z, code[i].w};
+    uint32_t y[8];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float2 lo = unpack2<__half>(block::widen2(w[k])), hi = unpack2<__half>(block::widen2_hi(w[k]));
+      y[2 * k] = pack2<T>(lo.x * scale[i], lo.y * scale[i]);
+      y[2 * k + 1] = pack2<T>(hi.x * scale[i], hi.y * scale[i]);
+    }
+    uint4* dst = reinterpret_cast<uint4*>(c + (size_t)(row0 + i) * kLatentDim) + 2 * lane;
+    dst[0] = make_uint4(y[0], y[1], y[2], y[3]);
+    dst[1] = make_uint4(y[4], y[5], y[6], y[7]);
+  }
+  // position parts: four rows at a time, a chunk of eight values to a lane
+#pragma unroll
+  for (int i = 0; i < kRows; i += 4) {
+    const int k = i + (lane >> 3), chunk = lane & 7;
+    const uint8_t* page = reinterpret_cast<const uint8_t*>(__shfl_sync(0xffffffffu, (unsigned long long)at, k));
+    const int rk = __shfl_sync(0xffffffffu, r, k);
+    if (!(there >> k & 1)) continue;
+    const uint4 v = __ldg(reinterpret_cast<const uint4*>(page + 512 * P + chunk_at(rk, chunk)));
+    const float s = scale_of_byte(__ldg(page + 640 * P + rk));
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint32_t y[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const float2 f = unpack2<T>(w[q]);
+      y[q] = pack2<T>(f.x * s, f.y * s);
+    }
+    *reinterpret_cast<uint4*>(reinterpret_cast<T*>(a.k_pe) + (size_t)(row0 + k) * kPositionDim + 8 * chunk) =
+        make_uint4(y[0], y[1], y[2], y[3]);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_latent_append(const LatentPool& pool, const LatentAppendArgs& a, int num_sms, cudaStream_t stream) {
+  (void)num_sms;
+  const int per = 16, parts = 1 + (a.q.heads + per - 1) / per;
+  const long long ctas = (a.n * parts * 32 + kThreads - 1) / kThreads;
+  if (ctas > 0x7fffffffLL) return cudaErrorInvalidValue;
+  const unsigned grid = (unsigned)ctas;
+  if (pool.bf16) {
+    if (a.rope.interleaved)
+      latent_append_kernel<__nv_bfloat16, true><<<grid, kThreads, 0, stream>>>(pool, a, parts, per);
+    else
+      latent_append_kernel<__nv_bfloat16, false><<<grid, kThreads, 0, stream>>>(pool, a, parts, per);
+  } else {
+    if (a.rope.interleaved)
+      latent_append_kernel<__half, true><<<grid, kThreads, 0, stream>>>(pool, a, parts, per);
+    else
+      latent_append_kernel<__half, false><<<grid, kThreads, 0, stream>>>(pool, a, parts, per);
+  }
+  return cudaGetLastError();
+}
+
+cudaError_t launch_latent_read(const LatentPool& pool, const LatentReadArgs& a, cudaStream_t stream) {
+  const unsigned grid = (unsigned)(((long long)(a.n + kRows - 1) / kRows * 32 + kThreads - 1) / kThreads);
+  if (pool.bf16)
+    latent_read_kernel<__nv_bfloat16><<<grid, kThreads, 0, stream>>>(pool, a);
+  else
+    latent_read_kernel<__half><<<grid, kThreads, 0, stream>>>(pool, a);
+  return cudaGetLastError();
+}
+
+}  // namespace rq

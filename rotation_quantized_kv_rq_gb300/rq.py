@@ -24,13 +24,17 @@ RQ_PLANAR, RQ_ISO, RQ_DENSE = 0, 1, 2
 RQ_FP8 = 8
 RQ_F16, RQ_BF16 = 0, 1
 HEAD_DIM = 128
+LATENT_DIM, POSITION_DIM, PROMPT_DIM = 512, 64, 192  # a latent, a position part, a head's query in the expanded form
+LATENT_TOKEN_BYTES = 641
 BLOCK_TOKENS, BLOCK_BYTES = 16, 4112  # RQ_FP8: tokens that share a scale, bytes of such a block
 _IO_TYPES = {torch.float16: RQ_F16, torch.bfloat16: RQ_BF16}
 
 EXPORTS = ["rq_create", "rq_free", "rq_page_bytes", "rq_lloyd_max_codebook", "rq_get_codebook",
            "rq_quantize_append", "rq_decode_attention", "rq_verify_attention", "rq_set_profile_events",
            "rq_decode_attention_noalloc", "rq_tree_verify_attention", "rq_decode_step", "rq_extend_attention", "rq_status_string",
-           "rq_rope_create", "rq_rope_free", "rq_norm_rope", "rq_rope_append"]
+           "rq_rope_create", "rq_rope_free", "rq_norm_rope", "rq_rope_append",
+           "rq_latent_create", "rq_latent_free", "rq_latent_page_bytes", "rq_latent_append", "rq_latent_attention",
+           "rq_latent_read", "rq_prompt_attention"]
 
 
 class RQError(RuntimeError):
@@ -62,6 +66,28 @@ class rq_rows(ctypes.Structure):
     _fields_ = [
         ("x", ctypes.c_void_p), ("stride", ctypes.c_longlong), ("heads", ctypes.c_int), ("weight", ctypes.c_void_p),
         ("out", ctypes.c_void_p), ("out_stride", ctypes.c_longlong),
+    ]
+
+
+class rq_latent_config(ctypes.Structure):
+    _fields_ = [
+        ("num_heads", ctypes.c_int), ("latent_dim", ctypes.c_int), ("position_dim", ctypes.c_int), ("page_size", ctypes.c_int),
+        ("num_pages", ctypes.c_int), ("max_batch", ctypes.c_int), ("max_query_tokens", ctypes.c_int),
+        ("max_pages_per_seq", ctypes.c_int), ("sm_scale", ctypes.c_float), ("device", ctypes.c_int), ("io_type", ctypes.c_int),
+    ]
+
+
+class rq_heads(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("stride", ctypes.c_longlong), ("head_stride", ctypes.c_longlong),
+                ("heads", ctypes.c_int)]
+
+
+class rq_prompt(ctypes.Structure):
+    _fields_ = [
+        ("q", rq_heads), ("k", rq_heads), ("v", rq_heads), ("k_pe", ctypes.c_void_p), ("k_pe_stride", ctypes.c_longlong),
+        ("out", ctypes.c_void_p), ("q_offsets", ctypes.c_void_p), ("k_offsets", ctypes.c_void_p), ("B", ctypes.c_int),
+        ("nq", ctypes.c_int), ("nk", ctypes.c_int), ("max_new", ctypes.c_int), ("sm_scale", ctypes.c_float),
+        ("io_type", ctypes.c_int),
     ]
 
 
@@ -122,6 +148,21 @@ def lib(path: str | None = None) -> ctypes.CDLL:
             L.rq_rope_append.argtypes = [vp, vp, rows, rows, vp, ctypes.c_longlong, ctypes.c_float, vp, vp,
                                          ctypes.c_int, vp, vp, vp]
             L.rq_rope_append.restype = ctypes.c_int
+            ci, cll, heads = ctypes.c_int, ctypes.c_longlong, ctypes.POINTER(rq_heads)
+            L.rq_latent_create.argtypes = [ctypes.POINTER(vp), ctypes.POINTER(rq_latent_config)]
+            L.rq_latent_create.restype = ci
+            L.rq_latent_free.argtypes = [vp]
+            L.rq_latent_free.restype = None
+            L.rq_latent_page_bytes.argtypes = [vp]
+            L.rq_latent_page_bytes.restype = ctypes.c_size_t
+            L.rq_latent_append.argtypes = [vp, vp, vp, cll, vp, ctypes.c_float, vp, cll, heads, heads, vp, vp, ci, vp, vp, vp]
+            L.rq_latent_append.restype = ci
+            L.rq_latent_attention.argtypes = [vp, heads, heads, ci, vp, vp, vp, ci, vp, ci, vp, vp, vp]
+            L.rq_latent_attention.restype = ci
+            L.rq_latent_read.argtypes = [vp, vp, vp, ci, vp, vp, ci, ci, vp, vp, vp, vp]
+            L.rq_latent_read.restype = ci
+            L.rq_prompt_attention.argtypes = [ctypes.POINTER(rq_prompt), vp, vp]
+            L.rq_prompt_attention.restype = ci
             L.rq_status_string.argtypes = [ctypes.c_int]
             L.rq_status_string.restype = ctypes.c_char_p
             _lib = L
@@ -392,6 +433,79 @@ def rq_rope_append(ctx, rope, q, k, v, positions, slot_mapping, kv_pages, q_weig
                                 _stream(stream, kv_pages.device)))
 
 
+def rq_latent_create(num_heads: int, page_size: int, num_pages: int, max_batch: int, max_query_tokens: int = 1,
+                     max_pages_per_seq: int = 1, sm_scale: float = 0.0, device: int = -1, dtype=torch.float16,
+                     latent_dim: int = LATENT_DIM, position_dim: int = POSITION_DIM) -> ctypes.c_void_p:
+    """dtype: the element type of latents, position parts, queries and outputs, float16 or bfloat16."""
+    if dtype not in _IO_TYPES:
+        raise RQError("rq_latent_create", RQ_ERR_UNSUPPORTED)
+    ctx = Context()
+    ctx.dtype = dtype
+    cfg = rq_latent_config(num_heads, latent_dim, position_dim, page_size, num_pages, max_batch, max_query_tokens,
+                           max_pages_per_seq, float(sm_scale), int(device), _IO_TYPES[dtype])
+    _check("rq_latent_create", lib().rq_latent_create(ctypes.byref(ctx), ctypes.byref(cfg)))
+    return ctx
+
+
+def rq_latent_free(ctx) -> None:
+    lib().rq_latent_free(ctx)
+
+
+def rq_latent_page_bytes(ctx) -> int:
+    return int(lib().rq_latent_page_bytes(ctx))
+
+
+def _heads(t) -> rq_heads:
+    """rq_heads of t [n][heads][dims], any strides of tokens and heads; a dim's stride is checked by the callers."""
+    st = t.stride()
+    return rq_heads(t.data_ptr(), st[0], st[1], t.shape[1])
+
+
+def rq_latent_append(ctx, rope, c, k_pe, positions, slot_mapping, pages, weight=None, eps: float = 1e-6, q_pe=None,
+                     q_pe_out=None, status=None, stream=None) -> None:
+    """The low-level call; shapes and types are checked by LatentCache.append."""
+    _check("rq_latent_append",
+           lib().rq_latent_append(ctx, rope, c.data_ptr(), c.stride(0), _ptr(weight), float(eps), k_pe.data_ptr(),
+                                  k_pe.stride(0), None if q_pe is None else _heads(q_pe),
+                                  None if q_pe_out is None else _heads(q_pe_out), _ptr(positions), _ptr(slot_mapping),
+                                  slot_mapping.numel(), _ptr(pages), _ptr(status), _stream(stream, pages.device)))
+
+
+def rq_latent_attention(ctx, q_c, q_pe, tree_mask, pages, block_table, seq_lens, out, status=None, stream=None):
+    """q_c, q_pe: [B][T][heads][512 and 64], all B * T tokens in one stride; out [B][T][heads][512].  The low-level call;
+    shapes and types are checked by LatentCache."""
+    B, T, heads = q_c.shape[:3]
+    rows = []
+    for t in (q_c, q_pe):
+        st = t.stride()
+        if T > 1 and B > 1 and st[0] != T * st[1]:
+            raise RQError("rq_latent_attention", RQ_ERR_INVALID)
+        rows.append(rq_heads(t.data_ptr(), st[0] if T == 1 else st[1], st[2], heads))
+    _check("rq_latent_attention",
+           lib().rq_latent_attention(ctx, rows[0], rows[1], T, _ptr(tree_mask), _ptr(pages), _ptr(block_table),
+                                     block_table.shape[-1], _ptr(seq_lens), B, _ptr(out), _ptr(status),
+                                     _stream(stream, pages.device)))
+    return out
+
+
+def rq_latent_read(ctx, pages, block_table, starts, offsets, c, k_pe, status=None, stream=None):
+    """Into c [n][512], k_pe [n][64].  Checked by LatentCache.read."""
+    _check("rq_latent_read",
+           lib().rq_latent_read(ctx, _ptr(pages), _ptr(block_table), block_table.shape[-1], _ptr(starts), _ptr(offsets),
+                                offsets.numel() - 1, c.shape[0], _ptr(c), _ptr(k_pe), _ptr(status),
+                                _stream(stream, pages.device)))
+    return c, k_pe
+
+
+def rq_prompt_attention(q, k, k_pe, v, q_offsets, k_offsets, max_new, out, sm_scale=0.0, status=None, stream=None):
+    """The low-level call; shapes and types are checked by prompt_attention."""
+    args = rq_prompt(_heads(q), _heads(k), _heads(v), k_pe.data_ptr(), k_pe.stride(0), out.data_ptr(), q_offsets.data_ptr(),
+                     k_offsets.data_ptr(), q_offsets.numel() - 1, q.shape[0], k.shape[0], max_new, float(sm_scale),
+                     _IO_TYPES[q.dtype])
+    _check("rq_prompt_attention", lib().rq_prompt_attention(args, _ptr(status), _stream(stream, q.device)))
+    return out
+
+
 def rq_set_profile_events(ctx, ev_start=None, ev_end=None) -> None:
     """Record torch.cuda.Event pairs around the split-K attention kernel of later calls."""
     a = ctypes.c_void_p(ev_start.cuda_event) if ev_start is not None else None
@@ -578,3 +692,190 @@ class KVCache:
             self.close()
         except Exception:
             pass
+
+
+def _dense(t, dims, dtype, device) -> bool:
+    """t [n][heads][dims] (or [n][dims]) on the device, its last dim contiguous."""
+    return t.dtype == dtype and t.device == device and t.shape[-1] == dims and t.stride(-1) == 1
+
+
+def _ints(t, n, device) -> bool:
+    return t.dtype == torch.int32 and t.device == device and t.dim() == 1 and t.shape[0] == n and t.is_contiguous()
+
+
+class LatentCache:
+    """A cache of latents: one vector of 512 a token that all heads share (e4m3 codes) and one position part of 64 (16
+    bits), with a power-of-two scale a token; [num_pages][641 * page_size] uint8, and a status word.
+
+    dtype: float16 or bfloat16, of latents, position parts, queries and outputs.  sm_scale: the softmax scale of the
+    expanded heads (0: 1 / sqrt(192)).  pages: a pool of the caller's instead of a new one."""
+
+    def __init__(self, num_heads, page_size, num_pages, max_batch, max_query_tokens=1, max_pages_per_seq=None, sm_scale=0.0,
+                 device="cuda", dtype=torch.float16, pages=None):
+        self.ctx = None
+        self.device = torch.device(device)
+        if self.device.index is None:
+            self.device = torch.device("cuda", torch.cuda.current_device())
+        self.num_heads, self.page_size, self.num_pages, self.dtype = num_heads, page_size, num_pages, dtype
+        if max_pages_per_seq is None:
+            max_pages_per_seq = num_pages
+        self.ctx = rq_latent_create(num_heads, page_size, num_pages, max_batch, max_query_tokens, max_pages_per_seq, sm_scale,
+                                    self.device.index, dtype)
+        self.page_bytes = rq_latent_page_bytes(self.ctx)
+        shape = (num_pages, self.page_bytes)
+        if pages is None:
+            pages = torch.zeros(shape, dtype=torch.uint8, device=self.device)
+        elif (tuple(pages.shape) != shape or pages.dtype != torch.uint8 or pages.device != self.device or
+              not pages.is_contiguous()):
+            raise RQError("rq_latent_create", RQ_ERR_INVALID)
+        self.pages = pages
+        self._views = None
+        self.status = torch.zeros(1, dtype=torch.int32, device=self.device)
+
+    def append(self, c, k_pe, slot_mapping, rope=None, positions=None, weight=None, eps=1e-6, q_pe=None, q_pe_out=None,
+               stream=None):
+        """Everything between the projections and the cache in one launch: the norm (weight: float32 [512], or None) of
+        latents c [n][512], the rotation (rope: a Rope of rotary_dim <= 64, or None) of position parts k_pe [n][64] and of
+        the queries' q_pe [n][heads][64], and the coding into slot_mapping (int32 [n]).  Returns the turned q_pe (None without;
+        q_pe_out: where to write, q_pe itself for in place).  Slices of a projection's output are taken as they are."""
+        name, n, device, dtype = "rq_latent_append", slot_mapping.numel(), self.device, self.dtype
+        if (not _ints(slot_mapping, n, device) or c.shape != (n, LATENT_DIM) or not _dense(c, LATENT_DIM, dtype, device) or
+                k_pe.shape != (n, POSITION_DIM) or not _dense(k_pe, POSITION_DIM, dtype, device) or
+                (rope is not None and rope.device != device) or
+                (weight is not None and (weight.dtype != torch.float32 or weight.shape != (LATENT_DIM,) or
+                                         not weight.is_contiguous() or weight.device != device))):
+            raise RQError(name, RQ_ERR_INVALID)
+        if q_pe is not None:
+            if q_pe.dim() != 3 or q_pe.shape[0] != n or not _dense(q_pe, POSITION_DIM, dtype, device):
+                raise RQError(name, RQ_ERR_INVALID)
+            if q_pe_out is None:
+                q_pe_out = torch.empty(q_pe.shape, dtype=dtype, device=device)
+            elif q_pe_out.shape != q_pe.shape or not _dense(q_pe_out, POSITION_DIM, dtype, device):
+                raise RQError(name, RQ_ERR_INVALID)
+        elif q_pe_out is not None:
+            raise RQError(name, RQ_ERR_INVALID)
+        positions = rope.positions(positions, n, name) if rope is not None else None
+        if n:
+            rq_latent_append(self.ctx, rope.rope if rope is not None else None, c, k_pe, positions, slot_mapping, self.pages,
+                             weight, eps, q_pe, q_pe_out, self.status, stream)
+        return q_pe_out
+
+    def _attend(self, q_c, q_pe, tree_mask, block_table, seq_lens, out, stream):
+        name, device, dtype, heads = "rq_latent_attention", self.device, self.dtype, self.num_heads
+        if q_c.dim() != 4 or q_pe.dim() != 4:
+            raise RQError(name, RQ_ERR_INVALID)
+        B, T = q_c.shape[:2]
+        if (q_c.shape != (B, T, heads, LATENT_DIM) or not _dense(q_c, LATENT_DIM, dtype, device) or
+                q_pe.shape != (B, T, heads, POSITION_DIM) or not _dense(q_pe, POSITION_DIM, dtype, device) or T < 1 or
+                not _ints(seq_lens, B, device) or block_table.dtype != torch.int32 or block_table.device != device or
+                block_table.dim() != 2 or block_table.shape[0] != B or not block_table.is_contiguous() or
+                (tree_mask is not None and (tree_mask.dtype not in (torch.int64, torch.uint64) or
+                                            tree_mask.shape != (B, T) or not tree_mask.is_contiguous() or
+                                            tree_mask.device != device))):
+            raise RQError(name, RQ_ERR_INVALID)
+        if out is None:
+            out = torch.empty((B, T, heads, LATENT_DIM), dtype=dtype, device=device)
+        elif out.shape != q_c.shape or not out.is_contiguous() or out.dtype != dtype or out.device != device:
+            raise RQError(name, RQ_ERR_INVALID)
+        if B == 0:
+            return out
+        return rq_latent_attention(self.ctx, q_c, q_pe, tree_mask, self.pages, block_table, seq_lens, out, self.status, stream)
+
+    def decode(self, q_c, q_pe, block_table, seq_lens, out=None, stream=None):
+        """Absorbed attention of each sequence's newest token: q_c [B][heads][512], q_pe [B][heads][64], block_table
+        int32 [B][max_pages], seq_lens int32 [B]; the result is in the latents' space, [B][heads][512]."""
+        if q_c.dim() != 3 or q_pe.dim() != 3:
+            raise RQError("rq_latent_attention", RQ_ERR_INVALID)
+        return self._attend(q_c[:, None], q_pe[:, None], None, block_table, seq_lens, None if out is None else out[:, None],
+                            stream)[:, 0]
+
+    def verify(self, q_c, q_pe, block_table, seq_lens, out=None, stream=None):
+        """The same of the last T cached tokens of each sequence, row j up to its own: q_c [B][T][heads][512], q_pe
+        [B][T][heads][64]."""
+        return self._attend(q_c, q_pe, None, block_table, seq_lens, out, stream)
+
+    def tree_verify(self, q_c, q_pe, tree_mask, block_table, seq_lens, out=None, stream=None):
+        """verify with tree_mask int64/uint64 [B][T]: row j sees the prefix and draft i where bit i is set."""
+        if tree_mask is None:
+            raise RQError("rq_latent_attention", RQ_ERR_INVALID)
+        return self._attend(q_c, q_pe, tree_mask, block_table, seq_lens, out, stream)
+
+    def read(self, block_table, offsets, n, starts=None, c=None, k_pe=None, stream=None):
+        """Tokens read back, (c [n][512], k_pe [n][64]): rows offsets[b] .. offsets[b + 1] - 1 (offsets: int32 [B + 1]) are
+        sequence b's from position starts[b] (int32 [B]; None: 0) on.  Rows of no sequence are left as they are."""
+        name, device, dtype = "rq_latent_read", self.device, self.dtype
+        B = block_table.shape[0] if block_table.dim() == 2 else -1
+        if (B < 0 or n < 0 or block_table.dtype != torch.int32 or block_table.device != device or
+                not block_table.is_contiguous() or not _ints(offsets, B + 1, device) or
+                (starts is not None and not _ints(starts, B, device))):
+            raise RQError(name, RQ_ERR_INVALID)
+        if c is None:
+            c = torch.empty((n, LATENT_DIM), dtype=dtype, device=device)
+        if k_pe is None:
+            k_pe = torch.empty((n, POSITION_DIM), dtype=dtype, device=device)
+        for t, dims in ((c, LATENT_DIM), (k_pe, POSITION_DIM)):
+            if t.shape != (n, dims) or t.dtype != dtype or t.device != device or not t.is_contiguous():
+                raise RQError(name, RQ_ERR_INVALID)
+        if B and n:
+            rq_latent_read(self.ctx, self.pages, block_table, starts, offsets, c, k_pe, self.status, stream)
+        return c, k_pe
+
+    def codes(self):
+        """The pool's codes as float8_e4m3fn [num_pages][4][page_size][128] (a view), in the byte order of include/rq.h."""
+        return self._page_views()[0]
+
+    def position_parts(self):
+        """The pool's position parts before their scales, [num_pages][page_size][64] of the cache's dtype (a view, in the
+        byte order of include/rq.h)."""
+        return self._page_views()[1]
+
+    def scales(self):
+        """The scale of each token, float8_e8m0fnu [num_pages][page_size] (a view)."""
+        return self._page_views()[2]
+
+    def _page_views(self):
+        if self._views is None or self._views[3] is not self.pages:
+            P = self.page_size
+            self._views = (self.pages[:, :512 * P].view(torch.float8_e4m3fn).unflatten(1, (4, P, 128)),
+                           self.pages[:, 512 * P:640 * P].view(self.dtype).unflatten(1, (P, POSITION_DIM)),
+                           self.pages[:, 640 * P:].view(torch.float8_e8m0fnu), self.pages)
+        return self._views[:3]
+
+    def close(self):
+        if self.ctx is not None:
+            torch.cuda.synchronize(self.device)
+            rq_latent_free(self.ctx)
+            self.ctx = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+def prompt_attention(q, k, k_pe, v, q_offsets, k_offsets, max_new, sm_scale=0.0, out=None, status=None, stream=None):
+    """Causal attention of new tokens in the expanded form of latent attention, sequences packed one after the other: q
+    [nq][heads][192], k and v [nk][heads][128], k_pe [nk][64] (the part of the keys that all heads share), fp16 or bf16, any
+    strides of tokens and heads.  q_offsets, k_offsets: int32 [B + 1]; a sequence's queries are its last tokens, query j sees
+    its keys up to nk - nq + j.  max_new: the most queries of a sequence.  sm_scale 0: 1 / sqrt(192).  Returns
+    [nq][heads][128]; status (int32 [1]) collects RQ_STATUS_* bits."""
+    name, device, dtype = "rq_prompt_attention", q.device, q.dtype
+    if q.dim() != 3 or k.dim() != 3 or k_pe.dim() != 2 or v.dim() != 3 or dtype not in _IO_TYPES or q_offsets.dim() != 1:
+        raise RQError(name, RQ_ERR_INVALID)
+    nq, heads, nk, B = q.shape[0], q.shape[1], k.shape[0], q_offsets.shape[0] - 1
+    if (device.type != "cuda" or B < 0 or heads < 1 or k.shape != (nk, heads, 128) or v.shape != (nk, heads, 128) or
+            k_pe.shape != (nk, POSITION_DIM) or not _dense(q, PROMPT_DIM, dtype, device) or
+            not _dense(k, 128, dtype, device) or not _dense(v, 128, dtype, device) or
+            not _dense(k_pe, POSITION_DIM, dtype, device) or not _ints(q_offsets, B + 1, device) or
+            not _ints(k_offsets, B + 1, device) or max_new < 0 or
+            (status is not None and (status.dtype != torch.int32 or status.device != device))):
+        raise RQError(name, RQ_ERR_INVALID)
+    if out is None:
+        out = torch.empty((nq, heads, 128), dtype=dtype, device=device)
+    elif out.shape != (nq, heads, 128) or out.dtype != dtype or out.device != device or not out.is_contiguous():
+        raise RQError(name, RQ_ERR_INVALID)
+    if device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            return rq_prompt_attention(q, k, k_pe, v, q_offsets, k_offsets, max_new, out, sm_scale, status, stream)
+    return rq_prompt_attention(q, k, k_pe, v, q_offsets, k_offsets, max_new, out, sm_scale, status, stream)
