@@ -44,8 +44,8 @@
 
 #include "../../include/rq.h"
 #include "rq_block.cuh"
+#include "rq_roles.cuh"
 #include "rq_rope.cuh"
-#include "rq_tc.cuh"
 
 namespace rq {
 namespace {
@@ -93,92 +93,11 @@ static_assert(kRawStages == 4, "two tiles' halves");
 static_assert(kOffMisc % 16 == 0 && offsetof(Misc, scales) % 16 == 0, "float4 reads");
 static_assert(kSmem + 64 <= 232448, "one CTA's shared memory");
 
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float d;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-  return d;
-}
-__device__ __forceinline__ uint64_t pair(float lo, float hi) {
-  uint64_t d;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
-  return d;
-}
-__device__ __forceinline__ void unpair(uint64_t d, float& lo, float& hi) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(d));
-}
-__device__ __forceinline__ void fma2(float& x, float& y, uint64_t f, uint64_t b) {  // (x, y) = (x, y) * f + b
-  uint64_t d = pair(x, y);
-  asm("fma.rn.f32x2 %0, %0, %1, %2;" : "+l"(d) : "l"(f), "l"(b));
-  unpair(d, x, y);
-}
-__device__ __forceinline__ void add2(uint64_t& a, float x, float y) {
-  const uint64_t d = pair(x, y);
-  asm("add.rn.f32x2 %0, %0, %1;" : "+l"(a) : "l"(d));
-}
-__device__ __forceinline__ uint32_t word(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
-__device__ __forceinline__ uint32_t smem_addr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
-// A warp's wait, bounded (about a second) like tc::role_wait, but asleep between its looks at the
-// barrier.  All lanes look: one lane's loop beside 31 waiting ones took about 1000 cycles longer.
-__device__ __forceinline__ bool warp_wait(const uint64_t& bar, uint32_t parity, volatile int* abort_flag) {
-  bool ok = false;
-  for (int i = 0; i < (1 << 16); ++i) {
-    uint32_t done;
-    asm volatile("{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}"
-                 : "=r"(done)
-                 : "r"(smem_addr(&bar)), "r"(parity & 1), "r"(20000u)  // ns
-                 : "memory");
-    ok = done;
-    if (done || *abort_flag) break;
-  }
-  if (!ok) *abort_flag = 1;
-  return __all_sync(0xffffffffu, ok);
-}
-// A warp's arrival, by one lane (a predicate, no branch) behind all lanes' accesses.
-__device__ __forceinline__ void warp_arrive(uint64_t& bar) {
-  __syncwarp();
-  asm volatile("{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n @e mbarrier.arrive.shared::cta.b64 _, [%0];\n}" ::"r"(
-                   smem_addr(&bar))
-               : "memory");
-}
-// The MMAs and commit of tc::, by one elected lane of a whole warp: with the operands uniform over the
-// warp an MMA is issued in 16 to 22 cycles, against 50 in a branch that one lane takes.
-__device__ __forceinline__ void elect_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t accumulate) {
-  asm volatile(
-      "{\n .reg .pred p, e;\n elect.sync _|e, 0xffffffff;\n setp.ne.b32 p, %4, 0;\n"
-      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
-      "l"(a), "l"(b), "r"(id), "r"(accumulate));
-}
-__device__ __forceinline__ void elect_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t accumulate) {
-  asm volatile(
-      "{\n .reg .pred p, e;\n elect.sync _|e, 0xffffffff;\n setp.ne.b32 p, %4, 0;\n"
-      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
-      "r"(a), "l"(b), "r"(id), "r"(accumulate));
-}
-__device__ __forceinline__ void elect_commit(uint32_t mbar) {
-  asm volatile(
-      "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
-      " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}" ::"r"(mbar)
-      : "memory");
-}
 // Place of column c of a half tile: the token's offset.
 __host__ __device__ constexpr int token_of(int c) {
   const int i = c & 3, t = c >> 3 & 3;
   return 32 * (c >> 5) + 16 * (c >> 2 & 1) + 2 * t + (i & 1) + 8 * (i >> 1);
 }
-__device__ __forceinline__ uint4 lds128(uint32_t addr) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
-  return v;
-}
-__device__ __forceinline__ void sts128(uint32_t addr, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
-  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
-}
-
 // One unit's geometry: 256 rows rb of sequence b.
 struct Unit {
   int len, tiles;

@@ -262,7 +262,7 @@ struct PromptArgs {
   int bf16;
   int32_t* status;
 };
-cudaError_t launch_prompt_attention(const PromptArgs& a, cudaStream_t stream);
+cudaError_t launch_prompt_attention(const PromptArgs& a, int num_sms, cudaStream_t stream);
 
 // Dynamic shared memory the attention kernel needs (set as the kernel's maximum once).
 size_t attention_smem_bytes();

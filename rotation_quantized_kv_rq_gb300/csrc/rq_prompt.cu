@@ -1,75 +1,561 @@
-// Causal attention of new tokens in the expanded form of latent attention: heads of 192 (128 of their own and 64 that
-// all heads share) against values of 128, sequences packed one after the other.
+// Causal attention of new tokens in the expanded form of latent attention, sequences packed one after the other: heads of
+// 192 (128 of their own and 64 that all heads share) against values of 128, on the 5th-generation tensor cores.
+//
+// score = scale (q[:128] . k + q[128:] . k_pe), out = sum softmax(score) v, in one pass over the keys with a running maximum
+// and sum.  What bounds it is the tensor cores' rate: 640 flops a visible (row, key) of a head.
+//
+// A CTA (one per SM) takes 256 query rows of one (sequence, head), two blocks of 128, and walks its keys in tiles of
+// 128, its warps specialised and coupled through mbarriers:
+//   softmax (warps 0-7, a thread per row): takes its row of S from tensor memory into registers, masks, writes 16-bit
+//     weights over S;
+//   MMA (warp 8): for each block in turn O_b += W_b V(t) and behind it S_b(t + 1) = Q_b K(t + 1)^T, so that one block is on the
+//     tensor cores while the other is in its softmax;
+//   copies (warp 9): TMA tiles straight from the caller's tensors, whatever their strides, into a ring of eight 16 KB
+//     slots: a tile's keys are three of them (64 dims each, the shared part the third), its values two (64 keys each).  A
+//     slot is given back when its last MMAs are done, not when the tile is: the 96 KB of queries leave room for 1.6 tiles;
+//   values (warps 10, 11): in tiles that some row of the CTA sees in part, values that are not finite are taken out before the
+//     weights, zeros among them, are multiplied with them, and given to the rows that see them at the end.
+// Tensor memory: O_b at columns 128 b, S_b at 256 + 128 b with W_b over its first half.
+// Few rows and long sequences: a cluster of up to eight CTAs shares a unit's tiles, and joins through distributed shared memory.
+// Every wait is bounded: one that runs out sets RQ_STATUS_TIMEOUT and an abort flag every role polls.
+#include <cuda.h>
 #include <math_constants.h>
 
+#include <cstddef>
+#include <type_traits>
+
 #include "../../include/rq.h"
+#include "rq_roles.cuh"
 #include "rq_rope.cuh"
 
 namespace rq {
 namespace {
 
-constexpr int kThreads = 128;
+using namespace tc;
 
-// One row of one head a CTA: a thread a key for the scores, then a thread a dim for the sum.
+constexpr int kSoftWarps = 8, kFixWarps = 2, kMmaWarp = 8, kCopyWarp = 9, kFixWarp = 10, kThreads = 384;
+constexpr int kHalf = 128, kRows = 256, kTok = 128, kDim = 128;
+constexpr int kSlots = 8;                        // of the ring
+constexpr uint32_t kSlotBytes = 16384, kQBytes = 6 * kSlotBytes;
+constexpr uint32_t kColS = 256;
+constexpr float kLift = 7.f, kReach = 15.f;      // weights are 2^(score - m), m between maximum - kReach and maximum - kLift
+constexpr float kNone = -3.402823466e38f;        // m before any visible key
+constexpr float kLarge = 1048576.f;              // |maximum| from which weights are formed in two roundings
+constexpr int kMaxSplit = 8;
+
+struct Misc {
+  uint64_t full[kSlots], empty[kSlots], q_full, s_full[2], p_full[2], o_done[2], fix_ask, fix_done, drain;
+  uint32_t tmem;
+  int abort, any;
+  int from[3][kDim];       // first key with +inf, -inf, NaN among a dim's values
+};
+constexpr uint32_t kOffRing = kQBytes, kOffMisc = kOffRing + kSlots * kSlotBytes;
+constexpr int kSmem = (int)(kOffMisc + sizeof(Misc)) + 1024;
+static_assert(kSmem <= 232448, "one CTA's shared memory");
+constexpr uint32_t kOffML = kRows * kDim * 4;  // a part's rows for the join stand over queries and ring, then the rows' m and l
+static_assert(kOffML + 2 * kRows * 4 <= kOffMisc, "a part's rows for the join");
+
+// Instruction descriptor of kind::f16 for T (fp16 0, bf16 1 at bits 7 and 10); bit 16: B with N along its rows.
 template <typename T>
-__global__ void __launch_bounds__(kThreads) prompt_rows_kernel(const PromptArgs a) {
-  __shared__ float q[kPromptDim], w[kThreads], red[kThreads / 32];
-  const int tid = threadIdx.x, j = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
-  const int q0 = __ldg(a.q_offsets + b), q1 = __ldg(a.q_offsets + b + 1);
-  const int k0 = __ldg(a.k_offsets + b), k1 = __ldg(a.k_offsets + b + 1);
+__host__ __device__ constexpr uint32_t idesc(int M, int N, int b_rows) {
+  const uint32_t type = std::is_same<T, __half>::value ? 0u : 1u;
+  return idesc_f16(M, N) | type << 7 | type << 10 | (uint32_t)b_rows << 16;
+}
+// Values: K along keys (eight to 1024 bytes), N along dims, 64 of them to a 128-byte row and 8192 bytes to the next 64.
+__device__ __forceinline__ uint64_t vdesc(uint32_t saddr) {
+  return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)(8192 >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) |
+         ((uint64_t)2 << 61);
+}
+__device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap& map, int x, int y, int z, uint32_t bar) {
+  asm volatile(
+      "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
+      " @e cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];\n}" ::"r"(dst),
+      "l"(&map), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void expect(uint32_t bar, uint32_t bytes) {
+  asm volatile("{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n @e mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n}" ::"r"(bar),
+               "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
+  uint32_t r[32];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,"
+      "%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]),
+        "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),
+        "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]),
+        "=r"(r[31])
+      : "r"(taddr));
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The address of a peer's shared memory, and loads from there.
+__device__ __forceinline__ uint32_t peer_addr(uint32_t addr, uint32_t rank) {
+  uint32_t a;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
+  return a;
+}
+__device__ __forceinline__ float peer_ld(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ float4 peer_ld4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+
+struct Maps {
+  CUtensorMap q, k, pe, v;
+};
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_constant__ Maps maps, const PromptArgs a, int splits) {
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t base = smem_addr(smem_raw) + (1024 - (smem_addr(smem_raw) & 1023) & 1023);
+  uint8_t* const smem = smem_raw + (base - smem_addr(smem_raw));
+  Misc& ms = *reinterpret_cast<Misc*>(smem + kOffMisc);
+  const uint32_t q_ops = base, ring = base + kOffRing;
+  volatile int* const abort_flag = &ms.abort;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int part = blockIdx.x % splits, h = blockIdx.x / splits, b = blockIdx.y;
+
+  // ---- the unit: rows r0 .. r0 + 255 of sequence b, the ones with the most keys first ----
+  const int q0 = __ldg(a.q_offsets + b), q1 = __ldg(a.q_offsets + b + 1), k0 = __ldg(a.k_offsets + b), k1 = __ldg(a.k_offsets + b + 1);
   if (q0 < 0 || q1 < q0 || q1 > a.nq || k0 < 0 || k1 < k0 || k1 > a.nk || q1 - q0 > a.max_new) {
     if (tid == 0 && a.status) atomicOr(a.status, RQ_STATUS_BAD_LEN);
     return;
   }
-  if (j >= q1 - q0) return;
-  const T* row = reinterpret_cast<const T*>(a.q.x) + (q0 + (long long)j) * a.q.stride + h * a.q.head_stride;
-  for (int i = tid; i < kPromptDim; i += kThreads) q[i] = (float)row[i] * (a.sm_scale * 1.44269504088896340736f);
-  const int end = (k1 - k0) - (q1 - q0) + j + 1;
-  float m = -CUDART_INF_F, l = 0.f, acc = 0.f;
-  for (int t0 = 0; t0 < end; t0 += kThreads) {
-    const int p = t0 + tid;
-    __syncthreads();
-    float s = -CUDART_INF_F;
-    if (p < end) {
-      const T* k = reinterpret_cast<const T*>(a.k.x) + (k0 + (long long)p) * a.k.stride + h * a.k.head_stride;
-      const T* pe = reinterpret_cast<const T*>(a.k_pe) + (k0 + (long long)p) * a.k_pe_stride;
-      s = 0.f;
-      for (int i = 0; i < 128; ++i) s = fmaf(q[i], (float)k[i], s);
-      for (int i = 0; i < 64; ++i) s = fmaf(q[128 + i], (float)pe[i], s);
+  const int nq = q1 - q0, nk = k1 - k0, ahead = nk - nq, n_rb = (nq + kRows - 1) / kRows;
+  if ((int)blockIdx.z >= n_rb) return;  // (a cluster's CTAs alike)
+  const int r0 = (n_rb - 1 - (int)blockIdx.z) * kRows;
+  // tiles that a block's rows see, and this part's range of them
+  auto tiles_to = [&](int row) { return max(0, (ahead + min(nq, row) + kTok - 1) / kTok); };
+  const int all0 = tiles_to(r0 + kHalf), all1 = r0 + kHalf < nq ? tiles_to(r0 + kRows) : 0, all = max(all0, all1);
+  const int t_first = (int)((long long)part * all / splits), t_end = (int)((long long)(part + 1) * all / splits);
+  const int n = t_end - t_first;
+  const int n_b[2] = {min(max(all0 - t_first, 0), n), min(max(all1 - t_first, 0), n)};
+  // from this tile on, rows of the CTA see tiles in part
+  const int t_fix = max(0, (ahead + r0 + 1) / kTok - t_first);
+
+  if (tid == 0) {
+    for (int i = 0; i < kSlots; ++i) {
+      mbar_init(smem_addr(&ms.full[i]), 1);
+      mbar_init(smem_addr(&ms.empty[i]), 1);
     }
-    float top = s;
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    if ((tid & 31) == 0) red[tid >> 5] = top;
-    __syncthreads();
-    top = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
-    const float m_new = fmaxf(m, top), from = m_new == -CUDART_INF_F ? 0.f : m_new;
-    const float alpha = m == -CUDART_INF_F ? 0.f : exp2f(m - from);
-    m = m_new;
-    const float e = p < end ? exp2f(s - from) : 0.f;
-    w[tid] = e;
-    float sum = e;
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    __syncthreads();
-    if ((tid & 31) == 0) red[tid >> 5] = sum;
-    __syncthreads();
-    l = l * alpha + (red[0] + red[1] + red[2] + red[3]);
-    acc *= alpha;
-    const T* v = reinterpret_cast<const T*>(a.v.x) + (k0 + (long long)t0) * a.v.stride + h * a.v.head_stride + tid;
-    for (int k = 0; k < min(kThreads, end - t0); ++k) acc = fmaf(w[k], (float)v[k * a.v.stride], acc);
+    mbar_init(smem_addr(&ms.q_full), 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_addr(&ms.s_full[i]), 1);
+      mbar_init(smem_addr(&ms.p_full[i]), kSoftWarps / 2);
+      mbar_init(smem_addr(&ms.o_done[i]), 1);
+    }
+    mbar_init(smem_addr(&ms.fix_ask), 1);
+    mbar_init(smem_addr(&ms.fix_done), kFixWarps);
+    mbar_init(smem_addr(&ms.drain), 1);
+    ms.abort = 0;
+    ms.any = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  const float y = end <= 0 ? 0.f : acc / l;
-  reinterpret_cast<T*>(a.out)[((q0 + (size_t)j) * a.q.heads + h) * 128 + tid] = (T)y;
+  for (int i = tid; i < 3 * kDim; i += kThreads) ms.from[i / kDim][i % kDim] = INT32_MAX;
+  __syncwarp();
+  if (warp == kMmaWarp) tmem_alloc(smem_addr(&ms.tmem), 512);
+  fence_before_sync();
+  __syncthreads();
+  fence_after_sync();
+  const uint32_t tmem = *(volatile uint32_t*)&ms.tmem;
+  const uint32_t lane_off = (uint32_t)(32 * (warp & 3)) << 16;
+  const int blk = warp >> 2 & 1, brow = 32 * (warp & 3) + lane, row = r0 + kHalf * blk + brow;
+  const bool valid = row < nq;
+  const int qpos = valid ? ahead + row : -1;  // the last key that the row sees
+  float m_run = kNone, l_run = 0.f;
+  bool ok = true;
+  uint32_t loaded = 0;  // copies: slots asked for
+  // slots of tile t in the order of use: K(0) V(0) K(1) V(1) ...
+  auto k_slot = [](int t) { return 5u * t; };
+  auto v_slot = [](int t) { return 5u * t + 3u; };
+
+  if (warp < kSoftWarps) {
+    // ================= softmax: one thread per row =================
+    const float scale = a.sm_scale * 1.44269504088896340736f;
+    const uint32_t s_tile = tmem + lane_off + kColS + 128 * blk, o_cols = tmem + lane_off + 128 * blk;
+    float from = 0.f;
+    for (int t = 0; t < n_b[blk]; ++t) {
+      const int t0 = (t_first + t) * kTok;
+      ok = warp_wait(ms.s_full[blk], t, abort_flag);  // S_b(t), and W_b(t - 1) V before it
+      if (!ok) break;
+      fence_after_sync();
+      float s[kTok];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) tmem_ld32(s_tile + 32 * c, s + 32 * c);
+      tmem_wait_ld();
+      settle<kTok>(s);
+      if (t0 + kTok - 1 > qpos) {
+#pragma unroll
+        for (int c = 0; c < kTok; ++c)
+          if (t0 + c > qpos) s[c] = -CUDART_INF_F;
+      }
+      float top[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+      for (int c = 4; c < kTok; c += 8) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) top[i] = c + 4 + i < kTok ? max3(top[i], s[c + i], s[c + 4 + i]) : fmaxf(top[i], s[c + i]);
+      }
+      const float most = fmaxf(max3(top[0], top[1], top[2]), top[3]) * scale;
+      const float above = most - (m_run == kNone ? -CUDART_INF_F : m_run);  // (NaN where nothing is seen: no move)
+      if (__any_sync(0xffffffffu, above > kReach)) {
+        float alpha = 1.f;
+        if (above > kReach) {
+          from = most - kLift;
+          alpha = ex2(m_run - from);
+          m_run = from;
+          l_run *= alpha;
+        }
+        if (t > 0) {  // O *= alpha (the warp's rows)
+#pragma unroll 1
+          for (int c = 0; c < kDim / 16; ++c) {
+            float v[16];
+            tmem_ld16(o_cols + 16 * c, v);
+            tmem_wait_ld();
+            settle<16>(v);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v[i] *= alpha;
+            tmem_st16(o_cols + 16 * c, v);
+          }
+        }
+      }
+      if (__any_sync(0xffffffffu, fabsf(from) > kLarge)) {  // the difference needs the rounded product
+#pragma unroll
+        for (int c = 0; c < kTok; ++c) s[c] = s[c] * scale - from;
+      } else {
+        const uint64_t f = pair(scale, scale), d = pair(-from, -from);
+#pragma unroll
+        for (int c = 0; c < kTok; c += 2) fma2(s[c], s[c + 1], f, d);
+      }
+      uint64_t sum[2] = {0ull, 0ull};
+#pragma unroll
+      for (int c = 0; c < kTok; c += 32) {
+        uint32_t pw[16];
+#pragma unroll
+        for (int i = 0; i < 32; i += 2) {
+          const float w0 = ex2(s[c + i]), w1 = ex2(s[c + i + 1]);
+          add2(sum[i >> 1 & 1], w0, w1);
+          pw[i >> 1] = rope::pack2<T>(w0, w1);
+        }
+        tmem_st16u(s_tile + c / 2, pw);
+      }
+      float x[4];
+      unpair(sum[0], x[0], x[1]);
+      unpair(sum[1], x[2], x[3]);
+      l_run += (x[0] + x[1]) + (x[2] + x[3]);
+      tmem_wait_st();
+      fence_before_sync();
+      warp_arrive(ms.p_full[blk]);
+    }
+    if (ok && n_b[blk] > 0) ok = warp_wait(ms.o_done[blk], 0, abort_flag);
+    fence_after_sync();
+  } else if (warp == kMmaWarp) {
+    // ================= MMA issue =================
+    constexpr uint32_t id_s = idesc<T>(kHalf, kTok, 0), id_o = idesc<T>(kHalf, kDim, 1);
+    const int last_b = n_b[1] > 0 ? 1 : 0;  // the block that uses a tile last
+    bool issued = false;
+    int fixed = 0;
+    auto wait = [&](uint64_t& bar, uint32_t parity) { return ok = warp_wait(bar, parity, abort_flag); };
+    auto s_mmas = [&](int bb, int t) {  // S_b(t)
+#pragma unroll
+      for (int c = 0; c < 3; ++c) {
+        const uint32_t at = k_slot(t) + c, sl = at % kSlots;
+        if (!wait(ms.full[sl], at / kSlots)) return;
+        const uint32_t q_at = q_ops + (3 * bb + c) * kSlotBytes, k_at = ring + sl * kSlotBytes;
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks)
+          elect_mma_ss(tmem + kColS + 128 * bb, sdesc(q_at + 32 * ks), sdesc(k_at + 32 * ks), id_s, c > 0 || ks > 0);
+        issued = true;
+        if (bb == last_b) elect_commit(smem_addr(&ms.empty[sl]));
+      }
+      elect_commit(smem_addr(&ms.s_full[bb]));
+    };
+    if (n > 0) wait(ms.q_full, 0);
+#pragma unroll
+    for (int bb = 0; bb < 2; ++bb)
+      if (ok && n_b[bb] > 0) s_mmas(bb, 0);
+    for (int t = 0; t < n && ok; ++t) {
+      bool first = true;
+#pragma unroll
+      for (int bb = 0; bb < 2; ++bb) {
+        if (!ok || t >= n_b[bb]) continue;
+        if (first && t >= t_fix) {  // the values' warps look at this tile
+          bool there = true;
+          for (int c = 0; c < 2 && there; ++c) there = wait(ms.full[(v_slot(t) + c) % kSlots], (v_slot(t) + c) / kSlots);
+          if (!there) break;
+          warp_arrive(ms.fix_ask);
+          if (!wait(ms.fix_done, fixed++)) break;
+        }
+        first = false;
+        if (!wait(ms.p_full[bb], t)) break;
+        fence_after_sync();
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const uint32_t at = v_slot(t) + c, sl = at % kSlots;
+          if (!wait(ms.full[sl], at / kSlots)) break;
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks)  // keys 64 c + 16 ks ..
+            elect_mma_ts(tmem + 128 * bb, tmem + kColS + 128 * bb + 32 * c + 8 * ks, vdesc(ring + sl * kSlotBytes + 2048 * ks), id_o,
+                         t > 0 || c > 0 || ks > 0);
+          if (bb == last_b) elect_commit(smem_addr(&ms.empty[sl]));
+        }
+        if (!ok) break;
+        if (t + 1 < n_b[bb])
+          s_mmas(bb, t + 1);  // over the same columns, behind the MMAs that read them
+        else
+          elect_commit(smem_addr(&ms.o_done[bb]));
+      }
+    }
+    if (!ok && issued) {  // nothing may be running when the tensor memory is freed
+      elect_commit(smem_addr(&ms.drain));
+      for (int i = 0; i < kWaitLimit; ++i)
+        if (mbar_test(smem_addr(&ms.drain), 0u)) break;
+    }
+  } else if (warp == kCopyWarp) {
+    // ================= copies =================
+    if (n > 0) {
+      expect(smem_addr(&ms.q_full), kQBytes);
+#pragma unroll
+      for (int i = 0; i < 6; ++i)
+        load_box(q_ops + i * kSlotBytes, maps.q, 64 * (i % 3), h, q0 + r0 + kHalf * (i / 3), smem_addr(&ms.q_full));
+    }
+    auto slot = [&](uint32_t at) {  // the bar of slot `at`, once it is free; 0 after a wait that ran out
+      const uint32_t sl = at % kSlots;
+      if (at >= kSlots && !(ok = warp_wait(ms.empty[sl], at / kSlots - 1, abort_flag))) return 0u;
+      loaded = at + 1;
+      expect(smem_addr(&ms.full[sl]), kSlotBytes);
+      return smem_addr(&ms.full[sl]);
+    };
+    auto keys = [&](int t) {
+      const int z = k0 + (t_first + t) * kTok;
+      for (int c = 0; c < 3; ++c) {
+        const uint32_t bar = slot(k_slot(t) + c), dst = ring + (k_slot(t) + c) % kSlots * kSlotBytes;
+        if (!ok) return;
+        if (c < 2)
+          load_box(dst, maps.k, 64 * c, h, z, bar);
+        else
+          load_box(dst, maps.pe, 0, 0, z, bar);
+      }
+    };
+    if (n > 0) keys(0);
+    for (int t = 0; t < n && ok; ++t) {
+      for (int c = 0; c < 2 && ok; ++c) {
+        const uint32_t bar = slot(v_slot(t) + c), dst = ring + (v_slot(t) + c) % kSlots * kSlotBytes;
+        if (!ok) break;
+        const int z = k0 + (t_first + t) * kTok + 64 * c;
+        load_box(dst, maps.v, 0, h, z, bar);
+        load_box(dst + 8192, maps.v, 64, h, z, bar);
+      }
+      if (ok && t + 1 < n) keys(t + 1);
+    }
+  } else if (warp < kFixWarp + kFixWarps) {
+    // ================= values that are not finite, in tiles seen in part =================
+    // 16-bit halves whose exponent is all ones, two to a word
+    constexpr bool kF16 = std::is_same<T, __half>::value;
+    constexpr uint32_t kExp = kF16 ? 0x7C007C00u : 0x7F807F80u, kOne = kF16 ? 0x04000400u : 0x00800080u;
+    for (int t = t_fix, i = 0; t < n; ++t, ++i) {
+      if (!(ok = warp_wait(ms.fix_ask, i, abort_flag))) break;
+      bool any = false;
+      for (int c = 0; c < 2 && ok; ++c) {
+        const uint32_t at = v_slot(t) + c, sl = at % kSlots;
+        if (!(ok = warp_wait(ms.full[sl], at / kSlots, abort_flag))) break;  // complete: the MMA warp has waited for it
+        // row (key) r of half d (64 dims): eight chunks; a warp takes one half
+        const int d = warp - kFixWarp;
+        for (int r8 = 0; r8 < 16; ++r8) {
+          const int r = 4 * r8 + (lane >> 3), chunk = lane & 7;
+          const uint32_t addr = ring + sl * kSlotBytes + 8192 * d + sw128(r, chunk);
+          const uint4 v = lds128(addr);
+          const uint32_t odd = ((v.x & kExp) + kOne) | ((v.y & kExp) + kOne) | ((v.z & kExp) + kOne) | ((v.w & kExp) + kOne);
+          if (!(odd & 0x80008000u)) continue;
+          const int key = (t_first + t) * kTok + 64 * c + r;
+          uint32_t w[4];
+          for (int k = 0; k < 4; ++k) {
+            w[k] = word(v, k);
+            for (int s = 0; s < 2; ++s) {
+              const uint32_t x = w[k] >> (16 * s) & 0xFFFFu, e = kExp & 0xFFFFu;
+              if ((x & e) != e) continue;
+              const int kind = (x & 0x7FFFu) != e ? 2 : x >> 15 ? 1 : 0;
+              if (key < nk) {
+                atomicMin(&ms.from[kind][64 * d + 8 * chunk + 2 * k + s], key);
+                ms.any = 1;
+              }
+              w[k] &= s ? 0x0000FFFFu : 0xFFFF0000u;
+            }
+          }
+          sts128(addr, w[0], w[1], w[2], w[3]);
+          any = true;
+        }
+      }
+      if (!ok) break;
+      if (any) fence_async_smem();
+      warp_arrive(ms.fix_done);
+    }
+  }
+  if (!ok && lane == 0 && a.status) atomicOr(a.status, RQ_STATUS_TIMEOUT);
+  fence_before_sync();
+  __syncthreads();
+  fence_after_sync();
+  const bool aborted = ms.abort != 0;
+
+  // ---- write the rows, or join the parts ----
+  T* const out = reinterpret_cast<T*>(a.out) + ((size_t)q0 * a.q.heads + h) * kDim;
+  if (warp < kSoftWarps && !aborted) {
+    const float empty = qpos >= 0 ? CUDART_NAN_F : 0.f;  // a row whose scores are all minus infinity; one that sees nothing
+    const float inv = splits == 1 ? 1.f / l_run : 1.f;
+#pragma unroll 2
+    for (int c = 0; c < kDim / 16; ++c) {
+      float y[16];
+      if (n_b[blk] > 0) {
+        __syncwarp();
+        tmem_ld16(tmem + lane_off + 128 * blk + 16 * c, y);
+        tmem_wait_ld();
+        settle<16>(y);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) y[i] = l_run == 0.f ? (splits == 1 ? empty : 0.f) : y[i] * inv;
+      } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) y[i] = 0.f;
+      }
+      if (ms.any) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          if (ms.from[0][16 * c + i] <= qpos) y[i] += CUDART_INF_F;
+          if (ms.from[1][16 * c + i] <= qpos) y[i] -= CUDART_INF_F;
+          if (ms.from[2][16 * c + i] <= qpos) y[i] = CUDART_NAN_F;
+        }
+      }
+      if (splits > 1) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          reinterpret_cast<float4*>(smem)[(4 * c + i) * kRows + kHalf * blk + brow] =
+              make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
+      } else if (valid) {
+        uint4* const dst = reinterpret_cast<uint4*>(out + (size_t)row * a.q.heads * kDim) + 2 * c;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          dst[i] = make_uint4(rope::pack2<T>(y[8 * i], y[8 * i + 1]), rope::pack2<T>(y[8 * i + 2], y[8 * i + 3]),
+                              rope::pack2<T>(y[8 * i + 4], y[8 * i + 5]), rope::pack2<T>(y[8 * i + 6], y[8 * i + 7]));
+      }
+    }
+    if (splits > 1) {
+      float* const ml = reinterpret_cast<float*>(smem + kOffML);
+      ml[kHalf * blk + brow] = m_run;
+      ml[kRows + kHalf * blk + brow] = l_run;
+    }
+  }
+  if (aborted && warp == kCopyWarp) {  // copies in flight land before the block ends
+    for (uint32_t i = loaded > kSlots ? loaded - kSlots : 0; i < loaded; ++i)
+      for (int w = 0; w < kWaitLimit; ++w)
+        if (mbar_test(smem_addr(&ms.full[i % kSlots]), (i / kSlots) & 1)) break;
+    if (n > 0)
+      for (int w = 0; w < kWaitLimit; ++w)
+        if (mbar_test(smem_addr(&ms.q_full), 0u)) break;
+  }
+  if (splits > 1) {
+    cluster_sync();
+    // rows `per` of this part's share; a warp takes a row at a time, a lane four dims
+    const int per = kRows / splits;
+    for (int i = warp; i < per && !aborted; i += kThreads / 32) {
+      const int rr = part * per + i;
+      if (r0 + rr >= nq) break;
+      float m = kNone, sum = 0.f;
+      float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int f = 0; f < splits; ++f) {
+        const float mf = peer_ld(peer_addr(base + kOffML + 4 * rr, f)), lf = peer_ld(peer_addr(base + kOffML + 4 * (kRows + rr), f));
+        const float4 v = peer_ld4(peer_addr(base + (uint32_t)(lane * kRows + rr) * 16, f));
+        const float to = fmaxf(m, mf), wa = ex2(m - to), w = ex2(mf - to);
+        m = to;
+        sum = fmaf(sum, wa, lf * w);
+        y.x = fmaf(y.x, wa, v.x * w), y.y = fmaf(y.y, wa, v.y * w), y.z = fmaf(y.z, wa, v.z * w), y.w = fmaf(y.w, wa, v.w * w);
+      }
+      const float none = ahead + r0 + rr >= 0 ? CUDART_NAN_F : 0.f, inv = 1.f / sum;
+      if (sum == 0.f)
+        y = make_float4(none, none, none, none);
+      else
+        y = make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv);
+      *reinterpret_cast<uint2*>(out + (size_t)(r0 + rr) * a.q.heads * kDim + 4 * lane) =
+          make_uint2(rope::pack2<T>(y.x, y.y), rope::pack2<T>(y.z, y.w));
+    }
+    cluster_sync();  // a peer's shared memory is read until here
+  }
+  __syncthreads();
+  if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
+}
+
+typedef CUresult (*EncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                             const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeFn encoder() {
+  static const EncodeFn fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &found) != cudaSuccess ||
+        found != cudaDriverEntryPointSuccess)
+      p = nullptr;
+    return (EncodeFn)p;
+  }();
+  return fn;
+}
+
+// Boxes of 64 dims and `box` rows of one head of x [n][heads][dims].
+bool encode(CUtensorMap* map, bool bf16, const HeadsDev& x, int dims, int n, int box) {
+  const cuuint64_t sizes[3] = {(cuuint64_t)dims, (cuuint64_t)x.heads, (cuuint64_t)n};
+  // a stride that is not used (one head, one row) may be anything
+  const cuuint64_t strides[2] = {(cuuint64_t)(x.heads > 1 ? x.head_stride : dims) * 2, (cuuint64_t)(n > 1 ? x.stride : dims) * 2};
+  const cuuint32_t boxes[3] = {64u, 1u, (cuuint32_t)box}, steps[3] = {1u, 1u, 1u};
+  return encoder()(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(x.x), sizes, strides,
+                   boxes, steps, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename T>
+cudaError_t launch(const Maps& maps, const PromptArgs& a, int splits, int n_rb, cudaStream_t stream) {
+  static_assert(sizeof(Maps) + sizeof(PromptArgs) + 16 <= 4096, "kernel parameters");
+  cudaError_t e = cudaFuncSetAttribute(prompt_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(a.q.heads * splits), (unsigned)a.B, (unsigned)n_rb);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmem;
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = (unsigned)splits;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, prompt_kernel<T>, maps, a, splits);
 }
 
 }  // namespace
 
-cudaError_t launch_prompt_attention(const PromptArgs& a, cudaStream_t stream) {
-  const dim3 grid((unsigned)a.max_new, (unsigned)a.q.heads, (unsigned)a.B);
-  if (a.bf16)
-    prompt_rows_kernel<__nv_bfloat16><<<grid, kThreads, 0, stream>>>(a);
-  else
-    prompt_rows_kernel<__half><<<grid, kThreads, 0, stream>>>(a);
-  return cudaGetLastError();
+cudaError_t launch_prompt_attention(const PromptArgs& a, int num_sms, cudaStream_t stream) {
+  if (!encoder()) return cudaErrorNotSupported;
+  const int n_rb = (a.max_new + kRows - 1) / kRows;
+  if (n_rb > 65535) return cudaErrorInvalidValue;
+  Maps maps{};
+  HeadsDev k = a.k, v = a.v, pe{a.k_pe, a.k_pe_stride, 0, 1};
+  if (a.nk == 0) k = v = pe = a.q;  // no key is ever read
+  const int nk = a.nk > 0 ? a.nk : 1;
+  if (!encode(&maps.q, a.bf16, a.q, kPromptDim, a.nq, kHalf) || !encode(&maps.k, a.bf16, k, kDim, nk, kTok) ||
+      !encode(&maps.pe, a.bf16, pe, kPositionDim, nk, kTok) || !encode(&maps.v, a.bf16, v, kDim, nk, kTok / 2))
+    return cudaErrorInvalidValue;
+  // few units: the most parts (a power of two) that leave every SM at most one of them, and each some 4 tiles at the batch's
+  // mean length
+  const long long units = (long long)a.B * n_rb * a.q.heads, tiles = a.nk / a.B / kTok;
+  int splits = 1;
+  while (splits < kMaxSplit && units * 2 * splits <= num_sms && tiles >= 8 * splits) splits *= 2;
+  return a.bf16 ? launch<__nv_bfloat16>(maps, a, splits, n_rb, stream) : launch<__half>(maps, a, splits, n_rb, stream);
 }
 
 }  // namespace rq

@@ -506,6 +506,8 @@ def check_prompt(out, q, k, pe, v, qo, ko, dtype, sm=0.0):
     ([5, 1, 300], [1000, 127, 128], 5),
     ([600], [400], 1),
     ([1, 1], [511, 0], 16),
+    ([3, 200], [5000, 9000], 2),     # few units: a cluster shares each one's keys
+    ([2, 1, 300], [0, 7000, 900], 3),
 ])
 def test_prompt(dtype, new, old, heads):
     dtype = DT[dtype]
