@@ -213,7 +213,7 @@ int rq_latent_read(rq_latent* ctx, const void* pages, const int32_t* block_table
 }
 
 int rq_prompt_attention(const rq_prompt* p, int32_t* d_status, void* stream) {
-  if (!p || p->B < 0 || p->B > 65535 || p->nq < 0 || p->nk < 0 || p->max_new < 0 || p->max_new > 65535 * 256 || !(p->sm_scale >= 0.f) ||
+  if (!p || p->B < 0 || p->B > 65535 || p->nq < 0 || p->nk < 0 || p->max_new < 0 || p->max_new > 65535 * 512 || !(p->sm_scale >= 0.f) ||
       std::isinf(p->sm_scale) || (p->io_type != RQ_F16 && p->io_type != RQ_BF16))
     return RQ_ERR_INVALID;
   if (p->B == 0 || p->nq == 0 || p->max_new == 0) return RQ_OK;

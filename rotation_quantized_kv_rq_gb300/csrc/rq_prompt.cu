@@ -4,20 +4,21 @@
 // score = scale (q[:128] . k + q[128:] . k_pe), out = sum softmax(score) v, in one pass over the keys with a running maximum
 // and sum.  What bounds it is the tensor cores' rate: 640 flops a visible (row, key) of a head.
 //
-// A CTA (one per SM) takes 256 query rows of one (sequence, head), two blocks of 128, and walks its keys in tiles of
-// 128, its warps specialised and coupled through mbarriers:
-//   softmax (warps 0-7, a thread per row): takes its row of S from tensor memory into registers, masks, writes 16-bit
-//     weights over S;
-//   MMA (warp 8): for each block in turn O_b += W_b V(t) and behind it S_b(t + 1) = Q_b K(t + 1)^T, so that one block is on the
-//     tensor cores while the other is in its softmax;
-//   copies (warp 9): TMA tiles straight from the caller's tensors, whatever their strides, into a ring of eight 16 KB
-//     slots: a tile's keys are three of them (64 dims each, the shared part the third), its values two (64 keys each).  A
-//     slot is given back when its last MMAs are done, not when the tile is: the 96 KB of queries leave room for 1.6 tiles;
-//   values (warps 10, 11): in tiles that some row of the CTA sees in part, values that are not finite are taken out before the
-//     weights, zeros among them, are multiplied with them, and given to the rows that see them at the end.
+// A pair of CTAs (two SMs) takes 512 query rows of one (sequence, head), two blocks of 256, 128 rows of each block to a
+// CTA, and walks the keys in tiles of 128.  Its MMAs span both (M = 256): each CTA holds half of a tile's keys and half of its
+// values' dims, 40 KB a tile instead of 80, so that three tiles stand beside the 96 KB of queries.  (One CTA alone, with
+// 1.6 tiles, waited for its loads: 4,950 cycles a tile, 1 x 16,384 x 16 heads 1,134 us.)  Warps are specialised and
+// coupled through mbarriers:
+//   softmax (warps 0-7 of both, a thread per row): takes its row of S from tensor memory into registers, masks, writes
+//     16-bit weights over S;
+//   MMA (warp 8 of the leader): for each block in turn O_b += W_b V(t) and behind it S_b(t + 1) = Q_b K(t + 1)^T, so that one block
+//     is on the tensor cores while the other is in its softmax;
+//   copies (warp 9 of both): TMA tiles straight from the caller's tensors, whatever their strides;
+//   values (warps 10, 11 of both): in tiles that some row of the pair sees in part, values that are not finite are taken
+//     out before the weights, zeros among them, are multiplied with them, and given to the rows that see them at the end.
 // Tensor memory: O_b at columns 128 b, S_b at 256 + 128 b with W_b over its first half.
-// Few rows and long sequences: a cluster of up to eight CTAs shares a unit's tiles, and joins through distributed shared memory.
-// Every wait is bounded: one that runs out sets RQ_STATUS_TIMEOUT and an abort flag every role polls.
+// Few rows and long sequences: a cluster of up to four pairs shares a unit's tiles, and joins through distributed shared
+// memory.  Every wait is bounded: one that runs out sets RQ_STATUS_TIMEOUT and an abort flag every role polls.
 #include <cuda.h>
 #include <math_constants.h>
 
@@ -34,25 +35,30 @@ namespace {
 using namespace tc;
 
 constexpr int kSoftWarps = 8, kFixWarps = 2, kMmaWarp = 8, kCopyWarp = 9, kFixWarp = 10, kThreads = 384;
-constexpr int kHalf = 128, kRows = 256, kTok = 128, kDim = 128;
-constexpr int kSlots = 8;                        // of the ring
-constexpr uint32_t kSlotBytes = 16384, kQBytes = 6 * kSlotBytes;
+constexpr int kHalf = 128, kRows = 256, kUnitRows = 512;  // rows of a block in a CTA, of a CTA, of a pair
+constexpr int kTok = 128, kDim = 128;
+constexpr int kStages = 3;                               // tiles of keys, and of values
+constexpr uint32_t kChunk = 16384;                       // 128 rows of 64 dims
+constexpr uint32_t kQBytes = 6 * kChunk, kKBytes = 3 * kChunk / 2, kVBytes = kChunk;  // a CTA's
 constexpr uint32_t kColS = 256;
 constexpr float kLift = 7.f, kReach = 15.f;      // weights are 2^(score - m), m between maximum - kReach and maximum - kLift
 constexpr float kNone = -3.402823466e38f;        // m before any visible key
 constexpr float kLarge = 1048576.f;              // |maximum| from which weights are formed in two roundings
-constexpr int kMaxSplit = 8;
+constexpr int kMaxSplit = 4;
 
 struct Misc {
-  uint64_t full[kSlots], empty[kSlots], q_full, s_full[2], p_full[2], o_done[2], fix_ask, fix_done, drain;
+  // the leader's: K(t), V(t), the queries are there; [block] W(t); the values' warps are through with a tile
+  uint64_t k_full[kStages], v_full[kStages], q_full, p_full[2], fix_done[kStages];
+  // both CTAs': K(t), V(t) are read; [block] S(t); [block] the last W V; drained; a CTA's values of a tile seen in part
+  uint64_t k_empty[kStages], v_empty[kStages], s_full[2], o_done[2], drain, v_here[kStages];
   uint32_t tmem;
   int abort, any;
-  int from[3][kDim];       // first key with +inf, -inf, NaN among a dim's values
+  int from[3][kDim / 2];   // first key with +inf, -inf, NaN among the values of a dim of the CTA's half
 };
-constexpr uint32_t kOffRing = kQBytes, kOffMisc = kOffRing + kSlots * kSlotBytes;
+constexpr uint32_t kOffK = kQBytes, kOffV = kOffK + kStages * kKBytes, kOffMisc = kOffV + kStages * kVBytes;
 constexpr int kSmem = (int)(kOffMisc + sizeof(Misc)) + 1024;
 static_assert(kSmem <= 232448, "one CTA's shared memory");
-constexpr uint32_t kOffML = kRows * kDim * 4;  // a part's rows for the join stand over queries and ring, then the rows' m and l
+constexpr uint32_t kOffML = kRows * kDim * 4;  // a part's rows for the join stand over queries and tiles, then the rows' m and l
 static_assert(kOffML + 2 * kRows * 4 <= kOffMisc, "a part's rows for the join");
 
 // Instruction descriptor of kind::f16 for T (fp16 0, bf16 1 at bits 7 and 10); bit 16: B with N along its rows.
@@ -61,22 +67,20 @@ __host__ __device__ constexpr uint32_t idesc(int M, int N, int b_rows) {
   const uint32_t type = std::is_same<T, __half>::value ? 0u : 1u;
   return idesc_f16(M, N) | type << 7 | type << 10 | (uint32_t)b_rows << 16;
 }
-// Values: K along keys (eight to 1024 bytes), N along dims, 64 of them to a 128-byte row and 8192 bytes to the next 64.
-__device__ __forceinline__ uint64_t vdesc(uint32_t saddr) {
-  return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)(8192 >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) |
-         ((uint64_t)2 << 61);
+// A box of the tensor to this CTA's shared memory; the bytes count at a barrier of the leader (pair_bar), or of this CTA.
+__device__ __forceinline__ void load_pair(uint32_t dst, const CUtensorMap& map, int x, int y, int z, uint32_t pair_bar) {
+  asm volatile(
+      "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
+      " @e cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3, %4}], [%5];\n}"
+      ::"r"(dst), "l"(&map), "r"(x), "r"(y), "r"(z), "r"(pair_bar)
+      : "memory");
 }
-__device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap& map, int x, int y, int z, uint32_t bar) {
+__device__ __forceinline__ void load_here(uint32_t dst, const CUtensorMap& map, int x, int y, int z, uint32_t bar) {
   asm volatile(
       "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
       " @e cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];\n}" ::"r"(dst),
       "l"(&map), "r"(x), "r"(y), "r"(z), "r"(bar)
       : "memory");
-}
-__device__ __forceinline__ void expect(uint32_t bar, uint32_t bytes) {
-  asm volatile("{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n @e mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n}" ::"r"(bar),
-               "r"(bytes)
-               : "memory");
 }
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
   uint32_t r[32];
@@ -91,26 +95,6 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
 #pragma unroll
   for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-// The address of a peer's shared memory, and loads from there.
-__device__ __forceinline__ uint32_t peer_addr(uint32_t addr, uint32_t rank) {
-  uint32_t a;
-  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
-  return a;
-}
-__device__ __forceinline__ float peer_ld(uint32_t addr) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
-  return v;
-}
-__device__ __forceinline__ float4 peer_ld4(uint32_t addr) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
-  return v;
-}
-
 struct Maps {
   CUtensorMap q, k, pe, v;
 };
@@ -121,64 +105,64 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
   const uint32_t base = smem_addr(smem_raw) + (1024 - (smem_addr(smem_raw) & 1023) & 1023);
   uint8_t* const smem = smem_raw + (base - smem_addr(smem_raw));
   Misc& ms = *reinterpret_cast<Misc*>(smem + kOffMisc);
-  const uint32_t q_ops = base, ring = base + kOffRing;
+  const uint32_t q_ops = base, k_ring = base + kOffK, v_ring = base + kOffV;
   volatile int* const abort_flag = &ms.abort;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int part = blockIdx.x % splits, h = blockIdx.x / splits, b = blockIdx.y;
+  const uint32_t cta = cluster_rank(), rank = cta & 1, lead = cta & ~1u;  // parts of a unit are pairs of its cluster
+  const int part = (int)(cta >> 1), h = (int)blockIdx.x / (2 * splits), b = blockIdx.y;
 
-  // ---- the unit: rows r0 .. r0 + 255 of sequence b, the ones with the most keys first ----
+  // ---- the unit: rows r0 .. r0 + 511 of sequence b, the ones with the most keys first ----
   const int q0 = __ldg(a.q_offsets + b), q1 = __ldg(a.q_offsets + b + 1), k0 = __ldg(a.k_offsets + b), k1 = __ldg(a.k_offsets + b + 1);
   if (q0 < 0 || q1 < q0 || q1 > a.nq || k0 < 0 || k1 < k0 || k1 > a.nk || q1 - q0 > a.max_new) {
     if (tid == 0 && a.status) atomicOr(a.status, RQ_STATUS_BAD_LEN);
     return;
   }
-  const int nq = q1 - q0, nk = k1 - k0, ahead = nk - nq, n_rb = (nq + kRows - 1) / kRows;
+  const int nq = q1 - q0, nk = k1 - k0, ahead = nk - nq, n_rb = (nq + kUnitRows - 1) / kUnitRows;
   if ((int)blockIdx.z >= n_rb) return;  // (a cluster's CTAs alike)
-  const int r0 = (n_rb - 1 - (int)blockIdx.z) * kRows;
+  const int r0 = (n_rb - 1 - (int)blockIdx.z) * kUnitRows;
   // tiles that a block's rows see, and this part's range of them
   auto tiles_to = [&](int row) { return max(0, (ahead + min(nq, row) + kTok - 1) / kTok); };
-  const int all0 = tiles_to(r0 + kHalf), all1 = r0 + kHalf < nq ? tiles_to(r0 + kRows) : 0, all = max(all0, all1);
+  const int all0 = tiles_to(r0 + kRows), all1 = r0 + kRows < nq ? tiles_to(r0 + kUnitRows) : 0, all = max(all0, all1);
   const int t_first = (int)((long long)part * all / splits), t_end = (int)((long long)(part + 1) * all / splits);
   const int n = t_end - t_first;
   const int n_b[2] = {min(max(all0 - t_first, 0), n), min(max(all1 - t_first, 0), n)};
-  // from this tile on, rows of the CTA see tiles in part
-  const int t_fix = max(0, (ahead + r0 + 1) / kTok - t_first);
+  // from this tile on, rows of the pair see tiles in part
+  const int t_fix = max(0, max(0, ahead + r0 + 1) / kTok - t_first);
 
   if (tid == 0) {
-    for (int i = 0; i < kSlots; ++i) {
-      mbar_init(smem_addr(&ms.full[i]), 1);
-      mbar_init(smem_addr(&ms.empty[i]), 1);
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(smem_addr(&ms.k_full[i]), 1);
+      mbar_init(smem_addr(&ms.v_full[i]), 1);
+      mbar_init(smem_addr(&ms.k_empty[i]), 1);
+      mbar_init(smem_addr(&ms.v_empty[i]), 1);
+      mbar_init(smem_addr(&ms.v_here[i]), 1);
+      mbar_init(smem_addr(&ms.fix_done[i]), 2 * kFixWarps);
     }
     mbar_init(smem_addr(&ms.q_full), 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_addr(&ms.s_full[i]), 1);
-      mbar_init(smem_addr(&ms.p_full[i]), kSoftWarps / 2);
+      mbar_init(smem_addr(&ms.p_full[i]), kSoftWarps);  // four warps of either CTA
       mbar_init(smem_addr(&ms.o_done[i]), 1);
     }
-    mbar_init(smem_addr(&ms.fix_ask), 1);
-    mbar_init(smem_addr(&ms.fix_done), kFixWarps);
     mbar_init(smem_addr(&ms.drain), 1);
     ms.abort = 0;
     ms.any = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  for (int i = tid; i < 3 * kDim; i += kThreads) ms.from[i / kDim][i % kDim] = INT32_MAX;
+  for (int i = tid; i < 3 * kDim / 2; i += kThreads) (&ms.from[0][0])[i] = INT32_MAX;
   __syncwarp();
-  if (warp == kMmaWarp) tmem_alloc(smem_addr(&ms.tmem), 512);
+  if (warp == kMmaWarp) pair_tmem_alloc(smem_addr(&ms.tmem), 512);
   fence_before_sync();
   __syncthreads();
+  cluster_sync();  // the peer's barriers are there
   fence_after_sync();
   const uint32_t tmem = *(volatile uint32_t*)&ms.tmem;
   const uint32_t lane_off = (uint32_t)(32 * (warp & 3)) << 16;
-  const int blk = warp >> 2 & 1, brow = 32 * (warp & 3) + lane, row = r0 + kHalf * blk + brow;
+  const int blk = warp >> 2 & 1, brow = 32 * (warp & 3) + lane, row = r0 + kRows * blk + kHalf * (int)rank + brow;
   const bool valid = row < nq;
   const int qpos = valid ? ahead + row : -1;  // the last key that the row sees
   float m_run = kNone, l_run = 0.f;
   bool ok = true;
-  uint32_t loaded = 0;  // copies: slots asked for
-  // slots of tile t in the order of use: K(0) V(0) K(1) V(1) ...
-  auto k_slot = [](int t) { return 5u * t; };
-  auto v_slot = [](int t) { return 5u * t + 3u; };
 
   if (warp < kSoftWarps) {
     // ================= softmax: one thread per row =================
@@ -255,150 +239,122 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
       l_run += (x[0] + x[1]) + (x[2] + x[3]);
       tmem_wait_st();
       fence_before_sync();
-      warp_arrive(ms.p_full[blk]);
+      warp_arrive_pair(peer_addr(smem_addr(&ms.p_full[blk]), lead));
     }
     if (ok && n_b[blk] > 0) ok = warp_wait(ms.o_done[blk], 0, abort_flag);
     fence_after_sync();
   } else if (warp == kMmaWarp) {
-    // ================= MMA issue =================
-    constexpr uint32_t id_s = idesc<T>(kHalf, kTok, 0), id_o = idesc<T>(kHalf, kDim, 1);
-    const int last_b = n_b[1] > 0 ? 1 : 0;  // the block that uses a tile last
-    bool issued = false;
-    int fixed = 0;
-    auto wait = [&](uint64_t& bar, uint32_t parity) { return ok = warp_wait(bar, parity, abort_flag); };
-    auto s_mmas = [&](int bb, int t) {  // S_b(t)
+    // ================= MMA issue: the leader's =================
+    if (rank == 0 && n > 0) {
+      constexpr uint32_t id_s = idesc<T>(kRows, kTok, 0), id_o = idesc<T>(kRows, kDim, 1);
+      const int last_b = n_b[1] > 0 ? 1 : 0;  // the block that uses a tile last
+      const uint32_t both = 3u << cta;
+      bool issued = false;
+      auto wait = [&](uint64_t& bar, uint32_t parity) { return ok = warp_wait(bar, parity, abort_flag); };
+      auto s_mmas = [&](int bb, int t) {  // S_b(t)
+        const int st = t % kStages;
+        if (!wait(ms.k_full[st], t / kStages)) return;
+        const uint32_t q_at = q_ops + 3 * bb * kChunk, k_at = k_ring + st * kKBytes;
 #pragma unroll
-      for (int c = 0; c < 3; ++c) {
-        const uint32_t at = k_slot(t) + c, sl = at % kSlots;
-        if (!wait(ms.full[sl], at / kSlots)) return;
-        const uint32_t q_at = q_ops + (3 * bb + c) * kSlotBytes, k_at = ring + sl * kSlotBytes;
-#pragma unroll
-        for (int ks = 0; ks < 4; ++ks)
-          elect_mma_ss(tmem + kColS + 128 * bb, sdesc(q_at + 32 * ks), sdesc(k_at + 32 * ks), id_s, c > 0 || ks > 0);
+        for (int ks = 0; ks < 12; ++ks)
+          pair_mma_ss(tmem + kColS + 128 * bb, sdesc(q_at + (ks >> 2) * kChunk + 32 * (ks & 3)),
+                      sdesc(k_at + (ks >> 2) * (kChunk / 2) + 32 * (ks & 3)), id_s, ks > 0);
         issued = true;
-        if (bb == last_b) elect_commit(smem_addr(&ms.empty[sl]));
-      }
-      elect_commit(smem_addr(&ms.s_full[bb]));
-    };
-    if (n > 0) wait(ms.q_full, 0);
+        if (bb == last_b && t + kStages < n) pair_commit(smem_addr(&ms.k_empty[st]), both);
+        pair_commit(smem_addr(&ms.s_full[bb]), both);
+      };
+      wait(ms.q_full, 0);
 #pragma unroll
-    for (int bb = 0; bb < 2; ++bb)
-      if (ok && n_b[bb] > 0) s_mmas(bb, 0);
-    for (int t = 0; t < n && ok; ++t) {
-      bool first = true;
+      for (int bb = 0; bb < 2; ++bb)
+        if (ok && n_b[bb] > 0) s_mmas(bb, 0);
+      for (int t = 0; t < n && ok; ++t) {
+        const int st = t % kStages;
+        if (!wait(ms.v_full[st], t / kStages)) break;
+        if (t >= t_fix && !wait(ms.fix_done[st], (t - t_fix) / kStages)) break;
 #pragma unroll
-      for (int bb = 0; bb < 2; ++bb) {
-        if (!ok || t >= n_b[bb]) continue;
-        if (first && t >= t_fix) {  // the values' warps look at this tile
-          bool there = true;
-          for (int c = 0; c < 2 && there; ++c) there = wait(ms.full[(v_slot(t) + c) % kSlots], (v_slot(t) + c) / kSlots);
-          if (!there) break;
-          warp_arrive(ms.fix_ask);
-          if (!wait(ms.fix_done, fixed++)) break;
+        for (int bb = 0; bb < 2; ++bb) {
+          if (!ok || t >= n_b[bb]) continue;
+          if (!wait(ms.p_full[bb], t)) break;
+          fence_after_sync();
+#pragma unroll
+          for (int ks = 0; ks < 8; ++ks)  // keys 16 ks ..
+            pair_mma_ts(tmem + 128 * bb, tmem + kColS + 128 * bb + 8 * ks, sdesc(v_ring + st * kVBytes + 2048 * ks), id_o, t > 0 || ks > 0);
+          if (bb == last_b && t + kStages < n) pair_commit(smem_addr(&ms.v_empty[st]), both);
+          if (t + 1 < n_b[bb])
+            s_mmas(bb, t + 1);  // over the same columns, behind the MMAs that read them
+          else
+            pair_commit(smem_addr(&ms.o_done[bb]), both);
         }
-        first = false;
-        if (!wait(ms.p_full[bb], t)) break;
-        fence_after_sync();
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const uint32_t at = v_slot(t) + c, sl = at % kSlots;
-          if (!wait(ms.full[sl], at / kSlots)) break;
-#pragma unroll
-          for (int ks = 0; ks < 4; ++ks)  // keys 64 c + 16 ks ..
-            elect_mma_ts(tmem + 128 * bb, tmem + kColS + 128 * bb + 32 * c + 8 * ks, vdesc(ring + sl * kSlotBytes + 2048 * ks), id_o,
-                         t > 0 || c > 0 || ks > 0);
-          if (bb == last_b) elect_commit(smem_addr(&ms.empty[sl]));
-        }
-        if (!ok) break;
-        if (t + 1 < n_b[bb])
-          s_mmas(bb, t + 1);  // over the same columns, behind the MMAs that read them
-        else
-          elect_commit(smem_addr(&ms.o_done[bb]));
       }
-    }
-    if (!ok && issued) {  // nothing may be running when the tensor memory is freed
-      elect_commit(smem_addr(&ms.drain));
-      for (int i = 0; i < kWaitLimit; ++i)
-        if (mbar_test(smem_addr(&ms.drain), 0u)) break;
+      if (!ok && issued) {  // nothing may be running when the tensor memory is freed
+        pair_commit(smem_addr(&ms.drain), both);
+        for (int i = 0; i < kWaitLimit; ++i)
+          if (mbar_test(smem_addr(&ms.drain), 0u)) break;
+      }
     }
   } else if (warp == kCopyWarp) {
-    // ================= copies =================
+    // ================= copies: this CTA's share =================
     if (n > 0) {
-      expect(smem_addr(&ms.q_full), kQBytes);
+      if (rank == 0) elect_expect(smem_addr(&ms.q_full), 2 * kQBytes);
+      const uint32_t bar = peer_addr(smem_addr(&ms.q_full), lead);
 #pragma unroll
       for (int i = 0; i < 6; ++i)
-        load_box(q_ops + i * kSlotBytes, maps.q, 64 * (i % 3), h, q0 + r0 + kHalf * (i / 3), smem_addr(&ms.q_full));
+        load_pair(q_ops + i * kChunk, maps.q, 64 * (i % 3), h, q0 + r0 + kRows * (i / 3) + kHalf * (int)rank, bar);
     }
-    auto slot = [&](uint32_t at) {  // the bar of slot `at`, once it is free; 0 after a wait that ran out
-      const uint32_t sl = at % kSlots;
-      if (at >= kSlots && !(ok = warp_wait(ms.empty[sl], at / kSlots - 1, abort_flag))) return 0u;
-      loaded = at + 1;
-      expect(smem_addr(&ms.full[sl]), kSlotBytes);
-      return smem_addr(&ms.full[sl]);
-    };
-    auto keys = [&](int t) {
-      const int z = k0 + (t_first + t) * kTok;
-      for (int c = 0; c < 3; ++c) {
-        const uint32_t bar = slot(k_slot(t) + c), dst = ring + (k_slot(t) + c) % kSlots * kSlotBytes;
-        if (!ok) return;
-        if (c < 2)
-          load_box(dst, maps.k, 64 * c, h, z, bar);
-        else
-          load_box(dst, maps.pe, 0, 0, z, bar);
-      }
-    };
-    if (n > 0) keys(0);
     for (int t = 0; t < n && ok; ++t) {
-      for (int c = 0; c < 2 && ok; ++c) {
-        const uint32_t bar = slot(v_slot(t) + c), dst = ring + (v_slot(t) + c) % kSlots * kSlotBytes;
-        if (!ok) break;
-        const int z = k0 + (t_first + t) * kTok + 64 * c;
-        load_box(dst, maps.v, 0, h, z, bar);
-        load_box(dst + 8192, maps.v, 64, h, z, bar);
+      const int st = t % kStages, z = k0 + (t_first + t) * kTok;
+      if (t >= kStages && !(ok = warp_wait(ms.k_empty[st], t / kStages - 1, abort_flag))) break;
+      if (rank == 0) elect_expect(smem_addr(&ms.k_full[st]), 2 * kKBytes);
+      const uint32_t kbar = peer_addr(smem_addr(&ms.k_full[st]), lead), dst = k_ring + st * kKBytes;
+      const int zk = z + kTok / 2 * (int)rank;  // this CTA's 64 keys
+      load_pair(dst, maps.k, 0, h, zk, kbar);
+      load_pair(dst + kChunk / 2, maps.k, 64, h, zk, kbar);
+      load_pair(dst + kChunk, maps.pe, 0, 0, zk, kbar);
+      if (t >= kStages && !(ok = warp_wait(ms.v_empty[st], t / kStages - 1, abort_flag))) break;
+      if (t < t_fix) {
+        if (rank == 0) elect_expect(smem_addr(&ms.v_full[st]), 2 * kVBytes);
+        load_pair(v_ring + st * kVBytes, maps.v, 64 * (int)rank, h, z, peer_addr(smem_addr(&ms.v_full[st]), lead));
+      } else {  // seen in part: the values' warps of this CTA first
+        elect_expect(smem_addr(&ms.v_here[st]), kVBytes);
+        load_here(v_ring + st * kVBytes, maps.v, 64 * (int)rank, h, z, smem_addr(&ms.v_here[st]));
+        if (rank == 0) warp_arrive(ms.v_full[st]);
       }
-      if (ok && t + 1 < n) keys(t + 1);
     }
   } else if (warp < kFixWarp + kFixWarps) {
     // ================= values that are not finite, in tiles seen in part =================
     // 16-bit halves whose exponent is all ones, two to a word
     constexpr bool kF16 = std::is_same<T, __half>::value;
     constexpr uint32_t kExp = kF16 ? 0x7C007C00u : 0x7F807F80u, kOne = kF16 ? 0x04000400u : 0x00800080u;
-    for (int t = t_fix, i = 0; t < n; ++t, ++i) {
-      if (!(ok = warp_wait(ms.fix_ask, i, abort_flag))) break;
+    for (int t = t_fix; t < n; ++t) {
+      const int st = t % kStages;
+      if (!(ok = warp_wait(ms.v_here[st], (t - t_fix) / kStages, abort_flag))) break;
       bool any = false;
-      for (int c = 0; c < 2 && ok; ++c) {
-        const uint32_t at = v_slot(t) + c, sl = at % kSlots;
-        if (!(ok = warp_wait(ms.full[sl], at / kSlots, abort_flag))) break;  // complete: the MMA warp has waited for it
-        // row (key) r of half d (64 dims): eight chunks; a warp takes one half
-        const int d = warp - kFixWarp;
-        for (int r8 = 0; r8 < 16; ++r8) {
-          const int r = 4 * r8 + (lane >> 3), chunk = lane & 7;
-          const uint32_t addr = ring + sl * kSlotBytes + 8192 * d + sw128(r, chunk);
-          const uint4 v = lds128(addr);
-          const uint32_t odd = ((v.x & kExp) + kOne) | ((v.y & kExp) + kOne) | ((v.z & kExp) + kOne) | ((v.w & kExp) + kOne);
-          if (!(odd & 0x80008000u)) continue;
-          const int key = (t_first + t) * kTok + 64 * c + r;
-          uint32_t w[4];
-          for (int k = 0; k < 4; ++k) {
-            w[k] = word(v, k);
-            for (int s = 0; s < 2; ++s) {
-              const uint32_t x = w[k] >> (16 * s) & 0xFFFFu, e = kExp & 0xFFFFu;
-              if ((x & e) != e) continue;
-              const int kind = (x & 0x7FFFu) != e ? 2 : x >> 15 ? 1 : 0;
-              if (key < nk) {
-                atomicMin(&ms.from[kind][64 * d + 8 * chunk + 2 * k + s], key);
-                ms.any = 1;
-              }
-              w[k] &= s ? 0x0000FFFFu : 0xFFFF0000u;
+      for (int r8 = warp - kFixWarp; r8 < kTok / 4; r8 += kFixWarps) {  // a row (key) is eight chunks
+        const int r = 4 * r8 + (lane >> 3), chunk = lane & 7;
+        const uint32_t addr = v_ring + st * kVBytes + sw128(r, chunk);
+        const uint4 v = lds128(addr);
+        const uint32_t odd = ((v.x & kExp) + kOne) | ((v.y & kExp) + kOne) | ((v.z & kExp) + kOne) | ((v.w & kExp) + kOne);
+        if (!(odd & 0x80008000u)) continue;
+        const int key = (t_first + t) * kTok + r;
+        uint32_t w[4];
+        for (int k = 0; k < 4; ++k) {
+          w[k] = word(v, k);
+          for (int s = 0; s < 2; ++s) {
+            const uint32_t x = w[k] >> (16 * s) & 0xFFFFu, e = kExp & 0xFFFFu;
+            if ((x & e) != e) continue;
+            const int kind = (x & 0x7FFFu) != e ? 2 : x >> 15 ? 1 : 0;
+            if (key < nk) {
+              atomicMin(&ms.from[kind][8 * chunk + 2 * k + s], key);
+              ms.any = 1;
             }
+            w[k] &= s ? 0x0000FFFFu : 0xFFFF0000u;
           }
-          sts128(addr, w[0], w[1], w[2], w[3]);
-          any = true;
         }
+        sts128(addr, w[0], w[1], w[2], w[3]);
+        any = true;
       }
-      if (!ok) break;
       if (any) fence_async_smem();
-      warp_arrive(ms.fix_done);
+      warp_arrive_pair(peer_addr(smem_addr(&ms.fix_done[st]), lead));
     }
   }
   if (!ok && lane == 0 && a.status) atomicOr(a.status, RQ_STATUS_TIMEOUT);
@@ -406,12 +362,21 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
   __syncthreads();
   fence_after_sync();
   const bool aborted = ms.abort != 0;
+  if (aborted) {  // copies in flight land before the block ends: a millisecond is many times what one takes
+    const long long start = clock64();
+    while (clock64() - start < 2000000) __nanosleep(1000);
+  }
+  cluster_sync();  // the peer is done with this CTA's operands, and its values' warps have left what they found
 
   // ---- write the rows, or join the parts ----
   T* const out = reinterpret_cast<T*>(a.out) + ((size_t)q0 * a.q.heads + h) * kDim;
   if (warp < kSoftWarps && !aborted) {
     const float empty = qpos >= 0 ? CUDART_NAN_F : 0.f;  // a row whose scores are all minus infinity; one that sees nothing
     const float inv = splits == 1 ? 1.f / l_run : 1.f;
+    // what the values' warps found: dims 64 r .. of the pair's CTA r
+    int odd[2];
+    for (int r = 0; r < 2; ++r) odd[r] = __float_as_int(peer_ld(peer_addr(smem_addr(&ms.any), lead + r)));
+    auto first_of = [&](int kind, int d) { return __float_as_int(peer_ld(peer_addr(smem_addr(&ms.from[kind][d & 63]), lead + (d >> 6)))); };
 #pragma unroll 2
     for (int c = 0; c < kDim / 16; ++c) {
       float y[16];
@@ -426,12 +391,12 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
 #pragma unroll
         for (int i = 0; i < 16; ++i) y[i] = 0.f;
       }
-      if (ms.any) {
+      if (odd[c >> 2]) {
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-          if (ms.from[0][16 * c + i] <= qpos) y[i] += CUDART_INF_F;
-          if (ms.from[1][16 * c + i] <= qpos) y[i] -= CUDART_INF_F;
-          if (ms.from[2][16 * c + i] <= qpos) y[i] = CUDART_NAN_F;
+          if (first_of(0, 16 * c + i) <= qpos) y[i] += CUDART_INF_F;
+          if (first_of(1, 16 * c + i) <= qpos) y[i] -= CUDART_INF_F;
+          if (first_of(2, 16 * c + i) <= qpos) y[i] = CUDART_NAN_F;
         }
       }
       if (splits > 1) {
@@ -453,43 +418,38 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
       ml[kRows + kHalf * blk + brow] = l_run;
     }
   }
-  if (aborted && warp == kCopyWarp) {  // copies in flight land before the block ends
-    for (uint32_t i = loaded > kSlots ? loaded - kSlots : 0; i < loaded; ++i)
-      for (int w = 0; w < kWaitLimit; ++w)
-        if (mbar_test(smem_addr(&ms.full[i % kSlots]), (i / kSlots) & 1)) break;
-    if (n > 0)
-      for (int w = 0; w < kWaitLimit; ++w)
-        if (mbar_test(smem_addr(&ms.q_full), 0u)) break;
-  }
   if (splits > 1) {
     cluster_sync();
     // rows `per` of this part's share; a warp takes a row at a time, a lane four dims
     const int per = kRows / splits;
     for (int i = warp; i < per && !aborted; i += kThreads / 32) {
-      const int rr = part * per + i;
-      if (r0 + rr >= nq) break;
+      const int rr = part * per + i, at = r0 + kRows * (rr / kHalf) + kHalf * (int)rank + rr % kHalf;
+      if (at >= nq) continue;
       float m = kNone, sum = 0.f;
       float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
       for (int f = 0; f < splits; ++f) {
-        const float mf = peer_ld(peer_addr(base + kOffML + 4 * rr, f)), lf = peer_ld(peer_addr(base + kOffML + 4 * (kRows + rr), f));
-        const float4 v = peer_ld4(peer_addr(base + (uint32_t)(lane * kRows + rr) * 16, f));
+        const float mf = peer_ld(peer_addr(base + kOffML + 4 * rr, 2 * f + rank)),
+                    lf = peer_ld(peer_addr(base + kOffML + 4 * (kRows + rr), 2 * f + rank));
+        const float4 v = peer_ld4(peer_addr(base + (uint32_t)(lane * kRows + rr) * 16, 2 * f + rank));
         const float to = fmaxf(m, mf), wa = ex2(m - to), w = ex2(mf - to);
         m = to;
         sum = fmaf(sum, wa, lf * w);
         y.x = fmaf(y.x, wa, v.x * w), y.y = fmaf(y.y, wa, v.y * w), y.z = fmaf(y.z, wa, v.z * w), y.w = fmaf(y.w, wa, v.w * w);
       }
-      const float none = ahead + r0 + rr >= 0 ? CUDART_NAN_F : 0.f, inv = 1.f / sum;
+      const float none = ahead + at >= 0 ? CUDART_NAN_F : 0.f, inv = 1.f / sum;
       if (sum == 0.f)
         y = make_float4(none, none, none, none);
       else
         y = make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv);
-      *reinterpret_cast<uint2*>(out + (size_t)(r0 + rr) * a.q.heads * kDim + 4 * lane) =
+      *reinterpret_cast<uint2*>(out + (size_t)at * a.q.heads * kDim + 4 * lane) =
           make_uint2(rope::pack2<T>(y.x, y.y), rope::pack2<T>(y.z, y.w));
     }
-    cluster_sync();  // a peer's shared memory is read until here
   }
+  fence_before_sync();
   __syncthreads();
-  if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
+  cluster_sync();  // a peer's shared memory is read until here
+  fence_after_sync();
+  if (warp == kMmaWarp) pair_tmem_dealloc(tmem, 512);
 }
 
 typedef CUresult (*EncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
@@ -524,13 +484,13 @@ cudaError_t launch(const Maps& maps, const PromptArgs& a, int splits, int n_rb, 
   cudaError_t e = cudaFuncSetAttribute(prompt_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(a.q.heads * splits), (unsigned)a.B, (unsigned)n_rb);
+  cfg.gridDim = dim3((unsigned)(2 * a.q.heads * splits), (unsigned)a.B, (unsigned)n_rb);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = kSmem;
   cfg.stream = stream;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = (unsigned)splits;
+  at[0].val.clusterDim.x = 2u * (unsigned)splits;
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
@@ -541,20 +501,20 @@ cudaError_t launch(const Maps& maps, const PromptArgs& a, int splits, int n_rb, 
 
 cudaError_t launch_prompt_attention(const PromptArgs& a, int num_sms, cudaStream_t stream) {
   if (!encoder()) return cudaErrorNotSupported;
-  const int n_rb = (a.max_new + kRows - 1) / kRows;
+  const int n_rb = (a.max_new + kUnitRows - 1) / kUnitRows;
   if (n_rb > 65535) return cudaErrorInvalidValue;
   Maps maps{};
   HeadsDev k = a.k, v = a.v, pe{a.k_pe, a.k_pe_stride, 0, 1};
   if (a.nk == 0) k = v = pe = a.q;  // no key is ever read
   const int nk = a.nk > 0 ? a.nk : 1;
-  if (!encode(&maps.q, a.bf16, a.q, kPromptDim, a.nq, kHalf) || !encode(&maps.k, a.bf16, k, kDim, nk, kTok) ||
-      !encode(&maps.pe, a.bf16, pe, kPositionDim, nk, kTok) || !encode(&maps.v, a.bf16, v, kDim, nk, kTok / 2))
+  if (!encode(&maps.q, a.bf16, a.q, kPromptDim, a.nq, kHalf) || !encode(&maps.k, a.bf16, k, kDim, nk, kTok / 2) ||
+      !encode(&maps.pe, a.bf16, pe, kPositionDim, nk, kTok / 2) || !encode(&maps.v, a.bf16, v, kDim, nk, kTok))
     return cudaErrorInvalidValue;
   // few units: the most parts (a power of two) that leave every SM at most one of them, and each some 4 tiles at the batch's
   // mean length
   const long long units = (long long)a.B * n_rb * a.q.heads, tiles = a.nk / a.B / kTok;
   int splits = 1;
-  while (splits < kMaxSplit && units * 2 * splits <= num_sms && tiles >= 8 * splits) splits *= 2;
+  while (splits < kMaxSplit && units * 4 * splits <= num_sms && tiles >= 8 * splits) splits *= 2;
   return a.bf16 ? launch<__nv_bfloat16>(maps, a, splits, n_rb, stream) : launch<__half>(maps, a, splits, n_rb, stream);
 }
 
