@@ -247,7 +247,7 @@ struct LatentAttnArgs {
   int32_t* status;
   float* ws;  // latent_attention_workspace floats
 };
-size_t latent_attention_workspace(int num_sms);
+size_t latent_attention_workspace(int num_sms, long long rows, int max_batch);  // rows: the most query rows of a sequence
 cudaError_t latent_attention_prepare();
 cudaError_t launch_latent_attention(const LatentPool& pool, const LatentAttnArgs& a, int num_sms, cudaStream_t stream);
 

@@ -94,7 +94,7 @@ int rq_latent_create(rq_latent** out, const rq_latent_config* cfg) {
   if (cfg->sm_scale == 0.f) ctx->cfg.sm_scale = (float)(1.0 / std::sqrt((double)rq::kPromptDim));
   ctx->device = dev;
   cudaError_t e = cudaDeviceGetAttribute(&ctx->num_sms, cudaDevAttrMultiProcessorCount, dev);
-  if (e == cudaSuccess) e = cudaMalloc(&ctx->d_ws, rq::latent_attention_workspace(ctx->num_sms) * sizeof(float));
+  if (e == cudaSuccess) e = cudaMalloc(&ctx->d_ws, rq::latent_attention_workspace(ctx->num_sms, (long long)cfg->max_query_tokens * cfg->num_heads, cfg->max_batch) * sizeof(float));
   if (e == cudaSuccess) e = rq::latent_attention_prepare();
   if (e != cudaSuccess) {
     cudaFree(ctx->d_ws);

@@ -1,122 +1,838 @@
 // Attention in the absorbed form over the cache of latents: decode, chain and tree verify.
+//
+// score = sm_scale (q_c . c + q_pe . p), out = sum softmax(score) c: keys and values are one row a token, for all heads.
+// The codes are operands of the tensor cores' 8-bit MMAs as they stand in the cache, for scores (K along dims) and for the
+// weighted sum (N along dims) alike; what they are multiplied with is split instead.  A query row is 2^E times e4m3
+// numbers: a bf16 value's 8 bits are exactly two of 4, an fp16 value's 11 three (what falls below e4m3's smallest step is off by
+// 2^-10 where the row's largest is 224 to 448).  A weight times its token's scale is an e5m2 number, which brings the range, and
+// one (bf16) or two (fp16) e4m3 numbers for the rest: 2^-8 or 2^-12 of it.  8-bit MMAs run at twice the 16-bit rate, so that two
+// passes cost what one over widened codes would, without the widening.  Position parts are a 16-bit MMA into the same
+// accumulators.
+//
+// What bounds it: 641 cache bytes a token against 2 * 1,088 flops a (token, row); from some 90 rows on the tensor cores.
+//
+// A pair of CTAs (two SMs) takes 128 query rows of one sequence (64 to a CTA) and walks the cache in tiles of 256 tokens; its
+// MMAs span both (M = 128, N = 256: 64 to 66 cycles, the full rate; one CTA with M = 128 has no room: 512 f32 columns of
+// output a row are all of its tensor memory).  A CTA holds 128 of a tile's tokens as keys, five slots of 16 KB (128 dims
+// each, and the position parts), and 256 of the 512 dims of all its tokens as values, four slots (64 tokens each).  Roles:
+//   softmax (warps 0-7 of both, four threads a row of 64 tokens each): scores from tensor memory, scales, mask, weights
+//     to shared memory as the pieces above;
+//   MMA (warp 8 of the leader): S(t + 1) before O += W(t) C(t), so that S is there a tile ahead;
+//   copies (warp 9 of both): TMA boxes of the pages into a ring of slots, in the order of use;
+//   scales (warp 10 of both): exponent bytes of a tile to floats;
+//   tail (warp 11 of both): zeros over a last tile's rows behind the tokens that are seen, which may hold anything.
+// Tensor memory: O at columns 0 to 255 (lanes 64 .. 127 hold the second half of the columns' dims), S(t) at 256 + 128 (t mod 2).
+//
+// Work is cut evenly: tiles of all units (sequence, 128 rows) in order, one range for each pair.  A unit that spans ranges
+// leaves its parts (m, l, out) in the workspace, and a second kernel joins them.
+// Every wait is bounded: one that runs out sets RQ_STATUS_TIMEOUT and an abort flag every role polls.
 #include <math_constants.h>
+
+#include <cstddef>
+#include <type_traits>
 
 #include "../../include/rq.h"
 #include "rq_block.cuh"
 #include "rq_latent.cuh"
+#include "rq_roles.cuh"
 #include "rq_rope.cuh"
+#include "rq_tma.h"
 
 namespace rq {
 namespace {
 
 using namespace latent;
+using namespace tc;
 
-constexpr int kThreads = 128;
+constexpr int kSoftWarps = 8, kMmaWarp = 8, kCopyWarp = 9, kScaleWarp = 10, kTailWarp = 11, kThreads = 384;
+constexpr int kRows = 64, kUnitRows = 128, kTok = 256;  // rows of a CTA, of a pair; tokens of a tile
+constexpr uint32_t kSlotBytes = 16384;
+constexpr uint32_t kColS = 256;
+// weights are 2^(score + E - m), m the running maximum of score + E less kLift, moved where a score is past it by more than
+// kReach: below 2^12 an e5m2 number's remainder stays within e4m3's 448
+constexpr float kLift = 10.f, kReach = 12.f;
+constexpr float kNone = -3.402823466e38f;  // m before any visible token
+// floats of a fragment's slot: 128 rows x 512 (as [dim / 4][row][4]), then the rows' m and l
+constexpr size_t kSlotFloats = (size_t)kUnitRows * kLatentDim + 2 * kUnitRows;
 
-// One query row a CTA: a thread a token for the scores, then a thread four dims for the sum.
 template <typename T>
-__global__ void __launch_bounds__(kThreads) latent_rows_kernel(const LatentPool pool, const LatentAttnArgs a) {
-  __shared__ float q[kLatentDim + kPositionDim], w[kThreads], red[kThreads / 32];
-  __shared__ const uint8_t* at[kThreads];
-  __shared__ int off[kThreads];
-  const int tid = threadIdx.x, P = pool.page_size;
-  const long long token = blockIdx.x / a.heads;
-  const int h = blockIdx.x % a.heads, b = (int)(token / a.T), j = (int)(token % a.T);
-  const int cap = a.max_pages * P;
-  int len = __ldg(a.seq_lens + b);
-  if (len < 0 || len > cap || (len > 0 && len < a.T)) {
-    if (tid == 0 && a.status) atomicOr(a.status, RQ_STATUS_BAD_LEN);
-    len = len < 0 ? 0 : min(len, cap);
+struct Shape {
+  static constexpr int kPieces = std::is_same<T, __half>::value ? 3 : 2;
+  static constexpr int kSlots = kPieces == 3 ? 4 : 7;
+  static constexpr uint32_t kPieceQ = 32768, kQBytes = kPieces * kPieceQ + 8192;  // [piece][4 chunks of 128 dims][64 rows], position parts
+  static constexpr uint32_t kPieceP = 16384, kPBytes = kPieces * kPieceP;         // [piece][2 halves of 128 tokens][64 rows]
+  static constexpr uint32_t kOffP = kQBytes, kOffRing = kOffP + kPBytes, kOffMisc = kOffRing + kSlots * kSlotBytes;
+};
+
+struct Frag {           // tiles r0 .. r0 + n - 1 of one unit
+  int b, rt, r0, n, len, end;  // end: tokens that the unit's rows see lie before it
+  int whole, frags;     // the unit is all here; else its number of fragments
+  int range, range_last;  // its first range, and whether the fragment there is that range's last
+  int done;             // no more fragments
+};
+struct Misc {
+  // the leader's: a slot is full; the queries; W(t); a tail's zeros are written
+  uint64_t full[7], q_full, p_full, tail_done[7];
+  // both CTAs': a slot is read; S(t); O(t); drained; a slot of the tail is here; scales of a tile
+  uint64_t empty[7], s_full[2], o_done, drain, here[7], sc_full[2], sc_empty[2];
+  Frag f;
+  uint32_t tmem;
+  int abort;
+  alignas(16) float ks[2][kTok], ev[2][kTok], dn[2][kTok];  // 2^E (or NaN), E, 2^-E of a tile's tokens
+  float top[2][4][kRows];
+};
+static_assert(Shape<__half>::kOffMisc + sizeof(Misc) + 1024 <= 232448, "one CTA's shared memory");
+static_assert(Shape<__nv_bfloat16>::kOffMisc + sizeof(Misc) + 1024 <= 232448, "one CTA's shared memory");
+
+struct Unit {
+  int len, end, tiles;
+};
+__device__ __forceinline__ Unit unit_of(const LatentAttnArgs& a, int cap, int b, int rt, bool report) {
+  Unit u;
+  u.len = __ldg(a.seq_lens + b);
+  if (u.len < 0 || u.len > cap || (u.len > 0 && u.len < a.T)) {
+    if (report && a.status) atomicOr(a.status, RQ_STATUS_BAD_LEN);
+    u.len = u.len < 0 ? 0 : min(u.len, cap);
   }
-  const float up = a.sm_scale * 1.44269504088896340736f;
-  const T* qc = reinterpret_cast<const T*>(a.q_c.x) + token * a.q_c.stride + h * a.q_c.head_stride;
-  const T* qp = reinterpret_cast<const T*>(a.q_pe.x) + token * a.q_pe.stride + h * a.q_pe.head_stride;
-  for (int i = tid; i < kLatentDim; i += kThreads) q[i] = (float)qc[i];
-  for (int i = tid; i < kPositionDim; i += kThreads) q[kLatentDim + i] = (float)qp[i];
-  const uint64_t mask = a.tree_mask ? __ldg(a.tree_mask + token) : 0ull;
-  float m = -CUDART_INF_F, l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
-  for (int t0 = 0; t0 < len; t0 += kThreads) {
-    const int p = t0 + tid, draft = p - (len - a.T);
-    const bool see = p < len && (draft < 0 || (a.tree_mask ? (mask >> draft & 1) != 0 : draft <= j));
-    float s = -CUDART_INF_F, scale = 0.f;
+  const long long rows = (long long)a.T * a.heads;
+  const int last = (int)((min(rows, (rt + 1ll) * kUnitRows) - 1) / a.heads);  // the last row's token
+  u.end = a.tree_mask ? u.len : max(0, min(u.len, u.len - a.T + last + 1));
+  u.tiles = max(1, (u.end + kTok - 1) / kTok);  // rows that see nothing are written too
+  return u;
+}
+
+// Instruction descriptors: kind::f8f6f4 with A of e4m3 (0) or e5m2 (1), B of e4m3; bit 16: B with N along its rows.
+__host__ __device__ constexpr uint32_t idesc_f8(int M, int N, uint32_t a_type, uint32_t b_rows) {
+  return idesc_f16(M, N) | a_type << 7 | b_rows << 16;
+}
+__device__ __forceinline__ void pair_mma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p, e;\n elect.sync _|e, 0xffffffff;\n setp.ne.b32 p, %4, 0;\n"
+      " @e tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+      "l"(a), "l"(b), "r"(id), "r"(accumulate));
+}
+// A box of the pool's planes ([page][plane][row][128 bytes]) for each lane whose turn it is; the bytes count at `bar`, a barrier of
+// the leader (pair), or of this CTA.
+__device__ __forceinline__ void load_pair(uint32_t dst, const CUtensorMap& map, int row, int plane, int page, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(
+          dst),
+      "l"(&map), "r"(0), "r"(row), "r"(plane), "r"(page), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void load_here(uint32_t dst, const CUtensorMap& map, int row, int plane, int page, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+      "l"(&map), "r"(0), "r"(row), "r"(plane), "r"(page), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void soft_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+
+// Two f32 to e4m3 (past 448 to 448), and back as f16x2; e5m2 is an fp16 number's upper byte.
+__device__ __forceinline__ uint32_t e4m3_of(uint32_t h2) {
+  uint32_t c;
+  asm("{\n .reg .b16 c;\n cvt.rn.satfinite.e4m3x2.f16x2 c, %1;\n cvt.u32.u16 %0, c;\n}" : "=r"(c) : "r"(h2));
+  return c;
+}
+__device__ __forceinline__ uint32_t e5m2_of(uint32_t h2) {
+  uint32_t c;
+  asm("{\n .reg .b16 c;\n cvt.rn.satfinite.e5m2x2.f16x2 c, %1;\n cvt.u32.u16 %0, c;\n}" : "=r"(c) : "r"(h2));
+  return c;
+}
+__device__ __forceinline__ uint32_t hsub2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t e5m2_wide(uint32_t codes) { return __byte_perm(codes, 0u, 0x1404); }  // {0, lo, 0, hi}
+
+// The smallest E in [-100, 100] with top <= 448 * 2^E, or top <= 2^(15 + E), from top's bits.
+__device__ __forceinline__ int query_exp(uint32_t top_c, uint32_t top_p) {
+  const int c = (int)(top_c >> 23) - 127 - 8 + ((top_c & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+  const int p = (int)(top_p >> 23) - 127 - 15 + ((top_p & 0x7FFFFFu) != 0u ? 1 : 0);
+  return min(max(max(c, p), -100), 100);
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads, 1)
+    latent_kernel(const __grid_constant__ CUtensorMap map, const LatentPool pool, const LatentAttnArgs a, int box, int4* info) {
+  using S = Shape<T>;
+  constexpr int NP = S::kPieces, kSlots = S::kSlots;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t base = smem_addr(smem_raw) + (1024 - (smem_addr(smem_raw) & 1023) & 1023);
+  Misc& ms = *reinterpret_cast<Misc*>(smem_raw + (base - smem_addr(smem_raw)) + S::kOffMisc);
+  const uint32_t q_ops = base, p_ops = base + S::kOffP, ring = base + S::kOffRing;
+  volatile int* const abort_flag = &ms.abort;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t rank = cluster_rank();
+  const int P = pool.page_size, cap = a.max_pages * P;
+  const long long n_rows = (long long)a.T * a.heads;
+  const int n_rt = (int)((n_rows + kUnitRows - 1) / kUnitRows);
+
+  // ---- the pair's range of tiles: x .. end - 1 of `total`, kept by thread 0 ----
+  const long long pairs = gridDim.x >> 1, me = blockIdx.x >> 1;
+  long long total, parts, x = 0, x_end = 0, at = 0, item = 0;  // at: the first tile of unit `item`
+  {
+    long long* const scan = reinterpret_cast<long long*>(smem_raw + (base - smem_addr(smem_raw)));  // over Q
+    __shared__ long long s_found[2];
+    const long long n_items = (long long)a.B * n_rt, chunk = (n_items + kThreads - 1) / kThreads;
+    long long mine = 0;
+    for (long long i = tid * chunk; i < min(n_items, (tid + 1) * chunk); ++i)
+      mine += unit_of(a, cap, (int)(i / n_rt), (int)(i % n_rt), blockIdx.x == 0).tiles;
+    scan[tid] = mine;
     __syncthreads();
-    if (see) {
-      int page = __ldg(a.block_table + (size_t)b * a.max_pages + p / P);
-      if (page < 0 || page >= pool.num_pages) {
-        if (a.status) atomicOr(a.status, RQ_STATUS_BAD_PAGE);
-        page = 0;
+    for (int o = 1; o < kThreads; o <<= 1) {
+      const long long v = tid >= o ? scan[tid - o] : 0;
+      __syncthreads();
+      scan[tid] += v;
+      __syncthreads();
+    }
+    total = scan[kThreads - 1];
+    parts = min(pairs, total);
+    if (me >= parts) return;  // both CTAs of a pair
+    x = me * total / parts;
+    x_end = (me + 1) * total / parts;
+    const long long before = scan[tid] - mine;
+    if (x >= before && x < scan[tid]) {
+      long long p = before, i = tid * chunk;
+      for (;; ++i) {
+        const long long n = unit_of(a, cap, (int)(i / n_rt), (int)(i % n_rt), false).tiles;
+        if (x < p + n) break;
+        p += n;
       }
-      const uint8_t* base = pool.pages + page_at(page, P);
-      const int r = p % P;
-      at[tid] = base;
-      off[tid] = r;
-      scale = scale_of_byte(base[640 * P + r]);
-      float sum = 0.f;
-      for (int c = 0; c < 32; ++c) {
-        const uint4 v = *reinterpret_cast<const uint4*>(base + (c >> 3) * 128 * P + chunk_at(r, c & 7));
-        const uint32_t w4[4] = {v.x, v.y, v.z, v.w};
-        for (int k = 0; k < 4; ++k) {
-          const float2 lo = rope::unpack2<__half>(block::widen2(w4[k])), hi = rope::unpack2<__half>(block::widen2_hi(w4[k]));
-          const float* qq = q + 16 * c + 4 * k;
-          sum += lo.x * qq[0] + lo.y * qq[1] + hi.x * qq[2] + hi.y * qq[3];
+      s_found[0] = p;
+      s_found[1] = i;
+    }
+    __syncthreads();
+    at = s_found[0];
+    item = s_found[1];
+  }
+  if (tid == 0) {
+    for (int i = 0; i < kSlots; ++i) {
+      mbar_init(smem_addr(&ms.full[i]), 1);
+      mbar_init(smem_addr(&ms.empty[i]), 1);
+      mbar_init(smem_addr(&ms.here[i]), 1);
+      mbar_init(smem_addr(&ms.tail_done[i]), 2);
+    }
+    mbar_init(smem_addr(&ms.q_full), 2 * kSoftWarps);
+    mbar_init(smem_addr(&ms.p_full), 2 * kSoftWarps);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_addr(&ms.s_full[i]), 1);
+      mbar_init(smem_addr(&ms.sc_full[i]), 1);
+      mbar_init(smem_addr(&ms.sc_empty[i]), kSoftWarps);
+    }
+    mbar_init(smem_addr(&ms.o_done), 1);
+    mbar_init(smem_addr(&ms.drain), 1);
+    ms.abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  __syncwarp();
+  if (warp == kMmaWarp) pair_tmem_alloc(smem_addr(&ms.tmem), 512);
+  fence_before_sync();
+  __syncthreads();
+  cluster_sync();  // the peer's barriers are there
+  fence_after_sync();
+  const uint32_t tmem = *(volatile uint32_t*)&ms.tmem;
+
+  // softmax: row of the CTA (= lane of tensor memory, twice), the quarter of a tile's tokens and of the dims
+  const int quad = warp & 3, col_half = warp >> 2 & 1, row = 32 * (quad & 1) + lane, tok_half = quad >> 1;
+  const int quarter = 2 * tok_half + col_half;
+  const uint32_t lane_off = (uint32_t)(32 * quad) << 16;
+  uint32_t done_tiles = 0, done_frags = 0;  // with tokens: tiles and fragments before
+  uint32_t at_slot = 0;                     // slots used before
+  uint32_t tails = 0;                       // parity of the tail's use of each slot
+  for (;;) {
+    if (tid == 0) {  // the next fragment
+      Frag& f = ms.f;
+      f.done = x >= x_end;
+      if (!f.done) {
+        f.b = (int)(item / n_rt);
+        f.rt = (int)(item % n_rt);
+        const Unit un = unit_of(a, cap, f.b, f.rt, false);
+        f.len = un.len;
+        f.end = un.end;
+        f.r0 = (int)(x - at);
+        f.n = (int)min((long long)un.tiles - f.r0, x_end - x);
+        f.whole = f.n == un.tiles;
+        const long long u0 = at, u1 = u0 + un.tiles - 1, first = ((u0 + 1) * parts - 1) / total;  // the range that holds tile u0
+        f.range = (int)first;
+        f.range_last = first * total / parts != u0;
+        f.frags = (int)(((u1 + 1) * parts - 1) / total - first) + 1;
+        if (f.r0 == 0 && rank == 0) info[item] = make_int4(f.range, f.whole ? 0 : f.frags, f.range_last, 0);
+        x += f.n;
+        if (x - at == un.tiles) {
+          at = x;
+          ++item;
         }
       }
+    }
+    fence_before_sync();
+    __syncthreads();
+    fence_after_sync();
+    if (ms.f.done) break;
+    const int b = ms.f.b, r0 = ms.f.r0, len = ms.f.len, end = ms.f.end;
+    const int n = end > 0 ? ms.f.n : 0;  // tiles with tokens
+    const long long urow = (long long)ms.f.rt * kUnitRows + kRows * (int)rank + row;  // the thread's query row
+    const bool valid = urow < n_rows;
+    const int j = valid ? (int)(urow / a.heads) : 0, head = valid ? (int)(urow % a.heads) : 0;
+    const uint32_t t_base = done_tiles;
+    float m_run = kNone, l_run = 0.f;
+    bool ok = true;
+
+    if (warp < kSoftWarps) {
+      float q_scale = 0.f;
+      if (n > 0) {
+        // ---- the row's quarter of the queries as pieces ----
+        const long long token = (long long)b * a.T + j;
+        const uint4* qc = reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(a.q_c.x) + token * a.q_c.stride +
+                                                         head * a.q_c.head_stride + 128 * quarter);
+        const uint4* qp = reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(a.q_pe.x) + token * a.q_pe.stride +
+                                                         head * a.q_pe.head_stride + 16 * quarter);
+        const uint4 none = make_uint4(0u, 0u, 0u, 0u);
+        uint32_t top_c = 0u, top_p = 0u;
+#pragma unroll 4
+        for (int c = 0; c < 18; ++c) {
+          const uint4 v = !valid ? none : c < 16 ? __ldg(qc + c) : __ldg(qp + c - 16);
+          uint32_t top = 0u;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float2 f = rope::unpack2<T>(word(v, k));
+            top = max(top, max(__float_as_uint(f.x) & 0x7FFFFFFFu, __float_as_uint(f.y) & 0x7FFFFFFFu));
+          }
+          if (c < 16) top_c = max(top_c, top); else top_p = max(top_p, top);
+        }
+        int e = max(top_c, top_p) >= 0x7F800000u ? 1000 : query_exp(top_c, top_p);
+        ms.top[0][quarter][row] = __int_as_float(e);
+        soft_sync();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) e = max(e, __float_as_int(ms.top[0][i][row]));
+        const bool odd = e == 1000;  // a row that is not finite: all its scores are NaN
+        if (odd) e = 0;
+        const float down = block::pow2(-e);
+        q_scale = odd ? CUDART_NAN_F : a.sm_scale * 1.44269504088896340736f * block::pow2(e);
+#pragma unroll 2
+        for (int c = 0; c < 8; ++c) {  // 16 dims
+          uint32_t piece[NP][4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint4 v = valid && !odd ? __ldg(qc + 2 * c + (k >> 1)) : none;
+            const float2 f0 = rope::unpack2<T>(word(v, 2 * (k & 1))), f1 = rope::unpack2<T>(word(v, 2 * (k & 1) + 1));
+            float y[4] = {f0.x * down, f0.y * down, f1.x * down, f1.y * down};
+#pragma unroll
+            for (int p = 0; p < NP; ++p) {
+              piece[p][k] = block::code4(y[0], y[1], y[2], y[3]);
+              const float2 lo = rope::unpack2<__half>(block::widen2(piece[p][k])), hi = rope::unpack2<__half>(block::widen2_hi(piece[p][k]));
+              y[0] -= lo.x, y[1] -= lo.y, y[2] -= hi.x, y[3] -= hi.y;
+            }
+          }
+#pragma unroll
+          for (int p = 0; p < NP; ++p)
+            sts128(q_ops + p * S::kPieceQ + 8192 * quarter + sw128(row, c), piece[p][0], piece[p][1], piece[p][2], piece[p][3]);
+        }
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const uint4 v = valid && !odd ? __ldg(qp + c) : none;
+          uint32_t w[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float2 f = rope::unpack2<T>(word(v, k));
+            w[k] = rope::pack2<T>(f.x * down, f.y * down);
+          }
+          sts128(q_ops + NP * S::kPieceQ + sw128(row, 2 * quarter + c), w[0], w[1], w[2], w[3]);
+        }
+        fence_async_smem();
+        warp_arrive_pair(peer_addr(smem_addr(&ms.q_full), 0));
+      }
+      // ================= softmax =================
+      // the row sees tokens before `all`, of the drafts behind them the ones up to its own or those of its mask
+      const int all = valid ? len - a.T : -1;
+      const uint64_t mask = !valid ? 0ull : a.tree_mask ? __ldg(a.tree_mask + (long long)b * a.T + j) : 0ull;
+      const int qpos = valid ? len - a.T + j : -1;
+      const int sees = a.tree_mask ? all - 1 : qpos;  // the last token up to which all is seen
+      for (int t = 0; t < n; ++t) {
+        const uint32_t k = t_base + t, buf = k & 1;
+        const int t0 = (r0 + t) * kTok + 64 * quarter;
+        if (!(ok = warp_wait(ms.sc_full[buf], k >> 1, abort_flag))) break;
+        if (!(ok = warp_wait(ms.s_full[buf], k >> 1, abort_flag))) break;
+        fence_after_sync();
+        float s[64];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          float v[16];
+          tmem_ld16(tmem + lane_off + kColS + 128 * buf + 64 * col_half + 16 * c, v);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) s[16 * c + i] = v[i];
+        }
+        tmem_wait_ld();
+        settle<64>(s);
+        const float4* const ks = reinterpret_cast<const float4*>(&ms.ks[buf][64 * quarter]);
+        const float4* const ev = reinterpret_cast<const float4*>(&ms.ev[buf][64 * quarter]);
+        float top = -CUDART_INF_F;
+#pragma unroll
+        for (int c = 0; c < 16; ++c) {  // score + E
+          const float4 f = ks[c], e = ev[c];
+          fma2(s[4 * c], s[4 * c + 1], pair(f.x * q_scale, f.y * q_scale), pair(e.x, e.y));
+          fma2(s[4 * c + 2], s[4 * c + 3], pair(f.z * q_scale, f.w * q_scale), pair(e.z, e.w));
+        }
+        if (t0 + 63 > sees) {
+#pragma unroll
+          for (int c = 0; c < 64; ++c) {
+            const int p = t0 + c, draft = p - all;
+            const bool see = a.tree_mask ? draft < 0 || (p < len && draft < 64 && (mask >> draft & 1)) : p <= qpos;
+            if (!(see && valid)) s[c] = -CUDART_INF_F;
+          }
+        }
+#pragma unroll
+        for (int c = 0; c < 64; c += 2) top = max3(top, s[c], s[c + 1]);
+        ms.top[buf][quarter][row] = top;
+        soft_sync();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) top = fmaxf(top, ms.top[buf][i][row]);
+        const float above = top - (m_run == kNone ? -CUDART_INF_F : m_run);  // (NaN where nothing is seen: no move)
+        float alpha = 1.f;
+        const bool move = __any_sync(0xffffffffu, above > kReach);
+        if (above > kReach) {
+          alpha = ex2(m_run - (top - kLift));
+          m_run = top - kLift;
+          l_run *= alpha;
+        }
+        const float from = m_run == kNone ? 0.f : m_run;
+        uint32_t piece[NP][16];
+        {
+          const float4* const dn = reinterpret_cast<const float4*>(&ms.dn[buf][64 * quarter]);
+          uint64_t sum[2] = {0ull, 0ull};
+#pragma unroll
+          for (int c = 0; c < 16; ++c) {
+            const float4 d = dn[c];
+            const float w0 = ex2(s[4 * c] - from), w1 = ex2(s[4 * c + 1] - from), w2 = ex2(s[4 * c + 2] - from), w3 = ex2(s[4 * c + 3] - from);
+            const uint64_t d01 = pair(d.x, d.y), d23 = pair(d.z, d.w), w01 = pair(w0, w1), w23 = pair(w2, w3);
+            asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(sum[0]) : "l"(w01), "l"(d01));
+            asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(sum[1]) : "l"(w23), "l"(d23));
+            uint32_t h[2] = {rope::pack2<__half>(w0, w1), rope::pack2<__half>(w2, w3)}, code[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              code[i] = e5m2_of(h[i]);
+              h[i] = hsub2(h[i], e5m2_wide(code[i]));
+            }
+            piece[0][c] = __byte_perm(code[0], code[1], 0x5410);
+#pragma unroll
+            for (int p = 1; p < NP; ++p) {
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                code[i] = e4m3_of(h[i]);
+                if (p + 1 < NP) h[i] = hsub2(h[i], block::widen2(code[i]));
+              }
+              piece[p][c] = __byte_perm(code[0], code[1], 0x5410);
+            }
+          }
+          float y[4];
+          unpair(sum[0], y[0], y[1]);
+          unpair(sum[1], y[2], y[3]);
+          l_run += (y[0] + y[1]) + (y[2] + y[3]);
+        }
+        warp_arrive(ms.sc_empty[buf]);
+        // O(t - 1) is done: its weights' place is free, and O may be scaled
+        if (t > 0) {
+          if (!(ok = warp_wait(ms.o_done, k - 1, abort_flag))) break;
+          if (move) {
+            fence_after_sync();
+#pragma unroll 1
+            for (int c = 0; c < 8; ++c) {
+              float v[16];
+              const uint32_t cols = tmem + lane_off + 128 * col_half + 16 * c;
+              tmem_ld16(cols, v);
+              tmem_wait_ld();
+              settle<16>(v);
+#pragma unroll
+              for (int i = 0; i < 16; ++i) v[i] *= alpha;
+              tmem_st16(cols, v);
+            }
+            tmem_wait_st();
+          }
+        }
+#pragma unroll
+        for (int p = 0; p < NP; ++p) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            sts128(p_ops + p * S::kPieceP + 8192 * tok_half + sw128(row, 4 * col_half + c), piece[p][4 * c], piece[p][4 * c + 1],
+                   piece[p][4 * c + 2], piece[p][4 * c + 3]);
+        }
+        fence_async_smem();
+        fence_before_sync();
+        warp_arrive_pair(peer_addr(smem_addr(&ms.p_full), 0));
+      }
+      if (ok && n > 0) ok = warp_wait(ms.o_done, t_base + n - 1, abort_flag);
+      fence_after_sync();
+    } else if (warp == kMmaWarp) {
+      // ================= MMA issue: the leader's =================
+      if (rank == 0 && n > 0) {
+        constexpr uint32_t id_s = idesc_f8(kUnitRows, kTok, 0, 0), id_o5 = idesc_f8(kUnitRows, 256, 1, 1), id_o4 = idesc_f8(kUnitRows, 256, 0, 1);
+        constexpr uint32_t type = std::is_same<T, __half>::value ? 0u : 1u;
+        constexpr uint32_t id_p = idesc_f16(kUnitRows, kTok) | type << 7 | type << 10;
+        bool issued = false;
+        uint32_t k_at = at_slot;  // the next slot in the order of use
+        auto wait = [&](uint64_t& bar, uint32_t parity) { return ok = warp_wait(bar, parity, abort_flag); };
+        auto s_mmas = [&](int t) {  // S(t)
+          const uint32_t d = tmem + kColS + 128 * ((t_base + t) & 1);
+#pragma unroll
+          for (int c = 0; c < 5; ++c) {
+            const uint32_t sl = k_at % kSlots, b_at = ring + sl * kSlotBytes;
+            if (!wait(ms.full[sl], k_at / kSlots)) return;
+            if (c < 4) {
+#pragma unroll
+              for (int p = 0; p < NP; ++p)
+#pragma unroll
+                for (int ks = 0; ks < 4; ++ks)
+                  pair_mma_f8(d, sdesc(q_ops + p * S::kPieceQ + 8192 * c + 32 * ks), sdesc(b_at + 32 * ks), id_s, c > 0 || p > 0 || ks > 0);
+            } else {
+#pragma unroll
+              for (int ks = 0; ks < 4; ++ks)
+                pair_mma_ss(d, sdesc(q_ops + NP * S::kPieceQ + 32 * ks), sdesc(b_at + 32 * ks), id_p, 1);
+            }
+            issued = true;
+            pair_commit(smem_addr(&ms.empty[sl]), 3);
+            ++k_at;
+          }
+          pair_commit(smem_addr(&ms.s_full[(t_base + t) & 1]), 3);
+        };
+        if (wait(ms.q_full, done_frags)) {
+          fence_after_sync();
+          s_mmas(0);
+        }
+        for (int t = 0; t < n && ok; ++t) {
+          if (t + 1 < n) s_mmas(t + 1);
+          if (!ok || !wait(ms.p_full, t_base + t)) break;
+          fence_after_sync();
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {  // 64 tokens
+            const uint32_t sl = k_at % kSlots, b_at = ring + sl * kSlotBytes;
+            if (!wait(ms.full[sl], k_at / kSlots)) break;
+            if ((r0 + t) * kTok + 64 * (g + 1) > end) {
+              if (!wait(ms.tail_done[sl], tails >> sl & 1)) break;
+              tails ^= 1u << sl;
+            }
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks) {
+              const uint32_t w_at = p_ops + 8192 * (g >> 1) + 64 * (g & 1) + 32 * ks;
+#pragma unroll
+              for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int p = 0; p < NP; ++p)
+                  pair_mma_f8(tmem + 128 * h, sdesc(w_at + p * S::kPieceP), sdesc(b_at + 8192 * h + 4096 * ks), p == 0 ? id_o5 : id_o4,
+                              t > 0 || g > 0 || ks > 0 || p > 0);
+            }
+            pair_commit(smem_addr(&ms.empty[sl]), 3);
+            ++k_at;
+          }
+          if (!ok) break;
+          pair_commit(smem_addr(&ms.o_done), 3);
+        }
+        if (!ok && issued) {  // nothing may be running when the tensor memory is freed
+          pair_commit(smem_addr(&ms.drain), 3);
+          for (int i = 0; i < kWaitLimit; ++i)
+            if (mbar_test(smem_addr(&ms.drain), 0u)) break;
+        }
+      }
+    } else if (warp == kCopyWarp) {
+      // ================= copies: this CTA's share =================
+      const int32_t* table = a.block_table + (size_t)b * a.max_pages;
+      const int per_half = 128 / box, per_slot = 64 / box;  // boxes
+      uint32_t c_at = at_slot;
+      // boxes 0 .. 256 / box - 1 of a tile, a lane each: page (or -1) and row in it
+      auto place = [&](int t, int& page, int& in_page) {
+        const int p = (r0 + t) * kTok + box * lane;
+        page = -1, in_page = 0;
+        if (t >= n || box * lane >= kTok || p >= end) return;
+        page = __ldg(table + p / P);
+        in_page = p % P;
+        if (page < 0 || page >= pool.num_pages) {
+          if (a.status) atomicOr(a.status, RQ_STATUS_BAD_PAGE);
+          page = 0;
+        }
+      };
+      auto free_slot = [&]() {
+        const uint32_t sl = c_at % kSlots;
+        return c_at < kSlots || (ok = warp_wait(ms.empty[sl], c_at / kSlots - 1, abort_flag));
+      };
+      auto boxes = [&](int p, int count) { return min(max(0, (end - p + box - 1) / box), count); };  // from token p on
+      auto keys = [&](int t, int page, int in_page) {
+        const int p = (r0 + t) * kTok;
+        const int both = boxes(p, per_half) + boxes(p + 128, per_half), mine = boxes(p + 128 * (int)rank, per_half);
+        const int pg = __shfl_sync(0xffffffffu, page, per_half * (int)rank + lane & 31), ip = __shfl_sync(0xffffffffu, in_page, per_half * (int)rank + lane & 31);
+        for (int c = 0; c < 5; ++c, ++c_at) {
+          if (!free_slot()) return;
+          const uint32_t sl = c_at % kSlots;
+          if (rank == 0) elect_expect(smem_addr(&ms.full[sl]), (uint32_t)(both * box * 128));
+          __syncwarp();
+          if (lane < mine) load_pair(ring + sl * kSlotBytes + lane * box * 128, map, ip, c, pg, peer_addr(smem_addr(&ms.full[sl]), 0));
+        }
+      };
+      auto values = [&](int t, int page, int in_page) {
+        for (int g = 0; g < 4; ++g, ++c_at) {
+          if (!free_slot()) return;
+          const uint32_t sl = c_at % kSlots;
+          const int p = (r0 + t) * kTok + 64 * g, count = boxes(p, per_slot);
+          const bool tail = p + 64 > end;
+          // lane: box lane % per_slot of dims 128 (2 rank + lane / per_slot) ..
+          const int i = lane % per_slot, c = lane / per_slot;
+          const int pg = __shfl_sync(0xffffffffu, page, per_slot * g + i & 31), ip = __shfl_sync(0xffffffffu, in_page, per_slot * g + i & 31);
+          const uint32_t dst = ring + sl * kSlotBytes + 8192 * c + i * box * 128;
+          const bool mine = c < 2 && i < count;
+          if (!tail) {
+            if (rank == 0) elect_expect(smem_addr(&ms.full[sl]), 2 * kSlotBytes);
+            __syncwarp();
+            if (mine) load_pair(dst, map, ip, 2 * (int)rank + c, pg, peer_addr(smem_addr(&ms.full[sl]), 0));
+          } else {  // the tail's warp of this CTA first
+            elect_expect(smem_addr(&ms.here[sl]), (uint32_t)(2 * count * box * 128));
+            __syncwarp();
+            if (mine) load_here(dst, map, ip, 2 * (int)rank + c, pg, smem_addr(&ms.here[sl]));
+            if (rank == 0) warp_arrive(ms.full[sl]);
+          }
+        }
+      };
+      int page[2], in_page[2];
+      place(0, page[0], in_page[0]);
+      place(1, page[1], in_page[1]);
+      if (n > 0) keys(0, page[0], in_page[0]);
+      for (int t = 0; t < n && ok; ++t) {
+        int next_page, next_in;
+        place(t + 2, next_page, next_in);
+        if (t + 1 < n) keys(t + 1, page[1], in_page[1]);
+        if (ok) values(t, page[0], in_page[0]);
+        page[0] = page[1], in_page[0] = in_page[1];
+        page[1] = next_page, in_page[1] = next_in;
+      }
+    } else if (warp == kScaleWarp) {
+      // ================= scales =================
+      const int32_t* table = a.block_table + (size_t)b * a.max_pages;
+      auto bytes_of = [&](int t) {  // eight tokens of a tile to a lane
+        const int p = (r0 + t) * kTok + 8 * lane;
+        if (t >= n || p >= end) return make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
+        int page = __ldg(table + p / P);
+        if (page < 0 || page >= pool.num_pages) page = 0;  // (reported by the copies)
+        return __ldg(reinterpret_cast<const uint2*>(pool.pages + page_at(page, P) + 640 * P + p % P));
+      };
+      uint2 now = bytes_of(0);
+      for (int t = 0; t < n; ++t) {
+        const uint32_t k = t_base + t, buf = k & 1;
+        const uint2 next = bytes_of(t + 1);
+        if (k >= 2 && !(ok = warp_wait(ms.sc_empty[buf], (k >> 1) - 1, abort_flag))) break;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          float f[3][4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const uint32_t byte = (i ? now.y : now.x) >> (8 * q) & 0xFFu;
+            const int e = byte == kNanExp ? 0 : min(max((int)byte - 127, kMinExp), kMaxExp);
+            f[0][q] = scale_of_byte(byte);
+            f[1][q] = (float)e;
+            f[2][q] = block::pow2(-e);
+          }
+          reinterpret_cast<float4*>(ms.ks[buf])[2 * lane + i] = make_float4(f[0][0], f[0][1], f[0][2], f[0][3]);
+          reinterpret_cast<float4*>(ms.ev[buf])[2 * lane + i] = make_float4(f[1][0], f[1][1], f[1][2], f[1][3]);
+          reinterpret_cast<float4*>(ms.dn[buf])[2 * lane + i] = make_float4(f[2][0], f[2][1], f[2][2], f[2][3]);
+        }
+        warp_arrive(ms.sc_full[buf]);
+        now = next;
+      }
+    } else if (warp == kTailWarp) {
+      // ================= the tail: zeros behind the last token that is seen =================
+      if (n > 0) {
+        const int t = n - 1, p0 = (r0 + t) * kTok;
+        // the tile's value slots are the fragment's last four
+        for (int g = 0; g < 4; ++g) {
+          const int p = p0 + 64 * g;
+          if (p + 64 <= end) continue;
+          const uint32_t seq = at_slot + 9u * n - 4u + g, sl = seq % kSlots;
+          if (!(ok = warp_wait(ms.here[sl], tails >> sl & 1, abort_flag))) break;
+          tails ^= 1u << sl;
+          const int first = max(0, end - p);
+          for (int i = first * 16 + lane; i < 64 * 16; i += 32)  // row i / 16: eight chunks of either 128 dims
+            sts128(ring + sl * kSlotBytes + 8192 * (i >> 3 & 1) + (i >> 4) * 128 + (i & 7) * 16, 0u, 0u, 0u, 0u);
+          fence_async_smem();
+          warp_arrive_pair(peer_addr(smem_addr(&ms.tail_done[sl]), 0));
+        }
+      }
+    }
+    if (!ok && lane == 0 && a.status) atomicOr(a.status, RQ_STATUS_TIMEOUT);
+    done_tiles += n;
+    done_frags += n > 0;
+    at_slot += 9u * n;
+    fence_before_sync();
+    __syncthreads();
+    fence_after_sync();
+    if (ms.abort) break;  // uniform: no role raises it between the barrier and here
+
+    // ---- write the rows, or the fragment's part of them ----
+    if (warp < kSoftWarps) {
+      ms.top[0][quarter][row] = l_run;
+      soft_sync();
+      const float l = (ms.top[0][0][row] + ms.top[0][1][row]) + (ms.top[0][2][row] + ms.top[0][3][row]);
+      const bool whole = ms.f.whole;
+      const int sees = valid ? (a.tree_mask ? len - a.T - 1 : len - a.T + j) : -1;
+      // a row that sees nothing is zero; one whose scores are all minus infinity is NaN
+      const float empty = whole && sees >= 0 ? CUDART_NAN_F : 0.f, inv = whole ? 1.f / l : 1.f;
+      const int srow = kRows * (int)rank + row, dim0 = 256 * tok_half + 128 * col_half;
+      float* const slot = a.ws + (2ll * me + (me == ms.f.range ? ms.f.range_last : 0)) * kSlotFloats;
+      T* const out = reinterpret_cast<T*>(a.out) + (((size_t)b * a.T + j) * a.heads + head) * kLatentDim + dim0;
+#pragma unroll 2
       for (int c = 0; c < 8; ++c) {
-        const uint4 v = *reinterpret_cast<const uint4*>(base + 512 * P + chunk_at(r, c));
-        const uint32_t w4[4] = {v.x, v.y, v.z, v.w};
-        for (int k = 0; k < 4; ++k) {
-          const float2 f = rope::unpack2<T>(w4[k]);
-          sum += f.x * q[kLatentDim + 8 * c + 2 * k] + f.y * q[kLatentDim + 8 * c + 2 * k + 1];
+        float y[16];
+        if (n > 0) {
+          __syncwarp();
+          tmem_ld16(tmem + lane_off + 128 * col_half + 16 * c, y);
+          tmem_wait_ld();
+          settle<16>(y);
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) y[i] = l == 0.f || n == 0 ? empty : y[i] * inv;
+        if (!valid) continue;
+        if (whole) {
+          uint4* const dst = reinterpret_cast<uint4*>(out) + 2 * c;
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            dst[i] = make_uint4(rope::pack2<T>(y[8 * i], y[8 * i + 1]), rope::pack2<T>(y[8 * i + 2], y[8 * i + 3]),
+                                rope::pack2<T>(y[8 * i + 4], y[8 * i + 5]), rope::pack2<T>(y[8 * i + 6], y[8 * i + 7]));
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            reinterpret_cast<float4*>(slot)[(dim0 / 4 + 4 * c + i) * kUnitRows + srow] =
+                make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
         }
       }
-      s = sum * scale * up;
+      if (!whole && quarter == 0) {
+        slot[kUnitRows * kLatentDim + srow] = m_run;
+        slot[kUnitRows * kLatentDim + kUnitRows + srow] = l;
+      }
     }
-    float top = s;
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    if ((tid & 31) == 0) red[tid >> 5] = top;
-    __syncthreads();
-    top = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
-    const float m_new = fmaxf(m, top), from = m_new == -CUDART_INF_F ? 0.f : m_new;
-    const float alpha = m == -CUDART_INF_F ? 0.f : exp2f(m - from);
-    m = m_new;
-    const float e = see ? exp2f(s - from) : 0.f;
-    w[tid] = e * scale;
-    float sum = e;
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    __syncthreads();
-    if ((tid & 31) == 0) red[tid >> 5] = sum;
-    __syncthreads();
-    l = l * alpha + (red[0] + red[1] + red[2] + red[3]);
-    for (int i = 0; i < 4; ++i) acc[i] *= alpha;
-    for (int k = 0; k < min(kThreads, len - t0); ++k) {
-      if (w[k] == 0.f) continue;
-      const int d = 4 * tid;
-      const uint32_t v = *reinterpret_cast<const uint32_t*>(at[k] + (d >> 7) * 128 * P + chunk_at(off[k], (d & 127) >> 4) + (d & 15));
-      const float2 lo = rope::unpack2<__half>(block::widen2(v)), hi = rope::unpack2<__half>(block::widen2_hi(v));
-      acc[0] = fmaf(w[k], lo.x, acc[0]), acc[1] = fmaf(w[k], lo.y, acc[1]);
-      acc[2] = fmaf(w[k], hi.x, acc[2]), acc[3] = fmaf(w[k], hi.y, acc[3]);
+    fence_before_sync();
+    __syncthreads();  // ms.f and the rows' sums are written again
+    fence_after_sync();
+  }
+  if (ms.abort) {  // copies in flight land before the block ends: a millisecond is many times what one takes
+    const long long start = clock64();
+    while (clock64() - start < 2000000) __nanosleep(1000);
+  }
+  fence_before_sync();
+  __syncthreads();
+  cluster_sync();  // the peer is done with this CTA's operands and barriers
+  fence_after_sync();
+  if (warp == kMmaWarp) pair_tmem_dealloc(tmem, 512);
+}
+
+// Joins the parts of units that span ranges.  A CTA takes 8 rows and 32 / G groups of 4 dims of a unit, its parts in G shares.
+template <typename T, int G>
+__global__ void __launch_bounds__(256) latent_join_kernel(const LatentAttnArgs a, const int4* info, int row_groups) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  __shared__ float part[G][32 / G][8][6];
+  const int tid = threadIdx.x, r8 = tid & 7, d = (tid >> 3) % (32 / G), share = (tid >> 3) / (32 / G);
+  const long long unit = blockIdx.x / row_groups;
+  const int4 u = __ldg(info + unit);
+  if (u.y == 0) return;
+  const long long n_rows = (long long)a.T * a.heads;
+  const int n_rt = (int)((n_rows + kUnitRows - 1) / kUnitRows), b = (int)(unit / n_rt), rt = (int)(unit % n_rt);
+  const int srow = 8 * (int)(blockIdx.x % row_groups) + r8, d4 = blockIdx.y * (32 / G) + d;
+  const long long urow = (long long)rt * kUnitRows + srow;
+  const bool valid = urow < n_rows;
+  float m = kNone, l = 0.f;
+  float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (valid) {
+#pragma unroll 4
+    for (int f = share; f < u.y; f += G) {
+      const float* s = a.ws + (2ll * (u.x + f) + (f == 0 ? u.z : 0)) * kSlotFloats;
+      const float mf = __ldcg(s + kUnitRows * kLatentDim + srow), lf = __ldcg(s + kUnitRows * kLatentDim + kUnitRows + srow);
+      const float4 v = __ldcg(reinterpret_cast<const float4*>(s) + d4 * kUnitRows + srow);
+      const float to = fmaxf(m, mf), wa = ex2(m - to), w = ex2(mf - to);
+      m = to;
+      l = fmaf(l, wa, lf * w);
+      y.x = fmaf(y.x, wa, v.x * w), y.y = fmaf(y.y, wa, v.y * w), y.z = fmaf(y.z, wa, v.z * w), y.w = fmaf(y.w, wa, v.w * w);
     }
   }
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  T* out = reinterpret_cast<T*>(a.out) + ((size_t)token * a.heads + h) * kLatentDim + 4 * tid;
-  *reinterpret_cast<uint2*>(out) =
-      make_uint2(rope::pack2<T>(acc[0] * inv, acc[1] * inv), rope::pack2<T>(acc[2] * inv, acc[3] * inv));
+  if (G > 1) {
+    float* p = part[share][d][r8];
+    p[0] = m, p[1] = l, p[2] = y.x, p[3] = y.y, p[4] = y.z, p[5] = y.w;
+    __syncthreads();
+    if (share > 0) return;
+#pragma unroll
+    for (int g = 1; g < G; ++g) {
+      const float* p = part[g][d][r8];
+      const float to = fmaxf(m, p[0]), wa = ex2(m - to), w = ex2(p[0] - to);
+      m = to;
+      l = fmaf(l, wa, p[1] * w);
+      y.x = fmaf(y.x, wa, p[2] * w), y.y = fmaf(y.y, wa, p[3] * w), y.z = fmaf(y.z, wa, p[4] * w), y.w = fmaf(y.w, wa, p[5] * w);
+    }
+  }
+  if (!valid) return;
+  const int j = (int)(urow / a.heads), head = (int)(urow % a.heads), len = __ldg(a.seq_lens + b);
+  const float none = (a.tree_mask ? len - a.T - 1 : len - a.T + j) >= 0 ? CUDART_NAN_F : 0.f, inv = 1.f / l;
+  y = l == 0.f ? make_float4(none, none, none, none) : make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv);
+  T* const out = reinterpret_cast<T*>(a.out) + (((size_t)b * a.T + j) * a.heads + head) * kLatentDim + 4 * d4;
+  *reinterpret_cast<uint2*>(out) = make_uint2(rope::pack2<T>(y.x, y.y), rope::pack2<T>(y.z, y.w));
+}
+
+template <typename T>
+cudaError_t launch(const CUtensorMap& map, const LatentPool& pool, const LatentAttnArgs& a, int box, int num_sms, int4* info, long long units,
+                   cudaStream_t stream) {
+  const int pairs = num_sms / 2;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = 2;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2u * (unsigned)pairs);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = Shape<T>::kOffMisc + sizeof(Misc) + 1024;
+  cfg.stream = stream;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, latent_kernel<T>, map, pool, a, box, info);
+  if (e != cudaSuccess) return e;
+  const long long rows = (long long)a.T * a.heads;
+  const int row_groups = (int)((rows < kUnitRows ? rows : kUnitRows) + 7) / 8;
+  if (units * row_groups > 0x7fffffffLL) return cudaErrorInvalidValue;
+  const bool many = units * 8 <= pairs;  // eight parts a unit or more
+  cudaLaunchAttribute behind[1];
+  behind[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  behind[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t join = {};
+  join.gridDim = dim3((unsigned)(units * row_groups), many ? 32u : 4u);
+  join.blockDim = dim3(256);
+  join.stream = stream;
+  join.attrs = behind;
+  join.numAttrs = 1;
+  return many ? cudaLaunchKernelEx(&join, latent_join_kernel<T, 8>, a, (const int4*)info, row_groups)
+              : cudaLaunchKernelEx(&join, latent_join_kernel<T, 1>, a, (const int4*)info, row_groups);
 }
 
 }  // namespace
 
-size_t latent_attention_workspace(int num_sms) { return (size_t)num_sms; }
-cudaError_t latent_attention_prepare() { return cudaSuccess; }
+size_t latent_attention_workspace(int num_sms, long long rows, int max_batch) {
+  const size_t parts = 2 * (size_t)(num_sms / 2) * kSlotFloats;  // two slots a pair
+  return parts + 4 * (size_t)((rows + kUnitRows - 1) / kUnitRows) * (size_t)max_batch;  // and a note for each unit
+}
+
+cudaError_t latent_attention_prepare() {
+  const int h = Shape<__half>::kOffMisc + sizeof(Misc) + 1024, b = Shape<__nv_bfloat16>::kOffMisc + sizeof(Misc) + 1024;
+  cudaError_t e = cudaFuncSetAttribute(latent_kernel<__half>, cudaFuncAttributeMaxDynamicSharedMemorySize, h);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(latent_kernel<__nv_bfloat16>, cudaFuncAttributeMaxDynamicSharedMemorySize, b);
+  return e;
+}
 
 cudaError_t launch_latent_attention(const LatentPool& pool, const LatentAttnArgs& a, int num_sms, cudaStream_t stream) {
-  (void)num_sms;
-  const long long rows = (long long)a.B * a.T * a.heads;
-  if (rows > 0x7fffffffLL) return cudaErrorInvalidValue;
-  if (pool.bf16)
-    latent_rows_kernel<__nv_bfloat16><<<(unsigned)rows, kThreads, 0, stream>>>(pool, a);
-  else
-    latent_rows_kernel<__half><<<(unsigned)rows, kThreads, 0, stream>>>(pool, a);
-  return cudaGetLastError();
+  if (!tensor_map_encoder()) return cudaErrorNotSupported;
+  const long long units = (long long)a.B * (((long long)a.T * a.heads + kUnitRows - 1) / kUnitRows);
+  const cuuint64_t P = (cuuint64_t)pool.page_size;
+  const int box = pool.page_size % 64 == 0 ? 64 : pool.page_size % 32 == 0 ? 32 : 16;  // rows that stand together in a page
+  CUtensorMap map;
+  const cuuint64_t sizes[4] = {128, P, 5, (cuuint64_t)pool.num_pages}, strides[3] = {128, 128 * P, kLatentTokenBytes * P};
+  const cuuint32_t boxes[4] = {128u, (cuuint32_t)box, 1u, 1u}, steps[4] = {1u, 1u, 1u, 1u};
+  if (tensor_map_encoder()(&map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<uint8_t*>(pool.pages), sizes, strides, boxes, steps,
+                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    return cudaErrorInvalidValue;
+  int4* const info = reinterpret_cast<int4*>(a.ws + 2 * (size_t)(num_sms / 2) * kSlotFloats);
+  return pool.bf16 ? launch<__nv_bfloat16>(map, pool, a, box, num_sms, info, units, stream)
+                   : launch<__half>(map, pool, a, box, num_sms, info, units, stream);
 }
 
 }  // namespace rq

@@ -19,7 +19,6 @@
 // Tensor memory: O_b at columns 128 b, S_b at 256 + 128 b with W_b over its first half.
 // Few rows and long sequences: a cluster of up to four pairs shares a unit's tiles, and joins through distributed shared
 // memory.  Every wait is bounded: one that runs out sets RQ_STATUS_TIMEOUT and an abort flag every role polls.
-#include <cuda.h>
 #include <math_constants.h>
 
 #include <cstddef>
@@ -28,6 +27,7 @@
 #include "../../include/rq.h"
 #include "rq_roles.cuh"
 #include "rq_rope.cuh"
+#include "rq_tma.h"
 
 namespace rq {
 namespace {
@@ -452,28 +452,13 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
   if (warp == kMmaWarp) pair_tmem_dealloc(tmem, 512);
 }
 
-typedef CUresult (*EncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                             const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeFn encoder() {
-  static const EncodeFn fn = [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult found;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &found) != cudaSuccess ||
-        found != cudaDriverEntryPointSuccess)
-      p = nullptr;
-    return (EncodeFn)p;
-  }();
-  return fn;
-}
-
 // Boxes of 64 dims and `box` rows of one head of x [n][heads][dims].
 bool encode(CUtensorMap* map, bool bf16, const HeadsDev& x, int dims, int n, int box) {
   const cuuint64_t sizes[3] = {(cuuint64_t)dims, (cuuint64_t)x.heads, (cuuint64_t)n};
   // a stride that is not used (one head, one row) may be anything
   const cuuint64_t strides[2] = {(cuuint64_t)(x.heads > 1 ? x.head_stride : dims) * 2, (cuuint64_t)(n > 1 ? x.stride : dims) * 2};
   const cuuint32_t boxes[3] = {64u, 1u, (cuuint32_t)box}, steps[3] = {1u, 1u, 1u};
-  return encoder()(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(x.x), sizes, strides,
+  return tensor_map_encoder()(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(x.x), sizes, strides,
                    boxes, steps, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -500,7 +485,7 @@ cudaError_t launch(const Maps& maps, const PromptArgs& a, int splits, int n_rb, 
 }  // namespace
 
 cudaError_t launch_prompt_attention(const PromptArgs& a, int num_sms, cudaStream_t stream) {
-  if (!encoder()) return cudaErrorNotSupported;
+  if (!tensor_map_encoder()) return cudaErrorNotSupported;
   const int n_rb = (a.max_new + kUnitRows - 1) / kUnitRows;
   if (n_rb > 65535) return cudaErrorInvalidValue;
   Maps maps{};

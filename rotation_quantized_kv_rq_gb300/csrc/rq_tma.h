@@ -1,0 +1,25 @@
+// Tensor maps of the TMA copies: the driver's encoder, found at run time (the library links the runtime alone).
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+namespace rq {
+
+typedef CUresult (*TensorMapEncode)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                                    const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                    CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+inline TensorMapEncode tensor_map_encoder() {  // null without one
+  static const TensorMapEncode fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &found) != cudaSuccess ||
+        found != cudaDriverEntryPointSuccess)
+      p = nullptr;
+    return (TensorMapEncode)p;
+  }();
+  return fn;
+}
+
+}  // namespace rq
