@@ -477,7 +477,8 @@ int rq_latent_append(rq_latent *ctx, const rq_rope *rope, const void *c, long lo
  *   pages, block_table, max_pages, seq_lens   as rq_decode_attention
  *   out         device [B][T][num_heads][512], 16-byte aligned
  * 0 < seq_lens[b] < T sets RQ_STATUS_BAD_LEN.  Calls on one context must not overlap on the GPU.
- * Errors: RQ_ERR_INVALID, RQ_ERR_CAPACITY (B, T or max_pages above the context's), RQ_ERR_CUDA.
+ * Errors: RQ_ERR_INVALID, RQ_ERR_CAPACITY (B, T or max_pages above the context's, or B * ceil(T * num_heads / 128) *
+ * ceil(max_pages * P / 256) above 2^31 - 1), RQ_ERR_CUDA.
  */
 int rq_latent_attention(rq_latent *ctx, const rq_heads *q_c, const rq_heads *q_pe, int T, const uint64_t *tree_mask,
                         const void *pages, const int32_t *block_table, int max_pages, const int32_t *seq_lens, int B, void *out,

@@ -47,6 +47,9 @@ using namespace tc;
 constexpr int kSoftWarps = 8, kMmaWarp = 8, kCopyWarp = 9, kScaleWarp = 10, kTailWarp = 11, kThreads = 384;
 constexpr int kRows = 64, kUnitRows = 128, kTok = 256;  // rows of a CTA, of a pair; tokens of a tile
 constexpr uint32_t kSlotBytes = 16384;
+// Slots are filled and given back in units of two or one: a tile's keys are three units (dims 0 .. 255, 256 .. 511, the
+// position parts), its values two (128 tokens each).  A wait or a commit costs the issuing warp about as much as three MMAs.
+constexpr int kUnits = 8;  // barriers for units: more than there can be in the ring
 constexpr uint32_t kColS = 256;
 // weights are 2^(score + E - m), m the running maximum of score + E less kLift, moved where a score is past it by more than
 // kReach: below 2^12 an e5m2 number's remainder stays within e4m3's 448
@@ -66,20 +69,21 @@ struct Shape {
 
 struct Frag {           // tiles r0 .. r0 + n - 1 of one unit
   int b, rt, r0, n, len, end;  // end: tokens that the unit's rows see lie before it
-  int whole, frags;     // the unit is all here; else its number of fragments
+  int whole;            // the unit is all here
   int range, range_last;  // its first range, and whether the fragment there is that range's last
   int done;             // no more fragments
 };
 struct Misc {
-  // the leader's: a slot is full; the queries; W(t); a tail's zeros are written
-  uint64_t full[7], q_full, p_full, tail_done[7];
-  // both CTAs': a slot is read; S(t); O(t); drained; a slot of the tail is here; scales of a tile
-  uint64_t empty[7], s_full[2], o_done, drain, here[7], sc_full[2], sc_empty[2];
+  // the leader's: a unit is full; the queries; W(t); a tail's zeros are written
+  uint64_t full[kUnits], q_full, p_full, tail_done[kUnits];
+  // both CTAs': a unit is read; S(t); O(t); drained; a unit of the tail is here; scales of a tile
+  uint64_t empty[kUnits], s_full[2], o_done, drain, here[kUnits], sc_full[2], sc_empty[2];
   Frag f;
   uint32_t tmem;
   int abort;
   alignas(16) float ks[2][kTok], ev[2][kTok], dn[2][kTok];  // 2^E (or NaN), E, 2^-E of a tile's tokens
   float top[2][4][kRows];
+  float q_scale[kRows];
 };
 static_assert(Shape<__half>::kOffMisc + sizeof(Misc) + 1024 <= 232448, "one CTA's shared memory");
 static_assert(Shape<__nv_bfloat16>::kOffMisc + sizeof(Misc) + 1024 <= 232448, "one CTA's shared memory");
@@ -95,7 +99,7 @@ __device__ __forceinline__ Unit unit_of(const LatentAttnArgs& a, int cap, int b,
     u.len = u.len < 0 ? 0 : min(u.len, cap);
   }
   const long long rows = (long long)a.T * a.heads;
-  const int last = (int)((min(rows, (rt + 1ll) * kUnitRows) - 1) / a.heads);  // the last row's token
+  const int last = (int)((uint32_t)(min(rows, (rt + 1ll) * kUnitRows) - 1) / (uint32_t)a.heads);  // the last row's token (rows: below 2^30)
   u.end = a.tree_mask ? u.len : max(0, min(u.len, u.len - a.T + last + 1));
   u.tiles = max(1, (u.end + kTok - 1) / kTok);  // rows that see nothing are written too
   return u;
@@ -105,11 +109,20 @@ __device__ __forceinline__ Unit unit_of(const LatentAttnArgs& a, int cap, int b,
 __host__ __device__ constexpr uint32_t idesc_f8(int M, int N, uint32_t a_type, uint32_t b_rows) {
   return idesc_f16(M, N) | a_type << 7 | b_rows << 16;
 }
-__device__ __forceinline__ void pair_mma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t accumulate) {
+// An operand by the low word of its descriptor (address >> 4; the high word is the same for all: 1024 bytes from eight rows to the
+// next, the 128-byte swizzle).  Few instructions an MMA: the issuing warp shares its scheduler with the softmax.
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr) { return saddr >> 4 | 1u << 16; }
+__device__ __forceinline__ void pair_mma_f8(uint32_t d, uint32_t a, uint32_t b, uint32_t id, uint32_t accumulate) {
   asm volatile(
-      "{\n .reg .pred p, e;\n elect.sync _|e, 0xffffffff;\n setp.ne.b32 p, %4, 0;\n"
-      " @e tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n}" ::"r"(d),
-      "l"(a), "l"(b), "r"(id), "r"(accumulate));
+      "{\n .reg .pred p, e;\n .reg .b64 a, b;\n elect.sync _|e, 0xffffffff;\n setp.ne.b32 p, %4, 0;\n mov.b64 a, {%1, %5};\n"
+      " mov.b64 b, {%2, %5};\n @e tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], a, b, %3, p;\n}" ::"r"(d),
+      "r"(a), "r"(b), "r"(id), "r"(accumulate), "n"(0x40004040));
+}
+__device__ __forceinline__ void pair_mma_16(uint32_t d, uint32_t a, uint32_t b, uint32_t id) {
+  asm volatile(
+      "{\n .reg .pred p, e;\n .reg .b64 a, b;\n elect.sync _|e, 0xffffffff;\n setp.ne.b32 p, 1, 0;\n mov.b64 a, {%1, %4};\n"
+      " mov.b64 b, {%2, %4};\n @e tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %3, p;\n}" ::"r"(d),
+      "r"(a), "r"(b), "r"(id), "n"(0x40004040));
 }
 // A box of the pool's planes ([page][plane][row][128 bytes]) for each lane whose turn it is; the bytes count at `bar`, a barrier of
 // the leader (pair), or of this CTA.
@@ -128,23 +141,41 @@ __device__ __forceinline__ void load_here(uint32_t dst, const CUtensorMap& map, 
 }
 __device__ __forceinline__ void soft_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
-// Two f32 to e4m3 (past 448 to 448), and back as f16x2; e5m2 is an fp16 number's upper byte.
-__device__ __forceinline__ uint32_t e4m3_of(uint32_t h2) {
-  uint32_t c;
-  asm("{\n .reg .b16 c;\n cvt.rn.satfinite.e4m3x2.f16x2 c, %1;\n cvt.u32.u16 %0, c;\n}" : "=r"(c) : "r"(h2));
+// Pieces of two weights (fp16, 0 to 2^12) in few operations of the integer and fp16 pipes (a conversion to 8 bits takes 14
+// cycles of a scheduler, these two).  e5m2 is an fp16 number's upper byte: the first piece is the number rounded to that, its
+// code the upper bytes.  What is left is within 2^8; times 2^-8 its fp16 pattern, moved up by a bit, is e4m3's in the upper
+// byte (both have their smallest normal and their steps below it in the same place): rounded by half a step, the sign put back.
+__device__ __forceinline__ uint32_t first_piece(uint32_t& h) {  // (ties go up: the next piece takes what is left either way)
+  const uint32_t c = h + 0x00800080u & 0xFF00FF00u;
+  asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(h) : "r"(c));
+  asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(h) : "r"(0x1C001C00u));  // 2^-8
   return c;
 }
-__device__ __forceinline__ uint32_t e5m2_of(uint32_t h2) {
-  uint32_t c;
-  asm("{\n .reg .b16 c;\n cvt.rn.satfinite.e5m2x2.f16x2 c, %1;\n cvt.u32.u16 %0, c;\n}" : "=r"(c) : "r"(h2));
-  return c;
+__device__ __forceinline__ uint32_t next_piece(uint32_t h) {  // h times 2^-8
+  return (2u * h + 0x00800080u) & 0x7FFF7FFFu | h & 0x80008000u;
 }
-__device__ __forceinline__ uint32_t hsub2(uint32_t a, uint32_t b) {
+// What is left of h behind the piece of next_piece.
+__device__ __forceinline__ uint32_t behind(uint32_t h, uint32_t code) {
+  const uint32_t c = (code & 0x7F007F00u) >> 1 | h & 0x80008000u;
   uint32_t d;
-  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(h), "r"(c));
   return d;
 }
-__device__ __forceinline__ uint32_t e5m2_wide(uint32_t codes) { return __byte_perm(codes, 0u, 0x1404); }  // {0, lo, 0, hi}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t plus2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
 
 // The smallest E in [-100, 100] with top <= 448 * 2^E, or top <= 2^(15 + E), from top's bits.
 __device__ __forceinline__ int query_exp(uint32_t top_c, uint32_t top_p) {
@@ -169,34 +200,41 @@ __global__ void __launch_bounds__(kThreads, 1)
   const long long n_rows = (long long)a.T * a.heads;
   const int n_rt = (int)((n_rows + kUnitRows - 1) / kUnitRows);
 
-  // ---- the pair's range of tiles: x .. end - 1 of `total`, kept by thread 0 ----
-  const long long pairs = gridDim.x >> 1, me = blockIdx.x >> 1;
-  long long total, parts, x = 0, x_end = 0, at = 0, item = 0;  // at: the first tile of unit `item`
+  // ---- the pair's range of tiles: x .. x_end - 1 of `total`, kept by thread 0 ----
+  // range c starts at c * each + min(c, more)
+  const uint32_t pairs = gridDim.x >> 1, me = blockIdx.x >> 1;
+  uint32_t total, parts, each, more, x, x_end, at, item;  // at: the first tile of unit `item`
   {
-    long long* const scan = reinterpret_cast<long long*>(smem_raw + (base - smem_addr(smem_raw)));  // over Q
-    __shared__ long long s_found[2];
-    const long long n_items = (long long)a.B * n_rt, chunk = (n_items + kThreads - 1) / kThreads;
-    long long mine = 0;
-    for (long long i = tid * chunk; i < min(n_items, (tid + 1) * chunk); ++i)
-      mine += unit_of(a, cap, (int)(i / n_rt), (int)(i % n_rt), blockIdx.x == 0).tiles;
-    scan[tid] = mine;
-    __syncthreads();
-    for (int o = 1; o < kThreads; o <<= 1) {
-      const long long v = tid >= o ? scan[tid - o] : 0;
-      __syncthreads();
-      scan[tid] += v;
-      __syncthreads();
+    __shared__ uint32_t s_sums[kThreads / 32], s_found[2];
+    const uint32_t n_items = (uint32_t)a.B * n_rt, chunk = (n_items + kThreads - 1) / kThreads;
+    uint32_t mine = 0;
+    for (uint32_t i = tid * chunk; i < min(n_items, (tid + 1) * chunk); ++i)
+      mine += unit_of(a, cap, (int)(i / (uint32_t)n_rt), (int)(i % (uint32_t)n_rt), blockIdx.x == 0).tiles;
+    uint32_t sum = mine;  // inclusive, over the warp, then over the warps before
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t v = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += v;
     }
-    total = scan[kThreads - 1];
+    if (lane == 31) s_sums[warp] = sum;
+    __syncthreads();
+    uint32_t before = 0;
+    total = 0;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) {
+      if (w == warp) before = total;
+      total += s_sums[w];
+    }
     parts = min(pairs, total);
     if (me >= parts) return;  // both CTAs of a pair
-    x = me * total / parts;
-    x_end = (me + 1) * total / parts;
-    const long long before = scan[tid] - mine;
-    if (x >= before && x < scan[tid]) {
-      long long p = before, i = tid * chunk;
+    each = total / parts, more = total - each * parts;
+    x = me * each + min(me, more);
+    x_end = x + each + (me < more ? 1u : 0u);
+    before += sum - mine;
+    if (x >= before && x < before + mine) {
+      uint32_t p = before, i = tid * chunk;
       for (;; ++i) {
-        const long long n = unit_of(a, cap, (int)(i / n_rt), (int)(i % n_rt), false).tiles;
+        const uint32_t n = unit_of(a, cap, (int)(i / (uint32_t)n_rt), (int)(i % (uint32_t)n_rt), false).tiles;
         if (x < p + n) break;
         p += n;
       }
@@ -207,8 +245,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     at = s_found[0];
     item = s_found[1];
   }
+  auto range_of = [&](uint32_t tile) {  // the range that holds a tile
+    const uint32_t longer = more * (each + 1u);
+    return tile < longer ? tile / (each + 1u) : more + (tile - longer) / each;
+  };
   if (tid == 0) {
-    for (int i = 0; i < kSlots; ++i) {
+    for (int i = 0; i < kUnits; ++i) {
       mbar_init(smem_addr(&ms.full[i]), 1);
       mbar_init(smem_addr(&ms.empty[i]), 1);
       mbar_init(smem_addr(&ms.here[i]), 1);
@@ -239,28 +281,29 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int quarter = 2 * tok_half + col_half;
   const uint32_t lane_off = (uint32_t)(32 * quad) << 16;
   uint32_t done_tiles = 0, done_frags = 0;  // with tokens: tiles and fragments before
-  uint32_t at_slot = 0;                     // slots used before
-  uint32_t tails = 0;                       // parity of the tail's use of each slot
+  uint32_t tails = 0;                       // parity of the tail's use of each unit's barriers
+  // copies: slots and units asked for, slots and units given back, which of the last 32 units are of two slots
+  uint32_t asked = 0, asked_units = 0, freed = 0, freed_units = 0, twos = 0;
   for (;;) {
     if (tid == 0) {  // the next fragment
       Frag& f = ms.f;
       f.done = x >= x_end;
       if (!f.done) {
-        f.b = (int)(item / n_rt);
-        f.rt = (int)(item % n_rt);
+        f.b = (int)(item / (uint32_t)n_rt);
+        f.rt = (int)(item % (uint32_t)n_rt);
         const Unit un = unit_of(a, cap, f.b, f.rt, false);
         f.len = un.len;
         f.end = un.end;
         f.r0 = (int)(x - at);
-        f.n = (int)min((long long)un.tiles - f.r0, x_end - x);
+        f.n = (int)min((uint32_t)un.tiles - (x - at), x_end - x);
         f.whole = f.n == un.tiles;
-        const long long u0 = at, u1 = u0 + un.tiles - 1, first = ((u0 + 1) * parts - 1) / total;  // the range that holds tile u0
+        const uint32_t first = f.r0 == 0 ? me : range_of(at);
         f.range = (int)first;
-        f.range_last = first * total / parts != u0;
-        f.frags = (int)(((u1 + 1) * parts - 1) / total - first) + 1;
-        if (f.r0 == 0 && rank == 0) info[item] = make_int4(f.range, f.whole ? 0 : f.frags, f.range_last, 0);
+        f.range_last = first * each + min(first, more) != at;
+        if (f.r0 == 0 && rank == 0)
+          info[item] = make_int4(f.range, f.whole ? 0 : (int)(range_of(at + un.tiles - 1) - first) + 1, f.range_last, 0);
         x += f.n;
-        if (x - at == un.tiles) {
+        if (x - at == (uint32_t)un.tiles) {
           at = x;
           ++item;
         }
@@ -274,7 +317,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int n = end > 0 ? ms.f.n : 0;  // tiles with tokens
     const long long urow = (long long)ms.f.rt * kUnitRows + kRows * (int)rank + row;  // the thread's query row
     const bool valid = urow < n_rows;
-    const int j = valid ? (int)(urow / a.heads) : 0, head = valid ? (int)(urow % a.heads) : 0;
+    const int j = valid ? (int)((uint32_t)urow / (uint32_t)a.heads) : 0, head = valid ? (int)((uint32_t)urow % (uint32_t)a.heads) : 0;
     const uint32_t t_base = done_tiles;
     float m_run = kNone, l_run = 0.f;
     bool ok = true;
@@ -282,66 +325,82 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp < kSoftWarps) {
       float q_scale = 0.f;
       if (n > 0) {
-        // ---- the row's quarter of the queries as pieces ----
-        const long long token = (long long)b * a.T + j;
-        const uint4* qc = reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(a.q_c.x) + token * a.q_c.stride +
-                                                         head * a.q_c.head_stride + 128 * quarter);
-        const uint4* qp = reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(a.q_pe.x) + token * a.q_pe.stride +
-                                                         head * a.q_pe.head_stride + 16 * quarter);
-        const uint4 none = make_uint4(0u, 0u, 0u, 0u);
-        uint32_t top_c = 0u, top_p = 0u;
-#pragma unroll 4
-        for (int c = 0; c < 18; ++c) {
-          const uint4 v = !valid ? none : c < 16 ? __ldg(qc + c) : __ldg(qp + c - 16);
-          uint32_t top = 0u;
+        // ---- queries as pieces: eight rows to a warp, a lane 16 dims and an eighth of a position part of every fourth row ----
+#pragma unroll 1
+        for (int r4 = 0; r4 < 8; r4 += 4) {
+          uint4 raw[4][2], pe;
+          const int row0 = 8 * warp + r4;
+          auto at_row = [&](int r, const HeadsDev& h) {  // null past the last row
+            const long long u = (long long)ms.f.rt * kUnitRows + kRows * (int)rank + r;
+            if (u >= n_rows) return (const T*)nullptr;
+            const int jj = (int)((uint32_t)u / (uint32_t)a.heads), hh = (int)((uint32_t)u % (uint32_t)a.heads);
+            return reinterpret_cast<const T*>(h.x) + ((long long)b * a.T + jj) * h.stride + hh * h.head_stride;
+          };
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float2 f = rope::unpack2<T>(word(v, k));
-            top = max(top, max(__float_as_uint(f.x) & 0x7FFFFFFFu, __float_as_uint(f.y) & 0x7FFFFFFFu));
+          for (int r = 0; r < 4; ++r) {
+            const T* src = at_row(row0 + r, a.q_c);
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+              raw[r][i] = src ? __ldg(reinterpret_cast<const uint4*>(src) + 2 * lane + i) : make_uint4(0u, 0u, 0u, 0u);
           }
-          if (c < 16) top_c = max(top_c, top); else top_p = max(top_p, top);
-        }
-        int e = max(top_c, top_p) >= 0x7F800000u ? 1000 : query_exp(top_c, top_p);
-        ms.top[0][quarter][row] = __int_as_float(e);
-        soft_sync();
+          {
+            const T* src = at_row(row0 + (lane >> 3), a.q_pe);
+            pe = src ? __ldg(reinterpret_cast<const uint4*>(src) + (lane & 7)) : make_uint4(0u, 0u, 0u, 0u);
+          }
+          auto largest = [&](const uint4& v) {
+            uint32_t top = 0u;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) e = max(e, __float_as_int(ms.top[0][i][row]));
-        const bool odd = e == 1000;  // a row that is not finite: all its scores are NaN
-        if (odd) e = 0;
-        const float down = block::pow2(-e);
-        q_scale = odd ? CUDART_NAN_F : a.sm_scale * 1.44269504088896340736f * block::pow2(e);
-#pragma unroll 2
-        for (int c = 0; c < 8; ++c) {  // 16 dims
-          uint32_t piece[NP][4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const uint4 v = valid && !odd ? __ldg(qc + 2 * c + (k >> 1)) : none;
-            const float2 f0 = rope::unpack2<T>(word(v, 2 * (k & 1))), f1 = rope::unpack2<T>(word(v, 2 * (k & 1) + 1));
-            float y[4] = {f0.x * down, f0.y * down, f1.x * down, f1.y * down};
-#pragma unroll
-            for (int p = 0; p < NP; ++p) {
-              piece[p][k] = block::code4(y[0], y[1], y[2], y[3]);
-              const float2 lo = rope::unpack2<__half>(block::widen2(piece[p][k])), hi = rope::unpack2<__half>(block::widen2_hi(piece[p][k]));
-              y[0] -= lo.x, y[1] -= lo.y, y[2] -= hi.x, y[3] -= hi.y;
+            for (int k = 0; k < 4; ++k) {
+              const float2 f = rope::unpack2<T>(word(v, k));
+              top = max(top, max(__float_as_uint(f.x) & 0x7FFFFFFFu, __float_as_uint(f.y) & 0x7FFFFFFFu));
             }
+            return top;
+          };
+          uint32_t top_p = largest(pe);  // of row lane / 8
+#pragma unroll
+          for (int o = 1; o < 8; o <<= 1) top_p = max(top_p, __shfl_xor_sync(0xffffffffu, top_p, o));
+          float pe_down = 0.f;
+#pragma unroll 1
+          for (int r = 0; r < 4; ++r) {
+            const uint32_t top_c = __reduce_max_sync(0xffffffffu, max(largest(raw[0][0]), largest(raw[0][1])));
+            const uint32_t top_r = __shfl_sync(0xffffffffu, top_p, 8 * r);
+            const bool odd = max(top_c, top_r) >= 0x7F800000u;  // a row that is not finite: all its scores are NaN
+            const int e = odd ? 0 : query_exp(top_c, top_r);
+            const float down = block::pow2(-e);
+            if ((lane >> 3) == r) pe_down = odd ? 0.f : down;
+            if (lane == 0) ms.q_scale[row0 + r] = odd ? CUDART_NAN_F : a.sm_scale * 1.44269504088896340736f * block::pow2(e);
+            uint32_t piece[NP][4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const uint4& v = raw[0][k >> 1];
+              const float2 f0 = rope::unpack2<T>(word(v, 2 * (k & 1))), f1 = rope::unpack2<T>(word(v, 2 * (k & 1) + 1));
+              float y[4] = {f0.x * down, f0.y * down, f1.x * down, f1.y * down};
+#pragma unroll
+              for (int p = 0; p < NP; ++p) {
+                piece[p][k] = odd ? 0u : block::code4(y[0], y[1], y[2], y[3]);
+                if (p + 1 == NP) break;
+                const float2 lo = rope::unpack2<__half>(block::widen2(piece[p][k])), hi = rope::unpack2<__half>(block::widen2_hi(piece[p][k]));
+                y[0] -= lo.x, y[1] -= lo.y, y[2] -= hi.x, y[3] -= hi.y;
+              }
+            }
+#pragma unroll
+            for (int p = 0; p < NP; ++p)
+              sts128(q_ops + p * S::kPieceQ + 8192 * (lane >> 3) + sw128(row0 + r, lane & 7), piece[p][0], piece[p][1], piece[p][2], piece[p][3]);
+#pragma unroll
+            for (int i = 0; i < 3; ++i) raw[i][0] = raw[i + 1][0], raw[i][1] = raw[i + 1][1];  // (one row's code, not four)
           }
-#pragma unroll
-          for (int p = 0; p < NP; ++p)
-            sts128(q_ops + p * S::kPieceQ + 8192 * quarter + sw128(row, c), piece[p][0], piece[p][1], piece[p][2], piece[p][3]);
-        }
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const uint4 v = valid && !odd ? __ldg(qp + c) : none;
           uint32_t w[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const float2 f = rope::unpack2<T>(word(v, k));
-            w[k] = rope::pack2<T>(f.x * down, f.y * down);
+            const float2 f = rope::unpack2<T>(word(pe, k));
+            w[k] = pe_down == 0.f ? 0u : rope::pack2<T>(f.x * pe_down, f.y * pe_down);
           }
-          sts128(q_ops + NP * S::kPieceQ + sw128(row, 2 * quarter + c), w[0], w[1], w[2], w[3]);
+          sts128(q_ops + NP * S::kPieceQ + sw128(row0 + (lane >> 3), lane & 7), w[0], w[1], w[2], w[3]);
         }
         fence_async_smem();
         warp_arrive_pair(peer_addr(smem_addr(&ms.q_full), 0));
+        soft_sync();  // the rows' scales are there
+        q_scale = ms.q_scale[row];
       }
       // ================= softmax =================
       // the row sees tokens before `all`, of the drafts behind them the ones up to its own or those of its mask
@@ -365,14 +424,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tmem_wait_ld();
         settle<64>(s);
-        const float4* const ks = reinterpret_cast<const float4*>(&ms.ks[buf][64 * quarter]);
-        const float4* const ev = reinterpret_cast<const float4*>(&ms.ev[buf][64 * quarter]);
-        float top = -CUDART_INF_F;
+        {
+          const ulonglong2* const ks = reinterpret_cast<const ulonglong2*>(&ms.ks[buf][64 * quarter]);
+          const ulonglong2* const ev = reinterpret_cast<const ulonglong2*>(&ms.ev[buf][64 * quarter]);
+          const uint64_t q2 = pair(q_scale, q_scale);
 #pragma unroll
-        for (int c = 0; c < 16; ++c) {  // score + E
-          const float4 f = ks[c], e = ev[c];
-          fma2(s[4 * c], s[4 * c + 1], pair(f.x * q_scale, f.y * q_scale), pair(e.x, e.y));
-          fma2(s[4 * c + 2], s[4 * c + 3], pair(f.z * q_scale, f.w * q_scale), pair(e.z, e.w));
+          for (int c = 0; c < 16; ++c) {  // score + E
+            const ulonglong2 f = ks[c], e = ev[c];
+            unpair(fma2(pair(s[4 * c], s[4 * c + 1]), mul2(f.x, q2), e.x), s[4 * c], s[4 * c + 1]);
+            unpair(fma2(pair(s[4 * c + 2], s[4 * c + 3]), mul2(f.y, q2), e.y), s[4 * c + 2], s[4 * c + 3]);
+          }
         }
         if (t0 + 63 > sees) {
 #pragma unroll
@@ -382,8 +443,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!(see && valid)) s[c] = -CUDART_INF_F;
           }
         }
+        float top = max3(s[0], s[1], s[2]), top1 = max3(s[3], s[4], s[5]);
 #pragma unroll
-        for (int c = 0; c < 64; c += 2) top = max3(top, s[c], s[c + 1]);
+        for (int c = 6; c < 62; c += 4) top = max3(top, s[c], s[c + 1]), top1 = max3(top1, s[c + 2], s[c + 3]);
+        top = max3(top, top1, fmaxf(s[62], s[63]));
         ms.top[buf][quarter][row] = top;
         soft_sync();
 #pragma unroll
@@ -399,30 +462,31 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float from = m_run == kNone ? 0.f : m_run;
         uint32_t piece[NP][16];
         {
-          const float4* const dn = reinterpret_cast<const float4*>(&ms.dn[buf][64 * quarter]);
+          const ulonglong2* const dn = reinterpret_cast<const ulonglong2*>(&ms.dn[buf][64 * quarter]);
           uint64_t sum[2] = {0ull, 0ull};
+          const uint64_t back = pair(-from, -from);
 #pragma unroll
           for (int c = 0; c < 16; ++c) {
-            const float4 d = dn[c];
-            const float w0 = ex2(s[4 * c] - from), w1 = ex2(s[4 * c + 1] - from), w2 = ex2(s[4 * c + 2] - from), w3 = ex2(s[4 * c + 3] - from);
-            const uint64_t d01 = pair(d.x, d.y), d23 = pair(d.z, d.w), w01 = pair(w0, w1), w23 = pair(w2, w3);
-            asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(sum[0]) : "l"(w01), "l"(d01));
-            asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(sum[1]) : "l"(w23), "l"(d23));
-            uint32_t h[2] = {rope::pack2<__half>(w0, w1), rope::pack2<__half>(w2, w3)}, code[2];
+            const ulonglong2 d = dn[c];
+            float w[4];
+            unpair(plus2(pair(s[4 * c], s[4 * c + 1]), back), w[0], w[1]);
+            unpair(plus2(pair(s[4 * c + 2], s[4 * c + 3]), back), w[2], w[3]);
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              code[i] = e5m2_of(h[i]);
-              h[i] = hsub2(h[i], e5m2_wide(code[i]));
-            }
-            piece[0][c] = __byte_perm(code[0], code[1], 0x5410);
+            for (int i = 0; i < 4; ++i) w[i] = ex2(w[i]);
+            sum[0] = fma2(pair(w[0], w[1]), d.x, sum[0]);
+            sum[1] = fma2(pair(w[2], w[3]), d.y, sum[1]);
+            uint32_t h[2] = {rope::pack2<__half>(w[0], w[1]), rope::pack2<__half>(w[2], w[3])}, code[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) code[i] = first_piece(h[i]);
+            piece[0][c] = __byte_perm(code[0], code[1], 0x7531);
 #pragma unroll
             for (int p = 1; p < NP; ++p) {
 #pragma unroll
               for (int i = 0; i < 2; ++i) {
-                code[i] = e4m3_of(h[i]);
-                if (p + 1 < NP) h[i] = hsub2(h[i], block::widen2(code[i]));
+                code[i] = next_piece(h[i]);
+                if (p + 1 < NP) h[i] = behind(h[i], code[i]);
               }
-              piece[p][c] = __byte_perm(code[0], code[1], 0x5410);
+              piece[p][c] = __byte_perm(code[0], code[1], 0x7531);
             }
           }
           float y[4];
@@ -470,59 +534,77 @@ __global__ void __launch_bounds__(kThreads, 1)
         constexpr uint32_t type = std::is_same<T, __half>::value ? 0u : 1u;
         constexpr uint32_t id_p = idesc_f16(kUnitRows, kTok) | type << 7 | type << 10;
         bool issued = false;
-        uint32_t k_at = at_slot;  // the next slot in the order of use
-        auto wait = [&](uint64_t& bar, uint32_t parity) { return ok = warp_wait(bar, parity, abort_flag); };
+        // units and slots in the order of use: K(0) | K(1) V(0) | K(2) V(1) | ...
+        uint32_t u = 5u * t_base, sl = 9u * t_base;
+        auto unit_full = [&](uint32_t v) -> uint64_t& { return ms.full[v % kUnits]; };
+        uint32_t look = warp_look(unit_full(u), u / kUnits);
+        auto take = [&]() {  // unit u is full; the next one is looked at
+          ok = warp_wait_after(look, unit_full(u), u / kUnits, abort_flag);
+          if (ok) look = warp_look(unit_full(u + 1), (u + 1) / kUnits);
+          return ok;
+        };
+        uint32_t p_look = 0;
+        auto give = [&]() {
+          pair_commit(smem_addr(&ms.empty[u % kUnits]), 3);
+          ++u;
+          issued = true;
+        };
+        const uint32_t q_lo = desc_lo(q_ops), w_lo = desc_lo(p_ops), ring_lo = desc_lo(ring);
+        auto slot = [&]() { return ring_lo + sl++ % kSlots * (kSlotBytes / 16); };
         auto s_mmas = [&](int t) {  // S(t)
           const uint32_t d = tmem + kColS + 128 * ((t_base + t) & 1);
 #pragma unroll
-          for (int c = 0; c < 5; ++c) {
-            const uint32_t sl = k_at % kSlots, b_at = ring + sl * kSlotBytes;
-            if (!wait(ms.full[sl], k_at / kSlots)) return;
-            if (c < 4) {
+          for (int c2 = 0; c2 < 2; ++c2) {
+            if (!take()) return;
+#pragma unroll
+            for (int c = 2 * c2; c < 2 * c2 + 2; ++c) {
+              const uint32_t b_at = slot();
 #pragma unroll
               for (int p = 0; p < NP; ++p)
 #pragma unroll
                 for (int ks = 0; ks < 4; ++ks)
-                  pair_mma_f8(d, sdesc(q_ops + p * S::kPieceQ + 8192 * c + 32 * ks), sdesc(b_at + 32 * ks), id_s, c > 0 || p > 0 || ks > 0);
-            } else {
-#pragma unroll
-              for (int ks = 0; ks < 4; ++ks)
-                pair_mma_ss(d, sdesc(q_ops + NP * S::kPieceQ + 32 * ks), sdesc(b_at + 32 * ks), id_p, 1);
+                  pair_mma_f8(d, q_lo + (p * S::kPieceQ + 8192 * c + 32 * ks) / 16, b_at + 2 * ks, id_s, c > 0 || p > 0 || ks > 0);
             }
-            issued = true;
-            pair_commit(smem_addr(&ms.empty[sl]), 3);
-            ++k_at;
+            give();
           }
+          if (!take()) return;
+          if (t > 0) p_look = warp_look(ms.p_full, t_base + t - 1);
+          const uint32_t b_at = slot();
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks)
+            pair_mma_16(d, q_lo + (NP * S::kPieceQ + 32 * ks) / 16, b_at + 2 * ks, id_p);
+          give();
           pair_commit(smem_addr(&ms.s_full[(t_base + t) & 1]), 3);
         };
-        if (wait(ms.q_full, done_frags)) {
+        if (ok = warp_wait(ms.q_full, done_frags, abort_flag); ok) {
           fence_after_sync();
           s_mmas(0);
         }
         for (int t = 0; t < n && ok; ++t) {
+          p_look = 0;
           if (t + 1 < n) s_mmas(t + 1);
-          if (!ok || !wait(ms.p_full, t_base + t)) break;
+          if (!ok || !(ok = warp_wait_after(p_look, ms.p_full, t_base + t, abort_flag))) break;
           fence_after_sync();
 #pragma unroll
-          for (int g = 0; g < 4; ++g) {  // 64 tokens
-            const uint32_t sl = k_at % kSlots, b_at = ring + sl * kSlotBytes;
-            if (!wait(ms.full[sl], k_at / kSlots)) break;
-            if ((r0 + t) * kTok + 64 * (g + 1) > end) {
-              if (!wait(ms.tail_done[sl], tails >> sl & 1)) break;
-              tails ^= 1u << sl;
+          for (int g2 = 0; g2 < 2; ++g2) {  // 128 tokens
+            if (!take()) break;
+            if ((r0 + t) * kTok + 128 * (g2 + 1) > end) {
+              if (!(ok = warp_wait(ms.tail_done[u % kUnits], tails >> (u % kUnits) & 1, abort_flag))) break;
+              tails ^= 1u << (u % kUnits);
             }
 #pragma unroll
-            for (int ks = 0; ks < 2; ++ks) {
-              const uint32_t w_at = p_ops + 8192 * (g >> 1) + 64 * (g & 1) + 32 * ks;
+            for (int g = 0; g < 2; ++g) {
+              const uint32_t b_at = slot(), w_at = w_lo + (8192 * g2 + 64 * g) / 16;
 #pragma unroll
-              for (int h = 0; h < 2; ++h)
+              for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
-                for (int p = 0; p < NP; ++p)
-                  pair_mma_f8(tmem + 128 * h, sdesc(w_at + p * S::kPieceP), sdesc(b_at + 8192 * h + 4096 * ks), p == 0 ? id_o5 : id_o4,
-                              t > 0 || g > 0 || ks > 0 || p > 0);
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                  for (int p = 0; p < NP; ++p)
+                    pair_mma_f8(tmem + 128 * h, w_at + (p * S::kPieceP + 32 * ks) / 16, b_at + (8192 * h + 4096 * ks) / 16,
+                                p == 0 ? id_o5 : id_o4, g2 > 0 || g > 0 || ks > 0 || p > 0 ? 1u : (uint32_t)t);
             }
-            pair_commit(smem_addr(&ms.empty[sl]), 3);
-            ++k_at;
+            give();
           }
           if (!ok) break;
           pair_commit(smem_addr(&ms.o_done), 3);
@@ -537,7 +619,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ================= copies: this CTA's share =================
       const int32_t* table = a.block_table + (size_t)b * a.max_pages;
       const int per_half = 128 / box, per_slot = 64 / box;  // boxes
-      uint32_t c_at = at_slot;
       // boxes 0 .. 256 / box - 1 of a tile, a lane each: page (or -1) and row in it
       auto place = [&](int t, int& page, int& in_page) {
         const int p = (r0 + t) * kTok + box * lane;
@@ -550,44 +631,58 @@ __global__ void __launch_bounds__(kThreads, 1)
           page = 0;
         }
       };
-      auto free_slot = [&]() {
-        const uint32_t sl = c_at % kSlots;
-        return c_at < kSlots || (ok = warp_wait(ms.empty[sl], c_at / kSlots - 1, abort_flag));
+      // room for a unit of `count` slots: units are given back in order
+      auto room = [&](uint32_t count) {
+        while (asked + count - freed > (uint32_t)kSlots) {
+          if (!(ok = warp_wait(ms.empty[freed_units % kUnits], freed_units / kUnits, abort_flag))) return false;
+          freed += 1u + (twos >> (freed_units % 32) & 1u);
+          ++freed_units;
+        }
+        twos = (twos & ~(1u << (asked_units % 32))) | (count - 1u) << (asked_units % 32);
+        return true;
       };
       auto boxes = [&](int p, int count) { return min(max(0, (end - p + box - 1) / box), count); };  // from token p on
       auto keys = [&](int t, int page, int in_page) {
         const int p = (r0 + t) * kTok;
         const int both = boxes(p, per_half) + boxes(p + 128, per_half), mine = boxes(p + 128 * (int)rank, per_half);
-        const int pg = __shfl_sync(0xffffffffu, page, per_half * (int)rank + lane & 31), ip = __shfl_sync(0xffffffffu, in_page, per_half * (int)rank + lane & 31);
-        for (int c = 0; c < 5; ++c, ++c_at) {
-          if (!free_slot()) return;
-          const uint32_t sl = c_at % kSlots;
-          if (rank == 0) elect_expect(smem_addr(&ms.full[sl]), (uint32_t)(both * box * 128));
+        // lane: box lane % per_half of the unit's slot lane / per_half
+        const int i = lane % per_half, c = lane / per_half;
+        const int pg = __shfl_sync(0xffffffffu, page, per_half * (int)rank + i), ip = __shfl_sync(0xffffffffu, in_page, per_half * (int)rank + i);
+        for (int k = 0; k < 3; ++k) {
+          const int slots = k < 2 ? 2 : 1;
+          if (!room(slots)) return;
+          const uint32_t u = asked_units % kUnits;
+          if (rank == 0) elect_expect(smem_addr(&ms.full[u]), (uint32_t)(slots * both * box * 128));
           __syncwarp();
-          if (lane < mine) load_pair(ring + sl * kSlotBytes + lane * box * 128, map, ip, c, pg, peer_addr(smem_addr(&ms.full[sl]), 0));
+          if (c < slots && i < mine)
+            load_pair(ring + (asked + c) % kSlots * kSlotBytes + i * box * 128, map, ip, 2 * k + c, pg, peer_addr(smem_addr(&ms.full[u]), 0));
+          asked += slots;
+          ++asked_units;
         }
       };
       auto values = [&](int t, int page, int in_page) {
-        for (int g = 0; g < 4; ++g, ++c_at) {
-          if (!free_slot()) return;
-          const uint32_t sl = c_at % kSlots;
-          const int p = (r0 + t) * kTok + 64 * g, count = boxes(p, per_slot);
-          const bool tail = p + 64 > end;
-          // lane: box lane % per_slot of dims 128 (2 rank + lane / per_slot) ..
-          const int i = lane % per_slot, c = lane / per_slot;
-          const int pg = __shfl_sync(0xffffffffu, page, per_slot * g + i & 31), ip = __shfl_sync(0xffffffffu, in_page, per_slot * g + i & 31);
-          const uint32_t dst = ring + sl * kSlotBytes + 8192 * c + i * box * 128;
+        for (int g = 0; g < 2; ++g) {  // 128 tokens, two slots of 64
+          if (!room(2)) return;
+          const uint32_t u = asked_units % kUnits;
+          const int p = (r0 + t) * kTok + 128 * g, count = boxes(p, 2 * per_slot);
+          const bool tail = p + 128 > end;
+          // lane: box lane % (2 per_slot) of dims 128 (2 rank + lane / (2 per_slot)) ..
+          const int i = lane % (2 * per_slot), c = lane / (2 * per_slot);
+          const int pg = __shfl_sync(0xffffffffu, page, 2 * per_slot * g + i), ip = __shfl_sync(0xffffffffu, in_page, 2 * per_slot * g + i);
+          const uint32_t dst = ring + (asked + i / per_slot) % kSlots * kSlotBytes + 8192 * c + i % per_slot * box * 128;
           const bool mine = c < 2 && i < count;
           if (!tail) {
-            if (rank == 0) elect_expect(smem_addr(&ms.full[sl]), 2 * kSlotBytes);
+            if (rank == 0) elect_expect(smem_addr(&ms.full[u]), 4 * kSlotBytes);
             __syncwarp();
-            if (mine) load_pair(dst, map, ip, 2 * (int)rank + c, pg, peer_addr(smem_addr(&ms.full[sl]), 0));
+            if (mine) load_pair(dst, map, ip, 2 * (int)rank + c, pg, peer_addr(smem_addr(&ms.full[u]), 0));
           } else {  // the tail's warp of this CTA first
-            elect_expect(smem_addr(&ms.here[sl]), (uint32_t)(2 * count * box * 128));
+            elect_expect(smem_addr(&ms.here[u]), (uint32_t)(2 * count * box * 128));
             __syncwarp();
-            if (mine) load_here(dst, map, ip, 2 * (int)rank + c, pg, smem_addr(&ms.here[sl]));
-            if (rank == 0) warp_arrive(ms.full[sl]);
+            if (mine) load_here(dst, map, ip, 2 * (int)rank + c, pg, smem_addr(&ms.here[u]));
+            if (rank == 0) warp_arrive(ms.full[u]);
           }
+          asked += 2;
+          ++asked_units;
         }
       };
       int page[2], in_page[2];
@@ -639,25 +734,26 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ================= the tail: zeros behind the last token that is seen =================
       if (n > 0) {
         const int t = n - 1, p0 = (r0 + t) * kTok;
-        // the tile's value slots are the fragment's last four
-        for (int g = 0; g < 4; ++g) {
-          const int p = p0 + 64 * g;
-          if (p + 64 <= end) continue;
-          const uint32_t seq = at_slot + 9u * n - 4u + g, sl = seq % kSlots;
-          if (!(ok = warp_wait(ms.here[sl], tails >> sl & 1, abort_flag))) break;
-          tails ^= 1u << sl;
+        // the tile's values are the fragment's last two units, its last four slots
+        for (int g = 0; g < 2; ++g) {
+          const int p = p0 + 128 * g;
+          if (p + 128 <= end) continue;
+          const uint32_t u = (5u * (t_base + n) - 2u + g) % kUnits;
+          if (!(ok = warp_wait(ms.here[u], tails >> u & 1, abort_flag))) break;
+          tails ^= 1u << u;
           const int first = max(0, end - p);
-          for (int i = first * 16 + lane; i < 64 * 16; i += 32)  // row i / 16: eight chunks of either 128 dims
-            sts128(ring + sl * kSlotBytes + 8192 * (i >> 3 & 1) + (i >> 4) * 128 + (i & 7) * 16, 0u, 0u, 0u, 0u);
+          for (int i = first * 16 + lane; i < 128 * 16; i += 32) {  // row i / 16: eight chunks of either 128 dims
+            const uint32_t sl = (9u * (t_base + n) - 4u + 2 * g + (i >> 10)) % kSlots;
+            sts128(ring + sl * kSlotBytes + 8192 * (i >> 3 & 1) + (i >> 4 & 63) * 128 + (i & 7) * 16, 0u, 0u, 0u, 0u);
+          }
           fence_async_smem();
-          warp_arrive_pair(peer_addr(smem_addr(&ms.tail_done[sl]), 0));
+          warp_arrive_pair(peer_addr(smem_addr(&ms.tail_done[u]), 0));
         }
       }
     }
     if (!ok && lane == 0 && a.status) atomicOr(a.status, RQ_STATUS_TIMEOUT);
     done_tiles += n;
     done_frags += n > 0;
-    at_slot += 9u * n;
     fence_before_sync();
     __syncthreads();
     fence_after_sync();
@@ -673,7 +769,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // a row that sees nothing is zero; one whose scores are all minus infinity is NaN
       const float empty = whole && sees >= 0 ? CUDART_NAN_F : 0.f, inv = whole ? 1.f / l : 1.f;
       const int srow = kRows * (int)rank + row, dim0 = 256 * tok_half + 128 * col_half;
-      float* const slot = a.ws + (2ll * me + (me == ms.f.range ? ms.f.range_last : 0)) * kSlotFloats;
+      float* const slot = a.ws + (2ll * me + ((int)me == ms.f.range ? ms.f.range_last : 0)) * kSlotFloats;
       T* const out = reinterpret_cast<T*>(a.out) + (((size_t)b * a.T + j) * a.heads + head) * kLatentDim + dim0;
 #pragma unroll 2
       for (int c = 0; c < 8; ++c) {

@@ -52,6 +52,19 @@ __device__ __forceinline__ bool warp_wait(const uint64_t& bar, uint32_t parity, 
   if (!ok) *abort_flag = 1;
   return __all_sync(0xffffffffu, ok);
 }
+// A look at a barrier whose result is wanted later: a wait that finds it ready takes some 200 cycles, which a look ahead
+// spends beside other work.  warp_wait_after: the wait, unless the look found it ready.
+__device__ __forceinline__ uint32_t warp_look(const uint64_t& bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile("{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+               : "=r"(done)
+               : "r"(smem_addr(&bar)), "r"(parity & 1)
+               : "memory");
+  return done;
+}
+__device__ __forceinline__ bool warp_wait_after(uint32_t look, const uint64_t& bar, uint32_t parity, volatile int* abort_flag) {
+  return __all_sync(0xffffffffu, look) || warp_wait(bar, parity, abort_flag);
+}
 // A warp's arrival, by one lane (a predicate, no branch) behind all lanes' accesses.
 __device__ __forceinline__ void warp_arrive(uint64_t& bar) {
   __syncwarp();
