@@ -140,6 +140,8 @@ __device__ __forceinline__ void load_here(uint32_t dst, const CUtensorMap& map, 
       : "memory");
 }
 __device__ __forceinline__ void soft_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+// The four warps that share 32 rows.
+__device__ __forceinline__ void rows_sync(int half) { asm volatile("bar.sync %0, 128;" ::"r"(2 + half) : "memory"); }
 
 // Pieces of two weights (fp16, 0 to 2^12) in few operations of the integer and fp16 pipes (a conversion to 8 bits takes 14
 // cycles of a scheduler, these two).  e5m2 is an fp16 number's upper byte: the first piece is the number rounded to that, its
@@ -370,18 +372,22 @@ __global__ void __launch_bounds__(kThreads, 1)
             if ((lane >> 3) == r) pe_down = odd ? 0.f : down;
             if (lane == 0) ms.q_scale[row0 + r] = odd ? CUDART_NAN_F : a.sm_scale * 1.44269504088896340736f * block::pow2(e);
             uint32_t piece[NP][4];
+            const float down8 = odd ? 0.f : down * 0.00390625f;  // 2^-8: as next_piece wants it
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-              const uint4& v = raw[0][k >> 1];
-              const float2 f0 = rope::unpack2<T>(word(v, 2 * (k & 1))), f1 = rope::unpack2<T>(word(v, 2 * (k & 1) + 1));
-              float y[4] = {f0.x * down, f0.y * down, f1.x * down, f1.y * down};
+              uint32_t code[2][NP];
 #pragma unroll
-              for (int p = 0; p < NP; ++p) {
-                piece[p][k] = odd ? 0u : block::code4(y[0], y[1], y[2], y[3]);
-                if (p + 1 == NP) break;
-                const float2 lo = rope::unpack2<__half>(block::widen2(piece[p][k])), hi = rope::unpack2<__half>(block::widen2_hi(piece[p][k]));
-                y[0] -= lo.x, y[1] -= lo.y, y[2] -= hi.x, y[3] -= hi.y;
+              for (int i = 0; i < 2; ++i) {
+                const float2 f = rope::unpack2<T>(word(raw[0][k >> 1], 2 * (k & 1) + i));
+                uint32_t h = odd ? 0u : rope::pack2<__half>(f.x * down8, f.y * down8);  // exact, but for what is below 2^-24
+#pragma unroll
+                for (int p = 0; p < NP; ++p) {
+                  code[i][p] = next_piece(h);
+                  if (p + 1 < NP) h = behind(h, code[i][p]);
+                }
               }
+#pragma unroll
+              for (int p = 0; p < NP; ++p) piece[p][k] = __byte_perm(code[0][p], code[1][p], 0x7531);
             }
 #pragma unroll
             for (int p = 0; p < NP; ++p)
@@ -403,52 +409,63 @@ __global__ void __launch_bounds__(kThreads, 1)
         q_scale = ms.q_scale[row];
       }
       // ================= softmax =================
-      // the row sees tokens before `all`, of the drafts behind them the ones up to its own or those of its mask
-      const int all = valid ? len - a.T : -1;
-      const uint64_t mask = !valid ? 0ull : a.tree_mask ? __ldg(a.tree_mask + (long long)b * a.T + j) : 0ull;
-      const int qpos = valid ? len - a.T + j : -1;
-      const int sees = a.tree_mask ? all - 1 : qpos;  // the last token up to which all is seen
+      // Scores 16 columns at a time, twice: loops over them and not 64 columns in a row, so that the roles' code fits the
+      // instruction cache (unrolled, the warps spent more cycles without instructions than with them).
+      // The row sees tokens before `all`, of the drafts behind them the ones up to its own or those of its mask.  A row past the
+      // last one sees all: what becomes of it is not written.
+      const int all = valid ? (a.tree_mask ? len - a.T : len - a.T + j + 1) : INT32_MAX - 1024;
+      uint64_t mask = valid && a.tree_mask ? __ldg(a.tree_mask + (long long)b * a.T + j) : 0ull;
+      if (a.T < 64) mask &= (1ull << a.T) - 1ull;
+      const bool idle = !__any_sync(0xffffffffu, valid);  // (all four warps of the rows alike)
+      const uint32_t s_cols = tmem + lane_off + kColS + 64 * col_half;
       for (int t = 0; t < n; ++t) {
         const uint32_t k = t_base + t, buf = k & 1;
+        if (idle) {  // takes part in the counts; O(t - 1) says that the last count is over
+          if (t > 0 && !(ok = warp_wait(ms.o_done, k - 1, abort_flag))) break;
+          warp_arrive(ms.sc_empty[buf]);
+          warp_arrive_pair(peer_addr(smem_addr(&ms.p_full), 0));
+          continue;
+        }
         const int t0 = (r0 + t) * kTok + 64 * quarter;
-        if (!(ok = warp_wait(ms.sc_full[buf], k >> 1, abort_flag))) break;
         if (!(ok = warp_wait(ms.s_full[buf], k >> 1, abort_flag))) break;
+        if (!(ok = warp_wait(ms.sc_full[buf], k >> 1, abort_flag))) break;
         fence_after_sync();
-        float s[64];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          float v[16];
-          tmem_ld16(tmem + lane_off + kColS + 128 * buf + 64 * col_half + 16 * c, v);
-#pragma unroll
-          for (int i = 0; i < 16; ++i) s[16 * c + i] = v[i];
-        }
-        tmem_wait_ld();
-        settle<64>(s);
+        float top = -CUDART_INF_F;
         {
-          const ulonglong2* const ks = reinterpret_cast<const ulonglong2*>(&ms.ks[buf][64 * quarter]);
-          const ulonglong2* const ev = reinterpret_cast<const ulonglong2*>(&ms.ev[buf][64 * quarter]);
           const uint64_t q2 = pair(q_scale, q_scale);
+#pragma unroll 1
+          for (int c = 0; c < 64; c += 16) {  // score + E
+            float v[16];
+            tmem_ld16(s_cols + 128 * buf + c, v);
+            const ulonglong2* const ks = reinterpret_cast<const ulonglong2*>(&ms.ks[buf][64 * quarter + c]);
+            const ulonglong2* const ev = reinterpret_cast<const ulonglong2*>(&ms.ev[buf][64 * quarter + c]);
+            ulonglong2 f[4], e[4];
 #pragma unroll
-          for (int c = 0; c < 16; ++c) {  // score + E
-            const ulonglong2 f = ks[c], e = ev[c];
-            unpair(fma2(pair(s[4 * c], s[4 * c + 1]), mul2(f.x, q2), e.x), s[4 * c], s[4 * c + 1]);
-            unpair(fma2(pair(s[4 * c + 2], s[4 * c + 3]), mul2(f.y, q2), e.y), s[4 * c + 2], s[4 * c + 3]);
+            for (int i = 0; i < 4; ++i) f[i] = ks[i], e[i] = ev[i];
+            tmem_wait_ld();
+            settle<16>(v);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              unpair(fma2(pair(v[4 * i], v[4 * i + 1]), mul2(f[i].x, q2), e[i].x), v[4 * i], v[4 * i + 1]);
+              unpair(fma2(pair(v[4 * i + 2], v[4 * i + 3]), mul2(f[i].y, q2), e[i].y), v[4 * i + 2], v[4 * i + 3]);
+            }
+            const int first = t0 + c - all;  // of the columns' tokens, counted from the first that the mask is for
+            if (first > -16) {
+              const uint32_t seen = first >= 64 ? 0u : first >= 0 ? (uint32_t)(mask >> first) : (1u << -first) - 1u | (uint32_t)mask << -first;
+#pragma unroll
+              for (int i = 0; i < 16; ++i)
+                if (!(seen >> i & 1)) v[i] = -CUDART_INF_F;
+            }
+            float top1 = max3(v[0], v[1], v[2]);
+#pragma unroll
+            for (int i = 3; i < 15; i += 4) top = max3(top, v[i], v[i + 1]), top1 = max3(top1, v[i + 2], v[i + 3]);
+            top = max3(top, top1, v[15]);
+            tmem_st16(s_cols + 128 * buf + c, v);
           }
         }
-        if (t0 + 63 > sees) {
-#pragma unroll
-          for (int c = 0; c < 64; ++c) {
-            const int p = t0 + c, draft = p - all;
-            const bool see = a.tree_mask ? draft < 0 || (p < len && draft < 64 && (mask >> draft & 1)) : p <= qpos;
-            if (!(see && valid)) s[c] = -CUDART_INF_F;
-          }
-        }
-        float top = max3(s[0], s[1], s[2]), top1 = max3(s[3], s[4], s[5]);
-#pragma unroll
-        for (int c = 6; c < 62; c += 4) top = max3(top, s[c], s[c + 1]), top1 = max3(top1, s[c + 2], s[c + 3]);
-        top = max3(top, top1, fmaxf(s[62], s[63]));
         ms.top[buf][quarter][row] = top;
-        soft_sync();
+        tmem_wait_st();
+        rows_sync(quad & 1);
 #pragma unroll
         for (int i = 0; i < 4; ++i) top = fmaxf(top, ms.top[buf][i][row]);
         const float above = top - (m_run == kNone ? -CUDART_INF_F : m_run);  // (NaN where nothing is seen: no move)
@@ -460,41 +477,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           l_run *= alpha;
         }
         const float from = m_run == kNone ? 0.f : m_run;
-        uint32_t piece[NP][16];
-        {
-          const ulonglong2* const dn = reinterpret_cast<const ulonglong2*>(&ms.dn[buf][64 * quarter]);
-          uint64_t sum[2] = {0ull, 0ull};
-          const uint64_t back = pair(-from, -from);
-#pragma unroll
-          for (int c = 0; c < 16; ++c) {
-            const ulonglong2 d = dn[c];
-            float w[4];
-            unpair(plus2(pair(s[4 * c], s[4 * c + 1]), back), w[0], w[1]);
-            unpair(plus2(pair(s[4 * c + 2], s[4 * c + 3]), back), w[2], w[3]);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) w[i] = ex2(w[i]);
-            sum[0] = fma2(pair(w[0], w[1]), d.x, sum[0]);
-            sum[1] = fma2(pair(w[2], w[3]), d.y, sum[1]);
-            uint32_t h[2] = {rope::pack2<__half>(w[0], w[1]), rope::pack2<__half>(w[2], w[3])}, code[2];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) code[i] = first_piece(h[i]);
-            piece[0][c] = __byte_perm(code[0], code[1], 0x7531);
-#pragma unroll
-            for (int p = 1; p < NP; ++p) {
-#pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                code[i] = next_piece(h[i]);
-                if (p + 1 < NP) h[i] = behind(h[i], code[i]);
-              }
-              piece[p][c] = __byte_perm(code[0], code[1], 0x7531);
-            }
-          }
-          float y[4];
-          unpair(sum[0], y[0], y[1]);
-          unpair(sum[1], y[2], y[3]);
-          l_run += (y[0] + y[1]) + (y[2] + y[3]);
-        }
-        warp_arrive(ms.sc_empty[buf]);
         // O(t - 1) is done: its weights' place is free, and O may be scaled
         if (t > 0) {
           if (!(ok = warp_wait(ms.o_done, k - 1, abort_flag))) break;
@@ -514,13 +496,54 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_wait_st();
           }
         }
+        {
+          uint64_t sum[2] = {0ull, 0ull};
+          const uint64_t back = pair(-from, -from);
+#pragma unroll 1
+          for (int c = 0; c < 64; c += 16) {
+            float v[16];
+            tmem_ld16(s_cols + 128 * buf + c, v);
+            const ulonglong2* const dn = reinterpret_cast<const ulonglong2*>(&ms.dn[buf][64 * quarter + c]);
+            ulonglong2 d[4];
 #pragma unroll
-        for (int p = 0; p < NP; ++p) {
+            for (int i = 0; i < 4; ++i) d[i] = dn[i];
+            tmem_wait_ld();
+            settle<16>(v);
+            uint32_t piece[NP][4];
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
-            sts128(p_ops + p * S::kPieceP + 8192 * tok_half + sw128(row, 4 * col_half + c), piece[p][4 * c], piece[p][4 * c + 1],
-                   piece[p][4 * c + 2], piece[p][4 * c + 3]);
+            for (int i = 0; i < 4; ++i) {
+              float w[4];
+              unpair(plus2(pair(v[4 * i], v[4 * i + 1]), back), w[0], w[1]);
+              unpair(plus2(pair(v[4 * i + 2], v[4 * i + 3]), back), w[2], w[3]);
+#pragma unroll
+              for (int x = 0; x < 4; ++x) w[x] = ex2(w[x]);
+              sum[0] = fma2(pair(w[0], w[1]), d[i].x, sum[0]);
+              sum[1] = fma2(pair(w[2], w[3]), d[i].y, sum[1]);
+              uint32_t h[2] = {rope::pack2<__half>(w[0], w[1]), rope::pack2<__half>(w[2], w[3])}, code[2];
+#pragma unroll
+              for (int x = 0; x < 2; ++x) code[x] = first_piece(h[x]);
+              piece[0][i] = __byte_perm(code[0], code[1], 0x7531);
+#pragma unroll
+              for (int p = 1; p < NP; ++p) {
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                  code[x] = next_piece(h[x]);
+                  if (p + 1 < NP) h[x] = behind(h[x], code[x]);
+                }
+                piece[p][i] = __byte_perm(code[0], code[1], 0x7531);
+              }
+            }
+#pragma unroll
+            for (int p = 0; p < NP; ++p)
+              sts128(p_ops + p * S::kPieceP + 8192 * tok_half + sw128(row, 4 * col_half + (c >> 4)), piece[p][0], piece[p][1], piece[p][2],
+                     piece[p][3]);
+          }
+          float y[4];
+          unpair(sum[0], y[0], y[1]);
+          unpair(sum[1], y[2], y[3]);
+          l_run += (y[0] + y[1]) + (y[2] + y[3]);
         }
+        warp_arrive(ms.sc_empty[buf]);
         fence_async_smem();
         fence_before_sync();
         warp_arrive_pair(peer_addr(smem_addr(&ms.p_full), 0));
@@ -553,19 +576,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto slot = [&]() { return ring_lo + sl++ % kSlots * (kSlotBytes / 16); };
         auto s_mmas = [&](int t) {  // S(t)
           const uint32_t d = tmem + kColS + 128 * ((t_base + t) & 1);
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            if ((c & 1) == 0 && !take()) return;
+            const uint32_t b_at = slot(), a_at = q_lo + 512 * c;
 #pragma unroll
-          for (int c2 = 0; c2 < 2; ++c2) {
-            if (!take()) return;
+            for (int p = 0; p < NP; ++p)
 #pragma unroll
-            for (int c = 2 * c2; c < 2 * c2 + 2; ++c) {
-              const uint32_t b_at = slot();
-#pragma unroll
-              for (int p = 0; p < NP; ++p)
-#pragma unroll
-                for (int ks = 0; ks < 4; ++ks)
-                  pair_mma_f8(d, q_lo + (p * S::kPieceQ + 8192 * c + 32 * ks) / 16, b_at + 2 * ks, id_s, c > 0 || p > 0 || ks > 0);
-            }
-            give();
+              for (int ks = 0; ks < 4; ++ks)
+                pair_mma_f8(d, a_at + (p * S::kPieceQ + 32 * ks) / 16, b_at + 2 * ks, id_s, p > 0 || ks > 0 ? 1u : (uint32_t)c);
+            if (c & 1) give();
           }
           if (!take()) return;
           if (t > 0) p_look = warp_look(ms.p_full, t_base + t - 1);
@@ -585,26 +605,25 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (t + 1 < n) s_mmas(t + 1);
           if (!ok || !(ok = warp_wait_after(p_look, ms.p_full, t_base + t, abort_flag))) break;
           fence_after_sync();
-#pragma unroll
-          for (int g2 = 0; g2 < 2; ++g2) {  // 128 tokens
-            if (!take()) break;
-            if ((r0 + t) * kTok + 128 * (g2 + 1) > end) {
-              if (!(ok = warp_wait(ms.tail_done[u % kUnits], tails >> (u % kUnits) & 1, abort_flag))) break;
-              tails ^= 1u << (u % kUnits);
+#pragma unroll 1
+          for (int g = 0; g < 4; ++g) {  // 64 tokens
+            if ((g & 1) == 0) {
+              if (!take()) break;
+              if ((r0 + t) * kTok + 64 * (g + 2) > end) {
+                if (!(ok = warp_wait(ms.tail_done[u % kUnits], tails >> (u % kUnits) & 1, abort_flag))) break;
+                tails ^= 1u << (u % kUnits);
+              }
             }
+            const uint32_t b_at = slot(), w_at = w_lo + (g >> 1) * 512 + (g & 1) * 4;
 #pragma unroll
-            for (int g = 0; g < 2; ++g) {
-              const uint32_t b_at = slot(), w_at = w_lo + (8192 * g2 + 64 * g) / 16;
+            for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
-              for (int ks = 0; ks < 2; ++ks)
+              for (int h = 0; h < 2; ++h)
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
-#pragma unroll
-                  for (int p = 0; p < NP; ++p)
-                    pair_mma_f8(tmem + 128 * h, w_at + (p * S::kPieceP + 32 * ks) / 16, b_at + (8192 * h + 4096 * ks) / 16,
-                                p == 0 ? id_o5 : id_o4, g2 > 0 || g > 0 || ks > 0 || p > 0 ? 1u : (uint32_t)t);
-            }
-            give();
+                for (int p = 0; p < NP; ++p)
+                  pair_mma_f8(tmem + 128 * h, w_at + (p * S::kPieceP + 32 * ks) / 16, b_at + (8192 * h + 4096 * ks) / 16,
+                              p == 0 ? id_o5 : id_o4, ks > 0 || p > 0 ? 1u : (uint32_t)(t + g));
+            if (g & 1) give();
           }
           if (!ok) break;
           pair_commit(smem_addr(&ms.o_done), 3);
