@@ -191,6 +191,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     latent_kernel(const __grid_constant__ CUtensorMap map, const LatentPool pool, const LatentAttnArgs a, int box, int4* info) {
   using S = Shape<T>;
   constexpr int NP = S::kPieces, kSlots = S::kSlots;
+  constexpr bool kF16 = std::is_same<T, __half>::value;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t base = smem_addr(smem_raw) + (1024 - (smem_addr(smem_raw) & 1023) & 1023);
   Misc& ms = *reinterpret_cast<Misc*>(smem_raw + (base - smem_addr(smem_raw)) + S::kOffMisc);
@@ -202,6 +203,25 @@ __global__ void __launch_bounds__(kThreads, 1)
   const long long n_rows = (long long)a.T * a.heads;
   const int n_rt = (int)((n_rows + kUnitRows - 1) / kUnitRows);
 
+  if (tid == 32 * kMmaWarp) {
+    for (int i = 0; i < kUnits; ++i) {
+      mbar_init(smem_addr(&ms.full[i]), 1);
+      mbar_init(smem_addr(&ms.empty[i]), 1);
+      mbar_init(smem_addr(&ms.here[i]), 1);
+      mbar_init(smem_addr(&ms.tail_done[i]), 2);
+    }
+    mbar_init(smem_addr(&ms.q_full), 2 * kSoftWarps);
+    mbar_init(smem_addr(&ms.p_full), 2 * kSoftWarps);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_addr(&ms.s_full[i]), 1);
+      mbar_init(smem_addr(&ms.sc_full[i]), 1);
+      mbar_init(smem_addr(&ms.sc_empty[i]), kSoftWarps);
+    }
+    mbar_init(smem_addr(&ms.o_done), 1);
+    mbar_init(smem_addr(&ms.drain), 1);
+    ms.abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
   // ---- the pair's range of tiles: x .. x_end - 1 of `total`, kept by thread 0 ----
   // range c starts at c * each + min(c, more)
   const uint32_t pairs = gridDim.x >> 1, me = blockIdx.x >> 1;
@@ -251,32 +271,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t longer = more * (each + 1u);
     return tile < longer ? tile / (each + 1u) : more + (tile - longer) / each;
   };
-  if (tid == 0) {
-    for (int i = 0; i < kUnits; ++i) {
-      mbar_init(smem_addr(&ms.full[i]), 1);
-      mbar_init(smem_addr(&ms.empty[i]), 1);
-      mbar_init(smem_addr(&ms.here[i]), 1);
-      mbar_init(smem_addr(&ms.tail_done[i]), 2);
-    }
-    mbar_init(smem_addr(&ms.q_full), 2 * kSoftWarps);
-    mbar_init(smem_addr(&ms.p_full), 2 * kSoftWarps);
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(smem_addr(&ms.s_full[i]), 1);
-      mbar_init(smem_addr(&ms.sc_full[i]), 1);
-      mbar_init(smem_addr(&ms.sc_empty[i]), kSoftWarps);
-    }
-    mbar_init(smem_addr(&ms.o_done), 1);
-    mbar_init(smem_addr(&ms.drain), 1);
-    ms.abort = 0;
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-  }
   __syncwarp();
   if (warp == kMmaWarp) pair_tmem_alloc(smem_addr(&ms.tmem), 512);
   fence_before_sync();
-  __syncthreads();
-  cluster_sync();  // the peer's barriers are there
-  fence_after_sync();
-  const uint32_t tmem = *(volatile uint32_t*)&ms.tmem;
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  bool first_frag = true;
 
   // softmax: row of the CTA (= lane of tensor memory, twice), the quarter of a tile's tokens and of the dims
   const int quad = warp & 3, col_half = warp >> 2 & 1, row = 32 * (quad & 1) + lane, tok_half = quad >> 1;
@@ -313,8 +312,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     fence_before_sync();
     __syncthreads();
+    if (first_frag) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");  // the peer's barriers are there
+    first_frag = false;
     fence_after_sync();
     if (ms.f.done) break;
+    const uint32_t tmem = *(volatile uint32_t*)&ms.tmem;
     const int b = ms.f.b, r0 = ms.f.r0, len = ms.f.len, end = ms.f.end;
     const int n = end > 0 ? ms.f.n : 0;  // tiles with tokens
     const long long urow = (long long)ms.f.rt * kUnitRows + kRows * (int)rank + row;  // the thread's query row
@@ -328,35 +330,41 @@ __global__ void __launch_bounds__(kThreads, 1)
       float q_scale = 0.f;
       if (n > 0) {
         // ---- queries as pieces: eight rows to a warp, a lane 16 dims and an eighth of a position part of every fourth row ----
+        // lane l: where row l % 8 of the warp's stands, -1 past the last row
+        long long c_at = -1, pe_at = -1;
+        {
+          const long long u = (long long)ms.f.rt * kUnitRows + kRows * (int)rank + 8 * warp + (lane & 7);
+          if (u < n_rows) {
+            const uint32_t jj = (uint32_t)u / (uint32_t)a.heads, hh = (uint32_t)u - jj * (uint32_t)a.heads;
+            const long long token = (long long)b * a.T + jj;
+            c_at = token * a.q_c.stride + hh * a.q_c.head_stride;
+            pe_at = token * a.q_pe.stride + hh * a.q_pe.head_stride;
+          }
+        }
+        uint4 raw[8][2], pe2[2];  // all loads in flight together
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
+          const long long from = __shfl_sync(0xffffffffu, c_at, r);
+          const uint4* src = reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(a.q_c.x) + from) + 2 * lane;
+#pragma unroll
+          for (int i = 0; i < 2; ++i) raw[r][i] = from >= 0 ? __ldg(src + i) : make_uint4(0u, 0u, 0u, 0u);
+        }
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const long long from = __shfl_sync(0xffffffffu, pe_at, 4 * r + (lane >> 3));
+          pe2[r] = from >= 0 ? __ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(a.q_pe.x) + from) + (lane & 7)) : make_uint4(0u, 0u, 0u, 0u);
+        }
 #pragma unroll 1
         for (int r4 = 0; r4 < 8; r4 += 4) {
-          uint4 raw[4][2], pe;
           const int row0 = 8 * warp + r4;
-          auto at_row = [&](int r, const HeadsDev& h) {  // null past the last row
-            const long long u = (long long)ms.f.rt * kUnitRows + kRows * (int)rank + r;
-            if (u >= n_rows) return (const T*)nullptr;
-            const int jj = (int)((uint32_t)u / (uint32_t)a.heads), hh = (int)((uint32_t)u % (uint32_t)a.heads);
-            return reinterpret_cast<const T*>(h.x) + ((long long)b * a.T + jj) * h.stride + hh * h.head_stride;
-          };
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const T* src = at_row(row0 + r, a.q_c);
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-              raw[r][i] = src ? __ldg(reinterpret_cast<const uint4*>(src) + 2 * lane + i) : make_uint4(0u, 0u, 0u, 0u);
-          }
-          {
-            const T* src = at_row(row0 + (lane >> 3), a.q_pe);
-            pe = src ? __ldg(reinterpret_cast<const uint4*>(src) + (lane & 7)) : make_uint4(0u, 0u, 0u, 0u);
-          }
+          const uint4 pe = pe2[0];
+          // magnitudes order as their 16 bits do, NaN above infinity above the rest
           auto largest = [&](const uint4& v) {
-            uint32_t top = 0u;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const float2 f = rope::unpack2<T>(word(v, k));
-              top = max(top, max(__float_as_uint(f.x) & 0x7FFFFFFFu, __float_as_uint(f.y) & 0x7FFFFFFFu));
-            }
-            return top;
+            uint32_t m = v.x & 0x7FFF7FFFu;
+            asm("max.u16x2 %0, %0, %1;" : "+r"(m) : "r"(v.y & 0x7FFF7FFFu));
+            asm("max.u16x2 %0, %0, %1;" : "+r"(m) : "r"(v.z & 0x7FFF7FFFu));
+            asm("max.u16x2 %0, %0, %1;" : "+r"(m) : "r"(v.w & 0x7FFF7FFFu));
+            return max(m >> 16, m & 0xFFFFu);
           };
           uint32_t top_p = largest(pe);  // of row lane / 8
 #pragma unroll
@@ -366,20 +374,29 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int r = 0; r < 4; ++r) {
             const uint32_t top_c = __reduce_max_sync(0xffffffffu, max(largest(raw[0][0]), largest(raw[0][1])));
             const uint32_t top_r = __shfl_sync(0xffffffffu, top_p, 8 * r);
-            const bool odd = max(top_c, top_r) >= 0x7F800000u;  // a row that is not finite: all its scores are NaN
-            const int e = odd ? 0 : query_exp(top_c, top_r);
+            const bool odd = max(top_c, top_r) >= (kF16 ? 0x7C00u : 0x7F80u);  // a row that is not finite: all its scores are NaN
+            const float2 tops = rope::unpack2<T>(top_c | top_r << 16);
+            // (fp16: 2^(-e - 8) is a factor in fp16; what is below 2^-20 of 448 has few bits)
+            const int e = odd ? 0 : max(query_exp(__float_as_uint(tops.x), __float_as_uint(tops.y)), kF16 ? -20 : -100);
             const float down = block::pow2(-e);
             if ((lane >> 3) == r) pe_down = odd ? 0.f : down;
             if (lane == 0) ms.q_scale[row0 + r] = odd ? CUDART_NAN_F : a.sm_scale * 1.44269504088896340736f * block::pow2(e);
             uint32_t piece[NP][4];
-            const float down8 = odd ? 0.f : down * 0.00390625f;  // 2^-8: as next_piece wants it
+            const float down8 = down * 0.00390625f;  // 2^-8: as next_piece wants it
+            const uint32_t down8_2 = rope::pack2<__half>(down8, down8);
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               uint32_t code[2][NP];
 #pragma unroll
               for (int i = 0; i < 2; ++i) {
-                const float2 f = rope::unpack2<T>(word(raw[0][k >> 1], 2 * (k & 1) + i));
-                uint32_t h = odd ? 0u : rope::pack2<__half>(f.x * down8, f.y * down8);  // exact, but for what is below 2^-24
+                uint32_t h = word(raw[0][k >> 1], 2 * (k & 1) + i);  // times 2^(-e - 8): exact, but for what is below 2^-24
+                if constexpr (kF16) {
+                  asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(h) : "r"(down8_2));
+                } else {
+                  const float2 f = rope::unpack2<T>(h);
+                  h = rope::pack2<__half>(f.x * down8, f.y * down8);
+                }
+                if (odd) h = 0u;
 #pragma unroll
                 for (int p = 0; p < NP; ++p) {
                   code[i][p] = next_piece(h);
@@ -393,8 +410,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int p = 0; p < NP; ++p)
               sts128(q_ops + p * S::kPieceQ + 8192 * (lane >> 3) + sw128(row0 + r, lane & 7), piece[p][0], piece[p][1], piece[p][2], piece[p][3]);
 #pragma unroll
-            for (int i = 0; i < 3; ++i) raw[i][0] = raw[i + 1][0], raw[i][1] = raw[i + 1][1];  // (one row's code, not four)
+            for (int i = 0; i < 7; ++i) raw[i][0] = raw[i + 1][0], raw[i][1] = raw[i + 1][1];  // (one row's code, not eight)
           }
+          pe2[0] = pe2[1];
           uint32_t w[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
@@ -832,7 +850,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   cluster_sync();  // the peer is done with this CTA's operands and barriers
   fence_after_sync();
-  if (warp == kMmaWarp) pair_tmem_dealloc(tmem, 512);
+  if (warp == kMmaWarp) pair_tmem_dealloc(*(volatile uint32_t*)&ms.tmem, 512);
 }
 
 // Joins the parts of units that span ranges.  A CTA takes 8 rows and 32 / G groups of 4 dims of a unit, its parts in G shares.
