@@ -21,6 +21,7 @@
 // memory.  Every wait is bounded: one that runs out sets RQ_STATUS_TIMEOUT and an abort flag every role polls.
 #include <math_constants.h>
 
+#include <atomic>
 #include <cstddef>
 #include <type_traits>
 
@@ -466,8 +467,17 @@ bool encode(CUtensorMap* map, bool bf16, const HeadsDev& x, int dims, int n, int
 template <typename T>
 cudaError_t launch(const Maps& maps, const PromptArgs& a, int splits, int n_rb, cudaStream_t stream) {
   static_assert(sizeof(Maps) + sizeof(PromptArgs) + 16 <= 4096, "kernel parameters");
-  cudaError_t e = cudaFuncSetAttribute(prompt_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  // the kernel's shared-memory limit, once a device (the attribute is set again on devices past the 64th)
+  static std::atomic<unsigned long long> set{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
+  const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
+  if (!(set.load(std::memory_order_relaxed) & bit) || bit == 0) {
+    e = cudaFuncSetAttribute(prompt_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e != cudaSuccess) return e;
+    set.fetch_or(bit, std::memory_order_relaxed);
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(2 * a.q.heads * splits), (unsigned)a.B, (unsigned)n_rb);
   cfg.blockDim = dim3(kThreads);

@@ -472,18 +472,20 @@ def rq_latent_append(ctx, rope, c, k_pe, positions, slot_mapping, pages, weight=
 
 
 def rq_latent_attention(ctx, q_c, q_pe, tree_mask, pages, block_table, seq_lens, out, status=None, stream=None):
-    """q_c, q_pe: [B][T][heads][512 and 64], all B * T tokens in one stride; out [B][T][heads][512].  The low-level call;
-    shapes and types are checked by LatentCache."""
-    B, T, heads = q_c.shape[:3]
-    rows = []
-    for t in (q_c, q_pe):
-        st = t.stride()
-        if T > 1 and B > 1 and st[0] != T * st[1]:
-            raise RQError("rq_latent_attention", RQ_ERR_INVALID)
-        rows.append(rq_heads(t.data_ptr(), st[0] if T == 1 else st[1], st[2], heads))
+    """q_c, q_pe: [B][T][heads][512 and 64], all B * T tokens in one stride, or without the T (one token each); out like q_c,
+    contiguous.  The low-level call; shapes and types are checked by LatentCache."""
+    sc, sp, T = q_c.stride(), q_pe.stride(), 1
+    if len(sc) == 4:
+        B, T = q_c.shape[:2]
+        if T > 1:
+            if B > 1 and (sc[0] != T * sc[1] or sp[0] != T * sp[1]):
+                raise RQError("rq_latent_attention", RQ_ERR_INVALID)
+            sc, sp = sc[1:], sp[1:]
+    heads = q_c.shape[-2]
     _check("rq_latent_attention",
-           lib().rq_latent_attention(ctx, rows[0], rows[1], T, _ptr(tree_mask), _ptr(pages), _ptr(block_table),
-                                     block_table.shape[-1], _ptr(seq_lens), B, _ptr(out), _ptr(status),
+           lib().rq_latent_attention(ctx, rq_heads(q_c.data_ptr(), sc[0], sc[-2], heads), rq_heads(q_pe.data_ptr(), sp[0], sp[-2], heads),
+                                     T, None if tree_mask is None else tree_mask.data_ptr(), pages.data_ptr(), block_table.data_ptr(),
+                                     block_table.shape[1], seq_lens.data_ptr(), seq_lens.shape[0], out.data_ptr(), _ptr(status),
                                      _stream(stream, pages.device)))
     return out
 
@@ -694,13 +696,15 @@ class KVCache:
             pass
 
 
-def _dense(t, dims, dtype, device) -> bool:
-    """t [n][heads][dims] (or [n][dims]) on the device, its last dim contiguous."""
-    return t.dtype == dtype and t.device == device and t.shape[-1] == dims and t.stride(-1) == 1
+# Argument checks of the calls below: device indices and stride tuples, as a call's checks otherwise cost more than its kernels.
+
+def _rows_ok(t, shape, dtype, index) -> bool:
+    """t has the shape and type, is on CUDA device `index`, and its last dim is contiguous."""
+    return t.shape == shape and t.dtype is dtype and t.get_device() == index and t.stride()[-1] == 1
 
 
-def _ints(t, n, device) -> bool:
-    return t.dtype == torch.int32 and t.device == device and t.dim() == 1 and t.shape[0] == n and t.is_contiguous()
+def _ints(t, n, index) -> bool:
+    return t.dtype is torch.int32 and t.shape == (n,) and t.get_device() == index and (n < 2 or t.stride()[0] == 1)
 
 
 class LatentCache:
@@ -730,6 +734,7 @@ class LatentCache:
             raise RQError("rq_latent_create", RQ_ERR_INVALID)
         self.pages = pages
         self._views = None
+        self._index = self.device.index
         self.status = torch.zeros(1, dtype=torch.int32, device=self.device)
 
     def append(self, c, k_pe, slot_mapping, rope=None, positions=None, weight=None, eps=1e-6, q_pe=None, q_pe_out=None,
@@ -738,19 +743,19 @@ class LatentCache:
         latents c [n][512], the rotation (rope: a Rope of rotary_dim <= 64, or None) of position parts k_pe [n][64] and of
         the queries' q_pe [n][heads][64], and the coding into slot_mapping (int32 [n]).  Returns the turned q_pe (None without;
         q_pe_out: where to write, q_pe itself for in place).  Slices of a projection's output are taken as they are."""
-        name, n, device, dtype = "rq_latent_append", slot_mapping.numel(), self.device, self.dtype
-        if (not _ints(slot_mapping, n, device) or c.shape != (n, LATENT_DIM) or not _dense(c, LATENT_DIM, dtype, device) or
-                k_pe.shape != (n, POSITION_DIM) or not _dense(k_pe, POSITION_DIM, dtype, device) or
-                (rope is not None and rope.device != device) or
-                (weight is not None and (weight.dtype != torch.float32 or weight.shape != (LATENT_DIM,) or
-                                         not weight.is_contiguous() or weight.device != device))):
+        name, n, index, dtype = "rq_latent_append", slot_mapping.shape[0], self._index, self.dtype
+        if (not _ints(slot_mapping, n, index) or not _rows_ok(c, (n, LATENT_DIM), dtype, index) or
+                not _rows_ok(k_pe, (n, POSITION_DIM), dtype, index) or
+                (rope is not None and rope.device.index != index) or
+                (weight is not None and (weight.dtype is not torch.float32 or weight.shape != (LATENT_DIM,) or
+                                         weight.stride()[0] != 1 or weight.get_device() != index))):
             raise RQError(name, RQ_ERR_INVALID)
         if q_pe is not None:
-            if q_pe.dim() != 3 or q_pe.shape[0] != n or not _dense(q_pe, POSITION_DIM, dtype, device):
+            if q_pe.dim() != 3 or not _rows_ok(q_pe, (n, q_pe.shape[1], POSITION_DIM), dtype, index):
                 raise RQError(name, RQ_ERR_INVALID)
             if q_pe_out is None:
-                q_pe_out = torch.empty(q_pe.shape, dtype=dtype, device=device)
-            elif q_pe_out.shape != q_pe.shape or not _dense(q_pe_out, POSITION_DIM, dtype, device):
+                q_pe_out = torch.empty(q_pe.shape, dtype=dtype, device=self.device)
+            elif not _rows_ok(q_pe_out, q_pe.shape, dtype, index):
                 raise RQError(name, RQ_ERR_INVALID)
         elif q_pe_out is not None:
             raise RQError(name, RQ_ERR_INVALID)
@@ -760,23 +765,21 @@ class LatentCache:
                              weight, eps, q_pe, q_pe_out, self.status, stream)
         return q_pe_out
 
-    def _attend(self, q_c, q_pe, tree_mask, block_table, seq_lens, out, stream):
-        name, device, dtype, heads = "rq_latent_attention", self.device, self.dtype, self.num_heads
-        if q_c.dim() != 4 or q_pe.dim() != 4:
-            raise RQError(name, RQ_ERR_INVALID)
-        B, T = q_c.shape[:2]
-        if (q_c.shape != (B, T, heads, LATENT_DIM) or not _dense(q_c, LATENT_DIM, dtype, device) or
-                q_pe.shape != (B, T, heads, POSITION_DIM) or not _dense(q_pe, POSITION_DIM, dtype, device) or T < 1 or
-                not _ints(seq_lens, B, device) or block_table.dtype != torch.int32 or block_table.device != device or
+    def _attend(self, q_c, q_pe, dims, tree_mask, block_table, seq_lens, out, stream):
+        index, dtype, shape = self._index, self.dtype, q_c.shape
+        B = shape[0] if len(shape) == dims else -1
+        if (B < 0 or shape[-2] != self.num_heads or not _rows_ok(q_c, (*shape[:-1], LATENT_DIM), dtype, index) or
+                not _rows_ok(q_pe, (*shape[:-1], POSITION_DIM), dtype, index) or shape[1] < 1 or
+                not _ints(seq_lens, B, index) or block_table.dtype is not torch.int32 or block_table.get_device() != index or
                 block_table.dim() != 2 or block_table.shape[0] != B or not block_table.is_contiguous() or
                 (tree_mask is not None and (tree_mask.dtype not in (torch.int64, torch.uint64) or
-                                            tree_mask.shape != (B, T) or not tree_mask.is_contiguous() or
-                                            tree_mask.device != device))):
-            raise RQError(name, RQ_ERR_INVALID)
+                                            tree_mask.shape != shape[:2] or not tree_mask.is_contiguous() or
+                                            tree_mask.get_device() != index))):
+            raise RQError("rq_latent_attention", RQ_ERR_INVALID)
         if out is None:
-            out = torch.empty((B, T, heads, LATENT_DIM), dtype=dtype, device=device)
-        elif out.shape != q_c.shape or not out.is_contiguous() or out.dtype != dtype or out.device != device:
-            raise RQError(name, RQ_ERR_INVALID)
+            out = torch.empty(shape, dtype=dtype, device=self.device)
+        elif not _rows_ok(out, shape, dtype, index) or not out.is_contiguous():
+            raise RQError("rq_latent_attention", RQ_ERR_INVALID)
         if B == 0:
             return out
         return rq_latent_attention(self.ctx, q_c, q_pe, tree_mask, self.pages, block_table, seq_lens, out, self.status, stream)
@@ -784,38 +787,36 @@ class LatentCache:
     def decode(self, q_c, q_pe, block_table, seq_lens, out=None, stream=None):
         """Absorbed attention of each sequence's newest token: q_c [B][heads][512], q_pe [B][heads][64], block_table
         int32 [B][max_pages], seq_lens int32 [B]; the result is in the latents' space, [B][heads][512]."""
-        if q_c.dim() != 3 or q_pe.dim() != 3:
-            raise RQError("rq_latent_attention", RQ_ERR_INVALID)
-        return self._attend(q_c[:, None], q_pe[:, None], None, block_table, seq_lens, None if out is None else out[:, None],
-                            stream)[:, 0]
+        return self._attend(q_c, q_pe, 3, None, block_table, seq_lens, out, stream)
 
     def verify(self, q_c, q_pe, block_table, seq_lens, out=None, stream=None):
         """The same of the last T cached tokens of each sequence, row j up to its own: q_c [B][T][heads][512], q_pe
         [B][T][heads][64]."""
-        return self._attend(q_c, q_pe, None, block_table, seq_lens, out, stream)
+        return self._attend(q_c, q_pe, 4, None, block_table, seq_lens, out, stream)
 
     def tree_verify(self, q_c, q_pe, tree_mask, block_table, seq_lens, out=None, stream=None):
         """verify with tree_mask int64/uint64 [B][T]: row j sees the prefix and draft i where bit i is set."""
         if tree_mask is None:
             raise RQError("rq_latent_attention", RQ_ERR_INVALID)
-        return self._attend(q_c, q_pe, tree_mask, block_table, seq_lens, out, stream)
+        return self._attend(q_c, q_pe, 4, tree_mask, block_table, seq_lens, out, stream)
 
     def read(self, block_table, offsets, n, starts=None, c=None, k_pe=None, stream=None):
         """Tokens read back, (c [n][512], k_pe [n][64]): rows offsets[b] .. offsets[b + 1] - 1 (offsets: int32 [B + 1]) are
         sequence b's from position starts[b] (int32 [B]; None: 0) on.  Rows of no sequence are left as they are."""
-        name, device, dtype = "rq_latent_read", self.device, self.dtype
+        name, index, dtype = "rq_latent_read", self._index, self.dtype
         B = block_table.shape[0] if block_table.dim() == 2 else -1
-        if (B < 0 or n < 0 or block_table.dtype != torch.int32 or block_table.device != device or
-                not block_table.is_contiguous() or not _ints(offsets, B + 1, device) or
-                (starts is not None and not _ints(starts, B, device))):
+        if (B < 0 or n < 0 or block_table.dtype is not torch.int32 or block_table.get_device() != index or
+                not block_table.is_contiguous() or not _ints(offsets, B + 1, index) or
+                (starts is not None and not _ints(starts, B, index))):
             raise RQError(name, RQ_ERR_INVALID)
         if c is None:
-            c = torch.empty((n, LATENT_DIM), dtype=dtype, device=device)
+            c = torch.empty((n, LATENT_DIM), dtype=dtype, device=self.device)
+        elif not _rows_ok(c, (n, LATENT_DIM), dtype, index) or not c.is_contiguous():
+            raise RQError(name, RQ_ERR_INVALID)
         if k_pe is None:
-            k_pe = torch.empty((n, POSITION_DIM), dtype=dtype, device=device)
-        for t, dims in ((c, LATENT_DIM), (k_pe, POSITION_DIM)):
-            if t.shape != (n, dims) or t.dtype != dtype or t.device != device or not t.is_contiguous():
-                raise RQError(name, RQ_ERR_INVALID)
+            k_pe = torch.empty((n, POSITION_DIM), dtype=dtype, device=self.device)
+        elif not _rows_ok(k_pe, (n, POSITION_DIM), dtype, index) or not k_pe.is_contiguous():
+            raise RQError(name, RQ_ERR_INVALID)
         if B and n:
             rq_latent_read(self.ctx, self.pages, block_table, starts, offsets, c, k_pe, self.status, stream)
         return c, k_pe
@@ -860,22 +861,20 @@ def prompt_attention(q, k, k_pe, v, q_offsets, k_offsets, max_new, sm_scale=0.0,
     strides of tokens and heads.  q_offsets, k_offsets: int32 [B + 1]; a sequence's queries are its last tokens, query j sees
     its keys up to nk - nq + j.  max_new: the most queries of a sequence.  sm_scale 0: 1 / sqrt(192).  Returns
     [nq][heads][128]; status (int32 [1]) collects RQ_STATUS_* bits."""
-    name, device, dtype = "rq_prompt_attention", q.device, q.dtype
-    if q.dim() != 3 or k.dim() != 3 or k_pe.dim() != 2 or v.dim() != 3 or dtype not in _IO_TYPES or q_offsets.dim() != 1:
+    name, index, dtype, shape = "rq_prompt_attention", q.get_device(), q.dtype, q.shape
+    if len(shape) != 3 or k.dim() != 3 or dtype not in _IO_TYPES or q_offsets.dim() != 1 or index < 0:
         raise RQError(name, RQ_ERR_INVALID)
-    nq, heads, nk, B = q.shape[0], q.shape[1], k.shape[0], q_offsets.shape[0] - 1
-    if (device.type != "cuda" or B < 0 or heads < 1 or k.shape != (nk, heads, 128) or v.shape != (nk, heads, 128) or
-            k_pe.shape != (nk, POSITION_DIM) or not _dense(q, PROMPT_DIM, dtype, device) or
-            not _dense(k, 128, dtype, device) or not _dense(v, 128, dtype, device) or
-            not _dense(k_pe, POSITION_DIM, dtype, device) or not _ints(q_offsets, B + 1, device) or
-            not _ints(k_offsets, B + 1, device) or max_new < 0 or
-            (status is not None and (status.dtype != torch.int32 or status.device != device))):
+    nq, heads, nk, B = shape[0], shape[1], k.shape[0], q_offsets.shape[0] - 1
+    if (B < 0 or heads < 1 or shape[2] != PROMPT_DIM or q.stride()[2] != 1 or not _rows_ok(k, (nk, heads, 128), dtype, index) or
+            not _rows_ok(v, (nk, heads, 128), dtype, index) or not _rows_ok(k_pe, (nk, POSITION_DIM), dtype, index) or
+            not _ints(q_offsets, B + 1, index) or not _ints(k_offsets, B + 1, index) or max_new < 0 or
+            (status is not None and (status.dtype is not torch.int32 or status.get_device() != index))):
         raise RQError(name, RQ_ERR_INVALID)
     if out is None:
-        out = torch.empty((nq, heads, 128), dtype=dtype, device=device)
-    elif out.shape != (nq, heads, 128) or out.dtype != dtype or out.device != device or not out.is_contiguous():
+        out = torch.empty((nq, heads, 128), dtype=dtype, device=q.device)
+    elif not _rows_ok(out, (nq, heads, 128), dtype, index) or not out.is_contiguous():
         raise RQError(name, RQ_ERR_INVALID)
-    if device.index != torch.cuda.current_device():
-        with torch.cuda.device(device):
+    if index != torch.cuda.current_device():
+        with torch.cuda.device(index):
             return rq_prompt_attention(q, k, k_pe, v, q_offsets, k_offsets, max_new, out, sm_scale, status, stream)
     return rq_prompt_attention(q, k, k_pe, v, q_offsets, k_offsets, max_new, out, sm_scale, status, stream)
