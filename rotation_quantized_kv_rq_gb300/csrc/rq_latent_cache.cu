@@ -28,30 +28,22 @@ struct Turn {
   float c[4], s[4];  // of the pair of each of the four dims; s negated where the dim is a pair's first
   int other;         // lane of the half-warp that holds the other halves; -1: past rotary_dim
 };
+// All lanes of the warp call it: lane l computes pair l's cosine and sine, and takes those of its own pairs from others.
 template <bool INTERLEAVED>
-__device__ __forceinline__ Turn turn_of(const RopeTable& r, int j, const int32_t* positions, long long n, long long t) {
+__device__ __forceinline__ Turn turn_of(const RopeTable& r, int lane, const int32_t* positions, long long n, long long t) {
+  const int j = lane & 15;
+  float2 mine = make_float2(1.f, 0.f);
+  if (2 * lane < r.rotary_dim) mine = cos_sin(r, lane, positions, n, t);
+  const int away = r.rotary_dim >> 3;
+  const bool turns = 4 * j < r.rotary_dim, first = INTERLEAVED || j < away;
   Turn u;
-  u.other = -1;
-  if (4 * j >= r.rotary_dim) return u;
-  if (INTERLEAVED) {
-    u.other = j;
+  u.other = !turns ? -1 : INTERLEAVED ? j : first ? j + away : j - away;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const float2 cs = cos_sin(r, 2 * j + i, positions, n, t);
-      u.c[2 * i] = u.c[2 * i + 1] = cs.x;
-      u.s[2 * i] = -cs.y, u.s[2 * i + 1] = cs.y;
-    }
-  } else {
-    const int away = r.rotary_dim >> 3;
-    const bool first = j < away;
-    u.other = first ? j + away : j - away;
-    const int pair = first ? 4 * j : 4 * (j - away);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 cs = cos_sin(r, pair + i, positions, n, t);
-      u.c[i] = cs.x;
-      u.s[i] = first ? -cs.y : cs.y;
-    }
+  for (int i = 0; i < 4; ++i) {
+    const int pair = INTERLEAVED ? 2 * j + (i >> 1) : 4 * (first ? j : j - away) + i;
+    u.c[i] = __shfl_sync(0xffffffffu, mine.x, pair & 31);
+    const float sn = __shfl_sync(0xffffffffu, mine.y, pair & 31);
+    u.s[i] = (INTERLEAVED ? (i & 1) == 0 : first) ? -sn : sn;
   }
   return u;
 }
@@ -78,52 +70,65 @@ __device__ __forceinline__ void widen4(float (&x)[4], const uint2& w) {
   x[0] = a.x, x[1] = a.y, x[2] = b.x, x[3] = b.y;
 }
 
-// Warp (token, part): part 0 codes the token's latent and position part, part 1 + i turns queries of heads
-// i * per .. .
+// Queries of heads first .. last - 1 of token t, two heads to the warp at a time.
+template <typename T, bool INTERLEAVED>
+__device__ __forceinline__ void turn_heads(const LatentAppendArgs& a, long long t, int first, int last, const Turn& u) {
+  const int j = threadIdx.x & 15, half = threadIdx.x >> 4 & 1;
+  const T* src = reinterpret_cast<const T*>(a.q.x) + t * a.q.stride + 4 * j;
+  T* dst = reinterpret_cast<T*>(const_cast<void*>(a.q_out.x)) + t * a.q_out.stride + 4 * j;
+  constexpr int kBatch = 8;
+  for (int h0 = first; h0 < last; h0 += 2 * kBatch) {
+    uint2 raw[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int h = h0 + 2 * i + half;
+      raw[i] = h < last ? *reinterpret_cast<const uint2*>(src + h * a.q.head_stride) : make_uint2(0u, 0u);  // (may be in place)
+    }
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      if (h0 + 2 * i >= last) break;
+      const int h = h0 + 2 * i + half;
+      float x[4];
+      widen4<T>(x, raw[i]);
+      turn4<INTERLEAVED>(x, u);
+      if (h < last)
+        *reinterpret_cast<uint2*>(dst + h * a.q_out.head_stride) = make_uint2(pack2<T>(x[0], x[1]), pack2<T>(x[2], x[3]));
+    }
+  }
+}
+
+// Warp (token, part): part 0 codes the token's latent and position part, part i turns queries of heads per * (i - 1) .. ; with
+// one part, that warp turns all of them.
 template <typename T, bool INTERLEAVED>
 __global__ void __launch_bounds__(kThreads) latent_append_kernel(const LatentPool pool, const LatentAppendArgs a, int parts, int per) {
   const int lane = threadIdx.x & 31, j = lane & 15, half = lane >> 4;
   const long long w = ((long long)blockIdx.x * kThreads + threadIdx.x) >> 5;
-  const long long t = w / parts;
+  const long long t = parts == 1 ? w : w / parts;
   if (t >= a.n) return;
-  const int part = (int)(w % parts);
+  const int part = (int)(w - t * parts);
+  // a coding warp's rows are on their way while the angles are computed
+  const int slot = part == 0 ? __ldg(a.slots + t) : -1;
+  uint4 r0 = make_uint4(0u, 0u, 0u, 0u), r1 = r0;
+  uint2 rp = make_uint2(0u, 0u);
+  if (part == 0) {
+    const uint4* row = reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(a.c) + t * a.c_stride) + 2 * lane;
+    r0 = __ldg(row), r1 = __ldg(row + 1);
+    rp = __ldg(reinterpret_cast<const uint2*>(reinterpret_cast<const T*>(a.k_pe) + t * a.k_pe_stride) + j);
+  }
   Turn u;
   u.other = -1;
-  if (a.rope.rotary_dim > 0) u = turn_of<INTERLEAVED>(a.rope, j, a.positions, a.n, t);
+  if (a.rope.rotary_dim > 0) u = turn_of<INTERLEAVED>(a.rope, lane, a.positions, a.n, t);
   if (part > 0) {
-    const int first = (part - 1) * per, last = min(a.q.heads, first + per);
-    const T* src = reinterpret_cast<const T*>(a.q.x) + t * a.q.stride + 4 * j;
-    T* dst = reinterpret_cast<T*>(const_cast<void*>(a.q_out.x)) + t * a.q_out.stride + 4 * j;
-    constexpr int kBatch = 4;
-    for (int h0 = first; h0 < last; h0 += 2 * kBatch) {
-      uint2 raw[kBatch];
-#pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        const int h = h0 + 2 * i + half;
-        raw[i] = h < last ? *reinterpret_cast<const uint2*>(src + h * a.q.head_stride) : make_uint2(0u, 0u);  // (may be in place)
-      }
-#pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        const int h = h0 + 2 * i + half;
-        float x[4];
-        widen4<T>(x, raw[i]);
-        turn4<INTERLEAVED>(x, u);
-        if (h < last)
-          *reinterpret_cast<uint2*>(dst + h * a.q_out.head_stride) = make_uint2(pack2<T>(x[0], x[1]), pack2<T>(x[2], x[3]));
-      }
-    }
+    turn_heads<T, INTERLEAVED>(a, t, (part - 1) * per, min(a.q.heads, part * per), u);
     return;
   }
-  const int slot = __ldg(a.slots + t);
+  if (parts == 1) turn_heads<T, INTERLEAVED>(a, t, 0, a.q.heads, u);
   if (slot < 0) return;
   if (slot >= pool.num_pages * pool.page_size) {
     if (lane == 0 && a.status) atomicOr(a.status, RQ_STATUS_BAD_SLOT);
     return;
   }
   // the latent: 16 dims to a lane, one chunk of codes
-  const uint4* row = reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(a.c) + t * a.c_stride) + 2 * lane;
-  const uint4 r0 = __ldg(row), r1 = __ldg(row + 1);
-  const uint2 rp = __ldg(reinterpret_cast<const uint2*>(reinterpret_cast<const T*>(a.k_pe) + t * a.k_pe_stride) + j);
   float x[16];
   {
     const uint32_t w8[8] = {r0.x, r0.y, r0.z, r0.w, r1.x, r1.y, r1.z, r1.w};
@@ -134,16 +139,25 @@ __global__ void __launch_bounds__(kThreads) latent_append_kernel(const LatentPoo
     }
   }
   if (a.weight) {
-    float ss = 0.f;
+    float part4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int i = 0; i < 16; ++i) ss = fmaf(x[i], x[i], ss);
+    for (int i = 0; i < 16; ++i) part4[i & 3] = fmaf(x[i], x[i], part4[i & 3]);
+    float ss = (part4[0] + part4[1]) + (part4[2] + part4[3]);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    const float r = __frsqrt_rn(fmaf(ss, 1.f / kLatentDim, a.eps));
+    // The factor and the products with what their roundings leave, so that a code moves only for a value within some 2^-25 of the
+    // middle of two: a step of 2^-4 multiplies what rounding moves.
+    const float m = fmaf(ss, 1.f / kLatentDim, a.eps), r = __frsqrt_rn(m);
+    const float mr = m * r, r_lo = 0.5f * r * (fmaf(-mr, r, 1.f) - fmaf(m, r, -mr) * r);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float4 wt = __ldg(reinterpret_cast<const float4*>(a.weight) + 4 * lane + i);
-      x[4 * i] *= r * wt.x, x[4 * i + 1] *= r * wt.y, x[4 * i + 2] *= r * wt.z, x[4 * i + 3] *= r * wt.w;
+      const float4 w4 = __ldg(reinterpret_cast<const float4*>(a.weight) + 4 * lane + i);
+      const float wt[4] = {w4.x, w4.y, w4.z, w4.w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float y = x[4 * i + k] * wt[k], y_lo = fmaf(x[4 * i + k], wt[k], -y);
+        x[4 * i + k] = fmaf(y, r, fmaf(y, r_lo, y_lo * r));
+      }
     }
   }
   float p[4];
@@ -266,8 +280,8 @@ __global__ void __launch_bounds__(kThreads) latent_read_kernel(const LatentPool 
 }  // namespace
 
 cudaError_t launch_latent_append(const LatentPool& pool, const LatentAppendArgs& a, int num_sms, cudaStream_t stream) {
-  (void)num_sms;
-  const int per = 16, parts = 1 + (a.q.heads + per - 1) / per;
+  // One warp a token, so that the angles are computed once, where that fills the SMs; else queries in warps of 16 heads.
+  const int per = 16, parts = a.q.heads == 0 || a.n >= 16ll * num_sms ? 1 : 1 + (a.q.heads + per - 1) / per;
   const long long ctas = (a.n * parts * 32 + kThreads - 1) / kThreads;
   if (ctas > 0x7fffffffLL) return cudaErrorInvalidValue;
   const unsigned grid = (unsigned)ctas;
