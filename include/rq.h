@@ -516,9 +516,16 @@ typedef struct {
   int max_new;               /* the most queries of a sequence */
   float sm_scale;            /* 0 selects 1/sqrt(192) */
   int io_type;               /* RQ_F16 or RQ_BF16 */
+  void *workspace;           /* device, 16-byte aligned: contents undefined before and after, one call at a time */
+  size_t workspace_bytes;    /* at least rq_prompt_workspace */
 } rq_prompt;
 
-/* On the current device, which every pointer must be of.  B or nq = 0 is a no-op.  Errors: RQ_ERR_INVALID, RQ_ERR_CUDA. */
+/* Source: this library.  Bytes of workspace that rq_prompt_attention needs on a device (-1: the current), 80 MB; 0 if there is no
+   such device. */
+size_t rq_prompt_workspace(int device);
+
+/* On the current device, which every pointer must be of.  B or nq = 0 is a no-op.  Errors: RQ_ERR_INVALID, RQ_ERR_CAPACITY (a
+   workspace too small, or ceil(max_new / 512) * B * num_heads of 2^30 and more), RQ_ERR_CUDA. */
 int rq_prompt_attention(const rq_prompt *args, int32_t *d_status, void *stream);
 
 /* Source: this library.  Diagnostics.  While set, every attention call records ev_start on its

@@ -261,8 +261,11 @@ struct PromptArgs {
   float sm_scale;
   int bf16;
   int32_t* status;
+  float* ws;  // prompt_workspace bytes
+  int num_sms;
 };
-cudaError_t launch_prompt_attention(const PromptArgs& a, int num_sms, cudaStream_t stream);
+size_t prompt_workspace(int num_sms);
+cudaError_t launch_prompt_attention(const PromptArgs& a, cudaStream_t stream);
 
 // Dynamic shared memory the attention kernel needs (set as the kernel's maximum once).
 size_t attention_smem_bytes();

@@ -215,18 +215,33 @@ int rq_latent_read(rq_latent* ctx, const void* pages, const int32_t* block_table
   return to_status(rq::launch_latent_read(pool_of(ctx, pages), a, (cudaStream_t)stream));
 }
 
+size_t rq_prompt_workspace(int device) {
+  int dev = device, sms = 0;
+  if (dev < 0 && cudaGetDevice(&dev) != cudaSuccess) return 0;
+  return cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess ? rq::prompt_workspace(sms) : 0;
+}
+
 int rq_prompt_attention(const rq_prompt* p, int32_t* d_status, void* stream) {
-  if (!p || p->B < 0 || p->B > 65535 || p->nq < 0 || p->nk < 0 || p->max_new < 0 || p->max_new > 65535 * 512 || !(p->sm_scale >= 0.f) ||
+  if (!p || p->B < 0 || p->B > 65535 || p->nq < 0 || p->nk < 0 || p->max_new < 0 || !(p->sm_scale >= 0.f) ||
       std::isinf(p->sm_scale) || (p->io_type != RQ_F16 && p->io_type != RQ_BF16))
     return RQ_ERR_INVALID;
   if (p->B == 0 || p->nq == 0 || p->max_new == 0) return RQ_OK;
   const int H = p->q.heads;
-  if (bad_rows(&p->q, rq::kPromptDim, p->nq) || !p->out || misaligned16(p->out) || !p->q_offsets || !p->k_offsets)
+  if (bad_rows(&p->q, rq::kPromptDim, p->nq) || !p->out || misaligned16(p->out) || !p->q_offsets || !p->k_offsets ||
+      !p->workspace || misaligned16(p->workspace))
     return RQ_ERR_INVALID;
   if (p->nk > 0 && (bad_rows(&p->k, 128, p->nk) || bad_rows(&p->v, 128, p->nk) || p->k.heads != H || p->v.heads != H ||
                     !p->k_pe || misaligned16(p->k_pe) || (p->nk > 1 && bad_stride(p->k_pe_stride, rq::kPositionDim))))
     return RQ_ERR_INVALID;
+  // units (512 rows of a sequence and head) are counted in 30 bits
+  const int max_new = p->max_new < p->nq ? p->max_new : p->nq;
+  if (((long long)max_new + 511) / 512 * p->B * H > (1 << 30) - 1) return RQ_ERR_CAPACITY;
   rq::PromptArgs a{};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&a.num_sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return RQ_ERR_CUDA;
+  if (p->workspace_bytes < rq::prompt_workspace(a.num_sms)) return RQ_ERR_CAPACITY;
+  a.ws = (float*)p->workspace;
   a.q = heads_dev(&p->q);
   if (p->nk > 0) {
     a.k = heads_dev(&p->k);
@@ -240,14 +255,11 @@ int rq_prompt_attention(const rq_prompt* p, int32_t* d_status, void* stream) {
   a.B = p->B;
   a.nq = p->nq;
   a.nk = p->nk;
-  a.max_new = p->max_new < p->nq ? p->max_new : p->nq;
+  a.max_new = max_new;
   a.sm_scale = p->sm_scale > 0.f ? p->sm_scale : (float)(1.0 / std::sqrt((double)rq::kPromptDim));
   a.bf16 = p->io_type == RQ_BF16;
   a.status = d_status;
-  int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    return RQ_ERR_CUDA;
-  return to_status(rq::launch_prompt_attention(a, sms, (cudaStream_t)stream));
+  return to_status(rq::launch_prompt_attention(a, (cudaStream_t)stream));
 }
 
 }  // extern "C"

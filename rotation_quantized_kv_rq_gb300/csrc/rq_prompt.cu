@@ -17,8 +17,10 @@
 //   values (warps 10, 11 of both): in tiles that some row of the pair sees in part, values that are not finite are taken
 //     out before the weights, zeros among them, are multiplied with them, and given to the rows that see them at the end.
 // Tensor memory: O_b at columns 128 b, S_b at 256 + 128 b with W_b over its first half.
-// Few rows and long sequences: a cluster of up to four pairs shares a unit's tiles, and joins through distributed shared
-// memory.  Every wait is bounded: one that runs out sets RQ_STATUS_TIMEOUT and an abort flag every role polls.
+// The units with the most keys go first, and neighbouring pairs take neighbouring heads, whose rows share DRAM pages.  (Tiles of
+// all units cut into one even range a pair, pairs at unrelated places: 1 x 16,384 x 16 heads 846 -> 1,419 us.)  Where units
+// are few, or the last ones leave pairs idle, they are cut into parts, whose (m, l, out) a second kernel joins.
+// Every wait is bounded: one that runs out sets RQ_STATUS_TIMEOUT and an abort flag every role polls.
 #include <math_constants.h>
 
 #include <atomic>
@@ -45,7 +47,6 @@ constexpr uint32_t kColS = 256;
 constexpr float kLift = 7.f, kReach = 15.f;      // weights are 2^(score - m), m between maximum - kReach and maximum - kLift
 constexpr float kNone = -3.402823466e38f;        // m before any visible key
 constexpr float kLarge = 1048576.f;              // |maximum| from which weights are formed in two roundings
-constexpr int kMaxSplit = 4;
 
 struct Misc {
   // the leader's: K(t), V(t), the queries are there; [block] W(t); the values' warps are through with a tile
@@ -59,8 +60,9 @@ struct Misc {
 constexpr uint32_t kOffK = kQBytes, kOffV = kOffK + kStages * kKBytes, kOffMisc = kOffV + kStages * kVBytes;
 constexpr int kSmem = (int)(kOffMisc + sizeof(Misc)) + 1024;
 static_assert(kSmem <= 232448, "one CTA's shared memory");
-constexpr uint32_t kOffML = kRows * kDim * 4;  // a part's rows for the join stand over queries and tiles, then the rows' m and l
-static_assert(kOffML + 2 * kRows * 4 <= kOffMisc, "a part's rows for the join");
+// floats of a part's slot: 512 rows x 128 (as [dim / 4][row][4]), then the rows' m and l
+constexpr size_t kSlotFloats = (size_t)kUnitRows * kDim + 2 * kUnitRows;
+constexpr int kSlotsPerPair = 4;
 
 // Instruction descriptor of kind::f16 for T (fp16 0, bf16 1 at bits 7 and 10); bit 16: B with N along its rows.
 template <typename T>
@@ -100,27 +102,35 @@ struct Maps {
   CUtensorMap q, k, pe, v;
 };
 
+// Units in order: rows r0 .. r0 + 511 of a sequence, the ones with the most keys first, each for all heads.  The last ones may be
+// cut: units from `whole` on have `splits` parts each.
+struct Cut {
+  int n_rb, whole, splits;
+};
+
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_constant__ Maps maps, const PromptArgs a, int splits) {
+__global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_constant__ Maps maps, const PromptArgs a, const Cut cut) {
   extern __shared__ uint8_t smem_raw[];
   const uint32_t base = smem_addr(smem_raw) + (1024 - (smem_addr(smem_raw) & 1023) & 1023);
-  uint8_t* const smem = smem_raw + (base - smem_addr(smem_raw));
-  Misc& ms = *reinterpret_cast<Misc*>(smem + kOffMisc);
+  Misc& ms = *reinterpret_cast<Misc*>(smem_raw + (base - smem_addr(smem_raw)) + kOffMisc);
   const uint32_t q_ops = base, k_ring = base + kOffK, v_ring = base + kOffV;
   volatile int* const abort_flag = &ms.abort;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const uint32_t cta = cluster_rank(), rank = cta & 1, lead = cta & ~1u;  // parts of a unit are pairs of its cluster
-  const int part = (int)(cta >> 1), h = (int)blockIdx.x / (2 * splits), b = blockIdx.y;
+  const uint32_t rank = cluster_rank(), pair_id = blockIdx.x >> 1, heads = (uint32_t)a.q.heads;
 
-  // ---- the unit: rows r0 .. r0 + 511 of sequence b, the ones with the most keys first ----
+  // ---- the pair's unit, or part of one ----
+  const bool is_part = pair_id >= (uint32_t)cut.whole;
+  const uint32_t part_id = is_part ? pair_id - (uint32_t)cut.whole : 0u, splits = is_part ? (uint32_t)cut.splits : 1u;
+  const uint32_t unit = is_part ? (uint32_t)cut.whole + part_id / splits : pair_id, part = part_id % splits;
+  const int h = (int)(unit % heads), b = (int)(unit / heads % (uint32_t)a.B), turn = (int)(unit / heads / (uint32_t)a.B);
   const int q0 = __ldg(a.q_offsets + b), q1 = __ldg(a.q_offsets + b + 1), k0 = __ldg(a.k_offsets + b), k1 = __ldg(a.k_offsets + b + 1);
   if (q0 < 0 || q1 < q0 || q1 > a.nq || k0 < 0 || k1 < k0 || k1 > a.nk || q1 - q0 > a.max_new) {
     if (tid == 0 && a.status) atomicOr(a.status, RQ_STATUS_BAD_LEN);
     return;
   }
   const int nq = q1 - q0, nk = k1 - k0, ahead = nk - nq, n_rb = (nq + kUnitRows - 1) / kUnitRows;
-  if ((int)blockIdx.z >= n_rb) return;  // (a cluster's CTAs alike)
-  const int r0 = (n_rb - 1 - (int)blockIdx.z) * kUnitRows;
+  if (turn >= n_rb) return;  // (both CTAs of the pair)
+  const int r0 = (n_rb - 1 - turn) * kUnitRows;
   // tiles that a block's rows see, and this part's range of them
   auto tiles_to = [&](int row) { return max(0, (ahead + min(nq, row) + kTok - 1) / kTok); };
   const int all0 = tiles_to(r0 + kRows), all1 = r0 + kRows < nq ? tiles_to(r0 + kUnitRows) : 0, all = max(all0, all1);
@@ -240,7 +250,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
       l_run += (x[0] + x[1]) + (x[2] + x[3]);
       tmem_wait_st();
       fence_before_sync();
-      warp_arrive_pair(peer_addr(smem_addr(&ms.p_full[blk]), lead));
+      warp_arrive_pair(peer_addr(smem_addr(&ms.p_full[blk]), 0));
     }
     if (ok && n_b[blk] > 0) ok = warp_wait(ms.o_done[blk], 0, abort_flag);
     fence_after_sync();
@@ -249,7 +259,6 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
     if (rank == 0 && n > 0) {
       constexpr uint32_t id_s = idesc<T>(kRows, kTok, 0), id_o = idesc<T>(kRows, kDim, 1);
       const int last_b = n_b[1] > 0 ? 1 : 0;  // the block that uses a tile last
-      const uint32_t both = 3u << cta;
       bool issued = false;
       auto wait = [&](uint64_t& bar, uint32_t parity) { return ok = warp_wait(bar, parity, abort_flag); };
       auto s_mmas = [&](int bb, int t) {  // S_b(t)
@@ -261,8 +270,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
           pair_mma_ss(tmem + kColS + 128 * bb, sdesc(q_at + (ks >> 2) * kChunk + 32 * (ks & 3)),
                       sdesc(k_at + (ks >> 2) * (kChunk / 2) + 32 * (ks & 3)), id_s, ks > 0);
         issued = true;
-        if (bb == last_b && t + kStages < n) pair_commit(smem_addr(&ms.k_empty[st]), both);
-        pair_commit(smem_addr(&ms.s_full[bb]), both);
+        if (bb == last_b && t + kStages < n) pair_commit(smem_addr(&ms.k_empty[st]), 3);
+        pair_commit(smem_addr(&ms.s_full[bb]), 3);
       };
       wait(ms.q_full, 0);
 #pragma unroll
@@ -280,15 +289,15 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
 #pragma unroll
           for (int ks = 0; ks < 8; ++ks)  // keys 16 ks ..
             pair_mma_ts(tmem + 128 * bb, tmem + kColS + 128 * bb + 8 * ks, sdesc(v_ring + st * kVBytes + 2048 * ks), id_o, t > 0 || ks > 0);
-          if (bb == last_b && t + kStages < n) pair_commit(smem_addr(&ms.v_empty[st]), both);
+          if (bb == last_b && t + kStages < n) pair_commit(smem_addr(&ms.v_empty[st]), 3);
           if (t + 1 < n_b[bb])
             s_mmas(bb, t + 1);  // over the same columns, behind the MMAs that read them
           else
-            pair_commit(smem_addr(&ms.o_done[bb]), both);
+            pair_commit(smem_addr(&ms.o_done[bb]), 3);
         }
       }
       if (!ok && issued) {  // nothing may be running when the tensor memory is freed
-        pair_commit(smem_addr(&ms.drain), both);
+        pair_commit(smem_addr(&ms.drain), 3);
         for (int i = 0; i < kWaitLimit; ++i)
           if (mbar_test(smem_addr(&ms.drain), 0u)) break;
       }
@@ -297,7 +306,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
     // ================= copies: this CTA's share =================
     if (n > 0) {
       if (rank == 0) elect_expect(smem_addr(&ms.q_full), 2 * kQBytes);
-      const uint32_t bar = peer_addr(smem_addr(&ms.q_full), lead);
+      const uint32_t bar = peer_addr(smem_addr(&ms.q_full), 0);
 #pragma unroll
       for (int i = 0; i < 6; ++i)
         load_pair(q_ops + i * kChunk, maps.q, 64 * (i % 3), h, q0 + r0 + kRows * (i / 3) + kHalf * (int)rank, bar);
@@ -306,7 +315,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
       const int st = t % kStages, z = k0 + (t_first + t) * kTok;
       if (t >= kStages && !(ok = warp_wait(ms.k_empty[st], t / kStages - 1, abort_flag))) break;
       if (rank == 0) elect_expect(smem_addr(&ms.k_full[st]), 2 * kKBytes);
-      const uint32_t kbar = peer_addr(smem_addr(&ms.k_full[st]), lead), dst = k_ring + st * kKBytes;
+      const uint32_t kbar = peer_addr(smem_addr(&ms.k_full[st]), 0), dst = k_ring + st * kKBytes;
       const int zk = z + kTok / 2 * (int)rank;  // this CTA's 64 keys
       load_pair(dst, maps.k, 0, h, zk, kbar);
       load_pair(dst + kChunk / 2, maps.k, 64, h, zk, kbar);
@@ -314,7 +323,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
       if (t >= kStages && !(ok = warp_wait(ms.v_empty[st], t / kStages - 1, abort_flag))) break;
       if (t < t_fix) {
         if (rank == 0) elect_expect(smem_addr(&ms.v_full[st]), 2 * kVBytes);
-        load_pair(v_ring + st * kVBytes, maps.v, 64 * (int)rank, h, z, peer_addr(smem_addr(&ms.v_full[st]), lead));
+        load_pair(v_ring + st * kVBytes, maps.v, 64 * (int)rank, h, z, peer_addr(smem_addr(&ms.v_full[st]), 0));
       } else {  // seen in part: the values' warps of this CTA first
         elect_expect(smem_addr(&ms.v_here[st]), kVBytes);
         load_here(v_ring + st * kVBytes, maps.v, 64 * (int)rank, h, z, smem_addr(&ms.v_here[st]));
@@ -355,7 +364,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         any = true;
       }
       if (any) fence_async_smem();
-      warp_arrive_pair(peer_addr(smem_addr(&ms.fix_done[st]), lead));
+      warp_arrive_pair(peer_addr(smem_addr(&ms.fix_done[st]), 0));
     }
   }
   if (!ok && lane == 0 && a.status) atomicOr(a.status, RQ_STATUS_TIMEOUT);
@@ -369,15 +378,16 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
   }
   cluster_sync();  // the peer is done with this CTA's operands, and its values' warps have left what they found
 
-  // ---- write the rows, or join the parts ----
-  T* const out = reinterpret_cast<T*>(a.out) + ((size_t)q0 * a.q.heads + h) * kDim;
+  // ---- write the rows, or the part of them ----
   if (warp < kSoftWarps && !aborted) {
-    const float empty = qpos >= 0 ? CUDART_NAN_F : 0.f;  // a row whose scores are all minus infinity; one that sees nothing
-    const float inv = splits == 1 ? 1.f / l_run : 1.f;
+    // a row whose scores are all minus infinity; one that sees nothing
+    const float empty = !is_part && qpos >= 0 ? CUDART_NAN_F : 0.f, inv = is_part ? 1.f : 1.f / l_run;
     // what the values' warps found: dims 64 r .. of the pair's CTA r
     int odd[2];
-    for (int r = 0; r < 2; ++r) odd[r] = __float_as_int(peer_ld(peer_addr(smem_addr(&ms.any), lead + r)));
-    auto first_of = [&](int kind, int d) { return __float_as_int(peer_ld(peer_addr(smem_addr(&ms.from[kind][d & 63]), lead + (d >> 6)))); };
+    for (int r = 0; r < 2; ++r) odd[r] = __float_as_int(peer_ld(peer_addr(smem_addr(&ms.any), r)));
+    auto first_of = [&](int kind, int d) { return __float_as_int(peer_ld(peer_addr(smem_addr(&ms.from[kind][d & 63]), d >> 6))); };
+    float* const slot = a.ws + (size_t)part_id * kSlotFloats;
+    T* const out = reinterpret_cast<T*>(a.out) + (((size_t)q0 + row) * heads + h) * kDim;
 #pragma unroll 2
     for (int c = 0; c < kDim / 16; ++c) {
       float y[16];
@@ -387,11 +397,12 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         tmem_wait_ld();
         settle<16>(y);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) y[i] = l_run == 0.f ? (splits == 1 ? empty : 0.f) : y[i] * inv;
+        for (int i = 0; i < 16; ++i) y[i] = l_run == 0.f ? empty : y[i] * inv;
       } else {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) y[i] = 0.f;
+        for (int i = 0; i < 16; ++i) y[i] = empty;
       }
+      if (!valid) continue;
       if (odd[c >> 2]) {
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
@@ -400,50 +411,22 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
           if (first_of(2, 16 * c + i) <= qpos) y[i] = CUDART_NAN_F;
         }
       }
-      if (splits > 1) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          reinterpret_cast<float4*>(smem)[(4 * c + i) * kRows + kHalf * blk + brow] =
-              make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
-      } else if (valid) {
-        uint4* const dst = reinterpret_cast<uint4*>(out + (size_t)row * a.q.heads * kDim) + 2 * c;
+      if (!is_part) {
+        uint4* const dst = reinterpret_cast<uint4*>(out) + 2 * c;
 #pragma unroll
         for (int i = 0; i < 2; ++i)
           dst[i] = make_uint4(rope::pack2<T>(y[8 * i], y[8 * i + 1]), rope::pack2<T>(y[8 * i + 2], y[8 * i + 3]),
                               rope::pack2<T>(y[8 * i + 4], y[8 * i + 5]), rope::pack2<T>(y[8 * i + 6], y[8 * i + 7]));
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          reinterpret_cast<float4*>(slot)[(4 * c + i) * kUnitRows + (row - r0)] =
+              make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
       }
     }
-    if (splits > 1) {
-      float* const ml = reinterpret_cast<float*>(smem + kOffML);
-      ml[kHalf * blk + brow] = m_run;
-      ml[kRows + kHalf * blk + brow] = l_run;
-    }
-  }
-  if (splits > 1) {
-    cluster_sync();
-    // rows `per` of this part's share; a warp takes a row at a time, a lane four dims
-    const int per = kRows / splits;
-    for (int i = warp; i < per && !aborted; i += kThreads / 32) {
-      const int rr = part * per + i, at = r0 + kRows * (rr / kHalf) + kHalf * (int)rank + rr % kHalf;
-      if (at >= nq) continue;
-      float m = kNone, sum = 0.f;
-      float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int f = 0; f < splits; ++f) {
-        const float mf = peer_ld(peer_addr(base + kOffML + 4 * rr, 2 * f + rank)),
-                    lf = peer_ld(peer_addr(base + kOffML + 4 * (kRows + rr), 2 * f + rank));
-        const float4 v = peer_ld4(peer_addr(base + (uint32_t)(lane * kRows + rr) * 16, 2 * f + rank));
-        const float to = fmaxf(m, mf), wa = ex2(m - to), w = ex2(mf - to);
-        m = to;
-        sum = fmaf(sum, wa, lf * w);
-        y.x = fmaf(y.x, wa, v.x * w), y.y = fmaf(y.y, wa, v.y * w), y.z = fmaf(y.z, wa, v.z * w), y.w = fmaf(y.w, wa, v.w * w);
-      }
-      const float none = ahead + at >= 0 ? CUDART_NAN_F : 0.f, inv = 1.f / sum;
-      if (sum == 0.f)
-        y = make_float4(none, none, none, none);
-      else
-        y = make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv);
-      *reinterpret_cast<uint2*>(out + (size_t)at * a.q.heads * kDim + 4 * lane) =
-          make_uint2(rope::pack2<T>(y.x, y.y), rope::pack2<T>(y.z, y.w));
+    if (is_part && valid) {
+      slot[kUnitRows * kDim + (row - r0)] = m_run;
+      slot[kUnitRows * kDim + kUnitRows + (row - r0)] = l_run;
     }
   }
   fence_before_sync();
@@ -451,6 +434,36 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
   cluster_sync();  // a peer's shared memory is read until here
   fence_after_sync();
   if (warp == kMmaWarp) pair_tmem_dealloc(tmem, 512);
+}
+
+// Joins a unit's parts.  A CTA takes 8 rows, a thread 4 dims of one.
+template <typename T>
+__global__ void __launch_bounds__(256) prompt_join_kernel(const PromptArgs a, const Cut cut) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const uint32_t unit = (uint32_t)cut.whole + blockIdx.x, heads = (uint32_t)a.q.heads;
+  const int h = (int)(unit % heads), b = (int)(unit / heads % (uint32_t)a.B), turn = (int)(unit / heads / (uint32_t)a.B);
+  const int q0 = __ldg(a.q_offsets + b), q1 = __ldg(a.q_offsets + b + 1), k0 = __ldg(a.k_offsets + b), k1 = __ldg(a.k_offsets + b + 1);
+  if (q0 < 0 || q1 < q0 || q1 > a.nq || k0 < 0 || k1 < k0 || k1 > a.nk || q1 - q0 > a.max_new) return;
+  const int nq = q1 - q0, n_rb = (nq + kUnitRows - 1) / kUnitRows;
+  if (turn >= n_rb) return;
+  const int srow = 8 * (int)blockIdx.y + (threadIdx.x & 7), d4 = threadIdx.x >> 3, row = (n_rb - 1 - turn) * kUnitRows + srow;
+  if (row >= nq) return;
+  const float* s = a.ws + (size_t)blockIdx.x * cut.splits * kSlotFloats;
+  float m = kNone, l = 0.f;
+  float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int f = 0; f < cut.splits; ++f, s += kSlotFloats) {
+    const float mf = __ldcg(s + kUnitRows * kDim + srow), lf = __ldcg(s + kUnitRows * kDim + kUnitRows + srow);
+    const float4 v = __ldcg(reinterpret_cast<const float4*>(s) + d4 * kUnitRows + srow);
+    const float to = fmaxf(m, mf), wa = ex2(m - to), w = ex2(mf - to);
+    m = to;
+    l = fmaf(l, wa, lf * w);
+    y.x = fmaf(y.x, wa, v.x * w), y.y = fmaf(y.y, wa, v.y * w), y.z = fmaf(y.z, wa, v.z * w), y.w = fmaf(y.w, wa, v.w * w);
+  }
+  const float none = k1 - k0 - nq + row >= 0 ? CUDART_NAN_F : 0.f, inv = 1.f / l;
+  y = l == 0.f ? make_float4(none, none, none, none) : make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv);
+  *reinterpret_cast<uint2*>(reinterpret_cast<T*>(a.out) + (((size_t)q0 + row) * heads + h) * kDim + 4 * d4) =
+      make_uint2(rope::pack2<T>(y.x, y.y), rope::pack2<T>(y.z, y.w));
 }
 
 // Boxes of 64 dims and `box` rows of one head of x [n][heads][dims].
@@ -464,40 +477,74 @@ bool encode(CUtensorMap* map, bool bf16, const HeadsDev& x, int dims, int n, int
                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Which units are cut.  Units of one size (no more than 512 queries a sequence): the ones that would have the last round of
+// pairs to themselves, so that their parts fill it.  Units of several (causal over more rows): all, where they are fewer than
+// 4 pairs' worth, so that the longest does not outlast the rest.  At least 2 tiles a part, and a slot for each.
+Cut cut_of(const PromptArgs& a, long long units, int n_rb) {
+  const int pairs = a.num_sms / 2;
+  const double tiles = (double)a.nk / a.B / kTok + 1.0;
+  Cut c{n_rb, (int)units, 1};
+  if (units >= 6ll * pairs) return c;
+  long long cut = units % pairs, splits = cut > 0 ? pairs / cut : 1;
+  if (n_rb > 1) {
+    cut = units;
+    splits = units >= 4ll * pairs ? 1 : 4;
+  }
+  while (splits > 1 && (splits * 2.0 > tiles || cut * splits > (long long)kSlotsPerPair * pairs)) --splits;
+  if (splits > 1) c.whole = (int)(units - cut), c.splits = (int)splits;
+  return c;
+}
+
 template <typename T>
-cudaError_t launch(const Maps& maps, const PromptArgs& a, int splits, int n_rb, cudaStream_t stream) {
-  static_assert(sizeof(Maps) + sizeof(PromptArgs) + 16 <= 4096, "kernel parameters");
-  // the kernel's shared-memory limit, once a device (the attribute is set again on devices past the 64th)
+cudaError_t launch(const Maps& maps, const PromptArgs& a, int n_rb, cudaStream_t stream) {
+  static_assert(sizeof(Maps) + sizeof(PromptArgs) + 32 <= 4096, "kernel parameters");
+  // the kernel's shared-memory limit, once a device (at every call on those past the 64th)
   static std::atomic<unsigned long long> set{0};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
-  if (!(set.load(std::memory_order_relaxed) & bit) || bit == 0) {
+  if (!(set.load(std::memory_order_relaxed) & bit)) {
     e = cudaFuncSetAttribute(prompt_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
     set.fetch_or(bit, std::memory_order_relaxed);
   }
+  const long long units = (long long)a.B * n_rb * a.q.heads;
+  const Cut cut = cut_of(a, units, n_rb);
+  const long long n_cut = units - cut.whole, n_pairs = cut.whole + n_cut * cut.splits;
+  if (n_pairs > 0x3fffffffLL) return cudaErrorInvalidValue;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = 2;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(2 * a.q.heads * splits), (unsigned)a.B, (unsigned)n_rb);
+  cfg.gridDim = dim3(2u * (unsigned)n_pairs);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = kSmem;
   cfg.stream = stream;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = 2u * (unsigned)splits;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, prompt_kernel<T>, maps, a, splits);
+  e = cudaLaunchKernelEx(&cfg, prompt_kernel<T>, maps, a, cut);
+  if (e != cudaSuccess || n_cut == 0) return e;
+  cudaLaunchAttribute behind[1];
+  behind[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  behind[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t join = {};
+  join.gridDim = dim3((unsigned)n_cut, (unsigned)((a.max_new < kUnitRows ? a.max_new : kUnitRows) + 7) / 8);
+  join.blockDim = dim3(256);
+  join.stream = stream;
+  join.attrs = behind;
+  join.numAttrs = 1;
+  return cudaLaunchKernelEx(&join, prompt_join_kernel<T>, a, cut);
 }
 
 }  // namespace
 
-cudaError_t launch_prompt_attention(const PromptArgs& a, int num_sms, cudaStream_t stream) {
+size_t prompt_workspace(int num_sms) { return (size_t)kSlotsPerPair * (num_sms / 2) * kSlotFloats * sizeof(float); }
+
+cudaError_t launch_prompt_attention(const PromptArgs& a, cudaStream_t stream) {
   if (!tensor_map_encoder()) return cudaErrorNotSupported;
   const int n_rb = (a.max_new + kUnitRows - 1) / kUnitRows;
-  if (n_rb > 65535) return cudaErrorInvalidValue;
   Maps maps{};
   HeadsDev k = a.k, v = a.v, pe{a.k_pe, a.k_pe_stride, 0, 1};
   if (a.nk == 0) k = v = pe = a.q;  // no key is ever read
@@ -505,12 +552,7 @@ cudaError_t launch_prompt_attention(const PromptArgs& a, int num_sms, cudaStream
   if (!encode(&maps.q, a.bf16, a.q, kPromptDim, a.nq, kHalf) || !encode(&maps.k, a.bf16, k, kDim, nk, kTok / 2) ||
       !encode(&maps.pe, a.bf16, pe, kPositionDim, nk, kTok / 2) || !encode(&maps.v, a.bf16, v, kDim, nk, kTok))
     return cudaErrorInvalidValue;
-  // few units: the most parts (a power of two) that leave every SM at most one of them, and each some 4 tiles at the batch's
-  // mean length
-  const long long units = (long long)a.B * n_rb * a.q.heads, tiles = a.nk / a.B / kTok;
-  int splits = 1;
-  while (splits < kMaxSplit && units * 4 * splits <= num_sms && tiles >= 8 * splits) splits *= 2;
-  return a.bf16 ? launch<__nv_bfloat16>(maps, a, splits, n_rb, stream) : launch<__half>(maps, a, splits, n_rb, stream);
+  return a.bf16 ? launch<__nv_bfloat16>(maps, a, n_rb, stream) : launch<__half>(maps, a, n_rb, stream);
 }
 
 }  // namespace rq

@@ -34,7 +34,7 @@ EXPORTS = ["rq_create", "rq_free", "rq_page_bytes", "rq_lloyd_max_codebook", "rq
            "rq_decode_attention_noalloc", "rq_tree_verify_attention", "rq_decode_step", "rq_extend_attention", "rq_status_string",
            "rq_rope_create", "rq_rope_free", "rq_norm_rope", "rq_rope_append",
            "rq_latent_create", "rq_latent_free", "rq_latent_page_bytes", "rq_latent_append", "rq_latent_attention",
-           "rq_latent_read", "rq_prompt_attention"]
+           "rq_latent_read", "rq_prompt_workspace", "rq_prompt_attention"]
 
 
 class RQError(RuntimeError):
@@ -87,7 +87,7 @@ class rq_prompt(ctypes.Structure):
         ("q", rq_heads), ("k", rq_heads), ("v", rq_heads), ("k_pe", ctypes.c_void_p), ("k_pe_stride", ctypes.c_longlong),
         ("out", ctypes.c_void_p), ("q_offsets", ctypes.c_void_p), ("k_offsets", ctypes.c_void_p), ("B", ctypes.c_int),
         ("nq", ctypes.c_int), ("nk", ctypes.c_int), ("max_new", ctypes.c_int), ("sm_scale", ctypes.c_float),
-        ("io_type", ctypes.c_int),
+        ("io_type", ctypes.c_int), ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
     ]
 
 
@@ -161,6 +161,8 @@ def lib(path: str | None = None) -> ctypes.CDLL:
             L.rq_latent_attention.restype = ci
             L.rq_latent_read.argtypes = [vp, vp, vp, ci, vp, vp, ci, ci, vp, vp, vp, vp]
             L.rq_latent_read.restype = ci
+            L.rq_prompt_workspace.argtypes = [ci]
+            L.rq_prompt_workspace.restype = ctypes.c_size_t
             L.rq_prompt_attention.argtypes = [ctypes.POINTER(rq_prompt), vp, vp]
             L.rq_prompt_attention.restype = ci
             L.rq_status_string.argtypes = [ctypes.c_int]
@@ -499,11 +501,19 @@ def rq_latent_read(ctx, pages, block_table, starts, offsets, c, k_pe, status=Non
     return c, k_pe
 
 
-def rq_prompt_attention(q, k, k_pe, v, q_offsets, k_offsets, max_new, out, sm_scale=0.0, status=None, stream=None):
-    """The low-level call; shapes and types are checked by prompt_attention."""
+_prompt_bytes: dict = {}  # by device
+
+
+def rq_prompt_workspace(device: int = -1) -> int:
+    return int(lib().rq_prompt_workspace(device))
+
+
+def rq_prompt_attention(q, k, k_pe, v, q_offsets, k_offsets, max_new, out, workspace, sm_scale=0.0, status=None, stream=None):
+    """The low-level call; shapes and types are checked by prompt_attention.  workspace: a uint8 tensor of rq_prompt_workspace
+    bytes."""
     args = rq_prompt(_heads(q), _heads(k), _heads(v), k_pe.data_ptr(), k_pe.stride(0), out.data_ptr(), q_offsets.data_ptr(),
-                     k_offsets.data_ptr(), q_offsets.numel() - 1, q.shape[0], k.shape[0], max_new, float(sm_scale),
-                     _IO_TYPES[q.dtype])
+                     k_offsets.data_ptr(), q_offsets.shape[0] - 1, q.shape[0], k.shape[0], max_new, float(sm_scale),
+                     _IO_TYPES[q.dtype], workspace.data_ptr(), workspace.numel())
     _check("rq_prompt_attention", lib().rq_prompt_attention(args, _ptr(status), _stream(stream, q.device)))
     return out
 
@@ -874,7 +884,15 @@ def prompt_attention(q, k, k_pe, v, q_offsets, k_offsets, max_new, sm_scale=0.0,
         out = torch.empty((nq, heads, 128), dtype=dtype, device=q.device)
     elif not _rows_ok(out, (nq, heads, 128), dtype, index) or not out.is_contiguous():
         raise RQError(name, RQ_ERR_INVALID)
+    nbytes = _prompt_bytes.get(index)
+    if nbytes is None:
+        nbytes = _prompt_bytes[index] = rq_prompt_workspace(index)
+    workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
     if index != torch.cuda.current_device():
         with torch.cuda.device(index):
-            return rq_prompt_attention(q, k, k_pe, v, q_offsets, k_offsets, max_new, out, sm_scale, status, stream)
-    return rq_prompt_attention(q, k, k_pe, v, q_offsets, k_offsets, max_new, out, sm_scale, status, stream)
+            rq_prompt_attention(q, k, k_pe, v, q_offsets, k_offsets, max_new, out, workspace, sm_scale, status, stream)
+    else:
+        rq_prompt_attention(q, k, k_pe, v, q_offsets, k_offsets, max_new, out, workspace, sm_scale, status, stream)
+    if stream is not None:  # not the current one: the workspace stays its own until the call is through there
+        workspace.record_stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream)))
+    return out

@@ -60,7 +60,8 @@ def test_null_calls():
 def prompt(**over):
     heads = lambda at, dims, h=4: dict(x=at, stride=h * dims, head_stride=dims, heads=h)  # noqa: E731
     base = dict(q=heads(0x10000, 192), k=heads(0x20000, 128), v=heads(0x30000, 128), k_pe=0x40000, k_pe_stride=64, out=0x50000,
-                q_offsets=0x60000, k_offsets=0x60100, B=2, nq=8, nk=8, max_new=8, sm_scale=0.0, io_type=0)
+                q_offsets=0x60000, k_offsets=0x60100, B=2, nq=8, nk=8, max_new=8, sm_scale=0.0, io_type=0,
+                workspace=0x100000, workspace_bytes=1 << 30)
     for key, value in over.items():
         base[key] = dict(base[key], **value) if isinstance(value, dict) else value
     args = rq.rq_prompt()
@@ -75,7 +76,7 @@ def prompt(**over):
     dict(k=dict(x=0x20002)), dict(v=dict(stride=4)), dict(v=dict(x=None)), dict(k_pe=None), dict(k_pe=0x40004),
     dict(k_pe_stride=60), dict(k_pe_stride=56), dict(out=None), dict(out=0x50008), dict(q_offsets=None), dict(k_offsets=None),
     dict(B=-1), dict(B=65536), dict(nq=-1), dict(nk=-1), dict(max_new=-1), dict(sm_scale=-1.0), dict(sm_scale=float("nan")),
-    dict(io_type=3),
+    dict(io_type=3), dict(workspace=None), dict(workspace=0x100004),
 ], ids=str)
 def test_prompt_refuses(over):
     assert rq.lib().rq_prompt_attention(ctypes.byref(prompt(**over)), None, None) == rq.RQ_ERR_INVALID
