@@ -579,11 +579,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t u = 5u * t_base, sl = 9u * t_base;
         auto unit_full = [&](uint32_t v) -> uint64_t& { return ms.full[v % kUnits]; };
         uint32_t look = warp_look(unit_full(u), u / kUnits);
-        auto take = [&]() {  // unit u is full; the next one is looked at
-          ok = warp_wait_after(look, unit_full(u), u / kUnits, abort_flag);
-          if (ok) look = warp_look(unit_full(u + 1), (u + 1) / kUnits);
-          return ok;
-        };
+        auto take = [&]() { return ok = warp_wait_after(look, unit_full(u), u / kUnits, abort_flag); };  // unit u is full
+        auto peek = [&]() { look = warp_look(unit_full(u + 1), (u + 1) / kUnits); };  // late in unit u, so that the look finds what there is
         uint32_t p_look = 0;
         auto give = [&]() {
           pair_commit(smem_addr(&ms.empty[u % kUnits]), 3);
@@ -599,13 +596,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             if ((c & 1) == 0 && !take()) return;
             const uint32_t b_at = slot(), a_at = q_lo + 512 * c;
 #pragma unroll
-            for (int p = 0; p < NP; ++p)
+            for (int p = 0; p < NP; ++p) {
+              if (p + 1 == NP && (c & 1)) peek();
 #pragma unroll
               for (int ks = 0; ks < 4; ++ks)
                 pair_mma_f8(d, a_at + (p * S::kPieceQ + 32 * ks) / 16, b_at + 2 * ks, id_s, p > 0 || ks > 0 ? 1u : (uint32_t)c);
+            }
             if (c & 1) give();
           }
           if (!take()) return;
+          peek();
           if (t > 0) p_look = warp_look(ms.p_full, t_base + t - 1);
           const uint32_t b_at = slot();
 #pragma unroll
@@ -634,13 +634,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             const uint32_t b_at = slot(), w_at = w_lo + (g >> 1) * 512 + (g & 1) * 4;
 #pragma unroll
-            for (int ks = 0; ks < 2; ++ks)
+            for (int ks = 0; ks < 2; ++ks) {
+              if (ks == 1 && (g & 1)) peek();
 #pragma unroll
               for (int h = 0; h < 2; ++h)
 #pragma unroll
                 for (int p = 0; p < NP; ++p)
                   pair_mma_f8(tmem + 128 * h, w_at + (p * S::kPieceP + 32 * ks) / 16, b_at + (8192 * h + 4096 * ks) / 16,
                               p == 0 ? id_o5 : id_o4, ks > 0 || p > 0 ? 1u : (uint32_t)(t + g));
+            }
             if (g & 1) give();
           }
           if (!ok) break;
