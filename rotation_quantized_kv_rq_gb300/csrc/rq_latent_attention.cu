@@ -45,7 +45,8 @@ using namespace latent;
 using namespace tc;
 
 constexpr int kSoftWarps = 8, kMmaWarp = 8, kCopyWarp = 9, kScaleWarp = 10, kTailWarp = 11, kThreads = 384;
-constexpr int kRows = 64, kUnitRows = 128, kTok = 256;  // rows of a CTA, of a pair; tokens of a tile
+constexpr int kMmaRows = 128, kTok = 256;  // rows of a pair's MMAs, tokens of a tile
+constexpr int kUnitRows = 128;             // the most rows of a unit
 constexpr uint32_t kSlotBytes = 16384;
 // Slots are filled and given back in units of two or one: a tile's keys are three units (dims 0 .. 255, 256 .. 511, the
 // position parts), its values two (128 tokens each).  A wait or a commit costs the issuing warp about as much as three MMAs.
@@ -58,13 +59,17 @@ constexpr float kNone = -3.402823466e38f;  // m before any visible token
 // floats of a fragment's slot: 128 rows x 512 (as [dim / 4][row][4]), then the rows' m and l
 constexpr size_t kSlotFloats = (size_t)kUnitRows * kLatentDim + 2 * kUnitRows;
 
-template <typename T>
+// A CTA has 64 rows of an MMA.  Where a unit has no more than 64 rows in all (RC = 32 to a CTA) operands are kept for 32: an MMA
+// finds whatever follows in the place of the rest, rows whose results nobody reads, and the ring has 10 or 8 slots, more than
+// a tile or nearly, instead of 7 or 4.
+template <typename T, int RC>
 struct Shape {
   static constexpr int kPieces = std::is_same<T, __half>::value ? 3 : 2;
-  static constexpr int kSlots = kPieces == 3 ? 4 : 7;
-  static constexpr uint32_t kPieceQ = 32768, kQBytes = kPieces * kPieceQ + 8192;  // [piece][4 chunks of 128 dims][64 rows], position parts
-  static constexpr uint32_t kPieceP = 16384, kPBytes = kPieces * kPieceP;         // [piece][2 halves of 128 tokens][64 rows]
-  static constexpr uint32_t kOffP = kQBytes, kOffRing = kOffP + kPBytes, kOffMisc = kOffRing + kSlots * kSlotBytes;
+  static constexpr uint32_t kRowsBytes = RC * 128;  // a chunk of 128 dims, or of 128 tokens' weights
+  static constexpr uint32_t kPieceQ = 4 * kRowsBytes, kQBytes = kPieces * kPieceQ + kRowsBytes;  // [piece][4 chunks][RC rows], position parts
+  static constexpr uint32_t kPieceP = 2 * kRowsBytes, kPBytes = kPieces * kPieceP;               // [piece][2 halves of 128 tokens][RC rows]
+  static constexpr uint32_t kOffMisc = 221184, kOffP = kQBytes, kOffRing = kOffP + kPBytes;
+  static constexpr int kSlots = (kOffMisc - kOffRing) / kSlotBytes;
 };
 
 struct Frag {           // tiles r0 .. r0 + n - 1 of one unit
@@ -82,16 +87,16 @@ struct Misc {
   uint32_t tmem;
   int abort;
   alignas(16) float ks[2][kTok], ev[2][kTok], dn[2][kTok];  // 2^E (or NaN), E, 2^-E of a tile's tokens
-  float top[2][4][kRows];
-  float q_scale[kRows];
+  float top[2][4][64];
+  float q_scale[64];
 };
-static_assert(Shape<__half>::kOffMisc + sizeof(Misc) + 1024 <= 232448, "one CTA's shared memory");
-static_assert(Shape<__nv_bfloat16>::kOffMisc + sizeof(Misc) + 1024 <= 232448, "one CTA's shared memory");
+constexpr int kSmem = (int)(Shape<__half, 64>::kOffMisc + sizeof(Misc)) + 1024;
+static_assert(kSmem + 128 <= 232448, "one CTA's shared memory");
 
 struct Unit {
   int len, end, tiles;
 };
-__device__ __forceinline__ Unit unit_of(const LatentAttnArgs& a, int cap, int b, int rt, bool report) {
+__device__ __forceinline__ Unit unit_of(const LatentAttnArgs& a, int unit_rows, int cap, int b, int rt, bool report) {
   Unit u;
   u.len = __ldg(a.seq_lens + b);
   if (u.len < 0 || u.len > cap || (u.len > 0 && u.len < a.T)) {
@@ -99,7 +104,7 @@ __device__ __forceinline__ Unit unit_of(const LatentAttnArgs& a, int cap, int b,
     u.len = u.len < 0 ? 0 : min(u.len, cap);
   }
   const long long rows = (long long)a.T * a.heads;
-  const int last = (int)((uint32_t)(min(rows, (rt + 1ll) * kUnitRows) - 1) / (uint32_t)a.heads);  // the last row's token (rows: below 2^30)
+  const int last = (int)((uint32_t)(min(rows, (rt + 1ll) * unit_rows) - 1) / (uint32_t)a.heads);  // the last row's token (rows: below 2^30)
   u.end = a.tree_mask ? u.len : max(0, min(u.len, u.len - a.T + last + 1));
   u.tiles = max(1, (u.end + kTok - 1) / kTok);  // rows that see nothing are written too
   return u;
@@ -186,10 +191,11 @@ __device__ __forceinline__ int query_exp(uint32_t top_c, uint32_t top_p) {
   return min(max(max(c, p), -100), 100);
 }
 
-template <typename T>
+template <typename T, int RC>
 __global__ void __launch_bounds__(kThreads, 1)
     latent_kernel(const __grid_constant__ CUtensorMap map, const LatentPool pool, const LatentAttnArgs a, int box, int4* info) {
-  using S = Shape<T>;
+  using S = Shape<T, RC>;
+  constexpr int kUR = 2 * RC;  // rows of a unit
   constexpr int NP = S::kPieces, kSlots = S::kSlots;
   constexpr bool kF16 = std::is_same<T, __half>::value;
   extern __shared__ uint8_t smem_raw[];
@@ -201,7 +207,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t rank = cluster_rank();
   const int P = pool.page_size, cap = a.max_pages * P;
   const long long n_rows = (long long)a.T * a.heads;
-  const int n_rt = (int)((n_rows + kUnitRows - 1) / kUnitRows);
+  const int n_rt = (int)((n_rows + kUR - 1) / kUR);
 
   if (tid == 32 * kMmaWarp) {
     for (int i = 0; i < kUnits; ++i) {
@@ -231,7 +237,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t n_items = (uint32_t)a.B * n_rt, chunk = (n_items + kThreads - 1) / kThreads;
     uint32_t mine = 0;
     for (uint32_t i = tid * chunk; i < min(n_items, (tid + 1) * chunk); ++i)
-      mine += unit_of(a, cap, (int)(i / (uint32_t)n_rt), (int)(i % (uint32_t)n_rt), blockIdx.x == 0).tiles;
+      mine += unit_of(a, kUR, cap, (int)(i / (uint32_t)n_rt), (int)(i % (uint32_t)n_rt), blockIdx.x == 0).tiles;
     uint32_t sum = mine;  // inclusive, over the warp, then over the warps before
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -256,7 +262,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (x >= before && x < before + mine) {
       uint32_t p = before, i = tid * chunk;
       for (;; ++i) {
-        const uint32_t n = unit_of(a, cap, (int)(i / (uint32_t)n_rt), (int)(i % (uint32_t)n_rt), false).tiles;
+        const uint32_t n = unit_of(a, kUR, cap, (int)(i / (uint32_t)n_rt), (int)(i % (uint32_t)n_rt), false).tiles;
         if (x < p + n) break;
         p += n;
       }
@@ -292,7 +298,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!f.done) {
         f.b = (int)(item / (uint32_t)n_rt);
         f.rt = (int)(item % (uint32_t)n_rt);
-        const Unit un = unit_of(a, cap, f.b, f.rt, false);
+        const Unit un = unit_of(a, kUR, cap, f.b, f.rt, false);
         f.len = un.len;
         f.end = un.end;
         f.r0 = (int)(x - at);
@@ -319,8 +325,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tmem = *(volatile uint32_t*)&ms.tmem;
     const int b = ms.f.b, r0 = ms.f.r0, len = ms.f.len, end = ms.f.end;
     const int n = end > 0 ? ms.f.n : 0;  // tiles with tokens
-    const long long urow = (long long)ms.f.rt * kUnitRows + kRows * (int)rank + row;  // the thread's query row
-    const bool valid = urow < n_rows;
+    const long long urow = (long long)ms.f.rt * kUR + RC * (int)rank + row;  // the thread's query row
+    const bool valid = row < RC && urow < n_rows;
     const int j = valid ? (int)((uint32_t)urow / (uint32_t)a.heads) : 0, head = valid ? (int)((uint32_t)urow % (uint32_t)a.heads) : 0;
     const uint32_t t_base = done_tiles;
     float m_run = kNone, l_run = 0.f;
@@ -328,12 +334,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (warp < kSoftWarps) {
       float q_scale = 0.f;
-      if (n > 0) {
+      if (n > 0 && 8 * warp < RC) {
         // ---- queries as pieces: eight rows to a warp, a lane 16 dims and an eighth of a position part of every fourth row ----
         // lane l: where row l % 8 of the warp's stands, -1 past the last row
         long long c_at = -1, pe_at = -1;
         {
-          const long long u = (long long)ms.f.rt * kUnitRows + kRows * (int)rank + 8 * warp + (lane & 7);
+          const long long u = (long long)ms.f.rt * kUR + RC * (int)rank + 8 * warp + (lane & 7);
           if (u < n_rows) {
             const uint32_t jj = (uint32_t)u / (uint32_t)a.heads, hh = (uint32_t)u - jj * (uint32_t)a.heads;
             const long long token = (long long)b * a.T + jj;
@@ -370,7 +376,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int o = 1; o < 8; o <<= 1) top_p = max(top_p, __shfl_xor_sync(0xffffffffu, top_p, o));
           float pe_down = 0.f;
-#pragma unroll 1
+#pragma unroll
           for (int r = 0; r < 4; ++r) {
             const uint32_t top_c = __reduce_max_sync(0xffffffffu, max(largest(raw[0][0]), largest(raw[0][1])));
             const uint32_t top_r = __shfl_sync(0xffffffffu, top_p, 8 * r);
@@ -408,7 +414,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
 #pragma unroll
             for (int p = 0; p < NP; ++p)
-              sts128(q_ops + p * S::kPieceQ + 8192 * (lane >> 3) + sw128(row0 + r, lane & 7), piece[p][0], piece[p][1], piece[p][2], piece[p][3]);
+              sts128(q_ops + p * S::kPieceQ + S::kRowsBytes * (lane >> 3) + sw128(row0 + r, lane & 7), piece[p][0], piece[p][1], piece[p][2], piece[p][3]);
 #pragma unroll
             for (int i = 0; i < 7; ++i) raw[i][0] = raw[i + 1][0], raw[i][1] = raw[i + 1][1];  // (one row's code, not eight)
           }
@@ -422,9 +428,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           sts128(q_ops + NP * S::kPieceQ + sw128(row0 + (lane >> 3), lane & 7), w[0], w[1], w[2], w[3]);
         }
         fence_async_smem();
+      }
+      if (n > 0) {
         warp_arrive_pair(peer_addr(smem_addr(&ms.q_full), 0));
         soft_sync();  // the rows' scales are there
-        q_scale = ms.q_scale[row];
+        if (row < RC) q_scale = ms.q_scale[row];
       }
       // ================= softmax =================
       // Scores 16 columns at a time, twice: loops over them and not 64 columns in a row, so that the roles' code fits the
@@ -553,7 +561,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
 #pragma unroll
             for (int p = 0; p < NP; ++p)
-              sts128(p_ops + p * S::kPieceP + 8192 * tok_half + sw128(row, 4 * col_half + (c >> 4)), piece[p][0], piece[p][1], piece[p][2],
+              sts128(p_ops + p * S::kPieceP + S::kRowsBytes * tok_half + sw128(row, 4 * col_half + (c >> 4)), piece[p][0], piece[p][1], piece[p][2],
                      piece[p][3]);
           }
           float y[4];
@@ -571,9 +579,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == kMmaWarp) {
       // ================= MMA issue: the leader's =================
       if (rank == 0 && n > 0) {
-        constexpr uint32_t id_s = idesc_f8(kUnitRows, kTok, 0, 0), id_o5 = idesc_f8(kUnitRows, 256, 1, 1), id_o4 = idesc_f8(kUnitRows, 256, 0, 1);
+        constexpr uint32_t id_s = idesc_f8(kMmaRows, kTok, 0, 0), id_o5 = idesc_f8(kMmaRows, 256, 1, 1), id_o4 = idesc_f8(kMmaRows, 256, 0, 1);
         constexpr uint32_t type = std::is_same<T, __half>::value ? 0u : 1u;
-        constexpr uint32_t id_p = idesc_f16(kUnitRows, kTok) | type << 7 | type << 10;
+        constexpr uint32_t id_p = idesc_f16(kMmaRows, kTok) | type << 7 | type << 10;
         bool issued = false;
         // units and slots in the order of use: K(0) | K(1) V(0) | K(2) V(1) | ...
         uint32_t u = 5u * t_base, sl = 9u * t_base;
@@ -594,7 +602,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
           for (int c = 0; c < 4; ++c) {
             if ((c & 1) == 0 && !take()) return;
-            const uint32_t b_at = slot(), a_at = q_lo + 512 * c;
+            const uint32_t b_at = slot(), a_at = q_lo + S::kRowsBytes / 16 * c;
 #pragma unroll
             for (int p = 0; p < NP; ++p) {
               if (p + 1 == NP && (c & 1)) peek();
@@ -632,7 +640,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tails ^= 1u << (u % kUnits);
               }
             }
-            const uint32_t b_at = slot(), w_at = w_lo + (g >> 1) * 512 + (g & 1) * 4;
+            const uint32_t b_at = slot(), w_at = w_lo + (g >> 1) * (S::kRowsBytes / 16) + (g & 1) * 4;
 #pragma unroll
             for (int ks = 0; ks < 2; ++ks) {
               if (ks == 1 && (g & 1)) peek();
@@ -807,7 +815,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int sees = valid ? (a.tree_mask ? len - a.T - 1 : len - a.T + j) : -1;
       // a row that sees nothing is zero; one whose scores are all minus infinity is NaN
       const float empty = whole && sees >= 0 ? CUDART_NAN_F : 0.f, inv = whole ? 1.f / l : 1.f;
-      const int srow = kRows * (int)rank + row, dim0 = 256 * tok_half + 128 * col_half;
+      const int srow = RC * (int)rank + row, dim0 = 256 * tok_half + 128 * col_half;
       float* const slot = a.ws + (2ll * me + ((int)me == ms.f.range ? ms.f.range_last : 0)) * kSlotFloats;
       T* const out = reinterpret_cast<T*>(a.out) + (((size_t)b * a.T + j) * a.heads + head) * kLatentDim + dim0;
 #pragma unroll 2
@@ -831,13 +839,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else {
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            reinterpret_cast<float4*>(slot)[(dim0 / 4 + 4 * c + i) * kUnitRows + srow] =
+            reinterpret_cast<float4*>(slot)[(dim0 / 4 + 4 * c + i) * kUR + srow] =
                 make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
         }
       }
-      if (!whole && quarter == 0) {
-        slot[kUnitRows * kLatentDim + srow] = m_run;
-        slot[kUnitRows * kLatentDim + kUnitRows + srow] = l;
+      if (!whole && quarter == 0 && valid) {
+        slot[kUR * kLatentDim + srow] = m_run;
+        slot[kUR * kLatentDim + kUR + srow] = l;
       }
     }
     fence_before_sync();
@@ -857,7 +865,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // Joins the parts of units that span ranges.  A CTA takes 8 rows and 32 / G groups of 4 dims of a unit, its parts in G shares.
 template <typename T, int G>
-__global__ void __launch_bounds__(256) latent_join_kernel(const LatentAttnArgs a, const int4* info, int row_groups) {
+__global__ void __launch_bounds__(256) latent_join_kernel(const LatentAttnArgs a, const int4* info, int row_groups, int unit_rows) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   __shared__ float part[G][32 / G][8][6];
   const int tid = threadIdx.x, r8 = tid & 7, d = (tid >> 3) % (32 / G), share = (tid >> 3) / (32 / G);
@@ -865,9 +873,9 @@ __global__ void __launch_bounds__(256) latent_join_kernel(const LatentAttnArgs a
   const int4 u = __ldg(info + unit);
   if (u.y == 0) return;
   const long long n_rows = (long long)a.T * a.heads;
-  const int n_rt = (int)((n_rows + kUnitRows - 1) / kUnitRows), b = (int)(unit / n_rt), rt = (int)(unit % n_rt);
+  const int n_rt = (int)((n_rows + unit_rows - 1) / unit_rows), b = (int)(unit / n_rt), rt = (int)(unit % n_rt);
   const int srow = 8 * (int)(blockIdx.x % row_groups) + r8, d4 = blockIdx.y * (32 / G) + d;
-  const long long urow = (long long)rt * kUnitRows + srow;
+  const long long urow = (long long)rt * unit_rows + srow;
   const bool valid = urow < n_rows;
   float m = kNone, l = 0.f;
   float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -875,8 +883,8 @@ __global__ void __launch_bounds__(256) latent_join_kernel(const LatentAttnArgs a
 #pragma unroll 4
     for (int f = share; f < u.y; f += G) {
       const float* s = a.ws + (2ll * (u.x + f) + (f == 0 ? u.z : 0)) * kSlotFloats;
-      const float mf = __ldcg(s + kUnitRows * kLatentDim + srow), lf = __ldcg(s + kUnitRows * kLatentDim + kUnitRows + srow);
-      const float4 v = __ldcg(reinterpret_cast<const float4*>(s) + d4 * kUnitRows + srow);
+      const float mf = __ldcg(s + unit_rows * kLatentDim + srow), lf = __ldcg(s + unit_rows * kLatentDim + unit_rows + srow);
+      const float4 v = __ldcg(reinterpret_cast<const float4*>(s) + d4 * unit_rows + srow);
       const float to = fmaxf(m, mf), wa = ex2(m - to), w = ex2(mf - to);
       m = to;
       l = fmaf(l, wa, lf * w);
@@ -905,7 +913,7 @@ __global__ void __launch_bounds__(256) latent_join_kernel(const LatentAttnArgs a
   *reinterpret_cast<uint2*>(out) = make_uint2(rope::pack2<T>(y.x, y.y), rope::pack2<T>(y.z, y.w));
 }
 
-template <typename T>
+template <typename T, int RC>
 cudaError_t launch(const CUtensorMap& map, const LatentPool& pool, const LatentAttnArgs& a, int box, int num_sms, int4* info, long long units,
                    cudaStream_t stream) {
   const int pairs = num_sms / 2;
@@ -916,14 +924,14 @@ cudaError_t launch(const CUtensorMap& map, const LatentPool& pool, const LatentA
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2u * (unsigned)pairs);
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = Shape<T>::kOffMisc + sizeof(Misc) + 1024;
+  cfg.dynamicSmemBytes = kSmem;
   cfg.stream = stream;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, latent_kernel<T>, map, pool, a, box, info);
+  cudaError_t e = cudaLaunchKernelEx(&cfg, latent_kernel<T, RC>, map, pool, a, box, info);
   if (e != cudaSuccess) return e;
   const long long rows = (long long)a.T * a.heads;
-  const int row_groups = (int)((rows < kUnitRows ? rows : kUnitRows) + 7) / 8;
+  const int row_groups = (int)((rows < 2 * RC ? rows : 2 * RC) + 7) / 8;
   if (units * row_groups > 0x7fffffffLL) return cudaErrorInvalidValue;
   const bool many = units * 8 <= pairs;  // eight parts a unit or more
   cudaLaunchAttribute behind[1];
@@ -935,8 +943,8 @@ cudaError_t launch(const CUtensorMap& map, const LatentPool& pool, const LatentA
   join.stream = stream;
   join.attrs = behind;
   join.numAttrs = 1;
-  return many ? cudaLaunchKernelEx(&join, latent_join_kernel<T, 8>, a, (const int4*)info, row_groups)
-              : cudaLaunchKernelEx(&join, latent_join_kernel<T, 1>, a, (const int4*)info, row_groups);
+  return many ? cudaLaunchKernelEx(&join, latent_join_kernel<T, 8>, a, (const int4*)info, row_groups, 2 * RC)
+              : cudaLaunchKernelEx(&join, latent_join_kernel<T, 1>, a, (const int4*)info, row_groups, 2 * RC);
 }
 
 }  // namespace
@@ -947,9 +955,10 @@ size_t latent_attention_workspace(int num_sms, long long rows, int max_batch) {
 }
 
 cudaError_t latent_attention_prepare() {
-  const int h = Shape<__half>::kOffMisc + sizeof(Misc) + 1024, b = Shape<__nv_bfloat16>::kOffMisc + sizeof(Misc) + 1024;
-  cudaError_t e = cudaFuncSetAttribute(latent_kernel<__half>, cudaFuncAttributeMaxDynamicSharedMemorySize, h);
-  if (e == cudaSuccess) e = cudaFuncSetAttribute(latent_kernel<__nv_bfloat16>, cudaFuncAttributeMaxDynamicSharedMemorySize, b);
+  cudaError_t e = cudaFuncSetAttribute(latent_kernel<__half, 32>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(latent_kernel<__half, 64>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(latent_kernel<__nv_bfloat16, 32>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(latent_kernel<__nv_bfloat16, 64>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   return e;
 }
 
@@ -966,8 +975,12 @@ cudaError_t launch_latent_attention(const LatentPool& pool, const LatentAttnArgs
                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
     return cudaErrorInvalidValue;
   int4* const info = reinterpret_cast<int4*>(a.ws + 2 * (size_t)(num_sms / 2) * kSlotFloats);
-  return pool.bf16 ? launch<__nv_bfloat16>(map, pool, a, box, num_sms, info, units, stream)
-                   : launch<__half>(map, pool, a, box, num_sms, info, units, stream);
+  const bool few = (long long)a.T * a.heads <= 64;
+  if (pool.bf16)
+    return few ? launch<__nv_bfloat16, 32>(map, pool, a, box, num_sms, info, units, stream)
+               : launch<__nv_bfloat16, 64>(map, pool, a, box, num_sms, info, units, stream);
+  return few ? launch<__half, 32>(map, pool, a, box, num_sms, info, units, stream)
+             : launch<__half, 64>(map, pool, a, box, num_sms, info, units, stream);
 }
 
 }  // namespace rq
