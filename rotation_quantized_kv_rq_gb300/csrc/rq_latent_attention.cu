@@ -870,7 +870,7 @@ __global__ void __launch_bounds__(256) latent_join_kernel(const LatentAttnArgs a
   __shared__ float part[G][32 / G][8][6];
   const int tid = threadIdx.x, r8 = tid & 7, d = (tid >> 3) % (32 / G), share = (tid >> 3) / (32 / G);
   const long long unit = blockIdx.x / row_groups;
-  const int4 u = __ldg(info + unit);
+  const int4 u = __ldcg(info + unit);
   if (u.y == 0) return;
   const long long n_rows = (long long)a.T * a.heads;
   const int n_rt = (int)((n_rows + unit_rows - 1) / unit_rows), b = (int)(unit / n_rt), rt = (int)(unit % n_rt);

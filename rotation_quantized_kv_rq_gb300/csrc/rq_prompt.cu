@@ -477,20 +477,24 @@ bool encode(CUtensorMap* map, bool bf16, const HeadsDev& x, int dims, int n, int
                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Which units are cut.  Units of one size (no more than 512 queries a sequence): the ones that would have the last round of
-// pairs to themselves, so that their parts fill it.  Units of several (causal over more rows): all, where they are fewer than
-// 4 pairs' worth, so that the longest does not outlast the rest.  At least 2 tiles a part, and a slot for each.
+// Which units are cut, at the batch's mean lengths.  Units of one size (no more than 512 queries a sequence): the ones that would
+// have the last round of pairs to themselves, so that their parts fill it.  Units of several sizes (causal over more rows): all,
+// where the longest would outlast an even share of the work.  A part opens and closes in the time of some 4 tiles, so it has
+// at least that many; and there is a slot for each.
+// Device time, us, without and with: 4 x 512 of 8K x 64 heads (256 units on 76 pairs) 490 | 449; 8,192 x 8 heads (128 units of 4 to
+// 64 tiles, share 57) 127 | 174, not cut; 8,192 x 2 heads 118 | 65; 2 x 1,024 over 7K x 4 heads 117 | 67; 64 over 16K x 2 heads 232 | 31.
 Cut cut_of(const PromptArgs& a, long long units, int n_rb) {
   const int pairs = a.num_sms / 2;
-  const double tiles = (double)a.nk / a.B / kTok + 1.0;
+  const double rows = (double)a.nq / a.B, keys = (double)a.nk / a.B, longest = keys / kTok + 1.0;
   Cut c{n_rb, (int)units, 1};
   if (units >= 6ll * pairs) return c;
   long long cut = units % pairs, splits = cut > 0 ? pairs / cut : 1;
   if (n_rb > 1) {
+    const double share = (keys - 0.5 * rows + kUnitRows / 2) / kTok * (rows / kUnitRows) * a.B * a.q.heads / pairs;
     cut = units;
-    splits = units >= 4ll * pairs ? 1 : 4;
+    splits = longest > 1.25 * share ? (long long)(longest / share) + 1 : 1;
   }
-  while (splits > 1 && (splits * 2.0 > tiles || cut * splits > (long long)kSlotsPerPair * pairs)) --splits;
+  while (splits > 1 && (splits * 4.0 > longest || cut * splits > (long long)kSlotsPerPair * pairs)) --splits;
   if (splits > 1) c.whole = (int)(units - cut), c.splits = (int)splits;
   return c;
 }

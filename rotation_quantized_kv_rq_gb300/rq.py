@@ -753,8 +753,9 @@ class LatentCache:
         latents c [n][512], the rotation (rope: a Rope of rotary_dim <= 64, or None) of position parts k_pe [n][64] and of
         the queries' q_pe [n][heads][64], and the coding into slot_mapping (int32 [n]).  Returns the turned q_pe (None without;
         q_pe_out: where to write, q_pe itself for in place).  Slices of a projection's output are taken as they are."""
-        name, n, index, dtype = "rq_latent_append", slot_mapping.shape[0], self._index, self.dtype
-        if (not _ints(slot_mapping, n, index) or not _rows_ok(c, (n, LATENT_DIM), dtype, index) or
+        name, index, dtype = "rq_latent_append", self._index, self.dtype
+        n = slot_mapping.shape[0] if slot_mapping.dim() == 1 else -1
+        if (n < 0 or not _ints(slot_mapping, n, index) or not _rows_ok(c, (n, LATENT_DIM), dtype, index) or
                 not _rows_ok(k_pe, (n, POSITION_DIM), dtype, index) or
                 (rope is not None and rope.device.index != index) or
                 (weight is not None and (weight.dtype is not torch.float32 or weight.shape != (LATENT_DIM,) or
