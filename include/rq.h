@@ -501,7 +501,8 @@ int rq_latent_read(rq_latent *ctx, const void *pages, const int32_t *block_table
  * queries being its last tokens: its query j sees its keys 0 .. nk_b - nq_b + j.  A head's key is its own 128 dims and the 64 that
  * all heads share.  out = softmax(sm_scale (q[:128] . k + q[128:] . k_pe)) v; a row that sees no key gives zeros.
  * Sequences whose offsets fall, pass nq or nk, or have more than max_new queries set RQ_STATUS_BAD_LEN and are skipped;
- * rows of no sequence are left as they are.
+ * rows of no sequence are left as they are.  A call gives the same bits each time; B, num_heads, nq, nk and max_new choose how its
+ * work is cut, and so the order of its sums.
  */
 typedef struct {
   rq_heads q;                /* [nq] rows of num_heads heads of 192 */

@@ -23,7 +23,9 @@
 // Every wait is bounded: one that runs out sets RQ_STATUS_TIMEOUT and an abort flag every role polls.
 #include <math_constants.h>
 
+#include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <cstddef>
 #include <type_traits>
 
@@ -108,7 +110,10 @@ struct Cut {
   int n_rb, whole, splits;
 };
 
-template <typename T>
+// dual: calls of no more than 256 queries a sequence.  They fill one block only: both blocks take them, one the even tiles and
+// one the odd, so that here too one is on the tensor cores while the other is in its softmax; joined at the end.  2 x 100
+// rows over 4,000 x 128 heads 250 -> 180 us.  (As a choice of each unit's in one kernel it cost the others 3 to 4%.)
+template <typename T, bool dual>
 __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_constant__ Maps maps, const PromptArgs a, const Cut cut) {
   extern __shared__ uint8_t smem_raw[];
   const uint32_t base = smem_addr(smem_raw) + (1024 - (smem_addr(smem_raw) & 1023) & 1023);
@@ -136,7 +141,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
   const int all0 = tiles_to(r0 + kRows), all1 = r0 + kRows < nq ? tiles_to(r0 + kUnitRows) : 0, all = max(all0, all1);
   const int t_first = (int)((long long)part * all / splits), t_end = (int)((long long)(part + 1) * all / splits);
   const int n = t_end - t_first;
-  const int n_b[2] = {min(max(all0 - t_first, 0), n), min(max(all1 - t_first, 0), n)};
+  const int n_b[2] = {dual ? (n + 1) / 2 : min(max(all0 - t_first, 0), n), dual ? n / 2 : min(max(all1 - t_first, 0), n)};
   // from this tile on, rows of the pair see tiles in part
   const int t_fix = max(0, max(0, ahead + r0 + 1) / kTok - t_first);
 
@@ -169,7 +174,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
   fence_after_sync();
   const uint32_t tmem = *(volatile uint32_t*)&ms.tmem;
   const uint32_t lane_off = (uint32_t)(32 * (warp & 3)) << 16;
-  const int blk = warp >> 2 & 1, brow = 32 * (warp & 3) + lane, row = r0 + kRows * blk + kHalf * (int)rank + brow;
+  const int blk = warp >> 2 & 1, brow = 32 * (warp & 3) + lane, row = r0 + (dual ? 0 : kRows * blk) + kHalf * (int)rank + brow;
   const bool valid = row < nq;
   const int qpos = valid ? ahead + row : -1;  // the last key that the row sees
   float m_run = kNone, l_run = 0.f;
@@ -181,7 +186,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
     const uint32_t s_tile = tmem + lane_off + kColS + 128 * blk, o_cols = tmem + lane_off + 128 * blk;
     float from = 0.f;
     for (int t = 0; t < n_b[blk]; ++t) {
-      const int t0 = (t_first + t) * kTok;
+      const int t0 = (t_first + (dual ? 2 * t + blk : t)) * kTok;
       ok = warp_wait(ms.s_full[blk], t, abort_flag);  // S_b(t), and W_b(t - 1) V before it
       if (!ok) break;
       fence_after_sync();
@@ -258,7 +263,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
     // ================= MMA issue: the leader's =================
     if (rank == 0 && n > 0) {
       constexpr uint32_t id_s = idesc<T>(kRows, kTok, 0), id_o = idesc<T>(kRows, kDim, 1);
-      const int last_b = n_b[1] > 0 ? 1 : 0;  // the block that uses a tile last
+      const int last_b = !dual && n_b[1] > 0 ? 1 : 0;  // the block that uses a tile last (dual: the one that uses it)
       bool issued = false;
       auto wait = [&](uint64_t& bar, uint32_t parity) { return ok = warp_wait(bar, parity, abort_flag); };
       auto s_mmas = [&](int bb, int t) {  // S_b(t)
@@ -270,28 +275,29 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
           pair_mma_ss(tmem + kColS + 128 * bb, sdesc(q_at + (ks >> 2) * kChunk + 32 * (ks & 3)),
                       sdesc(k_at + (ks >> 2) * (kChunk / 2) + 32 * (ks & 3)), id_s, ks > 0);
         issued = true;
-        if (bb == last_b && t + kStages < n) pair_commit(smem_addr(&ms.k_empty[st]), 3);
+        if ((dual || bb == last_b) && t + kStages < n) pair_commit(smem_addr(&ms.k_empty[st]), 3);
         pair_commit(smem_addr(&ms.s_full[bb]), 3);
       };
       wait(ms.q_full, 0);
 #pragma unroll
       for (int bb = 0; bb < 2; ++bb)
-        if (ok && n_b[bb] > 0) s_mmas(bb, 0);
+        if (ok && n_b[bb] > 0) s_mmas(bb, dual ? bb : 0);
       for (int t = 0; t < n && ok; ++t) {
         const int st = t % kStages;
         if (!wait(ms.v_full[st], t / kStages)) break;
         if (t >= t_fix && !wait(ms.fix_done[st], (t - t_fix) / kStages)) break;
 #pragma unroll
         for (int bb = 0; bb < 2; ++bb) {
-          if (!ok || t >= n_b[bb]) continue;
-          if (!wait(ms.p_full[bb], t)) break;
+          const int i = dual ? t >> 1 : t;  // the block's tile
+          if (!ok || (dual ? bb != (t & 1) : t >= n_b[bb])) continue;
+          if (!wait(ms.p_full[bb], i)) break;
           fence_after_sync();
 #pragma unroll
           for (int ks = 0; ks < 8; ++ks)  // keys 16 ks ..
-            pair_mma_ts(tmem + 128 * bb, tmem + kColS + 128 * bb + 8 * ks, sdesc(v_ring + st * kVBytes + 2048 * ks), id_o, t > 0 || ks > 0);
-          if (bb == last_b && t + kStages < n) pair_commit(smem_addr(&ms.v_empty[st]), 3);
-          if (t + 1 < n_b[bb])
-            s_mmas(bb, t + 1);  // over the same columns, behind the MMAs that read them
+            pair_mma_ts(tmem + 128 * bb, tmem + kColS + 128 * bb + 8 * ks, sdesc(v_ring + st * kVBytes + 2048 * ks), id_o, i > 0 || ks > 0);
+          if ((dual || bb == last_b) && t + kStages < n) pair_commit(smem_addr(&ms.v_empty[st]), 3);
+          if (i + 1 < n_b[bb])
+            s_mmas(bb, dual ? t + 2 : t + 1);  // over the same columns, behind the MMAs that read them
           else
             pair_commit(smem_addr(&ms.o_done[bb]), 3);
         }
@@ -309,7 +315,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
       const uint32_t bar = peer_addr(smem_addr(&ms.q_full), 0);
 #pragma unroll
       for (int i = 0; i < 6; ++i)
-        load_pair(q_ops + i * kChunk, maps.q, 64 * (i % 3), h, q0 + r0 + kRows * (i / 3) + kHalf * (int)rank, bar);
+        load_pair(q_ops + i * kChunk, maps.q, 64 * (i % 3), h, q0 + r0 + (dual ? 0 : kRows * (i / 3)) + kHalf * (int)rank, bar);
     }
     for (int t = 0; t < n && ok; ++t) {
       const int st = t % kStages, z = k0 + (t_first + t) * kTok;
@@ -379,7 +385,37 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
   cluster_sync();  // the peer is done with this CTA's operands, and its values' warps have left what they found
 
   // ---- write the rows, or the part of them ----
-  if (warp < kSoftWarps && !aborted) {
+  float* const other = reinterpret_cast<float*>(smem_raw + (base - smem_addr(smem_raw)));  // over the operands: [dim / 4][row][4], m, l
+  if (dual) {
+    if (blk == 1 && warp < kSoftWarps && !aborted) {
+#pragma unroll 1
+      for (int c = 0; c < kDim / 16; ++c) {
+        float y[16];
+        if (n_b[1] > 0) {
+          tmem_ld16(tmem + lane_off + 128 + 16 * c, y);
+          tmem_wait_ld();
+          settle<16>(y);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) y[i] = 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          reinterpret_cast<float4*>(other)[(4 * c + i) * kHalf + brow] = make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
+      }
+      other[kHalf * kDim + brow] = m_run;
+      other[kHalf * kDim + kHalf + brow] = l_run;
+    }
+    __syncthreads();
+  }
+  if (warp < kSoftWarps && !aborted && !(dual && blk == 1)) {
+    float w0 = 1.f, w1 = 0.f;  // dual: the factors of the two blocks' rows
+    if (dual) {
+      const float m1 = other[kHalf * kDim + brow], l1 = other[kHalf * kDim + kHalf + brow], to = fmaxf(m_run, m1);
+      w0 = ex2(m_run - to), w1 = ex2(m1 - to);
+      l_run = fmaf(l_run, w0, l1 * w1);
+      m_run = to;
+    }
     // a row whose scores are all minus infinity; one that sees nothing
     const float empty = !is_part && qpos >= 0 ? CUDART_NAN_F : 0.f, inv = is_part ? 1.f : 1.f / l_run;
     // what the values' warps found: dims 64 r .. of the pair's CTA r
@@ -396,6 +432,14 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         tmem_ld16(tmem + lane_off + 128 * blk + 16 * c, y);
         tmem_wait_ld();
         settle<16>(y);
+        if (dual) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float4 v = reinterpret_cast<const float4*>(other)[(4 * c + i) * kHalf + brow];
+            y[4 * i] = fmaf(y[4 * i], w0, v.x * w1), y[4 * i + 1] = fmaf(y[4 * i + 1], w0, v.y * w1);
+            y[4 * i + 2] = fmaf(y[4 * i + 2], w0, v.z * w1), y[4 * i + 3] = fmaf(y[4 * i + 3], w0, v.w * w1);
+          }
+        }
 #pragma unroll
         for (int i = 0; i < 16; ++i) y[i] = l_run == 0.f ? empty : y[i] * inv;
       } else {
@@ -490,11 +534,12 @@ Cut cut_of(const PromptArgs& a, long long units, int n_rb) {
   if (units >= 6ll * pairs) return c;
   long long cut = units % pairs, splits = cut > 0 ? pairs / cut : 1;
   if (n_rb > 1) {
-    const double share = (keys - 0.5 * rows + kUnitRows / 2) / kTok * (rows / kUnitRows) * a.B * a.q.heads / pairs;
+    // (at least a tile: rows of no sequence, or sequences with fewer keys than queries, would make it nothing)
+    const double share = fmax(1.0, (keys - 0.5 * rows + kUnitRows / 2) / kTok * (rows / kUnitRows) * a.B * a.q.heads / pairs);
     cut = units;
     splits = longest > 1.25 * share ? (long long)(longest / share) + 1 : 1;
   }
-  while (splits > 1 && (splits * 4.0 > longest || cut * splits > (long long)kSlotsPerPair * pairs)) --splits;
+  if (cut > 0) splits = std::min({splits, (long long)(longest / 4), (long long)kSlotsPerPair * pairs / cut});
   if (splits > 1) c.whole = (int)(units - cut), c.splits = (int)splits;
   return c;
 }
@@ -504,12 +549,14 @@ cudaError_t launch(const Maps& maps, const PromptArgs& a, int n_rb, cudaStream_t
   static_assert(sizeof(Maps) + sizeof(PromptArgs) + 32 <= 4096, "kernel parameters");
   // the kernel's shared-memory limit, once a device (at every call on those past the 64th)
   static std::atomic<unsigned long long> set{0};
+  const bool dual = a.max_new <= kRows;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
   if (!(set.load(std::memory_order_relaxed) & bit)) {
-    e = cudaFuncSetAttribute(prompt_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    e = cudaFuncSetAttribute(prompt_kernel<T, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(prompt_kernel<T, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
     set.fetch_or(bit, std::memory_order_relaxed);
   }
@@ -528,7 +575,7 @@ cudaError_t launch(const Maps& maps, const PromptArgs& a, int n_rb, cudaStream_t
   cfg.stream = stream;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, prompt_kernel<T>, maps, a, cut);
+  e = dual ? cudaLaunchKernelEx(&cfg, prompt_kernel<T, true>, maps, a, cut) : cudaLaunchKernelEx(&cfg, prompt_kernel<T, false>, maps, a, cut);
   if (e != cudaSuccess || n_cut == 0) return e;
   cudaLaunchAttribute behind[1];
   behind[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

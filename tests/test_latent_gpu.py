@@ -508,6 +508,11 @@ def check_prompt(out, q, k, pe, v, qo, ko, dtype, sm=0.0):
     ([1, 1], [511, 0], 16),
     ([3, 200], [5000, 9000], 2),     # few units: a cluster shares each one's keys
     ([2, 1, 300], [0, 7000, 900], 3),
+    ([256, 129, 7], [130, 0, 1024], 4),
+    ([100, 30, 0, 1], [4000, 333, 5, 0], 70),  # more units than pairs of SMs, no more than 256 queries
+    ([1100, 513], [20, 0], 3),       # rows of several sizes, cut
+    ([64, 2], [5000, 3000], 2),      # no more than 256 queries, cut
+    ([600], [0], 130),
 ])
 def test_prompt(dtype, new, old, heads):
     dtype = DT[dtype]
@@ -522,7 +527,9 @@ def test_prompt(dtype, new, old, heads):
     assert torch.equal(again[2:-2], out[2:-2])
     # other strides: heads outside tokens, contiguous copies
     t = [x.transpose(0, 1).contiguous().transpose(0, 1) for x in (q, k, v)]
-    assert torch.equal(rq.prompt_attention(t[0], t[1], pe.contiguous(), t[2], int32(qo), int32(ko), max(new) + 100)[2:-2], out[2:-2])
+    assert torch.equal(rq.prompt_attention(t[0], t[1], pe.contiguous(), t[2], int32(qo), int32(ko), max(new))[2:-2], out[2:-2])
+    # a larger bound may lay the work out otherwise, and so add in another order
+    check_prompt(rq.prompt_attention(q, k, pe, v, int32(qo), int32(ko), max(new) + 100), q, k, pe, v, qo, ko, dtype)
 
 
 @pytest.mark.parametrize("dtype", ["f16", "bf16"])
@@ -543,34 +550,35 @@ def test_prompt_rising_scores():
 
 @pytest.mark.parametrize("dtype", ["f16", "bf16"])
 @pytest.mark.parametrize("value", [math.nan, math.inf, -math.inf])
-def test_prompt_values_that_are_not_finite(dtype, value):
+@pytest.mark.parametrize("n", [300, 200])
+def test_prompt_values_that_are_not_finite(dtype, value, n):
     """A value that is not finite reaches the rows that see it, in its dim, and no other; nor does a key's, or one of the
     next sequence."""
     dtype = DT[dtype]
-    q, k, pe, v, qo, ko = prompt_case(7, [300, 40], [37, 5], 2, dtype)
-    clean = rq.prompt_attention(q, k, pe, v, int32(qo), int32(ko), 300)
-    for pos in (37 + 1, 37 + 130, 37 + 299, 10, ko[1]):
+    q, k, pe, v, qo, ko = prompt_case(7, [n, 40], [37, 5], 2, dtype)
+    clean = rq.prompt_attention(q, k, pe, v, int32(qo), int32(ko), n)
+    for pos in (37 + 1, 37 + 130, 37 + n - 1, 10, ko[1]):
         v2 = v.clone()
         v2[pos, 1, 5] = value
-        out = rq.prompt_attention(q, k, pe, v2, int32(qo), int32(ko), 300)
+        out = rq.prompt_attention(q, k, pe, v2, int32(qo), int32(ko), n)
         hit = torch.zeros_like(out, dtype=torch.bool)
-        hit[max(0, pos - 37):300 if pos < ko[1] else 340, 1, 5] = True
+        hit[max(0, pos - 37):n if pos < ko[1] else n + 40, 1, 5] = True
         if pos == ko[1]:
-            hit[:300] = False
+            hit[:n] = False
         assert not torch.isfinite(out[hit]).any() and torch.equal(out[~hit], clean[~hit]), pos
         k2, pe2 = k.clone(), pe.clone()
         k2[pos, 0, 3] = value
-        out = rq.prompt_attention(q, k2, pe, v, int32(qo), int32(ko), 300)
+        out = rq.prompt_attention(q, k2, pe, v, int32(qo), int32(ko), n)
         hit.zero_()
-        hit[max(0, pos - 37):300, 0] = True
+        hit[max(0, pos - 37):n, 0] = True
         if pos == ko[1]:
-            hit[:300] = False
-            hit[300:, 0] = True
+            hit[:n] = False
+            hit[n:, 0] = True
         assert torch.equal(out[~hit], clean[~hit])
         if math.isnan(value):
             assert torch.isnan(out[hit]).all()
             pe2[pos, 9] = value
-            out = rq.prompt_attention(q, k, pe2, v, int32(qo), int32(ko), 300)
+            out = rq.prompt_attention(q, k, pe2, v, int32(qo), int32(ko), n)
             hit |= hit.any(1, keepdim=True)
             assert torch.isnan(out[hit]).all() and torch.equal(out[~hit], clean[~hit])
 
@@ -703,3 +711,112 @@ def test_views_of_the_pool():
     n, r = divmod(int(slot), 32)
     got = c[n, :, r].float().cpu().numpy().reshape(4, 8, 16)[:, np.arange(8) ^ (r % 8)].reshape(512)
     assert np.array_equal(got, codes[slot]) and float(s[n, r]) == 2.0 ** (byte[slot] - 127)
+
+
+def test_prompt_on_another_stream_and_captured():
+    """Calls of several cuts on two streams at once, each with its own workspace, then one captured and replayed on new inputs."""
+    cases = [prompt_case(i, new, old, 3, torch.bfloat16) for i, (new, old) in enumerate((([64], [4000]), ([1100, 3], [0, 700]), ([700], [90])))]
+    run = lambda c: rq.prompt_attention(*c[:4], int32(c[4]), int32(c[5]), int(np.diff(c[4]).max()))  # noqa: E731
+    want = [run(c) for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(3):
+        for c, s in zip(cases, streams):
+            with torch.cuda.stream(s):
+                got.append(run(c))
+    torch.cuda.synchronize()
+    assert all(torch.equal(g, want[i % len(cases)]) for i, g in enumerate(got))
+    q, k, pe, v, qo, ko = cases[0]
+    qo, ko = int32(qo), int32(ko)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = rq.prompt_attention(q, k, pe, v, qo, ko, 64)
+    q.copy_(torch.randn_like(q))
+    v.copy_(torch.randn_like(v))
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, rq.prompt_attention(q, k, pe, v, qo, ko, 64))
+
+
+def test_prompt_workspace_is_checked():
+    q, k, pe, v, qo, ko = prompt_case(1, [5], [3], 2, torch.float16)
+    out = torch.full((5, 2, 128), 7.0, dtype=torch.float16, device="cuda")
+    small = torch.empty(rq.rq_prompt_workspace(0) - 16, dtype=torch.uint8, device="cuda")
+    with pytest.raises(rq.RQError) as e:
+        rq.rq_prompt_attention(q, k, pe, v, int32(qo), int32(ko), 5, out, small)
+    assert e.value.code == rq.RQ_ERR_CAPACITY and (out == 7).all()
+
+
+def test_two_caches_on_two_streams_at_once():
+    """Each cache has its own workspace: calls that are cut over many tokens, in flight together."""
+    cases = [Case(seed, [5000, 300], 1, 20, 32, torch.float16) for seed in (1, 2)]
+    want = [c.run() for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    args = [(c.q_c, c.q_pe, dev(c.table), dev(c.lens)) for c in cases]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(5):
+        for c, s, a in zip(cases, streams, args):
+            with torch.cuda.stream(s):
+                got.append(c.cache.verify(*a))
+    torch.cuda.synchronize()
+    assert all(torch.equal(g, want[i % 2]) for i, g in enumerate(got))
+
+
+def test_offsets_past_32_bits():
+    """A pool past 4 GiB, and rows past 2^31 elements in every tensor, against small ones."""
+    P, dtype, heads, rng = 64, torch.bfloat16, 128, gen(4)
+    x = dev(rng.standard_normal((70, 576)), dtype)
+    small, big = make(heads, P, 2, dtype, batch=4096, t=9), make(heads, P, 110000, dtype, batch=4096, t=9)
+    first, far = np.arange(70), np.arange(70) + np.where(np.arange(70) < 64, 109999, 107000 - 1) * 64
+    small.append(x[:, :512], x[:, 512:], int32(first))
+    big.append(x[:, :512], x[:, 512:], int32(far))
+    assert torch.equal(big.pages[109999], small.pages[0])
+    near_table, far_table = int32([[0, 1]]), int32([[109999, 107000]])
+    q_c, q_pe = dev(rng.standard_normal((1, 9, heads, 512)), dtype), dev(rng.standard_normal((1, 9, heads, 64)), dtype)
+    want = small.verify(q_c, q_pe, near_table, int32([70]))
+    assert torch.equal(big.verify(q_c, q_pe, far_table, int32([70])), want)
+
+    q_many, out = torch.zeros(4096, 9, heads, 512, dtype=dtype, device="cuda"), torch.empty(4096, 9, heads, 512, dtype=dtype, device="cuda")
+    pe_many = torch.zeros(4096, 9, heads, 64, dtype=dtype, device="cuda")
+    q_many[-1], pe_many[-1] = q_c[0], q_pe[0]
+    lens, tables = int32([0] * 4095 + [70]), far_table.expand(4096, 2).contiguous()
+    big.verify(q_many, pe_many, tables, lens, out=out)
+    ref, tol = L.attention(host(q_c), host(q_pe), small.pages.cpu().numpy(), np.array([[0, 1]]), np.array([70]), P, L.chain(9), 192 ** -0.5, dtype)
+    within(host(out[-1:]), ref, tol + R.half_step(dtype, ref) * (1 + 2.0 ** -8))
+    assert not out[0].any() and not out[4094].any()
+    del q_many, pe_many, out
+
+    c, pe = small.read(near_table, int32([0, 70]), 70)
+    n = 4_300_000
+    c_far, pe_far = torch.empty(n, 512, dtype=dtype, device="cuda"), torch.empty(n, 64, dtype=dtype, device="cuda")
+    big.read(far_table, int32([n - 70, n]), n, c=c_far, k_pe=pe_far)
+    assert torch.equal(c_far[-70:], c) and torch.equal(pe_far[-70:], pe)
+    del c_far, pe_far
+
+    n = 100_000
+    down, q = torch.zeros(n, 576, dtype=dtype, device="cuda"), torch.zeros(n, heads, 192, dtype=dtype, device="cuda")
+    down[-70:], q[-9:, :, 128:] = x, q_pe[0]
+    rope, slots, pos = rq.Rope(64), torch.full((n,), -1, dtype=torch.int32, device="cuda"), torch.arange(n, dtype=torch.int32, device="cuda")
+    slots[-70:] = int32(first)
+    big.append(down[:, :512], down[:, 512:], slots, rope, pos, q_pe=q[..., 128:], q_pe_out=q[..., 128:])
+    turned = small.append(x[:, :512], x[:, 512:], int32(first), rope, pos[-70:], q_pe=torch.cat([torch.zeros(61, heads, 64, dtype=dtype, device="cuda"), q_pe[0]]))
+    near = lambda a, b: np.abs(host(a) - host(b)).max() <= torch.finfo(dtype).eps * np.abs(host(b)).max()  # noqa: E731
+    assert near(q[-9:, :, 128:], turned[-9:])  # (a long call and a short one round apart)
+    (c, pe), (c_ref, pe_ref) = (m.read(near_table, int32([0, 70]), 70) for m in (big, small))
+    assert torch.equal(c, c_ref) and near(pe, pe_ref)
+    assert int(big.status.item()) == 0 and int(small.status.item()) == 0
+    del q, big
+
+    nq = 140_000
+    q = torch.empty(nq, heads, 192, dtype=dtype, device="cuda")
+    kv, k_pe = torch.empty(nq, 64 + heads, 128, dtype=dtype, device="cuda"), torch.empty(nq, 64, dtype=dtype, device="cuda")
+    q[-9:] = dev(rng.standard_normal((9, heads, 192)), dtype)
+    kv[-300:] = dev(rng.standard_normal((300, 64 + heads, 128)), dtype)
+    k_pe[-300:] = dev(rng.standard_normal((300, 64)), dtype)
+    k, v = kv[:, 64:], kv[:, :heads]
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = rq.prompt_attention(q, k, k_pe, v, int32([nq - 9, nq]), int32([nq - 300, nq]), 9, status=status)
+    check_prompt(out[-9:], q[-9:], k[-300:], k_pe[-300:], v[-300:], [0, 9], [0, 300], dtype)
+    assert int(status.item()) == 0
