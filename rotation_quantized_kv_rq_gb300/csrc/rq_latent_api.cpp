@@ -172,9 +172,9 @@ int rq_latent_attention(rq_latent* ctx, const rq_heads* q_c, const rq_heads* q_p
     return RQ_ERR_INVALID;
   if (B > ctx->cfg.max_batch || T > ctx->cfg.max_query_tokens || max_pages > ctx->cfg.max_pages_per_seq)
     return RQ_ERR_CAPACITY;
-  // tiles of 256 tokens over all sequences and groups of 128 rows are counted in 31 bits
+  // tiles of 256 tokens, and three more for each group, over all sequences and groups of 128 rows are counted in 31 bits
   const long long groups = (long long)B * (((long long)T * ctx->cfg.num_heads + 127) / 128);
-  if (groups > INT32_MAX / (((long long)max_pages * ctx->cfg.page_size + 255) / 256)) return RQ_ERR_CAPACITY;
+  if (groups > INT32_MAX / (((long long)max_pages * ctx->cfg.page_size + 255) / 256 + 3)) return RQ_ERR_CAPACITY;
   DeviceScope scope(ctx->device);
   if (!scope.ok()) return RQ_ERR_CUDA;
   rq::LatentAttnArgs a{};

@@ -23,7 +23,7 @@
 //   tail (warp 11 of both): zeros over a last tile's rows behind the tokens that are seen, which may hold anything.
 // Tensor memory: O at columns 0 to 255 (lanes 64 .. 127 hold the second half of the columns' dims), S(t) at 256 + 128 (t mod 2).
 //
-// Work is cut evenly: tiles of all units (sequence, 128 rows) in order, one range for each pair.  A unit that spans ranges
+// Work is cut evenly: tiles of all units (sequence, 128 rows) in order and kOpen more for each unit, one range for each pair.  A unit that spans ranges
 // leaves its parts (m, l, out) in the workspace, and a second kernel joins them.
 // Every wait is bounded: one that runs out sets RQ_STATUS_TIMEOUT and an abort flag every role polls.
 #include <math_constants.h>
@@ -56,6 +56,10 @@ constexpr uint32_t kColS = 256;
 // kReach: below 2^12 an e5m2 number's remainder stays within e4m3's 448
 constexpr float kLift = 10.f, kReach = 12.f;
 constexpr float kNone = -3.402823466e38f;  // m before any visible token
+// Opening a unit (its queries as pieces, the first scores) takes the time of some three tiles: in the cut of the work a unit counts
+// for its tiles and kOpen more, so that a pair that opens a second one has as many tiles less.  Counted as 0 | 2 | 3 | 4, device us:
+// 32 x 1K-32K x 16 heads 105 | 95 | 91 | 92, tree of 5 x 500-9K x 260 rows 40 | 37 | 34 | 34.
+constexpr int kOpen = 3;
 // floats of a fragment's slot: 128 rows x 512 (as [dim / 4][row][4]), then the rows' m and l
 constexpr size_t kSlotFloats = (size_t)kUnitRows * kLatentDim + 2 * kUnitRows;
 
@@ -228,16 +232,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     ms.abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  // ---- the pair's range of tiles: x .. x_end - 1 of `total`, kept by thread 0 ----
+  // ---- the pair's range: x .. x_end - 1 of `total` (kOpen and the tiles of each unit), kept by thread 0 ----
   // range c starts at c * each + min(c, more)
   const uint32_t pairs = gridDim.x >> 1, me = blockIdx.x >> 1;
-  uint32_t total, parts, each, more, x, x_end, at, item;  // at: the first tile of unit `item`
+  uint32_t total, parts, each, more, x, x_end, at, item;  // at: where unit `item` begins
+  Unit un;
   {
     __shared__ uint32_t s_sums[kThreads / 32], s_found[2];
+    __shared__ Unit s_unit;
     const uint32_t n_items = (uint32_t)a.B * n_rt, chunk = (n_items + kThreads - 1) / kThreads;
     uint32_t mine = 0;
     for (uint32_t i = tid * chunk; i < min(n_items, (tid + 1) * chunk); ++i)
-      mine += unit_of(a, kUR, cap, (int)(i / (uint32_t)n_rt), (int)(i % (uint32_t)n_rt), blockIdx.x == 0).tiles;
+      mine += kOpen + unit_of(a, kUR, cap, (int)(i / (uint32_t)n_rt), (int)(i % (uint32_t)n_rt), blockIdx.x == 0).tiles;
     uint32_t sum = mine;  // inclusive, over the warp, then over the warps before
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -262,16 +268,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (x >= before && x < before + mine) {
       uint32_t p = before, i = tid * chunk;
       for (;; ++i) {
-        const uint32_t n = unit_of(a, kUR, cap, (int)(i / (uint32_t)n_rt), (int)(i % (uint32_t)n_rt), false).tiles;
-        if (x < p + n) break;
-        p += n;
+        un = unit_of(a, kUR, cap, (int)(i / (uint32_t)n_rt), (int)(i % (uint32_t)n_rt), false);
+        if (x < p + kOpen + un.tiles) break;
+        p += kOpen + un.tiles;
       }
       s_found[0] = p;
       s_found[1] = i;
+      s_unit = un;
     }
     __syncthreads();
     at = s_found[0];
     item = s_found[1];
+    un = s_unit;
   }
   auto range_of = [&](uint32_t tile) {  // the range that holds a tile
     const uint32_t longer = more * (each + 1u);
@@ -298,19 +306,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!f.done) {
         f.b = (int)(item / (uint32_t)n_rt);
         f.rt = (int)(item % (uint32_t)n_rt);
-        const Unit un = unit_of(a, kUR, cap, f.b, f.rt, false);
+        if (!first_frag) un = unit_of(a, kUR, cap, f.b, f.rt, false);
         f.len = un.len;
         f.end = un.end;
-        f.r0 = (int)(x - at);
-        f.n = (int)min((uint32_t)un.tiles - (x - at), x_end - x);
+        f.r0 = max(0, (int)(x - at) - kOpen);
+        f.n = min(un.tiles, (int)(x_end - at) - kOpen) - f.r0;
+        f.done = f.n <= 0;  // the range ends before the unit's first tile
+      }
+      if (!f.done) {
         f.whole = f.n == un.tiles;
-        const uint32_t first = f.r0 == 0 ? me : range_of(at);
+        const uint32_t first = range_of(at + kOpen);  // (this one, where r0 is 0)
         f.range = (int)first;
-        f.range_last = first * each + min(first, more) != at;
+        f.range_last = first * each + min(first, more) < at;
         if (f.r0 == 0 && rank == 0)
-          info[item] = make_int4(f.range, f.whole ? 0 : (int)(range_of(at + un.tiles - 1) - first) + 1, f.range_last, 0);
-        x += f.n;
-        if (x - at == (uint32_t)un.tiles) {
+          info[item] = make_int4(f.range, f.whole ? 0 : (int)(range_of(at + kOpen + un.tiles - 1) - first) + 1, f.range_last, 0);
+        x = at + kOpen + f.r0 + f.n;
+        if (f.r0 + f.n == un.tiles) {
           at = x;
           ++item;
         }
