@@ -48,8 +48,10 @@ constexpr int kSoftWarps = 8, kMmaWarp = 8, kCopyWarp = 9, kScaleWarp = 10, kTai
 constexpr int kMmaRows = 128, kTok = 256;  // rows of a pair's MMAs, tokens of a tile
 constexpr int kUnitRows = 128;             // the most rows of a unit
 constexpr uint32_t kSlotBytes = 16384;
-// Slots are filled and given back in units of two or one: a tile's keys are three units (dims 0 .. 255, 256 .. 511, the
-// position parts), its values two (128 tokens each).  A wait or a commit costs the issuing warp about as much as three MMAs.
+// Slots are filled and given back in units of two: a tile's keys are three units (dims 0 .. 255, 256 .. 511, and one slot of position
+// parts), its values two (128 tokens each).  A wait or a commit costs the issuing warp about as much as three MMAs.  A ring of
+// four slots (fp16, 64 rows) would hold two of them, too few to hide a load behind: there a unit is one slot (64 x 16K x 128
+// heads fp16 309 -> 287 us).
 constexpr int kUnits = 8;  // barriers for units: more than there can be in the ring
 constexpr uint32_t kColS = 256;
 // weights are 2^(score + E - m), m the running maximum of score + E less kLift, moved where a score is past it by more than
@@ -74,6 +76,7 @@ struct Shape {
   static constexpr uint32_t kPieceP = 2 * kRowsBytes, kPBytes = kPieces * kPieceP;               // [piece][2 halves of 128 tokens][RC rows]
   static constexpr uint32_t kOffMisc = 221184, kOffP = kQBytes, kOffRing = kOffP + kPBytes;
   static constexpr int kSlots = (kOffMisc - kOffRing) / kSlotBytes;
+  static constexpr int kPer = kSlots < 5 ? 1 : 2, kKeys = 4 / kPer + 1, kValues = 4 / kPer;  // slots of a unit, units of a tile
 };
 
 struct Frag {           // tiles r0 .. r0 + n - 1 of one unit
@@ -200,7 +203,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     latent_kernel(const __grid_constant__ CUtensorMap map, const LatentPool pool, const LatentAttnArgs a, int box, int4* info) {
   using S = Shape<T, RC>;
   constexpr int kUR = 2 * RC;  // rows of a unit
-  constexpr int NP = S::kPieces, kSlots = S::kSlots;
+  constexpr int NP = S::kPieces, kSlots = S::kSlots, kPer = S::kPer;
   constexpr bool kF16 = std::is_same<T, __half>::value;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t base = smem_addr(smem_raw) + (1024 - (smem_addr(smem_raw) & 1023) & 1023);
@@ -232,6 +235,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     ms.abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
+  __syncwarp();
+  if (warp == kMmaWarp) pair_tmem_alloc(smem_addr(&ms.tmem), 512);  // (while the lengths come)
+  fence_before_sync();
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   // ---- the pair's range: x .. x_end - 1 of `total` (kOpen and the tiles of each unit), kept by thread 0 ----
   // range c starts at c * each + min(c, more)
   const uint32_t pairs = gridDim.x >> 1, me = blockIdx.x >> 1;
@@ -260,12 +267,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       total += s_sums[w];
     }
     parts = min(pairs, total);
-    if (me >= parts) return;  // both CTAs of a pair
     each = total / parts, more = total - each * parts;
     x = me * each + min(me, more);
-    x_end = x + each + (me < more ? 1u : 0u);
+    x_end = me < parts ? x + each + (me < more ? 1u : 0u) : x;  // (a pair without a range: done at once)
     before += sum - mine;
-    if (x >= before && x < before + mine) {
+    if (x < x_end && x >= before && x < before + mine) {
       uint32_t p = before, i = tid * chunk;
       for (;; ++i) {
         un = unit_of(a, kUR, cap, (int)(i / (uint32_t)n_rt), (int)(i % (uint32_t)n_rt), false);
@@ -285,10 +291,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t longer = more * (each + 1u);
     return tile < longer ? tile / (each + 1u) : more + (tile - longer) / each;
   };
-  __syncwarp();
-  if (warp == kMmaWarp) pair_tmem_alloc(smem_addr(&ms.tmem), 512);
-  fence_before_sync();
-  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   bool first_frag = true;
 
   // softmax: row of the CTA (= lane of tensor memory, twice), the quarter of a tile's tokens and of the dims
@@ -345,12 +347,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (warp < kSoftWarps) {
       float q_scale = 0.f;
-      if (n > 0 && 8 * warp < RC) {
-        // ---- queries as pieces: eight rows to a warp, a lane 16 dims and an eighth of a position part of every fourth row ----
-        // lane l: where row l % 8 of the warp's stands, -1 past the last row
+      if (n > 0) {
+        // ---- queries as pieces: kRW rows to a warp, a lane 16 dims and an eighth of a position part of every fourth row ----
+        constexpr int kRW = RC / kSoftWarps;
+        // lane l: where row l % kRW of the warp's stands, -1 past the last row
         long long c_at = -1, pe_at = -1;
         {
-          const long long u = (long long)ms.f.rt * kUR + RC * (int)rank + 8 * warp + (lane & 7);
+          const long long u = (long long)ms.f.rt * kUR + RC * (int)rank + kRW * warp + lane % kRW;
           if (u < n_rows) {
             const uint32_t jj = (uint32_t)u / (uint32_t)a.heads, hh = (uint32_t)u - jj * (uint32_t)a.heads;
             const long long token = (long long)b * a.T + jj;
@@ -358,22 +361,22 @@ __global__ void __launch_bounds__(kThreads, 1)
             pe_at = token * a.q_pe.stride + hh * a.q_pe.head_stride;
           }
         }
-        uint4 raw[8][2], pe2[2];  // all loads in flight together
+        uint4 raw[kRW][2], pe2[kRW / 4];  // all loads in flight together
 #pragma unroll
-        for (int r = 0; r < 8; ++r) {
+        for (int r = 0; r < kRW; ++r) {
           const long long from = __shfl_sync(0xffffffffu, c_at, r);
           const uint4* src = reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(a.q_c.x) + from) + 2 * lane;
 #pragma unroll
           for (int i = 0; i < 2; ++i) raw[r][i] = from >= 0 ? __ldg(src + i) : make_uint4(0u, 0u, 0u, 0u);
         }
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
+        for (int r = 0; r < kRW / 4; ++r) {
           const long long from = __shfl_sync(0xffffffffu, pe_at, 4 * r + (lane >> 3));
           pe2[r] = from >= 0 ? __ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(a.q_pe.x) + from) + (lane & 7)) : make_uint4(0u, 0u, 0u, 0u);
         }
 #pragma unroll 1
-        for (int r4 = 0; r4 < 8; r4 += 4) {
-          const int row0 = 8 * warp + r4;
+        for (int r4 = 0; r4 < kRW; r4 += 4) {
+          const int row0 = kRW * warp + r4;
           const uint4 pe = pe2[0];
           // magnitudes order as their 16 bits do, NaN above infinity above the rest
           auto largest = [&](const uint4& v) {
@@ -427,9 +430,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int p = 0; p < NP; ++p)
               sts128(q_ops + p * S::kPieceQ + S::kRowsBytes * (lane >> 3) + sw128(row0 + r, lane & 7), piece[p][0], piece[p][1], piece[p][2], piece[p][3]);
 #pragma unroll
-            for (int i = 0; i < 7; ++i) raw[i][0] = raw[i + 1][0], raw[i][1] = raw[i + 1][1];  // (one row's code, not eight)
+            for (int i = 0; i + 1 < kRW; ++i) raw[i][0] = raw[i + 1][0], raw[i][1] = raw[i + 1][1];  // (four rows' code, not eight)
           }
-          pe2[0] = pe2[1];
+          if constexpr (kRW > 4) pe2[0] = pe2[1];
           uint32_t w[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
@@ -595,7 +598,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         constexpr uint32_t id_p = idesc_f16(kMmaRows, kTok) | type << 7 | type << 10;
         bool issued = false;
         // units and slots in the order of use: K(0) | K(1) V(0) | K(2) V(1) | ...
-        uint32_t u = 5u * t_base, sl = 9u * t_base;
+        uint32_t u = (uint32_t)(S::kKeys + S::kValues) * t_base, sl = 9u * t_base;
         auto unit_full = [&](uint32_t v) -> uint64_t& { return ms.full[v % kUnits]; };
         uint32_t look = warp_look(unit_full(u), u / kUnits);
         auto take = [&]() { return ok = warp_wait_after(look, unit_full(u), u / kUnits, abort_flag); };  // unit u is full
@@ -612,16 +615,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t d = tmem + kColS + 128 * ((t_base + t) & 1);
 #pragma unroll 1
           for (int c = 0; c < 4; ++c) {
-            if ((c & 1) == 0 && !take()) return;
+            if (c % kPer == 0 && !take()) return;
             const uint32_t b_at = slot(), a_at = q_lo + S::kRowsBytes / 16 * c;
 #pragma unroll
             for (int p = 0; p < NP; ++p) {
-              if (p + 1 == NP && (c & 1)) peek();
+              if (p + 1 == NP && c % kPer == kPer - 1) peek();
 #pragma unroll
               for (int ks = 0; ks < 4; ++ks)
                 pair_mma_f8(d, a_at + (p * S::kPieceQ + 32 * ks) / 16, b_at + 2 * ks, id_s, p > 0 || ks > 0 ? 1u : (uint32_t)c);
             }
-            if (c & 1) give();
+            if (c % kPer == kPer - 1) give();
           }
           if (!take()) return;
           peek();
@@ -644,9 +647,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           fence_after_sync();
 #pragma unroll 1
           for (int g = 0; g < 4; ++g) {  // 64 tokens
-            if ((g & 1) == 0) {
+            if (g % kPer == 0) {
               if (!take()) break;
-              if ((r0 + t) * kTok + 64 * (g + 2) > end) {
+              if ((r0 + t) * kTok + 64 * (g + kPer) > end) {
                 if (!(ok = warp_wait(ms.tail_done[u % kUnits], tails >> (u % kUnits) & 1, abort_flag))) break;
                 tails ^= 1u << (u % kUnits);
               }
@@ -654,7 +657,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t b_at = slot(), w_at = w_lo + (g >> 1) * (S::kRowsBytes / 16) + (g & 1) * 4;
 #pragma unroll
             for (int ks = 0; ks < 2; ++ks) {
-              if (ks == 1 && (g & 1)) peek();
+              if (ks == 1 && g % kPer == kPer - 1) peek();
 #pragma unroll
               for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -662,7 +665,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                   pair_mma_f8(tmem + 128 * h, w_at + (p * S::kPieceP + 32 * ks) / 16, b_at + (8192 * h + 4096 * ks) / 16,
                               p == 0 ? id_o5 : id_o4, ks > 0 || p > 0 ? 1u : (uint32_t)(t + g));
             }
-            if (g & 1) give();
+            if (g % kPer == kPer - 1) give();
           }
           if (!ok) break;
           pair_commit(smem_addr(&ms.o_done), 3);
@@ -706,31 +709,31 @@ __global__ void __launch_bounds__(kThreads, 1)
         // lane: box lane % per_half of the unit's slot lane / per_half
         const int i = lane % per_half, c = lane / per_half;
         const int pg = __shfl_sync(0xffffffffu, page, per_half * (int)rank + i), ip = __shfl_sync(0xffffffffu, in_page, per_half * (int)rank + i);
-        for (int k = 0; k < 3; ++k) {
-          const int slots = k < 2 ? 2 : 1;
+        for (int k = 0; k < S::kKeys; ++k) {
+          const int slots = k + 1 < S::kKeys ? kPer : 1;
           if (!room(slots)) return;
           const uint32_t u = asked_units % kUnits;
           if (rank == 0) elect_expect(smem_addr(&ms.full[u]), (uint32_t)(slots * both * box * 128));
           __syncwarp();
           if (c < slots && i < mine)
-            load_pair(ring + (asked + c) % kSlots * kSlotBytes + i * box * 128, map, ip, 2 * k + c, pg, peer_addr(smem_addr(&ms.full[u]), 0));
+            load_pair(ring + (asked + c) % kSlots * kSlotBytes + i * box * 128, map, ip, kPer * k + c, pg, peer_addr(smem_addr(&ms.full[u]), 0));
           asked += slots;
           ++asked_units;
         }
       };
       auto values = [&](int t, int page, int in_page) {
-        for (int g = 0; g < 2; ++g) {  // 128 tokens, two slots of 64
-          if (!room(2)) return;
+        for (int g = 0; g < S::kValues; ++g) {  // slots of 64 tokens
+          if (!room(kPer)) return;
           const uint32_t u = asked_units % kUnits;
-          const int p = (r0 + t) * kTok + 128 * g, count = boxes(p, 2 * per_slot);
-          const bool tail = p + 128 > end;
-          // lane: box lane % (2 per_slot) of dims 128 (2 rank + lane / (2 per_slot)) ..
-          const int i = lane % (2 * per_slot), c = lane / (2 * per_slot);
-          const int pg = __shfl_sync(0xffffffffu, page, 2 * per_slot * g + i), ip = __shfl_sync(0xffffffffu, in_page, 2 * per_slot * g + i);
+          const int p = (r0 + t) * kTok + 64 * kPer * g, count = boxes(p, kPer * per_slot);
+          const bool tail = p + 64 * kPer > end;
+          // lane: box lane % (kPer per_slot) of dims 128 (2 rank + lane / (kPer per_slot)) ..
+          const int i = lane % (kPer * per_slot), c = lane / (kPer * per_slot);
+          const int pg = __shfl_sync(0xffffffffu, page, kPer * per_slot * g + i), ip = __shfl_sync(0xffffffffu, in_page, kPer * per_slot * g + i);
           const uint32_t dst = ring + (asked + i / per_slot) % kSlots * kSlotBytes + 8192 * c + i % per_slot * box * 128;
           const bool mine = c < 2 && i < count;
           if (!tail) {
-            if (rank == 0) elect_expect(smem_addr(&ms.full[u]), 4 * kSlotBytes);
+            if (rank == 0) elect_expect(smem_addr(&ms.full[u]), 2 * kPer * kSlotBytes);
             __syncwarp();
             if (mine) load_pair(dst, map, ip, 2 * (int)rank + c, pg, peer_addr(smem_addr(&ms.full[u]), 0));
           } else {  // the tail's warp of this CTA first
@@ -739,7 +742,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (mine) load_here(dst, map, ip, 2 * (int)rank + c, pg, smem_addr(&ms.here[u]));
             if (rank == 0) warp_arrive(ms.full[u]);
           }
-          asked += 2;
+          asked += kPer;
           ++asked_units;
         }
       };
@@ -792,16 +795,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ================= the tail: zeros behind the last token that is seen =================
       if (n > 0) {
         const int t = n - 1, p0 = (r0 + t) * kTok;
-        // the tile's values are the fragment's last two units, its last four slots
-        for (int g = 0; g < 2; ++g) {
-          const int p = p0 + 128 * g;
-          if (p + 128 <= end) continue;
-          const uint32_t u = (5u * (t_base + n) - 2u + g) % kUnits;
+        // the tile's values are the fragment's last kValues units, its last four slots
+        for (int g = 0; g < S::kValues; ++g) {
+          const int p = p0 + 64 * kPer * g;
+          if (p + 64 * kPer <= end) continue;
+          const uint32_t u = ((uint32_t)(S::kKeys + S::kValues) * (t_base + n) - S::kValues + g) % kUnits;
           if (!(ok = warp_wait(ms.here[u], tails >> u & 1, abort_flag))) break;
           tails ^= 1u << u;
           const int first = max(0, end - p);
-          for (int i = first * 16 + lane; i < 128 * 16; i += 32) {  // row i / 16: eight chunks of either 128 dims
-            const uint32_t sl = (9u * (t_base + n) - 4u + 2 * g + (i >> 10)) % kSlots;
+          for (int i = first * 16 + lane; i < 64 * kPer * 16; i += 32) {  // row i / 16: eight chunks of either 128 dims
+            const uint32_t sl = (9u * (t_base + n) - 4u + kPer * g + (i >> 10)) % kSlots;
             sts128(ring + sl * kSlotBytes + 8192 * (i >> 3 & 1) + (i >> 4 & 63) * 128 + (i & 7) * 16, 0u, 0u, 0u, 0u);
           }
           fence_async_smem();
