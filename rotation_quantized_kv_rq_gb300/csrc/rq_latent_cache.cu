@@ -64,6 +64,13 @@ __device__ __forceinline__ void turn4(float (&x)[4], const Turn& u) {
   for (int i = 0; i < 4; ++i) x[i] = fmaf(y[i], u.s[i], x[i] * u.c[i]);
 }
 
+// s += x; returns what the rounding leaves.
+__device__ __forceinline__ float plus(float& s, float x) {
+  const float sum = s + x, of_x = sum - s, left = (s - (sum - of_x)) + (x - of_x);
+  s = sum;
+  return left;
+}
+
 template <typename T>
 __device__ __forceinline__ void widen4(float (&x)[4], const uint2& w) {
   const float2 a = unpack2<T>(w.x), b = unpack2<T>(w.y);
@@ -143,12 +150,17 @@ __global__ void __launch_bounds__(kThreads) latent_append_kernel(const LatentPoo
 #pragma unroll
     for (int i = 0; i < 16; ++i) part4[i & 3] = fmaf(x[i], x[i], part4[i & 3]);
     float ss = (part4[0] + part4[1]) + (part4[2] + part4[3]);
+    // The sum, the factor and the products with what their roundings leave, the last rounded to odd, so that a code moves only for a
+    // value within some 2^-27 of the middle of two: a step of 2^-4 multiplies what rounding moves.
+    float ss_lo = 0.f;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    // The factor and the products with what their roundings leave, so that a code moves only for a value within some 2^-25 of the
-    // middle of two: a step of 2^-4 multiplies what rounding moves.
-    const float m = fmaf(ss, 1.f / kLatentDim, a.eps), r = __frsqrt_rn(m);
-    const float mr = m * r, r_lo = 0.5f * r * (fmaf(-mr, r, 1.f) - fmaf(m, r, -mr) * r);
+    for (int o = 16; o > 0; o >>= 1) {
+      const float other = __shfl_xor_sync(0xffffffffu, ss, o), lo = o < 16 ? __shfl_xor_sync(0xffffffffu, ss_lo, o) : 0.f;
+      ss_lo = (ss_lo + lo) + plus(ss, other);
+    }
+    float m = ss * (1.f / kLatentDim);
+    const float m_lo = fmaf(ss_lo, 1.f / kLatentDim, plus(m, a.eps)), r = __frsqrt_rn(m);
+    const float mr = m * r, r_lo = 0.5f * r * (fmaf(-mr, r, 1.f) - fmaf(m, r, -mr) * r - m_lo * r * r);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const float4 w4 = __ldg(reinterpret_cast<const float4*>(a.weight) + 4 * lane + i);
@@ -156,7 +168,8 @@ __global__ void __launch_bounds__(kThreads) latent_append_kernel(const LatentPoo
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const float y = x[4 * i + k] * wt[k], y_lo = fmaf(x[4 * i + k], wt[k], -y);
-        x[4 * i + k] = fmaf(y, r, fmaf(y, r_lo, y_lo * r));
+        // (the factor is a square root's: a product that is a float to the last bit is rare, and may go either way from a middle)
+        x[4 * i + k] = __uint_as_float(__float_as_uint(__fmaf_rz(y, r, fmaf(y, r_lo, y_lo * r))) | 1u);
       }
     }
   }

@@ -168,6 +168,32 @@ def test_append_range_and_faults(dtype):
     cache.append(t[:0, :512], t[:0, 512:], int32([]))
 
 
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_append_norm_of_rows_apart(dtype):
+    """With the norm: a row of zeros, one value in a row, values far apart, and (bf16) squares past float32's range, which are not
+    finite."""
+    dtype, P = DT[dtype], 16
+    rows = np.zeros((4, 576))
+    rows[1, 7] = -3.0
+    rows[2, :512] = 2.0 ** -10
+    rows[2, 100] = 4096.0
+    rows[3, :512] = 1.0 if dtype == torch.float16 else 2.0 ** 100
+    t, w, eps = dev(rows, dtype), dev(np.full(512, 1.5), torch.float32), 1e-6
+    cache = make(1, P, 1, dtype)
+    before = cache.pages.cpu().numpy().copy()
+    cache.append(t[:, :512], t[:, 512:], int32([3, 0, 9, 15]), weight=w, eps=eps)
+    x = host(t)[:, :512]
+    x = x / np.sqrt((x * x).mean(-1, keepdims=True) + eps) * 1.5
+    want = {}
+    for i, s in enumerate((3, 0, 9, 15)):
+        e = L.exponent(np.abs(x[i]).max(), 0.0)
+        want[s] = (x[i], NORM_ERR * np.abs(x[i])), (np.zeros(64), np.zeros(64)), e
+    if dtype == torch.bfloat16:
+        want[15] = None
+    check_pool(cache, before, want, "norm")
+    assert int(cache.status.item()) == (rq.RQ_STATUS_NOT_FINITE if dtype == torch.bfloat16 else 0)
+
+
 def test_append_refuses():
     cache = make(4, 16, 4, torch.float16)
     x = torch.zeros(6, 576, dtype=torch.float16, device="cuda")
