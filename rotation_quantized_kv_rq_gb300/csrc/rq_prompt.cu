@@ -21,6 +21,9 @@
 // all units cut into one even range a pair, pairs at unrelated places: 1 x 16,384 x 16 heads 846 -> 1,419 us.)  Where units
 // are few, or the last ones leave pairs idle, they are cut into parts, whose (m, l, out) a second kernel joins.
 // Every wait is bounded: one that runs out sets RQ_STATUS_TIMEOUT and an abort flag every role polls.
+//
+// Device time, bf16: 1 x 16,384 x 16 heads 848 us (1,620 TFLOP/s, 84% of the burst rate), 4 x 512 over 7,680 x 64 heads 447 us
+// (1,490, 77%), 8,192 x 8 heads 120 us; six prompts of 1 to 400 x 5 heads fp16 23 us, the opening, 6 tiles at most and the join.
 #include <math_constants.h>
 
 #include <algorithm>
@@ -112,7 +115,7 @@ struct Cut {
 
 // dual: calls of no more than 256 queries a sequence.  They fill one block only: both blocks take them, one the even tiles and
 // one the odd, so that here too one is on the tensor cores while the other is in its softmax; joined at the end.  2 x 100
-// rows over 4,000 x 128 heads 250 -> 180 us.  (As a choice of each unit's in one kernel it cost the others 3 to 4%.)
+// rows over 4,000 x 128 heads 250 -> 177 us.  (As a choice of each unit's in one kernel it cost the others 3 to 4%.)
 template <typename T, bool dual>
 __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_constant__ Maps maps, const PromptArgs a, const Cut cut) {
   extern __shared__ uint8_t smem_raw[];

@@ -728,6 +728,32 @@ def test_on_another_stream_and_captured():
     assert torch.equal(out, want)
 
 
+def test_outputs_over_inputs():
+    """Attention may write over its latent queries; an output over other inputs is refused."""
+    for T in (1, 3):
+        case = Case(3, [5000, 40, 700], T, 60, 16, torch.bfloat16)  # (cut, and of several units)
+        case.q_c = case.q_c.contiguous()
+        want, q = case.run(), case.q_c.clone()
+        assert case.run(q_c=q, out=q) is q and torch.equal(q, want)
+    big = torch.zeros(3 * 3 * 60 * 512 + 512, dtype=torch.bfloat16, device="cuda")
+    for bad in (dict(q_c=big[:-512].view(3, 3, 60, 512), out=big[512:].view(3, 3, 60, 512)),
+                dict(q_pe=big[:3 * 3 * 60 * 64].view(3, 3, 60, 64), out=big[:-512].view(3, 3, 60, 512)),
+                dict(q_c=big[:-512].view(3, 60, 3, 512).transpose(1, 2), out=big[:-512].view(3, 3, 60, 512))):
+        with pytest.raises(rq.RQError) as e:
+            case.run(**bad)
+        assert e.value.code == rq.RQ_ERR_INVALID
+    rows = torch.zeros(64 * 1024, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(rq.RQError) as e:
+        case.cache.read(dev(case.table[:1]), int32([0, 40]), 40, c=rows[:40 * 512].view(40, 512), k_pe=rows[512:512 + 40 * 64].view(40, 64))
+    assert e.value.code == rq.RQ_ERR_INVALID
+    q, k, pe, v, qo, ko = prompt_case(2, [30], [10], 2, torch.float16)
+    k, v = k.contiguous(), v.contiguous()
+    for out in (k[10:], v[:30], q.flatten()[:30 * 256].view(30, 2, 128)):
+        with pytest.raises(rq.RQError) as e:
+            rq.prompt_attention(q, k, pe, v, int32(qo), int32(ko), 30, out=out)
+        assert e.value.code == rq.RQ_ERR_INVALID
+
+
 def test_views_of_the_pool():
     case = Case(2, [20], 1, 1, 32, torch.float16)
     codes, part, byte = L.unpack(case.pages, 32, torch.float16)
