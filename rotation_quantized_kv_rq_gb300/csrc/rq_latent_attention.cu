@@ -468,6 +468,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t k = t_base + t, buf = k & 1;
         if (idle) {  // takes part in the counts; O(t - 1) says that the last count is over
           if (t > 0 && !(ok = warp_wait(ms.o_done, k - 1, abort_flag))) break;
+          if (!(ok = warp_wait(ms.sc_full[buf], k >> 1, abort_flag))) break;  // (or its count could end twice before the scales' warp looks)
           warp_arrive(ms.sc_empty[buf]);
           warp_arrive_pair(peer_addr(smem_addr(&ms.p_full), 0));
           continue;

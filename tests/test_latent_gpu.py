@@ -332,6 +332,22 @@ def test_tree(dtype, lens, T, heads, P):
 
 
 @pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("heads", [1, 16, 33, 128])
+def test_attention_over_many_tiles(dtype, heads):
+    """Many tiles to a pair of SMs, whose second SM may have no rows: the tokens over and over, which changes no softmax."""
+    case = Case(5, [2048], 1, heads, 64, DT[dtype])
+    times, batch = 12, 40
+    cache = make(heads, 64, case.pages.shape[0], DT[dtype], batch=batch, max_pages_per_seq=32 * times)
+    cache.pages.copy_(case.cache.pages)
+    table = dev(np.tile(case.table[:, :32], (batch, times)))
+    every = lambda x: x.expand(batch, -1, -1, -1).contiguous()  # noqa: E731
+    out = cache.verify(every(case.q_c), every(case.q_pe), table, int32([2048 * times] * batch))
+    assert int(cache.status.item()) == 0
+    for b in (0, 17, batch - 1):
+        case.check(out[b:b + 1], what=f"sequence {b}")
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
 def test_attention_scales_and_queries(dtype):
     """Scales far apart in one sequence, queries of any size, zero rows, large scores."""
     dtype = DT[dtype]
