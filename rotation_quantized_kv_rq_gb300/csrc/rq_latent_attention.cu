@@ -28,8 +28,8 @@
 // Every wait is bounded: one that runs out sets RQ_STATUS_TIMEOUT and an abort flag every role polls.
 //
 // Device time: 64 x 16,384 x 128 heads bf16 217 us (1,344 TFLOP/s, 70% of the 16-bit rate), fp16 (three pieces) 287; 32 x 1K-32K x
-// 16 heads bf16 89 us (3.2 TB/s: MMAs of M = 128 for 16 rows); verify 8 x 16K + 4 x 32 heads fp16 71; 1 x 1,024 x 16 heads fp16
-// 16 us, a chain of latencies: lengths, queries, first copies, scores, weights, output, join.  A tile's 68 MMAs (bf16) take
+// 16 heads bf16 81 us (3.6 TB/s: MMAs of M = 128 for 16 rows); verify 8 x 16K + 4 x 32 heads fp16 71; 1 x 1,024 x 16 heads fp16
+// 14 us, a chain of latencies: lengths, queries, first copies, scores, weights, output, join.  A tile's 68 MMAs (bf16) take
 // 4,433 cycles of 6,000 to 7,000: the softmax's tensor memory and shared memory accesses and the copies slow them.  Pages of 16
 // tokens (boxes of 2 KB) take 20% more than of 64.
 #include <math_constants.h>
@@ -74,12 +74,20 @@ constexpr size_t kSlotFloats = (size_t)kUnitRows * kLatentDim + 2 * kUnitRows;
 // A CTA has 64 rows of an MMA.  Where a unit has no more than 64 rows in all (RC = 32 to a CTA) operands are kept for 32: an MMA
 // finds whatever follows in the place of the rest, rows whose results nobody reads, and the ring has 10 or 8 slots, more than
 // a tile or nearly, instead of 7 or 4.
-template <typename T, int RC>
+//
+// Where it has no more than 32 (RV = 16 rows to a CTA, of RC = 32 kept), the queries' first two pieces are different rows of one
+// operand, row r and r + 16, whose scores the softmax adds: half the MMAs for scores.  (Weights are pieces of two types, and
+// one MMA's operand is of one.)  The lanes of the two rows then take 16 columns of 32 each, which halves the softmax, and the
+// weights go to the first row's place.  32 x 1K-32K x 16 heads bf16 89 -> 81 us, fp16 113 -> 98,
+// 1 x 1,024 15.9 -> 14.3.
+template <typename T, int RC, int RV>
 struct Shape {
-  static constexpr int kPieces = std::is_same<T, __half>::value ? 3 : 2;
+  static constexpr int kPieces = std::is_same<T, __half>::value ? 3 : 2, kQueryPieces = RV < RC ? kPieces - 1 : kPieces;
   static constexpr uint32_t kRowsBytes = RC * 128;  // a chunk of 128 dims, or of 128 tokens' weights
-  static constexpr uint32_t kPieceQ = 4 * kRowsBytes, kQBytes = kPieces * kPieceQ + kRowsBytes;  // [piece][4 chunks][RC rows], position parts
-  static constexpr uint32_t kPieceP = 2 * kRowsBytes, kPBytes = kPieces * kPieceP;               // [piece][2 halves of 128 tokens][RC rows]
+  static constexpr uint32_t kPieceQ = 4 * kRowsBytes, kQBytes = kQueryPieces * kPieceQ + kRowsBytes;  // [piece][4 chunks][RC rows], position parts
+  static constexpr uint32_t kPieceP = 2 * kRowsBytes, kTileP = kPieces * kPieceP;                // [piece][2 halves of 128 tokens][RC rows]
+  static constexpr int kTilesP = RC < 64 ? 2 : 1;  // weights of two tiles, where there is room: one's are written while the other's are read
+  static constexpr uint32_t kPBytes = kTilesP * kTileP;
   static constexpr uint32_t kOffMisc = 221184, kOffP = kQBytes, kOffRing = kOffP + kPBytes;
   static constexpr int kSlots = (kOffMisc - kOffRing) / kSlotBytes;
   static constexpr int kPer = kSlots < 5 ? 1 : 2, kKeys = 4 / kPer + 1, kValues = 4 / kPer;  // slots of a unit, units of a tile
@@ -93,9 +101,9 @@ struct Frag {           // tiles r0 .. r0 + n - 1 of one unit
 };
 struct Misc {
   // the leader's: a unit is full; the queries; W(t); a tail's zeros are written
-  uint64_t full[kUnits], q_full, p_full, tail_done[kUnits];
+  uint64_t full[kUnits], q_full, p_full[2], tail_done[kUnits];
   // both CTAs': a unit is read; S(t); O(t); drained; a unit of the tail is here; scales of a tile
-  uint64_t empty[kUnits], s_full[2], o_done, drain, here[kUnits], sc_full[2], sc_empty[2];
+  uint64_t empty[kUnits], s_full[2], o_done[2], drain, here[kUnits], sc_full[2], sc_empty[2];
   Frag f;
   uint32_t tmem;
   int abort;
@@ -103,7 +111,7 @@ struct Misc {
   float top[2][4][64];
   float q_scale[64];
 };
-constexpr int kSmem = (int)(Shape<__half, 64>::kOffMisc + sizeof(Misc)) + 1024;
+constexpr int kSmem = (int)(Shape<__half, 64, 64>::kOffMisc + sizeof(Misc)) + 1024;
 static_assert(kSmem + 128 <= 232448, "one CTA's shared memory");
 
 struct Unit {
@@ -204,12 +212,13 @@ __device__ __forceinline__ int query_exp(uint32_t top_c, uint32_t top_p) {
   return min(max(max(c, p), -100), 100);
 }
 
-template <typename T, int RC>
+template <typename T, int RC, int RV>
 __global__ void __launch_bounds__(kThreads, 1)
     latent_kernel(const __grid_constant__ CUtensorMap map, const LatentPool pool, const LatentAttnArgs a, int box, int4* info) {
-  using S = Shape<T, RC>;
-  constexpr int kUR = 2 * RC;  // rows of a unit
-  constexpr int NP = S::kPieces, kSlots = S::kSlots, kPer = S::kPer;
+  using S = Shape<T, RC, RV>;
+  constexpr bool kTwice = RV < RC;  // a row stands in two places
+  constexpr int kUR = 2 * RV;       // rows of a unit
+  constexpr int NP = S::kPieces, NQ = S::kQueryPieces, kSlots = S::kSlots, kPer = S::kPer;
   constexpr bool kF16 = std::is_same<T, __half>::value;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t base = smem_addr(smem_raw) + (1024 - (smem_addr(smem_raw) & 1023) & 1023);
@@ -230,13 +239,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(smem_addr(&ms.tail_done[i]), 2);
     }
     mbar_init(smem_addr(&ms.q_full), 2 * kSoftWarps);
-    mbar_init(smem_addr(&ms.p_full), 2 * kSoftWarps);
     for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_addr(&ms.p_full[i]), 2 * kSoftWarps);
+      mbar_init(smem_addr(&ms.o_done[i]), 1);
       mbar_init(smem_addr(&ms.s_full[i]), 1);
       mbar_init(smem_addr(&ms.sc_full[i]), 1);
       mbar_init(smem_addr(&ms.sc_empty[i]), kSoftWarps);
     }
-    mbar_init(smem_addr(&ms.o_done), 1);
     mbar_init(smem_addr(&ms.drain), 1);
     ms.abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -344,7 +353,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tmem = *(volatile uint32_t*)&ms.tmem;
     const int b = ms.f.b, r0 = ms.f.r0, len = ms.f.len, end = ms.f.end;
     const int n = end > 0 ? ms.f.n : 0;  // tiles with tokens
-    const long long urow = (long long)ms.f.rt * kUR + RC * (int)rank + row;  // the thread's query row
+    const long long urow = (long long)ms.f.rt * kUR + RV * (int)rank + (kTwice ? row % RV : row);  // the thread's query row
     const bool valid = row < RC && urow < n_rows;
     const int j = valid ? (int)((uint32_t)urow / (uint32_t)a.heads) : 0, head = valid ? (int)((uint32_t)urow % (uint32_t)a.heads) : 0;
     const uint32_t t_base = done_tiles;
@@ -353,13 +362,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (warp < kSoftWarps) {
       float q_scale = 0.f;
-      if (n > 0) {
+      if (n > 0 && (!kTwice || 4 * warp < RV)) {
         // ---- queries as pieces: kRW rows to a warp, a lane 16 dims and an eighth of a position part of every fourth row ----
-        constexpr int kRW = RC / kSoftWarps;
+        constexpr int kRW = kTwice ? 4 : RC / kSoftWarps;
         // lane l: where row l % kRW of the warp's stands, -1 past the last row
         long long c_at = -1, pe_at = -1;
         {
-          const long long u = (long long)ms.f.rt * kUR + RC * (int)rank + kRW * warp + lane % kRW;
+          const long long u = (long long)ms.f.rt * kUR + RV * (int)rank + kRW * warp + lane % kRW;
           if (u < n_rows) {
             const uint32_t jj = (uint32_t)u / (uint32_t)a.heads, hh = (uint32_t)u - jj * (uint32_t)a.heads;
             const long long token = (long long)b * a.T + jj;
@@ -434,7 +443,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
 #pragma unroll
             for (int p = 0; p < NP; ++p)
-              sts128(q_ops + p * S::kPieceQ + S::kRowsBytes * (lane >> 3) + sw128(row0 + r, lane & 7), piece[p][0], piece[p][1], piece[p][2], piece[p][3]);
+              sts128(q_ops + (kTwice ? p >> 1 : p) * S::kPieceQ + S::kRowsBytes * (lane >> 3) + sw128(row0 + r + (kTwice ? RV * (p & 1) : 0), lane & 7),
+                     piece[p][0], piece[p][1], piece[p][2], piece[p][3]);
+            if constexpr (kTwice && NP > 2)  // a third piece has no other beside it
+              sts128(q_ops + S::kPieceQ + S::kRowsBytes * (lane >> 3) + sw128(row0 + r + RV, lane & 7), 0u, 0u, 0u, 0u);
 #pragma unroll
             for (int i = 0; i + 1 < kRW; ++i) raw[i][0] = raw[i + 1][0], raw[i][1] = raw[i + 1][1];  // (four rows' code, not eight)
           }
@@ -445,14 +457,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float2 f = rope::unpack2<T>(word(pe, k));
             w[k] = pe_down == 0.f ? 0u : rope::pack2<T>(f.x * pe_down, f.y * pe_down);
           }
-          sts128(q_ops + NP * S::kPieceQ + sw128(row0 + (lane >> 3), lane & 7), w[0], w[1], w[2], w[3]);
+          sts128(q_ops + NQ * S::kPieceQ + sw128(row0 + (lane >> 3), lane & 7), w[0], w[1], w[2], w[3]);
+          if constexpr (kTwice) sts128(q_ops + NQ * S::kPieceQ + sw128(row0 + (lane >> 3) + RV, lane & 7), 0u, 0u, 0u, 0u);
         }
         fence_async_smem();
       }
       if (n > 0) {
         warp_arrive_pair(peer_addr(smem_addr(&ms.q_full), 0));
         soft_sync();  // the rows' scales are there
-        if (row < RC) q_scale = ms.q_scale[row];
+        if (row < RC) q_scale = ms.q_scale[kTwice ? row % RV : row];
       }
       // ================= softmax =================
       // Scores 16 columns at a time, twice: loops over them and not 64 columns in a row, so that the roles' code fits the
@@ -464,13 +477,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (a.T < 64) mask &= (1ull << a.T) - 1ull;
       const bool idle = !__any_sync(0xffffffffu, valid);  // (all four warps of the rows alike)
       const uint32_t s_cols = tmem + lane_off + kColS + 64 * col_half;
+      constexpr int kStep = kTwice ? 32 : 16;
+      const int own = kTwice ? lane & 16 : 0;  // the lane's 16 columns of a step
+      constexpr int kBack = S::kTilesP;
+      auto o_is_done = [&](uint32_t k) { return warp_wait(ms.o_done[k & 1], k >> 1, abort_flag); };  // O(k), counted over fragments
       for (int t = 0; t < n; ++t) {
         const uint32_t k = t_base + t, buf = k & 1;
-        if (idle) {  // takes part in the counts; O(t - 1) says that the last count is over
-          if (t > 0 && !(ok = warp_wait(ms.o_done, k - 1, abort_flag))) break;
-          if (!(ok = warp_wait(ms.sc_full[buf], k >> 1, abort_flag))) break;  // (or its count could end twice before the scales' warp looks)
+        const uint32_t p_tile = p_ops + (kBack > 1 ? buf * S::kTileP : 0u);
+        if (idle) {  // takes part in the counts; O(t - kTilesP) says that the last count is over, the scales that theirs is
+          if (t >= kBack && !(ok = o_is_done(k - kBack))) break;
+          if (!(ok = warp_wait(ms.sc_full[buf], k >> 1, abort_flag))) break;
           warp_arrive(ms.sc_empty[buf]);
-          warp_arrive_pair(peer_addr(smem_addr(&ms.p_full), 0));
+          warp_arrive_pair(peer_addr(smem_addr(&ms.p_full[buf]), 0));
           continue;
         }
         const int t0 = (r0 + t) * kTok + 64 * quarter;
@@ -481,22 +499,31 @@ __global__ void __launch_bounds__(kThreads, 1)
         {
           const uint64_t q2 = pair(q_scale, q_scale);
 #pragma unroll 1
-          for (int c = 0; c < 64; c += 16) {  // score + E
-            float v[16];
+          for (int c = 0; c < 64; c += kStep) {  // score + E
+            float v[16], other[16];
             tmem_ld16(s_cols + 128 * buf + c, v);
-            const ulonglong2* const ks = reinterpret_cast<const ulonglong2*>(&ms.ks[buf][64 * quarter + c]);
-            const ulonglong2* const ev = reinterpret_cast<const ulonglong2*>(&ms.ev[buf][64 * quarter + c]);
+            if constexpr (kTwice) tmem_ld16(s_cols + 128 * buf + c + 16, other);
+            const ulonglong2* const ks = reinterpret_cast<const ulonglong2*>(&ms.ks[buf][64 * quarter + c + own]);
+            const ulonglong2* const ev = reinterpret_cast<const ulonglong2*>(&ms.ev[buf][64 * quarter + c + own]);
             ulonglong2 f[4], e[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) f[i] = ks[i], e[i] = ev[i];
             tmem_wait_ld();
             settle<16>(v);
+            if constexpr (kTwice) {
+              settle<16>(other);
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                const float sent = __shfl_xor_sync(0xffffffffu, own ? v[i] : other[i], RV);
+                v[i] = (own ? other[i] : v[i]) + sent;
+              }
+            }
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               unpair(fma2(pair(v[4 * i], v[4 * i + 1]), mul2(f[i].x, q2), e[i].x), v[4 * i], v[4 * i + 1]);
               unpair(fma2(pair(v[4 * i + 2], v[4 * i + 3]), mul2(f[i].y, q2), e[i].y), v[4 * i + 2], v[4 * i + 3]);
             }
-            const int first = t0 + c - all;  // of the columns' tokens, counted from the first that the mask is for
+            const int first = t0 + c + own - all;  // of the columns' tokens, counted from the first that the mask is for
             if (first > -16) {
               const uint32_t seen = first >= 64 ? 0u : first >= 0 ? (uint32_t)(mask >> first) : (1u << -first) - 1u | (uint32_t)mask << -first;
 #pragma unroll
@@ -510,6 +537,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_st16(s_cols + 128 * buf + c, v);
           }
         }
+        if constexpr (kTwice) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, RV));
         ms.top[buf][quarter][row] = top;
         tmem_wait_st();
         rows_sync(quad & 1);
@@ -524,9 +552,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           l_run *= alpha;
         }
         const float from = m_run == kNone ? 0.f : m_run;
-        // O(t - 1) is done: its weights' place is free, and O may be scaled
-        if (t > 0) {
-          if (!(ok = warp_wait(ms.o_done, k - 1, abort_flag))) break;
+        // the weights' place is free behind O(t - kTilesP), and O may be scaled behind O(t - 1)
+        if (kBack > 1 && t >= kBack && !(ok = o_is_done(k - kBack))) break;
+        if (t > 0 && (kBack == 1 || move)) {
+          if (!(ok = o_is_done(k - 1))) break;
           if (move) {
             fence_after_sync();
 #pragma unroll 1
@@ -547,10 +576,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint64_t sum[2] = {0ull, 0ull};
           const uint64_t back = pair(-from, -from);
 #pragma unroll 1
-          for (int c = 0; c < 64; c += 16) {
+          for (int c = 0; c < 64; c += kStep) {
             float v[16];
             tmem_ld16(s_cols + 128 * buf + c, v);
-            const ulonglong2* const dn = reinterpret_cast<const ulonglong2*>(&ms.dn[buf][64 * quarter + c]);
+            const ulonglong2* const dn = reinterpret_cast<const ulonglong2*>(&ms.dn[buf][64 * quarter + c + own]);
             ulonglong2 d[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) d[i] = dn[i];
@@ -582,7 +611,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
 #pragma unroll
             for (int p = 0; p < NP; ++p)
-              sts128(p_ops + p * S::kPieceP + S::kRowsBytes * tok_half + sw128(row, 4 * col_half + (c >> 4)), piece[p][0], piece[p][1], piece[p][2],
+              sts128(p_tile + p * S::kPieceP + S::kRowsBytes * tok_half + sw128(kTwice ? row % RV : row, 4 * col_half + ((c + own) >> 4)), piece[p][0], piece[p][1], piece[p][2],
                      piece[p][3]);
           }
           float y[4];
@@ -593,9 +622,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         warp_arrive(ms.sc_empty[buf]);
         fence_async_smem();
         fence_before_sync();
-        warp_arrive_pair(peer_addr(smem_addr(&ms.p_full), 0));
+        warp_arrive_pair(peer_addr(smem_addr(&ms.p_full[buf]), 0));
       }
-      if (ok && n > 0) ok = warp_wait(ms.o_done, t_base + n - 1, abort_flag);
+      if (ok && n > 0) ok = o_is_done(t_base + n - 1);
       fence_after_sync();
     } else if (warp == kMmaWarp) {
       // ================= MMA issue: the leader's =================
@@ -625,8 +654,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (c % kPer == 0 && !take()) return;
             const uint32_t b_at = slot(), a_at = q_lo + S::kRowsBytes / 16 * c;
 #pragma unroll
-            for (int p = 0; p < NP; ++p) {
-              if (p + 1 == NP && c % kPer == kPer - 1) peek();
+            for (int p = 0; p < NQ; ++p) {
+              if (p + 1 == NQ && c % kPer == kPer - 1) peek();
 #pragma unroll
               for (int ks = 0; ks < 4; ++ks)
                 pair_mma_f8(d, a_at + (p * S::kPieceQ + 32 * ks) / 16, b_at + 2 * ks, id_s, p > 0 || ks > 0 ? 1u : (uint32_t)c);
@@ -635,11 +664,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (!take()) return;
           peek();
-          if (t > 0) p_look = warp_look(ms.p_full, t_base + t - 1);
+          if (t > 0) p_look = warp_look(ms.p_full[(t_base + t - 1) & 1], (t_base + t - 1) >> 1);
           const uint32_t b_at = slot();
 #pragma unroll
           for (int ks = 0; ks < 4; ++ks)
-            pair_mma_16(d, q_lo + (NP * S::kPieceQ + 32 * ks) / 16, b_at + 2 * ks, id_p);
+            pair_mma_16(d, q_lo + (NQ * S::kPieceQ + 32 * ks) / 16, b_at + 2 * ks, id_p);
           give();
           pair_commit(smem_addr(&ms.s_full[(t_base + t) & 1]), 3);
         };
@@ -650,8 +679,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int t = 0; t < n && ok; ++t) {
           p_look = 0;
           if (t + 1 < n) s_mmas(t + 1);
-          if (!ok || !(ok = warp_wait_after(p_look, ms.p_full, t_base + t, abort_flag))) break;
+          if (!ok || !(ok = warp_wait_after(p_look, ms.p_full[(t_base + t) & 1], (t_base + t) >> 1, abort_flag))) break;
           fence_after_sync();
+          const uint32_t w_tile = S::kTilesP > 1 ? ((t_base + t) & 1) * (S::kTileP / 16) : 0u;
 #pragma unroll 1
           for (int g = 0; g < 4; ++g) {  // 64 tokens
             if (g % kPer == 0) {
@@ -661,7 +691,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tails ^= 1u << (u % kUnits);
               }
             }
-            const uint32_t b_at = slot(), w_at = w_lo + (g >> 1) * (S::kRowsBytes / 16) + (g & 1) * 4;
+            const uint32_t b_at = slot(), w_at = w_lo + w_tile + (g >> 1) * (S::kRowsBytes / 16) + (g & 1) * 4;
 #pragma unroll
             for (int ks = 0; ks < 2; ++ks) {
               if (ks == 1 && g % kPer == kPer - 1) peek();
@@ -675,7 +705,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (g % kPer == kPer - 1) give();
           }
           if (!ok) break;
-          pair_commit(smem_addr(&ms.o_done), 3);
+          pair_commit(smem_addr(&ms.o_done[(t_base + t) & 1]), 3);
         }
         if (!ok && issued) {  // nothing may be running when the tensor memory is freed
           pair_commit(smem_addr(&ms.drain), 3);
@@ -831,12 +861,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp < kSoftWarps) {
       ms.top[0][quarter][row] = l_run;
       soft_sync();
-      const float l = (ms.top[0][0][row] + ms.top[0][1][row]) + (ms.top[0][2][row] + ms.top[0][3][row]);
+      float l = (ms.top[0][0][row] + ms.top[0][1][row]) + (ms.top[0][2][row] + ms.top[0][3][row]);
+      if constexpr (kTwice) l += __shfl_xor_sync(0xffffffffu, l, RV);
       const bool whole = ms.f.whole;
       const int sees = valid ? (a.tree_mask ? len - a.T - 1 : len - a.T + j) : -1;
       // a row that sees nothing is zero; one whose scores are all minus infinity is NaN
       const float empty = whole && sees >= 0 ? CUDART_NAN_F : 0.f, inv = whole ? 1.f / l : 1.f;
-      const int srow = RC * (int)rank + row, dim0 = 256 * tok_half + 128 * col_half;
+      const bool writes = valid && (!kTwice || lane < RV);
+      const int srow = RV * (int)rank + (kTwice ? row % RV : row), dim0 = 256 * tok_half + 128 * col_half;
       float* const slot = a.ws + (2ll * me + ((int)me == ms.f.range ? ms.f.range_last : 0)) * kSlotFloats;
       T* const out = reinterpret_cast<T*>(a.out) + (((size_t)b * a.T + j) * a.heads + head) * kLatentDim + dim0;
 #pragma unroll 2
@@ -850,7 +882,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
 #pragma unroll
         for (int i = 0; i < 16; ++i) y[i] = l == 0.f || n == 0 ? empty : y[i] * inv;
-        if (!valid) continue;
+        if (!writes) continue;
         if (whole) {
           uint4* const dst = reinterpret_cast<uint4*>(out) + 2 * c;
 #pragma unroll
@@ -864,7 +896,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
         }
       }
-      if (!whole && quarter == 0 && valid) {
+      if (!whole && quarter == 0 && writes) {
         slot[kUR * kLatentDim + srow] = m_run;
         slot[kUR * kLatentDim + kUR + srow] = l;
       }
@@ -934,7 +966,7 @@ __global__ void __launch_bounds__(256) latent_join_kernel(const LatentAttnArgs a
   *reinterpret_cast<uint2*>(out) = make_uint2(rope::pack2<T>(y.x, y.y), rope::pack2<T>(y.z, y.w));
 }
 
-template <typename T, int RC>
+template <typename T, int RC, int RV = RC>
 cudaError_t launch(const CUtensorMap& map, const LatentPool& pool, const LatentAttnArgs& a, int box, int num_sms, int4* info, long long units,
                    cudaStream_t stream) {
   const int pairs = num_sms / 2;
@@ -949,10 +981,10 @@ cudaError_t launch(const CUtensorMap& map, const LatentPool& pool, const LatentA
   cfg.stream = stream;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, latent_kernel<T, RC>, map, pool, a, box, info);
+  cudaError_t e = cudaLaunchKernelEx(&cfg, latent_kernel<T, RC, RV>, map, pool, a, box, info);
   if (e != cudaSuccess) return e;
   const long long rows = (long long)a.T * a.heads;
-  const int row_groups = (int)((rows < 2 * RC ? rows : 2 * RC) + 7) / 8;
+  const int row_groups = (int)((rows < 2 * RV ? rows : 2 * RV) + 7) / 8;
   if (units * row_groups > 0x7fffffffLL) return cudaErrorInvalidValue;
   const bool many = units * 8 <= pairs;  // eight parts a unit or more
   cudaLaunchAttribute behind[1];
@@ -964,8 +996,8 @@ cudaError_t launch(const CUtensorMap& map, const LatentPool& pool, const LatentA
   join.stream = stream;
   join.attrs = behind;
   join.numAttrs = 1;
-  return many ? cudaLaunchKernelEx(&join, latent_join_kernel<T, 8>, a, (const int4*)info, row_groups, 2 * RC)
-              : cudaLaunchKernelEx(&join, latent_join_kernel<T, 1>, a, (const int4*)info, row_groups, 2 * RC);
+  return many ? cudaLaunchKernelEx(&join, latent_join_kernel<T, 8>, a, (const int4*)info, row_groups, 2 * RV)
+              : cudaLaunchKernelEx(&join, latent_join_kernel<T, 1>, a, (const int4*)info, row_groups, 2 * RV);
 }
 
 }  // namespace
@@ -975,12 +1007,17 @@ size_t latent_attention_workspace(int num_sms, long long rows, int max_batch) {
   return parts + 4 * (size_t)((rows + kUnitRows - 1) / kUnitRows) * (size_t)max_batch;  // and a note for each unit
 }
 
-cudaError_t latent_attention_prepare() {
-  cudaError_t e = cudaFuncSetAttribute(latent_kernel<__half, 32>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-  if (e == cudaSuccess) e = cudaFuncSetAttribute(latent_kernel<__half, 64>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-  if (e == cudaSuccess) e = cudaFuncSetAttribute(latent_kernel<__nv_bfloat16, 32>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-  if (e == cudaSuccess) e = cudaFuncSetAttribute(latent_kernel<__nv_bfloat16, 64>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+template <typename T>
+static cudaError_t prepare() {
+  cudaError_t e = cudaFuncSetAttribute(latent_kernel<T, 32, 16>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(latent_kernel<T, 32, 32>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(latent_kernel<T, 64, 64>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   return e;
+}
+
+cudaError_t latent_attention_prepare() {
+  const cudaError_t e = prepare<__half>();
+  return e == cudaSuccess ? prepare<__nv_bfloat16>() : e;
 }
 
 cudaError_t launch_latent_attention(const LatentPool& pool, const LatentAttnArgs& a, int num_sms, cudaStream_t stream) {
@@ -996,12 +1033,14 @@ cudaError_t launch_latent_attention(const LatentPool& pool, const LatentAttnArgs
                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
     return cudaErrorInvalidValue;
   int4* const info = reinterpret_cast<int4*>(a.ws + 2 * (size_t)(num_sms / 2) * kSlotFloats);
-  const bool few = (long long)a.T * a.heads <= 64;
-  if (pool.bf16)
-    return few ? launch<__nv_bfloat16, 32>(map, pool, a, box, num_sms, info, units, stream)
-               : launch<__nv_bfloat16, 64>(map, pool, a, box, num_sms, info, units, stream);
-  return few ? launch<__half, 32>(map, pool, a, box, num_sms, info, units, stream)
-             : launch<__half, 64>(map, pool, a, box, num_sms, info, units, stream);
+  const long long rows = (long long)a.T * a.heads;
+  const auto of_type = [&](auto t) {
+    using T = decltype(t);
+    return rows <= 32   ? launch<T, 32, 16>(map, pool, a, box, num_sms, info, units, stream)
+           : rows <= 64 ? launch<T, 32>(map, pool, a, box, num_sms, info, units, stream)
+                        : launch<T, 64>(map, pool, a, box, num_sms, info, units, stream);
+  };
+  return pool.bf16 ? of_type(__nv_bfloat16()) : of_type(__half());
 }
 
 }  // namespace rq
