@@ -4,8 +4,8 @@
 // append: y = c / sqrt(mean c^2 + eps) w, p = rot(k_pe), E the least exponent with |y| <= 448 2^E and |p| <= 2^15 2^E; codes
 // e4m3(y 2^-E), parts p 2^-E in 16 bits.  A row is a warp's, 16 dims to a lane, so that sums and maxima stay in it and a token's
 // bytes are written by one warp.  In long calls the warp turns the token's queries too, with the angles it has; in short ones
-// they have warps of their own (64 tokens x 128 heads: 2.8 us, a chain of latencies).  32,768 tokens x 16 heads: 41.6 us, 4.6 TB/s, 70%
-// of the copy rate, bound by instruction issue (72%).
+// they have warps of their own (64 tokens x 128 heads: 2.8 us, a chain of latencies).  32,768 tokens x 16 heads: 44 us, 4.4 TB/s, 66%
+// of the copy rate, bound by instruction issue.
 // read: a warp takes eight rows, whose bytes are in flight together: 16 x 1K-16K tokens in 48 us, 5.2 TB/s, 78%.
 #include "../../include/rq.h"
 #include "rq_block.cuh"
@@ -78,6 +78,14 @@ __device__ __forceinline__ float plus(float& s, float x) {
   return left;
 }
 
+// Two sums; `left` gathers what the roundings leave.
+__device__ __forceinline__ void plus2(uint64_t& s, uint64_t x, uint64_t& left) {
+  asm("{\n .reg .b64 sum, of_x, of_s, a, b;\n add.rn.f32x2 sum, %0, %2;\n sub.rn.f32x2 of_x, sum, %0;\n sub.rn.f32x2 of_s, sum, of_x;\n"
+      " sub.rn.f32x2 a, %0, of_s;\n sub.rn.f32x2 b, %2, of_x;\n add.rn.f32x2 a, a, b;\n add.rn.f32x2 %1, %1, a;\n mov.b64 %0, sum;\n}"
+      : "+l"(s), "+l"(left)
+      : "l"(x));
+}
+
 template <typename T>
 __device__ __forceinline__ void widen4(float (&x)[4], const uint2& w) {
   const float2 a = unpack2<T>(w.x), b = unpack2<T>(w.y);
@@ -114,7 +122,7 @@ __device__ __forceinline__ void turn_heads(const LatentAppendArgs& a, long long 
 // Warp (token, part): part 0 codes the token's latent and position part, part i turns queries of heads per * (i - 1) .. ; with
 // one part, that warp turns all of them.
 template <typename T, bool INTERLEAVED>
-__global__ void __launch_bounds__(kThreads) latent_append_kernel(const LatentPool pool, const LatentAppendArgs a, int parts, int per) {
+__global__ void __launch_bounds__(kThreads, 4) latent_append_kernel(const LatentPool pool, const LatentAppendArgs a, int parts, int per) {
   const int lane = threadIdx.x & 31, j = lane & 15, half = lane >> 4;
   const long long w = ((long long)blockIdx.x * kThreads + threadIdx.x) >> 5;
   const long long t = parts == 1 ? w : w / parts;
@@ -153,16 +161,29 @@ __global__ void __launch_bounds__(kThreads) latent_append_kernel(const LatentPoo
     }
   }
   if (a.weight) {
-    float part4[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int i = 0; i < 16; ++i) part4[i & 3] = fmaf(x[i], x[i], part4[i & 3]);
-    float ss = (part4[0] + part4[1]) + (part4[2] + part4[3]);
     // The sum, the factor and the products with what their roundings leave, the last rounded to odd, so that a code moves only for a
-    // value within some 2^-27 of the middle of two: a step of 2^-4 multiplies what rounding moves.
-    float ss_lo = 0.f;
+    // value at the very middle of two: a step of 2^-4 multiplies what rounding moves.  Of 16.8 million codes none is off the
+    // definition's; with plain float32 sums and products 3 to 17 were (41 us, with these 44).
+    float ss, ss_lo;
+    {
+      uint64_t sum[2], left = 0ull;  // squares of values of 8 or 11 bits are exact
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint64_t v = f2(x[2 * i], x[2 * i + 1]), q = mul2(v, v);
+        if (i < 2)
+          sum[i] = q;
+        else
+          plus2(sum[i & 1], q, left);
+      }
+      plus2(sum[0], sum[1], left);
+      float other, other_lo;
+      split2(sum[0], ss, other);
+      split2(left, ss_lo, other_lo);
+      ss_lo += other_lo + plus(ss, other);
+    }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
-      const float other = __shfl_xor_sync(0xffffffffu, ss, o), lo = o < 16 ? __shfl_xor_sync(0xffffffffu, ss_lo, o) : 0.f;
+      const float other = __shfl_xor_sync(0xffffffffu, ss, o), lo = __shfl_xor_sync(0xffffffffu, ss_lo, o);
       ss_lo = (ss_lo + lo) + plus(ss, other);
     }
     float m = ss * (1.f / kLatentDim);
