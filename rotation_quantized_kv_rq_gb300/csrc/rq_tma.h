@@ -1,4 +1,4 @@
-// Tensor maps of the TMA copies: the driver's encoder, found at run time (the library links the runtime alone).
+// Tensor maps of the TMA copies: CUDA's encoder, found at run time (the library links the runtime alone).
 #pragma once
 
 #include <cuda.h>
