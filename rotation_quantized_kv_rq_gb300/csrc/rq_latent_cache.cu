@@ -6,7 +6,7 @@
 // bytes are written by one warp.  In long calls the warp turns the token's queries too, with the angles it has; in short ones
 // they have warps of their own (64 tokens x 128 heads: 2.8 us, a chain of latencies).  32,768 tokens x 16 heads: 44 us, 4.4 TB/s, 66%
 // of the copy rate, bound by instruction issue.
-// read: a warp takes eight rows, whose bytes are in flight together: 16 x 1K-16K tokens in 48 us, 5.2 TB/s, 78%.
+// read: a warp takes four rows, whose bytes are in flight together: 16 x 1K-16K tokens in 44 us, 5.7 TB/s, 85%; 1,500 in 3.2.
 #include "../../include/rq.h"
 #include "rq_block.cuh"
 #include "rq_latent.cuh"
@@ -236,8 +236,9 @@ __global__ void __launch_bounds__(kThreads, 4) latent_append_kernel(const Latent
   if (lane == 0) page[640 * P + r] = (uint8_t)(bad ? kNanExp : e + 127);
 }
 
-// A warp reads eight rows: their sequences and pages are looked up by a lane each, then their bytes are in flight together.
-constexpr int kRows = 8;
+// A warp reads four rows: their sequences and pages are looked up by a lane each, then their bytes are in flight together.  (Eight,
+// with half the warps: 48 us where four take 44.)
+constexpr int kRows = 4;
 template <typename T>
 __global__ void __launch_bounds__(kThreads) latent_read_kernel(const LatentPool pool, const LatentReadArgs a) {
   const int lane = threadIdx.x & 31, P = pool.page_size;
@@ -281,6 +282,14 @@ __global__ void __launch_bounds__(kThreads) latent_read_kernel(const LatentPool 
       scale[i] = scale_of_byte(__ldg(page + 640 * P + ri));
     }
   }
+  uint4 part[kRows / 4];  // four rows at a time, a chunk of eight values to a lane
+#pragma unroll
+  for (int i = 0; i < kRows; i += 4) {
+    const int k = i + (lane >> 3);
+    const uint8_t* page = reinterpret_cast<const uint8_t*>(__shfl_sync(0xffffffffu, (unsigned long long)at, k));
+    const int rk = __shfl_sync(0xffffffffu, r, k);
+    if (there >> k & 1) part[i / 4] = __ldg(reinterpret_cast<const uint4*>(page + 512 * P + chunk_at(rk, lane & 7)));
+  }
   T* const c = reinterpret_cast<T*>(a.c);
 #pragma unroll
   for (int i = 0; i < kRows; ++i) {
@@ -297,23 +306,19 @@ __global__ void __launch_bounds__(kThreads) latent_read_kernel(const LatentPool 
     dst[0] = make_uint4(y[0], y[1], y[2], y[3]);
     dst[1] = make_uint4(y[4], y[5], y[6], y[7]);
   }
-  // position parts: four rows at a time, a chunk of eight values to a lane
 #pragma unroll
   for (int i = 0; i < kRows; i += 4) {
-    const int k = i + (lane >> 3), chunk = lane & 7;
-    const uint8_t* page = reinterpret_cast<const uint8_t*>(__shfl_sync(0xffffffffu, (unsigned long long)at, k));
-    const int rk = __shfl_sync(0xffffffffu, r, k);
+    const int q4 = lane >> 3, k = i + q4;
     if (!(there >> k & 1)) continue;
-    const uint4 v = __ldg(reinterpret_cast<const uint4*>(page + 512 * P + chunk_at(rk, chunk)));
-    const float s = scale_of_byte(__ldg(page + 640 * P + rk));
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    const float s = q4 < 2 ? (q4 == 0 ? scale[i] : scale[i + 1]) : (q4 == 2 ? scale[i + 2] : scale[i + 3]);
+    const uint32_t w[4] = {part[i / 4].x, part[i / 4].y, part[i / 4].z, part[i / 4].w};
     uint32_t y[4];
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       const float2 f = unpack2<T>(w[q]);
       y[q] = pack2<T>(f.x * s, f.y * s);
     }
-    *reinterpret_cast<uint4*>(reinterpret_cast<T*>(a.k_pe) + (size_t)(row0 + k) * kPositionDim + 8 * chunk) =
+    *reinterpret_cast<uint4*>(reinterpret_cast<T*>(a.k_pe) + (size_t)(row0 + k) * kPositionDim + 8 * (lane & 7)) =
         make_uint4(y[0], y[1], y[2], y[3]);
   }
 }
