@@ -312,7 +312,8 @@ def test_attention(dtype, lens, T, heads, P):
 
 
 @pytest.mark.parametrize("dtype", ["f16", "bf16"])
-@pytest.mark.parametrize("lens,T,heads,P", [([13, 500, 77], 13, 20, 32), ([64, 300], 64, 3, 16), ([2], 2, 1, 16), ([9000, 260], 7, 16, 64)])
+@pytest.mark.parametrize("lens,T,heads,P", [([13, 500, 77], 13, 20, 32), ([64, 300], 64, 3, 16), ([2], 2, 1, 16), ([9000, 260], 7, 16, 64),
+                                            ([500, 40, 6], 6, 5, 16), ([2000, 31], 16, 2, 32), ([1025], 20, 3, 64)])
 def test_tree(dtype, lens, T, heads, P):
     """Random trees, with a row that sees no draft and, in a sequence of drafts only, a row that sees nothing."""
     case = Case(T, lens, T, heads, P, DT[dtype])
@@ -387,9 +388,10 @@ def test_attention_heavy_token_beside_many_light_ones(dtype):
     assert np.abs(out[..., :2] - 0.5).max() < 2.0 ** -9, out[..., :2]
 
 
-def test_attention_nan_tokens_reach_rows_that_see_them():
+@pytest.mark.parametrize("heads", [3, 8, 30])
+def test_attention_nan_tokens_reach_rows_that_see_them(heads):
     """A token stored as NaN among the drafts, and garbage behind the sequence."""
-    case = Case(9, [270, 300], 6, 30, 16, torch.bfloat16)
+    case = Case(9, [270, 300], 6, heads, 16, torch.bfloat16)
     clean = case.run()
     bad = case.slots(0, np.array([270 - 6 + 3]))[0]
     case.pages[bad // 16, 640 * 16 + bad % 16] = 255
@@ -403,15 +405,16 @@ def test_attention_nan_tokens_reach_rows_that_see_them():
 
 @pytest.mark.parametrize("dtype", ["f16", "bf16"])
 @pytest.mark.parametrize("value", [math.nan, math.inf, -math.inf])
-def test_attention_queries_not_finite(dtype, value):
-    case = Case(4, [600, 0], 2, 70, 16, DT[dtype])
+@pytest.mark.parametrize("heads", [10, 30, 70])
+def test_attention_queries_not_finite(dtype, value, heads):
+    case = Case(4, [600, 0], 2, heads, 16, DT[dtype])
     clean = case.run()
     case.q_c[0, 1, 2, 7] = value
-    case.q_pe[0, 0, 69, 3] = value
+    case.q_pe[0, 0, heads - 1, 3] = value
     case.q_c[1, 0, 0, 0] = value
     out = case.run()
-    hit = torch.zeros(2, 2, 70, dtype=torch.bool, device="cuda")
-    hit[0, 1, 2] = hit[0, 0, 69] = True
+    hit = torch.zeros(2, 2, heads, dtype=torch.bool, device="cuda")
+    hit[0, 1, 2] = hit[0, 0, heads - 1] = True
     assert torch.isnan(out[hit]).all() and torch.equal(out[~hit], clean[~hit])
     assert not out[1].any()
 
