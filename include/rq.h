@@ -474,7 +474,8 @@ int rq_latent_append(rq_latent *ctx, const rq_rope *rope, const void *c, long lo
  * cached tokens (append them first): a decode step (T = 1), a chain of drafts (tree_mask NULL: row j sees positions
  * 0 .. seq_lens[b] - T + j) or a tree of them (device uint64 [B][T], T <= 64: row j sees the prefix and draft i exactly when bit
  * i of tree_mask[b][j] is set).  A row that sees no token gives zeros.
- *   q_c, q_pe   rows of num_heads heads, 512 and 64 elements, of B * T tokens
+ *   q_c, q_pe   rows of num_heads heads, 512 and 64 elements, of B * T tokens.  A row with an infinity or NaN, or whose largest
+ *               value times sm_scale is past float32, is NaN if it sees a token
  *   pages, block_table, max_pages, seq_lens   as rq_decode_attention
  *   out         device [B][T][num_heads][512], 16-byte aligned; may be q_c itself, other overlaps with the queries are refused
  * 0 < seq_lens[b] < T sets RQ_STATUS_BAD_LEN.  Calls on one context must not overlap on the GPU.

@@ -34,6 +34,7 @@
 // tokens (boxes of 2 KB) take 20% more than of 64.
 #include <math_constants.h>
 
+#include <cfloat>
 #include <cstddef>
 #include <type_traits>
 
@@ -205,11 +206,13 @@ __device__ __forceinline__ uint64_t plus2(uint64_t a, uint64_t b) {
   return d;
 }
 
-// The smallest E in [-100, 100] with top <= 448 * 2^E, or top <= 2^(15 + E), from top's bits.
+// The smallest E of -126 and more with top_c <= 448 * 2^E and top_p <= 2^(15 + E), from their bits.  The largest bf16 number's is
+// 120, and from -126 on even the smallest one, 2^-133, is a multiple of e4m3's smallest step: a row of any finite magnitude fits
+// its pieces.
 __device__ __forceinline__ int query_exp(uint32_t top_c, uint32_t top_p) {
   const int c = (int)(top_c >> 23) - 127 - 8 + ((top_c & 0x7FFFFFu) > 0x600000u ? 1 : 0);
   const int p = (int)(top_p >> 23) - 127 - 15 + ((top_p & 0x7FFFFFu) != 0u ? 1 : 0);
-  return min(max(max(c, p), -100), 100);
+  return max(max(c, p), -126);
 }
 
 template <typename T, int RC, int RV>
@@ -412,10 +415,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool odd = max(top_c, top_r) >= (kF16 ? 0x7C00u : 0x7F80u);  // a row that is not finite: all its scores are NaN
             const float2 tops = rope::unpack2<T>(top_c | top_r << 16);
             // (fp16: 2^(-e - 8) is a factor in fp16; what is below 2^-20 of 448 has few bits)
-            const int e = odd ? 0 : max(query_exp(__float_as_uint(tops.x), __float_as_uint(tops.y)), kF16 ? -20 : -100);
+            const int e = odd ? 0 : max(query_exp(__float_as_uint(tops.x), __float_as_uint(tops.y)), kF16 ? -20 : -126);
             const float down = block::pow2(-e);
             if ((lane >> 3) == r) pe_down = odd ? 0.f : down;
-            if (lane == 0) ms.q_scale[row0 + r] = odd ? CUDART_NAN_F : a.sm_scale * 1.44269504088896340736f * block::pow2(e);
+            // (a factor past float32: the row's largest value times sm_scale is too)
+            const float factor = a.sm_scale * (1.44269504088896340736f * block::pow2(e));
+            if (lane == 0) ms.q_scale[row0 + r] = odd || factor > FLT_MAX ? CUDART_NAN_F : factor;
             uint32_t piece[NP][4];
             const float down8 = down * 0.00390625f;  // 2^-8: as next_piece wants it
             const uint32_t down8_2 = rope::pack2<__half>(down8, down8);
@@ -519,9 +524,9 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              unpair(fma2(pair(v[4 * i], v[4 * i + 1]), mul2(f[i].x, q2), e[i].x), v[4 * i], v[4 * i + 1]);
-              unpair(fma2(pair(v[4 * i + 2], v[4 * i + 3]), mul2(f[i].y, q2), e[i].y), v[4 * i + 2], v[4 * i + 3]);
+            for (int i = 0; i < 4; ++i) {  // the token's scale first: it takes no sum out of range, where the two factors' product may be
+              unpair(fma2(mul2(pair(v[4 * i], v[4 * i + 1]), f[i].x), q2, e[i].x), v[4 * i], v[4 * i + 1]);
+              unpair(fma2(mul2(pair(v[4 * i + 2], v[4 * i + 3]), f[i].y), q2, e[i].y), v[4 * i + 2], v[4 * i + 3]);
             }
             const int first = t0 + c + own - all;  // of the columns' tokens, counted from the first that the mask is for
             if (first > -16) {

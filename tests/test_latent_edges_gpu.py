@@ -1,0 +1,65 @@
+"""Latent attention where its calls can go wrong, on the GPU against the float64 definitions of latent_ref."""
+import numpy as np
+import pytest
+import torch
+
+from tests import block_ref as R
+from tests import latent_ref as L
+from tests.test_latent_gpu import DT, Case, dev, gen, host, int32, make, within
+
+pytestmark = pytest.mark.gpu
+
+# a weight's pieces in the absorbed form, rounded to fp16 before
+PIECES = {torch.bfloat16: 2.0 ** -8 + 2.0 ** -11, torch.float16: 2.0 ** -12 + 2.0 ** -11}
+
+
+# --------------------------------------------------------------------------- the absorbed form
+
+@pytest.mark.parametrize("heads", [9, 30, 70])
+@pytest.mark.parametrize("power", [-120, 98, 107, 109, 118, 127])
+def test_bf16_queries_of_any_magnitude(power, heads):
+    """Queries of some 2^power against a scale of 2^-power.  Both are exact, so the definition is that of ordinary queries and a
+    scale of 1; and the kernel splits a row by its own power of two, so its error is too."""
+    case = Case(power & 7, [300, 20], 2, heads, 16, torch.bfloat16, sm_scale=2.0 ** -power, gain=0.07 * 2.0 ** power)
+    if power == 127:
+        case.q_c[0, 1, 0, 5] = torch.finfo(torch.bfloat16).max
+    out = case.run()
+    ref, tol = L.attention(host(case.q_c) * 2.0 ** -power, host(case.q_pe) * 2.0 ** -power, case.pages, case.table, case.lens, case.P,
+                           L.chain(2), 1.0, torch.bfloat16)
+    within(host(out), ref, tol + R.half_step(torch.bfloat16, ref) * (1 + 2.0 ** -8))
+
+
+@pytest.mark.parametrize("heads", [9, 30, 70])
+@pytest.mark.parametrize("power", [40, 90, 125])
+def test_large_queries_across_large_latents(power, heads):
+    """Query and latents of the largest magnitudes whose products are all zero: the mean of the latents.  The scales of the two
+    multiply past float32's range."""
+    rng, n, P, dtype = gen(power), 300, 16, torch.bfloat16
+    c = rng.standard_normal((n, 512)) * 2.0 ** 66
+    c[:, 0] = 0.0
+    pages = np.zeros((n // P + 1, 641 * P), np.uint8)
+    L.put(pages, P, np.arange(n), c, np.zeros((n, 64)), dtype)
+    codes, _, byte = L.unpack(pages, P, dtype)
+    c = (codes * L.scale(byte)[:, None])[:n]
+    assert byte[:n].max() == 127 + 60
+    cache = make(heads, P, len(pages), dtype, batch=1, sm_scale=1.0)
+    cache.pages.copy_(torch.from_numpy(pages))
+    q_c = torch.zeros(1, heads, 512, dtype=dtype, device="cuda")
+    q_c[..., 0] = 2.0 ** power
+    out = host(cache.decode(q_c, q_c.new_zeros(1, heads, 64), int32(np.arange(len(pages)))[None], int32([n])))
+    ref = np.broadcast_to(c.mean(0), out.shape)
+    tol = (PIECES[dtype] + 2.0 ** -20) * np.abs(c).mean(0)
+    within(out, ref, tol + R.half_step(dtype, ref) * (1 + 2.0 ** -8))
+
+
+@pytest.mark.parametrize("heads", [9, 30, 70])
+def test_queries_times_scale_past_float32(heads):
+    """A row whose largest value times sm_scale is past float32 is NaN; the others are as they were."""
+    case = Case(2, [300, 20], 2, heads, 16, torch.bfloat16, sm_scale=2.0 ** 20, gain=0.07 * 2.0 ** -20)
+    clean = case.run()
+    case.q_c[0, 1, 3] = 2.0 ** 125
+    case.q_pe[1, 0, 2] = -2.0 ** 127
+    out = case.run()
+    hit = torch.zeros(2, 2, heads, dtype=torch.bool, device="cuda")
+    hit[0, 1, 3] = hit[1, 0, 2] = True
+    assert torch.isnan(out[hit]).all() and torch.equal(out[~hit], clean[~hit]) and torch.isfinite(clean).all()
