@@ -552,8 +552,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         float alpha = 1.f;
         const bool move = __any_sync(0xffffffffu, above > kReach);
         if (above > kReach) {
-          alpha = ex2(m_run - (top - kLift));
-          m_run = top - kLift;
+          float to = top - kLift;
+          if (top - to > kReach) to = top;  // (float32's steps are 16 apart from 2^27 on: a lift of 16 would take the weight past fp16)
+          alpha = ex2(m_run - to);
+          m_run = to;
           l_run *= alpha;
         }
         const float from = m_run == kNone ? 0.f : m_run;

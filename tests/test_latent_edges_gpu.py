@@ -63,3 +63,26 @@ def test_queries_times_scale_past_float32(heads):
     hit = torch.zeros(2, 2, heads, dtype=torch.bool, device="cuda")
     hit[0, 1, 3] = hit[1, 0, 2] = True
     assert torch.isnan(out[hit]).all() and torch.equal(out[~hit], clean[~hit]) and torch.isfinite(clean).all()
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("heads", [3, 25, 70])
+@pytest.mark.parametrize("power", [20, 24, 25, 26, 27, 28, 29, 33])
+def test_attention_scores_of_any_magnitude(dtype, heads, power):
+    """Scores up to 2^power and (in units of the exponential's) past it, whose largest rises through the tiles: the token with
+    the largest has all the weight, however coarse float32's steps are there."""
+    rng, n, P, dtype = gen(power), 600, 16, DT[dtype]
+    c = rng.integers(-7, 8, (n, 512)) / 8.0
+    c[:, 0], c[:, 1] = 0.25, 1.0
+    c[5, 0], c[300, 0], c[599, 0] = 0.5, 0.75, 1.0
+    pages = np.zeros((n // P + 1, 641 * P), np.uint8)
+    L.put(pages, P, np.arange(n), c, np.zeros((n, 64)), dtype)
+    cache = make(heads, P, len(pages), dtype, batch=1, sm_scale=2.0 ** power)
+    cache.pages.copy_(torch.from_numpy(pages))
+    q_c = torch.zeros(1, heads, 512, dtype=dtype, device="cuda")
+    q_c[..., 0] = 1.0
+    table = int32(np.arange(len(pages)))[None]
+    for length, top in ((600, 599), (599, 300), (300, 5)):
+        out = host(cache.decode(q_c, q_c.new_zeros(1, heads, 64), table, int32([length])))
+        ref = np.broadcast_to(c[top], out.shape)
+        within(out, ref, (PIECES[dtype] + 2.0 ** -20) * np.abs(ref) + R.half_step(dtype, ref), f"{length} tokens")
