@@ -51,7 +51,9 @@ constexpr uint32_t kQBytes = 6 * kChunk, kKBytes = 3 * kChunk / 2, kVBytes = kCh
 constexpr uint32_t kColS = 256;
 constexpr float kLift = 7.f, kReach = 15.f;      // weights are 2^(score - m), m between maximum - kReach and maximum - kLift
 constexpr float kNone = -3.402823466e38f;        // m before any visible key
-constexpr float kLarge = 1048576.f;              // |maximum| from which weights are formed in two roundings
+// |maximum| from which weights are formed in two roundings: m comes from the rounded product, and a weight from an exact one would be
+// off by half of a step there, a factor of 2^(2^-4) at 2^20, past fp16's range from 2^24 on
+constexpr float kLarge = 1048576.f;
 
 struct Misc {
   // the leader's: K(t), V(t), the queries are there; [block] W(t); the values' warps are through with a tile
@@ -209,7 +211,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
 #pragma unroll
         for (int i = 0; i < 4; ++i) top[i] = c + 4 + i < kTok ? max3(top[i], s[c + i], s[c + 4 + i]) : fmaxf(top[i], s[c + i]);
       }
-      const float most = fmaxf(max3(top[0], top[1], top[2]), top[3]) * scale;
+      const float most = __fmul_rn(fmaxf(max3(top[0], top[1], top[2]), top[3]), scale);
       const float above = most - (m_run == kNone ? -CUDART_INF_F : m_run);  // (NaN where nothing is seen: no move)
       if (__any_sync(0xffffffffu, above > kReach)) {
         float alpha = 1.f;
@@ -232,11 +234,15 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
           }
         }
       }
-      if (__any_sync(0xffffffffu, fabsf(from) > kLarge)) {  // the difference needs the rounded product
+      {
+        uint64_t f = pair(scale, scale);
+        const uint64_t d = pair(-from, -from);
+        if (__any_sync(0xffffffffu, fabsf(from) > kLarge)) {  // products rounded as the maximum's, not in one operation with the difference
+          const uint64_t none = pair(-0.f, -0.f);
 #pragma unroll
-        for (int c = 0; c < kTok; ++c) s[c] = s[c] * scale - from;
-      } else {
-        const uint64_t f = pair(scale, scale), d = pair(-from, -from);
+          for (int c = 0; c < kTok; c += 2) fma2(s[c], s[c + 1], f, none);
+          f = pair(1.f, 1.f);
+        }
 #pragma unroll
         for (int c = 0; c < kTok; c += 2) fma2(s[c], s[c + 1], f, d);
       }

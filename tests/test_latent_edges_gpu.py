@@ -3,6 +3,7 @@ import numpy as np
 import pytest
 import torch
 
+from rotation_quantized_kv_rq_gb300 import rq
 from tests import block_ref as R
 from tests import latent_ref as L
 from tests.test_latent_gpu import DT, Case, dev, gen, host, int32, make, within
@@ -86,3 +87,20 @@ def test_attention_scores_of_any_magnitude(dtype, heads, power):
         out = host(cache.decode(q_c, q_c.new_zeros(1, heads, 64), table, int32([length])))
         ref = np.broadcast_to(c[top], out.shape)
         within(out, ref, (PIECES[dtype] + 2.0 ** -20) * np.abs(ref) + R.half_step(dtype, ref), f"{length} tokens")
+
+
+# ---------------------------------------------------------------------------- the expanded form
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("power", [-4, -1, 0, 1, 2, 3, 4, 8, 12])
+def test_prompt_scores_of_any_magnitude(dtype, power):
+    """Queries and keys of some 2,000, each query the same as its own key: that key's value is the result, however coarse float32's
+    steps are at scores of 2^25 to 2^41."""
+    rng, new, old, heads, dtype = gen(power + 20), 200, 300, 2, DT[dtype]
+    q = dev(2000 * rng.standard_normal((new, heads, 192)), dtype)
+    k = dev(2000 * rng.standard_normal((old + new, heads, 128)), dtype)
+    k[old:] = q[..., :128]
+    v = dev(rng.standard_normal((old + new, heads, 128)), dtype)
+    out = rq.prompt_attention(q, k, k.new_zeros(old + new, 64), v, int32([0, new]), int32([0, old + new]), new, sm_scale=2.0 ** power)
+    ref = host(v[old:])  # (the exponential is off by 2^-20 at most)
+    within(host(out), ref, 2.0 ** -20 * np.abs(ref) + R.half_step(dtype, ref))
