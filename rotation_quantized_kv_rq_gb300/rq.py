@@ -201,6 +201,22 @@ def _stream(stream, device) -> int:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _empty(shape, dtype, device, stream, result=True):
+    """A tensor that a call on `stream` writes first.  It is the stream's own memory: the current stream's would still be used by
+    what is queued there and was freed since.  result: the caller gets it, and uses it on the current stream."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        raw = int(getattr(stream, "cuda_stream", stream))  # 0, and CUDA's name for it, 1: the default stream
+        stream = torch.cuda.ExternalStream(raw, device) if raw > 1 else torch.cuda.default_stream(device)
+    user = torch.cuda.current_stream(device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if result and user != stream:
+        t.record_stream(user)
+    return t
+
+
 def rq_lloyd_max_codebook(bits: int, head_dim: int = HEAD_DIM) -> np.ndarray:
     out = np.zeros(1 << bits, np.float32)
     _check("rq_lloyd_max_codebook",
@@ -765,7 +781,7 @@ class LatentCache:
             if q_pe.dim() != 3 or not _rows_ok(q_pe, (n, q_pe.shape[1], POSITION_DIM), dtype, index):
                 raise RQError(name, RQ_ERR_INVALID)
             if q_pe_out is None:
-                q_pe_out = torch.empty(q_pe.shape, dtype=dtype, device=self.device)
+                q_pe_out = _empty(q_pe.shape, dtype, self.device, stream)
             elif not _rows_ok(q_pe_out, q_pe.shape, dtype, index):
                 raise RQError(name, RQ_ERR_INVALID)
         elif q_pe_out is not None:
@@ -788,7 +804,7 @@ class LatentCache:
                                             tree_mask.get_device() != index))):
             raise RQError("rq_latent_attention", RQ_ERR_INVALID)
         if out is None:
-            out = torch.empty(shape, dtype=dtype, device=self.device)
+            out = _empty(shape, dtype, self.device, stream)
         elif not _rows_ok(out, shape, dtype, index) or not out.is_contiguous():
             raise RQError("rq_latent_attention", RQ_ERR_INVALID)
         if B == 0:
@@ -821,11 +837,11 @@ class LatentCache:
                 (starts is not None and not _ints(starts, B, index))):
             raise RQError(name, RQ_ERR_INVALID)
         if c is None:
-            c = torch.empty((n, LATENT_DIM), dtype=dtype, device=self.device)
+            c = _empty((n, LATENT_DIM), dtype, self.device, stream)
         elif not _rows_ok(c, (n, LATENT_DIM), dtype, index) or not c.is_contiguous():
             raise RQError(name, RQ_ERR_INVALID)
         if k_pe is None:
-            k_pe = torch.empty((n, POSITION_DIM), dtype=dtype, device=self.device)
+            k_pe = _empty((n, POSITION_DIM), dtype, self.device, stream)
         elif not _rows_ok(k_pe, (n, POSITION_DIM), dtype, index) or not k_pe.is_contiguous():
             raise RQError(name, RQ_ERR_INVALID)
         if B and n:
@@ -882,18 +898,16 @@ def prompt_attention(q, k, k_pe, v, q_offsets, k_offsets, max_new, sm_scale=0.0,
             (status is not None and (status.dtype is not torch.int32 or status.get_device() != index))):
         raise RQError(name, RQ_ERR_INVALID)
     if out is None:
-        out = torch.empty((nq, heads, 128), dtype=dtype, device=q.device)
+        out = _empty((nq, heads, 128), dtype, q.device, stream)
     elif not _rows_ok(out, (nq, heads, 128), dtype, index) or not out.is_contiguous():
         raise RQError(name, RQ_ERR_INVALID)
     nbytes = _prompt_bytes.get(index)
     if nbytes is None:
         nbytes = _prompt_bytes[index] = rq_prompt_workspace(index)
-    workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+    workspace = _empty(nbytes, torch.uint8, q.device, stream, result=False)
     if index != torch.cuda.current_device():
         with torch.cuda.device(index):
             rq_prompt_attention(q, k, k_pe, v, q_offsets, k_offsets, max_new, out, workspace, sm_scale, status, stream)
     else:
         rq_prompt_attention(q, k, k_pe, v, q_offsets, k_offsets, max_new, out, workspace, sm_scale, status, stream)
-    if stream is not None:  # not the current one: the workspace stays its own until the call is through there
-        workspace.record_stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream)))
     return out

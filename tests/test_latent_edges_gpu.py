@@ -6,7 +6,7 @@ import torch
 from rotation_quantized_kv_rq_gb300 import rq
 from tests import block_ref as R
 from tests import latent_ref as L
-from tests.test_latent_gpu import DT, Case, dev, gen, host, int32, make, within
+from tests.test_latent_gpu import DT, Case, check_prompt, dev, gen, host, int32, make, prompt_case, within
 
 pytestmark = pytest.mark.gpu
 
@@ -104,3 +104,79 @@ def test_prompt_scores_of_any_magnitude(dtype, power):
     out = rq.prompt_attention(q, k, k.new_zeros(old + new, 64), v, int32([0, new]), int32([0, old + new]), new, sm_scale=2.0 ** power)
     ref = host(v[old:])  # (the exponential is off by 2^-20 at most)
     within(host(out), ref, 2.0 ** -20 * np.abs(ref) + R.half_step(dtype, ref))
+
+
+# ------------------------------------------------------------------------------------ streams
+
+def beside(call, nbytes):
+    """call(stream) while the current stream has yet to read memory of nbytes that is free again on the host's side: what the call
+    allocates for itself is not that memory."""
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    want = call(s)
+    torch.cuda.synchronize()
+    want = [t.clone() for t in (want if isinstance(want, tuple) else (want,))]
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    taken, kept = torch.full((nbytes,), 5, dtype=torch.uint8, device="cuda"), torch.zeros(nbytes, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    torch.cuda._sleep(400_000_000)  # some 0.2 s
+    kept.copy_(taken)
+    del taken
+    got = call(s)
+    s.synchronize()
+    torch.cuda.synchronize()
+    assert (kept == 5).all()
+    for a, b in zip(got if isinstance(got, tuple) else (got,), want):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("raw", [False, True])
+def test_stream_argument_of_the_prompt(raw):
+    """The call's own workspace and output are not memory that the current stream still uses.  (Cut, so that it has parts.)"""
+    q, k, pe, v, qo, ko = prompt_case(3, [64, 2], [5000, 3000], 2, torch.bfloat16)
+    qo, ko = int32(qo), int32(ko)
+    run = lambda s: rq.prompt_attention(q, k, pe, v, qo, ko, 64, stream=s.cuda_stream if raw else s)  # noqa: E731
+    beside(run, rq.rq_prompt_workspace(0))
+    out = run(torch.cuda.Stream())
+    with torch.cuda.stream(torch.cuda.Stream()):
+        zero = rq.prompt_attention(q, k, pe, v, qo, ko, 64, stream=0)
+    torch.cuda.synchronize()
+    assert torch.equal(zero, out)
+    check_prompt(out, q, k, pe, v, qo.tolist(), ko.tolist(), torch.bfloat16)
+
+
+def test_stream_argument_of_the_cache():
+    case = Case(5, [400, 70, 33, 9], 1, 128, 16, torch.float16)
+    cache, tab, lens = case.cache, dev(case.table), dev(case.lens)
+    q_c, q_pe = case.q_c[:, 0].contiguous(), case.q_pe[:, 0].contiguous()
+    beside(lambda s: cache.decode(q_c, q_pe, tab, lens, stream=s), q_c.numel() * 2)
+    beside(lambda s: cache.read(tab, int32([0, 400, 470, 503, 512]), 512, stream=s), 512 * 1024)
+    n, rope = 200, rq.Rope(64)
+    x, q = dev(gen(1).standard_normal((n, 576)), torch.float16), dev(gen(2).standard_normal((n, 128, 64)), torch.float16)
+    slots, pos = torch.full((n,), -1, dtype=torch.int32, device="cuda"), torch.arange(n, dtype=torch.int32, device="cuda")
+    beside(lambda s: cache.append(x[:, :512], x[:, 512:], slots, rope, pos, q_pe=q, stream=s), n * 128 * 128)
+
+
+def test_stream_argument_while_captured():
+    """On the capturing stream and on one forked from it."""
+    q, k, pe, v, qo, ko = prompt_case(3, [64, 2], [5000, 3000], 2, torch.bfloat16)
+    qo, ko = int32(qo), int32(ko)
+    case = Case(5, [400, 70, 33, 9], 1, 20, 16, torch.float16)
+    q_c, q_pe, tab, lens = case.q_c[:, 0].contiguous(), case.q_pe[:, 0].contiguous(), dev(case.table), dev(case.lens)
+    run = lambda s: (rq.prompt_attention(q, k, pe, v, qo, ko, 64, stream=s), case.cache.decode(q_c, q_pe, tab, lens, stream=s))  # noqa: E731
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    run(torch.cuda.current_stream())
+    with torch.cuda.graph(graph):
+        current = torch.cuda.current_stream()
+        first = run(current)
+        side.wait_stream(current)
+        second = run(side)
+        current.wait_stream(side)
+    for t in (q, v, q_c):
+        t.copy_(torch.randn_like(t))
+    graph.replay()
+    torch.cuda.synchronize()
+    for a, b, c in zip(first, second, run(None)):
+        assert torch.equal(a, c) and torch.equal(b, c)
