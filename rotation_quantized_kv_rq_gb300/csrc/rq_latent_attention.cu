@@ -167,8 +167,16 @@ __device__ __forceinline__ void load_here(uint32_t dst, const CUtensorMap& map, 
       : "memory");
 }
 __device__ __forceinline__ void soft_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
-// The four warps that share 32 rows.
-__device__ __forceinline__ void rows_sync(int half) { asm volatile("bar.sync %0, 128;" ::"r"(2 + half) : "memory"); }
+// The four warps that share 32 rows meet: whether all of them are ok.  One whose wait ran out comes here too, once, before it leaves,
+// and the others leave behind it: this barrier has no limit of its own.
+__device__ __forceinline__ bool rows_agree(int half, bool ok) {
+  uint32_t all;
+  asm volatile("{\n .reg .pred p, q;\n setp.ne.u32 q, %2, 0;\n bar.red.and.pred p, %1, 128, q;\n selp.u32 %0, 1, 0, p;\n}"
+               : "=r"(all)
+               : "r"(2 + half), "r"((uint32_t)ok)
+               : "memory");
+  return all;
+}
 
 // Pieces of two weights (fp16, 0 to 2^12) in few operations of the integer and fp16 pipes (a conversion to 8 bits takes 14
 // cycles of a scheduler, these two).  e5m2 is an fp16 number's upper byte: the first piece is the number rounded to that, its
@@ -497,8 +505,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           continue;
         }
         const int t0 = (r0 + t) * kTok + 64 * quarter;
-        if (!(ok = warp_wait(ms.s_full[buf], k >> 1, abort_flag))) break;
-        if (!(ok = warp_wait(ms.sc_full[buf], k >> 1, abort_flag))) break;
+        ok = ok && warp_wait(ms.s_full[buf], k >> 1, abort_flag) && warp_wait(ms.sc_full[buf], k >> 1, abort_flag);
+        if (!ok) {
+          rows_agree(quad & 1, false);
+          break;
+        }
         fence_after_sync();
         float top = -CUDART_INF_F;
         {
@@ -545,7 +556,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if constexpr (kTwice) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, RV));
         ms.top[buf][quarter][row] = top;
         tmem_wait_st();
-        rows_sync(quad & 1);
+        if (!(ok = rows_agree(quad & 1, true))) break;
 #pragma unroll
         for (int i = 0; i < 4; ++i) top = fmaxf(top, ms.top[buf][i][row]);
         const float above = top - (m_run == kNone ? -CUDART_INF_F : m_run);  // (NaN where nothing is seen: no move)
@@ -559,10 +570,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           l_run *= alpha;
         }
         const float from = m_run == kNone ? 0.f : m_run;
-        // the weights' place is free behind O(t - kTilesP), and O may be scaled behind O(t - 1)
-        if (kBack > 1 && t >= kBack && !(ok = o_is_done(k - kBack))) break;
+        // the weights' place is free behind O(t - kTilesP), and O may be scaled behind O(t - 1) (a wait that runs out: to the next meeting)
+        if (kBack > 1 && t >= kBack && !(ok = o_is_done(k - kBack))) continue;
         if (t > 0 && (kBack == 1 || move)) {
-          if (!(ok = o_is_done(k - 1))) break;
+          if (!(ok = o_is_done(k - 1))) continue;
           if (move) {
             fence_after_sync();
 #pragma unroll 1
