@@ -270,12 +270,19 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t pairs = gridDim.x >> 1, me = blockIdx.x >> 1;
   uint32_t total, parts, each, more, x, x_end, at, item;  // at: where unit `item` begins
   Unit un;
+  auto range_of = [&](uint32_t tile) {  // the range that holds a tile
+    const uint32_t longer = more * (each + 1u);
+    return tile < longer ? tile / (each + 1u) : more + (tile - longer) / each;
+  };
   {
     __shared__ uint32_t s_sums[kThreads / 32], s_found[2];
     __shared__ Unit s_unit;
+    // a thread's units; the first ones are the last warps', which have the least to do while a unit opens
     const uint32_t n_items = (uint32_t)a.B * n_rt, chunk = (n_items + kThreads - 1) / kThreads;
+    const int order = kThreads / 32 - 1 - warp;
+    const uint32_t owner = 32 * order + lane;
     uint32_t mine = 0;
-    for (uint32_t i = tid * chunk; i < min(n_items, (tid + 1) * chunk); ++i)
+    for (uint32_t i = owner * chunk; i < min(n_items, (owner + 1) * chunk); ++i)
       mine += kOpen + unit_of(a, kUR, cap, (int)(i / (uint32_t)n_rt), (int)(i % (uint32_t)n_rt), blockIdx.x == 0).tiles;
     uint32_t sum = mine;  // inclusive, over the warp, then over the warps before
 #pragma unroll
@@ -283,13 +290,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t v = __shfl_up_sync(0xffffffffu, sum, o);
       if (lane >= o) sum += v;
     }
-    if (lane == 31) s_sums[warp] = sum;
+    if (lane == 31) s_sums[order] = sum;
     __syncthreads();
     uint32_t before = 0;
     total = 0;
 #pragma unroll
     for (int w = 0; w < kThreads / 32; ++w) {
-      if (w == warp) before = total;
+      if (w == order) before = total;
       total += s_sums[w];
     }
     parts = min(pairs, total);
@@ -298,7 +305,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     x_end = me < parts ? x + each + (me < more ? 1u : 0u) : x;  // (a pair without a range: done at once)
     before += sum - mine;
     if (x < x_end && x >= before && x < before + mine) {
-      uint32_t p = before, i = tid * chunk;
+      uint32_t p = before, i = owner * chunk;
       for (;; ++i) {
         un = unit_of(a, kUR, cap, (int)(i / (uint32_t)n_rt), (int)(i % (uint32_t)n_rt), false);
         if (x < p + kOpen + un.tiles) break;
@@ -312,11 +319,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     at = s_found[0];
     item = s_found[1];
     un = s_unit;
+    // A note for each unit, for the join: its first range, its parts (0: it is whole), whether it is the last of its first range.  The
+    // CTAs take the threads' units in turn and write their notes here, before any wait that can run out: the join finds every one.
+    if (owner % gridDim.x == blockIdx.x)
+      for (uint32_t i = owner * chunk, p = before; i < min(n_items, (owner + 1) * chunk); ++i) {
+        const uint32_t end = p + (chunk == 1 ? mine : kOpen + unit_of(a, kUR, cap, (int)(i / (uint32_t)n_rt), (int)(i % (uint32_t)n_rt), false).tiles);
+        const uint32_t first = range_of(p + kOpen), begins = first * each + min(first, more);
+        const bool whole = end <= begins + each + (first < more ? 1u : 0u);
+        info[i] = make_int4((int)first, whole ? 0 : (int)(range_of(end - 1) - first) + 1, begins < p, 0);
+        p = end;
+      }
   }
-  auto range_of = [&](uint32_t tile) {  // the range that holds a tile
-    const uint32_t longer = more * (each + 1u);
-    return tile < longer ? tile / (each + 1u) : more + (tile - longer) / each;
-  };
   bool first_frag = true;
 
   // softmax: row of the CTA (= lane of tensor memory, twice), the quarter of a tile's tokens and of the dims
@@ -346,8 +359,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t first = range_of(at + kOpen);  // (this one, where r0 is 0)
         f.range = (int)first;
         f.range_last = first * each + min(first, more) < at;
-        if (f.r0 == 0 && rank == 0)
-          info[item] = make_int4(f.range, f.whole ? 0 : (int)(range_of(at + kOpen + un.tiles - 1) - first) + 1, f.range_last, 0);
         x = at + kOpen + f.r0 + f.n;
         if (f.r0 + f.n == un.tiles) {
           at = x;
