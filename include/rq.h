@@ -460,8 +460,8 @@ typedef struct {
  *   c, k_pe     device, 16-byte aligned: token t at c + t * c_stride (512 elements) and k_pe + t * k_pe_stride (64);
  *               strides are multiples of 8
  *   q_pe        NULL, or the queries' position parts (64 elements a head, any number of heads)
- *   q_pe_out    with q_pe: where they go, itself for in place; other overlaps with the call's inputs are refused, and so is
- *               an output between the heads of q_pe
+ *   q_pe_out    with q_pe: where they go, itself for in place; other overlaps with the call's inputs are refused, and so are
+ *               an output between the heads of q_pe and rows that share elements with each other
  *   positions   device int32 [num_axes][n]; may be NULL without a rotation
  * n = 0 is a no-op.  Errors: RQ_ERR_INVALID, RQ_ERR_CUDA.
  */

@@ -62,6 +62,18 @@ bool overlap(const Span& a, const Span& b) {
   return d < a.row || d + b.row > a.stride;
 }
 
+// Whether two of the n tokens' rows of `dims` elements share some (strides at least dims, bad_rows says).
+bool rows_meet(const rq_heads* r, int dims, long long n) {
+  if (r->heads == 1 || n == 1) return false;
+  const long long s = r->stride, h = r->head_stride;
+  if ((s - dims) / h >= r->heads - 1 || (h - dims) / s >= n - 1) return false;  // all heads before the next token, or all tokens before the next head
+  for (long long d = 1; d < r->heads; ++d) {  // d heads on, k tokens back
+    const long long at = d * h, k = at / s;
+    if ((k >= 1 && k < n && at - k * s < dims) || (k + 1 < n && (k + 1) * s - at < dims)) return true;
+  }
+  return false;
+}
+
 rq::LatentPool pool_of(const rq_latent* ctx, const void* pages) {
   return rq::LatentPool{(const uint8_t*)pages, ctx->cfg.page_size, ctx->cfg.num_pages, ctx->cfg.io_type == RQ_BF16};
 }
@@ -132,7 +144,8 @@ int rq_latent_append(rq_latent* ctx, const rq_rope* rope, const void* c, long lo
   if (rope && (rope->table.rotary_dim > kPe || rope->device != ctx->device || (rope->table.rotary_dim > 0 && !positions)))
     return RQ_ERR_INVALID;
   if (q_pe) {
-    if (bad_rows(q_pe, kPe, n) || bad_rows(q_pe_out, kPe, n) || q_pe->heads != q_pe_out->heads) return RQ_ERR_INVALID;
+    if (bad_rows(q_pe, kPe, n) || bad_rows(q_pe_out, kPe, n) || q_pe->heads != q_pe_out->heads || rows_meet(q_pe_out, kPe, n))
+      return RQ_ERR_INVALID;
     const Span o = span(q_pe_out, kPe, n);
     const bool in_place = q_pe->x == q_pe_out->x && (n == 1 || q_pe->stride == q_pe_out->stride) &&
                           (q_pe->heads == 1 || q_pe->head_stride == q_pe_out->head_stride);

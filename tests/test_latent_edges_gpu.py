@@ -180,3 +180,24 @@ def test_stream_argument_while_captured():
     torch.cuda.synchronize()
     for a, b, c in zip(first, second, run(None)):
         assert torch.equal(a, c) and torch.equal(b, c)
+
+
+# ---------------------------------------------------------------------------------- refusals
+
+def test_append_refuses_outputs_over_themselves():
+    """Turned queries two of whose rows share elements; rows of tokens and heads that interleave do not."""
+    n, heads, cache = 6, 4, make(4, 16, 4, torch.float16)
+    x, buf = torch.zeros(n, 576, dtype=torch.float16, device="cuda"), torch.zeros(1 << 14, dtype=torch.float16, device="cuda")
+    q, slots = dev(gen(1).standard_normal((n, heads, 64)), torch.float16), int32(range(n))
+    call = lambda o, q=q: cache.append(x[:len(q), :512], x[:len(q), 512:], slots[:len(q)], q_pe=q, q_pe_out=o)  # noqa: E731
+    for strides in ((256, 64), (64, 384), (64 * 3, 64 * 20), (128 * 4, 128), (64, 64 * 7), (72, 440), (256, 1728), (192, 448), (320, 128)):
+        out = call(buf.as_strided((n, heads, 64), (*strides, 1)))
+        assert torch.equal(out, q), strides
+    for strides in ((64, 64), (128, 64), (192, 64), (64, 128), (64, 320), (248, 64), (72, 360), (256, 1024), (192, 128), (200, 64)):
+        for in_place in (False, True):
+            out = buf.as_strided((n, heads, 64), (*strides, 1))
+            with pytest.raises(rq.RQError) as e:
+                call(out, out if in_place else q)
+            assert e.value.code == rq.RQ_ERR_INVALID, strides
+    one = buf.as_strided((1, heads, 64), (8, 64, 1))  # a stride that is not used may be anything
+    assert torch.equal(call(one, q[:1]), q[:1])
