@@ -201,20 +201,28 @@ def _stream(stream, device) -> int:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
-def _empty(shape, dtype, device, stream, result=True):
-    """A tensor that a call on `stream` writes first.  It is the stream's own memory: the current stream's would still be used by
-    what is queued there and was freed since.  result: the caller gets it, and uses it on the current stream."""
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+def _made(stream, device, make, result=True):
+    """make(), a tensor that a call on `stream` writes first.  It is the stream's own memory: the current stream's would still be
+    used by what is queued there and was freed since.  result: the caller gets it, and uses it on the current stream."""
+    if stream is None or device.type != "cuda":  # (a tensor elsewhere: refused by the call)
+        return make()
     if not isinstance(stream, torch.cuda.Stream):
         raw = int(getattr(stream, "cuda_stream", stream))  # 0, and CUDA's name for it, 1: the default stream
         stream = torch.cuda.ExternalStream(raw, device) if raw > 1 else torch.cuda.default_stream(device)
     user = torch.cuda.current_stream(device)
     with torch.cuda.stream(stream):
-        t = torch.empty(shape, dtype=dtype, device=device)
+        t = make()
     if result and user != stream:
         t.record_stream(user)
     return t
+
+
+def _empty(shape, dtype, device, stream, result=True):
+    return _made(stream, device, lambda: torch.empty(shape, dtype=dtype, device=device), result)
+
+
+def _empty_like(t, stream, memory_format=torch.preserve_format):
+    return _made(stream, t.device, lambda: torch.empty_like(t, memory_format=memory_format))
 
 
 def rq_lloyd_max_codebook(bits: int, head_dim: int = HEAD_DIM) -> np.ndarray:
@@ -585,9 +593,9 @@ class Rope:
         if len(given) == 2 and (k.dtype != first.dtype or k.dim() != 3 or k.shape[0] != n or k.device != self.device):
             raise RQError("rq_norm_rope", RQ_ERR_INVALID)
         if q is not None and q_out is None:
-            q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
+            q_out = _empty_like(q, stream, torch.contiguous_format)
         if k is not None and k_out is None:
-            k_out = torch.empty_like(k, memory_format=torch.contiguous_format)
+            k_out = _empty_like(k, stream, torch.contiguous_format)
         rq_norm_rope(self.rope, q, k, self.positions(positions, n, "rq_norm_rope"), q_weight, k_weight, eps, q_out,
                      k_out, stream)
         return q_out, k_out
@@ -658,7 +666,7 @@ class KVCache:
                 (q is not None and (q.dim() != 3 or q.shape[0] != n or q.dtype != dtype or q.device != device))):
             raise RQError(name, RQ_ERR_INVALID)
         if q is not None and q_out is None:
-            q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
+            q_out = _empty_like(q, stream, torch.contiguous_format)
         positions = rope.positions(positions, n, name) if rope is not None else None
         rq_rope_append(self.ctx, rope.rope if rope is not None else None, q, k, v, positions, slot_mapping, self.pages,
                        q_weight, k_weight, eps, q_out, self.status, stream)
@@ -685,27 +693,27 @@ class KVCache:
 
     def decode(self, q, block_table, seq_lens, out=None, stream=None):
         if out is None:
-            out = torch.empty_like(q)
+            out = _empty_like(q, stream)
         return rq_decode_attention(self.ctx, q, self.pages, block_table, seq_lens, out, self.status, stream)
 
     def decode_step(self, q, k_new, v_new, block_table, seq_lens, out=None, stream=None):
         if out is None:
-            out = torch.empty_like(q)
+            out = _empty_like(q, stream)
         return rq_decode_step(self.ctx, q, k_new, v_new, self.pages, block_table, seq_lens, out, self.status, stream)
 
     def extend(self, q, block_table, seq_lens, out=None, stream=None):
         if out is None:
-            out = torch.empty_like(q)
+            out = _empty_like(q, stream)
         return rq_extend_attention(self.ctx, q, self.pages, block_table, seq_lens, out, self.status, stream)
 
     def verify(self, q, block_table, seq_lens, out=None, stream=None):
         if out is None:
-            out = torch.empty_like(q)
+            out = _empty_like(q, stream)
         return rq_verify_attention(self.ctx, q, self.pages, block_table, seq_lens, out, self.status, stream)
 
     def tree_verify(self, q, tree_mask, block_table, seq_lens, out=None, stream=None):
         if out is None:
-            out = torch.empty_like(q)
+            out = _empty_like(q, stream)
         return rq_tree_verify_attention(self.ctx, q, tree_mask, self.pages, block_table, seq_lens, out, self.status,
                                         stream)
 
