@@ -201,3 +201,46 @@ def test_append_refuses_outputs_over_themselves():
             assert e.value.code == rq.RQ_ERR_INVALID, strides
     one = buf.as_strided((1, heads, 64), (8, 64, 1))  # a stride that is not used may be anything
     assert torch.equal(call(one, q[:1]), q[:1])
+
+
+# ------------------------------------------------------------------- what other tests pass by
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("heads", [5, 20, 40])
+def test_queries_with_an_outlier(dtype, heads):
+    """One dim a thousand times the others: the pieces of a row have one scale, so the others' low bits are lost as
+    latent_ref.attention counts them, and no more."""
+    case = Case(heads, [500, 33], 2, heads, 32, DT[dtype], sm_scale=0.0024)
+    case.q_c[..., 17] *= 1000
+    case.q_c[:, :, 1, 300] *= -1000
+    case.check(case.run())
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_verify_of_many_rows_over_long_sequences(dtype):
+    case = Case(7, [9000, 4100, 4], 4, 32, 64, DT[dtype])
+    case.check(case.run())
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("new,old", [([3000] + [16] * 7, [0] * 8), ([64] * 20, [0] * 13 + [8000] + [5] * 6), ([1, 1500, 2], [2500, 10, 0])])
+def test_prompts_of_very_different_lengths(dtype, new, old):
+    dtype = DT[dtype]
+    q, k, pe, v, qo, ko = prompt_case(len(new), new, old, 2, dtype)
+    out = rq.prompt_attention(q, k, pe, v, int32(qo), int32(ko), max(new))
+    check_prompt(out, q, k, pe, v, qo, ko, dtype)
+    assert torch.equal(out, rq.prompt_attention(q, k, pe, v, int32(qo), int32(ko), max(new)))
+
+
+@pytest.mark.parametrize("n,heads", [(300, 3), (200, 70), (1100, 2)])
+def test_prompt_weights_of_nothing_and_all(n, heads):
+    """Keys that are all the same, and scores that fall by 2^10 a key: means, and the row's own first keys."""
+    rng, dtype = gen(n), torch.bfloat16
+    q = torch.ones(n, heads, 192, dtype=dtype, device="cuda")
+    k, pe = torch.ones(n, heads, 128, dtype=dtype, device="cuda"), torch.zeros(n, 64, dtype=dtype, device="cuda")
+    v = dev(rng.standard_normal((n, heads, 128)), dtype)
+    off = int32([0, n])
+    check_prompt(rq.prompt_attention(q, k, pe, v, off, off, n), q, k, pe, v, [0, n], [0, n], dtype)
+    pe[:, 0] = -1024.0 * torch.arange(n, device="cuda")
+    out = host(rq.prompt_attention(q, k, pe, v, off, off, n, sm_scale=1.0))
+    within(out, np.broadcast_to(host(v)[:1], out.shape), (2.0 ** -8 + 2.0 ** -20) * np.abs(host(v)[:1]))
