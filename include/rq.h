@@ -87,8 +87,8 @@ extern "C" {
 #define RQ_STATUS_BAD_SLOT 2   /* slot_mapping entry >= num_pages * page_size */
 #define RQ_STATUS_BAD_LEN 4    /* seq_len < 0 or above max_pages * page_size, or below T */
 #define RQ_STATUS_NORM_OVERFLOW 8 /* a vector norm above the fp16 range (stored as inf); RQ_FP8: a finite
-                                     magnitude above 448 * 2^60 (stored as that) */
-#define RQ_STATUS_NOT_FINITE 32 /* an infinity or NaN among the values an RQ_FP8 append coded */
+                                     magnitude above 448 * 2^60 (stored as that); latents: see their storage */
+#define RQ_STATUS_NOT_FINITE 32 /* an infinity or NaN among the values that an RQ_FP8 or latent append coded */
 #define RQ_STATUS_BAD_ORDER 64  /* an RQ_FP8 append with tokens of one block apart from one another */
 #define RQ_STATUS_TIMEOUT 16   /* an attention kernel's staged page copy did not complete within
                                   its bounded wait (outputs of that call are unspecified; free an
@@ -455,7 +455,8 @@ typedef struct {
  * its latent over 512 dims (weight: device float32 [512], 16-byte aligned; NULL: none), the rotation of its position part
  * and of its queries' position parts, and the coding into slot slot_mapping[t] (page * P + offset).  A slot < 0 is
  * skipped, one past the pool sets RQ_STATUS_BAD_SLOT and is skipped (its queries are turned all the same).  Slots of a call
- * must be distinct.  The norm and the rotation are computed in float32 and coded from there.
+ * must be distinct.  The norm and the rotation are computed in float32 and coded from there: with a weight, a latent whose squares'
+ * sum is past float32 counts as not finite, and squares below 2^-126 lose bits (which an eps of 2^-100 and more outweighs).
  *   rope        of rotary_dim at most 64; NULL: no rotation.  It must live on the context's device
  *   c, k_pe     device, 16-byte aligned: token t at c + t * c_stride (512 elements) and k_pe + t * k_pe_stride (64);
  *               strides are multiples of 8
@@ -474,13 +475,16 @@ int rq_latent_append(rq_latent *ctx, const rq_rope *rope, const void *c, long lo
  * cached tokens (append them first): a decode step (T = 1), a chain of drafts (tree_mask NULL: row j sees positions
  * 0 .. seq_lens[b] - T + j) or a tree of them (device uint64 [B][T], T <= 64: row j sees the prefix and draft i exactly when bit
  * i of tree_mask[b][j] is set).  A row that sees no token gives zeros.
+ * Scores, maxima and sums are float32.  A query value is off by 2^-17 of its row's largest magnitude at most (bf16 values of 2^-9 of
+ * that and more, fp16 values of 2^-6, are exact), a weight by 2^-8 (bf16) or 2^-12 (fp16) of itself, with fewer bits below 2^-14 of
+ * the row's largest.
  *   q_c, q_pe   rows of num_heads heads, 512 and 64 elements, of B * T tokens.  A row with an infinity or NaN, or whose largest
  *               value times sm_scale is past float32, is NaN if it sees a token
  *   pages, block_table, max_pages, seq_lens   as rq_decode_attention
  *   out         device [B][T][num_heads][512], 16-byte aligned; may be q_c itself, other overlaps with the queries are refused
  * 0 < seq_lens[b] < T sets RQ_STATUS_BAD_LEN.  Calls on one context must not overlap on the GPU.
  * Errors: RQ_ERR_INVALID, RQ_ERR_CAPACITY (B, T or max_pages above the context's, or B * ceil(T * num_heads / 128) *
- * ceil(max_pages * P / 256) above 2^31 - 1), RQ_ERR_CUDA.
+ * (ceil(max_pages * P / 256) + 3) above 2^31 - 1), RQ_ERR_CUDA.
  */
 int rq_latent_attention(rq_latent *ctx, const rq_heads *q_c, const rq_heads *q_pe, int T, const uint64_t *tree_mask,
                         const void *pages, const int32_t *block_table, int max_pages, const int32_t *seq_lens, int B, void *out,
@@ -502,7 +506,8 @@ int rq_latent_read(rq_latent *ctx, const void *pages, const int32_t *block_table
  * Source: this library.  Causal attention of new tokens in the expanded form, for a batch of sequences packed one
  * after the other: sequence b has queries q_offsets[b] .. q_offsets[b + 1] - 1 and keys k_offsets[b] .. k_offsets[b + 1] - 1, the
  * queries being its last tokens: its query j sees its keys 0 .. nk_b - nq_b + j.  A head's key is its own 128 dims and the 64 that
- * all heads share.  out = softmax(sm_scale (q[:128] . k + q[128:] . k_pe)) v; a row that sees no key gives zeros.
+ * all heads share.  out = softmax(sm_scale (q[:128] . k + q[128:] . k_pe)) v; a row that sees no key gives zeros.  Scores, maxima and
+ * sums are float32; weights are rounded to io_type (fp16: below 2^-32 of the row's largest to nothing) for their product with v.
  * Sequences whose offsets fall, pass nq or nk, or have more than max_new queries set RQ_STATUS_BAD_LEN and are skipped;
  * rows of no sequence are left as they are.  A call gives the same bits each time; B, num_heads, nq, nk and max_new choose how its
  * work is cut, and so the order of its sums.

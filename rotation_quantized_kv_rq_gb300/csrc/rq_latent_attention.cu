@@ -25,7 +25,8 @@
 //
 // Work is cut evenly: tiles of all units (sequence, 128 rows) in order and kOpen more for each unit, one range for each pair.  A unit that spans ranges
 // leaves its parts (m, l, out) in the workspace, and a second kernel joins them.
-// Every wait is bounded: one that runs out sets RQ_STATUS_TIMEOUT and an abort flag every role polls.
+// Every wait is bounded: one that runs out sets RQ_STATUS_TIMEOUT and an abort flag every role polls.  Warps that meet in a loop
+// of such waits leave it together (rows_agree), and what the join reads is there whichever of them ran out.
 //
 // Device time: 64 x 16,384 x 128 heads bf16 217 us (1,344 TFLOP/s, 70% of the 16-bit rate), fp16 (three pieces) 287; 32 x 1K-32K x
 // 16 heads bf16 81 us (3.6 TB/s: MMAs of M = 128 for 16 rows); verify 8 x 16K + 4 x 32 heads fp16 71; 1 x 1,024 x 16 heads fp16

@@ -5,7 +5,7 @@
 // e4m3(y 2^-E), parts p 2^-E in 16 bits.  A row is a warp's, 16 dims to a lane, so that sums and maxima stay in it and a token's
 // bytes are written by one warp.  In long calls the warp turns the token's queries too, with the angles it has; in short ones
 // they have warps of their own (64 tokens x 128 heads: 2.8 us, a chain of latencies).  32,768 tokens x 16 heads: 44 us, 4.4 TB/s, 66%
-// of the copy rate, bound by instruction issue.
+// of the copy rate: 69% of the issue slots are taken, and what stalls the rest first are the loads.
 // read: a warp takes four rows, whose bytes are in flight together: 16 x 1K-16K tokens in 44 us, 5.7 TB/s, 85%; 1,500 in 3.2.
 #include "../../include/rq.h"
 #include "rq_block.cuh"

@@ -10,7 +10,8 @@
 // 1.6 tiles, waited for its loads: 4,950 cycles a tile, 1 x 16,384 x 16 heads 1,134 us.)  Warps are specialised and
 // coupled through mbarriers:
 //   softmax (warps 0-7 of both, a thread per row): takes its row of S from tensor memory into registers, masks, writes
-//     16-bit weights over S;
+//     16-bit weights over S (their MMA's operands have the values' type, so bf16 outputs are up to 1.4 times as far from the 64-bit
+//     result as with f32 weights; two pieces a weight would double the MMAs over the values; the sum takes them unrounded);
 //   MMA (warp 8 of the leader): for each block in turn O_b += W_b V(t) and behind it S_b(t + 1) = Q_b K(t + 1)^T, so that one block
 //     is on the tensor cores while the other is in its softmax;
 //   copies (warp 9 of both): TMA tiles straight from the caller's tensors, whatever their strides;
@@ -22,8 +23,9 @@
 // are few, or the last ones leave pairs idle, they are cut into parts, whose (m, l, out) a second kernel joins.
 // Every wait is bounded: one that runs out sets RQ_STATUS_TIMEOUT and an abort flag every role polls.
 //
-// Device time, bf16: 1 x 16,384 x 16 heads 848 us (1,620 TFLOP/s, 84% of the burst rate), 4 x 512 over 7,680 x 64 heads 447 us
-// (1,490, 77%), 8,192 x 8 heads 120 us; six prompts of 1 to 400 x 5 heads fp16 23 us, the opening, 6 tiles at most and the join.
+// Device time, bf16: 1 x 16,384 x 16 heads 836 to 863 us (1,640 to 1,590 TFLOP/s, 85 to 83% of the burst rate; 892 under the power cap),
+// 4 x 512 over 7,680 x 64 heads 450 to 460 us (1,450, 75%), 8,192 x 8 heads 120 us; six prompts of 1 to 400 x 5 heads fp16 24 to 28 us: one
+// unit's opening, four tiles and closing, one after the other (not cut: a part has at least four tiles).
 #include <math_constants.h>
 
 #include <algorithm>
