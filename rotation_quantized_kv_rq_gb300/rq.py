@@ -204,7 +204,7 @@ def _stream(stream, device) -> int:
 def _made(stream, device, make, result=True):
     """make(), a tensor that a call on `stream` writes first.  It is the stream's own memory: the current stream's would still be
     used by what is queued there and was freed since.  result: the caller gets it, and uses it on the current stream."""
-    if stream is None or device.type != "cuda":  # (a tensor elsewhere: refused by the call)
+    if stream is None or device.type != "cuda" or _stream(stream, device) == _stream(None, device):
         return make()
     if not isinstance(stream, torch.cuda.Stream):
         raw = int(getattr(stream, "cuda_stream", stream))  # 0, and CUDA's name for it, 1: the default stream
